@@ -423,3 +423,8 @@ def matmul(A, B, C=None, transA: str = "N", transB: str = "N", alpha: float = 1.
     sgemm(transA, transB, M, N, K, alpha, A, _stored_ld(A, "A"), B, _stored_ld(B, "B"), beta, C,
           _stored_ld(C, "C"), stream)
     return C
+
+
+from .fp8 import (Fp8Matrix, quantize_fp8, rmsnorm_fp8, rmsnorm_fp8_backward)  # noqa: E402
+
+__all__ += ["Fp8Matrix", "quantize_fp8", "rmsnorm_fp8", "rmsnorm_fp8_backward"]

@@ -12,6 +12,7 @@
 #include <cstdlib>
 #include <mutex>
 
+#include "fp8_internal.h"
 #include "kernel_small.h"
 #include "kernel_tma.cuh"
 #include "sgemm.h"
@@ -104,6 +105,7 @@ int device_state(int* device_out, DeviceState** st_out) {
       if (err == cudaSuccess) err = prepare_tc_pair();
       if (err == cudaSuccess) err = prepare_presplit();
       if (err == cudaSuccess) err = prepare_skinny();
+      if (err == cudaSuccess) err = prepare_fp8_norm();
       if (err == cudaSuccess) st.pair_clusters = pair_clusters_or_none();
       if (err == cudaSuccess && !st.pool) {
         cudaMemPoolProps props = {};
@@ -869,6 +871,18 @@ int launch_gemm(const Problem& pr, const sgemm_plan_t& plan, const DeviceState& 
 }
 
 }  // namespace
+
+int sgemm_impl::call_device(CallDevice* out) {
+  int dev;
+  DeviceState* st;
+  const int s = device_state(&dev, &st);
+  if (s != SGEMM_OK) return s;
+  out->sm_count = st->sm_count;
+  out->pair_clusters = st->pair_clusters;
+  out->fault = st->fault;
+  out->pool = st->pool;
+  return SGEMM_OK;
+}
 
 int sgemm_impl::plan_without_split_arrays(char transA, char transB, int64_t M, int64_t N, int64_t K, float alpha, const float* A,
                               int64_t lda, const float* B, int64_t ldb, float beta, const float* C, int64_t ldc,

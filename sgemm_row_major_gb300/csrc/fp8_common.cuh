@@ -1,0 +1,149 @@
+// fp8_common.cuh -- device helpers shared by the 8-bit operators: conversion to codes, the scale
+// of a group, and chunk loads and stores of FP32 / BF16 rows.
+#pragma once
+
+#include <cstdint>
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+#include "device_utils.cuh"
+#include "sgemm_fp8.h"
+
+namespace sgemm_impl {
+namespace f8 {
+
+constexpr float kMaxE4M3 = 448.0f, kMaxE5M2 = 57344.0f;
+constexpr float kMaxFloat = 3.402823466e38f;
+constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: the smallest scale, whose reciprocal is finite
+
+// |x| where it is finite, else 0: what counts towards a group's largest value.
+__device__ __forceinline__ float finite_abs(float x) {
+  const float a = fabsf(x);
+  return a <= kMaxFloat ? a : 0.0f;
+}
+
+// A group's scale.  top * kMinScale is far below any value that matters, so a group of zeros
+// (and one without finite values) simply gets the smallest scale.
+__device__ __forceinline__ float group_scale(float amax, float top) { return fmaxf(__fdiv_rn(amax, top), kMinScale); }
+
+// Two values (already divided by their scale, so at most `top` a rounding or two beyond it when
+// finite) to two codes, the first in the low byte; round to nearest even, NaN for a non-finite
+// value (the conversion alone would turn an infinity into the largest finite code).
+__device__ __forceinline__ uint32_t codes2(float a, float b, bool e5m2) {
+  const float nan = __int_as_float(0x7FFFFFFF);
+  a = fabsf(a) <= kMaxFloat ? a : nan;
+  b = fabsf(b) <= kMaxFloat ? b : nan;
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
+}
+
+__device__ __forceinline__ uint32_t codes4(const float* v, float inv, bool e5m2) {
+  return codes2(v[0] * inv, v[1] * inv, e5m2) | (codes2(v[2] * inv, v[3] * inv, e5m2) << 16);
+}
+
+// V consecutive elements as stored (16 bytes): 4 floats or 8 BF16 values.
+template <typename T>
+struct Chunk;
+template <>
+struct Chunk<float> {
+  static constexpr int V = 4;
+  uint4 raw;
+  __device__ __forceinline__ void get(float* v) const {
+    v[0] = __uint_as_float(raw.x);
+    v[1] = __uint_as_float(raw.y);
+    v[2] = __uint_as_float(raw.z);
+    v[3] = __uint_as_float(raw.w);
+  }
+  __device__ __forceinline__ void put(const float* v) {
+    raw = make_uint4(__float_as_uint(v[0]), __float_as_uint(v[1]), __float_as_uint(v[2]), __float_as_uint(v[3]));
+  }
+};
+template <>
+struct Chunk<__nv_bfloat16> {
+  static constexpr int V = 8;
+  uint4 raw;
+  __device__ __forceinline__ void get(float* v) const {  // BF16 is the upper half of an FP32 value
+    const uint32_t u[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(u[i] << 16);
+      v[2 * i + 1] = __uint_as_float(u[i] & 0xFFFF0000u);
+    }
+  }
+  __device__ __forceinline__ void put(const float* v) {
+    uint32_t u[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const __nv_bfloat162 b = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+      u[i] = *reinterpret_cast<const uint32_t*>(&b);
+    }
+    raw = make_uint4(u[0], u[1], u[2], u[3]);
+  }
+};
+
+__device__ __forceinline__ float to_float(float x) { return x; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
+__device__ __forceinline__ void from_float(float* p, float x) { *p = x; }
+__device__ __forceinline__ void from_float(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
+
+// Elements [0, n) of a chunk of V at p (zeros beyond n); `vec`: p is 16-byte aligned.
+template <typename T>
+__device__ __forceinline__ Chunk<T> load_chunk(const T* p, int64_t n, bool vec) {
+  constexpr int V = Chunk<T>::V;
+  Chunk<T> c;
+  c.raw = make_uint4(0u, 0u, 0u, 0u);
+  if (vec && n >= V) {
+    c.raw = *reinterpret_cast<const uint4*>(p);
+  } else if (n > 0) {
+    float v[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) v[i] = i < n ? to_float(p[i]) : 0.0f;
+    c.put(v);  // exact: every value came from T
+  }
+  return c;
+}
+
+template <typename T>
+__device__ __forceinline__ void store_chunk(T* p, const float* v, int64_t n, bool vec) {
+  constexpr int V = Chunk<T>::V;
+  if (vec && n >= V) {
+    Chunk<T> c;
+    c.put(v);
+    *reinterpret_cast<uint4*>(p) = c.raw;
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) from_float(p + i, v[i]);
+  }
+}
+
+// V codes (4 or 8) of one chunk; `vec`: p is aligned to V bytes.
+template <int V>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float* v, float inv, int64_t n, bool vec, bool e5m2) {
+  uint32_t u[V / 4];
+#pragma unroll
+  for (int i = 0; i < V / 4; ++i) u[i] = codes4(v + 4 * i, inv, e5m2);
+  if (vec && n >= V) {
+    if (V == 4) *reinterpret_cast<uint32_t*>(p) = u[0];
+    else        *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[V / 4 - 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) p[i] = (uint8_t)(u[i / 4] >> (8 * (i % 4)));
+  }
+}
+
+template <int LANES>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int d = LANES / 2; d > 0; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+
+__device__ __forceinline__ float warp_sum(float v) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+  return v;
+}
+
+}  // namespace f8
+}  // namespace sgemm_impl

@@ -1,0 +1,219 @@
+"""The RMS norm with residual addition and 8-bit output (sgemm_fp8_rmsnorm) and its gradients,
+against the formulas in 64 bits.
+
+Tolerances.  A sum of n FP32 terms in any order is within n u of the sum of magnitudes (u = 2^-24), so
+rstd is within (n / 2 + 4) u and each y within (n / 2 + 8) u of exact; a code adds half a unit in the
+last place of the format, 2^-4 of a normal value or 2^-10 of the scale.  BF16 outputs add 2^-8."""
+import numpy as np
+import pytest
+
+import sgemm_row_major_gb300 as sg
+from fp8_util import U, dequantize, strided
+
+FAKE = 1 << 20
+EPS = 1e-6
+
+
+def data(rows, cols, seed, dtype, residual):
+    import torch
+    g = torch.Generator().manual_seed(seed)
+    t = getattr(torch, dtype)
+    x = torch.randn(rows, cols, generator=g)
+    x[:, ::37] *= 20.0
+    w = 1.0 + 0.2 * torch.randn(cols, generator=g)
+    r = (3.0 * torch.randn(rows, cols, generator=g)).to(t) if residual else None
+    return x.to(t), w.to(t), r
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def check_forward(x, w, r, out, dtype):
+    rows, cols = x.shape
+    h = f64(x) + (f64(r) if r is not None else 0.0)
+    half = 2.0 ** -8 if dtype == "bfloat16" else U
+    rel = (cols / 2 + 8) * U
+    rstd = 1.0 / np.sqrt((h * h).mean(1) + EPS)
+    y = h * rstd[:, None] * f64(w)
+    if r is not None:
+        assert np.all(np.abs(f64(out.h) - h) <= half * np.abs(h) + U * np.abs(h))
+    assert np.all(np.abs(f64(out.rstd) - rstd) <= rel * rstd)
+    if out.y is not None:
+        # h itself is rounded once before the product
+        assert np.all(np.abs(f64(out.y) - y) <= (rel + half) * 1.01 * np.abs(y) + 1e-38)
+    if out.q is not None:
+        s = f64(out.q.scale)
+        pad = -cols % 128
+        amax = np.abs(np.pad(y, ((0, 0), (0, pad)))).reshape(rows, -1, 128).max(2)
+        assert np.all(np.abs(s - np.maximum(amax / 448, 2.0 ** -126)) <= (rel + 2 * U) * s)
+        each = np.repeat(s, 128, 1)[:, :cols]
+        tol = (2.0 ** -4 * np.abs(y) + 2.0 ** -10 * each) * (1 + 2 * rel) + 2 * rel * np.abs(y)
+        assert np.all(np.abs(dequantize(out.q) - y) <= tol)
+
+
+SHAPES = [(1, 1), (3, 7), (1, 4096), (5, 128), (70, 1000), (2, 8200), (3, 8192), (2, 16392), (2, 32768), (1, 40001), (600, 64)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("residual", [False, True])
+@pytest.mark.parametrize("rows,cols", SHAPES)
+def test_forward(rows, cols, dtype, residual):
+    x, w, r = data(rows, cols, rows + cols, dtype, residual)
+    out = sg.rmsnorm_fp8(x.cuda(), w.cuda(), EPS, r.cuda() if residual else None, y=True)
+    check_forward(x, w, r, out, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("pad,offset", [(8, 0), (3, 0), (0, 1)])
+def test_forward_strides(dtype, pad, offset):
+    x, w, r = data(40, 520, 5, dtype, True)
+    out = sg.rmsnorm_fp8(strided(x, pad, offset), w.cuda(), EPS, strided(r, pad + 1, offset), y=True)
+    check_forward(x, w, r, out, dtype)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cols", [520, 40000])
+def test_sum_may_overwrite_an_input(cols):
+    """H may be X or R (registers hold a row; the wide form reads before it writes)."""
+    import torch
+    from sgemm_row_major_gb300 import fp8
+    x, w, r = data(9, cols, 6, "float32", True)
+    want = sg.rmsnorm_fp8(x.cuda(), w.cuda(), EPS, r.cuda(), y=True)
+    for over in (0, 1):
+        ins = [x.cuda(), r.cuda()]
+        y, dw = torch.empty(9, cols, device="cuda"), w.cuda()
+        st = fp8._lib().sgemm_fp8_rmsnorm(9, cols, 0, ins[0].data_ptr(), cols, ins[1].data_ptr(), cols, dw.data_ptr(), EPS,
+                                          ins[over].data_ptr(), cols, y.data_ptr(), cols, None, 0, None, 0, None, None)
+        torch.cuda.synchronize()
+        assert st == 0 and torch.equal(ins[over], want.h) and torch.equal(y, want.y)
+
+
+@pytest.mark.gpu
+def test_special_rows():
+    """A row of zeros gives zeros; a NaN or an infinity reaches every code of its row's groups as the formula says,
+    and no other row."""
+    import torch
+    x, w, _ = data(4, 256, 7, "float32", False)
+    x[0] = 0.0
+    x[1, 3] = float("nan")
+    x[2, 200] = float("inf")
+    out = sg.rmsnorm_fp8(x.cuda(), w.cuda(), EPS, y=True)
+    q = dequantize(out.q)
+    assert np.all(q[0] == 0) and np.all(np.isnan(q[1])) and np.isnan(q[2, 200])
+    assert np.all(q[2, :200] == 0) and np.all(np.isfinite(q[3]))
+    y = out.y.cpu()
+    assert torch.isnan(y[1]).all() and torch.isnan(y[2, 200]) and (y[2, :200] == 0).all()
+
+
+def grads(dy, h, w, rstd, dh):
+    """The formulas in 64 bits, and the sums of magnitudes their rounding errors scale with."""
+    dn = dy * w
+    m = (dn * h).mean(1, keepdims=True)
+    mm = np.abs(dn * h).mean(1, keepdims=True)
+    r = rstd[:, None]
+    dx = r * dn - r ** 3 * m * h + dh
+    mag = r * np.abs(dn) + r ** 3 * mm * np.abs(h) + np.abs(dh)
+    return dx, mag, (dy * h * r).sum(0), np.abs(dy * h * r).sum(0)
+
+
+GRAD_SHAPES = [(1, 1), (3, 7), (1, 4096), (700, 128), (330, 1000), (5, 4104), (200, 8192), (4, 8200), (3, 49152), (2000, 64)]
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("past", [False, True])
+@pytest.mark.parametrize("rows,cols", GRAD_SHAPES)
+def test_backward(rows, cols, dtype, past):
+    import torch
+    h, w, dh = data(rows, cols, rows * 3 + cols, dtype, past)
+    dy = torch.randn(rows, cols, generator=torch.Generator().manual_seed(8)).to(h.dtype)
+    rstd = (h.float().square().mean(1) + EPS).rsqrt()
+    args = (dy.cuda(), h.cuda(), w.cuda(), rstd.cuda(), dh.cuda() if past else None)
+    dx, dw = sg.rmsnorm_fp8_backward(*args)
+    ref, mag, rdw, mdw = grads(f64(dy), f64(h), f64(w), f64(rstd), f64(dh) if past else 0.0)
+    half = 2.0 ** -8 if dtype == "bfloat16" else U
+    assert np.all(np.abs(f64(dx) - ref) <= (cols + 8) * U * mag + half * np.abs(ref) + 1e-38)
+    assert np.all(np.abs(f64(dw) - rdw) <= (rows + 8) * U * mdw)
+    again = sg.rmsnorm_fp8_backward(*args)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)  # no order depends on scheduling
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("pad,offset", [(8, 0), (3, 0), (0, 1)])
+def test_backward_strides(pad, offset):
+    h, w, dh = data(50, 520, 11, "float32", True)
+    dy, _, _ = data(50, 520, 12, "float32", False)
+    rstd = (h.square().mean(1) + EPS).rsqrt()
+    dx, dw = sg.rmsnorm_fp8_backward(strided(dy, pad, offset), strided(h, pad + 4, offset), w.cuda(), rstd.cuda(), strided(dh, pad, 0))
+    ref, mag, rdw, mdw = grads(f64(dy), f64(h), f64(w), f64(rstd), f64(dh))
+    assert np.all(np.abs(f64(dx) - ref) <= 530 * U * mag)
+    assert np.all(np.abs(f64(dw) - rdw) <= 60 * U * mdw)
+
+
+@pytest.mark.gpu
+def test_gradient_against_differences():
+    """Central differences of L = sum(g * y) over the FP32 forward pass itself: the step e = 2^-6 leaves a truncation
+    error below e^2 (third derivatives of y are O(1) here) and the rounding of L, cols * u * |L| / e."""
+    import torch
+    rows, cols, e = 3, 96, 2.0 ** -6
+    x, w, _ = data(rows, cols, 13, "float32", False)
+    x.clamp_(-2, 2)
+    g = torch.randn(rows, cols, generator=torch.Generator().manual_seed(14))
+    out = sg.rmsnorm_fp8(x.cuda(), w.cuda(), EPS, y=True)
+    dx, dw = sg.rmsnorm_fp8_backward(g.cuda(), x.cuda(), w.cuda(), out.rstd)
+
+    def loss(x_, w_):
+        return (f64(sg.rmsnorm_fp8(x_.cuda(), w_.cuda(), EPS, codes=False, y=True).y) * f64(g)).sum()
+
+    tol = 16 * e * e + 2 * cols * rows * U * 40 / e
+    for i, j in [(0, 0), (1, 50), (2, 95)]:
+        d = torch.zeros_like(x)
+        d[i, j] = e
+        assert abs((loss(x + d, w) - loss(x - d, w)) / (2 * e) - float(dx[i, j])) <= tol
+        d = torch.zeros_like(w)
+        d[j] = e
+        assert abs((loss(x, w + d) - loss(x, w - d)) / (2 * e) - float(dw[j])) <= tol
+
+
+@pytest.mark.gpu
+def test_empty_and_graph():
+    import torch
+    w = torch.ones(16, device="cuda")
+    out = sg.rmsnorm_fp8(torch.zeros(0, 16, device="cuda"), w)
+    assert tuple(out.q.shape) == (0, 16)
+    e = torch.zeros(0, 16, device="cuda")
+    dx, dw = sg.rmsnorm_fp8_backward(e, e, w, torch.zeros(0, device="cuda"))
+    assert tuple(dx.shape) == (0, 16) and torch.equal(dw, torch.zeros_like(dw))
+    x, w, r = (t.cuda() for t in data(33, 512, 15, "bfloat16", True))
+    dy = torch.randn(33, 512, device="cuda").bfloat16()
+    want = sg.rmsnorm_fp8(x, w, EPS, r)
+    wdx, wdw = sg.rmsnorm_fp8_backward(dy, want.h, w, want.rstd)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = sg.rmsnorm_fp8(x, w, EPS, r)
+        dx, dw = sg.rmsnorm_fp8_backward(dy, out.h, w, out.rstd)
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out.q.scale, want.q.scale) and torch.equal(dx, wdx) and torch.equal(dw, wdw)
+
+
+def test_refusals():
+    from sgemm_row_major_gb300 import fp8
+    lib = fp8._lib()
+    ok = [4, 256, 1, FAKE, 256, FAKE, 256, FAKE, 1e-6, FAKE, 256, FAKE, 256, FAKE, 256, FAKE, 2, FAKE, None]
+    for index, value in [(1, -1), (2, -1), (3, 5), (4, None), (4, FAKE + 1), (5, 255), (6, FAKE + 1), (7, 255), (8, None), (9, -1.0),
+                         (9, float("nan")), (10, FAKE + 1), (11, 3), (12, FAKE + 1), (13, 3), (15, 255), (16, None), (17, 1), (18, FAKE + 2)]:
+        bad = list(ok)
+        bad[index - 1] = value
+        assert lib.sgemm_fp8_rmsnorm(*bad) == -index, (index, value)
+    ok = [4, 256, 0, FAKE, 256, FAKE, 256, FAKE, FAKE, FAKE, 256, FAKE, 256, FAKE, None]
+    for index, value in [(1, -1), (2, -1), (3, 5), (4, None), (5, 255), (6, None), (7, 255), (8, None), (9, None), (10, FAKE + 1),
+                         (11, 255), (12, None), (13, 255), (14, FAKE + 1)]:
+        bad = list(ok)
+        bad[index - 1] = value
+        assert lib.sgemm_fp8_rmsnorm_backward(*bad) == -index, (index, value)
+    wide = [4, 49153, 0, FAKE, 49153, FAKE, 49153, FAKE, FAKE, None, 0, FAKE, 49153, FAKE, None]
+    assert lib.sgemm_fp8_rmsnorm_backward(*wide) == 4  # SGEMM_ERR_UNSUPPORTED, before the device is looked at
