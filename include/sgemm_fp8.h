@@ -92,6 +92,15 @@ int sgemm_fp8_plan(char transA, char transB, int64_t M, int64_t N, int64_t K, fl
                    int sm_count, sgemm_plan_t *plan);
 
 /*
+ * Process-wide override of sgemm_fp8()'s choice of kernel, for tests and
+ * benchmarks: variant = SGEMM_VARIANT_AUTO (0) restores it.  tile_n = 0 and
+ * split = 0 keep the planner's own; a forced split (SHORT: 1, 2, 4 or 8) may
+ * give a CTA no groups at all.  -1, -2, -3: an argument that names no kernel,
+ * tile or split.
+ */
+int sgemm_fp8_set_override(int variant, int tile_n, int split);
+
+/*
  * sgemm_fp8_quantize -- codes and scales of the rows x cols matrix X (type F32
  * or BF16), in groups of block_rows x block_cols elements.  For each group
  *     s = max(amax / top, 2^-126),  code = round(x * (1 / s)),

@@ -1,5 +1,6 @@
 // api_fp8.cu -- the C ABI of the 8-bit operators (sgemm_fp8.h): argument checks, workspace and launches.
 #include <algorithm>
+#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -22,11 +23,305 @@ bool known_format(int f) { return f == SGEMM_FP8_E4M3 || f == SGEMM_FP8_E5M2; }
 // Rows of 16-byte vectors: the base and the row stride in bytes are multiples of 16 (a NULL matrix is not read).
 bool rows16(const void* p, int64_t ld, int size) { return !p || (aligned(p, 16) && ld * size % 16 == 0); }
 
+// ---------------------------------------------------------------- product
+
+std::atomic<int> g_force_variant{SGEMM_VARIANT_AUTO}, g_force_tile{0}, g_force_split{0};
+
+int op_code(char t) {
+  if (t == 'N' || t == 'n') return 0;
+  if (t == 'T' || t == 't' || t == 'C' || t == 'c') return 1;
+  return -1;
+}
+
+// One operand of a product: `mn` output rows (or columns) x K, and how it is stored.
+struct Operand {
+  const sgemm_fp8_matrix_t* m = nullptr;
+  int64_t rows = 0, cols = 0;  // stored
+  int mn_major = 0;            // the stored rows run along the output, not along k
+  Fp8Scales scales;
+};
+
+// Fills *o; false when a field of *m cannot be used (`read`: the operand is read at all).
+bool check_operand(const sgemm_fp8_matrix_t* m, int64_t mn, int64_t K, bool mn_major, bool read, Operand* o) {
+  if (!m) return !read;
+  o->m = m;
+  o->mn_major = mn_major ? 1 : 0;
+  o->rows = mn_major ? K : mn;
+  o->cols = mn_major ? mn : K;
+  if (!known_format(m->format)) return false;
+  const int along_k = mn_major ? m->block_rows : m->block_cols, along_mn = mn_major ? m->block_cols : m->block_rows;
+  if (along_k != 128 || (along_mn != 1 && along_mn != 128)) return false;
+  if (m->ld < std::max<int64_t>(1, o->cols) || m->lds < std::max<int64_t>(1, ceil_div(o->cols, m->block_cols)))
+    return false;
+  if (read && (!m->data || !m->scale || !aligned(m->scale, 4))) return false;
+  o->scales.p = m->scale;
+  o->scales.shift = along_mn == 128 ? 7 : 0;
+  o->scales.si = mn_major ? 1 : m->lds;
+  o->scales.sk = mn_major ? m->lds : 1;
+  return true;
+}
+
+struct Product {
+  int64_t M, N, K;
+  float alpha;
+  Operand a, b;
+  Fp8Out out;
+};
+
+int check_product(char transA, char transB, int64_t M, int64_t N, int64_t K, float alpha, const sgemm_fp8_matrix_t* A,
+                  const sgemm_fp8_matrix_t* B, float beta, const void* C, int64_t ldc, const void* D, int64_t ldd,
+                  int type, Product* pr) {
+  const int ta = op_code(transA), tb = op_code(transB);
+  if (ta < 0) return -1;
+  if (tb < 0) return -2;
+  if (M < 0) return -3;
+  if (N < 0) return -4;
+  if (K < 0) return -5;
+  const bool work = M > 0 && N > 0, read = work && K > 0 && alpha != 0.0f;
+  *pr = Product{M, N, K, alpha, {}, {}, {}};
+  if (!check_operand(A, M, K, ta != 0, read, &pr->a)) return -7;
+  if (!check_operand(B, N, K, tb == 0, read, &pr->b)) return -8;
+  if (!known_type(type)) return -14;
+  const int size = type_size(type);
+  if (work && beta != 0.0f && (!C || !aligned(C, size))) return -10;
+  if (beta != 0.0f && ldc < std::max<int64_t>(1, N)) return -11;
+  if (work && (!D || !aligned(D, size))) return -12;
+  if (ldd < std::max<int64_t>(1, N) || (C == D && C && beta != 0.0f && ldc != ldd)) return -13;
+  Fp8Out& o = pr->out;
+  o.M = (int)std::min<int64_t>(M, INT_MAX);
+  o.N = (int)std::min<int64_t>(N, INT_MAX);
+  o.alpha = alpha;
+  o.beta = beta;
+  o.C = beta != 0.0f ? C : nullptr;
+  o.D = const_cast<void*>(D);
+  o.ldc = ldc;
+  o.ldd = ldd;
+  o.bf16 = type == SGEMM_BF16;
+  o.vec = rows16(o.C, ldc, size) && rows16(D, ldd, size);
+  return SGEMM_OK;
+}
+
+// TMA reads codes whose base and row stride are multiples of 16 bytes; others are copied first.
+int64_t repack_ld(const Operand& o) { return ceil_div(o.cols, 16) * 16; }
+int64_t repack_bytes(const Operand& o) {
+  return aligned(o.m->data, 16) && o.m->ld % 16 == 0 ? 0 : round256(o.rows * repack_ld(o));
+}
+
+// Pair kernel: the tile width whose rounds of tiles over the clusters cost least.  A group of 128 k
+// costs a tile tile_n / 256 of the tensor cores' time plus what does not shrink with it (the rows
+// of A, the barriers' round trips).
+constexpr int kPairFixedCols = 64;
+int pair_tile_n(int64_t M, int64_t N, int64_t clusters) {
+  int best = 256;
+  int64_t best_cost = INT64_MAX;
+  for (int n = 256; n >= 32; n -= 32) {
+    const int64_t rounds = ceil_div(ceil_div(M, 256) * ceil_div(N, n), clusters);
+    const int64_t cost = rounds * (n + kPairFixedCols);
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = n;
+    }
+  }
+  return best;
+}
+
+constexpr int64_t kShortRing = 108 * 1024;  // two CTAs per SM
+
+int plan_product(const Product& pr, int sm_count, int pair_clusters, sgemm_plan_t* plan) {
+  *plan = sgemm_plan_t{};
+  plan->split_k = 1;
+  if (pr.M == 0 || pr.N == 0) {
+    plan->variant = SGEMM_VARIANT_NONE;
+    return SGEMM_OK;
+  }
+  if (pr.M > kMaxDim || pr.N > kMaxDim || pr.K > kMaxDim) return SGEMM_ERR_UNSUPPORTED;
+  if (pr.K == 0 || pr.alpha == 0.0f) {
+    plan->variant = SGEMM_VARIANT_SCALE;
+    plan->kernel_launches = 1;
+    plan->threads = 256;
+    return SGEMM_OK;
+  }
+  if (pr.a.m->ld > INT_MAX || pr.b.m->ld > INT_MAX || pair_clusters == 0) return SGEMM_ERR_UNSUPPORTED;
+  const int64_t clusters = pair_clusters > 0 ? pair_clusters : std::max(1, sm_count / 2);
+  const int64_t groups = ceil_div(pr.K, 128);
+  const int64_t S = std::min(pr.M, pr.N), L = std::max(pr.M, pr.N);
+  int variant = g_force_variant.load();
+  if (variant == SGEMM_VARIANT_AUTO) variant = S <= 128 ? SGEMM_VARIANT_FP8_SHORT : SGEMM_VARIANT_FP8_PAIR;
+  const int force_tile = g_force_tile.load(), force_split = g_force_split.load();
+  plan->variant = variant;
+  plan->tile_k = 128;
+  plan->kernel_launches = 1;
+  plan->workspace_bytes = repack_bytes(pr.a) + repack_bytes(pr.b);
+  plan->kernel_launches += (repack_bytes(pr.a) > 0) + (repack_bytes(pr.b) > 0);
+  int64_t tiles;
+  if (variant == SGEMM_VARIANT_FP8_PAIR) {
+    plan->tile_m = 256;
+    plan->tile_n = force_tile ? force_tile : pair_tile_n(pr.M, pr.N, clusters);
+    plan->stages = 6;
+    plan->threads = 320;
+    plan->smem_bytes = 6 * 32768 + 1024;
+    tiles = ceil_div(pr.M, 256) * ceil_div(pr.N, plan->tile_n);
+    plan->grid_x = 2 * std::min<int64_t>(tiles, clusters);
+  } else {
+    const Operand& s_op = pr.M <= pr.N ? pr.a : pr.b;
+    const int64_t tiles_s = ceil_div(S, kFp8ShortMaxTile);
+    plan->tile_m = 128;
+    plan->tile_n = force_tile ? force_tile : (int)(ceil_div(ceil_div(S, tiles_s), 16) * 16);
+    tiles = ceil_div(L, 128) * ceil_div(S, plan->tile_n);
+    // K shares: as many CTAs as the device holds at two per SM, at least two groups each
+    int split = 1;
+    while (split < 8 && tiles * split * 2 <= 2 * sm_count && groups >= 4 * split) split *= 2;
+    if (force_split) split = force_split;
+    plan->split_k = split;
+    const int64_t stage = 16384 + (s_op.mn_major ? 16384 : plan->tile_n * 128);
+    plan->stages = (int)std::min<int64_t>(kFp8ShortMaxStages, kShortRing / stage);
+    plan->threads = 192;
+    plan->smem_bytes = (int64_t)fp8_short_smem(plan->tile_n, plan->stages, (int)stage);
+    plan->grid_x = tiles * split;
+  }
+  plan->dp_tiles = tiles;
+  plan->grid_y = 1;
+  return plan->grid_x > INT_MAX || tiles * groups > INT_MAX ? SGEMM_ERR_UNSUPPORTED : SGEMM_OK;
+}
+
+// Tensor-core instruction descriptor, kind::f8f6f4: FP32 accumulator, operand formats, the
+// operands' orders (1: MN-major), N and M of the instruction.
+uint32_t instruction(const Operand& a, const Operand& b, int m, int n) {
+  return (1u << 4) | ((uint32_t)a.m->format << 7) | ((uint32_t)b.m->format << 10) | ((uint32_t)a.mn_major << 15) |
+         ((uint32_t)b.mn_major << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(m >> 4) << 24);
+}
+
+// Tensor map of an operand's tiles (`mn` output rows each), after copying its codes to aligned rows
+// at *ws where it needs that.
+cudaError_t operand_map(const Operand& o, int mn, uint8_t** ws, CUtensorMap* map, cudaStream_t stream) {
+  const void* data = o.m->data;
+  int64_t ld = o.m->ld;
+  const int64_t copy = repack_bytes(o);
+  if (copy > 0) {
+    const cudaError_t e = launch_fp8_repack(data, ld, o.rows, o.cols, *ws, repack_ld(o), stream);
+    if (e != cudaSuccess) return e;
+    data = *ws;
+    ld = repack_ld(o);
+    *ws += copy;
+  }
+  return encode_fp8_map(data, o.cols, o.rows, ld, o.mn_major ? 128 : mn, map);
+}
+
+cudaError_t launch_product(const Product& pr, const sgemm_plan_t& plan, const CallDevice& dev, uint8_t* ws,
+                           cudaStream_t stream) {
+  CUtensorMap ma, mb;
+  if (plan.variant == SGEMM_VARIANT_FP8_PAIR) {
+    cudaError_t e = operand_map(pr.a, 128, &ws, &ma, stream);
+    if (e == cudaSuccess) e = operand_map(pr.b, plan.tile_n / 2, &ws, &mb, stream);
+    if (e != cudaSuccess) return e;
+    Fp8PairParams p;
+    p.out = pr.out;
+    p.K = (int)pr.K;
+    p.sa = pr.a.scales;
+    p.sb = pr.b.scales;
+    p.a_mn = pr.a.mn_major;
+    p.b_mn = pr.b.mn_major;
+    p.idesc = instruction(pr.a, pr.b, 256, plan.tile_n);
+    p.tile_n = plan.tile_n;
+    p.tiles_m = (int)ceil_div(pr.M, 256);
+    p.tiles_n = (int)ceil_div(pr.N, plan.tile_n);
+    p.clusters = (int)(plan.grid_x / 2);
+    p.timeout_ns = wait_timeout_ns();
+    p.fault = dev.fault;
+    return launch_fp8_pair(ma, mb, p, stream);
+  }
+  const bool trans = pr.M <= pr.N;
+  const Operand &l = trans ? pr.b : pr.a, &s = trans ? pr.a : pr.b;
+  cudaError_t e = operand_map(l, 128, &ws, &ma, stream);
+  if (e == cudaSuccess) e = operand_map(s, plan.tile_n, &ws, &mb, stream);
+  if (e != cudaSuccess) return e;
+  Fp8ShortParams p;
+  p.out = pr.out;
+  p.K = (int)pr.K;
+  p.L = (int)(trans ? pr.N : pr.M);
+  p.S = (int)(trans ? pr.M : pr.N);
+  p.trans = trans;
+  p.sl = l.scales;
+  p.ss = s.scales;
+  p.l_mn = l.mn_major;
+  p.s_mn = s.mn_major;
+  p.idesc = instruction(l, s, 128, plan.tile_n);
+  p.tile_s = plan.tile_n;
+  p.tiles_l = (int)ceil_div(p.L, 128);
+  p.tiles_s = (int)ceil_div(p.S, plan.tile_n);
+  p.split = plan.split_k;
+  p.stages = plan.stages;
+  p.stage_bytes = 16384 + (s.mn_major ? 16384 : plan.tile_n * 128);
+  p.timeout_ns = wait_timeout_ns();
+  p.fault = dev.fault;
+  return launch_fp8_short(ma, mb, p, stream);
+}
+
 int launch_status(cudaError_t e) { return e == cudaSuccess ? SGEMM_OK : record_cuda_failure(e); }
 
 }  // namespace
 
 extern "C" {
+
+int sgemm_fp8(char transA, char transB, int64_t M, int64_t N, int64_t K, float alpha, const sgemm_fp8_matrix_t* A,
+              const sgemm_fp8_matrix_t* B, float beta, const void* C, int64_t ldc, void* D, int64_t ldd, int type,
+              struct CUstream_st* stream_) {
+  Product pr;
+  int s = check_product(transA, transB, M, N, K, alpha, A, B, beta, C, ldc, D, ldd, type, &pr);
+  if (s != SGEMM_OK || M == 0 || N == 0) return s;
+  CallDevice dev;
+  s = call_device(&dev);
+  if (s != SGEMM_OK) return s;
+  sgemm_plan_t plan;
+  s = plan_product(pr, dev.sm_count, dev.pair_clusters, &plan);
+  if (s != SGEMM_OK) return s;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (plan.variant == SGEMM_VARIANT_SCALE) return launch_status(launch_fp8_scale(pr.out, stream));
+  void* ws = nullptr;
+  if (plan.workspace_bytes > 0) {
+    const cudaError_t e = cudaMallocFromPoolAsync(&ws, (size_t)plan.workspace_bytes, dev.pool, stream);
+    if (e != cudaSuccess) {
+      record_cuda_failure(e);
+      return e == cudaErrorMemoryAllocation ? SGEMM_ERR_NOMEM : SGEMM_ERR_CUDA;
+    }
+  }
+  cudaError_t e = launch_product(pr, plan, dev, static_cast<uint8_t*>(ws), stream);
+  if (ws) {
+    const cudaError_t ef = cudaFreeAsync(ws, stream);
+    if (e == cudaSuccess) e = ef;
+  }
+  return launch_status(e);
+}
+
+int sgemm_fp8_plan(char transA, char transB, int64_t M, int64_t N, int64_t K, float alpha, const sgemm_fp8_matrix_t* A,
+                   const sgemm_fp8_matrix_t* B, float beta, const void* C, int64_t ldc, const void* D, int64_t ldd,
+                   int type, int sm_count, sgemm_plan_t* plan) {
+  if (!plan) return -16;
+  Product pr;
+  int s = check_product(transA, transB, M, N, K, alpha, A, B, beta, C, ldc, D, ldd, type, &pr);
+  if (s != SGEMM_OK) return s;
+  CallDevice dev;
+  dev.sm_count = sm_count;
+  dev.pair_clusters = -1;
+  if (sm_count <= 0) {
+    s = call_device(&dev);
+    if (s != SGEMM_OK) return s;
+  }
+  return plan_product(pr, dev.sm_count, dev.pair_clusters, plan);
+}
+
+int sgemm_fp8_set_override(int variant, int tile_n, int split) {
+  if (variant != SGEMM_VARIANT_AUTO && variant != SGEMM_VARIANT_FP8_PAIR && variant != SGEMM_VARIANT_FP8_SHORT)
+    return -1;
+  const bool is_short = variant == SGEMM_VARIANT_FP8_SHORT;
+  const int step = is_short ? 16 : 32, most = is_short ? kFp8ShortMaxTile : 256;
+  if (tile_n < 0 || tile_n > most || tile_n % step != 0 || (tile_n > 0 && variant == SGEMM_VARIANT_AUTO)) return -2;
+  if ((split != 0 && !is_short) || (split != 0 && split != 1 && split != 2 && split != 4 && split != 8)) return -3;
+  g_force_variant.store(variant);
+  g_force_tile.store(tile_n);
+  g_force_split.store(split);
+  return SGEMM_OK;
+}
 
 int sgemm_fp8_quantize(int64_t rows, int64_t cols, const void* X, int type, int64_t ldx, int format, int block_rows,
                        int block_cols, void* codes, int64_t ldq, float* scale, int64_t lds,

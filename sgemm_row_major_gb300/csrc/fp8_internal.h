@@ -66,4 +66,67 @@ cudaError_t prepare_fp8_norm();
 int fp8_rmsnorm_backward_grid(int type, int64_t rows, int cols, int sm_count);
 cudaError_t launch_fp8_rmsnorm_backward(int type, const NormGradParams& p, int grid, cudaStream_t stream);
 
+// ---- product (kernel_fp8_pair.cu, kernel_fp8_short.cu)
+
+// Scales of one operand of a product: of row (or column) i of op(X) in group g of 128 k,
+// p[(i >> shift) * si + g * sk].
+struct Fp8Scales {
+  const float* p = nullptr;
+  int64_t si = 0, sk = 0;
+  int shift = 0;  // 0: one per row (column), 7: one per 128
+};
+
+// D = alpha * op(A) op(B) + beta * C
+struct Fp8Out {
+  int M = 0, N = 0;
+  float alpha = 1.0f, beta = 0.0f;
+  const void* C = nullptr;
+  void* D = nullptr;
+  int64_t ldc = 0, ldd = 0;
+  int bf16 = 0;  // type of C and D
+  int vec = 0;   // 1: rows of C and D start at multiples of 16 bytes
+};
+
+struct Fp8PairParams {
+  Fp8Out out;
+  int K = 0;
+  Fp8Scales sa, sb;
+  int a_mn = 0, b_mn = 0;  // 1: the stored rows run along M (N), not along K
+  uint32_t idesc = 0;
+  int tile_n = 0, tiles_m = 0, tiles_n = 0, clusters = 0;
+  uint64_t timeout_ns = 0;
+  unsigned* fault = nullptr;
+};
+cudaError_t prepare_fp8_pair();
+cudaError_t launch_fp8_pair(const CUtensorMap& mapA, const CUtensorMap& mapB, const Fp8PairParams& p,
+                            cudaStream_t stream);
+
+// The longer of M and N runs along the tensor-core rows (`l`), the other along the columns (`s`).
+struct Fp8ShortParams {
+  Fp8Out out;
+  int K = 0, L = 0, S = 0;
+  int trans = 0;  // 1: l runs along N (D_sl), 0: along M (D_ls)
+  Fp8Scales sl, ss;
+  int l_mn = 0, s_mn = 0;
+  uint32_t idesc = 0;
+  int tile_s = 0, tiles_l = 0, tiles_s = 0, split = 1, stages = 0, stage_bytes = 0;
+  uint64_t timeout_ns = 0;
+  unsigned* fault = nullptr;
+};
+cudaError_t prepare_fp8_short();
+constexpr int kFp8ShortMaxTile = 128, kFp8ShortMaxStages = 12;
+size_t fp8_short_smem(int tile_s, int stages, int stage_bytes);
+cudaError_t launch_fp8_short(const CUtensorMap& mapL, const CUtensorMap& mapS, const Fp8ShortParams& p,
+                             cudaStream_t stream);
+
+// Map over `outer` rows of `inner` 8-bit codes (row stride ld bytes, a multiple of 16): boxes of 128
+// codes x box_outer rows, 128-byte swizzle, zeros outside.
+cudaError_t encode_fp8_map(const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer,
+                           CUtensorMap* map);
+// Rows of `cols` codes copied to rows `ldd` apart (any alignment of the source).
+cudaError_t launch_fp8_repack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t ldd,
+                              cudaStream_t stream);
+// D = beta * C (alpha == 0 or K == 0).
+cudaError_t launch_fp8_scale(const Fp8Out& o, cudaStream_t stream);
+
 }  // namespace sgemm_impl

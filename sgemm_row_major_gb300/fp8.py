@@ -11,9 +11,10 @@ from __future__ import annotations
 import ctypes
 from collections import namedtuple
 
-from . import SgemmError, _ch, _ptr, _stream, load
+from . import PlanStruct, SgemmError, _ch, _stream, load
 
 FORMATS = {"e4m3": 0, "e5m2": 1}
+VARIANTS = {0: "AUTO", 1: "NONE", 2: "SCALE", 32: "FP8_PAIR", 33: "FP8_SHORT"}
 ROW, COL, BLOCK = (1, 128), (128, 1), (128, 128)
 
 
@@ -31,7 +32,12 @@ def _lib():
     if _functions is None:
         lib = load()
         i64, f32, vp, ci = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_int
+        mp, ch = ctypes.POINTER(MatrixStruct), ctypes.c_char
+        lib.sgemm_fp8_plan.restype = ci
+        lib.sgemm_fp8_plan.argtypes = [ch, ch, i64, i64, i64, f32, mp, mp, f32, vp, i64, vp, i64, ci, ci, ctypes.POINTER(PlanStruct)]
         for name, args in {
+            "sgemm_fp8": [ch, ch, i64, i64, i64, f32, mp, mp, f32, vp, i64, vp, i64, ci, vp],
+            "sgemm_fp8_set_override": [ci, ci, ci],
             "sgemm_fp8_quantize": [i64, i64, vp, ci, i64, ci, ci, ci, vp, i64, vp, i64, vp],
             "sgemm_fp8_rmsnorm": [i64, i64, ci, vp, i64, vp, i64, vp, f32, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp],
             "sgemm_fp8_rmsnorm_backward": [i64, i64, ci, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp],
@@ -142,6 +148,68 @@ def quantize_fp8(x, block=ROW, format="e4m3", stream=None) -> Fp8Matrix:
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_quantize")
     return m
+
+
+def _is_t(op) -> bool:
+    op = op.decode() if isinstance(op, bytes) else str(op)
+    if op[:1].upper() not in ("N", "T", "C"):
+        raise ValueError(f"unknown operation {op!r}: N or T")
+    return op[:1].upper() != "N"
+
+
+def matmul_fp8(A: Fp8Matrix, B: Fp8Matrix, C=None, transA="N", transB="N", alpha=1.0, beta=0.0, *, out=None, out_dtype=None,
+               stream=None):
+    """alpha * op(A) op(B) + beta * C on 8-bit matrices (sgemm_fp8), float32 or bfloat16.
+
+    A and B are the stored matrices; both must have groups of 128 along the summed dimension.  The result goes to `out`, else
+    to C in place, else to a new tensor of `out_dtype` (float32 unless given)."""
+    import torch
+    ta, tb = _is_t(transA), _is_t(transB)
+    M, K = A.data.shape[::-1] if ta else A.data.shape
+    N, kb = B.data.shape if tb else B.data.shape[::-1]
+    if kb != K:
+        raise ValueError("inner dimensions of op(A) and op(B) differ")
+    if C is None:
+        if beta != 0.0:
+            raise ValueError("beta != 0 needs C")
+        d = out if out is not None else _empty((M, N), out_dtype or torch.float32, A.data, stream)
+        c_ptr, ldc = None, max(N, 1)
+    else:
+        d = out if out is not None else C
+        _check(C, "C", 2, d.dtype)
+        if tuple(C.shape) != (M, N):
+            raise ValueError("C has the wrong shape")
+        c_ptr, ldc = C.data_ptr(), _ld(C)
+    t = _type(_check(d, "out").dtype)
+    if tuple(d.shape) != (M, N):
+        raise ValueError("out has the wrong shape")
+    if out_dtype is not None and d.dtype != out_dtype:
+        raise TypeError(f"out is {d.dtype}, not {out_dtype}")
+    st = _lib().sgemm_fp8(b"T" if ta else b"N", b"T" if tb else b"N", M, N, K, alpha, A._struct, B._struct, beta, c_ptr, ldc,
+                          d.data_ptr(), _ld(d), t, _stream(stream))
+    if st != 0:
+        raise SgemmError(st, "sgemm_fp8")
+    return d
+
+
+def sgemm_fp8_plan(transA, transB, M, N, K, alpha, A, B, beta, C, ldc, D, ldd, type, sm_count=0) -> dict:
+    """The launch sgemm_fp8() would make; A and B are MatrixStructs.  Raises on invalid arguments."""
+    plan = PlanStruct()
+    st = _lib().sgemm_fp8_plan(_ch(transA), _ch(transB), M, N, K, alpha, A, B, beta, C, ldc, D, ldd, type, sm_count,
+                               ctypes.byref(plan))
+    if st != 0:
+        raise SgemmError(st, "sgemm_fp8_plan")
+    out = {name: getattr(plan, name) for name, _ in PlanStruct._fields_}
+    out["variant_name"] = VARIANTS.get(out["variant"], str(out["variant"]))
+    return out
+
+
+def sgemm_fp8_set_override(variant="AUTO", tile_n=0, split=0) -> None:
+    """Forces sgemm_fp8()'s kernel ("FP8_PAIR", "FP8_SHORT"; "AUTO" restores the planner's choice), tile and K split."""
+    names = {v: k for k, v in VARIANTS.items()}
+    st = _lib().sgemm_fp8_set_override(names[variant], tile_n, split)
+    if st != 0:
+        raise SgemmError(st, "sgemm_fp8_set_override")
 
 
 NormOutput = namedtuple("NormOutput", "q h y rstd")
