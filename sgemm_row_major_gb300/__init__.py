@@ -425,8 +425,8 @@ def matmul(A, B, C=None, transA: str = "N", transB: str = "N", alpha: float = 1.
     return C
 
 
-from .fp8 import (Fp8Matrix, matmul_fp8, quantize_fp8, rmsnorm_fp8, rmsnorm_fp8_backward, sgemm_fp8_plan,  # noqa: E402
+from .fp8 import (Fp8Matrix, matmul_fp8, moe_fp8, quantize_fp8, rmsnorm_fp8, rmsnorm_fp8_backward, sgemm_fp8_plan,  # noqa: E402
                   sgemm_fp8_set_override)
 
-__all__ += ["Fp8Matrix", "matmul_fp8", "quantize_fp8", "rmsnorm_fp8", "rmsnorm_fp8_backward", "sgemm_fp8_plan",
+__all__ += ["Fp8Matrix", "matmul_fp8", "moe_fp8", "quantize_fp8", "rmsnorm_fp8", "rmsnorm_fp8_backward", "sgemm_fp8_plan",
             "sgemm_fp8_set_override"]

@@ -108,6 +108,7 @@ int device_state(int* device_out, DeviceState** st_out) {
       if (err == cudaSuccess) err = prepare_fp8_norm();
       if (err == cudaSuccess) err = prepare_fp8_pair();
       if (err == cudaSuccess) err = prepare_fp8_short();
+      if (err == cudaSuccess) err = prepare_fp8_moe();
       if (err == cudaSuccess) st.pair_clusters = pair_clusters_or_none();
       if (err == cudaSuccess && !st.pool) {
         cudaMemPoolProps props = {};

@@ -257,6 +257,36 @@ cudaError_t launch_product(const Product& pr, const sgemm_plan_t& plan, const Ca
   return launch_fp8_short(ma, mb, p, stream);
 }
 
+// ---------------------------------------------------------------- mixture of experts
+
+// Whether the stored rows x cols matrices of `experts` experts can be read.
+bool check_experts(const sgemm_fp8_experts_t* m, int64_t rows, int64_t cols, int64_t experts, bool read) {
+  if (!m) return !read;
+  if (m->ld < std::max<int64_t>(1, cols) || m->ld % 16 != 0 || m->ld > INT_MAX) return false;
+  if (m->lds < std::max<int64_t>(1, ceil_div(cols, 128))) return false;
+  if (experts > 1 && (m->stride < (rows - 1) * m->ld + cols || m->stride % 16 != 0 || m->stride >= (int64_t)1 << 39 ||
+                      m->stride_scale < (ceil_div(rows, 128) - 1) * m->lds + ceil_div(cols, 128)))
+    return false;
+  return !read || (m->data && aligned(m->data, 16) && m->scale && aligned(m->scale, 4));
+}
+
+cudaError_t experts_map(const sgemm_fp8_experts_t& m, int64_t rows, int64_t cols, int64_t experts, int box,
+                        CUtensorMap* map) {
+  return encode_fp8_maps(m.data, cols, rows, m.ld, experts, experts > 1 ? m.stride : m.ld, box, map);
+}
+
+// Pieces of one workspace, 256 bytes apart (counted first, then placed).
+struct Pieces {
+  uint8_t* base = nullptr;
+  int64_t at = 0;
+  template <typename T>
+  T* take(int64_t n) {
+    T* r = base ? reinterpret_cast<T*>(base + at) : nullptr;
+    at += round256(n * (int64_t)sizeof(T));
+    return r;
+  }
+};
+
 int launch_status(cudaError_t e) { return e == cudaSuccess ? SGEMM_OK : record_cuda_failure(e); }
 
 }  // namespace
@@ -469,6 +499,103 @@ int sgemm_fp8_rmsnorm_backward(int64_t rows, int64_t cols, int type, const void*
     if (e == cudaSuccess) e = ef;
   }
   return launch_status(e);
+}
+
+int sgemm_fp8_moe(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts, int top_k,
+                  const sgemm_fp8_matrix_t* X, const float* logits, int64_t ldl, int renormalize,
+                  const sgemm_fp8_experts_t* gate, const sgemm_fp8_experts_t* up, const sgemm_fp8_experts_t* down,
+                  void* Y, int64_t ldy, int type, struct CUstream_st* stream_) {
+  if (tokens < 0) return -1;
+  if (hidden < 0) return -2;
+  if (inner < 0) return -3;
+  if (experts < 0) return -4;
+  if (top_k < 0 || top_k > experts) return -5;
+  const bool work = tokens > 0 && hidden > 0, read = work && inner > 0 && top_k > 0;
+  Operand x;
+  if (!check_operand(X, tokens, hidden, false, read, &x)) return -6;
+  if (X && (X->format != SGEMM_FP8_E4M3 || X->block_rows != 1)) return -6;
+  if (read && (!logits || !aligned(logits, 4))) return -7;
+  if (ldl < std::max<int64_t>(1, experts)) return -8;
+  if (!check_experts(gate, inner, hidden, experts, read)) return -10;
+  if (!check_experts(up, inner, hidden, experts, read)) return -11;
+  if (!check_experts(down, hidden, inner, experts, read)) return -12;
+  if (!known_type(type)) return -15;
+  if (work && (!Y || !aligned(Y, type_size(type)))) return -13;
+  if (ldy < std::max<int64_t>(1, hidden)) return -14;
+  if (!work) return SGEMM_OK;
+  if (tokens > kMoeMaxTokens || experts > kMoeMaxExperts || top_k > kMoeMaxTopK || hidden % 16 != 0 ||
+      inner % 16 != 0 || hidden > kMaxDim || inner > kMaxDim || ldy > INT_MAX || (X && X->ld > INT_MAX))
+    return SGEMM_ERR_UNSUPPORTED;
+  CallDevice dev;
+  const int s = call_device(&dev);
+  if (s != SGEMM_OK) return s;
+  cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
+  if (!read) {  // a sum of nothing
+    return launch_status(cudaMemset2DAsync(Y, (size_t)ldy * type_size(type), 0, (size_t)hidden * type_size(type),
+                                           (size_t)tokens, stream));
+  }
+  MoeParams p;
+  p.tokens = (int)tokens;
+  p.hidden = (int)hidden;
+  p.inner = (int)inner;
+  p.experts = (int)experts;
+  p.top_k = top_k;
+  p.renormalize = renormalize != 0;
+  p.logits = logits;
+  p.ldl = ldl;
+  p.sx = X->scale;
+  p.ldsx = X->lds;
+  p.sg = gate->scale;
+  p.su = up->scale;
+  p.sd = down->scale;
+  p.ldsg = gate->lds;
+  p.ldsu = up->lds;
+  p.ldsd = down->lds;
+  p.stride_sg = gate->stride_scale;
+  p.stride_su = up->stride_scale;
+  p.stride_sd = down->stride_scale;
+  p.h_groups = (int)ceil_div(inner, 64);
+  p.y = Y;
+  p.ldy = ldy;
+  p.bf16 = type == SGEMM_BF16;
+  p.slots_max = (int)tokens * top_k;
+  p.active_max = (int)std::min<int64_t>(experts, p.slots_max);
+  p.timeout_ns = wait_timeout_ns();
+  p.fault = dev.fault;
+  shape_fp8_moe(&p, dev.sm_count);
+  uint8_t* x_copy = nullptr;
+  const auto place = [&](Pieces* w) {
+    p.h = w->take<uint8_t>(2 * (int64_t)p.slots_max * inner);
+    p.sh = w->take<float>((int64_t)p.slots_max * p.h_groups);
+    p.route.counts = w->take<int>(1);
+    p.route.expert = w->take<int>(p.active_max);
+    p.route.base = w->take<int>(p.active_max);
+    p.route.mask = w->take<unsigned long long>(p.active_max);
+    p.route.slot_token = w->take<int>(p.slots_max);
+    p.route.slot_weight = w->take<float>(p.slots_max);
+    p.route.poisoned = w->take<int>(tokens);
+    x_copy = w->take<uint8_t>(repack_bytes(x));
+  };
+  Pieces count;
+  place(&count);
+  void* ws = nullptr;
+  cudaError_t e = cudaMallocFromPoolAsync(&ws, (size_t)count.at, dev.pool, stream);
+  if (e != cudaSuccess) {
+    record_cuda_failure(e);
+    return e == cudaErrorMemoryAllocation ? SGEMM_ERR_NOMEM : SGEMM_ERR_CUDA;
+  }
+  Pieces w;
+  w.base = static_cast<uint8_t*>(ws);
+  place(&w);
+  MoeMaps maps;
+  e = operand_map(x, (int)ceil_div(tokens, 16) * 16, &x_copy, &maps.x, stream);
+  if (e == cudaSuccess) e = experts_map(*gate, inner, hidden, experts, 64, &maps.gate);
+  if (e == cudaSuccess) e = experts_map(*up, inner, hidden, experts, 64, &maps.up);
+  if (e == cudaSuccess) e = experts_map(*down, hidden, inner, experts, 128, &maps.down);
+  if (e == cudaSuccess) e = encode_fp8_map(p.h, inner, 2 * (int64_t)p.slots_max, inner, 32, &maps.h);
+  if (e == cudaSuccess) e = launch_fp8_moe(maps, p, dev.sm_count, stream);
+  const cudaError_t ef = cudaFreeAsync(ws, stream);
+  return launch_status(e == cudaSuccess ? ef : e);
 }
 
 }  // extern "C"

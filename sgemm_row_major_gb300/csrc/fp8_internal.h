@@ -119,10 +119,54 @@ size_t fp8_short_smem(int tile_s, int stages, int stage_bytes);
 cudaError_t launch_fp8_short(const CUtensorMap& mapL, const CUtensorMap& mapS, const Fp8ShortParams& p,
                              cudaStream_t stream);
 
+// ---- mixture of experts for a few tokens (kernel_fp8_moe.cu)
+constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 1024, kMoeMaxTopK = 16;
+// What the first kernel leaves for the second: the experts that some token chose (ascending), each
+// with its tokens, and a slot per (expert, token), numbered in that order.
+struct MoeRoute {
+  int* counts = nullptr;                  // [0]: active experts
+  int* expert = nullptr;                  // [active]
+  int* base = nullptr;                    // [active] first slot
+  unsigned long long* mask = nullptr;     // [active] bit t: token t chose the expert
+  int* slot_token = nullptr;              // [slots]
+  float* slot_weight = nullptr;           // [slots]
+  int* poisoned = nullptr;                // [tokens] 1: a NaN or +Inf logit
+};
+struct MoeParams {
+  int tokens = 0, hidden = 0, inner = 0, experts = 0, top_k = 0, renormalize = 0;
+  const float* logits = nullptr;
+  int64_t ldl = 0;
+  const float* sx = nullptr;              // scales of X, row stride ldsx
+  int64_t ldsx = 0;
+  const float *sg = nullptr, *su = nullptr, *sd = nullptr;  // scales of gate, up, down
+  int64_t ldsg = 0, ldsu = 0, ldsd = 0, stride_sg = 0, stride_su = 0, stride_sd = 0;
+  uint8_t* h = nullptr;                   // inner values: slot j has rows 2j (hi) and 2j + 1 (lo * 16) of `inner` codes
+  float* sh = nullptr;                    // [slots][h_groups], one scale per 64 of them
+  int h_groups = 0;
+  MoeRoute route;
+  void* y = nullptr;
+  int64_t ldy = 0;
+  int bf16 = 0;
+  int up_stages = 0, down_stages = 0, split = 1;
+  int active_max = 0, slots_max = 0;      // bounds of the routing arrays
+  uint64_t timeout_ns = 0;
+  unsigned* fault = nullptr;
+};
+struct MoeMaps {
+  CUtensorMap x, gate, up, h, down;
+};
+cudaError_t prepare_fp8_moe();
+// Fills the launch shape (stages, split) of p.
+void shape_fp8_moe(MoeParams* p, int sm_count);
+cudaError_t launch_fp8_moe(const MoeMaps& maps, const MoeParams& p, int sm_count, cudaStream_t stream);
+
 // Map over `outer` rows of `inner` 8-bit codes (row stride ld bytes, a multiple of 16): boxes of 128
 // codes x box_outer rows, 128-byte swizzle, zeros outside.
 cudaError_t encode_fp8_map(const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer,
                            CUtensorMap* map);
+// The same over `products` such matrices `stride` bytes apart (a multiple of 16).
+cudaError_t encode_fp8_maps(const void* base, int64_t inner, int64_t outer, int64_t ld, int64_t products,
+                            int64_t stride, int box_outer, CUtensorMap* map);
 // Rows of `cols` codes copied to rows `ldd` apart (any alignment of the source).
 cudaError_t launch_fp8_repack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t ldd,
                               cudaStream_t stream);

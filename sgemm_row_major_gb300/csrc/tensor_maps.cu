@@ -93,21 +93,26 @@ cudaError_t encode_bf16_map(const void* base, int64_t K, int64_t rows, int64_t l
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t encode_fp8_map(const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer,
-                           CUtensorMap* map) {
+cudaError_t encode_fp8_maps(const void* base, int64_t inner, int64_t outer, int64_t ld, int64_t products,
+                            int64_t stride, int box_outer, CUtensorMap* map) {
   cudaError_t e = bind_primary_context();
   if (e != cudaSuccess) return e;
   EncodeTiledFn fn = nullptr;
   e = encode_fn(&fn);
   if (e != cudaSuccess) return e;
-  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, 1};
-  const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)ld};  // one matrix: the second is not used
+  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, (cuuint64_t)products};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld, (cuuint64_t)stride};
   const cuuint32_t box[3] = {128u, (cuuint32_t)box_outer, 1u};
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_fp8_map(const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer,
+                           CUtensorMap* map) {
+  return encode_fp8_maps(base, inner, outer, ld, 1, ld, box_outer, map);  // one matrix: its stride is not used
 }
 
 cudaError_t encode_matrix_map(const float* base, int64_t inner, int64_t outer, int64_t ld, int box_inner,

@@ -23,6 +23,11 @@ class MatrixStruct(ctypes.Structure):
                 ("format", ctypes.c_int), ("block_rows", ctypes.c_int), ("block_cols", ctypes.c_int)]
 
 
+class ExpertsStruct(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("ld", ctypes.c_int64), ("stride", ctypes.c_int64), ("scale", ctypes.c_void_p),
+                ("lds", ctypes.c_int64), ("stride_scale", ctypes.c_int64)]
+
+
 _functions = None
 
 
@@ -32,12 +37,13 @@ def _lib():
     if _functions is None:
         lib = load()
         i64, f32, vp, ci = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_int
-        mp, ch = ctypes.POINTER(MatrixStruct), ctypes.c_char
+        mp, ep, ch = ctypes.POINTER(MatrixStruct), ctypes.POINTER(ExpertsStruct), ctypes.c_char
         lib.sgemm_fp8_plan.restype = ci
         lib.sgemm_fp8_plan.argtypes = [ch, ch, i64, i64, i64, f32, mp, mp, f32, vp, i64, vp, i64, ci, ci, ctypes.POINTER(PlanStruct)]
         for name, args in {
             "sgemm_fp8": [ch, ch, i64, i64, i64, f32, mp, mp, f32, vp, i64, vp, i64, ci, vp],
             "sgemm_fp8_set_override": [ci, ci, ci],
+            "sgemm_fp8_moe": [i64, i64, i64, i64, ci, mp, vp, i64, ci, ep, ep, ep, vp, i64, ci, vp],
             "sgemm_fp8_quantize": [i64, i64, vp, ci, i64, ci, ci, ci, vp, i64, vp, i64, vp],
             "sgemm_fp8_rmsnorm": [i64, i64, ci, vp, i64, vp, i64, vp, f32, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp],
             "sgemm_fp8_rmsnorm_backward": [i64, i64, ci, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp],
@@ -269,3 +275,45 @@ def rmsnorm_fp8_backward(dy, h, weight, rstd, dh=None, *, stream=None):
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_rmsnorm_backward")
     return dx, dw
+
+
+def _experts(w, name, experts, rows, cols) -> ExpertsStruct:
+    import torch
+    data, scale = w
+    _check(data, name, 3, torch.float8_e4m3fn)
+    _check(scale, name + " scales", 3, torch.float32)
+    if tuple(data.shape) != (experts, rows, cols):
+        raise ValueError(f"{name} must have shape {(experts, rows, cols)}, got {tuple(data.shape)}")
+    if tuple(scale.shape) != (experts, -(-rows // 128), -(-cols // 128)):
+        raise ValueError(f"{name} scales must have shape {(experts, -(-rows // 128), -(-cols // 128))}, got {tuple(scale.shape)}")
+    return ExpertsStruct(data.data_ptr(), data.stride(1), data.stride(0), scale.data_ptr(), max(scale.stride(1), 1), scale.stride(0))
+
+
+def moe_fp8(x: Fp8Matrix, logits, top_k, gate, up, down, *, renormalize=True, out=None, out_dtype=None, stream=None):
+    """A mixture-of-experts layer for a few tokens (sgemm_fp8_moe): for each row t of x the sum over the `top_k` experts with
+    the largest logits (ties: lowest index) of their softmax weight times down_e (silu(gate_e x_t) * (up_e x_t)).
+
+    x: E4M3 with groups of (1, 128), at most 64 rows; logits: float32 [tokens, experts]; gate and up: (codes [experts, inner,
+    hidden], scales [experts, inner / 128, hidden / 128]) with groups of 128 x 128, down: [experts, hidden, inner].  The
+    weights are divided by their sum over the chosen experts with renormalize=True.  Returns bfloat16 unless out_dtype or
+    out says otherwise."""
+    import torch
+    _check(logits, "logits", 2, torch.float32)
+    tokens, hidden = x.data.shape
+    experts, inner = gate[0].shape[:2]
+    if tuple(logits.shape) != (tokens, experts):
+        raise ValueError("logits must have one value per token and expert")
+    g = _experts(gate, "gate", experts, inner, hidden)
+    u = _experts(up, "up", experts, inner, hidden)
+    d = _experts(down, "down", experts, hidden, inner)
+    y = out if out is not None else _empty((tokens, hidden), out_dtype or torch.bfloat16, x.data, stream)
+    if tuple(y.shape) != (tokens, hidden):
+        raise ValueError("out has the wrong shape")
+    t = _type(_check(y, "out").dtype)
+    if out_dtype is not None and y.dtype != out_dtype:
+        raise TypeError(f"out is {y.dtype}, not {out_dtype}")
+    st = _lib().sgemm_fp8_moe(tokens, hidden, inner, experts, top_k, x._struct, logits.data_ptr(), _ld(logits), 1 if renormalize else 0,
+                              g, u, d, y.data_ptr(), _ld(y), t, _stream(stream))
+    if st != 0:
+        raise SgemmError(st, "sgemm_fp8_moe")
+    return y
