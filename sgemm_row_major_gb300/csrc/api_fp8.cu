@@ -157,9 +157,9 @@ int plan_product(const Product& pr, int sm_count, int pair_clusters, sgemm_plan_
   if (variant == SGEMM_VARIANT_FP8_PAIR) {
     plan->tile_m = 256;
     plan->tile_n = force_tile ? force_tile : pair_tile_n(pr.M, pr.N, clusters);
-    plan->stages = 6;
-    plan->threads = 320;
-    plan->smem_bytes = 6 * 32768 + 1024;
+    plan->stages = kFp8PairStages;
+    plan->threads = kFp8PairThreads;
+    plan->smem_bytes = fp8_pair_smem(pr.b.scales.shift == 0);
     tiles = ceil_div(pr.M, 256) * ceil_div(pr.N, plan->tile_n);
     plan->grid_x = 2 * std::min<int64_t>(tiles, clusters);
   } else {

@@ -51,6 +51,65 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// Bounded wait of a whole warp for a barrier phase, for waits that are short: every lane polls (each
+// has its own acquire), the clock is read only now and then, and nothing is called, so the sums that
+// the fold keeps in registers stay there.  Warp-uniform.
+__device__ __forceinline__ bool poll_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  bool ok = mbar_try_wait(bar, parity);
+  if (!__all_sync(0xffffffffu, ok)) {
+    const uint64_t t0 = global_timer_ns();
+    for (;;) {
+#pragma unroll 1
+      for (int i = 0; i < 32 && !ok; ++i) ok = mbar_try_wait(bar, parity);
+      if (ok || global_timer_ns() - t0 > timeout_ns) break;
+    }
+    ok = __all_sync(0xffffffffu, ok);
+  }
+  return ok;
+}
+
+// The same for one thread.
+__device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+#pragma unroll 1
+    for (int i = 0; i < 32; ++i)
+      if (mbar_try_wait(bar, parity)) return true;
+    if (global_timer_ns() - t0 > timeout_ns) return false;
+  }
+}
+
+// 8 consecutive 32-bit columns of this thread's TMEM lane.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
+  uint32_t r[8];
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(taddr)
+               : "memory");
+#pragma unroll
+  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// 4 bytes from global to shared memory, asynchronously.
+__device__ __forceinline__ void copy4_async(uint32_t dst, const float* src) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
+}
+// Arrives on `bar` (one of the arrivals it counts) when this thread's copies so far have landed.
+__device__ __forceinline__ void copies_arrive(uint32_t bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void copies_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
+
+template <int REGS>
+__device__ __forceinline__ void fewer_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+template <int REGS>
+__device__ __forceinline__ void more_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
+}
+
 __device__ __forceinline__ float read_c(const Fp8Out& o, int64_t i) {
   return o.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(o.C)[i]) : static_cast<const float*>(o.C)[i];
 }
@@ -64,34 +123,66 @@ __device__ __forceinline__ void store_one(const Fp8Out& o, int64_t row, int64_t 
   else        static_cast<float*>(o.D)[i] = x;
 }
 
-// Columns col .. col + 7 of a row (col a multiple of 8, all below N, out.vec): 16-byte vectors.
-__device__ __forceinline__ void store_eight(const Fp8Out& o, int64_t row, int64_t col, const float* v) {
-  float x[8];
+// Columns col .. col + 3 of a row, as far as they are in D, from their sums; vectors where out.vec
+// (col is a multiple of 4).
+__device__ __forceinline__ void store_four(const Fp8Out& o, int64_t row, int col, const float4 v) {
+  if (!o.vec || col + 4 > o.N) {
+    const float x[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = o.alpha * v[e];
+    for (int e = 0; e < 4; ++e)
+      if (col + e < o.N) store_one(o, row, col + e, x[e]);
+    return;
+  }
+  float4 x = make_float4(o.alpha * v.x, o.alpha * v.y, o.alpha * v.z, o.alpha * v.w);
+  if (o.beta != 0.0f) {
+    float4 c;
+    const int64_t i = row * o.ldc + col;
+    if (o.bf16) {
+      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(o.C) + i);
+      c = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
+                      __uint_as_float(u.y & 0xFFFF0000u));
+    } else {
+      c = *reinterpret_cast<const float4*>(static_cast<const float*>(o.C) + i);
+    }
+    x = make_float4(fmaf(o.alpha, v.x, o.beta * c.x), fmaf(o.alpha, v.y, o.beta * c.y),
+                    fmaf(o.alpha, v.z, o.beta * c.z), fmaf(o.alpha, v.w, o.beta * c.w));
+  }
+  const int64_t i = row * o.ldd + col;
   if (o.bf16) {
-    if (o.beta != 0.0f) {
-      Chunk<__nv_bfloat16> c;
-      float old[8];
-      c.raw = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(o.C) + row * o.ldc + col);
-      c.get(old);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fmaf(o.alpha, v[e], o.beta * old[e]);
-    }
-    Chunk<__nv_bfloat16> c;
-    c.put(x);
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(o.D) + row * o.ldd + col) = c.raw;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.D) + i) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   } else {
-    if (o.beta != 0.0f) {
-      const float4* c = reinterpret_cast<const float4*>(static_cast<const float*>(o.C) + row * o.ldc + col);
-      const float4 a = c[0], b = c[1];
-      const float old[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    *reinterpret_cast<float4*>(static_cast<float*>(o.D) + i) = x;
+  }
+}
+
+// Columns col .. col + 3 (as far as they are in D) of rows row, row + 8, row + 16 and row + 24 from
+// their sums, at v and 8, 16 and 24 pitches further: four lanes hold 16 consecutive columns, so a
+// warp's store writes 64 (BF16: 32) consecutive bytes of 8 rows.
+__device__ __forceinline__ void store_rows(const Fp8Out& o, int row, int col, const float* v, int pitch) {
+  if (o.vec && col + 4 <= o.N && o.beta == 0.0f) {
+    const int64_t step = 8 * o.ldd;
+    int64_t i = (int64_t)row * o.ldd + col;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = fmaf(o.alpha, v[e], o.beta * old[e]);
+    for (int r = 0; r < 4; ++r, i += step) {
+      const float4 x = *reinterpret_cast<const float4*>(v + 8 * r * pitch);
+      if (row + 8 * r < o.M) {
+        if (o.bf16) {
+          const __nv_bfloat162 a = __floats2bfloat162_rn(o.alpha * x.x, o.alpha * x.y);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(o.alpha * x.z, o.alpha * x.w);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.D) + i) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        } else {
+          *reinterpret_cast<float4*>(static_cast<float*>(o.D) + i) =
+              make_float4(o.alpha * x.x, o.alpha * x.y, o.alpha * x.z, o.alpha * x.w);
+        }
+      }
     }
-    float4* d = reinterpret_cast<float4*>(static_cast<float*>(o.D) + row * o.ldd + col);
-    d[0] = make_float4(x[0], x[1], x[2], x[3]);
-    d[1] = make_float4(x[4], x[5], x[6], x[7]);
+  } else {
+#pragma unroll 1
+    for (int r = 0; r < 4; ++r)
+      if (row + 8 * r < o.M) store_four(o, row + 8 * r, col, *reinterpret_cast<const float4*>(v + 8 * r * pitch));
   }
 }
 

@@ -97,6 +97,8 @@ struct Fp8PairParams {
   uint64_t timeout_ns = 0;
   unsigned* fault = nullptr;
 };
+constexpr int kFp8PairStages = 5, kFp8PairThreads = 640;
+int64_t fp8_pair_smem(bool cols);  // dynamic shared memory; cols: B has a scale per column
 cudaError_t prepare_fp8_pair();
 cudaError_t launch_fp8_pair(const CUtensorMap& mapA, const CUtensorMap& mapB, const Fp8PairParams& p,
                             cudaStream_t stream);

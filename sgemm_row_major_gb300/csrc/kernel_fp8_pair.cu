@@ -28,14 +28,33 @@ using namespace tc;
 constexpr int BM = 256, BMC = 128, BK = 128;
 constexpr int kPart = 128 * BK;           // 16 KB: one operand's tile in one CTA
 constexpr int kStageBytes = 2 * kPart;
-constexpr int kStages = 6;
-constexpr int kSmemBytes = kStages * kStageBytes + 1024;
-constexpr int kFoldWarps = 8;
-constexpr int kThreads = 32 * (2 + kFoldWarps);
-constexpr int kAccBufs = 2;
-constexpr uint32_t kAccCols = 256;
+constexpr int kStages = kFp8PairStages;
+constexpr int kChunk = 8;                 // groups whose scales are loaded together
+constexpr int kOutPitch = 20;             // words between the rows of a warp's 32 x 16 piece of D (16-byte accesses
+                                          // by row and by column both hit 32 banks)
+constexpr int kFirstFold = 4;             // warps 0-3: loads, products, scales of A, scales of B
+constexpr int kFoldWarps = 16;
+constexpr int kThreads = 32 * (kFirstFold + kFoldWarps);
+static_assert(kThreads == kFp8PairThreads, "the plan's figure");
+// 640 threads are launched with 96 registers each; the four warps that move data give most of
+// theirs to the folders: 128 x 32 + 512 x 112 = 640 x 96.
+constexpr int kMoverRegs = 32, kFoldRegs = 112;
+static_assert(128 * kMoverRegs + 32 * kFoldWarps * kFoldRegs <= kThreads * 96, "registers at launch");
+constexpr int kMaxBufs = 4;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxHalf = 128;             // accumulator columns a folder thread owns at most
+constexpr int kMaxCols = 64;              // accumulator columns a folder thread owns at most
+constexpr int kLoadCols = 32;             // of which it loads so many at a time
+
+// Scales of a chunk of groups: of the CTA's 128 rows, and of the tile's columns (COLS) or its two or
+// three column blocks.
+template <bool COLS>
+struct ScaleCfg {
+  static constexpr int kB = COLS ? 256 : 4;
+  static constexpr int kChunks = COLS ? 2 : 4;  // in shared memory
+  static constexpr int kFloats = kChunk * (BMC + kB);
+  static constexpr int kSmem = kStages * kStageBytes + kChunks * kFloats * 4 + kFoldWarps * 32 * kOutPitch * 4 + 1024;
+  static_assert(kSmem + 1024 <= 232448, "shared memory per CTA");
+};
 
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster,
                                               int32_t inner, int32_t outer) {
@@ -46,25 +65,22 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-// The 128 threads of the four warps that share a half of the accumulator's columns.
-__device__ __forceinline__ void half_barrier(int half) {
-  asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
-}
-
 // COLS: B has one scale per column (weight gradients), else one per 128 columns.
 template <bool COLS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                     const __grid_constant__ Fp8PairParams p) {
+  using Sc = ScaleCfg<COLS>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kStages], empty[kStages];
-  __shared__ __align__(8) uint64_t acc_full[kAccBufs], acc_empty[kAccBufs];
+  __shared__ __align__(8) uint64_t full[kStages], done[kStages];
+  __shared__ __align__(8) uint64_t acc_empty[kMaxBufs];
+  __shared__ __align__(8) uint64_t scale_full[Sc::kChunks], scale_empty[Sc::kChunks];
   __shared__ __align__(8) uint64_t fin;
   __shared__ uint32_t tmem_slot;
-  __shared__ __align__(16) float col_scale[COLS ? 2 : 1][2][COLS ? kMaxHalf : 1];
 
   const uint32_t raw_addr = smem_addr(smem_raw);
-  const uint32_t sbase = raw_addr + ((1024u - (raw_addr & 1023u)) & 1023u);
+  const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+  const uint32_t sbase = raw_addr + pad;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cl = (int)cluster_id_x();
@@ -72,16 +88,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int tiles = p.tiles_m * p.tiles_n;
   const int my_tiles = cl < tiles ? (tiles - cl + p.clusters - 1) / p.clusters : 0;
   const int units = my_tiles * groups;
-  const int halfn = p.tile_n / 2;  // columns of B this CTA loads, and accumulator columns of a folder
+  const int halfn = p.tile_n / 2;  // columns of B this CTA loads
+  const int bufs = min(kMaxBufs, (int)kTmemCols / p.tile_n);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
-      mbar_init(smem_addr(&empty[s]), 1);
+      mbar_init(smem_addr(&done[s]), 1);
     }
-    for (int b = 0; b < kAccBufs; ++b) {
-      mbar_init(smem_addr(&acc_full[b]), 1);
+    for (int b = 0; b < kMaxBufs; ++b) {
       mbar_init(smem_addr(&acc_empty[b]), 2 * kFoldWarps);
+    }
+    for (int c = 0; c < Sc::kChunks; ++c) {
+      mbar_init(smem_addr(&scale_full[c]), 64);  // the threads of the two warps that load them
+      mbar_init(smem_addr(&scale_empty[c]), kFoldWarps);
     }
     mbar_init(smem_addr(&fin), 1);
     fence_mbar_init();
@@ -91,189 +111,238 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_slot;
-
-  if (warp == 0) {
-    // ------------------------------------------------ loads (each CTA: its rows of A, its columns of B)
-    if (lane == 0) {
-      prefetch_tensormap(&mapA);
-      prefetch_tensormap(&mapB);
-      const uint32_t bytes = 2u * (uint32_t)(kPart + (p.b_mn ? kPart : halfn * BK));  // both CTAs'
-      int t = 0;
+  if (warp < kFirstFold) {
+    fewer_registers<kMoverRegs>();
+    if (warp == 0) {
+      // ------------------------------------------------ loads (each CTA: its rows of A, its columns of B)
+      if (lane == 0) {
+        prefetch_tensormap(&mapA);
+        prefetch_tensormap(&mapB);
+        const uint32_t bytes = 2u * (uint32_t)(kPart + (p.b_mn ? kPart : halfn * BK));  // both CTAs'
+        int t = 0;
+        bool ok = true;
+        for (int i = 0; ok && i < my_tiles; ++i) {
+          int tm, tn;
+          tile_coords(cl + i * p.clusters, p.tiles_m, p.tiles_n, tm, tn);
+          const int m0 = tm * BM + BMC * (int)rank, n0 = tn * p.tile_n + halfn * (int)rank;
+          for (int g = 0; g < groups; ++g, ++t) {
+            const int s = t % kStages;
+            if (t >= kStages && !spin_wait(smem_addr(&done[s]), (uint32_t)((t / kStages) - 1) & 1u, p.timeout_ns)) {
+              atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+              ok = false;
+              break;
+            }
+            // both CTAs' loads complete on the even CTA's barrier, which expects all their bytes
+            const uint32_t fb = map_to_rank(smem_addr(&full[s]), 0);
+            if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), bytes);
+            const uint32_t a = sbase + (uint32_t)(s * kStageBytes), b = a + kPart;
+            tma_load_pair(a, &mapA, fb, p.a_mn ? m0 : g * BK, p.a_mn ? g * BK : m0);
+            tma_load_pair(b, &mapB, fb, p.b_mn ? n0 : g * BK, p.b_mn ? g * BK : n0);
+          }
+        }
+        // leave only when every copy into shared memory has landed (the odd CTA's warp 1 waits for
+        // the products that read its last stages)
+        if (rank == 0)
+          for (int u = t > kStages ? t - kStages : 0; u < t; ++u)
+            if (!mbar_wait(smem_addr(&full[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns))
+              atomicOr(p.fault, (unsigned)kFaultDrainWait);
+      }
+    } else if (warp == 1) {
+      if (lane == 0 && rank != 0) {
+        bool ok = true;
+        for (int u = units > kStages ? units - kStages : 0; ok && u < units; ++u)
+          ok = mbar_wait(smem_addr(&done[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns);
+        if (!ok) atomicOr(p.fault, (unsigned)kFaultFullWait);
+      } else if (lane == 0) {
+        // ---------------------------------------------- products (even CTA)
+        const uint64_t astep = step_of(p.a_mn), bstep = step_of(p.b_mn);
+        int t = 0, b = 0;
+        uint32_t lap = 0;  // passes over the accumulators
+        bool ok = true;
+        for (; t < units; ++t) {
+          const int s = t % kStages;
+          ok = (lap == 0 || spin_wait(smem_addr(&acc_empty[b]), (lap - 1) & 1u, p.timeout_ns)) &&
+               spin_wait(smem_addr(&full[s]), (uint32_t)(t / kStages) & 1u, p.timeout_ns);
+          if (!ok) break;
+          tmem_fence_after_sync();
+          const uint32_t acc = tmem + (uint32_t)(b * p.tile_n);
+          const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
+          const uint64_t ad = tile_desc(a), bd = tile_desc(a + kPart);
+#pragma unroll
+          for (int ks = 0; ks < BK / 32; ++ks)
+            mma_f8_pair(acc, ad + (uint64_t)ks * astep, bd + (uint64_t)ks * bstep, p.idesc, ks == 0 ? 0u : 1u);
+          mma_commit_pair(smem_addr(&done[s]));  // in both CTAs: stage s is free, the accumulator holds group t
+          if (++b == bufs) {
+            b = 0;
+            ++lap;
+          }
+        }
+        if (!ok) atomicOr(p.fault, (unsigned)kFaultFullWait);
+        // leave only when every product has completed and its commits have landed here
+        for (int u = t > kStages ? t - kStages : 0; u < t; ++u)
+          if (!mbar_wait(smem_addr(&done[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns))
+            atomicOr(p.fault, (unsigned)kFaultDrainWait);
+      }
+    } else {
+      // ------------------------------------------------ scales, 8 groups at a time, up to kChunks ahead
+      // of the folders (the latency of a load is several groups' time): warp 2 of this CTA's 128 rows,
+      // warp 3 of the tile's columns or column blocks.
+      const uint32_t ring = sbase + (uint32_t)(kStages * kStageBytes);
+      int c = 0;
+      uint32_t lap = 0;
       bool ok = true;
       for (int i = 0; ok && i < my_tiles; ++i) {
         int tm, tn;
         tile_coords(cl + i * p.clusters, p.tiles_m, p.tiles_n, tm, tn);
-        const int m0 = tm * BM + BMC * (int)rank, n0 = tn * p.tile_n + halfn * (int)rank;
-        for (int g = 0; g < groups; ++g, ++t) {
-          const int s = t % kStages;
-          if (t >= kStages && !mbar_wait(smem_addr(&empty[s]), (uint32_t)((t / kStages) - 1) & 1u, p.timeout_ns)) {
-            atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+        const bool rows = warp == 2;
+        const int first = rows ? tm * BM + BMC * (int)rank : tn * p.tile_n;
+        const int last = (rows ? p.out.M : p.out.N) - 1;
+        const Fp8Scales& sc = rows ? p.sa : p.sb;
+        const int n = rows ? BMC : COLS ? p.tile_n : 3;
+        const int pitch = rows ? BMC : Sc::kB;
+        for (int g0 = 0; g0 < groups; g0 += kChunk) {
+          if (lap > 0 && !poll_wait(smem_addr(&scale_empty[c]), (lap - 1) & 1u, p.timeout_ns)) {
+            if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
             ok = false;
             break;
           }
-          // both CTAs' loads complete on the even CTA's barrier, which expects all their bytes
-          const uint32_t fb = map_to_rank(smem_addr(&full[s]), 0);
-          if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), bytes);
-          const uint32_t a = sbase + (uint32_t)(s * kStageBytes), b = a + kPart;
-          tma_load_pair(a, &mapA, fb, p.a_mn ? m0 : g * BK, p.a_mn ? g * BK : m0);
-          tma_load_pair(b, &mapB, fb, p.b_mn ? n0 : g * BK, p.b_mn ? g * BK : n0);
+          const uint32_t dst = ring + 4u * (uint32_t)(c * Sc::kFloats + (rows ? 0 : kChunk * BMC));
+          const int count = min(kChunk, groups - g0);
+          for (int j = lane; j < n; j += 32) {
+            const int64_t at = rows || COLS ? min(first + j, last) >> sc.shift : min((first >> 7) + j, last >> 7);
+            const float* src = sc.p + at * sc.si + (int64_t)g0 * sc.sk;
+            for (int g = 0; g < count; ++g) copy4_async(dst + 4u * (uint32_t)(g * pitch + j), src + (int64_t)g * sc.sk);
+          }
+          copies_arrive(smem_addr(&scale_full[c]));
+          if (++c == Sc::kChunks) {
+            c = 0;
+            ++lap;
+          }
         }
       }
-      // leave only when every copy into shared memory has landed (the odd CTA's warp 1 waits for
-      // the products that read its last stages)
-      if (rank == 0)
-        for (int u = t > kStages ? t - kStages : 0; u < t; ++u)
-          if (!mbar_wait(smem_addr(&full[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns))
-            atomicOr(p.fault, (unsigned)kFaultDrainWait);
-    }
-  } else if (warp == 1) {
-    if (lane == 0 && rank != 0) {
-      bool ok = true;
-      for (int u = units > kStages ? units - kStages : 0; ok && u < units; ++u)
-        ok = mbar_wait(smem_addr(&empty[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns);
-      if (!ok) atomicOr(p.fault, (unsigned)kFaultFullWait);
-    } else if (lane == 0) {
-      // ---------------------------------------------- products (even CTA)
-      const uint64_t astep = step_of(p.a_mn), bstep = step_of(p.b_mn);
-      int t_done = -1;
-      bool ok = true;
-      for (int t = 0; ok && t < units; ++t) {
-        const int s = t % kStages, b = t % kAccBufs;
-        ok = (t < kAccBufs ||
-              mbar_wait(smem_addr(&acc_empty[b]), (uint32_t)((t / kAccBufs) - 1) & 1u, p.timeout_ns)) &&
-             mbar_wait(smem_addr(&full[s]), (uint32_t)(t / kStages) & 1u, p.timeout_ns);
-        if (!ok) break;
-        tmem_fence_after_sync();
-        const uint32_t acc = tmem + (uint32_t)b * kAccCols;
-        const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
-        const uint64_t ad = tile_desc(a), bd = tile_desc(a + kPart);
-#pragma unroll
-        for (int ks = 0; ks < BK / 32; ++ks)
-          mma_f8_pair(acc, ad + (uint64_t)ks * astep, bd + (uint64_t)ks * bstep, p.idesc, ks == 0 ? 0u : 1u);
-        mma_commit_pair(smem_addr(&empty[s]));     // stage s reusable in both CTAs
-        mma_commit_pair(smem_addr(&acc_full[b]));  // accumulator b (both CTAs) holds group t
-        t_done = t;
-      }
-      if (!ok) atomicOr(p.fault, (unsigned)kFaultFullWait);
-      // leave only when every product has completed and its commits have landed here
-      for (int u = t_done + 1 > kStages ? t_done + 1 - kStages : 0; u <= t_done; ++u)
-        if (!mbar_wait(smem_addr(&empty[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns))
-          atomicOr(p.fault, (unsigned)kFaultDrainWait);
-      if (t_done >= 0 &&
-          !mbar_wait(smem_addr(&acc_full[t_done % kAccBufs]), (uint32_t)(t_done / kAccBufs) & 1u, p.timeout_ns))
-        atomicOr(p.fault, (unsigned)kFaultDrainWait);
+      copies_wait_all();
     }
   } else {
+    more_registers<kFoldRegs>();
     // ------------------------------------------------ folders, then D (both CTAs)
-    const int q = warp & 3;            // TMEM lane quarter this warp may access
-    const int half = (warp - 2) >> 2;  // which half of the tile's columns
-    const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(halfn * half);
-    const int hid = 32 * ((warp - 2) & 3) + lane;  // thread of its half
-    float2 sum[kMaxHalf / 2];
+    const int q = warp & 3;                     // TMEM lane quarter this warp may access
+    const int part = (warp - kFirstFold) >> 2;  // which quarter of the tile's columns
+    const int cols = p.tile_n / 4;              // a multiple of 8
+    const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(cols * part);
+    const float* scales = reinterpret_cast<const float*>(smem_raw + pad + kStages * kStageBytes);
+    float* out = reinterpret_cast<float*>(smem_raw + pad + kStages * kStageBytes + Sc::kChunks * Sc::kFloats * 4) +
+                 (warp - kFirstFold) * 32 * kOutPitch;
+    float2 sum[kMaxCols / 2];
 #pragma unroll
-    for (int e = 0; e < kMaxHalf / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
+    for (int e = 0; e < kMaxCols / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
     bool ok = true;
-    int t = 0;
-    for (int i = 0; i < my_tiles; ++i) {
+    int s = 0, b = 0, c = 0;                // stage, accumulator and scale chunk of the next group
+    uint32_t s_lap = 0, c_lap = 0;
+    for (int i = 0; ok && i < my_tiles; ++i) {
       int tm, tn;
       tile_coords(cl + i * p.clusters, p.tiles_m, p.tiles_n, tm, tn);
-      const int row = tm * BM + BMC * (int)rank + 32 * q + lane;
-      const int c0 = tn * p.tile_n + halfn * half;
-      // scales: this row's, and either the (at most two) column blocks' of this half or one column
-      // per thread of the half; the next group's are loaded while this group is waited for
-      const float* sa = p.sa.p + (int64_t)(min(row, p.out.M - 1) >> p.sa.shift) * p.sa.si;
-      const float *sb0, *sb1;
-      const int edge = ((c0 >> 7) + 1) * 128 - c0;  // columns of this half in its first column block
-      if (COLS) {
-        sb0 = sb1 = p.sb.p + (int64_t)min(c0 + min(hid, halfn - 1), p.out.N - 1) * p.sb.si;
-      } else {
-        sb0 = p.sb.p + (int64_t)(min(c0, p.out.N - 1) >> 7) * p.sb.si;
-        sb1 = p.sb.p + (int64_t)(min(c0 + halfn - 1, p.out.N - 1) >> 7) * p.sb.si;
-      }
-      float a_next = __ldg(sa), b0_next = __ldg(sb0), b1_next = COLS ? 0.0f : __ldg(sb1);
-      for (int g = 0; g < groups; ++g, ++t) {
-        const float a_cur = a_next, b0_cur = b0_next, b1_cur = b1_next;
-        if (g + 1 < groups) {
-          a_next = __ldg(sa + (int64_t)(g + 1) * p.sa.sk);
-          b0_next = __ldg(sb0 + (int64_t)(g + 1) * p.sb.sk);
-          if (!COLS) b1_next = __ldg(sb1 + (int64_t)(g + 1) * p.sb.sk);
+      const int c0 = tn * p.tile_n + cols * part;
+      const int edge = ((c0 >> 7) + 1) * 128 - c0;  // columns of this thread's in the column block of c0
+      // where its column scales (or its first block's) lie among a group's
+      const int b_at = COLS ? cols * part : (c0 >> 7) - ((tn * p.tile_n) >> 7);
+      for (int g = 0; g < groups; ++g) {
+        const int in_chunk = g & (kChunk - 1);
+        if (in_chunk == 0) ok = poll_wait(smem_addr(&scale_full[c]), c_lap & 1u, p.timeout_ns);
+        ok = ok && poll_wait(smem_addr(&done[s]), s_lap & 1u, p.timeout_ns);
+        if (!ok) {
+          if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+          break;
         }
-        if (COLS) {  // written two groups ago at the latest read: one barrier per group suffices
-          col_scale[t & 1][half][hid] = b0_cur;
-          half_barrier(half);
-        }
-        const int b = t % kAccBufs;
-        if (ok) {  // a warp that gave up keeps meeting the others at the barrier
-          ok = warp_wait(smem_addr(&acc_full[b]), (uint32_t)(t / kAccBufs) & 1u, p.timeout_ns);
-          if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
-        }
-        if (!ok) continue;
         tmem_fence_after_sync();
-        const float s0 = a_cur * b0_cur, s1 = a_cur * b1_cur;
+        const uint32_t acc = tq + (uint32_t)(b * p.tile_n);
+        const float* sc = scales + c * Sc::kFloats;
+        const float* scb = sc + kChunk * BMC + in_chunk * Sc::kB + b_at;
+        float sa, s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-        for (int ch = 0; ch < kMaxHalf / 32; ++ch) {
-          if (32 * ch < halfn) {
-            float v[2][16];
-            tmem_ld16(tq + (uint32_t)b * kAccCols + (uint32_t)(32 * ch), v[0]);
-            if (32 * ch + 16 < halfn) tmem_ld16(tq + (uint32_t)b * kAccCols + (uint32_t)(32 * ch + 16), v[1]);
+        for (int ch = 0; ch < kMaxCols / kLoadCols; ++ch) {
+          if (kLoadCols * ch < cols) {
+            float v[kLoadCols];
+#pragma unroll
+            for (int k = 0; k < kLoadCols; k += 16) {
+              const int at = kLoadCols * ch + k;
+              if (at + 16 <= cols) tmem_ld16(acc + (uint32_t)at, *reinterpret_cast<float(*)[16]>(v + k));
+              else if (at + 8 <= cols) tmem_ld8(acc + (uint32_t)at, v + k);
+            }
+            if (ch == 0) {  // while the accumulator is on its way
+              sa = sc[in_chunk * BMC + 32 * q + lane];
+              if (!COLS) {
+                s0 = sa * scb[0];
+                s1 = sa * scb[1];
+              }
+            }
             tmem_wait_ld();
-            if (32 * (ch + 1) >= halfn) {
+            if (kLoadCols * (ch + 1) >= cols) {
               // the whole accumulator is in registers: hand it back to the issuer
               tmem_fence_before_sync();
               __syncwarp();
               if (lane == 0) mbar_arrive_remote(smem_addr(&acc_empty[b]), 0);
             }
 #pragma unroll
-            for (int c = 0; c < 2; ++c) {
-              if (32 * ch + 16 * c >= halfn) continue;
-              tmem_ld_ready(v[c]);
+            for (int k = 0; k < kLoadCols; k += 8) {  // 8 columns at a time
+              const int at = kLoadCols * ch + k;
+              if (at >= cols) continue;
+              float* x = v + k;
+#pragma unroll
+              for (int e = 0; e < 8; ++e) asm volatile("" : "+f"(x[e]));  // used behind the wait only
+              float2* m = &sum[at / 2];
               if (COLS) {
-                const float4* cs = reinterpret_cast<const float4*>(&col_scale[t & 1][half][COLS ? 32 * ch + 16 * c : 0]);
-                const float2 sa2 = make_float2(a_cur, a_cur);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  const float4 w = cs[e];
-                  float2& m0 = sum[(32 * ch + 16 * c) / 2 + 2 * e];
-                  float2& m1 = sum[(32 * ch + 16 * c) / 2 + 2 * e + 1];
-                  m0 = __ffma2_rn(__fmul2_rn(make_float2(v[c][4 * e], v[c][4 * e + 1]), make_float2(w.x, w.y)), sa2, m0);
-                  m1 = __ffma2_rn(__fmul2_rn(make_float2(v[c][4 * e + 2], v[c][4 * e + 3]), make_float2(w.z, w.w)), sa2, m1);
-                }
+                const float4* w = reinterpret_cast<const float4*>(scb + at);
+                const float4 w0 = w[0], w1 = w[1];
+                const float2 sa2 = make_float2(sa, sa);
+                m[0] = __ffma2_rn(__fmul2_rn(make_float2(x[0], x[1]), make_float2(w0.x, w0.y)), sa2, m[0]);
+                m[1] = __ffma2_rn(__fmul2_rn(make_float2(x[2], x[3]), make_float2(w0.z, w0.w)), sa2, m[1]);
+                m[2] = __ffma2_rn(__fmul2_rn(make_float2(x[4], x[5]), make_float2(w1.x, w1.y)), sa2, m[2]);
+                m[3] = __ffma2_rn(__fmul2_rn(make_float2(x[6], x[7]), make_float2(w1.z, w1.w)), sa2, m[3]);
               } else {
-                const float s = 32 * ch + 16 * c < edge ? s0 : s1;
-                const float2 s2 = make_float2(s, s);
+                const float w = at < edge ? s0 : s1;
+                const float2 w2 = make_float2(w, w);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                  float2& m = sum[(32 * ch + 16 * c) / 2 + e];
-                  m = __ffma2_rn(make_float2(v[c][2 * e], v[c][2 * e + 1]), s2, m);
-                }
+                for (int e = 0; e < 4; ++e) m[e] = __ffma2_rn(make_float2(x[2 * e], x[2 * e + 1]), w2, m[e]);
               }
             }
           }
         }
-      }
-      // this thread holds columns c0 .. c0 + halfn - 1 of its row
-      if (ok && row < p.out.M) {
-#pragma unroll
-        for (int e = 0; e < kMaxHalf / 8; ++e) {
-          const int col = c0 + 8 * e;
-          if (8 * e >= halfn || col >= p.out.N) continue;
-          float v[8];
-#pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            v[2 * k] = sum[4 * e + k].x;
-            v[2 * k + 1] = sum[4 * e + k].y;
+        if (in_chunk == kChunk - 1 || g == groups - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&scale_empty[c]));
+          if (++c == Sc::kChunks) {
+            c = 0;
+            ++c_lap;
           }
-          if (p.out.vec && col + 8 <= p.out.N) {
-            store_eight(p.out, row, col, v);
-          } else {
+        }
+        if (++b == bufs) b = 0;
+        if (++s == kStages) {
+          s = 0;
+          ++s_lap;
+        }
+      }
+      // This thread holds columns c0 .. c0 + cols - 1 of its row: 32 rows x 16 columns at a time go
+      // through shared memory, so that 4 lanes write 64 (or, in BF16, 32) consecutive bytes.
+      if (ok) {
+        float4* mine = reinterpret_cast<float4*>(out + lane * kOutPitch);
+        const int at = 4 * (lane & 3);
+        const int row0 = tm * BM + BMC * (int)rank + 32 * q + (lane >> 2);
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              if (col + k < p.out.N) store_one(p.out, row, col + k, v[k]);
+        for (int ch = 0; ch < kMaxCols / 16; ++ch) {
+          if (16 * ch < cols) {
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              mine[e] = make_float4(sum[8 * ch + 2 * e].x, sum[8 * ch + 2 * e].y, sum[8 * ch + 2 * e + 1].x,
+                                    sum[8 * ch + 2 * e + 1].y);
+            __syncwarp();
+            const int col = c0 + 16 * ch + at;
+            if (16 * ch + at < cols && col < p.out.N) store_rows(p.out, row0, col, out + (lane >> 2) * kOutPitch + at, kOutPitch);
           }
         }
       }
 #pragma unroll
-      for (int e = 0; e < kMaxHalf / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
+      for (int e = 0; e < kMaxCols / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
     }
   }
 
@@ -293,19 +362,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }  // namespace
 }  // namespace f8
 
+int64_t fp8_pair_smem(bool cols) { return cols ? f8::ScaleCfg<true>::kSmem : f8::ScaleCfg<false>::kSmem; }
+
 cudaError_t prepare_fp8_pair() {
   cudaError_t e = cudaFuncSetAttribute(f8::fp8_pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       f8::kSmemBytes);
+                                       f8::ScaleCfg<false>::kSmem);
   if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(f8::fp8_pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize, f8::kSmemBytes);
+    e = cudaFuncSetAttribute(f8::fp8_pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             f8::ScaleCfg<true>::kSmem);
   return e;
 }
 
 cudaError_t launch_fp8_pair(const CUtensorMap& mapA, const CUtensorMap& mapB, const Fp8PairParams& p,
                             cudaStream_t stream) {
   const dim3 grid(2u * (unsigned)p.clusters);
-  if (p.sb.shift == 0) f8::fp8_pair_kernel<true><<<grid, f8::kThreads, f8::kSmemBytes, stream>>>(mapA, mapB, p);
-  else f8::fp8_pair_kernel<false><<<grid, f8::kThreads, f8::kSmemBytes, stream>>>(mapA, mapB, p);
+  if (p.sb.shift == 0)
+    f8::fp8_pair_kernel<true><<<grid, f8::kThreads, f8::ScaleCfg<true>::kSmem, stream>>>(mapA, mapB, p);
+  else
+    f8::fp8_pair_kernel<false><<<grid, f8::kThreads, f8::ScaleCfg<false>::kSmem, stream>>>(mapA, mapB, p);
   return cudaGetLastError();
 }
 

@@ -16,6 +16,7 @@ from . import PlanStruct, SgemmError, _ch, _stream, load
 FORMATS = {"e4m3": 0, "e5m2": 1}
 VARIANTS = {0: "AUTO", 1: "NONE", 2: "SCALE", 32: "FP8_PAIR", 33: "FP8_SHORT"}
 ROW, COL, BLOCK = (1, 128), (128, 1), (128, 128)
+GROUPS = (ROW, COL, BLOCK)
 
 
 class MatrixStruct(ctypes.Structure):
@@ -28,13 +29,18 @@ class ExpertsStruct(ctypes.Structure):
                 ("lds", ctypes.c_int64), ("stride_scale", ctypes.c_int64)]
 
 
-_functions = None
+_functions = None  # the compiled library, once its signatures are set
+_T = None          # torch, imported with the first call
+_CODES = {}        # torch dtype -> enum sgemm_fp8_format
+_TYPES = {}        # torch dtype -> enum sgemm_type
+_raw_stream = None
 
 
 def _lib():
     """The compiled library with the C signatures of this file's entry points."""
-    global _functions
+    global _functions, _T, _raw_stream
     if _functions is None:
+        import torch
         lib = load()
         i64, f32, vp, ci = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_int
         mp, ep, ch = ctypes.POINTER(MatrixStruct), ctypes.POINTER(ExpertsStruct), ctypes.c_char
@@ -50,17 +56,26 @@ def _lib():
         }.items():
             f = getattr(lib, name)
             f.restype, f.argtypes = ci, args
-        _functions = lib
+        _CODES.update({torch.float8_e4m3fn: 0, torch.float8_e5m2: 1})
+        _TYPES.update({torch.float32: 0, torch.bfloat16: 1})
+        # the handle alone: torch.cuda.current_stream() builds an object, which costs as much as a launch
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _T, _functions = torch, lib
     return _functions
 
 
-def _type(dtype) -> int:
-    import torch
-    if dtype == torch.float32:
-        return 0
-    if dtype == torch.bfloat16:
-        return 1
-    raise TypeError(f"expected a float32 or bfloat16 tensor, got {dtype}")
+def _on(stream, x):
+    """The stream handle a call on tensor x runs on."""
+    if stream is None and _raw_stream is not None:
+        return _raw_stream(x.get_device())
+    return _stream(stream)
+
+
+def _type(x, name) -> int:
+    t = _TYPES.get(x.dtype)
+    if t is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {x.dtype}")
+    return t
 
 
 def _check(x, name, dims=2, dtype=None):
@@ -75,25 +90,34 @@ def _check(x, name, dims=2, dtype=None):
     return x
 
 
+def _rows(x, name):
+    """(rows, columns, row stride) of a 2-D CUDA tensor with contiguous rows (a single row has no stride of its own)."""
+    if not x.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    shape = x.shape
+    if len(shape) != 2:
+        raise TypeError(f"{name} must have 2 dimensions")
+    rows, cols = shape
+    ld, inner = x.stride()
+    if inner != 1 and cols > 1:
+        raise TypeError(f"{name}: the last dimension must be contiguous")
+    if rows <= 1 or ld < 1:
+        ld = cols or 1
+    return rows, cols, ld
+
+
 def _ld(x) -> int:
-    """Row stride of a 2-D tensor (a single row has none of its own)."""
-    return max(x.stride(0) if x.shape[0] > 1 else x.shape[1], 1)
+    return _rows(x, "tensor")[2]
 
 
 def _empty(shape, dtype, like, stream):
     """Uninitialised memory that belongs to the stream the call runs on."""
-    import torch
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
+        return _T.empty(shape, dtype=dtype, device=like.device)
     if not hasattr(stream, "cuda_stream"):
-        stream = torch.cuda.ExternalStream(int(stream), device=like.device) if stream else torch.cuda.default_stream(like.device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=like.device)
-
-
-def _code_dtypes():
-    import torch
-    return {torch.float8_e4m3fn: 0, torch.float8_e5m2: 1}
+        stream = _T.cuda.ExternalStream(int(stream), device=like.device) if stream else _T.cuda.default_stream(like.device)
+    with _T.cuda.stream(stream):
+        return _T.empty(shape, dtype=dtype, device=like.device)
 
 
 class Fp8Matrix:
@@ -102,65 +126,64 @@ class Fp8Matrix:
 
     Element (r, c) is ``data[r, c] * scale[r // block[0], c // block[1]]``."""
 
-    __slots__ = ("data", "scale", "block", "_struct")
+    __slots__ = ("data", "scale", "block", "shape", "_struct")
 
     def __init__(self, data, scale, block=ROW):
-        import torch
-        fmt = 0 if data.dtype == torch.float8_e4m3fn else 1 if data.dtype == torch.float8_e5m2 else None
+        _lib()
+        fmt = _CODES.get(data.dtype)
         if fmt is None:
             raise TypeError(f"data must be float8_e4m3fn or float8_e5m2, got {data.dtype}")
-        _check(data, "data")
-        _check(scale, "scale", dtype=torch.float32)
+        if scale.dtype is not _T.float32:
+            raise TypeError(f"scale must be float32, got {scale.dtype}")
+        rows, cols, ld = _rows(data, "data")
+        srows, scols, lds = _rows(scale, "scale")
         br, bc = block
-        if (br, bc) not in (ROW, COL, BLOCK):
+        if (br, bc) not in GROUPS:
             raise ValueError("block must be (1, 128), (128, 1) or (128, 128)")
-        rows, cols = data.shape
-        if tuple(scale.shape) != (-(-rows // br), -(-cols // bc)):
-            raise ValueError(f"scale must have shape {(-(-rows // br), -(-cols // bc))}, got {tuple(scale.shape)}")
-        self.data, self.scale, self.block = data, scale, (br, bc)
-        self._struct = MatrixStruct(data.data_ptr(), _ld(data), scale.data_ptr(), _ld(scale), fmt, br, bc)
-
-    @property
-    def shape(self):
-        return self.data.shape
+        if srows != -(-rows // br) or scols != -(-cols // bc):
+            raise ValueError(f"scale must have shape {(-(-rows // br), -(-cols // bc))}, got {(srows, scols)}")
+        self.data, self.scale, self.block, self.shape = data, scale, (br, bc), data.shape
+        self._struct = MatrixStruct(data.data_ptr(), ld, scale.data_ptr(), lds, fmt, br, bc)
 
 
 def _new_matrix(rows, cols, block, fmt, like, stream):
     """An Fp8Matrix of uninitialised codes and scales; rows start at multiples of 16 bytes."""
-    import torch
-    dtype = torch.float8_e5m2 if fmt else torch.float8_e4m3fn
+    dtype = _T.float8_e5m2 if fmt else _T.float8_e4m3fn
     ld = (cols + 15) // 16 * 16
     data = _empty((rows, ld), dtype, like, stream)
     if ld != cols:
         data = data[:, :cols]
-    return Fp8Matrix(data, _empty((-(-rows // block[0]), -(-cols // block[1])), torch.float32, like, stream), block)
+    br, bc = block
+    scols = -(-cols // bc)
+    m = Fp8Matrix.__new__(Fp8Matrix)
+    m.scale = scale = _empty((-(-rows // br), scols), _T.float32, like, stream)
+    m.data, m.block, m.shape = data, block, data.shape
+    m._struct = MatrixStruct(data.data_ptr(), ld or 1, scale.data_ptr(), scols or 1, fmt, br, bc)
+    return m
 
 
 def quantize_fp8(x, block=ROW, format="e4m3", stream=None) -> Fp8Matrix:
     """Codes and scales of a 2-D float32 or bfloat16 tensor in groups of `block` elements: (1, 128), (128, 1) or
     (128, 128).  For each group the scale is max(amax / top, 2**-126) and the code of x is x * (1 / scale) rounded
     to nearest even (sgemm_fp8_quantize)."""
-    _check(x, "x")
-    if format not in FORMATS:
+    lib = _lib()
+    rows, cols, ldx = _rows(x, "x")
+    fmt = FORMATS.get(format)
+    if fmt is None:
         raise ValueError(f"unknown 8-bit format {format!r}")
-    t = _type(x.dtype)
-    if tuple(block) not in (ROW, COL, BLOCK):
+    t = _type(x, "x")
+    block = tuple(block)
+    if block not in GROUPS:
         raise ValueError("block must be (1, 128), (128, 1) or (128, 128)")
-    rows, cols = x.shape
-    m = _new_matrix(rows, cols, block, FORMATS[format], x, stream)
+    m = _new_matrix(rows, cols, block, fmt, x, stream)
     c = m._struct
-    st = _lib().sgemm_fp8_quantize(rows, cols, x.data_ptr(), t, _ld(x), c.format, c.block_rows, c.block_cols, c.data, c.ld,
-                                   c.scale, c.lds, _stream(stream))
+    st = lib.sgemm_fp8_quantize(rows, cols, x.data_ptr(), t, ldx, fmt, block[0], block[1], c.data, c.ld, c.scale, c.lds, _on(stream, x))
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_quantize")
     return m
 
 
-def _is_t(op) -> bool:
-    op = op.decode() if isinstance(op, bytes) else str(op)
-    if op[:1].upper() not in ("N", "T", "C"):
-        raise ValueError(f"unknown operation {op!r}: N or T")
-    return op[:1].upper() != "N"
+_OPS = {"N": (False, b"N"), "n": (False, b"N"), "T": (True, b"T"), "t": (True, b"T"), "C": (True, b"T"), "c": (True, b"T")}
 
 
 def matmul_fp8(A: Fp8Matrix, B: Fp8Matrix, C=None, transA="N", transB="N", alpha=1.0, beta=0.0, *, out=None, out_dtype=None,
@@ -169,30 +192,41 @@ def matmul_fp8(A: Fp8Matrix, B: Fp8Matrix, C=None, transA="N", transB="N", alpha
 
     A and B are the stored matrices; both must have groups of 128 along the summed dimension.  The result goes to `out`, else
     to C in place, else to a new tensor of `out_dtype` (float32 unless given)."""
-    import torch
-    ta, tb = _is_t(transA), _is_t(transB)
-    M, K = A.data.shape[::-1] if ta else A.data.shape
-    N, kb = B.data.shape if tb else B.data.shape[::-1]
+    lib = _lib()
+    try:
+        (ta, opa), (tb, opb) = _OPS[transA], _OPS[transB]
+    except KeyError:
+        raise ValueError(f"unknown operation {transA!r} or {transB!r}: N or T") from None
+    M, K = A.shape
+    if ta:
+        M, K = K, M
+    kb, N = B.shape
+    if tb:
+        kb, N = N, kb
     if kb != K:
         raise ValueError("inner dimensions of op(A) and op(B) differ")
-    if C is None:
-        if beta != 0.0:
-            raise ValueError("beta != 0 needs C")
-        d = out if out is not None else _empty((M, N), out_dtype or torch.float32, A.data, stream)
-        c_ptr, ldc = None, max(N, 1)
-    else:
-        d = out if out is not None else C
-        _check(C, "C", 2, d.dtype)
-        if tuple(C.shape) != (M, N):
+    c_ptr, ldc = None, N or 1
+    d = out
+    if C is not None:
+        rows, cols, ldc = _rows(C, "C")
+        if rows != M or cols != N:
             raise ValueError("C has the wrong shape")
-        c_ptr, ldc = C.data_ptr(), _ld(C)
-    t = _type(_check(d, "out").dtype)
-    if tuple(d.shape) != (M, N):
-        raise ValueError("out has the wrong shape")
-    if out_dtype is not None and d.dtype != out_dtype:
+        if d is None:
+            d = C
+        elif d.dtype is not C.dtype:
+            raise TypeError(f"C is {C.dtype} and out is {d.dtype}")
+        c_ptr = C.data_ptr()
+    elif beta != 0.0:
+        raise ValueError("beta != 0 needs C")
+    if d is None:
+        d = _empty((M, N), out_dtype or _T.float32, A.data, stream)
+    elif out_dtype is not None and d.dtype is not out_dtype:
         raise TypeError(f"out is {d.dtype}, not {out_dtype}")
-    st = _lib().sgemm_fp8(b"T" if ta else b"N", b"T" if tb else b"N", M, N, K, alpha, A._struct, B._struct, beta, c_ptr, ldc,
-                          d.data_ptr(), _ld(d), t, _stream(stream))
+    t = _type(d, "out")
+    rows, cols, ldd = _rows(d, "out")
+    if rows != M or cols != N:
+        raise ValueError("out has the wrong shape")
+    st = lib.sgemm_fp8(opa, opb, M, N, K, alpha, A._struct, B._struct, beta, c_ptr, ldc, d.data_ptr(), ldd, t, _on(stream, d))
     if st != 0:
         raise SgemmError(st, "sgemm_fp8")
     return d
@@ -219,6 +253,16 @@ def sgemm_fp8_set_override(variant="AUTO", tile_n=0, split=0) -> None:
 
 
 NormOutput = namedtuple("NormOutput", "q h y rstd")
+_NO_MATRIX = MatrixStruct()
+
+
+def _vector(x, name, n, dtype):
+    if not x.is_cuda or x.dtype is not dtype:
+        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+    if x.shape != (n,):
+        raise ValueError(f"{name} must have shape ({n},), got {tuple(x.shape)}")
+    if n > 1 and x.stride(0) != 1:
+        raise TypeError(f"{name} must be contiguous")
 
 
 def rmsnorm_fp8(x, weight, eps=1e-6, residual=None, *, codes=True, y=False, stream=None) -> NormOutput:
@@ -227,26 +271,24 @@ def rmsnorm_fp8(x, weight, eps=1e-6, residual=None, *, codes=True, y=False, stre
 
     Returns (q, h, y, rstd): `q` the E4M3 codes and scales of y in groups of (1, 128) (None with codes=False), `h` the sum
     (x itself without a residual), `y` in x's type when y=True (else None), `rstd` float32 of one value per row."""
-    import torch
-    t = _type(_check(x, "x").dtype)
-    rows, cols = x.shape
-    _check(weight, "weight", 1, x.dtype)
-    if weight.shape[0] != cols:
-        raise ValueError("weight must have one value per column of x")
-    h, r_ptr, ldr, h_ptr, ldh = x, None, 0, None, 0
+    lib = _lib()
+    t = _type(x, "x")
+    rows, cols, ldx = _rows(x, "x")
+    dtype = x.dtype
+    _vector(weight, "weight", cols, dtype)
+    h, r_ptr, ldr, h_ptr = x, None, 0, None
     if residual is not None:
-        _check(residual, "residual", 2, x.dtype)
-        if residual.shape != x.shape:
-            raise ValueError("residual must have x's shape")
-        h = _empty((rows, cols), x.dtype, x, stream)
-        r_ptr, ldr, h_ptr, ldh = residual.data_ptr(), _ld(residual), h.data_ptr(), max(cols, 1)
-    out = _empty((rows, cols), x.dtype, x, stream) if y else None
-    rstd = _empty((rows,), torch.float32, x, stream)
+        rrows, rcols, ldr = _rows(residual, "residual")
+        if rrows != rows or rcols != cols or residual.dtype is not dtype:
+            raise ValueError("residual must have x's shape and type")
+        h = _empty((rows, cols), dtype, x, stream)
+        r_ptr, h_ptr = residual.data_ptr(), h.data_ptr()
+    out = _empty((rows, cols), dtype, x, stream) if y else None
+    rstd = _empty((rows,), _T.float32, x, stream)
     q = _new_matrix(rows, cols, ROW, 0, x, stream) if codes else None
-    c = q._struct if codes else MatrixStruct()
-    st = _lib().sgemm_fp8_rmsnorm(rows, cols, t, x.data_ptr(), _ld(x), r_ptr, ldr, weight.data_ptr(), eps, h_ptr, ldh,
-                                  out.data_ptr() if y else None, max(cols, 1), c.data, c.ld, c.scale, c.lds, rstd.data_ptr(),
-                                  _stream(stream))
+    c = q._struct if codes else _NO_MATRIX
+    st = lib.sgemm_fp8_rmsnorm(rows, cols, t, x.data_ptr(), ldx, r_ptr, ldr, weight.data_ptr(), eps, h_ptr, cols or 1,
+                               out.data_ptr() if y else None, cols or 1, c.data, c.ld, c.scale, c.lds, rstd.data_ptr(), _on(stream, x))
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_rmsnorm")
     return NormOutput(q, h, out, rstd)
@@ -255,38 +297,41 @@ def rmsnorm_fp8(x, weight, eps=1e-6, residual=None, *, codes=True, y=False, stre
 def rmsnorm_fp8_backward(dy, h, weight, rstd, dh=None, *, stream=None):
     """(dx, dweight) of rmsnorm_fp8: `dy` the gradient of y, `h` and `rstd` as the forward pass returned them, `dh` the
     gradient that reaches h past the norm.  dx is the gradient of x and of the residual; dweight is float32."""
-    import torch
-    t = _type(_check(dy, "dy").dtype)
-    rows, cols = dy.shape
-    _check(h, "h", 2, dy.dtype)
-    _check(weight, "weight", 1, dy.dtype)
-    _check(rstd, "rstd", 1, torch.float32)
-    if h.shape != dy.shape or weight.shape[0] != cols or rstd.shape[0] != rows:
-        raise ValueError("dy, h, weight and rstd do not belong together")
+    lib = _lib()
+    t = _type(dy, "dy")
+    rows, cols, lddy = _rows(dy, "dy")
+    dtype = dy.dtype
+    _vector(weight, "weight", cols, dtype)
+    _vector(rstd, "rstd", rows, _T.float32)
+    hrows, hcols, ldh = _rows(h, "h")
+    if hrows != rows or hcols != cols or h.dtype is not dtype:
+        raise ValueError("h must have dy's shape and type")
+    dh_ptr, lddh = None, 0
     if dh is not None:
-        _check(dh, "dh", 2, dy.dtype)
-        if dh.shape != dy.shape:
-            raise ValueError("dh must have dy's shape")
-    dx = _empty((rows, cols), dy.dtype, dy, stream)
-    dw = _empty((cols,), torch.float32, dy, stream)
-    st = _lib().sgemm_fp8_rmsnorm_backward(rows, cols, t, dy.data_ptr(), _ld(dy), h.data_ptr(), _ld(h), weight.data_ptr(),
-                                           rstd.data_ptr(), None if dh is None else dh.data_ptr(), 0 if dh is None else _ld(dh),
-                                           dx.data_ptr(), max(cols, 1), dw.data_ptr(), _stream(stream))
+        drows, dcols, lddh = _rows(dh, "dh")
+        if drows != rows or dcols != cols or dh.dtype is not dtype:
+            raise ValueError("dh must have dy's shape and type")
+        dh_ptr = dh.data_ptr()
+    dx = _empty((rows, cols), dtype, dy, stream)
+    dw = _empty((cols,), _T.float32, dy, stream)
+    st = lib.sgemm_fp8_rmsnorm_backward(rows, cols, t, dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), rstd.data_ptr(),
+                                        dh_ptr, lddh, dx.data_ptr(), cols or 1, dw.data_ptr(), _on(stream, dy))
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_rmsnorm_backward")
     return dx, dw
 
 
 def _experts(w, name, experts, rows, cols) -> ExpertsStruct:
-    import torch
     data, scale = w
-    _check(data, name, 3, torch.float8_e4m3fn)
-    _check(scale, name + " scales", 3, torch.float32)
-    if tuple(data.shape) != (experts, rows, cols):
+    _check(data, name, 3, _T.float8_e4m3fn)
+    _check(scale, name + " scales", 3, _T.float32)
+    if data.shape != (experts, rows, cols):
         raise ValueError(f"{name} must have shape {(experts, rows, cols)}, got {tuple(data.shape)}")
-    if tuple(scale.shape) != (experts, -(-rows // 128), -(-cols // 128)):
+    if scale.shape != (experts, -(-rows // 128), -(-cols // 128)):
         raise ValueError(f"{name} scales must have shape {(experts, -(-rows // 128), -(-cols // 128))}, got {tuple(scale.shape)}")
-    return ExpertsStruct(data.data_ptr(), data.stride(1), data.stride(0), scale.data_ptr(), max(scale.stride(1), 1), scale.stride(0))
+    stride, ld, _ = data.stride()
+    sstride, lds, _ = scale.stride()
+    return ExpertsStruct(data.data_ptr(), ld, stride, scale.data_ptr(), lds or 1, sstride)
 
 
 def moe_fp8(x: Fp8Matrix, logits, top_k, gate, up, down, *, renormalize=True, out=None, out_dtype=None, stream=None):
@@ -297,23 +342,26 @@ def moe_fp8(x: Fp8Matrix, logits, top_k, gate, up, down, *, renormalize=True, ou
     hidden], scales [experts, inner / 128, hidden / 128]) with groups of 128 x 128, down: [experts, hidden, inner].  The
     weights are divided by their sum over the chosen experts with renormalize=True.  Returns bfloat16 unless out_dtype or
     out says otherwise."""
-    import torch
-    _check(logits, "logits", 2, torch.float32)
-    tokens, hidden = x.data.shape
+    lib = _lib()
+    tokens, hidden = x.shape
     experts, inner = gate[0].shape[:2]
-    if tuple(logits.shape) != (tokens, experts):
+    lrows, lcols, ldl = _rows(logits, "logits")
+    if logits.dtype is not _T.float32:
+        raise TypeError("logits must be float32")
+    if lrows != tokens or lcols != experts:
         raise ValueError("logits must have one value per token and expert")
     g = _experts(gate, "gate", experts, inner, hidden)
     u = _experts(up, "up", experts, inner, hidden)
     d = _experts(down, "down", experts, hidden, inner)
-    y = out if out is not None else _empty((tokens, hidden), out_dtype or torch.bfloat16, x.data, stream)
-    if tuple(y.shape) != (tokens, hidden):
+    y = out if out is not None else _empty((tokens, hidden), out_dtype or _T.bfloat16, x.data, stream)
+    yrows, ycols, ldy = _rows(y, "out")
+    if yrows != tokens or ycols != hidden:
         raise ValueError("out has the wrong shape")
-    t = _type(_check(y, "out").dtype)
-    if out_dtype is not None and y.dtype != out_dtype:
+    t = _type(y, "out")
+    if out_dtype is not None and y.dtype is not out_dtype:
         raise TypeError(f"out is {y.dtype}, not {out_dtype}")
-    st = _lib().sgemm_fp8_moe(tokens, hidden, inner, experts, top_k, x._struct, logits.data_ptr(), _ld(logits), 1 if renormalize else 0,
-                              g, u, d, y.data_ptr(), _ld(y), t, _stream(stream))
+    st = lib.sgemm_fp8_moe(tokens, hidden, inner, experts, top_k, x._struct, logits.data_ptr(), ldl, 1 if renormalize else 0, g, u, d,
+                           y.data_ptr(), ldy, t, _on(stream, y))
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_moe")
     return y
