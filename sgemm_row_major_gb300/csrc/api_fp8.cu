@@ -3,6 +3,7 @@
 #include <atomic>
 #include <climits>
 #include <cstdint>
+#include <iterator>
 
 #include "fp8_internal.h"
 #include "sgemm_fp8.h"
@@ -114,7 +115,7 @@ constexpr int kPairFixedCols = 64;
 int pair_tile_n(int64_t M, int64_t N, int64_t clusters) {
   int best = 256;
   int64_t best_cost = INT64_MAX;
-  for (int n = 256; n >= 32; n -= 32) {
+  for (int n : kFp8PairTiles) {
     const int64_t rounds = ceil_div(ceil_div(M, 256) * ceil_div(N, n), clusters);
     const int64_t cost = rounds * (n + kPairFixedCols);
     if (cost < best_cost) {
@@ -222,13 +223,12 @@ cudaError_t launch_product(const Product& pr, const sgemm_plan_t& plan, const Ca
     p.a_mn = pr.a.mn_major;
     p.b_mn = pr.b.mn_major;
     p.idesc = instruction(pr.a, pr.b, 256, plan.tile_n);
-    p.tile_n = plan.tile_n;
     p.tiles_m = (int)ceil_div(pr.M, 256);
     p.tiles_n = (int)ceil_div(pr.N, plan.tile_n);
     p.clusters = (int)(plan.grid_x / 2);
     p.timeout_ns = wait_timeout_ns();
     p.fault = dev.fault;
-    return launch_fp8_pair(ma, mb, p, stream);
+    return launch_fp8_pair(plan.tile_n, ma, mb, p, stream);
   }
   const bool trans = pr.M <= pr.N;
   const Operand &l = trans ? pr.b : pr.a, &s = trans ? pr.a : pr.b;
@@ -344,8 +344,11 @@ int sgemm_fp8_set_override(int variant, int tile_n, int split) {
   if (variant != SGEMM_VARIANT_AUTO && variant != SGEMM_VARIANT_FP8_PAIR && variant != SGEMM_VARIANT_FP8_SHORT)
     return -1;
   const bool is_short = variant == SGEMM_VARIANT_FP8_SHORT;
-  const int step = is_short ? 16 : 32, most = is_short ? kFp8ShortMaxTile : 256;
-  if (tile_n < 0 || tile_n > most || tile_n % step != 0 || (tile_n > 0 && variant == SGEMM_VARIANT_AUTO)) return -2;
+  const bool known = is_short ? tile_n > 0 && tile_n <= kFp8ShortMaxTile && tile_n % 16 == 0
+                              : variant == SGEMM_VARIANT_FP8_PAIR &&
+                                    std::find(std::begin(kFp8PairTiles), std::end(kFp8PairTiles), tile_n) !=
+                                        std::end(kFp8PairTiles);
+  if (tile_n != 0 && !known) return -2;
   if ((split != 0 && !is_short) || (split != 0 && split != 1 && split != 2 && split != 4 && split != 8)) return -3;
   g_force_variant.store(variant);
   g_force_tile.store(tile_n);

@@ -93,14 +93,15 @@ struct Fp8PairParams {
   Fp8Scales sa, sb;
   int a_mn = 0, b_mn = 0;  // 1: the stored rows run along M (N), not along K
   uint32_t idesc = 0;
-  int tile_n = 0, tiles_m = 0, tiles_n = 0, clusters = 0;
+  int tiles_m = 0, tiles_n = 0, clusters = 0;
   uint64_t timeout_ns = 0;
   unsigned* fault = nullptr;
 };
 constexpr int kFp8PairStages = 5, kFp8PairThreads = 640;
 int64_t fp8_pair_smem(bool cols);  // dynamic shared memory; cols: B has a scale per column
 cudaError_t prepare_fp8_pair();
-cudaError_t launch_fp8_pair(const CUtensorMap& mapA, const CUtensorMap& mapB, const Fp8PairParams& p,
+constexpr int kFp8PairTiles[] = {256, 224, 192, 128, 64};  // the tile widths there are kernels for
+cudaError_t launch_fp8_pair(int tile_n, const CUtensorMap& mapA, const CUtensorMap& mapB, const Fp8PairParams& p,
                             cudaStream_t stream);
 
 // The longer of M and N runs along the tensor-core rows (`l`), the other along the columns (`s`).

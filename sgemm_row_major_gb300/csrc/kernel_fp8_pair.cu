@@ -2,7 +2,7 @@
 //
 //     D = alpha * sum_g sA(i, g) sB(g, j) P_g(i, j) + beta * C,   P_g = sum over 128 k of code products
 //
-// Clusters of two CTAs on one TPC compute 256 x tile_n tiles (tile_n <= 256, a multiple of 32) with
+// Clusters of two CTAs on one TPC compute 256 x tile_n tiles (tile_n 64, 128, 192, 224 or 256) with
 // tcgen05.mma.cta_group::2.kind::f8f6f4, M = 256, N = tile_n, K = 32, both operands from shared
 // memory: each CTA holds 128 rows of A and half of the tile's columns of B.  Four such steps make
 // one P_g in a fresh TMEM accumulator (two of 256 columns alternate); 8 warps per CTA read it back
@@ -17,6 +17,8 @@
 // and write D.  Persistent clusters take tiles round robin in an order that keeps 8 rows of tiles
 // together (their A and B panels stay in L2); tile_n is chosen by the caller so that the last round
 // of tiles is nearly full.
+#include <type_traits>
+
 #include "fp8_gemm.cuh"
 
 namespace sgemm_impl {
@@ -42,8 +44,7 @@ constexpr int kMoverRegs = 32, kFoldRegs = 112;
 static_assert(128 * kMoverRegs + 32 * kFoldWarps * kFoldRegs <= kThreads * 96, "registers at launch");
 constexpr int kMaxBufs = 4;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxCols = 64;              // accumulator columns a folder thread owns at most
-constexpr int kLoadCols = 32;             // of which it loads so many at a time
+constexpr int kLoadCols = 32;             // accumulator columns a folder thread loads at a time, at most
 
 // Scales of a chunk of groups: of the CTA's 128 rows, and of the tile's columns (COLS) or its two or
 // three column blocks.
@@ -65,8 +66,10 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-// COLS: B has one scale per column (weight gradients), else one per 128 columns.
-template <bool COLS>
+// TN: the tile's columns.  COLS: B has one scale per column (weight gradients), else one per 128
+// columns.  Both are template arguments because the fold runs once per group in 16 warps: with the
+// tile's width at run time its branches made it 2.5 times as long.
+template <int TN, bool COLS>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                     const __grid_constant__ Fp8PairParams p) {
@@ -88,8 +91,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int tiles = p.tiles_m * p.tiles_n;
   const int my_tiles = cl < tiles ? (tiles - cl + p.clusters - 1) / p.clusters : 0;
   const int units = my_tiles * groups;
-  const int halfn = p.tile_n / 2;  // columns of B this CTA loads
-  const int bufs = min(kMaxBufs, (int)kTmemCols / p.tile_n);
+  constexpr int halfn = TN / 2;  // columns of B this CTA loads
+  constexpr int bufs = (int)kTmemCols / TN < kMaxBufs ? (int)kTmemCols / TN : kMaxBufs;
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -124,7 +127,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int i = 0; ok && i < my_tiles; ++i) {
           int tm, tn;
           tile_coords(cl + i * p.clusters, p.tiles_m, p.tiles_n, tm, tn);
-          const int m0 = tm * BM + BMC * (int)rank, n0 = tn * p.tile_n + halfn * (int)rank;
+          const int m0 = tm * BM + BMC * (int)rank, n0 = tn * TN + halfn * (int)rank;
           for (int g = 0; g < groups; ++g, ++t) {
             const int s = t % kStages;
             if (t >= kStages && !spin_wait(smem_addr(&done[s]), (uint32_t)((t / kStages) - 1) & 1u, p.timeout_ns)) {
@@ -165,7 +168,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
                spin_wait(smem_addr(&full[s]), (uint32_t)(t / kStages) & 1u, p.timeout_ns);
           if (!ok) break;
           tmem_fence_after_sync();
-          const uint32_t acc = tmem + (uint32_t)(b * p.tile_n);
+          const uint32_t acc = tmem + (uint32_t)(b * TN);
           const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
           const uint64_t ad = tile_desc(a), bd = tile_desc(a + kPart);
 #pragma unroll
@@ -195,10 +198,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         int tm, tn;
         tile_coords(cl + i * p.clusters, p.tiles_m, p.tiles_n, tm, tn);
         const bool rows = warp == 2;
-        const int first = rows ? tm * BM + BMC * (int)rank : tn * p.tile_n;
+        const int first = rows ? tm * BM + BMC * (int)rank : tn * TN;
         const int last = (rows ? p.out.M : p.out.N) - 1;
         const Fp8Scales& sc = rows ? p.sa : p.sb;
-        const int n = rows ? BMC : COLS ? p.tile_n : 3;
+        const int n = rows ? BMC : COLS ? TN : 3;
         const int pitch = rows ? BMC : Sc::kB;
         for (int g0 = 0; g0 < groups; g0 += kChunk) {
           if (lap > 0 && !poll_wait(smem_addr(&scale_empty[c]), (lap - 1) & 1u, p.timeout_ns)) {
@@ -227,24 +230,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ folders, then D (both CTAs)
     const int q = warp & 3;                     // TMEM lane quarter this warp may access
     const int part = (warp - kFirstFold) >> 2;  // which quarter of the tile's columns
-    const int cols = p.tile_n / 4;              // a multiple of 8
+    constexpr int cols = TN / 4;                // a multiple of 8
+    constexpr bool kOneBlock = TN == 256 || TN == 128 || TN == 64;  // a thread's columns are in one column block
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(cols * part);
     const float* scales = reinterpret_cast<const float*>(smem_raw + pad + kStages * kStageBytes);
     float* out = reinterpret_cast<float*>(smem_raw + pad + kStages * kStageBytes + Sc::kChunks * Sc::kFloats * 4) +
                  (warp - kFirstFold) * 32 * kOutPitch;
-    float2 sum[kMaxCols / 2];
+    float2 sum[cols / 2];
 #pragma unroll
-    for (int e = 0; e < kMaxCols / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
+    for (int e = 0; e < cols / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
     bool ok = true;
     int s = 0, b = 0, c = 0;                // stage, accumulator and scale chunk of the next group
     uint32_t s_lap = 0, c_lap = 0;
     for (int i = 0; ok && i < my_tiles; ++i) {
       int tm, tn;
       tile_coords(cl + i * p.clusters, p.tiles_m, p.tiles_n, tm, tn);
-      const int c0 = tn * p.tile_n + cols * part;
+      const int c0 = tn * TN + cols * part;
       const int edge = ((c0 >> 7) + 1) * 128 - c0;  // columns of this thread's in the column block of c0
       // where its column scales (or its first block's) lie among a group's
-      const int b_at = COLS ? cols * part : (c0 >> 7) - ((tn * p.tile_n) >> 7);
+      const int b_at = COLS ? cols * part : (c0 >> 7) - ((tn * TN) >> 7);
       for (int g = 0; g < groups; ++g) {
         const int in_chunk = g & (kChunk - 1);
         if (in_chunk == 0) ok = poll_wait(smem_addr(&scale_full[c]), c_lap & 1u, p.timeout_ns);
@@ -254,58 +258,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           break;
         }
         tmem_fence_after_sync();
-        const uint32_t acc = tq + (uint32_t)(b * p.tile_n);
+        const uint32_t acc = tq + (uint32_t)(b * TN);
         const float* sc = scales + c * Sc::kFloats;
         const float* scb = sc + kChunk * BMC + in_chunk * Sc::kB + b_at;
-        float sa, s0 = 0.0f, s1 = 0.0f;
-#pragma unroll
-        for (int ch = 0; ch < kMaxCols / kLoadCols; ++ch) {
-          if (kLoadCols * ch < cols) {
-            float v[kLoadCols];
-#pragma unroll
-            for (int k = 0; k < kLoadCols; k += 16) {
-              const int at = kLoadCols * ch + k;
-              if (at + 16 <= cols) tmem_ld16(acc + (uint32_t)at, *reinterpret_cast<float(*)[16]>(v + k));
-              else if (at + 8 <= cols) tmem_ld8(acc + (uint32_t)at, v + k);
-            }
-            if (ch == 0) {  // while the accumulator is on its way
-              sa = sc[in_chunk * BMC + 32 * q + lane];
-              if (!COLS) {
-                s0 = sa * scb[0];
-                s1 = sa * scb[1];
-              }
-            }
-            tmem_wait_ld();
-            if (kLoadCols * (ch + 1) >= cols) {
-              // the whole accumulator is in registers: hand it back to the issuer
-              tmem_fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive_remote(smem_addr(&acc_empty[b]), 0);
-            }
-#pragma unroll
-            for (int k = 0; k < kLoadCols; k += 8) {  // 8 columns at a time
-              const int at = kLoadCols * ch + k;
-              if (at >= cols) continue;
-              float* x = v + k;
-#pragma unroll
-              for (int e = 0; e < 8; ++e) asm volatile("" : "+f"(x[e]));  // used behind the wait only
-              float2* m = &sum[at / 2];
-              if (COLS) {
-                const float4* w = reinterpret_cast<const float4*>(scb + at);
-                const float4 w0 = w[0], w1 = w[1];
-                const float2 sa2 = make_float2(sa, sa);
-                m[0] = __ffma2_rn(__fmul2_rn(make_float2(x[0], x[1]), make_float2(w0.x, w0.y)), sa2, m[0]);
-                m[1] = __ffma2_rn(__fmul2_rn(make_float2(x[2], x[3]), make_float2(w0.z, w0.w)), sa2, m[1]);
-                m[2] = __ffma2_rn(__fmul2_rn(make_float2(x[4], x[5]), make_float2(w1.x, w1.y)), sa2, m[2]);
-                m[3] = __ffma2_rn(__fmul2_rn(make_float2(x[6], x[7]), make_float2(w1.z, w1.w)), sa2, m[3]);
-              } else {
-                const float w = at < edge ? s0 : s1;
-                const float2 w2 = make_float2(w, w);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) m[e] = __ffma2_rn(make_float2(x[2 * e], x[2 * e + 1]), w2, m[e]);
-              }
+        float sa = 0.0f, s0 = 0.0f, s1 = 0.0f;
+        const auto fold = [&](auto first, auto count) {  // columns first .. first + count - 1
+          constexpr int kFirst = decltype(first)::value, kCount = decltype(count)::value;
+          float v[kCount];
+          tmem_ld<kCount>(acc + (uint32_t)kFirst, v);
+          if (kFirst == 0) {  // while the accumulator is on its way
+            sa = sc[in_chunk * BMC + 32 * q + lane];
+            if (!COLS) {
+              s0 = sa * scb[0];
+              s1 = kOneBlock ? s0 : sa * scb[1];
             }
           }
+          tmem_wait_ld();
+          if (kFirst + kCount == cols) {  // the whole accumulator is in registers: hand it back to the issuer
+            tmem_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_remote(smem_addr(&acc_empty[b]), 0);
+          }
+#pragma unroll
+          for (int k = 0; k < kCount; k += 8) {
+            float* x = v + k;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) asm volatile("" : "+f"(x[e]));  // used behind the wait only
+            float2* m = &sum[(kFirst + k) / 2];
+            if (COLS) {
+              const float4* w = reinterpret_cast<const float4*>(scb + kFirst + k);
+              const float4 w0 = w[0], w1 = w[1];
+              const float2 sa2 = make_float2(sa, sa);
+              m[0] = __ffma2_rn(__fmul2_rn(make_float2(x[0], x[1]), make_float2(w0.x, w0.y)), sa2, m[0]);
+              m[1] = __ffma2_rn(__fmul2_rn(make_float2(x[2], x[3]), make_float2(w0.z, w0.w)), sa2, m[1]);
+              m[2] = __ffma2_rn(__fmul2_rn(make_float2(x[4], x[5]), make_float2(w1.x, w1.y)), sa2, m[2]);
+              m[3] = __ffma2_rn(__fmul2_rn(make_float2(x[6], x[7]), make_float2(w1.z, w1.w)), sa2, m[3]);
+            } else {
+              const float w = kOneBlock || kFirst + k < edge ? s0 : s1;
+              const float2 w2 = make_float2(w, w);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) m[e] = __ffma2_rn(make_float2(x[2 * e], x[2 * e + 1]), w2, m[e]);
+            }
+          }
+        };
+        if constexpr (cols > kLoadCols) {
+          fold(std::integral_constant<int, 0>{}, std::integral_constant<int, kLoadCols>{});
+          fold(std::integral_constant<int, kLoadCols>{}, std::integral_constant<int, cols - kLoadCols>{});
+        } else {
+          fold(std::integral_constant<int, 0>{}, std::integral_constant<int, cols>{});
         }
         if (in_chunk == kChunk - 1 || g == groups - 1) {
           __syncwarp();
@@ -328,11 +328,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const int at = 4 * (lane & 3);
         const int row0 = tm * BM + BMC * (int)rank + 32 * q + (lane >> 2);
 #pragma unroll
-        for (int ch = 0; ch < kMaxCols / 16; ++ch) {
-          if (16 * ch < cols) {
+        for (int ch = 0; ch < (cols + 15) / 16; ++ch) {
+          {
             __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 4 && 16 * ch + 4 * e < cols; ++e)
               mine[e] = make_float4(sum[8 * ch + 2 * e].x, sum[8 * ch + 2 * e].y, sum[8 * ch + 2 * e + 1].x,
                                     sum[8 * ch + 2 * e + 1].y);
             __syncwarp();
@@ -342,7 +342,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
 #pragma unroll
-      for (int e = 0; e < kMaxCols / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
+      for (int e = 0; e < cols / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
     }
   }
 
@@ -364,23 +364,39 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 
 int64_t fp8_pair_smem(bool cols) { return cols ? f8::ScaleCfg<true>::kSmem : f8::ScaleCfg<false>::kSmem; }
 
+namespace {
+// f(kernel, its dynamic shared memory) for the kernel of a tile width and scale form.
+template <typename F>
+cudaError_t with_pair_kernel(int tile_n, bool cols, const F& f) {
+  constexpr size_t kBlocks = f8::ScaleCfg<false>::kSmem, kCols = f8::ScaleCfg<true>::kSmem;
+  switch (tile_n) {
+    case 256: return cols ? f(f8::fp8_pair_kernel<256, true>, kCols) : f(f8::fp8_pair_kernel<256, false>, kBlocks);
+    case 224: return cols ? f(f8::fp8_pair_kernel<224, true>, kCols) : f(f8::fp8_pair_kernel<224, false>, kBlocks);
+    case 192: return cols ? f(f8::fp8_pair_kernel<192, true>, kCols) : f(f8::fp8_pair_kernel<192, false>, kBlocks);
+    case 128: return cols ? f(f8::fp8_pair_kernel<128, true>, kCols) : f(f8::fp8_pair_kernel<128, false>, kBlocks);
+    case 64: return cols ? f(f8::fp8_pair_kernel<64, true>, kCols) : f(f8::fp8_pair_kernel<64, false>, kBlocks);
+  }
+  return cudaErrorInvalidValue;
+}
+}  // namespace
+
 cudaError_t prepare_fp8_pair() {
-  cudaError_t e = cudaFuncSetAttribute(f8::fp8_pair_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       f8::ScaleCfg<false>::kSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(f8::fp8_pair_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             f8::ScaleCfg<true>::kSmem);
-  return e;
+  for (int tile_n : kFp8PairTiles)
+    for (int cols = 0; cols < 2; ++cols) {
+      const cudaError_t e = with_pair_kernel(tile_n, cols != 0, [](auto kernel, size_t smem) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+      });
+      if (e != cudaSuccess) return e;
+    }
+  return cudaSuccess;
 }
 
-cudaError_t launch_fp8_pair(const CUtensorMap& mapA, const CUtensorMap& mapB, const Fp8PairParams& p,
+cudaError_t launch_fp8_pair(int tile_n, const CUtensorMap& mapA, const CUtensorMap& mapB, const Fp8PairParams& p,
                             cudaStream_t stream) {
-  const dim3 grid(2u * (unsigned)p.clusters);
-  if (p.sb.shift == 0)
-    f8::fp8_pair_kernel<true><<<grid, f8::kThreads, f8::ScaleCfg<true>::kSmem, stream>>>(mapA, mapB, p);
-  else
-    f8::fp8_pair_kernel<false><<<grid, f8::kThreads, f8::ScaleCfg<false>::kSmem, stream>>>(mapA, mapB, p);
-  return cudaGetLastError();
+  return with_pair_kernel(tile_n, p.sb.shift == 0, [&](auto kernel, size_t smem) {
+    kernel<<<2u * (unsigned)p.clusters, f8::kThreads, smem, stream>>>(mapA, mapB, p);
+    return cudaGetLastError();
+  });
 }
 
 }  // namespace sgemm_impl

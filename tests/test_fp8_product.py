@@ -94,7 +94,7 @@ def test_formats(force, kernel, ops, fa, fb):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("tile", range(32, 257, 32))
+@pytest.mark.parametrize("tile", [64, 128, 192, 224, 256])
 def test_pair_tiles(force, tile):
     """Every tile width, with column blocks that begin inside a tile, B in both orders and with both groupings."""
     force("FP8_PAIR", tile)
@@ -332,7 +332,7 @@ def test_refusals():
     refused(-13, "NT", 8, 8, 128, beta=1.0, C=FAKE, ldc=9, ldd=8)  # C in place has one stride
     refused(-14, "NT", 8, 8, 128, type=2)
     refused(4, "NT", 1 << 31, 8, 128)
-    for bad in (("FP8_PAIR", 16, 0), ("FP8_PAIR", 288, 0), ("FP8_SHORT", 144, 0), ("AUTO", 32, 0)):
+    for bad in (("FP8_PAIR", 16, 0), ("FP8_PAIR", 96, 0), ("FP8_PAIR", 288, 0), ("FP8_SHORT", 144, 0), ("AUTO", 32, 0)):
         with pytest.raises(sg.SgemmError):
             sg.sgemm_fp8_set_override(*bad)
     for bad in (("FP8_PAIR", 0, 2), ("FP8_SHORT", 0, 3)):
