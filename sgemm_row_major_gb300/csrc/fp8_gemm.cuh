@@ -68,16 +68,19 @@ __device__ __forceinline__ bool poll_wait(uint32_t bar, uint32_t parity, uint64_
   return ok;
 }
 
-// The same for one thread.
-__device__ __forceinline__ bool spin_wait(uint32_t bar, uint32_t parity, uint64_t timeout_ns) {
-  if (mbar_try_wait(bar, parity)) return true;
-  const uint64_t t0 = global_timer_ns();
-  for (;;) {
-#pragma unroll 1
-    for (int i = 0; i < 32; ++i)
-      if (mbar_try_wait(bar, parity)) return true;
-    if (global_timer_ns() - t0 > timeout_ns) return false;
-  }
+// True in one lane of a converged warp, the same one every time.  The warps that issue copies and
+// products run their loops with all lanes and issue under this predicate: operands that the compiler
+// can see to be the same in every lane stay in uniform registers, while in a branch of one lane each
+// operand of each instruction is moved there first (a group of four products then took 700 cycles
+// to issue).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "elect.sync _|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
 }
 
 // 32 consecutive 32-bit columns of this thread's TMEM lane.

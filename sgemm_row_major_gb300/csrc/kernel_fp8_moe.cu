@@ -252,45 +252,49 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
   const int groups = (p.hidden + BK - 1) / BK;
 
   if (warp == 0) {
-    if (lane == 0) {
-      const uint32_t bytes = (uint32_t)stage_bytes;
-      int t = 0;
-      bool ok = true;
-      for (int i = 0; ok && i < my_items; ++i) {
-        const int item = (int)blockIdx.x + i * (int)gridDim.x;
-        const int e = r.expert[item / col_tiles], c0 = (item % col_tiles) * kUpCols;
-        for (int g = 0; g < groups; ++g, ++t) {
-          const int s = t % p.up_stages;
-          if (t >= p.up_stages &&
-              !mbar_wait(smem_addr(&empty[s]), (uint32_t)((t / p.up_stages) - 1) & 1u, p.timeout_ns)) {
-            atomicOr(p.fault, (unsigned)kFaultEmptyWait);
-            ok = false;
-            break;
-          }
+    const uint32_t bytes = (uint32_t)stage_bytes;
+    int t = 0, s = 0;
+    uint32_t lap = 0;
+    bool ok = true;
+    for (int i = 0; ok && i < my_items; ++i) {
+      const int item = (int)blockIdx.x + i * (int)gridDim.x;
+      const int e = r.expert[item / col_tiles], c0 = (item % col_tiles) * kUpCols;
+      for (int g = 0; g < groups; ++g, ++t) {
+        if (lap > 0 && !poll_wait(smem_addr(&empty[s]), (lap - 1) & 1u, p.timeout_ns)) {
+          if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+          ok = false;
+          break;
+        }
+        if (elect_one()) {
           const uint32_t bar = smem_addr(&full[s]), a = sbase + (uint32_t)(s * stage_bytes);
           mbar_arrive_expect_tx(bar, bytes);
           tma_load_3d(a, &mapG, bar, g * BK, c0, e);
           tma_load_3d(a + kWTile / 2, &mapU, bar, g * BK, c0, e);
           tma_load_3d(a + kWTile, &mapX, bar, g * BK, 0, 0);
         }
-      }
-      for (int u = t > p.up_stages ? t - p.up_stages : 0; u < t; ++u)  // every copy has landed before the CTA ends
-        if (!mbar_wait(smem_addr(&full[u % p.up_stages]), (uint32_t)(u / p.up_stages) & 1u, p.timeout_ns))
-          atomicOr(p.fault, (unsigned)kFaultDrainWait);
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
-      const uint32_t idesc = moe_idesc(ncols);
-      const int units = my_items * groups;
-      int done = 0;
-      for (int t = 0; t < units; ++t) {
-        const int s = t % p.up_stages, b = t & 1;
-        if ((t >= 2 && !mbar_wait(smem_addr(&acc_empty[b]), (uint32_t)((t / 2) - 1) & 1u, p.timeout_ns)) ||
-            !mbar_wait(smem_addr(&full[s]), (uint32_t)(t / p.up_stages) & 1u, p.timeout_ns)) {
-          atomicOr(p.fault, (unsigned)kFaultFullWait);
-          break;
+        if (++s == p.up_stages) {
+          s = 0;
+          ++lap;
         }
-        tmem_fence_after_sync();
+      }
+    }
+    for (int u = t > p.up_stages ? t - p.up_stages : 0; u < t; ++u)  // every copy has landed before the CTA ends
+      if (!poll_wait(smem_addr(&full[u % p.up_stages]), (uint32_t)(u / p.up_stages) & 1u, p.timeout_ns) && lane == 0)
+        atomicOr(p.fault, (unsigned)kFaultDrainWait);
+  } else if (warp == 1) {
+    const uint32_t idesc = moe_idesc(ncols);
+    const int units = my_items * groups;
+    int t = 0, s = 0;
+    uint32_t lap = 0;
+    for (; t < units; ++t) {
+      const int b = t & 1;
+      if ((t >= 2 && !poll_wait(smem_addr(&acc_empty[b]), (uint32_t)((t / 2) - 1) & 1u, p.timeout_ns)) ||
+          !poll_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns)) {
+        if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+        break;
+      }
+      tmem_fence_after_sync();
+      if (elect_one()) {
         const uint32_t a = sbase + (uint32_t)(s * stage_bytes);
         const uint64_t wd = tile_desc(a), xd = tile_desc(a + kWTile);
 #pragma unroll
@@ -299,15 +303,19 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
                  ks == 0 ? 0u : 1u);
         mma_commit(smem_addr(&empty[s]));
         mma_commit(smem_addr(&acc_full[b]));
-        done = t + 1;
       }
-      for (int u = done > p.up_stages ? done - p.up_stages : 0; u < done; ++u)
-        if (!mbar_wait(smem_addr(&empty[u % p.up_stages]), (uint32_t)(u / p.up_stages) & 1u, p.timeout_ns))
-          atomicOr(p.fault, (unsigned)kFaultDrainWait);
-      for (int u = done > 2 ? done - 2 : 0; u < done; ++u)
-        if (!mbar_wait(smem_addr(&acc_full[u & 1]), (uint32_t)(u / 2) & 1u, p.timeout_ns))
-          atomicOr(p.fault, (unsigned)kFaultDrainWait);
+      __syncwarp();
+      if (++s == p.up_stages) {
+        s = 0;
+        ++lap;
+      }
     }
+    bool ok = true;  // every product has completed, and its commits have landed, before the CTA ends
+    for (int u = t > p.up_stages ? t - p.up_stages : 0; u < t; ++u)
+      ok = ok && poll_wait(smem_addr(&empty[u % p.up_stages]), (uint32_t)(u / p.up_stages) & 1u, p.timeout_ns);
+    for (int u = t > 2 ? t - 2 : 0; u < t; ++u)
+      ok = ok && poll_wait(smem_addr(&acc_full[u & 1]), (uint32_t)(u / 2) & 1u, p.timeout_ns);
+    if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultDrainWait);
   } else {
     const int q = warp & 3;
     const int row = 32 * q + lane;  // rows 0-63: gate, 64-127: up
@@ -336,7 +344,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
         }
         fold_barrier();
         if (ok) {  // a warp that gave up keeps meeting the others at the barriers
-          ok = warp_wait(smem_addr(&acc_full[b]), (uint32_t)(t / 2) & 1u, p.timeout_ns);
+          ok = poll_wait(smem_addr(&acc_full[b]), (uint32_t)(t / 2) & 1u, p.timeout_ns);
           if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
         }
         if (!ok) continue;
@@ -455,69 +463,74 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   const auto slots_of = [&](int a) { return (a + 1 < n_active ? base[a + 1] : n_slots) - base[a]; };
 
   if (warp == 0) {
-    if (lane == 0) {
-      int t = 0;
-      for (int u = u0; u < u1; ++u, ++t) {
-        const int s = t % p.down_stages;
-        if (t >= p.down_stages &&
-            !mbar_wait(smem_addr(&empty[s]), (uint32_t)((t / p.down_stages) - 1) & 1u, p.timeout_ns)) {
-          atomicOr(p.fault, (unsigned)kFaultEmptyWait);
-          break;
-        }
-        const int a = u / groups, k0 = (u - a * groups) * BK;
-        const int boxes = (slots_of(a) + 15) / 16;  // of 16 slots (32 rows)
+    int t = 0, s = 0;
+    uint32_t lap = 0;
+    for (int u = u0; u < u1; ++u, ++t) {
+      if (lap > 0 && !poll_wait(smem_addr(&empty[s]), (lap - 1) & 1u, p.timeout_ns)) {
+        if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+        break;
+      }
+      const int a = u / groups, k0 = (u - a * groups) * BK;
+      const int boxes = (slots_of(a) + 15) / 16;  // of 16 slots (32 rows)
+      const int e = expert[a], slot = base[a];
+      if (elect_one()) {
         const uint32_t bar = smem_addr(&full[s]), at = sbase + (uint32_t)(s * stage_bytes);
         mbar_arrive_expect_tx(bar, (uint32_t)(kWTile + boxes * 32 * BK));
-        tma_load_3d(at, &mapD, bar, k0, l0, expert[a]);
+        tma_load_3d(at, &mapD, bar, k0, l0, e);
         for (int i = 0; i < boxes; ++i)
-          tma_load_3d(at + kWTile + (uint32_t)(i * 32 * BK), &mapH, bar, k0, 2 * (base[a] + 16 * i), 0);
+          tma_load_3d(at + kWTile + (uint32_t)(i * 32 * BK), &mapH, bar, k0, 2 * (slot + 16 * i), 0);
       }
-      for (int v = t > p.down_stages ? t - p.down_stages : 0; v < t; ++v)
-        if (!mbar_wait(smem_addr(&full[v % p.down_stages]), (uint32_t)(v / p.down_stages) & 1u, p.timeout_ns))
-          atomicOr(p.fault, (unsigned)kFaultDrainWait);
+      if (++s == p.down_stages) {
+        s = 0;
+        ++lap;
+      }
     }
+    for (int v = t > p.down_stages ? t - p.down_stages : 0; v < t; ++v)
+      if (!poll_wait(smem_addr(&full[v % p.down_stages]), (uint32_t)(v / p.down_stages) & 1u, p.timeout_ns) && lane == 0)
+        atomicOr(p.fault, (unsigned)kFaultDrainWait);
   } else if (warp == 1) {
-    if (lane == 0) {
-      // a unit's two halves of 64 inner columns have scales, and so accumulators, of their own
-      int issued = 0, done = 0;
-      for (int t = 0; t < u1 - u0; ++t) {
-        const int s = t % p.down_stages;
-        if (!mbar_wait(smem_addr(&full[s]), (uint32_t)(t / p.down_stages) & 1u, p.timeout_ns)) {
-          atomicOr(p.fault, (unsigned)kFaultFullWait);
-          break;
-        }
-        const uint32_t idesc = moe_idesc(32 * ((slots_of((u0 + t) / groups) + 15) / 16));
-        const uint32_t at = sbase + (uint32_t)(s * stage_bytes);
-        const uint64_t wd = tile_desc(at), hd = tile_desc(at + kWTile);
-        bool ok = true;
-        for (int b = 0; b < 2; ++b) {
-          if (t > 0 && !mbar_wait(smem_addr(&acc_empty[b]), (uint32_t)(t - 1) & 1u, p.timeout_ns)) {
-            ok = false;
-            break;
-          }
-          tmem_fence_after_sync();
+    // a unit's two halves of 64 inner columns have scales, and so accumulators, of their own
+    int issued = 0, done = 0, s = 0;
+    uint32_t lap = 0;
+    for (int t = 0; t < u1 - u0; ++t) {
+      bool ok = poll_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns);
+      const uint32_t idesc = moe_idesc(32 * ((slots_of((u0 + t) / groups) + 15) / 16));
+      const uint32_t at = sbase + (uint32_t)(s * stage_bytes);
+      const uint64_t wd = tile_desc(at), hd = tile_desc(at + kWTile);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        ok = ok && (t == 0 || poll_wait(smem_addr(&acc_empty[b]), (uint32_t)(t - 1) & 1u, p.timeout_ns));
+        if (!ok) break;
+        tmem_fence_after_sync();
+        if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks)
             mma_f8(tmem + (uint32_t)(128 * b), wd + (uint64_t)(2 * b + ks) * step_of(0),
                    hd + (uint64_t)(2 * b + ks) * step_of(0), idesc, ks == 0 ? 0u : 1u);
           mma_commit(smem_addr(&acc_full[b]));
+          if (b == 1) mma_commit(smem_addr(&empty[s]));
         }
-        mma_commit(smem_addr(&empty[s]));
-        issued = t + 1;
-        if (!ok) {
-          atomicOr(p.fault, (unsigned)kFaultFullWait);
-          break;
-        }
-        done = t + 1;
+        __syncwarp();
       }
-      for (int u = issued > p.down_stages ? issued - p.down_stages : 0; u < issued; ++u)
-        if (!mbar_wait(smem_addr(&empty[u % p.down_stages]), (uint32_t)(u / p.down_stages) & 1u, p.timeout_ns))
-          atomicOr(p.fault, (unsigned)kFaultDrainWait);
-      if (done > 0)
-        for (int b = 0; b < 2; ++b)
-          if (!mbar_wait(smem_addr(&acc_full[b]), (uint32_t)(done - 1) & 1u, p.timeout_ns))
-            atomicOr(p.fault, (unsigned)kFaultDrainWait);
+      if (!ok) {
+        if (elect_one()) mma_commit(smem_addr(&empty[s]));
+        __syncwarp();
+        issued = t + 1;
+        if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+        break;
+      }
+      issued = done = t + 1;
+      if (++s == p.down_stages) {
+        s = 0;
+        ++lap;
+      }
     }
+    bool ok = true;  // every product has completed, and its commits have landed, before the CTA ends
+    for (int u = issued > p.down_stages ? issued - p.down_stages : 0; u < issued; ++u)
+      ok = ok && poll_wait(smem_addr(&empty[u % p.down_stages]), (uint32_t)(u / p.down_stages) & 1u, p.timeout_ns);
+    for (int b = 0; b < 2 && done > 0; ++b)
+      ok = ok && poll_wait(smem_addr(&acc_full[b]), (uint32_t)(done - 1) & 1u, p.timeout_ns);
+    if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultDrainWait);
   } else {
     const int q = warp & 3;
     const int row = 32 * q + lane;
@@ -545,7 +558,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
       }
       fold_barrier();
       if (ok) {  // a warp that gave up keeps meeting the others at the barrier
-        ok = warp_wait(smem_addr(&acc_full[b]), (uint32_t)t & 1u, p.timeout_ns);
+        ok = poll_wait(smem_addr(&acc_full[b]), (uint32_t)t & 1u, p.timeout_ns);
         if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
       }
       if (!ok) continue;

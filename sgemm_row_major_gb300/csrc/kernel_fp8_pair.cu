@@ -121,71 +121,85 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (lane == 0) {
         prefetch_tensormap(&mapA);
         prefetch_tensormap(&mapB);
-        const uint32_t bytes = 2u * (uint32_t)(kPart + (p.b_mn ? kPart : halfn * BK));  // both CTAs'
-        int t = 0;
-        bool ok = true;
-        for (int i = 0; ok && i < my_tiles; ++i) {
-          int tm, tn;
-          tile_coords(cl + i * p.clusters, p.tiles_m, p.tiles_n, tm, tn);
-          const int m0 = tm * BM + BMC * (int)rank, n0 = tn * TN + halfn * (int)rank;
-          for (int g = 0; g < groups; ++g, ++t) {
-            const int s = t % kStages;
-            if (t >= kStages && !spin_wait(smem_addr(&done[s]), (uint32_t)((t / kStages) - 1) & 1u, p.timeout_ns)) {
-              atomicOr(p.fault, (unsigned)kFaultEmptyWait);
-              ok = false;
-              break;
-            }
+      }
+      __syncwarp();
+      const uint32_t bytes = 2u * (uint32_t)(kPart + (p.b_mn ? kPart : halfn * BK));  // both CTAs'
+      const uint32_t full0 = map_to_rank(smem_addr(&full[0]), 0);
+      int t = 0, s = 0;
+      uint32_t lap = 0;
+      bool ok = true;
+      for (int i = 0; ok && i < my_tiles; ++i) {
+        int tm, tn;
+        tile_coords(cl + i * p.clusters, p.tiles_m, p.tiles_n, tm, tn);
+        const int m0 = tm * BM + BMC * (int)rank, n0 = tn * TN + halfn * (int)rank;
+        for (int g = 0; g < groups; ++g, ++t) {
+          if (lap > 0 && !poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
+            if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
             // both CTAs' loads complete on the even CTA's barrier, which expects all their bytes
-            const uint32_t fb = map_to_rank(smem_addr(&full[s]), 0);
+            const uint32_t fb = full0 + 8u * (uint32_t)s;
             if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), bytes);
             const uint32_t a = sbase + (uint32_t)(s * kStageBytes), b = a + kPart;
             tma_load_pair(a, &mapA, fb, p.a_mn ? m0 : g * BK, p.a_mn ? g * BK : m0);
             tma_load_pair(b, &mapB, fb, p.b_mn ? n0 : g * BK, p.b_mn ? g * BK : n0);
           }
-        }
-        // leave only when every copy into shared memory has landed (the odd CTA's warp 1 waits for
-        // the products that read its last stages)
-        if (rank == 0)
-          for (int u = t > kStages ? t - kStages : 0; u < t; ++u)
-            if (!mbar_wait(smem_addr(&full[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns))
-              atomicOr(p.fault, (unsigned)kFaultDrainWait);
-      }
-    } else if (warp == 1) {
-      if (lane == 0 && rank != 0) {
-        bool ok = true;
-        for (int u = units > kStages ? units - kStages : 0; ok && u < units; ++u)
-          ok = mbar_wait(smem_addr(&done[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns);
-        if (!ok) atomicOr(p.fault, (unsigned)kFaultFullWait);
-      } else if (lane == 0) {
-        // ---------------------------------------------- products (even CTA)
-        const uint64_t astep = step_of(p.a_mn), bstep = step_of(p.b_mn);
-        int t = 0, b = 0;
-        uint32_t lap = 0;  // passes over the accumulators
-        bool ok = true;
-        for (; t < units; ++t) {
-          const int s = t % kStages;
-          ok = (lap == 0 || spin_wait(smem_addr(&acc_empty[b]), (lap - 1) & 1u, p.timeout_ns)) &&
-               spin_wait(smem_addr(&full[s]), (uint32_t)(t / kStages) & 1u, p.timeout_ns);
-          if (!ok) break;
-          tmem_fence_after_sync();
-          const uint32_t acc = tmem + (uint32_t)(b * TN);
-          const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
-          const uint64_t ad = tile_desc(a), bd = tile_desc(a + kPart);
-#pragma unroll
-          for (int ks = 0; ks < BK / 32; ++ks)
-            mma_f8_pair(acc, ad + (uint64_t)ks * astep, bd + (uint64_t)ks * bstep, p.idesc, ks == 0 ? 0u : 1u);
-          mma_commit_pair(smem_addr(&done[s]));  // in both CTAs: stage s is free, the accumulator holds group t
-          if (++b == bufs) {
-            b = 0;
+          if (++s == kStages) {
+            s = 0;
             ++lap;
           }
         }
-        if (!ok) atomicOr(p.fault, (unsigned)kFaultFullWait);
-        // leave only when every product has completed and its commits have landed here
-        for (int u = t > kStages ? t - kStages : 0; u < t; ++u)
-          if (!mbar_wait(smem_addr(&done[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns))
-            atomicOr(p.fault, (unsigned)kFaultDrainWait);
       }
+      // leave only when every copy into shared memory has landed (the odd CTA's warp 1 waits for
+      // the products that read its last stages)
+      if (rank == 0)
+        for (int u = t > kStages ? t - kStages : 0; u < t; ++u)
+          if (!poll_wait(smem_addr(&full[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns) && lane == 0)
+            atomicOr(p.fault, (unsigned)kFaultDrainWait);
+    } else if (warp == 1) {
+      int t = 0;  // groups whose products have been issued (odd CTA: will be)
+      if (rank != 0) {
+        t = units;
+      } else {
+        // ---------------------------------------------- products (even CTA)
+        const uint64_t astep = step_of(p.a_mn), bstep = step_of(p.b_mn);
+        int s = 0, b = 0;
+        uint32_t s_lap = 0, b_lap = 0;
+        for (; t < units; ++t) {
+          if (!((b_lap == 0 || poll_wait(smem_addr(&acc_empty[b]), (b_lap - 1) & 1u, p.timeout_ns)) &&
+                poll_wait(smem_addr(&full[s]), s_lap & 1u, p.timeout_ns))) {
+            if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+            break;
+          }
+          tmem_fence_after_sync();
+          if (elect_one()) {
+            const uint32_t acc = tmem + (uint32_t)(b * TN);
+            const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
+            const uint64_t ad = tile_desc(a), bd = tile_desc(a + kPart);
+#pragma unroll
+            for (int ks = 0; ks < BK / 32; ++ks)
+              mma_f8_pair(acc, ad + (uint64_t)ks * astep, bd + (uint64_t)ks * bstep, p.idesc, ks == 0 ? 0u : 1u);
+            mma_commit_pair(smem_addr(&done[s]));  // in both CTAs: stage s is free, the accumulator holds group t
+          }
+          __syncwarp();
+          if (++b == bufs) {
+            b = 0;
+            ++b_lap;
+          }
+          if (++s == kStages) {
+            s = 0;
+            ++s_lap;
+          }
+        }
+      }
+      // leave only when every product has completed and its commits have landed in this CTA
+      for (int u = t > kStages ? t - kStages : 0; u < t; ++u)
+        if (!poll_wait(smem_addr(&done[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns)) {
+          if (lane == 0) atomicOr(p.fault, (unsigned)kFaultDrainWait);
+          break;
+        }
     } else {
       // ------------------------------------------------ scales, 8 groups at a time, up to kChunks ahead
       // of the folders (the latency of a load is several groups' time): warp 2 of this CTA's 128 rows,

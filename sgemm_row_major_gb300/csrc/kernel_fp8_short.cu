@@ -85,39 +85,44 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_short_kernel(const __grid_con
 
   if (warp == 0) {
     // ------------------------------------------------ loads
-    if (lane == 0) {
-      const uint32_t bytes = (uint32_t)(BL * BK + (p.s_mn ? 128 * BK : p.tile_s * BK));
-      int t = 0;
-      for (; t < units; ++t) {
-        const int s = t % p.stages;
-        if (t >= p.stages && !mbar_wait(smem_addr(&empty[s]), (uint32_t)((t / p.stages) - 1) & 1u, p.timeout_ns)) {
-          atomicOr(p.fault, (unsigned)kFaultEmptyWait);
-          break;
-        }
+    const uint32_t bytes = (uint32_t)(BL * BK + (p.s_mn ? 128 * BK : p.tile_s * BK));
+    int t = 0, s = 0;
+    uint32_t lap = 0;
+    for (; t < units; ++t) {
+      if (lap > 0 && !poll_wait(smem_addr(&empty[s]), (lap - 1) & 1u, p.timeout_ns)) {
+        if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+        break;
+      }
+      if (elect_one()) {
         const int k0 = (g0 + t) * BK;
         const uint32_t bar = smem_addr(&full[s]), a = sbase + (uint32_t)(s * p.stage_bytes);
         mbar_arrive_expect_tx(bar, bytes);
         tma_load(a, &mapL, bar, p.l_mn ? l0 : k0, p.l_mn ? k0 : l0);
         tma_load(a + BL * BK, &mapS, bar, p.s_mn ? s0 : k0, p.s_mn ? k0 : s0);
       }
-      // leave only when every copy into shared memory has landed
-      for (int u = t > p.stages ? t - p.stages : 0; u < t; ++u)
-        if (!mbar_wait(smem_addr(&full[u % p.stages]), (uint32_t)(u / p.stages) & 1u, p.timeout_ns))
-          atomicOr(p.fault, (unsigned)kFaultDrainWait);
+      if (++s == p.stages) {
+        s = 0;
+        ++lap;
+      }
     }
+    // leave only when every copy into shared memory has landed
+    for (int u = t > p.stages ? t - p.stages : 0; u < t; ++u)
+      if (!poll_wait(smem_addr(&full[u % p.stages]), (uint32_t)(u / p.stages) & 1u, p.timeout_ns) && lane == 0)
+        atomicOr(p.fault, (unsigned)kFaultDrainWait);
   } else if (warp == 1) {
     // ------------------------------------------------ products
-    if (lane == 0) {
-      const uint64_t lstep = step_of(p.l_mn), sstep = step_of(p.s_mn);
-      int done = 0;
-      for (int t = 0; t < units; ++t) {
-        const int s = t % p.stages, b = t & 1;
-        if ((t >= 2 && !mbar_wait(smem_addr(&acc_empty[b]), (uint32_t)((t / 2) - 1) & 1u, p.timeout_ns)) ||
-            !mbar_wait(smem_addr(&full[s]), (uint32_t)(t / p.stages) & 1u, p.timeout_ns)) {
-          atomicOr(p.fault, (unsigned)kFaultFullWait);
-          break;
-        }
-        tmem_fence_after_sync();
+    const uint64_t lstep = step_of(p.l_mn), sstep = step_of(p.s_mn);
+    int t = 0, s = 0;
+    uint32_t lap = 0;
+    for (; t < units; ++t) {
+      const int b = t & 1;
+      if ((t >= 2 && !poll_wait(smem_addr(&acc_empty[b]), (uint32_t)((t / 2) - 1) & 1u, p.timeout_ns)) ||
+          !poll_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns)) {
+        if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+        break;
+      }
+      tmem_fence_after_sync();
+      if (elect_one()) {
         const uint32_t a = sbase + (uint32_t)(s * p.stage_bytes);
         const uint64_t ld = tile_desc(a), sd = tile_desc(a + BL * BK);
 #pragma unroll
@@ -126,16 +131,20 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_short_kernel(const __grid_con
                  ks == 0 ? 0u : 1u);
         mma_commit(smem_addr(&empty[s]));
         mma_commit(smem_addr(&acc_full[b]));
-        done = t + 1;
       }
-      // leave only when every product has completed and its commits have landed
-      for (int u = done > p.stages ? done - p.stages : 0; u < done; ++u)
-        if (!mbar_wait(smem_addr(&empty[u % p.stages]), (uint32_t)(u / p.stages) & 1u, p.timeout_ns))
-          atomicOr(p.fault, (unsigned)kFaultDrainWait);
-      for (int u = done > 2 ? done - 2 : 0; u < done; ++u)
-        if (!mbar_wait(smem_addr(&acc_full[u & 1]), (uint32_t)(u / 2) & 1u, p.timeout_ns))
-          atomicOr(p.fault, (unsigned)kFaultDrainWait);
+      __syncwarp();
+      if (++s == p.stages) {
+        s = 0;
+        ++lap;
+      }
     }
+    // leave only when every product has completed and its commits have landed
+    bool ok = true;
+    for (int u = t > p.stages ? t - p.stages : 0; u < t; ++u)
+      ok = ok && poll_wait(smem_addr(&empty[u % p.stages]), (uint32_t)(u / p.stages) & 1u, p.timeout_ns);
+    for (int u = t > 2 ? t - 2 : 0; u < t; ++u)
+      ok = ok && poll_wait(smem_addr(&acc_full[u & 1]), (uint32_t)(u / 2) & 1u, p.timeout_ns);
+    if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultDrainWait);
   }
 
   // ------------------------------------------------ folders: row 32q + lane of the tile, all its columns
@@ -162,7 +171,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_short_kernel(const __grid_con
       }
       fold_barrier();
       if (ok) {  // a warp that gave up keeps meeting the others at the barrier
-        ok = warp_wait(smem_addr(&acc_full[b]), (uint32_t)(t / 2) & 1u, p.timeout_ns);
+        ok = poll_wait(smem_addr(&acc_full[b]), (uint32_t)(t / 2) & 1u, p.timeout_ns);
         if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
       }
       if (!ok) continue;
