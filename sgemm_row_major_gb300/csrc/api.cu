@@ -106,7 +106,9 @@ int device_state(int* device_out, DeviceState** st_out) {
       if (err == cudaSuccess) err = prepare_presplit();
       if (err == cudaSuccess) err = prepare_skinny();
       if (err == cudaSuccess) err = prepare_fp8_norm();
-      if (err == cudaSuccess) err = prepare_fp8_pair();
+      if (err == cudaSuccess) err = prepare_fp8_pair_plain();
+      if (err == cudaSuccess) err = prepare_fp8_pair_add();
+      if (err == cudaSuccess) err = prepare_fp8_pair_any();
       if (err == cudaSuccess) err = prepare_fp8_short();
       if (err == cudaSuccess) err = prepare_fp8_moe();
       if (err == cudaSuccess) st.pair_clusters = pair_clusters_or_none();

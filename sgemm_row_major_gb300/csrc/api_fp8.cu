@@ -228,7 +228,8 @@ cudaError_t launch_product(const Product& pr, const sgemm_plan_t& plan, const Ca
     p.clusters = (int)(plan.grid_x / 2);
     p.timeout_ns = wait_timeout_ns();
     p.fault = dev.fault;
-    return launch_fp8_pair(plan.tile_n, ma, mb, p, stream);
+    return (!p.out.vec ? launch_fp8_pair_any : p.out.beta != 0.0f ? launch_fp8_pair_add : launch_fp8_pair_plain)(
+        plan.tile_n, ma, mb, p, stream);
   }
   const bool trans = pr.M <= pr.N;
   const Operand &l = trans ? pr.b : pr.a, &s = trans ? pr.a : pr.b;
@@ -388,7 +389,8 @@ int sgemm_fp8_quantize(int64_t rows, int64_t cols, const void* X, int type, int6
   p.s = scale;
   p.lds = lds;
   p.format = format;
-  p.vec = rows16(X, ldx, type_size(type)) && aligned(codes, 8) && ldq % 8 == 0;
+  p.x_vec = rows16(X, ldx, type_size(type));
+  p.q_vec = aligned(codes, 8) && ldq % 8 == 0;
   return launch_status(launch_fp8_quantize(type, block_rows, block_cols, p, reinterpret_cast<cudaStream_t>(stream)));
 }
 

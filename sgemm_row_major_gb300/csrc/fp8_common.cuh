@@ -29,15 +29,20 @@ __device__ __forceinline__ float group_scale(float amax, float top) { return fma
 // Two values (already divided by their scale, so at most `top` a rounding or two beyond it when
 // finite) to two codes, the first in the low byte; round to nearest even, NaN for a non-finite
 // value (the conversion alone would turn an infinity into the largest finite code).
+// CHECK = false: no value is infinite (a NaN needs no test).
+template <bool CHECK>
 __device__ __forceinline__ uint32_t codes2(float a, float b, bool e5m2) {
-  const float nan = __int_as_float(0x7FFFFFFF);
-  a = fabsf(a) <= kMaxFloat ? a : nan;
-  b = fabsf(b) <= kMaxFloat ? b : nan;
+  if (CHECK) {
+    const float nan = __int_as_float(0x7FFFFFFF);
+    a = fabsf(a) <= kMaxFloat ? a : nan;
+    b = fabsf(b) <= kMaxFloat ? b : nan;
+  }
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, e5m2 ? __NV_E5M2 : __NV_E4M3);
 }
 
-__device__ __forceinline__ uint32_t codes4(const float* v, float inv, bool e5m2) {
-  return codes2(v[0] * inv, v[1] * inv, e5m2) | (codes2(v[2] * inv, v[3] * inv, e5m2) << 16);
+template <bool CHECK>
+__device__ __forceinline__ uint32_t codes4(const float* v, const float* inv, bool e5m2) {
+  return codes2<CHECK>(v[0] * inv[0], v[1] * inv[1], e5m2) | (codes2<CHECK>(v[2] * inv[2], v[3] * inv[3], e5m2) << 16);
 }
 
 // V consecutive elements as stored (16 bytes): 4 floats or 8 BF16 values.
@@ -116,12 +121,13 @@ __device__ __forceinline__ void store_chunk(T* p, const float* v, int64_t n, boo
   }
 }
 
-// V codes (4 or 8) of one chunk; `vec`: p is aligned to V bytes.
-template <int V>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float* v, float inv, int64_t n, bool vec, bool e5m2) {
+// V codes (4 or 8) of one chunk, value i times inv[i]; `vec`: p is aligned to V bytes.
+template <int V, bool CHECK>
+__device__ __forceinline__ void store_codes(uint8_t* p, const float* v, const float* inv, int64_t n, bool vec,
+                                            bool e5m2) {
   uint32_t u[V / 4];
 #pragma unroll
-  for (int i = 0; i < V / 4; ++i) u[i] = codes4(v + 4 * i, inv, e5m2);
+  for (int i = 0; i < V / 4; ++i) u[i] = codes4<CHECK>(v + 4 * i, inv + 4 * i, e5m2);
   if (vec && n >= V) {
     if (V == 4) *reinterpret_cast<uint32_t*>(p) = u[0];
     else        *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[V / 4 - 1]);

@@ -1,4 +1,4 @@
-// fp8_gemm.cuh -- device helpers of the block-scaled 8-bit products (kernel_fp8_pair.cu,
+// fp8_gemm.cuh -- device helpers of the block-scaled 8-bit products (kernel_fp8_pair.cuh,
 // kernel_fp8_short.cu): tile descriptors, the tensor-core instructions, and the output's rows.
 #pragma once
 
@@ -153,66 +153,103 @@ __device__ __forceinline__ void store_one(const Fp8Out& o, int64_t row, int64_t 
   else        static_cast<float*>(o.D)[i] = x;
 }
 
-// Columns col .. col + 3 of a row, as far as they are in D, from their sums; vectors where out.vec
-// (col is a multiple of 4).
-__device__ __forceinline__ void store_four(const Fp8Out& o, int64_t row, int col, const float4 v) {
-  if (!o.vec || col + 4 > o.N) {
-    const float x[4] = {v.x, v.y, v.z, v.w};
+// A 32-row x 16-column piece of D from its sums in shared memory (`piece`, `pitch` words from row to
+// row), by one warp; its first row and column, of which `cols` are the tile's.  With aligned rows four
+// lanes hold 16 consecutive columns (64 bytes of FP32, 32 of BF16) of 8 rows at a time, otherwise 16
+// lanes hold one element each of 2 rows; what C holds is loaded for several rows before any is used.
+// OUT: which of these D and C need, known where the kernel is chosen (the caller holds 64 sums in
+// registers meanwhile: all cases in one kernel spilled them, and cost 9% at 8192^3).
+enum Output {
+  kOutPlain = 0,  // beta == 0, aligned rows
+  kOutAdd = 1,    // beta != 0, aligned rows
+  kOutAny = 2     // any alignment and beta
+};
+template <int OUT>
+__device__ __forceinline__ void store_piece(const Fp8Out& o, int row0, int col0, int cols, const float* piece,
+                                            int pitch) {
+  const int lane = threadIdx.x & 31;
+  if (OUT != kOutAny && col0 + cols <= o.N) {
+    const int at = 4 * (lane & 3), row = row0 + (lane >> 2);
+    if (at >= cols) return;
+    const float* v = piece + (lane >> 2) * pitch + at;
+    int64_t i = (int64_t)row * o.ldd + col0 + at;
+    if (OUT == kOutPlain) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (col + e < o.N) store_one(o, row, col + e, x[e]);
-    return;
-  }
-  float4 x = make_float4(o.alpha * v.x, o.alpha * v.y, o.alpha * v.z, o.alpha * v.w);
-  if (o.beta != 0.0f) {
-    float4 c;
-    const int64_t i = row * o.ldc + col;
-    if (o.bf16) {
-      const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(o.C) + i);
-      c = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u), __uint_as_float(u.y << 16),
-                      __uint_as_float(u.y & 0xFFFF0000u));
+      for (int r = 0; r < 4; ++r, i += 8 * o.ldd) {
+        const float4 x = *reinterpret_cast<const float4*>(v + 8 * r * pitch);
+        if (row + 8 * r < o.M) {
+          if (o.bf16) {
+            const __nv_bfloat162 a = __floats2bfloat162_rn(o.alpha * x.x, o.alpha * x.y);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(o.alpha * x.z, o.alpha * x.w);
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.D) + i) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+          } else {
+            *reinterpret_cast<float4*>(static_cast<float*>(o.D) + i) =
+                make_float4(o.alpha * x.x, o.alpha * x.y, o.alpha * x.z, o.alpha * x.w);
+          }
+        }
+      }
+    } else if (!o.bf16) {
+      int64_t j = (int64_t)row * o.ldc + col0 + at;
+#pragma unroll 1
+      for (int r = 0; r < 32; r += 16) {
+        float4 u[2];
+#pragma unroll
+        for (int k = 0; k < 2; ++k, j += 8 * o.ldc)
+          if (row + r + 8 * k < o.M) u[k] = *reinterpret_cast<const float4*>(static_cast<const float*>(o.C) + j);
+#pragma unroll
+        for (int k = 0; k < 2; ++k, i += 8 * o.ldd) {
+          const float4 x = *reinterpret_cast<const float4*>(v + (r + 8 * k) * pitch);
+          if (row + r + 8 * k < o.M)
+            *reinterpret_cast<float4*>(static_cast<float*>(o.D) + i) =
+                make_float4(fmaf(o.alpha, x.x, o.beta * u[k].x), fmaf(o.alpha, x.y, o.beta * u[k].y),
+                            fmaf(o.alpha, x.z, o.beta * u[k].z), fmaf(o.alpha, x.w, o.beta * u[k].w));
+        }
+      }
     } else {
-      c = *reinterpret_cast<const float4*>(static_cast<const float*>(o.C) + i);
-    }
-    x = make_float4(fmaf(o.alpha, v.x, o.beta * c.x), fmaf(o.alpha, v.y, o.beta * c.y),
-                    fmaf(o.alpha, v.z, o.beta * c.z), fmaf(o.alpha, v.w, o.beta * c.w));
-  }
-  const int64_t i = row * o.ldd + col;
-  if (o.bf16) {
-    const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
-    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.D) + i) =
-        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-  } else {
-    *reinterpret_cast<float4*>(static_cast<float*>(o.D) + i) = x;
-  }
-}
-
-// Columns col .. col + 3 (as far as they are in D) of rows row, row + 8, row + 16 and row + 24 from
-// their sums, at v and 8, 16 and 24 pitches further: four lanes hold 16 consecutive columns, so a
-// warp's store writes 64 (BF16: 32) consecutive bytes of 8 rows.
-__device__ __forceinline__ void store_rows(const Fp8Out& o, int row, int col, const float* v, int pitch) {
-  if (o.vec && col + 4 <= o.N && o.beta == 0.0f) {
-    const int64_t step = 8 * o.ldd;
-    int64_t i = (int64_t)row * o.ldd + col;
+      int64_t j = (int64_t)row * o.ldc + col0 + at;
+#pragma unroll 1
+      for (int r = 0; r < 32; r += 16) {
+        uint2 u[2];
 #pragma unroll
-    for (int r = 0; r < 4; ++r, i += step) {
-      const float4 x = *reinterpret_cast<const float4*>(v + 8 * r * pitch);
-      if (row + 8 * r < o.M) {
-        if (o.bf16) {
-          const __nv_bfloat162 a = __floats2bfloat162_rn(o.alpha * x.x, o.alpha * x.y);
-          const __nv_bfloat162 b = __floats2bfloat162_rn(o.alpha * x.z, o.alpha * x.w);
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.D) + i) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-        } else {
-          *reinterpret_cast<float4*>(static_cast<float*>(o.D) + i) =
-              make_float4(o.alpha * x.x, o.alpha * x.y, o.alpha * x.z, o.alpha * x.w);
+        for (int k = 0; k < 2; ++k, j += 8 * o.ldc)
+          if (row + r + 8 * k < o.M) u[k] = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(o.C) + j);
+#pragma unroll
+        for (int k = 0; k < 2; ++k, i += 8 * o.ldd) {
+          const float4 x = *reinterpret_cast<const float4*>(v + (r + 8 * k) * pitch);
+          if (row + r + 8 * k < o.M) {
+            const __nv_bfloat162 a =
+                __floats2bfloat162_rn(fmaf(o.alpha, x.x, o.beta * __uint_as_float(u[k].x << 16)),
+                                      fmaf(o.alpha, x.y, o.beta * __uint_as_float(u[k].x & 0xFFFF0000u)));
+            const __nv_bfloat162 b =
+                __floats2bfloat162_rn(fmaf(o.alpha, x.z, o.beta * __uint_as_float(u[k].y << 16)),
+                                      fmaf(o.alpha, x.w, o.beta * __uint_as_float(u[k].y & 0xFFFF0000u)));
+            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.D) + i) =
+                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+          }
         }
       }
     }
-  } else {
+    return;
+  }
+  const int at = lane & 15, col = col0 + at;
+  if (at >= cols || col >= o.N) return;
 #pragma unroll 1
-    for (int r = 0; r < 4; ++r)
-      if (row + 8 * r < o.M) store_four(o, row + 8 * r, col, *reinterpret_cast<const float4*>(v + 8 * r * pitch));
+  for (int r0 = lane >> 4; r0 < 32; r0 += 8) {
+    float c[4];
+    if (OUT != kOutPlain && o.beta != 0.0f)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (row0 + r0 + 2 * r < o.M) c[r] = read_c(o, (int64_t)(row0 + r0 + 2 * r) * o.ldc + col);
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+      const float v = piece[(r0 + 2 * r) * pitch + at];
+      if (row0 + r0 + 2 * r >= o.M) continue;
+      const float x = OUT != kOutPlain && o.beta != 0.0f ? fmaf(o.alpha, v, o.beta * c[r]) : o.alpha * v;
+      const int64_t i = (int64_t)(row0 + r0 + 2 * r) * o.ldd + col;
+      if (o.bf16) static_cast<__nv_bfloat16*>(o.D)[i] = __float2bfloat16_rn(x);
+      else        static_cast<float*>(o.D)[i] = x;
+    }
   }
 }
 

@@ -27,7 +27,7 @@ struct QuantParams {
   float* s = nullptr;
   int64_t lds = 0;
   int format = 0;
-  int vec = 0;  // 1: 16-byte loads and whole-vector stores are aligned
+  int x_vec = 0, q_vec = 0;  // 1: rows of X start at multiples of 16 bytes, of codes at multiples of 8
 };
 cudaError_t launch_fp8_quantize(int type, int block_rows, int block_cols, const QuantParams& p, cudaStream_t stream);
 
@@ -66,7 +66,7 @@ cudaError_t prepare_fp8_norm();
 int fp8_rmsnorm_backward_grid(int type, int64_t rows, int cols, int sm_count);
 cudaError_t launch_fp8_rmsnorm_backward(int type, const NormGradParams& p, int grid, cudaStream_t stream);
 
-// ---- product (kernel_fp8_pair.cu, kernel_fp8_short.cu)
+// ---- product (kernel_fp8_pair.cuh, kernel_fp8_short.cu)
 
 // Scales of one operand of a product: of row (or column) i of op(X) in group g of 128 k,
 // p[(i >> shift) * si + g * sk].
@@ -99,10 +99,17 @@ struct Fp8PairParams {
 };
 constexpr int kFp8PairStages = 5, kFp8PairThreads = 640;
 int64_t fp8_pair_smem(bool cols);  // dynamic shared memory; cols: B has a scale per column
-cudaError_t prepare_fp8_pair();
 constexpr int kFp8PairTiles[] = {256, 224, 192, 128, 64};  // the tile widths there are kernels for
-cudaError_t launch_fp8_pair(int tile_n, const CUtensorMap& mapA, const CUtensorMap& mapB, const Fp8PairParams& p,
-                            cudaStream_t stream);
+// One translation unit per form of the output: beta == 0 and aligned rows, beta != 0 and aligned
+// rows, anything.
+#define SGEMM_DECLARE_FP8_PAIR(name)                                                               \
+  cudaError_t prepare_fp8_pair_##name();                                                           \
+  cudaError_t launch_fp8_pair_##name(int tile_n, const CUtensorMap& mapA, const CUtensorMap& mapB, \
+                                     const Fp8PairParams& p, cudaStream_t stream);
+SGEMM_DECLARE_FP8_PAIR(plain)
+SGEMM_DECLARE_FP8_PAIR(add)
+SGEMM_DECLARE_FP8_PAIR(any)
+#undef SGEMM_DECLARE_FP8_PAIR
 
 // The longer of M and N runs along the tensor-core rows (`l`), the other along the columns (`s`).
 struct Fp8ShortParams {

@@ -385,10 +385,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
         const float scale = group_scale(lanes_max<32>(fmaxf(finite_abs(h[0]), finite_abs(h[1]))), kMaxE4M3);
         const float inv = __frcp_rn(scale);
         const float v0 = h[0] * inv, v1 = h[1] * inv;
-        const uint32_t hi = codes2(v0, v1, false);
+        const uint32_t hi = codes2<true>(v0, v1, false);
         const __half2 back = __half2(__nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)hi, __NV_E4M3));
         const float2 f = __half22float2(back);
-        const uint32_t lo = codes2((v0 - f.x) * kLoScale, (v1 - f.y) * kLoScale, false);
+        const uint32_t lo = codes2<true>((v0 - f.x) * kLoScale, (v1 - f.y) * kLoScale, false);
         const int col = c0 + 2 * lane;
         const int64_t slot = r.base[a] + j;
         if (col < p.inner) {  // inner is even

@@ -74,7 +74,10 @@ __device__ __forceinline__ void emit(const NormParams& p, int64_t row, int col, 
     const float s = group_scale(lanes_max<16>(m), kMaxE4M3);
     if (left > 0) {
       if (col % 128 == 0) p.s[row * p.lds + col / 128] = s;
-      store_codes<kChunk>(p.q + row * p.ldq + col, y, __frcp_rn(s), left, vec, false);
+      float inv[kChunk];
+#pragma unroll
+      for (int e = 0; e < kChunk; ++e) inv[e] = __frcp_rn(s);
+      store_codes<kChunk, true>(p.q + row * p.ldq + col, y, inv, left, vec, false);
     }
   }
 }

@@ -1,4 +1,5 @@
-// kernel_fp8_pair.cu -- block-scaled 8-bit product on CTA pairs for sm_103a.
+// kernel_fp8_pair.cuh -- block-scaled 8-bit product on CTA pairs for sm_103a (instantiated for the
+// forms of the output in kernel_fp8_pair_{plain,add,any}.cu).
 //
 //     D = alpha * sum_g sA(i, g) sB(g, j) P_g(i, j) + beta * C,   P_g = sum over 128 k of code products
 //
@@ -17,6 +18,8 @@
 // and write D.  Persistent clusters take tiles round robin in an order that keeps 8 rows of tiles
 // together (their A and B panels stay in L2); tile_n is chosen by the caller so that the last round
 // of tiles is nearly full.
+#pragma once
+
 #include <type_traits>
 
 #include "fp8_gemm.cuh"
@@ -69,7 +72,7 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
 // TN: the tile's columns.  COLS: B has one scale per column (weight gradients), else one per 128
 // columns.  Both are template arguments because the fold runs once per group in 16 warps: with the
 // tile's width at run time its branches made it 2.5 times as long.
-template <int TN, bool COLS>
+template <int TN, bool COLS, int OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
                     const __grid_constant__ Fp8PairParams p) {
@@ -336,23 +339,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         }
       }
       // This thread holds columns c0 .. c0 + cols - 1 of its row: 32 rows x 16 columns at a time go
-      // through shared memory, so that 4 lanes write 64 (or, in BF16, 32) consecutive bytes.
+      // through shared memory, so that neighbouring lanes write neighbouring columns.
       if (ok) {
         float4* mine = reinterpret_cast<float4*>(out + lane * kOutPitch);
-        const int at = 4 * (lane & 3);
-        const int row0 = tm * BM + BMC * (int)rank + 32 * q + (lane >> 2);
 #pragma unroll
         for (int ch = 0; ch < (cols + 15) / 16; ++ch) {
-          {
-            __syncwarp();
+          __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 4 && 16 * ch + 4 * e < cols; ++e)
-              mine[e] = make_float4(sum[8 * ch + 2 * e].x, sum[8 * ch + 2 * e].y, sum[8 * ch + 2 * e + 1].x,
-                                    sum[8 * ch + 2 * e + 1].y);
-            __syncwarp();
-            const int col = c0 + 16 * ch + at;
-            if (16 * ch + at < cols && col < p.out.N) store_rows(p.out, row0, col, out + (lane >> 2) * kOutPitch + at, kOutPitch);
-          }
+          for (int e = 0; e < 4 && 16 * ch + 4 * e < cols; ++e)
+            mine[e] = make_float4(sum[8 * ch + 2 * e].x, sum[8 * ch + 2 * e].y, sum[8 * ch + 2 * e + 1].x,
+                                  sum[8 * ch + 2 * e + 1].y);
+          __syncwarp();
+          store_piece<OUT>(p.out, tm * BM + BMC * (int)rank + 32 * q, c0 + 16 * ch, cols - 16 * ch < 16 ? cols - 16 * ch : 16,
+                      out, kOutPitch);
         }
       }
 #pragma unroll
@@ -376,28 +375,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }  // namespace
 }  // namespace f8
 
-int64_t fp8_pair_smem(bool cols) { return cols ? f8::ScaleCfg<true>::kSmem : f8::ScaleCfg<false>::kSmem; }
-
+namespace f8 {
 namespace {
 // f(kernel, its dynamic shared memory) for the kernel of a tile width and scale form.
-template <typename F>
+template <int OUT, typename F>
 cudaError_t with_pair_kernel(int tile_n, bool cols, const F& f) {
-  constexpr size_t kBlocks = f8::ScaleCfg<false>::kSmem, kCols = f8::ScaleCfg<true>::kSmem;
+  constexpr size_t kBlocks = ScaleCfg<false>::kSmem, kCols = ScaleCfg<true>::kSmem;
   switch (tile_n) {
-    case 256: return cols ? f(f8::fp8_pair_kernel<256, true>, kCols) : f(f8::fp8_pair_kernel<256, false>, kBlocks);
-    case 224: return cols ? f(f8::fp8_pair_kernel<224, true>, kCols) : f(f8::fp8_pair_kernel<224, false>, kBlocks);
-    case 192: return cols ? f(f8::fp8_pair_kernel<192, true>, kCols) : f(f8::fp8_pair_kernel<192, false>, kBlocks);
-    case 128: return cols ? f(f8::fp8_pair_kernel<128, true>, kCols) : f(f8::fp8_pair_kernel<128, false>, kBlocks);
-    case 64: return cols ? f(f8::fp8_pair_kernel<64, true>, kCols) : f(f8::fp8_pair_kernel<64, false>, kBlocks);
+    case 256: return cols ? f(fp8_pair_kernel<256, true, OUT>, kCols) : f(fp8_pair_kernel<256, false, OUT>, kBlocks);
+    case 224: return cols ? f(fp8_pair_kernel<224, true, OUT>, kCols) : f(fp8_pair_kernel<224, false, OUT>, kBlocks);
+    case 192: return cols ? f(fp8_pair_kernel<192, true, OUT>, kCols) : f(fp8_pair_kernel<192, false, OUT>, kBlocks);
+    case 128: return cols ? f(fp8_pair_kernel<128, true, OUT>, kCols) : f(fp8_pair_kernel<128, false, OUT>, kBlocks);
+    case 64: return cols ? f(fp8_pair_kernel<64, true, OUT>, kCols) : f(fp8_pair_kernel<64, false, OUT>, kBlocks);
   }
   return cudaErrorInvalidValue;
 }
-}  // namespace
 
-cudaError_t prepare_fp8_pair() {
+template <int OUT>
+cudaError_t prepare_pair() {
   for (int tile_n : kFp8PairTiles)
     for (int cols = 0; cols < 2; ++cols) {
-      const cudaError_t e = with_pair_kernel(tile_n, cols != 0, [](auto kernel, size_t smem) {
+      const cudaError_t e = with_pair_kernel<OUT>(tile_n, cols != 0, [](auto kernel, size_t smem) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
       });
       if (e != cudaSuccess) return e;
@@ -405,12 +403,22 @@ cudaError_t prepare_fp8_pair() {
   return cudaSuccess;
 }
 
-cudaError_t launch_fp8_pair(int tile_n, const CUtensorMap& mapA, const CUtensorMap& mapB, const Fp8PairParams& p,
-                            cudaStream_t stream) {
-  return with_pair_kernel(tile_n, p.sb.shift == 0, [&](auto kernel, size_t smem) {
-    kernel<<<2u * (unsigned)p.clusters, f8::kThreads, smem, stream>>>(mapA, mapB, p);
+template <int OUT>
+cudaError_t launch_pair(int tile_n, const CUtensorMap& mapA, const CUtensorMap& mapB, const Fp8PairParams& p,
+                        cudaStream_t stream) {
+  return with_pair_kernel<OUT>(tile_n, p.sb.shift == 0, [&](auto kernel, size_t smem) {
+    kernel<<<2u * (unsigned)p.clusters, kThreads, smem, stream>>>(mapA, mapB, p);
     return cudaGetLastError();
   });
 }
+}  // namespace
+}  // namespace f8
+
+#define SGEMM_DEFINE_FP8_PAIR(name, OUT)                                                                       \
+  cudaError_t prepare_fp8_pair_##name() { return f8::prepare_pair<OUT>(); }                                    \
+  cudaError_t launch_fp8_pair_##name(int tile_n, const CUtensorMap& mapA, const CUtensorMap& mapB,             \
+                                     const Fp8PairParams& p, cudaStream_t stream) {                            \
+    return f8::launch_pair<OUT>(tile_n, mapA, mapB, p, stream);                                                \
+  }
 
 }  // namespace sgemm_impl

@@ -19,107 +19,148 @@ constexpr int kTile = 128;
 constexpr int kQuantThreads = 256;
 enum Groups { kRow = 0, kCol = 1, kBlock = 2 };
 
-template <typename T, int G>
-__global__ void __launch_bounds__(kQuantThreads) quantize_kernel(const QuantParams p, int col_tiles) {
-  constexpr int V = Chunk<T>::V;
-  constexpr int kLanesPerRow = kTile / V;                      // 32 (FP32) or 16 (BF16)
-  constexpr int kRowsPerPass = kQuantThreads / kLanesPerRow;   // 8 or 16
-  constexpr int kPasses = kTile / kRowsPerPass;
-  __shared__ float part[G == kRow ? 1 : kRowsPerPass][G == kRow ? 1 : kTile];
+template <typename T>
+constexpr int kCtas = sizeof(T) == 2 ? 3 : 2;  // per SM: about 100 KB of loads in flight
 
-  const int64_t rt = (int64_t)blockIdx.x / col_tiles;
-  const int ct = (int)(blockIdx.x - rt * col_tiles);
-  const int lr = (int)threadIdx.x / kLanesPerRow, lc = (int)threadIdx.x % kLanesPerRow;
-  const int64_t row0 = rt * kTile + lr, col = (int64_t)ct * kTile + lc * V;
-  const int64_t left = p.cols - col;  // elements of this thread's chunk that exist (may be <= 0 or > V)
-  const T* x = static_cast<const T*>(p.x) + row0 * p.ldx + col;
-  const bool e5m2 = p.format == SGEMM_FP8_E5M2;
-  const float top = e5m2 ? kMaxE5M2 : kMaxE4M3;
+// What the threads of a CTA share of a tile: its place, and (128 x 1, 128 x 128) the partial maxima.
+// VEC: rows of X start at multiples of 16 bytes and hold whole chunks of V elements; otherwise
+// elements are loaded one by one.
+template <typename T, int G, bool VEC>
+struct Quant {
+  static constexpr int V = Chunk<T>::V;
+  static constexpr int kLanesPerRow = kTile / V;                     // 32 (FP32) or 16 (BF16)
+  static constexpr int kRowsPerPass = kQuantThreads / kLanesPerRow;  // 8 or 16
+  static constexpr int kPasses = kTile / kRowsPerPass;
 
-  Chunk<T> c[kPasses];
+  // Scales and codes of the tile.  CHECK = false: an infinite x is not expected; returns true when a
+  // group of this thread's has one (that group is then to be done again with CHECK).
+  template <bool CHECK>
+  static __device__ __forceinline__ bool tile(const QuantParams& p, int64_t rt, int ct, float (*part)[kTile]) {
+    const int lr = (int)threadIdx.x / kLanesPerRow, lc = (int)threadIdx.x % kLanesPerRow;
+    const int rows = (int)min((int64_t)kTile, p.rows - rt * kTile) - lr;  // of the tile, from this thread's first
+    const int64_t col = (int64_t)ct * kTile + lc * V;
+    const int left = (int)max((int64_t)0, min((int64_t)V, p.cols - col));  // elements of its chunks
+    const bool e5m2 = p.format == SGEMM_FP8_E5M2;
+    const float top = e5m2 ? kMaxE5M2 : kMaxE4M3;
+    const auto mag = [](float x) { return CHECK ? finite_abs(x) : fabsf(x); };  // fmaxf passes over a NaN
+    Chunk<T> c[kPasses];
+    {
+      const T* x = static_cast<const T*>(p.x) + (rt * kTile + lr) * p.ldx + col;
 #pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const bool in = row0 + i * kRowsPerPass < p.rows;
-    c[i] = load_chunk(x + (int64_t)i * kRowsPerPass * p.ldx, in ? left : 0, p.vec != 0);
-  }
-
-  float scale[V];  // of the thread's columns (128 x 1) or of everything (128 x 128: the first)
-  if (G != kRow) {
-    float m[V];
+      for (int i = 0; i < kPasses; ++i, x += kRowsPerPass * p.ldx) {
+        c[i].raw = make_uint4(0u, 0u, 0u, 0u);
+        if (i * kRowsPerPass < rows && left > 0) {
+          if (VEC) {
+            c[i].raw = *reinterpret_cast<const uint4*>(x);
+          } else {
+            float v[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) m[e] = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      float v[V];
-      c[i].get(v);
-#pragma unroll
-      for (int e = 0; e < V; ++e) m[e] = fmaxf(m[e], finite_abs(v[e]));
-    }
-#pragma unroll
-    for (int e = 0; e < V; ++e) part[lr][lc * V + e] = m[e];
-    __syncthreads();
-    if (threadIdx.x < kTile) {
-      float a = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kRowsPerPass; ++i) a = fmaxf(a, part[i][threadIdx.x]);
-      if (G == kBlock) a = lanes_max<32>(a);
-      part[0][threadIdx.x] = a;
-    }
-    __syncthreads();
-    if (G == kCol) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) scale[e] = group_scale(part[0][lc * V + e], top);
-      if (lr == 0)
-#pragma unroll
-        for (int e = 0; e < V; ++e)
-          if (e < left) p.s[rt * p.lds + col + e] = scale[e];
-    } else {
-      scale[0] = group_scale(fmaxf(fmaxf(part[0][0], part[0][32]), fmaxf(part[0][64], part[0][96])), top);
-      if (threadIdx.x == 0) p.s[rt * p.lds + ct] = scale[0];
-    }
-  }
-
-  float inv[V];
-  if (G == kCol) {
-#pragma unroll
-    for (int e = 0; e < V; ++e) inv[e] = __frcp_rn(scale[e]);
-  } else if (G == kBlock) {
-    inv[0] = __frcp_rn(scale[0]);
-  }
-#pragma unroll
-  for (int i = 0; i < kPasses; ++i) {
-    const int64_t row = row0 + i * kRowsPerPass;
-    float v[V];
-    c[i].get(v);
-    if (G == kRow) {
-      float m = 0.0f;
-#pragma unroll
-      for (int e = 0; e < V; ++e) m = fmaxf(m, finite_abs(v[e]));
-      const float s = group_scale(lanes_max<kLanesPerRow>(m), top);
-      inv[0] = __frcp_rn(s);
-      if (lc == 0 && row < p.rows) p.s[row * p.lds + ct] = s;
-    }
-    if (row < p.rows) {
-      uint8_t* q = p.q + row * p.ldq + col;
-      if (G == kCol) {
-        float t[V];
-#pragma unroll
-        for (int e = 0; e < V; ++e) t[e] = v[e] * inv[e];
-        store_codes<V>(q, t, 1.0f, left, p.vec != 0, e5m2);
-      } else {
-        store_codes<V>(q, v, inv[0], left, p.vec != 0, e5m2);
+            for (int e = 0; e < V; ++e) v[e] = e < left ? to_float(x[e]) : 0.0f;
+            c[i].put(v);
+          }
+        }
       }
     }
+    bool again = false;
+    float inv[G == kCol ? V : 1];
+    if (G != kRow) {
+      float m[G == kCol ? V : 1];
+#pragma unroll
+      for (int e = 0; e < (G == kCol ? V : 1); ++e) m[e] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i) {
+        float v[V];
+        c[i].get(v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          float& x = m[G == kCol ? e : 0];
+          x = fmaxf(x, mag(v[e]));
+        }
+      }
+      if (G == kBlock) {
+        const float w = lanes_max<32>(m[0]);
+        if ((threadIdx.x & 31) == 0) part[0][threadIdx.x >> 5] = w;
+        __syncthreads();
+        float a = part[0][0];
+#pragma unroll
+        for (int i = 1; i < kQuantThreads / 32; ++i) a = fmaxf(a, part[0][i]);
+        again = !CHECK && a > kMaxFloat;
+        const float s = group_scale(a, top);
+        if (threadIdx.x == 0) p.s[rt * p.lds + ct] = s;
+        inv[0] = __frcp_rn(s);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) part[lr][lc * V + e] = m[G == kCol ? e : 0];
+        __syncthreads();
+        if (threadIdx.x < kTile) {
+          float a = 0.0f;
+#pragma unroll
+          for (int i = 0; i < kRowsPerPass; ++i) a = fmaxf(a, part[i][threadIdx.x]);
+          const float s = group_scale(a, top);
+          part[0][threadIdx.x] = s;
+          const int64_t at = (int64_t)ct * kTile + threadIdx.x;
+          if (at < p.cols) p.s[rt * p.lds + at] = s;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < (G == kCol ? V : 1); ++e) {
+          const float s = part[0][lc * V + e];
+          again = again || (!CHECK && s > kMaxFloat);
+          inv[e] = __frcp_rn(s);
+        }
+      }
+    }
+    uint8_t* q = p.q + (rt * kTile + lr) * p.ldq + col;
+#pragma unroll
+    for (int i = 0; i < kPasses; ++i, q += kRowsPerPass * p.ldq) {
+      const bool in = i * kRowsPerPass < rows;
+      float v[V];
+      c[i].get(v);
+      if (G == kRow) {
+        float m = 0.0f;
+#pragma unroll
+        for (int e = 0; e < V; ++e) m = fmaxf(m, mag(v[e]));
+        m = lanes_max<kLanesPerRow>(m);
+        again = again || (!CHECK && m > kMaxFloat);
+        const float s = group_scale(m, top);
+        inv[0] = __frcp_rn(s);
+        if (lc == 0 && in) p.s[(rt * kTile + lr + i * kRowsPerPass) * p.lds + ct] = s;
+      }
+      if (in) {
+        float f[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) f[e] = inv[G == kCol ? e : 0];
+        store_codes<V, CHECK>(q, v, f, left, p.q_vec != 0, e5m2);
+      }
+    }
+    return again;
   }
+
+  static __device__ __noinline__ void checked_tile(const QuantParams& p, int64_t rt, int ct, float (*part)[kTile]) {
+    tile<true>(p, rt, ct, part);
+  }
+};
+
+template <typename T, int G, bool VEC>
+__global__ void __launch_bounds__(kQuantThreads, kCtas<T>) quantize_kernel(const __grid_constant__ QuantParams p,
+                                                                           int col_tiles) {
+  using Q = Quant<T, G, VEC>;
+  __shared__ float part[G == kCol ? Q::kRowsPerPass : 1][kTile];
+  const int64_t rt = (int64_t)blockIdx.x / col_tiles;
+  const int ct = (int)(blockIdx.x - rt * col_tiles);
+  // the tests for infinities cost as much as everything else here: a tile that has one is done again
+  if (__syncthreads_or(Q::template tile<false>(p, rt, ct, part))) Q::checked_tile(p, rt, ct, part);
 }
 
 template <typename T>
 cudaError_t launch(int block_rows, int block_cols, const QuantParams& p, cudaStream_t stream) {
   const int64_t ct = (p.cols + kTile - 1) / kTile, rt = (p.rows + kTile - 1) / kTile;
   const dim3 grid((unsigned)(ct * rt));
-  if (block_rows == 1) quantize_kernel<T, kRow><<<grid, kQuantThreads, 0, stream>>>(p, (int)ct);
-  else if (block_cols == 1) quantize_kernel<T, kCol><<<grid, kQuantThreads, 0, stream>>>(p, (int)ct);
-  else quantize_kernel<T, kBlock><<<grid, kQuantThreads, 0, stream>>>(p, (int)ct);
+  const auto run = [&](auto kernel) { kernel<<<grid, kQuantThreads, 0, stream>>>(p, (int)ct); };
+  const bool vec = p.x_vec && p.cols % Chunk<T>::V == 0;
+  if (block_rows == 1) vec ? run(quantize_kernel<T, kRow, true>) : run(quantize_kernel<T, kRow, false>);
+  else if (block_cols == 1) vec ? run(quantize_kernel<T, kCol, true>) : run(quantize_kernel<T, kCol, false>);
+  else vec ? run(quantize_kernel<T, kBlock, true>) : run(quantize_kernel<T, kBlock, false>);
   return cudaGetLastError();
 }
 

@@ -1,7 +1,7 @@
 // kernel_fp8_short.cu -- block-scaled 8-bit product with a short side, for sm_103a; and the small
 // passes around the products (aligned copies of codes, D = beta * C).
 //
-// The same sum as kernel_fp8_pair.cu for products whose time is that of reading the long operand
+// The same sum as kernel_fp8_pair.cuh for products whose time is that of reading the long operand
 // (the weights of a decoding step).  The long side runs along the 128 rows of the tensor core, the
 // short one along its columns (tile_s <= 128, a multiple of 16), so a row of one token costs a
 // 128 x 16 tile and not a 256-row one; when the short side is M the tile is D transposed and is
