@@ -153,12 +153,12 @@ __device__ __forceinline__ void store_one(const Fp8Out& o, int64_t row, int64_t 
   else        static_cast<float*>(o.D)[i] = x;
 }
 
-// A 32-row x 16-column piece of D from its sums in shared memory (`piece`, `pitch` words from row to
-// row), by one warp; its first row and column, of which `cols` are the tile's.  With aligned rows four
-// lanes hold 16 consecutive columns (64 bytes of FP32, 32 of BF16) of 8 rows at a time, otherwise 16
-// lanes hold one element each of 2 rows; what C holds is loaded for several rows before any is used.
-// OUT: which of these D and C need, known where the kernel is chosen (the caller holds 64 sums in
-// registers meanwhile: all cases in one kernel spilled them, and cost 9% at 8192^3).
+// A 32-row x 32-column piece of D from its sums in shared memory (`piece`, `pitch` words from row to
+// row), by one warp; its first row and column, of which `cols` are the tile's.  With aligned rows
+// eight lanes hold 32 consecutive columns (128 bytes of FP32, 64 of BF16) of 4 rows at a time,
+// otherwise a row is written by lanes with one element each; what C holds is loaded for several rows
+// before any is used.  OUT: which of these D and C need, known where the kernel is chosen (the caller
+// holds 128 sums in registers meanwhile).
 enum Output {
   kOutPlain = 0,  // beta == 0, aligned rows
   kOutAdd = 1,    // beta != 0, aligned rows
@@ -167,86 +167,67 @@ enum Output {
 template <int OUT>
 __device__ __forceinline__ void store_piece(const Fp8Out& o, int row0, int col0, int cols, const float* piece,
                                             int pitch) {
+  constexpr int kBatch = 4;  // rows of a lane in flight
   const int lane = threadIdx.x & 31;
   if (OUT != kOutAny && col0 + cols <= o.N) {
-    const int at = 4 * (lane & 3), row = row0 + (lane >> 2);
+    const int at = 4 * (lane & 7), row = row0 + (lane >> 3);
     if (at >= cols) return;
-    const float* v = piece + (lane >> 2) * pitch + at;
-    int64_t i = (int64_t)row * o.ldd + col0 + at;
-    if (OUT == kOutPlain) {
+    const float* v = piece + (lane >> 3) * pitch + at;
+    int64_t i = (int64_t)row * o.ldd + col0 + at, j = OUT == kOutAdd ? (int64_t)row * o.ldc + col0 + at : 0;
 #pragma unroll
-      for (int r = 0; r < 4; ++r, i += 8 * o.ldd) {
-        const float4 x = *reinterpret_cast<const float4*>(v + 8 * r * pitch);
-        if (row + 8 * r < o.M) {
+    for (int r0 = 0; r0 < 32; r0 += 4 * kBatch) {
+      float4 c[kBatch];
+      if (OUT == kOutAdd) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k, j += 4 * o.ldc) {
+          c[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+          if (row + r0 + 4 * k >= o.M) continue;
           if (o.bf16) {
-            const __nv_bfloat162 a = __floats2bfloat162_rn(o.alpha * x.x, o.alpha * x.y);
-            const __nv_bfloat162 b = __floats2bfloat162_rn(o.alpha * x.z, o.alpha * x.w);
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.D) + i) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(o.C) + j);
+            c[k] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
+                               __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
           } else {
-            *reinterpret_cast<float4*>(static_cast<float*>(o.D) + i) =
-                make_float4(o.alpha * x.x, o.alpha * x.y, o.alpha * x.z, o.alpha * x.w);
+            c[k] = *reinterpret_cast<const float4*>(static_cast<const float*>(o.C) + j);
           }
         }
       }
-    } else if (!o.bf16) {
-      int64_t j = (int64_t)row * o.ldc + col0 + at;
-#pragma unroll 1
-      for (int r = 0; r < 32; r += 16) {
-        float4 u[2];
 #pragma unroll
-        for (int k = 0; k < 2; ++k, j += 8 * o.ldc)
-          if (row + r + 8 * k < o.M) u[k] = *reinterpret_cast<const float4*>(static_cast<const float*>(o.C) + j);
-#pragma unroll
-        for (int k = 0; k < 2; ++k, i += 8 * o.ldd) {
-          const float4 x = *reinterpret_cast<const float4*>(v + (r + 8 * k) * pitch);
-          if (row + r + 8 * k < o.M)
-            *reinterpret_cast<float4*>(static_cast<float*>(o.D) + i) =
-                make_float4(fmaf(o.alpha, x.x, o.beta * u[k].x), fmaf(o.alpha, x.y, o.beta * u[k].y),
-                            fmaf(o.alpha, x.z, o.beta * u[k].z), fmaf(o.alpha, x.w, o.beta * u[k].w));
-        }
-      }
-    } else {
-      int64_t j = (int64_t)row * o.ldc + col0 + at;
-#pragma unroll 1
-      for (int r = 0; r < 32; r += 16) {
-        uint2 u[2];
-#pragma unroll
-        for (int k = 0; k < 2; ++k, j += 8 * o.ldc)
-          if (row + r + 8 * k < o.M) u[k] = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(o.C) + j);
-#pragma unroll
-        for (int k = 0; k < 2; ++k, i += 8 * o.ldd) {
-          const float4 x = *reinterpret_cast<const float4*>(v + (r + 8 * k) * pitch);
-          if (row + r + 8 * k < o.M) {
-            const __nv_bfloat162 a =
-                __floats2bfloat162_rn(fmaf(o.alpha, x.x, o.beta * __uint_as_float(u[k].x << 16)),
-                                      fmaf(o.alpha, x.y, o.beta * __uint_as_float(u[k].x & 0xFFFF0000u)));
-            const __nv_bfloat162 b =
-                __floats2bfloat162_rn(fmaf(o.alpha, x.z, o.beta * __uint_as_float(u[k].y << 16)),
-                                      fmaf(o.alpha, x.w, o.beta * __uint_as_float(u[k].y & 0xFFFF0000u)));
-            *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.D) + i) =
-                make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-          }
+      for (int k = 0; k < kBatch; ++k, i += 4 * o.ldd) {
+        float4 x = *reinterpret_cast<const float4*>(v + (r0 + 4 * k) * pitch);
+        if (row + r0 + 4 * k >= o.M) continue;
+        if (OUT == kOutAdd)
+          x = make_float4(fmaf(o.alpha, x.x, o.beta * c[k].x), fmaf(o.alpha, x.y, o.beta * c[k].y),
+                          fmaf(o.alpha, x.z, o.beta * c[k].z), fmaf(o.alpha, x.w, o.beta * c[k].w));
+        else
+          x = make_float4(o.alpha * x.x, o.alpha * x.y, o.alpha * x.z, o.alpha * x.w);
+        if (o.bf16) {
+          const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.D) + i) =
+              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        } else {
+          *reinterpret_cast<float4*>(static_cast<float*>(o.D) + i) = x;
         }
       }
     }
     return;
   }
-  const int at = lane & 15, col = col0 + at;
-  if (at >= cols || col >= o.N) return;
+  const int col = col0 + lane;
+  if (lane >= cols || col >= o.N) return;
+  const bool add = OUT != kOutPlain && o.beta != 0.0f;
 #pragma unroll 1
-  for (int r0 = lane >> 4; r0 < 32; r0 += 8) {
-    float c[4];
-    if (OUT != kOutPlain && o.beta != 0.0f)
+  for (int r0 = 0; r0 < 32; r0 += 8) {
+    float c[8];
 #pragma unroll
-      for (int r = 0; r < 4; ++r)
-        if (row0 + r0 + 2 * r < o.M) c[r] = read_c(o, (int64_t)(row0 + r0 + 2 * r) * o.ldc + col);
+    for (int k = 0; k < 8; ++k) {
+      c[k] = 0.0f;
+      if (add && row0 + r0 + k < o.M) c[k] = read_c(o, (int64_t)(row0 + r0 + k) * o.ldc + col);
+    }
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const float v = piece[(r0 + 2 * r) * pitch + at];
-      if (row0 + r0 + 2 * r >= o.M) continue;
-      const float x = OUT != kOutPlain && o.beta != 0.0f ? fmaf(o.alpha, v, o.beta * c[r]) : o.alpha * v;
-      const int64_t i = (int64_t)(row0 + r0 + 2 * r) * o.ldd + col;
+    for (int k = 0; k < 8; ++k) {
+      const float v = piece[(r0 + k) * pitch + lane];
+      if (row0 + r0 + k >= o.M) continue;
+      const float x = add ? fmaf(o.alpha, v, o.beta * c[k]) : o.alpha * v;
+      const int64_t i = (int64_t)(row0 + r0 + k) * o.ldd + col;
       if (o.bf16) static_cast<__nv_bfloat16*>(o.D)[i] = __float2bfloat16_rn(x);
       else        static_cast<float*>(o.D)[i] = x;
     }

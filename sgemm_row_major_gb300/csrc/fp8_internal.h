@@ -97,7 +97,7 @@ struct Fp8PairParams {
   uint64_t timeout_ns = 0;
   unsigned* fault = nullptr;
 };
-constexpr int kFp8PairStages = 5, kFp8PairThreads = 640;
+constexpr int kFp8PairStages = 5, kFp8PairThreads = 384;
 int64_t fp8_pair_smem(bool cols);  // dynamic shared memory; cols: B has a scale per column
 constexpr int kFp8PairTiles[] = {256, 224, 192, 128, 64};  // the tile widths there are kernels for
 // One translation unit per form of the output: beta == 0 and aligned rows, beta != 0 and aligned

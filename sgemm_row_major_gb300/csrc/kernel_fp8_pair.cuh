@@ -35,16 +35,17 @@ constexpr int kPart = 128 * BK;           // 16 KB: one operand's tile in one CT
 constexpr int kStageBytes = 2 * kPart;
 constexpr int kStages = kFp8PairStages;
 constexpr int kChunk = 8;                 // groups whose scales are loaded together
-constexpr int kOutPitch = 20;             // words between the rows of a warp's 32 x 16 piece of D (16-byte accesses
+constexpr int kOutPitch = 36;             // words between the rows of a warp's 32 x 32 piece of D (16-byte accesses
                                           // by row and by column both hit 32 banks)
 constexpr int kFirstFold = 4;             // warps 0-3: loads, products, scales of A, scales of B
-constexpr int kFoldWarps = 16;
+constexpr int kFoldWarps = 8;
 constexpr int kThreads = 32 * (kFirstFold + kFoldWarps);
 static_assert(kThreads == kFp8PairThreads, "the plan's figure");
-// 640 threads are launched with 96 registers each; the four warps that move data give most of
-// theirs to the folders: 128 x 32 + 512 x 112 = 640 x 96.
-constexpr int kMoverRegs = 32, kFoldRegs = 112;
-static_assert(128 * kMoverRegs + 32 * kFoldWarps * kFoldRegs <= kThreads * 96, "registers at launch");
+// 384 threads are launched with 168 registers each; the four warps that move data give most of
+// theirs to the folders: 128 x 40 + 256 x 232 = 384 x 168.  (16 folding warps with half the columns
+// and 112 registers each spilled in some forms and were up to a third slower there.)
+constexpr int kMoverRegs = 40, kFoldRegs = 232;
+static_assert(128 * kMoverRegs + 32 * kFoldWarps * kFoldRegs <= kThreads * 168, "registers at launch");
 constexpr int kMaxBufs = 4;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kLoadCols = 32;             // accumulator columns a folder thread loads at a time, at most
@@ -246,8 +247,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     more_registers<kFoldRegs>();
     // ------------------------------------------------ folders, then D (both CTAs)
     const int q = warp & 3;                     // TMEM lane quarter this warp may access
-    const int part = (warp - kFirstFold) >> 2;  // which quarter of the tile's columns
-    constexpr int cols = TN / 4;                // a multiple of 8
+    const int part = (warp - kFirstFold) >> 2;  // which half of the tile's columns
+    constexpr int cols = TN / 2;                // a multiple of 16
     constexpr bool kOneBlock = TN == 256 || TN == 128 || TN == 64;  // a thread's columns are in one column block
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(cols * part);
     const float* scales = reinterpret_cast<const float*>(smem_raw + pad + kStages * kStageBytes);
@@ -279,23 +280,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const float* sc = scales + c * Sc::kFloats;
         const float* scb = sc + kChunk * BMC + in_chunk * Sc::kB + b_at;
         float sa = 0.0f, s0 = 0.0f, s1 = 0.0f;
-        const auto fold = [&](auto first, auto count) {  // columns first .. first + count - 1
-          constexpr int kFirst = decltype(first)::value, kCount = decltype(count)::value;
-          float v[kCount];
-          tmem_ld<kCount>(acc + (uint32_t)kFirst, v);
-          if (kFirst == 0) {  // while the accumulator is on its way
-            sa = sc[in_chunk * BMC + 32 * q + lane];
-            if (!COLS) {
-              s0 = sa * scb[0];
-              s1 = kOneBlock ? s0 : sa * scb[1];
-            }
-          }
-          tmem_wait_ld();
-          if (kFirst + kCount == cols) {  // the whole accumulator is in registers: hand it back to the issuer
-            tmem_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive_remote(smem_addr(&acc_empty[b]), 0);
-          }
+        // 32 columns at a time, the next ones on their way while these are added
+        const auto add = [&](auto first, float* v) {
+          constexpr int kFirst = decltype(first)::value, kCount = cols - kFirst < kLoadCols ? cols - kFirst : kLoadCols;
 #pragma unroll
           for (int k = 0; k < kCount; k += 8) {
             float* x = v + k;
@@ -318,11 +305,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             }
           }
         };
-        if constexpr (cols > kLoadCols) {
-          fold(std::integral_constant<int, 0>{}, std::integral_constant<int, kLoadCols>{});
-          fold(std::integral_constant<int, kLoadCols>{}, std::integral_constant<int, cols - kLoadCols>{});
-        } else {
-          fold(std::integral_constant<int, 0>{}, std::integral_constant<int, cols>{});
+        const auto load = [&](auto first, float* v) {
+          constexpr int kFirst = decltype(first)::value, kCount = cols - kFirst < kLoadCols ? cols - kFirst : kLoadCols;
+          tmem_ld<kCount>(acc + (uint32_t)kFirst, v);
+        };
+        const auto release = [&] {  // the whole accumulator is in registers: hand it back to the issuer
+          tmem_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(smem_addr(&acc_empty[b]), 0);
+        };
+        constexpr std::integral_constant<int, 0> c_0{};
+        constexpr std::integral_constant<int, kLoadCols> c_1{};
+        constexpr std::integral_constant<int, 2 * kLoadCols> c_2{};
+        constexpr std::integral_constant<int, 3 * kLoadCols> c_3{};
+        float va[kLoadCols], vb[kLoadCols];
+        load(c_0, va);
+        sa = sc[in_chunk * BMC + 32 * q + lane];
+        if (!COLS) {
+          s0 = sa * scb[0];
+          s1 = kOneBlock ? s0 : sa * scb[1];
+        }
+        tmem_wait_ld();
+        if constexpr (cols > c_1) load(c_1, vb);
+        else release();
+        add(c_0, va);
+        if constexpr (cols > c_1) {
+          tmem_wait_ld();
+          if constexpr (cols > c_2) load(c_2, va);
+          else release();
+          add(c_1, vb);
+        }
+        if constexpr (cols > c_2) {
+          tmem_wait_ld();
+          if constexpr (cols > c_3) load(c_3, vb);
+          else release();
+          add(c_2, va);
+        }
+        if constexpr (cols > c_3) {
+          tmem_wait_ld();
+          release();
+          add(c_3, vb);
         }
         if (in_chunk == kChunk - 1 || g == groups - 1) {
           __syncwarp();
@@ -338,20 +360,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++s_lap;
         }
       }
-      // This thread holds columns c0 .. c0 + cols - 1 of its row: 32 rows x 16 columns at a time go
+      // This thread holds columns c0 .. c0 + cols - 1 of its row: 32 rows x 32 columns at a time go
       // through shared memory, so that neighbouring lanes write neighbouring columns.
       if (ok) {
         float4* mine = reinterpret_cast<float4*>(out + lane * kOutPitch);
 #pragma unroll
-        for (int ch = 0; ch < (cols + 15) / 16; ++ch) {
+        for (int at = 0; at < cols; at += 32) {
+          constexpr int kPiece = 32;
+          const int n = cols - at < kPiece ? cols - at : kPiece;
           __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 4 && 16 * ch + 4 * e < cols; ++e)
-            mine[e] = make_float4(sum[8 * ch + 2 * e].x, sum[8 * ch + 2 * e].y, sum[8 * ch + 2 * e + 1].x,
-                                  sum[8 * ch + 2 * e + 1].y);
+          for (int e = 0; e < n / 4; ++e)
+            mine[e] = make_float4(sum[at / 2 + 2 * e].x, sum[at / 2 + 2 * e].y, sum[at / 2 + 2 * e + 1].x,
+                                  sum[at / 2 + 2 * e + 1].y);
           __syncwarp();
-          store_piece<OUT>(p.out, tm * BM + BMC * (int)rank + 32 * q, c0 + 16 * ch, cols - 16 * ch < 16 ? cols - 16 * ch : 16,
-                      out, kOutPitch);
+          store_piece<OUT>(p.out, tm * BM + BMC * (int)rank + 32 * q, c0 + at, n, out, kOutPitch);
         }
       }
 #pragma unroll
