@@ -15,16 +15,16 @@ namespace f8 {
 //   MN-major: k-rows of 128 output rows each, one k per 128 bytes.
 // Both have 8-row atoms 1024 bytes apart; a tensor-core step of 32 k starts 32 bytes further along a
 // K-major row, 32 rows (4096 bytes) further down an MN-major tile.
-__device__ __forceinline__ uint64_t tile_desc(uint32_t smem_byte_addr) {
-  uint64_t d = 0;
-  d |= (uint64_t)((smem_byte_addr & 0x3FFFFu) >> 4);
-  d |= (uint64_t)(1024u >> 4) << 16;  // leading offset: next 128 output rows of an MN-major tile (never reached)
-  d |= (uint64_t)(1024u >> 4) << 32;  // stride offset: next 8 rows of the tile
-  d |= (uint64_t)1 << 46;             // descriptor version for tcgen05
-  d |= (uint64_t)2 << 61;             // 128-byte swizzle
-  return d;
+// Only the low word of a descriptor depends on the tile.
+constexpr uint32_t kDescHi = (1024u >> 4)    // stride offset: next 8 rows of the tile
+                             | (1u << 14)    // descriptor version for tcgen05
+                             | (2u << 29);   // 128-byte swizzle
+__device__ __forceinline__ uint32_t desc_lo(uint32_t smem_byte_addr) {
+  return ((smem_byte_addr & 0x3FFFFu) >> 4) |
+         ((1024u >> 4) << 16);  // leading offset: next 128 output rows of an MN-major tile (never reached)
 }
-__device__ __forceinline__ uint64_t step_of(int mn_major) { return mn_major ? (4096u >> 4) : (32u >> 4); }
+__device__ __forceinline__ uint64_t make_desc(uint32_t lo) { return ((uint64_t)kDescHi << 32) | lo; }
+__device__ __forceinline__ uint32_t step_of(int mn_major) { return mn_major ? (4096u >> 4) : (32u >> 4); }
 
 __device__ __forceinline__ void mma_f8_pair(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
                                             uint32_t accumulate) {

@@ -296,10 +296,11 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
       tmem_fence_after_sync();
       if (elect_one()) {
         const uint32_t a = sbase + (uint32_t)(s * stage_bytes);
-        const uint64_t wd = tile_desc(a), xd = tile_desc(a + kWTile);
+        const uint32_t wd = desc_lo(a), xd = desc_lo(a + kWTile);
 #pragma unroll
         for (int ks = 0; ks < BK / 32; ++ks)
-          mma_f8(tmem + (uint32_t)b * 64u, wd + (uint64_t)ks * step_of(0), xd + (uint64_t)ks * step_of(0), idesc,
+          mma_f8(tmem + (uint32_t)b * 64u, make_desc(wd + (uint32_t)ks * step_of(0)),
+                 make_desc(xd + (uint32_t)ks * step_of(0)), idesc,
                  ks == 0 ? 0u : 1u);
         mma_commit(smem_addr(&empty[s]));
         mma_commit(smem_addr(&acc_full[b]));
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
       bool ok = poll_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns);
       const uint32_t idesc = moe_idesc(32 * ((slots_of((u0 + t) / groups) + 15) / 16));
       const uint32_t at = sbase + (uint32_t)(s * stage_bytes);
-      const uint64_t wd = tile_desc(at), hd = tile_desc(at + kWTile);
+      const uint32_t wd = desc_lo(at), hd = desc_lo(at + kWTile);
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
         ok = ok && (t == 0 || poll_wait(smem_addr(&acc_empty[b]), (uint32_t)(t - 1) & 1u, p.timeout_ns));
@@ -505,8 +506,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
         if (elect_one()) {
 #pragma unroll
           for (int ks = 0; ks < 2; ++ks)
-            mma_f8(tmem + (uint32_t)(128 * b), wd + (uint64_t)(2 * b + ks) * step_of(0),
-                   hd + (uint64_t)(2 * b + ks) * step_of(0), idesc, ks == 0 ? 0u : 1u);
+            mma_f8(tmem + (uint32_t)(128 * b), make_desc(wd + (uint32_t)(2 * b + ks) * step_of(0)),
+                   make_desc(hd + (uint32_t)(2 * b + ks) * step_of(0)), idesc, ks == 0 ? 0u : 1u);
           mma_commit(smem_addr(&acc_full[b]));
           if (b == 1) mma_commit(smem_addr(&empty[s]));
         }

@@ -168,26 +168,25 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         t = units;
       } else {
         // ---------------------------------------------- products (even CTA)
-        const uint64_t astep = step_of(p.a_mn), bstep = step_of(p.b_mn);
+        const uint32_t astep = step_of(p.a_mn), bstep = step_of(p.b_mn);
+        const uint32_t desc0 = desc_lo(sbase);
         int s = 0, b = 0;
         uint32_t s_lap = 0, b_lap = 0;
-        for (; t < units; ++t) {
-          if (!((b_lap == 0 || poll_wait(smem_addr(&acc_empty[b]), (b_lap - 1) & 1u, p.timeout_ns)) &&
-                poll_wait(smem_addr(&full[s]), s_lap & 1u, p.timeout_ns))) {
-            if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
-            break;
-          }
+        bool ok = poll_wait(smem_addr(&full[0]), 0u, p.timeout_ns);
+        while (ok && t < units) {
+          ok = b_lap == 0 || poll_wait(smem_addr(&acc_empty[b]), (b_lap - 1) & 1u, p.timeout_ns);
+          if (!ok) break;
           tmem_fence_after_sync();
           if (elect_one()) {
             const uint32_t acc = tmem + (uint32_t)(b * TN);
-            const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
-            const uint64_t ad = tile_desc(a), bd = tile_desc(a + kPart);
+            const uint32_t ad = desc0 + (uint32_t)(s * (kStageBytes >> 4)), bd = ad + (kPart >> 4);
 #pragma unroll
-            for (int ks = 0; ks < BK / 32; ++ks)
-              mma_f8_pair(acc, ad + (uint64_t)ks * astep, bd + (uint64_t)ks * bstep, p.idesc, ks == 0 ? 0u : 1u);
+            for (uint32_t ks = 0; ks < BK / 32; ++ks)
+              mma_f8_pair(acc, make_desc(ad + ks * astep), make_desc(bd + ks * bstep), p.idesc, ks == 0 ? 0u : 1u);
             mma_commit_pair(smem_addr(&done[s]));  // in both CTAs: stage s is free, the accumulator holds group t
           }
           __syncwarp();
+          ++t;
           if (++b == bufs) {
             b = 0;
             ++b_lap;
@@ -196,7 +195,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             s = 0;
             ++s_lap;
           }
+          // the next group's operands, while this one's products run
+          if (t < units) ok = poll_wait(smem_addr(&full[s]), s_lap & 1u, p.timeout_ns);
         }
+        if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
       }
       // leave only when every product has completed and its commits have landed in this CTA
       for (int u = t > kStages ? t - kStages : 0; u < t; ++u)

@@ -111,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_short_kernel(const __grid_con
         atomicOr(p.fault, (unsigned)kFaultDrainWait);
   } else if (warp == 1) {
     // ------------------------------------------------ products
-    const uint64_t lstep = step_of(p.l_mn), sstep = step_of(p.s_mn);
+    const uint32_t lstep = step_of(p.l_mn), sstep = step_of(p.s_mn);
     int t = 0, s = 0;
     uint32_t lap = 0;
     for (; t < units; ++t) {
@@ -124,10 +124,11 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_short_kernel(const __grid_con
       tmem_fence_after_sync();
       if (elect_one()) {
         const uint32_t a = sbase + (uint32_t)(s * p.stage_bytes);
-        const uint64_t ld = tile_desc(a), sd = tile_desc(a + BL * BK);
+        const uint32_t ld = desc_lo(a), sd = desc_lo(a + BL * BK);
 #pragma unroll
         for (int ks = 0; ks < BK / 32; ++ks)
-          mma_f8(tmem + (uint32_t)b * acc_step, ld + (uint64_t)ks * lstep, sd + (uint64_t)ks * sstep, p.idesc,
+          mma_f8(tmem + (uint32_t)b * acc_step, make_desc(ld + (uint32_t)ks * lstep),
+                 make_desc(sd + (uint32_t)ks * sstep), p.idesc,
                  ks == 0 ? 0u : 1u);
         mma_commit(smem_addr(&empty[s]));
         mma_commit(smem_addr(&acc_full[b]));
