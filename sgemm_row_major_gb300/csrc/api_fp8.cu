@@ -228,8 +228,11 @@ cudaError_t launch_product(const Product& pr, const sgemm_plan_t& plan, const Ca
     p.clusters = (int)(plan.grid_x / 2);
     p.timeout_ns = wait_timeout_ns();
     p.fault = dev.fault;
-    return (!p.out.vec ? launch_fp8_pair_any : p.out.beta != 0.0f ? launch_fp8_pair_add : launch_fp8_pair_plain)(
-        plan.tile_n, ma, mb, p, stream);
+    if (!p.out.vec) return launch_fp8_pair_any(plan.tile_n, ma, mb, ma, p, stream);  // (D's map is not read)
+    if (p.out.beta != 0.0f) return launch_fp8_pair_add(plan.tile_n, ma, mb, ma, p, stream);
+    CUtensorMap md;
+    e = encode_out_map(p.out.D, pr.N, pr.M, p.out.ldd, p.out.bf16 != 0, &md);
+    return e == cudaSuccess ? launch_fp8_pair_plain(plan.tile_n, ma, mb, md, p, stream) : e;
   }
   const bool trans = pr.M <= pr.N;
   const Operand &l = trans ? pr.b : pr.a, &s = trans ? pr.a : pr.b;

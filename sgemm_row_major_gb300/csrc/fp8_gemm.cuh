@@ -2,6 +2,8 @@
 // kernel_fp8_short.cu): tile descriptors, the tensor-core instructions, and the output's rows.
 #pragma once
 
+#include <type_traits>
+
 #include "fp8_common.cuh"
 #include "fp8_internal.h"
 #include "kernel_tc_common.cuh"
@@ -153,83 +155,92 @@ __device__ __forceinline__ void store_one(const Fp8Out& o, int64_t row, int64_t 
   else        static_cast<float*>(o.D)[i] = x;
 }
 
-// A 32-row x 32-column piece of D from its sums in shared memory (`piece`, `pitch` words from row to
-// row), by one warp; its first row and column, of which `cols` are the tile's.  With aligned rows
-// eight lanes hold 32 consecutive columns (128 bytes of FP32, 64 of BF16) of 4 rows at a time,
-// otherwise a row is written by lanes with one element each; what C holds is loaded for several rows
-// before any is used.  OUT: which of these D and C need, known where the kernel is chosen (the caller
-// holds 128 sums in registers meanwhile).
+// How the output is written, known where the kernel is chosen (the caller holds 128 sums in registers
+// meanwhile; all cases in one kernel cost 9% at 8192^3).
 enum Output {
-  kOutPlain = 0,  // beta == 0, aligned rows
+  kOutPlain = 0,  // beta == 0, aligned rows: TMA
   kOutAdd = 1,    // beta != 0, aligned rows
   kOutAny = 2     // any alignment and beta
 };
-template <int OUT>
-__device__ __forceinline__ void store_piece(const Fp8Out& o, int row0, int col0, int cols, const float* piece,
-                                            int pitch) {
-  constexpr int kBatch = 4;  // rows of a lane in flight
-  const int lane = threadIdx.x & 31;
-  if (OUT != kOutAny && col0 + cols <= o.N) {
-    const int at = 4 * (lane & 7), row = row0 + (lane >> 3);
-    if (at >= cols) return;
-    const float* v = piece + (lane >> 3) * pitch + at;
-    int64_t i = (int64_t)row * o.ldd + col0 + at, j = OUT == kOutAdd ? (int64_t)row * o.ldc + col0 + at : 0;
+
+// Rows of one lane of an aligned piece, 4 rows apart, all of them in D: no tests between the
+// accesses, so that the loads of a batch are in flight together.
+template <bool BF16>
+__device__ __forceinline__ void store_aligned_rows(const Fp8Out& o, int64_t row, int64_t col, const float* v,
+                                                   int pitch) {
+  constexpr int kBatch = 4;
+  using T = typename std::conditional<BF16, uint2, float4>::type;  // 4 elements
+  constexpr int kSize = BF16 ? 2 : 4;
+  char* d = static_cast<char*>(o.D) + (row * o.ldd + col) * kSize;
+  const char* c = static_cast<const char*>(o.C) + (row * o.ldc + col) * kSize;
+  const int64_t dstep = 4 * o.ldd * kSize, cstep = 4 * o.ldc * kSize;
 #pragma unroll
-    for (int r0 = 0; r0 < 32; r0 += 4 * kBatch) {
-      float4 c[kBatch];
-      if (OUT == kOutAdd) {
+  for (int r0 = 0; r0 < 8; r0 += kBatch) {
+    float4 x[kBatch];
+    T old[kBatch];
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k, j += 4 * o.ldc) {
-          c[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-          if (row + r0 + 4 * k >= o.M) continue;
-          if (o.bf16) {
-            const uint2 u = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(o.C) + j);
-            c[k] = make_float4(__uint_as_float(u.x << 16), __uint_as_float(u.x & 0xFFFF0000u),
-                               __uint_as_float(u.y << 16), __uint_as_float(u.y & 0xFFFF0000u));
-          } else {
-            c[k] = *reinterpret_cast<const float4*>(static_cast<const float*>(o.C) + j);
-          }
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kBatch; ++k, i += 4 * o.ldd) {
-        float4 x = *reinterpret_cast<const float4*>(v + (r0 + 4 * k) * pitch);
-        if (row + r0 + 4 * k >= o.M) continue;
-        if (OUT == kOutAdd)
-          x = make_float4(fmaf(o.alpha, x.x, o.beta * c[k].x), fmaf(o.alpha, x.y, o.beta * c[k].y),
-                          fmaf(o.alpha, x.z, o.beta * c[k].z), fmaf(o.alpha, x.w, o.beta * c[k].w));
-        else
-          x = make_float4(o.alpha * x.x, o.alpha * x.y, o.alpha * x.z, o.alpha * x.w);
-        if (o.bf16) {
-          const __nv_bfloat162 a = __floats2bfloat162_rn(x.x, x.y), b = __floats2bfloat162_rn(x.z, x.w);
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o.D) + i) =
-              make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
-        } else {
-          *reinterpret_cast<float4*>(static_cast<float*>(o.D) + i) = x;
-        }
-      }
+    for (int k = 0; k < kBatch; ++k) {
+      x[k] = *reinterpret_cast<const float4*>(v + 4 * (r0 + k) * pitch);
+      old[k] = *reinterpret_cast<const T*>(c);
+      c += cstep;
     }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      float4 u;
+      if constexpr (BF16)
+        u = make_float4(__uint_as_float(old[k].x << 16), __uint_as_float(old[k].x & 0xFFFF0000u),
+                        __uint_as_float(old[k].y << 16), __uint_as_float(old[k].y & 0xFFFF0000u));
+      else
+        u = old[k];
+      const float4 y = make_float4(fmaf(o.alpha, x[k].x, o.beta * u.x), fmaf(o.alpha, x[k].y, o.beta * u.y),
+                                   fmaf(o.alpha, x[k].z, o.beta * u.z), fmaf(o.alpha, x[k].w, o.beta * u.w));
+      if constexpr (BF16) {
+        const __nv_bfloat162 a = __floats2bfloat162_rn(y.x, y.y), b = __floats2bfloat162_rn(y.z, y.w);
+        *reinterpret_cast<T*>(d) =
+            make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+      } else {
+        *reinterpret_cast<T*>(d) = y;
+      }
+      d += dstep;
+    }
+  }
+}
+
+// A 32-row x 32-column piece of D from its sums in shared memory (`piece`, `pitch` words from row to
+// row), by one warp.  With aligned rows eight lanes hold 32 consecutive columns (128 bytes of FP32, 64
+// of BF16) of 4 rows at a time, otherwise (and at D's edges) a row is written by lanes with one element
+// each; what C holds is loaded for several rows before any is used.
+template <int OUT>
+__device__ __forceinline__ void store_piece(const Fp8Out& o, int row0, int col0, const float* piece, int pitch) {
+  const int lane = threadIdx.x & 31;
+  if (OUT == kOutAdd && col0 + 32 <= o.N && row0 + 32 <= o.M) {
+    const int at = 4 * (lane & 7), row = lane >> 3;
+    const float* v = piece + row * pitch + at;
+    if (o.bf16) store_aligned_rows<true>(o, row0 + row, col0 + at, v, pitch);
+    else        store_aligned_rows<false>(o, row0 + row, col0 + at, v, pitch);
     return;
   }
   const int col = col0 + lane;
-  if (lane >= cols || col >= o.N) return;
-  const bool add = OUT != kOutPlain && o.beta != 0.0f;
+  if (col >= o.N) return;
+  const bool add = OUT == kOutAdd || o.beta != 0.0f;
+  const int rows = min(32, o.M - row0);
 #pragma unroll 1
-  for (int r0 = 0; r0 < 32; r0 += 8) {
+  for (int r0 = 0; r0 < rows; r0 += 8) {
     float c[8];
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       c[k] = 0.0f;
-      if (add && row0 + r0 + k < o.M) c[k] = read_c(o, (int64_t)(row0 + r0 + k) * o.ldc + col);
+      if (add && r0 + k < rows) c[k] = read_c(o, (int64_t)(row0 + r0 + k) * o.ldc + col);
     }
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
       const float v = piece[(r0 + k) * pitch + lane];
-      if (row0 + r0 + k >= o.M) continue;
       const float x = add ? fmaf(o.alpha, v, o.beta * c[k]) : o.alpha * v;
       const int64_t i = (int64_t)(row0 + r0 + k) * o.ldd + col;
-      if (o.bf16) static_cast<__nv_bfloat16*>(o.D)[i] = __float2bfloat16_rn(x);
-      else        static_cast<float*>(o.D)[i] = x;
+      if (r0 + k < rows) {
+        if (o.bf16) static_cast<__nv_bfloat16*>(o.D)[i] = __float2bfloat16_rn(x);
+        else        static_cast<float*>(o.D)[i] = x;
+      }
     }
   }
 }

@@ -99,13 +99,13 @@ struct Fp8PairParams {
 };
 constexpr int kFp8PairStages = 5, kFp8PairThreads = 384;
 int64_t fp8_pair_smem(bool cols);  // dynamic shared memory; cols: B has a scale per column
-constexpr int kFp8PairTiles[] = {256, 224, 192, 128, 64};  // the tile widths there are kernels for
+constexpr int kFp8PairTiles[] = {256, 128, 64};  // the tile widths there are kernels for
 // One translation unit per form of the output: beta == 0 and aligned rows, beta != 0 and aligned
 // rows, anything.
 #define SGEMM_DECLARE_FP8_PAIR(name)                                                               \
   cudaError_t prepare_fp8_pair_##name();                                                           \
   cudaError_t launch_fp8_pair_##name(int tile_n, const CUtensorMap& mapA, const CUtensorMap& mapB, \
-                                     const Fp8PairParams& p, cudaStream_t stream);
+                                     const CUtensorMap& mapD, const Fp8PairParams& p, cudaStream_t stream);
 SGEMM_DECLARE_FP8_PAIR(plain)
 SGEMM_DECLARE_FP8_PAIR(add)
 SGEMM_DECLARE_FP8_PAIR(any)
@@ -174,7 +174,10 @@ cudaError_t launch_fp8_moe(const MoeMaps& maps, const MoeParams& p, int sm_count
 // codes x box_outer rows, 128-byte swizzle, zeros outside.
 cudaError_t encode_fp8_map(const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer,
                            CUtensorMap* map);
-// The same over `products` such matrices `stride` bytes apart (a multiple of 16).
+// Map over D (`rows` x `cols` FP32 or BF16, row stride ld elements, 16-byte aligned rows): boxes of 32 x 32,
+// swizzled by their rows' width.
+cudaError_t encode_out_map(const void* base, int64_t cols, int64_t rows, int64_t ld, bool bf16, CUtensorMap* map);
+// The same as encode_fp8_map over `products` such matrices `stride` bytes apart (a multiple of 16).
 cudaError_t encode_fp8_maps(const void* base, int64_t inner, int64_t outer, int64_t ld, int64_t products,
                             int64_t stride, int box_outer, CUtensorMap* map);
 // Rows of `cols` codes copied to rows `ldd` apart (any alignment of the source).

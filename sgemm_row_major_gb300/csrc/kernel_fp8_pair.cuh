@@ -3,7 +3,7 @@
 //
 //     D = alpha * sum_g sA(i, g) sB(g, j) P_g(i, j) + beta * C,   P_g = sum over 128 k of code products
 //
-// Clusters of two CTAs on one TPC compute 256 x tile_n tiles (tile_n 64, 128, 192, 224 or 256) with
+// Clusters of two CTAs on one TPC compute 256 x tile_n tiles (tile_n 64, 128 or 256) with
 // tcgen05.mma.cta_group::2.kind::f8f6f4, M = 256, N = tile_n, K = 32, both operands from shared
 // memory: each CTA holds 128 rows of A and half of the tile's columns of B.  Four such steps make
 // one P_g in a fresh TMEM accumulator (two of 256 columns alternate); 8 warps per CTA read it back
@@ -37,6 +37,8 @@ constexpr int kStages = kFp8PairStages;
 constexpr int kChunk = 8;                 // groups whose scales are loaded together
 constexpr int kOutPitch = 36;             // words between the rows of a warp's 32 x 32 piece of D (16-byte accesses
                                           // by row and by column both hit 32 banks)
+constexpr int kOutBytes = 5 * 1024;       // of shared memory per folding warp (pieces for TMA: 4 KB, 1024-byte aligned)
+static_assert(32 * kOutPitch * 4 <= kOutBytes, "a piece of D");
 constexpr int kFirstFold = 4;             // warps 0-3: loads, products, scales of A, scales of B
 constexpr int kFoldWarps = 8;
 constexpr int kThreads = 32 * (kFirstFold + kFoldWarps);
@@ -57,7 +59,7 @@ struct ScaleCfg {
   static constexpr int kB = COLS ? 256 : 4;
   static constexpr int kChunks = COLS ? 2 : 4;  // in shared memory
   static constexpr int kFloats = kChunk * (BMC + kB);
-  static constexpr int kSmem = kStages * kStageBytes + kChunks * kFloats * 4 + kFoldWarps * 32 * kOutPitch * 4 + 1024;
+  static constexpr int kSmem = kStages * kStageBytes + kFoldWarps * kOutBytes + kChunks * kFloats * 4 + 1024;
   static_assert(kSmem + 1024 <= 232448, "shared memory per CTA");
 };
 
@@ -70,13 +72,63 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
+// One warp's 32 rows x 2N columns of D, from a row's sums in each lane, to global memory by TMA: 32
+// columns at a time in D's type, rows of 64 (BF16) or 128 bytes with the swizzle of that width, so that
+// the lanes' 16-byte stores to shared memory hit different banks.  Two BF16 pieces or one of FP32 fit
+// in the warp's buffer; a piece is written when the copy that read its place before is done reading.
+template <bool BF16, int N>
+__device__ __forceinline__ void tma_out(const CUtensorMap& map, uint8_t* buf, const Fp8Out& o, int row0, int col0,
+                                        const float2 (&sum)[N]) {
+  const int lane = threadIdx.x & 31;
+  const float2 alpha = make_float2(o.alpha, o.alpha);
+  constexpr bool kTwo = BF16 && (N / 16) % 2 == 0;  // the two places alternate from tile to tile too
+#pragma unroll
+  for (int piece = 0; piece < N / 16; ++piece) {
+    uint8_t* at = buf + (kTwo && piece % 2 ? 2048 : 0);
+    if (lane == 0) {
+      if (kTwo) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      else      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    }
+    __syncwarp();
+#pragma unroll
+    for (int e = 0; e < (BF16 ? 4 : 8); ++e) {  // 16 bytes
+      uint4 u;
+      if constexpr (BF16) {
+        uint32_t w[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float2 x = __fmul2_rn(sum[16 * piece + 4 * e + k], alpha);
+          const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+          w[k] = *reinterpret_cast<const uint32_t*>(&b);
+        }
+        u = make_uint4(w[0], w[1], w[2], w[3]);
+      } else {
+        const float2 x = __fmul2_rn(sum[16 * piece + 2 * e], alpha), y = __fmul2_rn(sum[16 * piece + 2 * e + 1], alpha);
+        u = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+      }
+      const int chunk = BF16 ? e ^ ((lane >> 1) & 3) : e ^ (lane & 7);
+      *reinterpret_cast<uint4*>(at + lane * (BF16 ? 64 : 128) + 16 * chunk) = u;
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (row0 < o.M && col0 + 32 * piece < o.N)
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(&map)),
+                     "r"(smem_addr(at)), "r"(col0 + 32 * piece), "r"(row0), "r"(0)
+                     : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+    }
+  }
+}
+
 // TN: the tile's columns.  COLS: B has one scale per column (weight gradients), else one per 128
 // columns.  Both are template arguments because the fold runs once per group in 16 warps: with the
 // tile's width at run time its branches made it 2.5 times as long.
 template <int TN, bool COLS, int OUT>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fp8_pair_kernel(const __grid_constant__ CUtensorMap mapA, const __grid_constant__ CUtensorMap mapB,
-                    const __grid_constant__ Fp8PairParams p) {
+                    const __grid_constant__ CUtensorMap mapD, const __grid_constant__ Fp8PairParams p) {
   using Sc = ScaleCfg<COLS>;
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kStages], done[kStages];
@@ -210,7 +262,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ------------------------------------------------ scales, 8 groups at a time, up to kChunks ahead
       // of the folders (the latency of a load is several groups' time): warp 2 of this CTA's 128 rows,
       // warp 3 of the tile's columns or column blocks.
-      const uint32_t ring = sbase + (uint32_t)(kStages * kStageBytes);
+      const uint32_t ring = sbase + (uint32_t)(kStages * kStageBytes + kFoldWarps * kOutBytes);
       int c = 0;
       uint32_t lap = 0;
       bool ok = true;
@@ -251,11 +303,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const int q = warp & 3;                     // TMEM lane quarter this warp may access
     const int part = (warp - kFirstFold) >> 2;  // which half of the tile's columns
     constexpr int cols = TN / 2;                // a multiple of 16
-    constexpr bool kOneBlock = TN == 256 || TN == 128 || TN == 64;  // a thread's columns are in one column block
+    static_assert(cols <= 128 && 128 % cols == 0, "a thread's columns lie in one column block");
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(cols * part);
-    const float* scales = reinterpret_cast<const float*>(smem_raw + pad + kStages * kStageBytes);
-    float* out = reinterpret_cast<float*>(smem_raw + pad + kStages * kStageBytes + Sc::kChunks * Sc::kFloats * 4) +
-                 (warp - kFirstFold) * 32 * kOutPitch;
+    uint8_t* out = smem_raw + pad + kStages * kStageBytes + (warp - kFirstFold) * kOutBytes;
+    const float* scales = reinterpret_cast<const float*>(smem_raw + pad + kStages * kStageBytes + kFoldWarps * kOutBytes);
     float2 sum[cols / 2];
 #pragma unroll
     for (int e = 0; e < cols / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
@@ -266,8 +317,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int tm, tn;
       tile_coords(cl + i * p.clusters, p.tiles_m, p.tiles_n, tm, tn);
       const int c0 = tn * TN + cols * part;
-      const int edge = ((c0 >> 7) + 1) * 128 - c0;  // columns of this thread's in the column block of c0
-      // where its column scales (or its first block's) lie among a group's
+      // where this thread's column scales (or its column block's) lie among a group's
       const int b_at = COLS ? cols * part : (c0 >> 7) - ((tn * TN) >> 7);
       for (int g = 0; g < groups; ++g) {
         const int in_chunk = g & (kChunk - 1);
@@ -281,7 +331,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t acc = tq + (uint32_t)(b * TN);
         const float* sc = scales + c * Sc::kFloats;
         const float* scb = sc + kChunk * BMC + in_chunk * Sc::kB + b_at;
-        float sa = 0.0f, s0 = 0.0f, s1 = 0.0f;
+        float sa = 0.0f, s0 = 0.0f;
         // 32 columns at a time, the next ones on their way while these are added
         const auto add = [&](auto first, float* v) {
           constexpr int kFirst = decltype(first)::value, kCount = cols - kFirst < kLoadCols ? cols - kFirst : kLoadCols;
@@ -300,8 +350,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               m[2] = __ffma2_rn(__fmul2_rn(make_float2(x[4], x[5]), make_float2(w1.x, w1.y)), sa2, m[2]);
               m[3] = __ffma2_rn(__fmul2_rn(make_float2(x[6], x[7]), make_float2(w1.z, w1.w)), sa2, m[3]);
             } else {
-              const float w = kOneBlock || kFirst + k < edge ? s0 : s1;
-              const float2 w2 = make_float2(w, w);
+              const float2 w2 = make_float2(s0, s0);
 #pragma unroll
               for (int e = 0; e < 4; ++e) m[e] = __ffma2_rn(make_float2(x[2 * e], x[2 * e + 1]), w2, m[e]);
             }
@@ -323,10 +372,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float va[kLoadCols], vb[kLoadCols];
         load(c_0, va);
         sa = sc[in_chunk * BMC + 32 * q + lane];
-        if (!COLS) {
-          s0 = sa * scb[0];
-          s1 = kOneBlock ? s0 : sa * scb[1];
-        }
+        if (!COLS) s0 = sa * scb[0];
         tmem_wait_ld();
         if constexpr (cols > c_1) load(c_1, vb);
         else release();
@@ -362,26 +408,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++s_lap;
         }
       }
-      // This thread holds columns c0 .. c0 + cols - 1 of its row: 32 rows x 32 columns at a time go
-      // through shared memory, so that neighbouring lanes write neighbouring columns.
-      if (ok) {
-        float4* mine = reinterpret_cast<float4*>(out + lane * kOutPitch);
+      // This thread holds columns c0 .. c0 + cols - 1 of its row; 32 rows x 32 columns at a time go
+      // through shared memory.
+      const int row0 = tm * BM + BMC * (int)rank + 32 * q;
+      if (ok && OUT == kOutPlain) {
+        // in D's type and the order TMA reads, which writes the piece (as far as it is in D) by itself
+        if (p.out.bf16) tma_out<true>(mapD, out, p.out, row0, c0, sum);
+        else            tma_out<false>(mapD, out, p.out, row0, c0, sum);
+      } else if (ok) {
+        float4* mine = reinterpret_cast<float4*>(out) + lane * (kOutPitch / 4);
 #pragma unroll
         for (int at = 0; at < cols; at += 32) {
-          constexpr int kPiece = 32;
-          const int n = cols - at < kPiece ? cols - at : kPiece;
           __syncwarp();
 #pragma unroll
-          for (int e = 0; e < n / 4; ++e)
+          for (int e = 0; e < 8; ++e)
             mine[e] = make_float4(sum[at / 2 + 2 * e].x, sum[at / 2 + 2 * e].y, sum[at / 2 + 2 * e + 1].x,
                                   sum[at / 2 + 2 * e + 1].y);
           __syncwarp();
-          store_piece<OUT>(p.out, tm * BM + BMC * (int)rank + 32 * q, c0 + at, n, out, kOutPitch);
+          store_piece<OUT>(p.out, row0, c0 + at, reinterpret_cast<const float*>(out), kOutPitch);
         }
       }
 #pragma unroll
       for (int e = 0; e < cols / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
     }
+    if (OUT == kOutPlain && lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
   }
 
   tmem_fence_before_sync();
@@ -408,8 +459,6 @@ cudaError_t with_pair_kernel(int tile_n, bool cols, const F& f) {
   constexpr size_t kBlocks = ScaleCfg<false>::kSmem, kCols = ScaleCfg<true>::kSmem;
   switch (tile_n) {
     case 256: return cols ? f(fp8_pair_kernel<256, true, OUT>, kCols) : f(fp8_pair_kernel<256, false, OUT>, kBlocks);
-    case 224: return cols ? f(fp8_pair_kernel<224, true, OUT>, kCols) : f(fp8_pair_kernel<224, false, OUT>, kBlocks);
-    case 192: return cols ? f(fp8_pair_kernel<192, true, OUT>, kCols) : f(fp8_pair_kernel<192, false, OUT>, kBlocks);
     case 128: return cols ? f(fp8_pair_kernel<128, true, OUT>, kCols) : f(fp8_pair_kernel<128, false, OUT>, kBlocks);
     case 64: return cols ? f(fp8_pair_kernel<64, true, OUT>, kCols) : f(fp8_pair_kernel<64, false, OUT>, kBlocks);
   }
@@ -429,10 +478,10 @@ cudaError_t prepare_pair() {
 }
 
 template <int OUT>
-cudaError_t launch_pair(int tile_n, const CUtensorMap& mapA, const CUtensorMap& mapB, const Fp8PairParams& p,
-                        cudaStream_t stream) {
+cudaError_t launch_pair(int tile_n, const CUtensorMap& mapA, const CUtensorMap& mapB, const CUtensorMap& mapD,
+                        const Fp8PairParams& p, cudaStream_t stream) {
   return with_pair_kernel<OUT>(tile_n, p.sb.shift == 0, [&](auto kernel, size_t smem) {
-    kernel<<<2u * (unsigned)p.clusters, kThreads, smem, stream>>>(mapA, mapB, p);
+    kernel<<<2u * (unsigned)p.clusters, kThreads, smem, stream>>>(mapA, mapB, mapD, p);
     return cudaGetLastError();
   });
 }
@@ -442,8 +491,8 @@ cudaError_t launch_pair(int tile_n, const CUtensorMap& mapA, const CUtensorMap& 
 #define SGEMM_DEFINE_FP8_PAIR(name, OUT)                                                                       \
   cudaError_t prepare_fp8_pair_##name() { return f8::prepare_pair<OUT>(); }                                    \
   cudaError_t launch_fp8_pair_##name(int tile_n, const CUtensorMap& mapA, const CUtensorMap& mapB,             \
-                                     const Fp8PairParams& p, cudaStream_t stream) {                            \
-    return f8::launch_pair<OUT>(tile_n, mapA, mapB, p, stream);                                                \
+                                     const CUtensorMap& mapD, const Fp8PairParams& p, cudaStream_t stream) {   \
+    return f8::launch_pair<OUT>(tile_n, mapA, mapB, mapD, p, stream);                                          \
   }
 
 }  // namespace sgemm_impl

@@ -115,6 +115,24 @@ cudaError_t encode_fp8_map(const void* base, int64_t inner, int64_t outer, int64
   return encode_fp8_maps(base, inner, outer, ld, 1, ld, box_outer, map);  // one matrix: its stride is not used
 }
 
+cudaError_t encode_out_map(const void* base, int64_t cols, int64_t rows, int64_t ld, bool bf16, CUtensorMap* map) {
+  cudaError_t e = bind_primary_context();
+  if (e != cudaSuccess) return e;
+  EncodeTiledFn fn = nullptr;
+  e = encode_fn(&fn);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t size = bf16 ? 2 : 4;
+  const cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, 1};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * size, (cuuint64_t)ld * size};  // one matrix: the second is not used
+  const cuuint32_t box[3] = {32u, 32u, 1u};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 3,
+                  const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  bf16 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 cudaError_t encode_matrix_map(const float* base, int64_t inner, int64_t outer, int64_t ld, int box_inner,
                               int box_outer, CUtensorMap* map) {
   cudaError_t e = bind_primary_context();
