@@ -596,7 +596,7 @@ int sgemm_fp8_moe(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts
   w.base = static_cast<uint8_t*>(ws);
   place(&w);
   MoeMaps maps;
-  e = operand_map(x, (int)ceil_div(tokens, 16) * 16, &x_copy, &maps.x, stream);
+  e = operand_map(x, tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64, &x_copy, &maps.x, stream);
   if (e == cudaSuccess) e = experts_map(*gate, inner, hidden, experts, 64, &maps.gate);
   if (e == cudaSuccess) e = experts_map(*up, inner, hidden, experts, 64, &maps.up);
   if (e == cudaSuccess) e = experts_map(*down, hidden, inner, experts, 128, &maps.down);

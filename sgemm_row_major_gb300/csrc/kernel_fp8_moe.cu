@@ -18,7 +18,9 @@
 // columns) units in order; each CTA folds its units per expert in FP32 registers, adds them weighted
 // into its tokens' sums in shared memory, and the cluster adds those in rank order into Y.
 //
-// Both: warp 0 loads (TMA), warp 1 issues the products, warps 2-5 fold; two CTAs per SM.
+// Both: one CTA per SM with as many 16 KB weight tiles in flight as its shared memory holds; warp 0
+// loads (TMA), warp 1 issues the products, warp 2 loads scales a chunk of groups ahead, warps 4-7 fold
+// the accumulators (two alternate) into FP32 sums in registers.
 #include <algorithm>
 
 #include "fp8_gemm.cuh"
@@ -30,12 +32,14 @@ namespace {
 using namespace tc;
 
 constexpr int BK = 128;
-constexpr int kThreads = 192, kFoldThreads = 128;
-constexpr int kMaxStages = 8;
+constexpr int kThreads = 256, kFirstFold = 4, kFoldWarps = 4, kFoldThreads = 128;
+constexpr int kMaxStages = 10;
 constexpr int kWTile = 128 * BK;  // 16 KB of weights per stage
 constexpr int kUpCols = 64;       // inner columns of a tile of the first kernel
 constexpr float kLoScale = 16.0f;
 constexpr int kPitch = 129;
+constexpr int kChunkGroups = 8;   // groups of 128 k whose scales are loaded together
+constexpr int kChunks = 3;        // in shared memory
 
 __device__ __forceinline__ void fold_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -56,29 +60,33 @@ struct Route {
   int *expert, *base;          // [active]
 };
 
-// Bytes of dynamic shared memory the first kernel's routing takes.
-__host__ __device__ inline size_t up_route_bytes(const MoeParams& p) {
-  return (size_t)p.experts * 8 + (size_t)p.active_max * 16 + (size_t)p.tokens * p.top_k * 8;
-}
-__host__ __device__ inline size_t down_route_bytes(const MoeParams& p) {
-  return (size_t)p.active_max * 8 + (size_t)p.slots_max * 8;
-}
-__host__ __device__ inline int token_cols(const MoeParams& p) { return (p.tokens + 15) / 16 * 16; }
+// Dynamic shared memory, in this order: the ring of stages (1024-byte aligned), the scale chunks, the
+// sums (first kernel: of an item's tokens; second: of Y), the routing.
+__host__ __device__ inline int token_cols(const MoeParams& p) { return p.tokens <= 16 ? 16 : p.tokens <= 32 ? 32 : 64; }
 __host__ __device__ inline size_t up_stage_bytes(const MoeParams& p) { return kWTile + (size_t)token_cols(p) * BK; }
+__host__ __device__ inline int up_chunk_floats(const MoeParams& p) { return kChunkGroups * (token_cols(p) + 4); }
+__host__ __device__ inline size_t up_smem(const MoeParams& p) {
+  return 1024 + p.up_stages * up_stage_bytes(p) + (size_t)kChunks * up_chunk_floats(p) * 4 +
+         (size_t)p.tokens * kPitch * 4 + 16 + (size_t)p.experts * 8 + (size_t)p.active_max * 16 +
+         (size_t)p.tokens * p.top_k * 8;
+}
 __host__ __device__ inline size_t down_stage_bytes(const MoeParams& p) {
   return kWTile + (size_t)2 * token_cols(p) * BK;
 }
-__host__ __device__ inline size_t up_smem(const MoeParams& p) {
-  return 1024 + p.up_stages * up_stage_bytes(p) + (size_t)p.tokens * kPitch * 4 + 16 + up_route_bytes(p);
+__host__ __device__ inline int down_chunk_floats(const MoeParams& p) {
+  return 2 * kChunkGroups * token_cols(p) + kChunkGroups;
 }
 __host__ __device__ inline size_t down_smem(const MoeParams& p) {
-  return 1024 + p.down_stages * down_stage_bytes(p) + (size_t)p.tokens * 128 * 4 + down_route_bytes(p);
+  return 1024 + p.down_stages * down_stage_bytes(p) + (size_t)kChunks * down_chunk_floats(p) * 4 +
+         (size_t)p.tokens * 128 * 4 + (size_t)p.active_max * 8 + (size_t)p.slots_max * 8;
 }
 
 // top_k experts of token t by one warp: experts and softmax weights to chosen / weight (expert -1
 // where there is none), 1 to *poisoned for a NaN or +Inf logit.
-__device__ void route_token(const MoeParams& p, int t, int* chosen, float* weight, int* poisoned) {
-  constexpr int kPer = kMoeMaxExperts / 32;
+// PER: experts per lane at most.
+template <int PER>
+__device__ __forceinline__ void route_token(const MoeParams& p, int t, int* chosen, float* weight, int* poisoned) {
+  constexpr int kPer = PER;
   const int lane = threadIdx.x & 31;
   const float* row = p.logits + (int64_t)t * p.ldl;
   const int per = (p.experts + 31) / 32;
@@ -147,25 +155,28 @@ __device__ void route_token(const MoeParams& p, int t, int* chosen, float* weigh
   }
 }
 
-__global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_constant__ CUtensorMap mapX,
+// NC: columns of the product, the tokens rounded up to 16, 32 or 64.
+template <int NC>
+__global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_constant__ CUtensorMap mapX,
                                                              const __grid_constant__ CUtensorMap mapG,
                                                              const __grid_constant__ CUtensorMap mapU,
                                                              const __grid_constant__ MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
-  __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2];
+  __shared__ __align__(8) uint64_t full[kMaxStages], done[kMaxStages];
+  __shared__ __align__(8) uint64_t acc_empty[2];
+  __shared__ __align__(8) uint64_t scale_full[kChunks], scale_empty[kChunks];
   __shared__ uint32_t tmem_slot;
   __shared__ int n_active;
   __shared__ int poisoned[kMoeMaxTokens];
-  __shared__ __align__(16) float col_scale[2][kFoldThreads];
 
   const uint32_t raw_addr = smem_addr(smem_raw);
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
   const uint32_t sbase = raw_addr + pad;
-  const int stage_bytes = (int)up_stage_bytes(p);
-  const int ncols = token_cols(p);
-  float* sums = reinterpret_cast<float*>(smem_raw + pad + p.up_stages * stage_bytes);  // [slot of the expert][kPitch]
-  unsigned long long* mask_of =  // [experts], then the active experts' arrays
+  constexpr int stage_bytes = kWTile + NC * BK;
+  constexpr int kChunkFloats = kChunkGroups * (NC + 4);  // per group: NC token scales, gate's, up's
+  float* chunks = reinterpret_cast<float*>(smem_raw + pad + p.up_stages * stage_bytes);
+  float* sums = chunks + kChunks * kChunkFloats;  // [slot of the expert][kPitch]
+  unsigned long long* mask_of =                   // [experts], then the active experts' arrays
       reinterpret_cast<unsigned long long*>((reinterpret_cast<uintptr_t>(sums + p.tokens * kPitch) + 15) & ~uintptr_t(15));
   Route r;
   r.mask = mask_of + p.experts;
@@ -177,21 +188,31 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
+    prefetch_tensormap(&mapX);
+    prefetch_tensormap(&mapG);
+    prefetch_tensormap(&mapU);
     for (int s = 0; s < p.up_stages; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
-      mbar_init(smem_addr(&empty[s]), 1);
+      mbar_init(smem_addr(&done[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_addr(&acc_full[b]), 1);
-      mbar_init(smem_addr(&acc_empty[b]), kFoldThreads / 32);
+    for (int b = 0; b < 2; ++b) mbar_init(smem_addr(&acc_empty[b]), kFoldWarps);
+    for (int c = 0; c < kChunks; ++c) {
+      mbar_init(smem_addr(&scale_full[c]), 32);
+      mbar_init(smem_addr(&scale_empty[c]), kFoldWarps);
     }
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 128);
-  // ------------------------------------------------ routing
   for (int e = (int)threadIdx.x; e < p.experts; e += kThreads) mask_of[e] = 0ull;
-  for (int t = warp; t < p.tokens; t += kThreads / 32)
-    route_token(p, t, chosen + t * p.top_k, weight + t * p.top_k, &poisoned[t]);
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // what the stream's kernel before this one wrote
+  // ------------------------------------------------ routing
+  for (int t = warp; t < p.tokens; t += kThreads / 32) {
+    int* ch = chosen + t * p.top_k;
+    float* w = weight + t * p.top_k;
+    if (p.experts <= 64) route_token<2>(p, t, ch, w, &poisoned[t]);
+    else if (p.experts <= 256) route_token<8>(p, t, ch, w, &poisoned[t]);
+    else route_token<kMoeMaxExperts / 32>(p, t, ch, w, &poisoned[t]);
+  }
   __syncthreads();
   for (int i = (int)threadIdx.x; i < p.tokens * p.top_k; i += kThreads)
     if (chosen[i] >= 0) {
@@ -227,9 +248,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_slot;
   r.n = n_active;
-  if (blockIdx.x == 0) {  // the second kernel's copy
-    if (threadIdx.x == 0) p.route.counts[0] = r.n;
-    for (int a = (int)threadIdx.x; a < r.n; a += kThreads) {
+  if (blockIdx.x == gridDim.x - 1 && warp == 3) {  // the second kernel's copy, by a warp with nothing else to do
+    if (lane == 0) p.route.counts[0] = r.n;
+    for (int a = lane; a < r.n; a += 32) {
       p.route.expert[a] = r.expert[a];
       p.route.base[a] = r.base[a];
       p.route.mask[a] = r.mask[a];
@@ -243,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
         p.route.slot_weight[r.base[a] + j] = w;
       }
     }
-    for (int t = (int)threadIdx.x; t < p.tokens; t += kThreads) p.route.poisoned[t] = poisoned[t];
+    for (int t = lane; t < p.tokens; t += 32) p.route.poisoned[t] = poisoned[t];
   }
 
   const int col_tiles = (p.inner + kUpCols - 1) / kUpCols;
@@ -252,7 +273,6 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
   const int groups = (p.hidden + BK - 1) / BK;
 
   if (warp == 0) {
-    const uint32_t bytes = (uint32_t)stage_bytes;
     int t = 0, s = 0;
     uint32_t lap = 0;
     bool ok = true;
@@ -260,14 +280,14 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
       const int item = (int)blockIdx.x + i * (int)gridDim.x;
       const int e = r.expert[item / col_tiles], c0 = (item % col_tiles) * kUpCols;
       for (int g = 0; g < groups; ++g, ++t) {
-        if (lap > 0 && !poll_wait(smem_addr(&empty[s]), (lap - 1) & 1u, p.timeout_ns)) {
+        if (lap > 0 && !poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
           if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
           ok = false;
           break;
         }
         if (elect_one()) {
           const uint32_t bar = smem_addr(&full[s]), a = sbase + (uint32_t)(s * stage_bytes);
-          mbar_arrive_expect_tx(bar, bytes);
+          mbar_arrive_expect_tx(bar, (uint32_t)stage_bytes);
           tma_load_3d(a, &mapG, bar, g * BK, c0, e);
           tma_load_3d(a + kWTile / 2, &mapU, bar, g * BK, c0, e);
           tma_load_3d(a + kWTile, &mapX, bar, g * BK, 0, 0);
@@ -282,7 +302,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
       if (!poll_wait(smem_addr(&full[u % p.up_stages]), (uint32_t)(u / p.up_stages) & 1u, p.timeout_ns) && lane == 0)
         atomicOr(p.fault, (unsigned)kFaultDrainWait);
   } else if (warp == 1) {
-    const uint32_t idesc = moe_idesc(ncols);
+    constexpr uint32_t step = 32u >> 4;
+    const uint32_t desc0 = desc_lo(sbase);
     const int units = my_items * groups;
     int t = 0, s = 0;
     uint32_t lap = 0;
@@ -295,15 +316,12 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
       }
       tmem_fence_after_sync();
       if (elect_one()) {
-        const uint32_t a = sbase + (uint32_t)(s * stage_bytes);
-        const uint32_t wd = desc_lo(a), xd = desc_lo(a + kWTile);
+        const uint32_t wd = desc0 + (uint32_t)(s * (stage_bytes >> 4)), xd = wd + (kWTile >> 4);
 #pragma unroll
-        for (int ks = 0; ks < BK / 32; ++ks)
-          mma_f8(tmem + (uint32_t)b * 64u, make_desc(wd + (uint32_t)ks * step_of(0)),
-                 make_desc(xd + (uint32_t)ks * step_of(0)), idesc,
+        for (uint32_t ks = 0; ks < BK / 32; ++ks)
+          mma_f8(tmem + (uint32_t)b * 64u, make_desc(wd + ks * step), make_desc(xd + ks * step), moe_idesc(NC),
                  ks == 0 ? 0u : 1u);
-        mma_commit(smem_addr(&empty[s]));
-        mma_commit(smem_addr(&acc_full[b]));
+        mma_commit(smem_addr(&done[s]));  // the stage is free, the accumulator holds group t
       }
       __syncwarp();
       if (++s == p.up_stages) {
@@ -311,76 +329,122 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
         ++lap;
       }
     }
-    bool ok = true;  // every product has completed, and its commits have landed, before the CTA ends
+    bool ok = true;  // every product has completed, and its commit has landed, before the CTA ends
     for (int u = t > p.up_stages ? t - p.up_stages : 0; u < t; ++u)
-      ok = ok && poll_wait(smem_addr(&empty[u % p.up_stages]), (uint32_t)(u / p.up_stages) & 1u, p.timeout_ns);
-    for (int u = t > 2 ? t - 2 : 0; u < t; ++u)
-      ok = ok && poll_wait(smem_addr(&acc_full[u & 1]), (uint32_t)(u / 2) & 1u, p.timeout_ns);
+      ok = ok && poll_wait(smem_addr(&done[u % p.up_stages]), (uint32_t)(u / p.up_stages) & 1u, p.timeout_ns);
     if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultDrainWait);
-  } else {
+  } else if (warp == 2) {
+    const uint32_t ring = smem_addr(chunks);
+    int c = 0;
+    uint32_t lap = 0;
+    bool ok = true;
+    for (int i = 0; ok && i < my_items; ++i) {
+      const int item = (int)blockIdx.x + i * (int)gridDim.x;
+      const int e = r.expert[item / col_tiles], rb = (item % col_tiles) * kUpCols >> 7;
+      const float* sg = p.sg + (int64_t)e * p.stride_sg + (int64_t)rb * p.ldsg;
+      const float* su = p.su + (int64_t)e * p.stride_su + (int64_t)rb * p.ldsu;
+      for (int g0 = 0; g0 < groups; g0 += kChunkGroups) {
+        if (lap > 0 && !poll_wait(smem_addr(&scale_empty[c]), (lap - 1) & 1u, p.timeout_ns)) {
+          if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+          ok = false;
+          break;
+        }
+        const uint32_t dst = ring + 4u * (uint32_t)(c * kChunkFloats);
+        const int count = min(kChunkGroups, groups - g0);
+        for (int j = lane; j < NC + 2; j += 32) {
+          const float* src = j < NC ? p.sx + (int64_t)min(j, p.tokens - 1) * p.ldsx : j == NC ? sg : su;
+          for (int g = 0; g < count; ++g) copy4_async(dst + 4u * (uint32_t)(g * (NC + 4) + j), src + g0 + g);
+        }
+        copies_arrive(smem_addr(&scale_full[c]));
+        if (++c == kChunks) {
+          c = 0;
+          ++lap;
+        }
+      }
+    }
+    copies_wait_all();
+  } else if (warp >= kFirstFold) {
     const int q = warp & 3;
     const int row = 32 * q + lane;  // rows 0-63: gate, 64-127: up
-    const int fid = (int)threadIdx.x - 64;
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
-    const float* sx = p.sx + (int64_t)min(fid, p.tokens - 1) * p.ldsx;
     bool ok = true;
-    int t = 0;
+    int s = 0, c = 0, b = 0;
+    uint32_t s_lap = 0, c_lap = 0;
     for (int i = 0; i < my_items; ++i) {
       const int item = (int)blockIdx.x + i * (int)gridDim.x;
       const int a = item / col_tiles, c0 = (item % col_tiles) * kUpCols;
-      const int e = r.expert[a];
-      const float* sw = row < 64 ? p.sg + (int64_t)e * p.stride_sg + (int64_t)(c0 >> 7) * p.ldsg
-                                 : p.su + (int64_t)e * p.stride_su + (int64_t)(c0 >> 7) * p.ldsu;
-      float sum[kMoeMaxTokens];
+      float2 sum[NC / 2];
 #pragma unroll
-      for (int j = 0; j < kMoeMaxTokens; ++j) sum[j] = 0.0f;
-      float w_next = __ldg(sw), x_next = __ldg(sx);
-      for (int g = 0; g < groups; ++g, ++t) {
-        const int b = t & 1;
-        const float w_cur = w_next;
-        col_scale[b][fid] = x_next;  // last read two groups ago: one barrier per group suffices
-        if (g + 1 < groups) {
-          w_next = __ldg(sw + g + 1);
-          x_next = __ldg(sx + g + 1);
+      for (int j = 0; j < NC / 2; ++j) sum[j] = make_float2(0.0f, 0.0f);
+      for (int g = 0; ok && g < groups; ++g) {
+        const int in_chunk = g & (kChunkGroups - 1);
+        if (in_chunk == 0) ok = poll_wait(smem_addr(&scale_full[c]), c_lap & 1u, p.timeout_ns);
+        ok = ok && poll_wait(smem_addr(&done[s]), s_lap & 1u, p.timeout_ns);
+        if (!ok) {
+          if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+          break;
         }
-        fold_barrier();
-        if (ok) {  // a warp that gave up keeps meeting the others at the barriers
-          ok = poll_wait(smem_addr(&acc_full[b]), (uint32_t)(t / 2) & 1u, p.timeout_ns);
-          if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
-        }
-        if (!ok) continue;
         tmem_fence_after_sync();
+        const float* sc = chunks + c * kChunkFloats + in_chunk * (NC + 4);
+        const float w = sc[NC + (q >> 1)];
+        const float2 w2 = make_float2(w, w);
 #pragma unroll
-        for (int c = 0; c < kMoeMaxTokens / 16; ++c)
-          if (16 * c < ncols) {
-            float v[16];
-            tmem_ld16(tq + (uint32_t)(64 * b + 16 * c), v);
-            tmem_wait_ld();
-            if (16 * (c + 1) >= ncols) {
-              tmem_fence_before_sync();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_addr(&acc_empty[b]));
-            }
-            tmem_ld_ready(v);
-#pragma unroll
-            for (int j = 0; j < 16; ++j) sum[16 * c + j] = fmaf(v[j] * col_scale[b][16 * c + j], w_cur, sum[16 * c + j]);
+        for (int j0 = 0; j0 < NC; j0 += 32) {
+          constexpr int kCols = NC < 32 ? NC : 32;
+          float v[kCols];
+          tmem_ld<kCols>(tq + (uint32_t)(64 * b + j0), v);
+          tmem_wait_ld();
+          if (j0 + kCols == NC) {
+            tmem_fence_before_sync();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&acc_empty[b]));
           }
+#pragma unroll
+          for (int j = 0; j < kCols; ++j) asm volatile("" : "+f"(v[j]));  // used behind the wait only
+#pragma unroll
+          for (int j = 0; j < kCols; j += 4) {
+            const float4 x = *reinterpret_cast<const float4*>(sc + j0 + j);
+            float2* m = &sum[(j0 + j) / 2];
+            m[0] = __ffma2_rn(__fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(x.x, x.y)), w2, m[0]);
+            m[1] = __ffma2_rn(__fmul2_rn(make_float2(v[j + 2], v[j + 3]), make_float2(x.z, x.w)), w2, m[1]);
+          }
+        }
+        if (in_chunk == kChunkGroups - 1 || g == groups - 1) {
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&scale_empty[c]));
+          if (++c == kChunks) {
+            c = 0;
+            ++c_lap;
+          }
+        }
+        b ^= 1;
+        if (++s == p.up_stages) {
+          s = 0;
+          ++s_lap;
+        }
       }
-      // the chosen tokens' sums, compacted, to shared memory; then a warp per slot
+      // the chosen tokens' sums, compacted, to shared memory; then a warp per slot.  (A warp that gave
+      // up keeps meeting the others at the barriers.)
       const unsigned long long mask = r.mask[a];
       fold_barrier();  // the previous item's sums have been read
+      {
+        int at = row;
 #pragma unroll
-      for (int j = 0; j < kMoeMaxTokens; ++j)
-        if ((mask >> j) & 1ull) sums[__popcll(mask & ((1ull << j) - 1ull)) * kPitch + row] = sum[j];
+        for (int j = 0; j < NC; ++j)
+          if ((mask >> j) & 1ull) {
+            sums[at] = j & 1 ? sum[j / 2].y : sum[j / 2].x;
+            at += kPitch;
+          }
+      }
       fold_barrier();
       if (!ok) continue;
       const int n = __popcll(mask);
-      for (int j = warp - 2; j < n; j += kFoldThreads / 32) {
-        const float* s = sums + j * kPitch;
+      for (int j = warp - kFirstFold; j < n; j += kFoldWarps) {
+        const float* u = sums + j * kPitch;
         float h[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-          const float gate = s[2 * lane + k], up = s[64 + 2 * lane + k];
+          const float gate = u[2 * lane + k], up = u[64 + 2 * lane + k];
           h[k] = gate / (1.0f + expf(-gate)) * up;
         }
         const float scale = group_scale(lanes_max<32>(fmaxf(finite_abs(h[0]), finite_abs(h[1]))), kMaxE4M3);
@@ -406,20 +470,26 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
   if (warp == 1) tmem_dealloc(tmem, 128);
 }
 
-__global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_constant__ CUtensorMap mapH,
+// NC: the tokens rounded up to 16, 32 or 64: slots of an expert at most.
+template <int NC>
+__global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_constant__ CUtensorMap mapH,
                                                                const __grid_constant__ CUtensorMap mapD,
                                                                const __grid_constant__ MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
-  __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2];
+  __shared__ __align__(8) uint64_t full[kMaxStages], done[kMaxStages];
+  __shared__ __align__(8) uint64_t acc_empty[2];
+  __shared__ __align__(8) uint64_t scale_full[kChunks], scale_empty[kChunks];
   __shared__ uint32_t tmem_slot;
-  __shared__ __align__(16) float col_scale[2][kMoeMaxTokens];
 
   const uint32_t raw_addr = smem_addr(smem_raw);
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
   const uint32_t sbase = raw_addr + pad;
-  const int stage_bytes = (int)down_stage_bytes(p);
-  float* ysum = reinterpret_cast<float*>(smem_raw + pad + p.down_stages * stage_bytes);  // [tokens][128]
+  constexpr int stage_bytes = kWTile + 2 * NC * BK;
+  constexpr int kChunkFloats = 2 * kChunkGroups * NC + kChunkGroups;  // slots' scales of 16 halves, weights' of 8 units
+  constexpr uint32_t kHalfCols = 2 * NC, kAccCols = 4 * NC;           // of an accumulator: a unit's two halves
+  constexpr uint32_t kTmemCols = 2 * kAccCols;
+  float* chunks = reinterpret_cast<float*>(smem_raw + pad + p.down_stages * stage_bytes);
+  float* ysum = chunks + kChunks * kChunkFloats;  // [tokens][128]
   int* expert = reinterpret_cast<int*>(ysum + p.tokens * 128);
   int* base = expert + p.active_max;
   int* slot_token = base + p.active_max;
@@ -430,18 +500,22 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   const int l0 = tile * 128;
   const int groups = (p.inner + BK - 1) / BK;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
+    prefetch_tensormap(&mapH);
+    prefetch_tensormap(&mapD);
     for (int s = 0; s < p.down_stages; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
-      mbar_init(smem_addr(&empty[s]), 1);
+      mbar_init(smem_addr(&done[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_addr(&acc_full[b]), 1);
-      mbar_init(smem_addr(&acc_empty[b]), kFoldThreads / 32);
+    for (int b = 0; b < 2; ++b) mbar_init(smem_addr(&acc_empty[b]), kFoldWarps);
+    for (int c = 0; c < kChunks; ++c) {
+      mbar_init(smem_addr(&scale_full[c]), 32);
+      mbar_init(smem_addr(&scale_empty[c]), kFoldWarps);
     }
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 256);
+  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
   for (int i = (int)threadIdx.x; i < p.tokens * 128; i += kThreads) ysum[i] = 0.0f;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel's routing and inner values are complete
   const int n_active = p.route.counts[0];
@@ -461,134 +535,187 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   const uint32_t tmem = tmem_slot;
   const int total = n_active * groups;
   const int u0 = (int)((int64_t)total * rank / p.split), u1 = (int)((int64_t)total * (rank + 1) / p.split);
+  const int a0 = groups > 0 ? u0 / groups : 0, g_first = u0 - a0 * groups;  // expert and group of the first unit
   const auto slots_of = [&](int a) { return (a + 1 < n_active ? base[a + 1] : n_slots) - base[a]; };
 
   if (warp == 0) {
-    int t = 0, s = 0;
+    int s = 0, a = a0, g = g_first;
     uint32_t lap = 0;
-    for (int u = u0; u < u1; ++u, ++t) {
-      if (lap > 0 && !poll_wait(smem_addr(&empty[s]), (lap - 1) & 1u, p.timeout_ns)) {
+    int t = 0;
+    for (; t < u1 - u0; ++t) {
+      if (lap > 0 && !poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
         if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
         break;
       }
-      const int a = u / groups, k0 = (u - a * groups) * BK;
       const int boxes = (slots_of(a) + 15) / 16;  // of 16 slots (32 rows)
       const int e = expert[a], slot = base[a];
       if (elect_one()) {
         const uint32_t bar = smem_addr(&full[s]), at = sbase + (uint32_t)(s * stage_bytes);
         mbar_arrive_expect_tx(bar, (uint32_t)(kWTile + boxes * 32 * BK));
-        tma_load_3d(at, &mapD, bar, k0, l0, e);
+        tma_load_3d(at, &mapD, bar, g * BK, l0, e);
         for (int i = 0; i < boxes; ++i)
-          tma_load_3d(at + kWTile + (uint32_t)(i * 32 * BK), &mapH, bar, k0, 2 * (slot + 16 * i), 0);
+          tma_load_3d(at + kWTile + (uint32_t)(i * 32 * BK), &mapH, bar, g * BK, 2 * (slot + 16 * i), 0);
       }
       if (++s == p.down_stages) {
         s = 0;
         ++lap;
+      }
+      if (++g == groups) {
+        g = 0;
+        ++a;
       }
     }
     for (int v = t > p.down_stages ? t - p.down_stages : 0; v < t; ++v)
       if (!poll_wait(smem_addr(&full[v % p.down_stages]), (uint32_t)(v / p.down_stages) & 1u, p.timeout_ns) && lane == 0)
         atomicOr(p.fault, (unsigned)kFaultDrainWait);
   } else if (warp == 1) {
-    // a unit's two halves of 64 inner columns have scales, and so accumulators, of their own
-    int issued = 0, done = 0, s = 0;
+    // a unit's two halves of 64 inner columns have scales, and so columns of the accumulator, of their own
+    constexpr uint32_t step = 32u >> 4;
+    const uint32_t desc0 = desc_lo(sbase);
+    int t = 0, s = 0, a = a0, g = g_first;
     uint32_t lap = 0;
-    for (int t = 0; t < u1 - u0; ++t) {
-      bool ok = poll_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns);
-      const uint32_t idesc = moe_idesc(32 * ((slots_of((u0 + t) / groups) + 15) / 16));
-      const uint32_t at = sbase + (uint32_t)(s * stage_bytes);
-      const uint32_t wd = desc_lo(at), hd = desc_lo(at + kWTile);
-#pragma unroll
-      for (int b = 0; b < 2; ++b) {
-        ok = ok && (t == 0 || poll_wait(smem_addr(&acc_empty[b]), (uint32_t)(t - 1) & 1u, p.timeout_ns));
-        if (!ok) break;
-        tmem_fence_after_sync();
-        if (elect_one()) {
-#pragma unroll
-          for (int ks = 0; ks < 2; ++ks)
-            mma_f8(tmem + (uint32_t)(128 * b), make_desc(wd + (uint32_t)(2 * b + ks) * step_of(0)),
-                   make_desc(hd + (uint32_t)(2 * b + ks) * step_of(0)), idesc, ks == 0 ? 0u : 1u);
-          mma_commit(smem_addr(&acc_full[b]));
-          if (b == 1) mma_commit(smem_addr(&empty[s]));
-        }
-        __syncwarp();
-      }
-      if (!ok) {
-        if (elect_one()) mma_commit(smem_addr(&empty[s]));
-        __syncwarp();
-        issued = t + 1;
+    for (; t < u1 - u0; ++t) {
+      const int b = t & 1;
+      if ((t >= 2 && !poll_wait(smem_addr(&acc_empty[b]), (uint32_t)((t / 2) - 1) & 1u, p.timeout_ns)) ||
+          !poll_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns)) {
         if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
         break;
       }
-      issued = done = t + 1;
+      const uint32_t idesc = moe_idesc(32 * ((slots_of(a) + 15) / 16));
+      tmem_fence_after_sync();
+      if (elect_one()) {
+        const uint32_t wd = desc0 + (uint32_t)(s * (stage_bytes >> 4)), hd = wd + (kWTile >> 4);
+        const uint32_t acc = tmem + (uint32_t)b * kAccCols;
+#pragma unroll
+        for (uint32_t ks = 0; ks < 4; ++ks)
+          mma_f8(acc + (ks >> 1) * kHalfCols, make_desc(wd + ks * step), make_desc(hd + ks * step), idesc, ks & 1u);
+        mma_commit(smem_addr(&done[s]));  // the stage is free, the accumulator holds unit t
+      }
+      __syncwarp();
       if (++s == p.down_stages) {
         s = 0;
         ++lap;
       }
+      if (++g == groups) {
+        g = 0;
+        ++a;
+      }
     }
-    bool ok = true;  // every product has completed, and its commits have landed, before the CTA ends
-    for (int u = issued > p.down_stages ? issued - p.down_stages : 0; u < issued; ++u)
-      ok = ok && poll_wait(smem_addr(&empty[u % p.down_stages]), (uint32_t)(u / p.down_stages) & 1u, p.timeout_ns);
-    for (int b = 0; b < 2 && done > 0; ++b)
-      ok = ok && poll_wait(smem_addr(&acc_full[b]), (uint32_t)(done - 1) & 1u, p.timeout_ns);
+    bool ok = true;  // every product has completed, and its commit has landed, before the CTA ends
+    for (int u = t > p.down_stages ? t - p.down_stages : 0; u < t; ++u)
+      ok = ok && poll_wait(smem_addr(&done[u % p.down_stages]), (uint32_t)(u / p.down_stages) & 1u, p.timeout_ns);
     if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultDrainWait);
-  } else {
+  } else if (warp == 2) {
+    // chunks: up to 8 consecutive units of one expert
+    const uint32_t ring = smem_addr(chunks);
+    int c = 0, a = a0, g = g_first;
+    uint32_t lap = 0;
+    for (int t = 0; t < u1 - u0;) {
+      if (lap > 0 && !poll_wait(smem_addr(&scale_empty[c]), (lap - 1) & 1u, p.timeout_ns)) {
+        if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+        break;
+      }
+      const int count = min(min(kChunkGroups, groups - g), u1 - u0 - t);
+      const uint32_t dst = ring + 4u * (uint32_t)(c * kChunkFloats);
+      const int n = slots_of(a), halves = min(2 * count, p.h_groups - 2 * g);
+      for (int j = lane; j < n; j += 32) {
+        const float* src = p.sh + (int64_t)(base[a] + j) * p.h_groups + 2 * g;
+        for (int h = 0; h < halves; ++h) copy4_async(dst + 4u * (uint32_t)(h * NC + j), src + h);
+      }
+      if (lane < count)
+        copy4_async(dst + 4u * (uint32_t)(2 * kChunkGroups * NC + lane),
+                    p.sd + (int64_t)expert[a] * p.stride_sd + (int64_t)(l0 >> 7) * p.ldsd + g + lane);
+      copies_arrive(smem_addr(&scale_full[c]));
+      t += count;
+      g += count;
+      if (g == groups) {
+        g = 0;
+        ++a;
+      }
+      if (++c == kChunks) {
+        c = 0;
+        ++lap;
+      }
+    }
+    copies_wait_all();
+  } else if (warp >= kFirstFold) {
     const int q = warp & 3;
     const int row = 32 * q + lane;
-    const int fid = (int)threadIdx.x - 64;
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
-    float sum[kMoeMaxTokens];
+    float sum[NC];
 #pragma unroll
-    for (int j = 0; j < kMoeMaxTokens; ++j) sum[j] = 0.0f;
+    for (int j = 0; j < NC; ++j) sum[j] = 0.0f;
     bool ok = true;
-    // scale of this thread's slot (fid < 64) in half v of the CTA's units, times the weights' scale
-    const auto scale_of = [&](int v) {
-      const int u = u0 + (v >> 1), a = u / groups, g = u - a * groups, hg = 2 * g + (v & 1);
-      if (u >= u1 || fid >= slots_of(a) || hg >= p.h_groups) return 0.0f;
-      return __ldg(p.sh + (int64_t)(base[a] + fid) * p.h_groups + hg) *
-             __ldg(p.sd + (int64_t)expert[a] * p.stride_sd + (int64_t)(l0 >> 7) * p.ldsd + g);
-    };
-    const int halves = 2 * (u1 - u0);
-    float s_next = fid < kMoeMaxTokens && halves > 0 ? scale_of(0) : 0.0f;
-    for (int v = 0; v < halves; ++v) {
-      const int b = v & 1, t = v >> 1;
-      const int a = (u0 + t) / groups, n = slots_of(a);
-      if (fid < kMoeMaxTokens) {
-        col_scale[b][fid] = s_next;  // last read two halves ago: one barrier per half suffices
-        s_next = scale_of(v + 1);
+    int s = 0, c = 0, a = a0, g = g_first, in_chunk = 0, left = 0;  // left: units of the chunk
+    uint32_t s_lap = 0, c_lap = 0;
+    int n = 0;
+    for (int t = 0; t < u1 - u0; ++t) {
+      const int b = t & 1;
+      if (left == 0) {
+        ok = poll_wait(smem_addr(&scale_full[c]), c_lap & 1u, p.timeout_ns);
+        in_chunk = 0;
+        left = min(min(kChunkGroups, groups - g), u1 - u0 - t);
+        n = slots_of(a);
       }
-      fold_barrier();
-      if (ok) {  // a warp that gave up keeps meeting the others at the barrier
-        ok = poll_wait(smem_addr(&acc_full[b]), (uint32_t)t & 1u, p.timeout_ns);
-        if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+      ok = ok && poll_wait(smem_addr(&done[s]), s_lap & 1u, p.timeout_ns);
+      if (!ok) {
+        if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+        break;
       }
-      if (!ok) continue;
       tmem_fence_after_sync();
+      const float* sc = chunks + c * kChunkFloats + 2 * in_chunk * NC;
+      const float w = chunks[c * kChunkFloats + 2 * kChunkGroups * NC + in_chunk];
+      const bool second = 2 * g + 1 < p.h_groups;  // the unit has a second half
+      const uint32_t acc = tq + (uint32_t)b * kAccCols;
+      // 8 slots of both halves at a time: hi, lo, hi, lo, ...
 #pragma unroll
-      for (int c = 0; c < kMoeMaxTokens / 8; ++c)
-        if (8 * c < n) {
-          float x[16];  // 8 slots: hi, lo, hi, lo, ...
-          tmem_ld16(tq + (uint32_t)(128 * b + 16 * c), x);
+      for (int j0 = 0; j0 < NC; j0 += 8) {
+        if (j0 < n) {
+          float x[2][16];
+          tmem_ld16(acc + (uint32_t)(2 * j0), x[0]);
+          tmem_ld16(acc + kHalfCols + (uint32_t)(2 * j0), x[1]);
           tmem_wait_ld();
-          if (8 * (c + 1) >= n) {
+          if (j0 + 8 >= n) {
             tmem_fence_before_sync();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&acc_empty[b]));
           }
-          tmem_ld_ready(x);
+          tmem_ld_ready(x[0]);
+          tmem_ld_ready(x[1]);
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            sum[8 * c + j] = fmaf(fmaf(x[2 * j + 1], 1.0f / kLoScale, x[2 * j]), col_scale[b][8 * c + j], sum[8 * c + j]);
+          for (int j = 0; j < 8; ++j) {
+            float v = fmaf(x[0][2 * j + 1], 1.0f / kLoScale, x[0][2 * j]) * sc[j0 + j];
+            if (second) v = fmaf(fmaf(x[1][2 * j + 1], 1.0f / kLoScale, x[1][2 * j]), sc[NC + j0 + j], v);
+            sum[j0 + j] = fmaf(v, w, sum[j0 + j]);
+          }
         }
-      if (b == 1 && (t + 1 == u1 - u0 || (u0 + t + 1) / groups != a)) {  // the expert's last unit here
+      }
+      ++in_chunk;
+      if (--left == 0) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&scale_empty[c]));
+        if (++c == kChunks) {
+          c = 0;
+          ++c_lap;
+        }
+      }
+      if (++s == p.down_stages) {
+        s = 0;
+        ++s_lap;
+      }
+      const bool last = ++g == groups;
+      if (last || t + 1 == u1 - u0) {  // the expert's last unit here
 #pragma unroll
-        for (int j = 0; j < kMoeMaxTokens; ++j)
-        {
+        for (int j = 0; j < NC; ++j) {
           if (j < n) {
             float& y = ysum[slot_token[base[a] + j] * 128 + row];  // only this thread touches this row
             y = fmaf(slot_weight[base[a] + j], sum[j], y);
           }
           sum[j] = 0.0f;  // those past n too: they may hold what lay behind the expert's rows
+        }
+        if (last) {
+          g = 0;
+          ++a;
         }
       }
     }
@@ -598,24 +725,24 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
-  if (warp == 1) tmem_dealloc(tmem, 256);
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
   __syncwarp();
   cluster_sync();
   const uint32_t y_addr = smem_addr(ysum);
   const int t0 = p.tokens * 128 * rank / p.split, t1 = p.tokens * 128 * (rank + 1) / p.split;
   for (int i = t0 + (int)threadIdx.x; i < t1; i += kThreads) {
     const int tok = i >> 7, col = l0 + (i & 127);
-    float v = 0.0f;
-    for (int r0 = 0; r0 < p.split; r0 += 8) {
-      float u[8];
+    float u[8], v = 0.0f;
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r0 + r < p.split)
-          asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(u[r]) : "r"(map_to_rank(y_addr + 4u * (uint32_t)i, (uint32_t)(r0 + r))) : "memory");
+    for (int k = 0; k < 8; ++k)
+      if (k < p.split)
+        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                     : "=f"(u[k])
+                     : "r"(map_to_rank(y_addr + 4u * (uint32_t)i, (uint32_t)k))
+                     : "memory");
 #pragma unroll
-      for (int r = 0; r < 8; ++r)
-        if (r0 + r < p.split) v += u[r];
-    }
+    for (int k = 0; k < 8; ++k)
+      if (k < p.split) v += u[k];
     if (p.route.poisoned[tok]) v = __int_as_float(0x7FFFFFFF);
     if (col < p.hidden) {
       const int64_t o = (int64_t)tok * p.ldy + col;
@@ -627,49 +754,75 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   cluster_sync();  // no CTA leaves while a peer may read its sums
 }
 
-constexpr size_t kCtaSmem = 110 * 1024;  // two CTAs per SM
-constexpr int kMaxSmem = 220 * 1024;
+constexpr size_t kMaxSmem = 227 * 1024 - 2048;  // less the kernels' static arrays
+
+// f(NC) for the token columns of p.
+template <typename F>
+cudaError_t with_token_cols(int cols, const F& f) {
+  return cols == 16   ? f(std::integral_constant<int, 16>{})
+         : cols == 32 ? f(std::integral_constant<int, 32>{})
+                      : f(std::integral_constant<int, 64>{});
+}
+
+cudaError_t launch_pdl(const void* kernel, int grid, int cluster, size_t smem, void** args, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = (unsigned)cluster;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelExC(&cfg, kernel, args);
+}
 
 }  // namespace
 }  // namespace f8
 
 cudaError_t prepare_fp8_moe() {
-  cudaError_t e = cudaFuncSetAttribute(f8::moe_up_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, f8::kMaxSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(f8::moe_down_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, f8::kMaxSmem);
-  return e;
+  for (int cols = 16; cols <= 64; cols *= 2) {
+    const cudaError_t e = f8::with_token_cols(cols, [](auto nc) {
+      constexpr int NC = decltype(nc)::value;
+      const cudaError_t up = cudaFuncSetAttribute(f8::moe_up_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                                  (int)f8::kMaxSmem);
+      return up != cudaSuccess ? up
+                               : cudaFuncSetAttribute(f8::moe_down_kernel<NC>,
+                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f8::kMaxSmem);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 void shape_fp8_moe(MoeParams* p, int sm_count) {
-  // as many stages as two CTAs per SM leave room for, two at least
-  for (p->up_stages = f8::kMaxStages; p->up_stages > 2 && f8::up_smem(*p) > f8::kCtaSmem;) --p->up_stages;
-  for (p->down_stages = f8::kMaxStages; p->down_stages > 2 && f8::down_smem(*p) > f8::kCtaSmem;) --p->down_stages;
+  for (p->up_stages = f8::kMaxStages; p->up_stages > 2 && f8::up_smem(*p) > f8::kMaxSmem;) --p->up_stages;
+  for (p->down_stages = f8::kMaxStages; p->down_stages > 2 && f8::down_smem(*p) > f8::kMaxSmem;) --p->down_stages;
   const int tiles = (p->hidden + 127) / 128;
   p->split = 1;
-  while (p->split < 8 && tiles * p->split * 2 <= 2 * sm_count) p->split *= 2;
+  while (p->split < 8 && tiles * p->split * 2 <= sm_count) p->split *= 2;
 }
 
 cudaError_t launch_fp8_moe(const MoeMaps& maps, const MoeParams& p, int sm_count, cudaStream_t stream) {
   const int col_tiles = (p.inner + f8::kUpCols - 1) / f8::kUpCols;
-  const int grid = std::min(2 * sm_count, p.active_max * col_tiles);
-  f8::moe_up_kernel<<<grid, f8::kThreads, f8::up_smem(p), stream>>>(maps.x, maps.gate, maps.up, p);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)((p.hidden + 127) / 128 * p.split));
-  cfg.blockDim = dim3(f8::kThreads);
-  cfg.dynamicSmemBytes = f8::down_smem(p);
-  cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)p.split;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = 2;
-  return cudaLaunchKernelEx(&cfg, f8::moe_down_kernel, maps.h, maps.down, p);
+  const int grid = std::min(sm_count, p.active_max * col_tiles);
+  return f8::with_token_cols(f8::token_cols(p), [&](auto nc) {
+    constexpr int NC = decltype(nc)::value;
+    CUtensorMap x = maps.x, g = maps.gate, u = maps.up, h = maps.h, d = maps.down;
+    MoeParams q = p;
+    void* up_args[] = {&x, &g, &u, &q};
+    const cudaError_t e = f8::launch_pdl(reinterpret_cast<const void*>(f8::moe_up_kernel<NC>), grid, 1, f8::up_smem(p),
+                                         up_args, stream);
+    if (e != cudaSuccess) return e;
+    void* down_args[] = {&h, &d, &q};
+    return f8::launch_pdl(reinterpret_cast<const void*>(f8::moe_down_kernel<NC>), (p.hidden + 127) / 128 * p.split,
+                          p.split, f8::down_smem(p), down_args, stream);
+  });
 }
 
 }  // namespace sgemm_impl
