@@ -575,13 +575,6 @@ int sgemm_fp8_moe(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts
   const auto place = [&](Pieces* w) {
     p.h = w->take<uint8_t>(2 * (int64_t)p.slots_max * inner);
     p.sh = w->take<float>((int64_t)p.slots_max * p.h_groups);
-    p.route.counts = w->take<int>(1);
-    p.route.expert = w->take<int>(p.active_max);
-    p.route.base = w->take<int>(p.active_max);
-    p.route.mask = w->take<unsigned long long>(p.active_max);
-    p.route.slot_token = w->take<int>(p.slots_max);
-    p.route.slot_weight = w->take<float>(p.slots_max);
-    p.route.poisoned = w->take<int>(tokens);
     x_copy = w->take<uint8_t>(repack_bytes(x));
   };
   Pieces count;

@@ -131,17 +131,6 @@ cudaError_t launch_fp8_short(const CUtensorMap& mapL, const CUtensorMap& mapS, c
 
 // ---- mixture of experts for a few tokens (kernel_fp8_moe.cu)
 constexpr int kMoeMaxTokens = 64, kMoeMaxExperts = 1024, kMoeMaxTopK = 16;
-// What the first kernel leaves for the second: the experts that some token chose (ascending), each
-// with its tokens, and a slot per (expert, token), numbered in that order.
-struct MoeRoute {
-  int* counts = nullptr;                  // [0]: active experts
-  int* expert = nullptr;                  // [active]
-  int* base = nullptr;                    // [active] first slot
-  unsigned long long* mask = nullptr;     // [active] bit t: token t chose the expert
-  int* slot_token = nullptr;              // [slots]
-  float* slot_weight = nullptr;           // [slots]
-  int* poisoned = nullptr;                // [tokens] 1: a NaN or +Inf logit
-};
 struct MoeParams {
   int tokens = 0, hidden = 0, inner = 0, experts = 0, top_k = 0, renormalize = 0;
   const float* logits = nullptr;
@@ -153,11 +142,11 @@ struct MoeParams {
   uint8_t* h = nullptr;                   // inner values: slot j has rows 2j (hi) and 2j + 1 (lo * 16) of `inner` codes
   float* sh = nullptr;                    // [slots][h_groups], one scale per 64 of them
   int h_groups = 0;
-  MoeRoute route;
   void* y = nullptr;
   int64_t ldy = 0;
   int bf16 = 0;
   int up_stages = 0, down_stages = 0, split = 1;
+  int dense = 0;                          // 1: nearly every expert will have a token
   int active_max = 0, slots_max = 0;      // bounds of the routing arrays
   uint64_t timeout_ns = 0;
   unsigned* fault = nullptr;

@@ -6,19 +6,24 @@
 // meets all the tokens that need it, as the 128 rows of a tensor-core product whose columns are
 // tokens (16 to 64 of them, so the products cost little beside the loads).
 //
-// moe_up_kernel: every CTA works out the routing from the logits by itself (a warp per token; top_k
-// rounds of a warp maximum), which costs less than a launch, and takes tiles of 64 inner columns of
-// active experts: rows 0-63 of the product are rows of W1_e, rows 64-127 rows of W3_e, the columns
-// all the tokens in order, so x is loaded as it lies and no token is gathered.  The sums of the
-// tokens that chose e become h = silu(gate) * up, stored as two E4M3 terms with a scale per 64
-// columns: hi = rn8(h / s), lo = rn8(16 (h / s - hi)), together within 2^-9.8 of the group's largest
-// value.  As the second product is bound by the weights, the doubled columns are free.
+// Every CTA of both kernels works out the routing from the logits by itself (a warp per token), which
+// costs less than a launch.
+//
+// moe_up_kernel takes tiles of 64 inner columns of active experts: rows 0-63 of the product are rows of
+// W1_e, rows 64-127 rows of W3_e, the columns all the tokens in order, so x is loaded as it lies and no
+// token is gathered.  The sums of the tokens that chose e become h = silu(gate) * up, stored as two
+// E4M3 terms with a scale per 64 columns: hi = rn8(h / s), lo = rn8(16 (h / s - hi)), together within
+// 2^-9.8 of the group's largest value.  As the second product is bound by the weights, the doubled
+// columns are free.
 //
 // moe_down_kernel: a cluster of CTAs per 128 rows of the hidden side shares the (expert, 128 inner
 // columns) units in order; each CTA folds its units per expert in FP32 registers, adds them weighted
-// into its tokens' sums in shared memory, and the cluster adds those in rank order into Y.
+// into its tokens' sums in shared memory, and the cluster adds those in rank order into Y.  A CTA of
+// each kernel fits on an SM beside one of the other, and the second kernel is launched when the first
+// has begun: it routes and fills its ring with W2 meanwhile, and waits for the first kernel only
+// before it loads h (one token: its 17 MB of W2 are then nearly all on chip).
 //
-// Both: one CTA per SM with as many 16 KB weight tiles in flight as its shared memory holds; warp 0
+// Both: one CTA per SM with as many 16 KB weight tiles in flight as half its shared memory holds; warp 0
 // loads (TMA), warp 1 issues the products, warp 2 loads scales a chunk of groups ahead, warps 4-7 fold
 // the accumulators (two alternate) into FP32 sums in registers.
 #include <algorithm>
@@ -40,6 +45,7 @@ constexpr float kLoScale = 16.0f;
 constexpr int kPitch = 129;
 constexpr int kChunkGroups = 8;   // groups of 128 k whose scales are loaded together
 constexpr int kChunks = 3;        // in shared memory
+constexpr int kPrefetch = 16;     // weight tiles a CTA sends for before it knows the routing, at most (40 MB in all)
 
 __device__ __forceinline__ void fold_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -53,12 +59,38 @@ __device__ __forceinline__ uint32_t order_key(float x) {
   return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-// Routing arrays in shared memory.
+// The routing, in shared memory: the experts that some token chose, in ascending order, each with its
+// tokens, and a slot per (expert, token), numbered in that order.
 struct Route {
-  int n;                       // active experts
-  unsigned long long* mask;    // [active]
-  int *expert, *base;          // [active]
+  unsigned long long* mask_of;  // [experts] bit t: token t chose the expert
+  unsigned long long* mask;     // [active] the same, of active experts
+  int *expert, *base;           // [active] its number and first slot
+  int* active_of;               // [experts]
+  int* chosen;                  // [tokens][top_k] experts, -1: none
+  float* weight;                // [tokens][top_k]
+  int* slot_token;              // [slots]
+  float* slot_weight;           // [slots]
+  int* poisoned;                // [tokens] 1: a NaN or +Inf logit
+  int* counts;                  // active experts, slots
 };
+__host__ __device__ inline size_t route_bytes(const MoeParams& p) {
+  return 16 + (size_t)p.experts * 12 + (size_t)p.active_max * 16 + (size_t)p.slots_max * 16 + (size_t)p.tokens * 4;
+}
+__device__ __forceinline__ Route route_at(const MoeParams& p, void* smem) {
+  Route r;
+  r.mask_of = reinterpret_cast<unsigned long long*>((reinterpret_cast<uintptr_t>(smem) + 7) & ~uintptr_t(7));
+  r.mask = r.mask_of + p.experts;
+  r.expert = reinterpret_cast<int*>(r.mask + p.active_max);
+  r.base = r.expert + p.active_max;
+  r.active_of = r.base + p.active_max;
+  r.chosen = r.active_of + p.experts;
+  r.weight = reinterpret_cast<float*>(r.chosen + p.slots_max);
+  r.slot_token = reinterpret_cast<int*>(r.weight + p.slots_max);
+  r.slot_weight = reinterpret_cast<float*>(r.slot_token + p.slots_max);
+  r.poisoned = reinterpret_cast<int*>(r.slot_weight + p.slots_max);
+  r.counts = r.poisoned + p.tokens;
+  return r;
+}
 
 // Dynamic shared memory, in this order: the ring of stages (1024-byte aligned), the scale chunks, the
 // sums (first kernel: of an item's tokens; second: of Y), the routing.
@@ -67,8 +99,7 @@ __host__ __device__ inline size_t up_stage_bytes(const MoeParams& p) { return kW
 __host__ __device__ inline int up_chunk_floats(const MoeParams& p) { return kChunkGroups * (token_cols(p) + 4); }
 __host__ __device__ inline size_t up_smem(const MoeParams& p) {
   return 1024 + p.up_stages * up_stage_bytes(p) + (size_t)kChunks * up_chunk_floats(p) * 4 +
-         (size_t)p.tokens * kPitch * 4 + 16 + (size_t)p.experts * 8 + (size_t)p.active_max * 16 +
-         (size_t)p.tokens * p.top_k * 8;
+         (size_t)p.tokens * kPitch * 4 + route_bytes(p);
 }
 __host__ __device__ inline size_t down_stage_bytes(const MoeParams& p) {
   return kWTile + (size_t)2 * token_cols(p) * BK;
@@ -78,86 +109,165 @@ __host__ __device__ inline int down_chunk_floats(const MoeParams& p) {
 }
 __host__ __device__ inline size_t down_smem(const MoeParams& p) {
   return 1024 + p.down_stages * down_stage_bytes(p) + (size_t)kChunks * down_chunk_floats(p) * 4 +
-         (size_t)p.tokens * 128 * 4 + (size_t)p.active_max * 8 + (size_t)p.slots_max * 8;
+         (size_t)p.tokens * 128 * 4 + route_bytes(p);
 }
 
-// top_k experts of token t by one warp: experts and softmax weights to chosen / weight (expert -1
-// where there is none), 1 to *poisoned for a NaN or +Inf logit.
-// PER: experts per lane at most.
+// The logits of one token as a warp holds them: expert e = 32 i + lane has keys[i], 0 where it cannot
+// be chosen (-Inf, past the end); returns whether one is NaN or +Inf.
 template <int PER>
-__device__ __forceinline__ void route_token(const MoeParams& p, int t, int* chosen, float* weight, int* poisoned) {
-  constexpr int kPer = PER;
+__device__ __forceinline__ bool load_keys(const MoeParams& p, int t, uint32_t (&keys)[PER]) {
   const int lane = threadIdx.x & 31;
   const float* row = p.logits + (int64_t)t * p.ldl;
-  const int per = (p.experts + 31) / 32;
-  uint32_t key[kPer];  // expert e = 32 i + lane
   bool bad = false;
 #pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    key[i] = 0u;
-    if (i < per && 32 * i + lane < p.experts) {
+  for (int i = 0; i < PER; ++i) {
+    keys[i] = 0u;
+    if (32 * i + lane < p.experts) {
       const float x = row[32 * i + lane];
       if (!(x < INFINITY)) bad = true;
-      else if (x > -INFINITY) key[i] = order_key(x + 0.0f);  // -0 counts as 0
+      else if (x > -INFINITY) keys[i] = order_key(x + 0.0f);  // -0 counts as 0
     }
   }
-  if (lane == 0) *poisoned = 0;
-  if (__any_sync(0xffffffffu, bad)) {
-    if (lane == 0) *poisoned = 1;
-    for (int j = lane; j < p.top_k; j += 32) chosen[j] = -1;
-    return;
-  }
-  float top = 0.0f, sum = 0.0f;
-  float mine = 0.0f;  // lane j: exp(logit - top) of choice j
-  int mine_e = -1;
-  for (int j = 0; j < p.top_k; ++j) {
-    uint32_t best = 0u;
-    int at = 0;
+  return bad;
+}
+__device__ __forceinline__ float key_value(uint32_t k) { return __uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k); }
+
+// The warp's tokens t0, t0 + step, ...: their top_k experts with softmax weights to r.chosen and
+// r.weight (expert -1 where there is none), 1 to r.poisoned for a token with a NaN or +Inf logit.
+// PER: experts per lane at most.  top_k rounds of a warp maximum, TK tokens side by side: a round is
+// 200 cycles of instructions that wait for one another.
+template <int PER, int TK>
+__device__ __forceinline__ void route_tokens(const MoeParams& p, const Route& r, int t0, int step) {
+  const int lane = threadIdx.x & 31;
+  for (; t0 < p.tokens; t0 += TK * step) {
+    uint32_t keys[TK][PER];
+    bool bad[TK];
 #pragma unroll
-    for (int i = 0; i < kPer; ++i)
-      if (i < per && key[i] > best) {  // the first of equals: the lowest index of this lane
-        best = key[i];
-        at = i;
+    for (int q = 0; q < TK; ++q) {
+#pragma unroll
+      for (int i = 0; i < PER; ++i) keys[q][i] = 0u;
+      bad[q] = false;
+      if (t0 + q * step < p.tokens) bad[q] = load_keys(p, t0 + q * step, keys[q]);
+    }
+    uint32_t most[TK], mine[TK];  // lane j: choice j
+    int mine_e[TK];
+    float all[TK];
+#pragma unroll
+    for (int q = 0; q < TK; ++q) {
+      bad[q] = __any_sync(0xffffffffu, bad[q]);
+      uint32_t m = 0u;
+#pragma unroll
+      for (int i = 0; i < PER; ++i) {
+        if (bad[q]) keys[q][i] = 0u;  // nothing is chosen
+        m = max(m, keys[q][i]);
       }
-    const uint32_t most = __reduce_max_sync(0xffffffffu, best);
-    if (most == 0u) break;  // no expert with a finite logit is left
-    const uint32_t e = __reduce_min_sync(0xffffffffu, best == most ? (uint32_t)(32 * at + lane) : 0xffffffffu);
-    const uint32_t bits = most & 0x80000000u ? most & 0x7FFFFFFFu : ~most;
-    const float x = __uint_as_float(bits);
-    if (j == 0) {
-      top = x;
-      if (!p.renormalize) {  // over all experts
-        float s = 0.0f;
+      most[q] = __reduce_max_sync(0xffffffffu, m);
+      all[q] = 0.0f;
+      mine[q] = 0u;
+      mine_e[q] = -1;
+    }
+    if (!p.renormalize)  // over all experts
 #pragma unroll
-        for (int i = 0; i < kPer; ++i)
-          if (i < per && key[i] != 0u) {
-            const uint32_t k = key[i];
-            s += expf(__uint_as_float(k & 0x80000000u ? k & 0x7FFFFFFFu : ~k) - top);
-          }
-        sum = warp_sum(s);
+      for (int q = 0; q < TK; ++q) {
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (keys[q][i] != 0u) all[q] += expf(key_value(keys[q][i]) - key_value(most[q]));
+        all[q] = warp_sum(all[q]);
+      }
+    for (int j = 0; j < p.top_k; ++j) {
+#pragma unroll
+      for (int q = 0; q < TK; ++q) {
+        uint32_t best = keys[q][0];
+#pragma unroll
+        for (int i = 1; i < PER; ++i) best = max(best, keys[q][i]);
+        const uint32_t k = __reduce_max_sync(0xffffffffu, best);
+        int e = -1;  // ties: the lowest index
+#pragma unroll
+        for (int i = PER - 1; i >= 0; --i) {
+          const unsigned at = __ballot_sync(0xffffffffu, keys[q][i] == k);
+          if (at != 0u) e = 32 * i + __ffs((int)at) - 1;
+        }
+        if (k == 0u) e = -1;  // no expert that can be chosen is left
+        if (lane == j) {
+          mine[q] = k;
+          mine_e[q] = e;
+        }
+#pragma unroll
+        for (int i = 0; i < PER; ++i)
+          if (e == 32 * i + lane) keys[q][i] = 0u;
       }
     }
-    const float w = expf(x - top);
-    if (p.renormalize) sum += w;
-    if (lane == j) {
-      mine = w;
-      mine_e = (int)e;
-    }
-    if ((int)(e & 31u) == lane) {
 #pragma unroll
-      for (int i = 0; i < kPer; ++i)
-        if (i == (int)(e >> 5)) key[i] = 0u;
+    for (int q = 0; q < TK; ++q) {
+      const int t = t0 + q * step;
+      const float w = mine_e[q] >= 0 ? expf(key_value(mine[q]) - key_value(most[q])) : 0.0f;
+      const float sum = p.renormalize ? warp_sum(w) : all[q];
+      if (t >= p.tokens) continue;
+      if (lane == 0) r.poisoned[t] = bad[q] ? 1 : 0;
+      if (lane < p.top_k) {
+        r.chosen[t * p.top_k + lane] = mine_e[q];
+        r.weight[t * p.top_k + lane] = w / sum;
+      }
     }
   }
-  if (lane < p.top_k) {
-    chosen[lane] = mine_e;
-    weight[lane] = mine / sum;
+}
+
+// The whole routing by the CTA's threads.
+__device__ __forceinline__ void route(const MoeParams& p, const Route& r) {
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int e = (int)threadIdx.x; e < p.experts; e += kThreads) r.mask_of[e] = 0ull;
+  if (p.experts <= 64 && p.tokens <= kThreads / 32) route_tokens<2, 1>(p, r, warp, kThreads / 32);
+  else if (p.experts <= 64) route_tokens<2, 4>(p, r, warp, kThreads / 32);
+  else if (p.experts <= 128) route_tokens<4, 4>(p, r, warp, kThreads / 32);
+  else if (p.experts <= 256) route_tokens<8, 2>(p, r, warp, kThreads / 32);
+  else route_tokens<kMoeMaxExperts / 32, 1>(p, r, warp, kThreads / 32);
+  __syncthreads();
+  for (int i = (int)threadIdx.x; i < p.slots_max; i += kThreads)
+    if (r.chosen[i] >= 0) {
+      const int t = i / p.top_k;
+      atomicOr(reinterpret_cast<unsigned*>(&r.mask_of[r.chosen[i]]) + (t >> 5), 1u << (t & 31));
+    }
+  __syncthreads();
+  if (warp == 0) {  // 32 experts at a time
+    int n = 0, slots = 0;
+    for (int e0 = 0; e0 < p.experts; e0 += 32) {
+      const int e = e0 + lane;
+      const unsigned long long m = e < p.experts ? r.mask_of[e] : 0ull;
+      const unsigned act = __ballot_sync(0xffffffffu, m != 0ull);
+      int c = __popcll(m), before = c;
+#pragma unroll
+      for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, before, d);
+        if (lane >= d) before += o;
+      }
+      if (m != 0ull) {
+        const int a = n + __popc(act & ((1u << lane) - 1u));
+        r.mask[a] = m;
+        r.expert[a] = e;
+        r.base[a] = slots + before - c;
+        r.active_of[e] = a;
+      }
+      n += __popc(act);
+      slots += __shfl_sync(0xffffffffu, before, 31);
+    }
+    if (lane == 0) {
+      r.counts[0] = n;
+      r.counts[1] = slots;
+    }
   }
+  __syncthreads();
+}
+
+// A box of a tensor map into L2.
+__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, int32_t inner, int32_t outer, int32_t product) {
+  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
+               "r"(inner), "r"(outer), "r"(product)
+               : "memory");
 }
 
 // NC: columns of the product, the tokens rounded up to 16, 32 or 64.
 template <int NC>
-__global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_constant__ CUtensorMap mapX,
+__global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_constant__ CUtensorMap mapX,
                                                              const __grid_constant__ CUtensorMap mapG,
                                                              const __grid_constant__ CUtensorMap mapU,
                                                              const __grid_constant__ MoeParams p) {
@@ -166,8 +276,6 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
   __shared__ __align__(8) uint64_t acc_empty[2];
   __shared__ __align__(8) uint64_t scale_full[kChunks], scale_empty[kChunks];
   __shared__ uint32_t tmem_slot;
-  __shared__ int n_active;
-  __shared__ int poisoned[kMoeMaxTokens];
 
   const uint32_t raw_addr = smem_addr(smem_raw);
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
@@ -176,17 +284,10 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
   constexpr int kChunkFloats = kChunkGroups * (NC + 4);  // per group: NC token scales, gate's, up's
   float* chunks = reinterpret_cast<float*>(smem_raw + pad + p.up_stages * stage_bytes);
   float* sums = chunks + kChunks * kChunkFloats;  // [slot of the expert][kPitch]
-  unsigned long long* mask_of =                   // [experts], then the active experts' arrays
-      reinterpret_cast<unsigned long long*>((reinterpret_cast<uintptr_t>(sums + p.tokens * kPitch) + 15) & ~uintptr_t(15));
-  Route r;
-  r.mask = mask_of + p.experts;
-  r.expert = reinterpret_cast<int*>(r.mask + p.active_max);
-  r.base = r.expert + p.active_max;
-  int* chosen = r.base + p.active_max;  // [tokens][top_k]
-  float* weight = reinterpret_cast<float*>(chosen + p.tokens * p.top_k);
-
+  const Route r = route_at(p, sums + p.tokens * kPitch);
+  const int col_tiles = (p.inner + kUpCols - 1) / kUpCols;
+  const int groups = (p.hidden + BK - 1) / BK;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     prefetch_tensormap(&mapX);
     prefetch_tensormap(&mapG);
@@ -203,74 +304,24 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 128);
-  for (int e = (int)threadIdx.x; e < p.experts; e += kThreads) mask_of[e] = 0ull;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // what the stream's kernel before this one wrote
-  // ------------------------------------------------ routing
-  for (int t = warp; t < p.tokens; t += kThreads / 32) {
-    int* ch = chosen + t * p.top_k;
-    float* w = weight + t * p.top_k;
-    if (p.experts <= 64) route_token<2>(p, t, ch, w, &poisoned[t]);
-    else if (p.experts <= 256) route_token<8>(p, t, ch, w, &poisoned[t]);
-    else route_token<kMoeMaxExperts / 32>(p, t, ch, w, &poisoned[t]);
-  }
-  __syncthreads();
-  for (int i = (int)threadIdx.x; i < p.tokens * p.top_k; i += kThreads)
-    if (chosen[i] >= 0) {
-      const int t = i / p.top_k;
-      atomicOr(reinterpret_cast<unsigned*>(&mask_of[chosen[i]]) + (t >> 5), 1u << (t & 31));
+  if (warp == 3 && p.dense) {  // the first item's weights if every expert is active, on their way to L2 while the routing runs
+    const int e = (int)blockIdx.x / col_tiles, c0 = ((int)blockIdx.x % col_tiles) * kUpCols;
+    for (int g = lane; e < p.experts && g < min(groups, kPrefetch); g += 32) {
+      prefetch_box(&mapG, g * BK, c0, e);
+      prefetch_box(&mapU, g * BK, c0, e);
     }
-  __syncthreads();
-  if (warp == 0) {  // active experts in ascending order, 32 at a time
-    int n = 0, slots = 0;
-    for (int e0 = 0; e0 < p.experts; e0 += 32) {
-      const int e = e0 + lane;
-      const unsigned long long m = e < p.experts ? mask_of[e] : 0ull;
-      const unsigned act = __ballot_sync(0xffffffffu, m != 0ull);
-      int c = __popcll(m), before = c;
-#pragma unroll
-      for (int d = 1; d < 32; d <<= 1) {
-        const int o = __shfl_up_sync(0xffffffffu, before, d);
-        if (lane >= d) before += o;
-      }
-      if (m != 0ull) {
-        const int a = n + __popc(act & ((1u << lane) - 1u));
-        r.mask[a] = m;
-        r.expert[a] = e;
-        r.base[a] = slots + before - c;
-      }
-      n += __popc(act);
-      slots += __shfl_sync(0xffffffffu, before, 31);
-    }
-    if (lane == 0) n_active = n;
   }
+  // what the stream's kernel before this one wrote; the second kernel may begin once that is there
+  // too, as it reads the logits on its own
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   tmem_fence_before_sync();
-  __syncthreads();
+  route(p, r);
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  r.n = n_active;
-  if (blockIdx.x == gridDim.x - 1 && warp == 3) {  // the second kernel's copy, by a warp with nothing else to do
-    if (lane == 0) p.route.counts[0] = r.n;
-    for (int a = lane; a < r.n; a += 32) {
-      p.route.expert[a] = r.expert[a];
-      p.route.base[a] = r.base[a];
-      p.route.mask[a] = r.mask[a];
-      unsigned long long m = r.mask[a];
-      for (int j = 0; m != 0ull; ++j, m &= m - 1ull) {
-        const int t = __ffsll((long long)m) - 1;
-        float w = 0.0f;
-        for (int i = 0; i < p.top_k; ++i)
-          if (chosen[t * p.top_k + i] == r.expert[a]) w = weight[t * p.top_k + i];
-        p.route.slot_token[r.base[a] + j] = t;
-        p.route.slot_weight[r.base[a] + j] = w;
-      }
-    }
-    for (int t = lane; t < p.tokens; t += 32) p.route.poisoned[t] = poisoned[t];
-  }
 
-  const int col_tiles = (p.inner + kUpCols - 1) / kUpCols;
-  const int items = r.n * col_tiles;
+  const int items = r.counts[0] * col_tiles;
   const int my_items = (int)blockIdx.x < items ? (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
-  const int groups = (p.hidden + BK - 1) / BK;
 
   if (warp == 0) {
     int t = 0, s = 0;
@@ -472,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_up_kernel(const __grid_consta
 
 // NC: the tokens rounded up to 16, 32 or 64: slots of an expert at most.
 template <int NC>
-__global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_constant__ CUtensorMap mapH,
+__global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_constant__ CUtensorMap mapH,
                                                                const __grid_constant__ CUtensorMap mapD,
                                                                const __grid_constant__ MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -487,20 +538,16 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
   constexpr int stage_bytes = kWTile + 2 * NC * BK;
   constexpr int kChunkFloats = 2 * kChunkGroups * NC + kChunkGroups;  // slots' scales of 16 halves, weights' of 8 units
   constexpr uint32_t kHalfCols = 2 * NC, kAccCols = 4 * NC;           // of an accumulator: a unit's two halves
-  constexpr uint32_t kTmemCols = 2 * kAccCols;
+  constexpr int kBufs = NC == 64 ? 1 : 2;
+  constexpr uint32_t kTmemCols = kBufs * kAccCols;  // at most 256: 128 of an SM's 512 are the first kernel's
   float* chunks = reinterpret_cast<float*>(smem_raw + pad + p.down_stages * stage_bytes);
   float* ysum = chunks + kChunks * kChunkFloats;  // [tokens][128]
-  int* expert = reinterpret_cast<int*>(ysum + p.tokens * 128);
-  int* base = expert + p.active_max;
-  int* slot_token = base + p.active_max;
-  float* slot_weight = reinterpret_cast<float*>(slot_token + p.slots_max);
-
+  const Route r = route_at(p, ysum + p.tokens * 128);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)blockIdx.x % p.split, tile = (int)blockIdx.x / p.split;
   const int l0 = tile * 128;
   const int groups = (p.inner + BK - 1) / BK;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     prefetch_tensormap(&mapH);
     prefetch_tensormap(&mapD);
@@ -516,53 +563,72 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
+  if (warp == 3 && p.dense) {  // as in the first kernel
+    const int u = (int)((int64_t)p.experts * groups * rank / p.split);
+    for (int i = lane; i < kPrefetch && u + i < p.experts * groups; i += 32)
+      prefetch_box(&mapD, (u + i) % groups * BK, l0, (u + i) / groups);
+  }
   for (int i = (int)threadIdx.x; i < p.tokens * 128; i += kThreads) ysum[i] = 0.0f;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // the first kernel's routing and inner values are complete
-  const int n_active = p.route.counts[0];
-  for (int a = (int)threadIdx.x; a < n_active; a += kThreads) {
-    expert[a] = p.route.expert[a];
-    base[a] = p.route.base[a];
-  }
-  const int n_slots =
-      n_active > 0 ? p.route.base[n_active - 1] + __popcll(p.route.mask[n_active - 1]) : 0;
-  for (int i = (int)threadIdx.x; i < n_slots; i += kThreads) {
-    slot_token[i] = p.route.slot_token[i];
-    slot_weight[i] = p.route.slot_weight[i];
-  }
   tmem_fence_before_sync();
-  __syncthreads();
+  route(p, r);  // the logits were complete before the first kernel let this one begin
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_slot;
+  const int n_active = r.counts[0], n_slots = r.counts[1];
+  const int *expert = r.expert, *base = r.base;
+  for (int i = (int)threadIdx.x; i < p.slots_max; i += kThreads)
+    if (r.chosen[i] >= 0) {
+      const int t = i / p.top_k, a = r.active_of[r.chosen[i]];
+      const int slot = base[a] + __popcll(r.mask[a] & ((1ull << t) - 1ull));
+      r.slot_token[slot] = t;
+      r.slot_weight[slot] = r.weight[i];
+    }
+  __syncthreads();
   const int total = n_active * groups;
   const int u0 = (int)((int64_t)total * rank / p.split), u1 = (int)((int64_t)total * (rank + 1) / p.split);
   const int a0 = groups > 0 ? u0 / groups : 0, g_first = u0 - a0 * groups;  // expert and group of the first unit
   const auto slots_of = [&](int a) { return (a + 1 < n_active ? base[a + 1] : n_slots) - base[a]; };
 
   if (warp == 0) {
-    int s = 0, a = a0, g = g_first;
-    uint32_t lap = 0;
-    int t = 0;
-    for (; t < u1 - u0; ++t) {
-      if (lap > 0 && !poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
-        if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
-        break;
-      }
+    // the weights of the first units while the first kernel runs, their inner values when it is done
+    const int ahead = min(p.down_stages, u1 - u0);
+    const auto load = [&](int s, int a, int g, bool weights, bool inner) {
       const int boxes = (slots_of(a) + 15) / 16;  // of 16 slots (32 rows)
       const int e = expert[a], slot = base[a];
       if (elect_one()) {
         const uint32_t bar = smem_addr(&full[s]), at = sbase + (uint32_t)(s * stage_bytes);
-        mbar_arrive_expect_tx(bar, (uint32_t)(kWTile + boxes * 32 * BK));
-        tma_load_3d(at, &mapD, bar, g * BK, l0, e);
-        for (int i = 0; i < boxes; ++i)
-          tma_load_3d(at + kWTile + (uint32_t)(i * 32 * BK), &mapH, bar, g * BK, 2 * (slot + 16 * i), 0);
+        if (weights) {
+          mbar_arrive_expect_tx(bar, (uint32_t)(kWTile + boxes * 32 * BK));
+          tma_load_3d(at, &mapD, bar, g * BK, l0, e);
+        }
+        if (inner)
+          for (int i = 0; i < boxes; ++i)
+            tma_load_3d(at + kWTile + (uint32_t)(i * 32 * BK), &mapH, bar, g * BK, 2 * (slot + 16 * i), 0);
       }
+      __syncwarp();
+    };
+    const auto next = [&](int* a, int* g) {
+      if (++*g == groups) {
+        *g = 0;
+        ++*a;
+      }
+    };
+    int a = a0, g = g_first;
+    for (int t = 0; t < ahead; ++t, next(&a, &g)) load(t, a, g, true, false);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    a = a0;
+    g = g_first;
+    for (int t = 0; t < ahead; ++t, next(&a, &g)) load(t, a, g, false, true);
+    int t = ahead, s = 0;
+    uint32_t lap = 1;
+    for (; t < u1 - u0; ++t, next(&a, &g)) {
+      if (!poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
+        if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+        break;
+      }
+      load(s, a, g, true, true);
       if (++s == p.down_stages) {
         s = 0;
         ++lap;
-      }
-      if (++g == groups) {
-        g = 0;
-        ++a;
       }
     }
     for (int v = t > p.down_stages ? t - p.down_stages : 0; v < t; ++v)
@@ -575,8 +641,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     int t = 0, s = 0, a = a0, g = g_first;
     uint32_t lap = 0;
     for (; t < u1 - u0; ++t) {
-      const int b = t & 1;
-      if ((t >= 2 && !poll_wait(smem_addr(&acc_empty[b]), (uint32_t)((t / 2) - 1) & 1u, p.timeout_ns)) ||
+      const int b = t % kBufs;
+      if ((t >= kBufs && !poll_wait(smem_addr(&acc_empty[b]), (uint32_t)((t / kBufs) - 1) & 1u, p.timeout_ns)) ||
           !poll_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns)) {
         if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
         break;
@@ -607,6 +673,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultDrainWait);
   } else if (warp == 2) {
     // chunks: up to 8 consecutive units of one expert
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t ring = smem_addr(chunks);
     int c = 0, a = a0, g = g_first;
     uint32_t lap = 0;
@@ -650,7 +717,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
     uint32_t s_lap = 0, c_lap = 0;
     int n = 0;
     for (int t = 0; t < u1 - u0; ++t) {
-      const int b = t & 1;
+      const int b = t % kBufs;
       if (left == 0) {
         ok = poll_wait(smem_addr(&scale_full[c]), c_lap & 1u, p.timeout_ns);
         in_chunk = 0;
@@ -708,8 +775,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
           if (j < n) {
-            float& y = ysum[slot_token[base[a] + j] * 128 + row];  // only this thread touches this row
-            y = fmaf(slot_weight[base[a] + j], sum[j], y);
+            float& y = ysum[r.slot_token[base[a] + j] * 128 + row];  // only this thread touches this row
+            y = fmaf(r.slot_weight[base[a] + j], sum[j], y);
           }
           sum[j] = 0.0f;  // those past n too: they may hold what lay behind the expert's rows
         }
@@ -743,7 +810,7 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
 #pragma unroll
     for (int k = 0; k < 8; ++k)
       if (k < p.split) v += u[k];
-    if (p.route.poisoned[tok]) v = __int_as_float(0x7FFFFFFF);
+    if (r.poisoned[tok]) v = __int_as_float(0x7FFFFFFF);
     if (col < p.hidden) {
       const int64_t o = (int64_t)tok * p.ldy + col;
       if (p.bf16) static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
@@ -754,7 +821,8 @@ __global__ void __launch_bounds__(kThreads, 1) moe_down_kernel(const __grid_cons
   cluster_sync();  // no CTA leaves while a peer may read its sums
 }
 
-constexpr size_t kMaxSmem = 227 * 1024 - 2048;  // less the kernels' static arrays
+constexpr size_t kHalfSmem = 112 * 1024;  // a CTA of each kernel per SM
+constexpr size_t kMaxSmem = 222 * 1024;
 
 // f(NC) for the token columns of p.
 template <typename F>
@@ -789,11 +857,17 @@ cudaError_t prepare_fp8_moe() {
   for (int cols = 16; cols <= 64; cols *= 2) {
     const cudaError_t e = f8::with_token_cols(cols, [](auto nc) {
       constexpr int NC = decltype(nc)::value;
-      const cudaError_t up = cudaFuncSetAttribute(f8::moe_up_kernel<NC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                  (int)f8::kMaxSmem);
-      return up != cudaSuccess ? up
-                               : cudaFuncSetAttribute(f8::moe_down_kernel<NC>,
-                                                      cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f8::kMaxSmem);
+      cudaError_t err = cudaSuccess;
+      for (const void* kernel : {reinterpret_cast<const void*>(f8::moe_up_kernel<NC>),
+                                 reinterpret_cast<const void*>(f8::moe_down_kernel<NC>)}) {
+        if (err == cudaSuccess)
+          err = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)f8::kMaxSmem);
+        // all of the SM's memory, so that the second kernel's CTAs find room beside the first's
+        if (err == cudaSuccess)
+          err = cudaFuncSetAttribute(kernel, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                     cudaSharedmemCarveoutMaxShared);
+      }
+      return err;
     });
     if (e != cudaSuccess) return e;
   }
@@ -801,11 +875,19 @@ cudaError_t prepare_fp8_moe() {
 }
 
 void shape_fp8_moe(MoeParams* p, int sm_count) {
-  for (p->up_stages = f8::kMaxStages; p->up_stages > 2 && f8::up_smem(*p) > f8::kMaxSmem;) --p->up_stages;
-  for (p->down_stages = f8::kMaxStages; p->down_stages > 2 && f8::down_smem(*p) > f8::kMaxSmem;) --p->down_stages;
   const int tiles = (p->hidden + 127) / 128;
   p->split = 1;
   while (p->split < 8 && tiles * p->split * 2 <= sm_count) p->split *= 2;
+  // Few units per CTA: half the shared memory each, so that the second kernel's ring is filled while the
+  // first runs.  Many: all of it, as the bytes in flight decide (32 tokens, 64 experts of 2048 x 1024: the
+  // second kernel ran at 3.5 TB/s with 4 stages).
+  const int64_t units = (int64_t)p->active_max * ((p->inner + 127) / 128) / p->split;
+  const size_t most = units > 16 ? f8::kMaxSmem : f8::kHalfSmem;
+  // Twice as many choices as experts: few experts stay without a token, so their weights are sent for
+  // before the routing is known.
+  p->dense = units > 16 && p->slots_max >= 2 * p->experts;
+  for (p->up_stages = f8::kMaxStages; p->up_stages > 2 && f8::up_smem(*p) > most;) --p->up_stages;
+  for (p->down_stages = f8::kMaxStages; p->down_stages > 2 && f8::down_smem(*p) > most;) --p->down_stages;
 }
 
 cudaError_t launch_fp8_moe(const MoeMaps& maps, const MoeParams& p, int sm_count, cudaStream_t stream) {
