@@ -575,6 +575,9 @@ int sgemm_fp8_moe(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts
   const auto place = [&](Pieces* w) {
     p.h = w->take<uint8_t>(2 * (int64_t)p.slots_max * inner);
     p.sh = w->take<float>((int64_t)p.slots_max * p.h_groups);
+    p.arrived = w->take<int>(ceil_div(hidden, 128));
+    p.route = w->take<int>(2 + 2 * (int64_t)p.active_max + 2 * (int64_t)p.slots_max + tokens);
+    p.part = w->take<float>(2 * (int64_t)p.down_grid * tokens * 128);
     x_copy = w->take<uint8_t>(repack_bytes(x));
   };
   Pieces count;

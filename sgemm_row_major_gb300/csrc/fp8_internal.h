@@ -145,8 +145,12 @@ struct MoeParams {
   void* y = nullptr;
   int64_t ldy = 0;
   int bf16 = 0;
-  int up_stages = 0, down_stages = 0, split = 1;
+  int up_stages = 0, down_stages = 0, down_grid = 0;
+  int* arrived = nullptr;                 // [ceil(hidden / 128)] CTAs whose sums are in `part`
+  float* part = nullptr;                  // [2 * down_grid][tokens][128]
+  int many = 0;                           // 1: many units per CTA: the kernels run one after the other
   int dense = 0;                          // 1: nearly every expert will have a token
+  int* route = nullptr;                   // the routing, left by the first kernel where `many`
   int active_max = 0, slots_max = 0;      // bounds of the routing arrays
   uint64_t timeout_ns = 0;
   unsigned* fault = nullptr;
@@ -155,7 +159,7 @@ struct MoeMaps {
   CUtensorMap x, gate, up, h, down;
 };
 cudaError_t prepare_fp8_moe();
-// Fills the launch shape (stages, split) of p.
+// Fills the launch shape (stages, grid) of p.
 void shape_fp8_moe(MoeParams* p, int sm_count);
 cudaError_t launch_fp8_moe(const MoeMaps& maps, const MoeParams& p, int sm_count, cudaStream_t stream);
 

@@ -6,8 +6,9 @@
 // meets all the tokens that need it, as the 128 rows of a tensor-core product whose columns are
 // tokens (16 to 64 of them, so the products cost little beside the loads).
 //
-// Every CTA of both kernels works out the routing from the logits by itself (a warp per token), which
-// costs less than a launch.
+// Every CTA of the first kernel works out the routing from the logits by itself (a warp per token),
+// which costs less than a launch; the second kernel does too where it runs beside the first, and
+// otherwise reads what the first left.
 //
 // moe_up_kernel takes tiles of 64 inner columns of active experts: rows 0-63 of the product are rows of
 // W1_e, rows 64-127 rows of W3_e, the columns all the tokens in order, so x is loaded as it lies and no
@@ -16,9 +17,10 @@
 // 2^-9.8 of the group's largest value.  As the second product is bound by the weights, the doubled
 // columns are free.
 //
-// moe_down_kernel: a cluster of CTAs per 128 rows of the hidden side shares the (expert, 128 inner
-// columns) units in order; each CTA folds its units per expert in FP32 registers, adds them weighted
-// into its tokens' sums in shared memory, and the cluster adds those in rank order into Y.  A CTA of
+// moe_down_kernel shares the (128 rows of the hidden side, expert, 128 inner columns) units evenly, in
+// that order; a CTA folds its units per expert in FP32 registers and adds them weighted into its tokens'
+// sums in shared memory.  Rows of one CTA go to Y; the others' sums go to slots of the workspace, and the
+// last CTA of such rows to arrive adds them in CTA order (which CTA that is does not matter).  A CTA of
 // each kernel fits on an SM beside one of the other, and the second kernel is launched when the first
 // has begun: it routes and fills its ring with W2 meanwhile, and waits for the first kernel only
 // before it loads h (one token: its 17 MB of W2 are then nearly all on chip).
@@ -256,6 +258,31 @@ __device__ __forceinline__ void route(const MoeParams& p, const Route& r) {
     }
   }
   __syncthreads();
+  for (int i = (int)threadIdx.x; i < p.slots_max; i += kThreads)
+    if (r.chosen[i] >= 0) {
+      const int t = i / p.top_k, a = r.active_of[r.chosen[i]];
+      const int slot = r.base[a] + __popcll(r.mask[a] & ((1ull << t) - 1ull));
+      r.slot_token[slot] = t;
+      r.slot_weight[slot] = r.weight[i];
+    }
+  __syncthreads();
+}
+
+// What the second kernel needs of it, to (store) or from the workspace, by `threads` threads.
+__device__ __forceinline__ void copy_route(const MoeParams& p, const Route& r, bool store, int thread, int threads) {
+  const auto copy = [&](int* shared, int* global, int n) {
+    for (int i = thread; i < n; i += threads) {
+      if (store) global[i] = shared[i];
+      else       shared[i] = global[i];
+    }
+  };
+  int* g = p.route;
+  copy(r.counts, g, 2);
+  copy(r.expert, g += 2, p.active_max);
+  copy(r.base, g += p.active_max, p.active_max);
+  copy(r.slot_token, g += p.active_max, p.slots_max);
+  copy(reinterpret_cast<int*>(r.slot_weight), g += p.slots_max, p.slots_max);
+  copy(r.poisoned, g + p.slots_max, p.tokens);
 }
 
 // A box of a tensor map into L2.
@@ -320,6 +347,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_slot;
 
+  if (blockIdx.x == gridDim.x - 1 && warp == 3) {  // by a warp with nothing else to do
+    for (int i = lane; i < (p.hidden + 127) / 128; i += 32) p.arrived[i] = 0;
+    if (p.many) copy_route(p, r, true, lane, 32);
+  }
   const int items = r.counts[0] * col_tiles;
   const int my_items = (int)blockIdx.x < items ? (items - (int)blockIdx.x + (int)gridDim.x - 1) / (int)gridDim.x : 0;
 
@@ -521,6 +552,14 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
   if (warp == 1) tmem_dealloc(tmem, 128);
 }
 
+__device__ __forceinline__ void store_y(const MoeParams& p, int tok, int col, int poisoned, float v) {
+  if (col >= p.hidden) return;
+  if (poisoned) v = __int_as_float(0x7FFFFFFF);
+  const int64_t o = (int64_t)tok * p.ldy + col;
+  if (p.bf16) static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
+  else        static_cast<float*>(p.y)[o] = v;
+}
+
 // NC: the tokens rounded up to 16, 32 or 64: slots of an expert at most.
 template <int NC>
 __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_constant__ CUtensorMap mapH,
@@ -531,6 +570,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   __shared__ __align__(8) uint64_t acc_empty[2];
   __shared__ __align__(8) uint64_t scale_full[kChunks], scale_empty[kChunks];
   __shared__ uint32_t tmem_slot;
+  __shared__ int last_tiles[2], n_last;  // tiles whose last sums are this CTA's (of two that it shares at most)
 
   const uint32_t raw_addr = smem_addr(smem_raw);
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
@@ -544,11 +584,11 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   float* ysum = chunks + kChunks * kChunkFloats;  // [tokens][128]
   const Route r = route_at(p, ysum + p.tokens * 128);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int rank = (int)blockIdx.x % p.split, tile = (int)blockIdx.x / p.split;
-  const int l0 = tile * 128;
+  const int tiles = (p.hidden + 127) / 128;  // of rows
   const int groups = (p.inner + BK - 1) / BK;
 
   if (threadIdx.x == 0) {
+    n_last = 0;
     prefetch_tensormap(&mapH);
     prefetch_tensormap(&mapD);
     for (int s = 0; s < p.down_stages; ++s) {
@@ -564,68 +604,77 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   }
   if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
   if (warp == 3 && p.dense) {  // as in the first kernel
-    const int u = (int)((int64_t)p.experts * groups * rank / p.split);
-    for (int i = lane; i < kPrefetch && u + i < p.experts * groups; i += 32)
-      prefetch_box(&mapD, (u + i) % groups * BK, l0, (u + i) / groups);
+    const int64_t all = (int64_t)p.experts * groups, u = all * tiles * blockIdx.x / gridDim.x;
+    for (int64_t v = u + lane; v < min(u + kPrefetch, all * tiles); v += 32)
+      prefetch_box(&mapD, (int)(v % groups) * BK, (int)(v / all) * 128, (int)(v % all / groups));
   }
   for (int i = (int)threadIdx.x; i < p.tokens * 128; i += kThreads) ysum[i] = 0.0f;
   tmem_fence_before_sync();
-  route(p, r);  // the logits were complete before the first kernel let this one begin
+  if (p.many) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    copy_route(p, r, false, (int)threadIdx.x, kThreads);
+    __syncthreads();
+  } else {
+    route(p, r);  // the logits were complete before the first kernel let this one begin
+  }
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_slot;
   const int n_active = r.counts[0], n_slots = r.counts[1];
   const int *expert = r.expert, *base = r.base;
-  for (int i = (int)threadIdx.x; i < p.slots_max; i += kThreads)
-    if (r.chosen[i] >= 0) {
-      const int t = i / p.top_k, a = r.active_of[r.chosen[i]];
-      const int slot = base[a] + __popcll(r.mask[a] & ((1ull << t) - 1ull));
-      r.slot_token[slot] = t;
-      r.slot_weight[slot] = r.weight[i];
+  // this CTA's units: [u0, u0 + mine) of tiles x active experts x groups
+  const int64_t per_tile = (int64_t)n_active * groups, total = per_tile * tiles;
+  const int ctas = (int)max((int64_t)1, min((int64_t)gridDim.x, total));  // that have units: one at least each
+  const auto bound = [&](int c) { return total * min(c, ctas) / ctas; };
+  const int64_t u0 = bound((int)blockIdx.x);
+  const int mine = (int)(bound((int)blockIdx.x + 1) - u0);
+  struct Place {  // of a unit: row tile, active expert, group
+    int tile, a, g;
+  };
+  const Place first = {per_tile > 0 ? (int)(u0 / per_tile) : 0, per_tile > 0 ? (int)(u0 % per_tile) / groups : 0,
+                       per_tile > 0 ? (int)(u0 % per_tile) % groups : 0};
+  const auto next = [&](Place* u) {
+    if (++u->g == groups) {
+      u->g = 0;
+      if (++u->a == n_active) {
+        u->a = 0;
+        ++u->tile;
+      }
     }
-  __syncthreads();
-  const int total = n_active * groups;
-  const int u0 = (int)((int64_t)total * rank / p.split), u1 = (int)((int64_t)total * (rank + 1) / p.split);
-  const int a0 = groups > 0 ? u0 / groups : 0, g_first = u0 - a0 * groups;  // expert and group of the first unit
+  };
   const auto slots_of = [&](int a) { return (a + 1 < n_active ? base[a + 1] : n_slots) - base[a]; };
 
   if (warp == 0) {
     // the weights of the first units while the first kernel runs, their inner values when it is done
-    const int ahead = min(p.down_stages, u1 - u0);
-    const auto load = [&](int s, int a, int g, bool weights, bool inner) {
-      const int boxes = (slots_of(a) + 15) / 16;  // of 16 slots (32 rows)
-      const int e = expert[a], slot = base[a];
+    const int ahead = min(p.down_stages, mine);
+    const auto load = [&](int s, const Place& u, bool weights, bool inner) {
+      const int boxes = (slots_of(u.a) + 15) / 16;  // of 16 slots (32 rows)
+      const int e = expert[u.a], slot = base[u.a];
       if (elect_one()) {
         const uint32_t bar = smem_addr(&full[s]), at = sbase + (uint32_t)(s * stage_bytes);
         if (weights) {
           mbar_arrive_expect_tx(bar, (uint32_t)(kWTile + boxes * 32 * BK));
-          tma_load_3d(at, &mapD, bar, g * BK, l0, e);
+          tma_load_3d(at, &mapD, bar, u.g * BK, u.tile * 128, e);
         }
         if (inner)
           for (int i = 0; i < boxes; ++i)
-            tma_load_3d(at + kWTile + (uint32_t)(i * 32 * BK), &mapH, bar, g * BK, 2 * (slot + 16 * i), 0);
+            tma_load_3d(at + kWTile + (uint32_t)(i * 32 * BK), &mapH, bar, u.g * BK, 2 * (slot + 16 * i), 0);
       }
       __syncwarp();
     };
-    const auto next = [&](int* a, int* g) {
-      if (++*g == groups) {
-        *g = 0;
-        ++*a;
-      }
-    };
-    int a = a0, g = g_first;
-    for (int t = 0; t < ahead; ++t, next(&a, &g)) load(t, a, g, true, false);
+    Place u = first;
+    if (!p.many)
+      for (int t = 0; t < ahead; ++t, next(&u)) load(t, u, true, false);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    a = a0;
-    g = g_first;
-    for (int t = 0; t < ahead; ++t, next(&a, &g)) load(t, a, g, false, true);
+    u = first;
+    for (int t = 0; t < ahead; ++t, next(&u)) load(t, u, p.many != 0, true);
     int t = ahead, s = 0;
     uint32_t lap = 1;
-    for (; t < u1 - u0; ++t, next(&a, &g)) {
+    for (; t < mine; ++t, next(&u)) {
       if (!poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
         if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
         break;
       }
-      load(s, a, g, true, true);
+      load(s, u, true, true);
       if (++s == p.down_stages) {
         s = 0;
         ++lap;
@@ -638,16 +687,17 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
     // a unit's two halves of 64 inner columns have scales, and so columns of the accumulator, of their own
     constexpr uint32_t step = 32u >> 4;
     const uint32_t desc0 = desc_lo(sbase);
-    int t = 0, s = 0, a = a0, g = g_first;
+    int t = 0, s = 0;
+    Place u = first;
     uint32_t lap = 0;
-    for (; t < u1 - u0; ++t) {
+    for (; t < mine; ++t, next(&u)) {
       const int b = t % kBufs;
       if ((t >= kBufs && !poll_wait(smem_addr(&acc_empty[b]), (uint32_t)((t / kBufs) - 1) & 1u, p.timeout_ns)) ||
           !poll_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns)) {
         if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
         break;
       }
-      const uint32_t idesc = moe_idesc(32 * ((slots_of(a) + 15) / 16));
+      const uint32_t idesc = moe_idesc(32 * ((slots_of(u.a) + 15) / 16));
       tmem_fence_after_sync();
       if (elect_one()) {
         const uint32_t wd = desc0 + (uint32_t)(s * (stage_bytes >> 4)), hd = wd + (kWTile >> 4);
@@ -662,10 +712,6 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
         s = 0;
         ++lap;
       }
-      if (++g == groups) {
-        g = 0;
-        ++a;
-      }
     }
     bool ok = true;  // every product has completed, and its commit has landed, before the CTA ends
     for (int u = t > p.down_stages ? t - p.down_stages : 0; u < t; ++u)
@@ -675,30 +721,28 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
     // chunks: up to 8 consecutive units of one expert
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint32_t ring = smem_addr(chunks);
-    int c = 0, a = a0, g = g_first;
+    int c = 0;
+    Place u = first;
     uint32_t lap = 0;
-    for (int t = 0; t < u1 - u0;) {
+    for (int t = 0; t < mine;) {
       if (lap > 0 && !poll_wait(smem_addr(&scale_empty[c]), (lap - 1) & 1u, p.timeout_ns)) {
         if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
         break;
       }
-      const int count = min(min(kChunkGroups, groups - g), u1 - u0 - t);
+      const int count = min(min(kChunkGroups, groups - u.g), mine - t);
       const uint32_t dst = ring + 4u * (uint32_t)(c * kChunkFloats);
-      const int n = slots_of(a), halves = min(2 * count, p.h_groups - 2 * g);
+      const int n = slots_of(u.a), halves = min(2 * count, p.h_groups - 2 * u.g);
       for (int j = lane; j < n; j += 32) {
-        const float* src = p.sh + (int64_t)(base[a] + j) * p.h_groups + 2 * g;
+        const float* src = p.sh + (int64_t)(base[u.a] + j) * p.h_groups + 2 * u.g;
         for (int h = 0; h < halves; ++h) copy4_async(dst + 4u * (uint32_t)(h * NC + j), src + h);
       }
       if (lane < count)
         copy4_async(dst + 4u * (uint32_t)(2 * kChunkGroups * NC + lane),
-                    p.sd + (int64_t)expert[a] * p.stride_sd + (int64_t)(l0 >> 7) * p.ldsd + g + lane);
+                    p.sd + (int64_t)expert[u.a] * p.stride_sd + (int64_t)u.tile * p.ldsd + u.g + lane);
       copies_arrive(smem_addr(&scale_full[c]));
       t += count;
-      g += count;
-      if (g == groups) {
-        g = 0;
-        ++a;
-      }
+      u.g += count - 1;
+      next(&u);
       if (++c == kChunks) {
         c = 0;
         ++lap;
@@ -713,112 +757,172 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
 #pragma unroll
     for (int j = 0; j < NC; ++j) sum[j] = 0.0f;
     bool ok = true;
-    int s = 0, c = 0, a = a0, g = g_first, in_chunk = 0, left = 0;  // left: units of the chunk
+    int s = 0, c = 0, b = 0;
+    Place u = first;
     uint32_t s_lap = 0, c_lap = 0;
-    int n = 0;
-    for (int t = 0; t < u1 - u0; ++t) {
-      const int b = t % kBufs;
-      if (left == 0) {
-        ok = poll_wait(smem_addr(&scale_full[c]), c_lap & 1u, p.timeout_ns);
-        in_chunk = 0;
-        left = min(min(kChunkGroups, groups - g), u1 - u0 - t);
-        n = slots_of(a);
-      }
-      ok = ok && poll_wait(smem_addr(&done[s]), s_lap & 1u, p.timeout_ns);
-      if (!ok) {
-        if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
-        break;
-      }
-      tmem_fence_after_sync();
-      const float* sc = chunks + c * kChunkFloats + 2 * in_chunk * NC;
-      const float w = chunks[c * kChunkFloats + 2 * kChunkGroups * NC + in_chunk];
-      const bool second = 2 * g + 1 < p.h_groups;  // the unit has a second half
-      const uint32_t acc = tq + (uint32_t)b * kAccCols;
-      // 8 slots of both halves at a time: hi, lo, hi, lo, ...
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the counters of arrivals are the first kernel's
+    if (total == 0)  // no token chose anything
+      for (int tile = (int)blockIdx.x; tile < tiles; tile += (int)gridDim.x)
+        for (int t = 0; t < p.tokens; ++t) store_y(p, t, tile * 128 + row, r.poisoned[t], 0.0f);
+    for (int t = 0; t < mine;) {
+      // a chunk of units of one expert, whose slots are rounded up to NS (with their number at run time
+      // the fold took 1400 cycles a unit)
+      const int count = min(min(kChunkGroups, groups - u.g), mine - t), n = slots_of(u.a);
+      ok = ok && poll_wait(smem_addr(&scale_full[c]), c_lap & 1u, p.timeout_ns);
+      const bool flush = t + count == mine || u.g + count == groups;  // the expert's last units here
+      const auto run = [&](auto slots) {
+        constexpr int NS = decltype(slots)::value;
+        const float* sc = chunks + c * kChunkFloats;
+        for (int i = 0; ok && i < count; ++i, sc += 2 * NC) {
+          ok = poll_wait(smem_addr(&done[s]), s_lap & 1u, p.timeout_ns);
+          if (!ok) break;
+          tmem_fence_after_sync();
+          const uint32_t acc = tq + (uint32_t)b * kAccCols;
+          const float w = chunks[c * kChunkFloats + 2 * kChunkGroups * NC + i];
+          const float w2 = 2 * (u.g + i) + 1 < p.h_groups ? w : 0.0f;  // the second half may be past the end
 #pragma unroll
-      for (int j0 = 0; j0 < NC; j0 += 8) {
-        if (j0 < n) {
-          float x[2][16];
-          tmem_ld16(acc + (uint32_t)(2 * j0), x[0]);
-          tmem_ld16(acc + kHalfCols + (uint32_t)(2 * j0), x[1]);
-          tmem_wait_ld();
-          if (j0 + 8 >= n) {
-            tmem_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&acc_empty[b]));
-          }
-          tmem_ld_ready(x[0]);
-          tmem_ld_ready(x[1]);
+          for (int j0 = 0; j0 < NS; j0 += 8) {  // 8 slots of both halves: hi, lo, hi, lo, ...
+            float x[2][16];
+            tmem_ld16(acc + (uint32_t)(2 * j0), x[0]);
+            tmem_ld16(acc + kHalfCols + (uint32_t)(2 * j0), x[1]);
+            float4 f[2][2];
 #pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float v = fmaf(x[0][2 * j + 1], 1.0f / kLoScale, x[0][2 * j]) * sc[j0 + j];
-            if (second) v = fmaf(fmaf(x[1][2 * j + 1], 1.0f / kLoScale, x[1][2 * j]), sc[NC + j0 + j], v);
-            sum[j0 + j] = fmaf(v, w, sum[j0 + j]);
-          }
-        }
-      }
-      ++in_chunk;
-      if (--left == 0) {
-        __syncwarp();
-        if (lane == 0) mbar_arrive(smem_addr(&scale_empty[c]));
-        if (++c == kChunks) {
-          c = 0;
-          ++c_lap;
-        }
-      }
-      if (++s == p.down_stages) {
-        s = 0;
-        ++s_lap;
-      }
-      const bool last = ++g == groups;
-      if (last || t + 1 == u1 - u0) {  // the expert's last unit here
+            for (int k = 0; k < 2; ++k) {
+              f[0][k] = *reinterpret_cast<const float4*>(sc + j0 + 4 * k);
+              f[1][k] = *reinterpret_cast<const float4*>(sc + NC + j0 + 4 * k);
+            }
+            tmem_wait_ld();
+            if (j0 + 8 == NS) {
+              tmem_fence_before_sync();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_addr(&acc_empty[b]));
+            }
+            tmem_ld_ready(x[0]);
+            tmem_ld_ready(x[1]);
+            const float f0[8] = {f[0][0].x, f[0][0].y, f[0][0].z, f[0][0].w, f[0][1].x, f[0][1].y, f[0][1].z, f[0][1].w};
+            const float f1[8] = {f[1][0].x, f[1][0].y, f[1][0].z, f[1][0].w, f[1][1].x, f[1][1].y, f[1][1].z, f[1][1].w};
 #pragma unroll
-        for (int j = 0; j < NC; ++j) {
-          if (j < n) {
-            float& y = ysum[r.slot_token[base[a] + j] * 128 + row];  // only this thread touches this row
-            y = fmaf(r.slot_weight[base[a] + j], sum[j], y);
+            for (int j = 0; j < 8; ++j) {
+              const float v0 = fmaf(x[0][2 * j + 1], 1.0f / kLoScale, x[0][2 * j]);
+              const float v1 = fmaf(x[1][2 * j + 1], 1.0f / kLoScale, x[1][2 * j]);
+              sum[j0 + j] = fmaf(v0 * f0[j], w, sum[j0 + j]);
+              if (w2 != 0.0f) sum[j0 + j] = fmaf(v1 * f1[j], w2, sum[j0 + j]);
+            }
           }
-          sum[j] = 0.0f;  // those past n too: they may hold what lay behind the expert's rows
+          if (++b == kBufs) b = 0;
+          if (++s == p.down_stages) {
+            s = 0;
+            ++s_lap;
+          }
         }
-        if (last) {
-          g = 0;
-          ++a;
+        if (flush) {
+          const int slot = base[u.a];
+#pragma unroll
+          for (int j0 = 0; j0 < NS; j0 += 8) {
+            float* y[8];
+            float v[8], cw[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const bool in = j0 + j < n;
+              y[j] = &ysum[(in ? r.slot_token[slot + j0 + j] : 0) * 128 + row];  // only this thread touches this row
+              cw[j] = in ? r.slot_weight[slot + j0 + j] : 0.0f;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] = *y[j];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              if (j0 + j < n) *y[j] = fmaf(cw[j], sum[j0 + j], v[j]);  // an expert's tokens differ
+              sum[j0 + j] = 0.0f;  // those past n too: they may hold what lay behind the expert's rows
+            }
+          }
         }
+      };
+      if (n <= 8) run(std::integral_constant<int, 8>{});
+      else if (n <= 16) run(std::integral_constant<int, 16>{});
+      else if (NC >= 32 && n <= 32) run(std::integral_constant<int, NC >= 32 ? 32 : 16>{});
+      else run(std::integral_constant<int, NC>{});
+      if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);  // (the barriers below are met all the same)
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_addr(&scale_empty[c]));
+      if (++c == kChunks) {
+        c = 0;
+        ++c_lap;
+      }
+      t += count;
+      u.g += count - 1;
+      const Place at = u;
+      next(&u);
+      const bool end = t == mine;
+      if (end || u.tile != at.tile) {  // the tile's last unit here: Y, or a slot
+        const int64_t t0 = at.tile * per_tile, t1 = t0 + per_tile;
+        const int col = at.tile * 128 + row;
+        if (u0 <= t0 && u0 + mine >= t1) {
+          for (int tok = 0; tok < p.tokens; ++tok) store_y(p, tok, col, r.poisoned[tok], ysum[tok * 128 + row]);
+        } else {
+          // CTAs c0 .. c1 share the tile; one that began before it uses its first slot for it, one that began
+          // in it its second
+          const int c0 = (int)(((t0 + 1) * ctas + total - 1) / total - 1), c1 = (int)((t1 * ctas + total - 1) / total - 1);
+          float* to = p.part + (2 * (int64_t)blockIdx.x + (u0 < t0 ? 0 : 1)) * p.tokens * 128 + row;
+          for (int tok = 0; tok < p.tokens; ++tok) to[tok * 128] = ysum[tok * 128 + row];
+          __threadfence();
+          fold_barrier();
+          if (threadIdx.x == kFirstFold * 32 && atomicAdd(&p.arrived[at.tile], 1) == c1 - c0)
+            last_tiles[n_last++] = at.tile;  // the others' sums are there
+        }
+        for (int tok = 0; tok < p.tokens; ++tok) ysum[tok * 128 + row] = 0.0f;
       }
     }
   }
-
-  // ------------------------------------------------ the CTAs' sums, added in rank order
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
-  __syncwarp();
-  cluster_sync();
-  const uint32_t y_addr = smem_addr(ysum);
-  const int t0 = p.tokens * 128 * rank / p.split, t1 = p.tokens * 128 * (rank + 1) / p.split;
-  for (int i = t0 + (int)threadIdx.x; i < t1; i += kThreads) {
-    const int tok = i >> 7, col = l0 + (i & 127);
-    float u[8], v = 0.0f;
+
+  // ------------------------------------------------ the slots of such tiles, added in CTA order: a warp
+  // per token, four rows a lane, the loads of eight slots of two tokens in flight
+  for (int i = 0; i < n_last; ++i) {
+    __threadfence();
+    const int tile = last_tiles[i];
+    const int64_t t0 = tile * per_tile, t1 = t0 + per_tile;
+    const int c0 = (int)(((t0 + 1) * ctas + total - 1) / total - 1), c1 = (int)((t1 * ctas + total - 1) / total - 1);
+    const int64_t slot = (int64_t)p.tokens * 128;
+    const float* from = p.part + (2 * (int64_t)c0 + 1) * slot + 4 * lane;
+    const int64_t back = bound(c0) < t0 ? -slot : 0;  // only c0 can have begun before the tile
+    for (int tok0 = warp; tok0 < p.tokens; tok0 += 2 * (kThreads / 32)) {
+      float4 v[2];
+      v[0] = v[1] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      for (int k0 = 0; k0 <= c1 - c0; k0 += 8) {
+        float4 x[2][8];
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < p.split)
-        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                     : "=f"(u[k])
-                     : "r"(map_to_rank(y_addr + 4u * (uint32_t)i, (uint32_t)k))
-                     : "memory");
+        for (int q = 0; q < 2; ++q)
 #pragma unroll
-    for (int k = 0; k < 8; ++k)
-      if (k < p.split) v += u[k];
-    if (r.poisoned[tok]) v = __int_as_float(0x7FFFFFFF);
-    if (col < p.hidden) {
-      const int64_t o = (int64_t)tok * p.ldy + col;
-      if (p.bf16) static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
-      else        static_cast<float*>(p.y)[o] = v;
+          for (int k = 0; k < 8; ++k) {
+            const int tok = tok0 + q * (kThreads / 32);
+            x[q][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            if (k0 + k <= c1 - c0 && tok < p.tokens)
+              x[q][k] = __ldcg(reinterpret_cast<const float4*>(from + 2 * (k0 + k) * slot + (k0 + k == 0 ? back : 0) + tok * 128));
+          }
+#pragma unroll
+        for (int q = 0; q < 2; ++q)
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            v[q].x += x[q][k].x;
+            v[q].y += x[q][k].y;
+            v[q].z += x[q][k].z;
+            v[q].w += x[q][k].w;
+          }
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const int tok = tok0 + q * (kThreads / 32), col = tile * 128 + 4 * lane;
+        if (tok >= p.tokens) continue;
+        store_y(p, tok, col, r.poisoned[tok], v[q].x);
+        store_y(p, tok, col + 1, r.poisoned[tok], v[q].y);
+        store_y(p, tok, col + 2, r.poisoned[tok], v[q].z);
+        store_y(p, tok, col + 3, r.poisoned[tok], v[q].w);
+      }
     }
   }
-  __syncthreads();
-  cluster_sync();  // no CTA leaves while a peer may read its sums
 }
 
 constexpr size_t kHalfSmem = 112 * 1024;  // a CTA of each kernel per SM
@@ -832,21 +936,17 @@ cudaError_t with_token_cols(int cols, const F& f) {
                       : f(std::integral_constant<int, 64>{});
 }
 
-cudaError_t launch_pdl(const void* kernel, int grid, int cluster, size_t smem, void** args, cudaStream_t stream) {
+cudaError_t launch_pdl(const void* kernel, int grid, size_t smem, void** args, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)grid);
   cfg.blockDim = dim3(kThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = stream;
-  cudaLaunchAttribute attr[2];
+  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  attr[1].id = cudaLaunchAttributeClusterDimension;
-  attr[1].val.clusterDim.x = (unsigned)cluster;
-  attr[1].val.clusterDim.y = 1;
-  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 2;
+  cfg.numAttrs = 1;
   return cudaLaunchKernelExC(&cfg, kernel, args);
 }
 
@@ -875,17 +975,17 @@ cudaError_t prepare_fp8_moe() {
 }
 
 void shape_fp8_moe(MoeParams* p, int sm_count) {
-  const int tiles = (p->hidden + 127) / 128;
-  p->split = 1;
-  while (p->split < 8 && tiles * p->split * 2 <= sm_count) p->split *= 2;
+  const int64_t units = (int64_t)p->active_max * ((p->inner + 127) / 128) * ((p->hidden + 127) / 128);
+  p->down_grid = (int)std::min<int64_t>(sm_count, units);
   // Few units per CTA: half the shared memory each, so that the second kernel's ring is filled while the
   // first runs.  Many: all of it, as the bytes in flight decide (32 tokens, 64 experts of 2048 x 1024: the
   // second kernel ran at 3.5 TB/s with 4 stages).
-  const int64_t units = (int64_t)p->active_max * ((p->inner + 127) / 128) / p->split;
-  const size_t most = units > 16 ? f8::kMaxSmem : f8::kHalfSmem;
+  const bool many = units > 20 * (int64_t)sm_count;
+  const size_t most = many ? f8::kMaxSmem : f8::kHalfSmem;
   // Twice as many choices as experts: few experts stay without a token, so their weights are sent for
   // before the routing is known.
-  p->dense = units > 16 && p->slots_max >= 2 * p->experts;
+  p->many = many;
+  p->dense = many && p->slots_max >= 2 * p->experts;
   for (p->up_stages = f8::kMaxStages; p->up_stages > 2 && f8::up_smem(*p) > most;) --p->up_stages;
   for (p->down_stages = f8::kMaxStages; p->down_stages > 2 && f8::down_smem(*p) > most;) --p->down_stages;
 }
@@ -898,12 +998,12 @@ cudaError_t launch_fp8_moe(const MoeMaps& maps, const MoeParams& p, int sm_count
     CUtensorMap x = maps.x, g = maps.gate, u = maps.up, h = maps.h, d = maps.down;
     MoeParams q = p;
     void* up_args[] = {&x, &g, &u, &q};
-    const cudaError_t e = f8::launch_pdl(reinterpret_cast<const void*>(f8::moe_up_kernel<NC>), grid, 1, f8::up_smem(p),
-                                         up_args, stream);
+    const cudaError_t e = f8::launch_pdl(reinterpret_cast<const void*>(f8::moe_up_kernel<NC>), grid, f8::up_smem(p), up_args,
+                                         stream);
     if (e != cudaSuccess) return e;
     void* down_args[] = {&h, &d, &q};
-    return f8::launch_pdl(reinterpret_cast<const void*>(f8::moe_down_kernel<NC>), (p.hidden + 127) / 128 * p.split,
-                          p.split, f8::down_smem(p), down_args, stream);
+    return f8::launch_pdl(reinterpret_cast<const void*>(f8::moe_down_kernel<NC>), p.down_grid, f8::down_smem(p), down_args,
+                          stream);
   });
 }
 

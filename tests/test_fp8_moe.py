@@ -84,7 +84,7 @@ def check(T, E, k, H, I, seed, renormalize=True, bf16=True, logits=None, pad=0):
 @pytest.mark.gpu
 @pytest.mark.parametrize("T,E,k,H,I", [(1, 1, 1, 16, 16), (1, 8, 2, 128, 128), (1, 64, 8, 512, 256), (2, 5, 5, 144, 208), (7, 16, 3, 400, 336),
                                        (16, 8, 2, 256, 1040), (17, 40, 6, 656, 64), (33, 12, 4, 384, 192), (64, 128, 8, 256, 128),
-                                       (64, 2, 2, 1040, 144), (5, 1000, 16, 128, 128)])
+                                       (64, 2, 2, 1040, 144), (5, 1000, 16, 128, 128), (33, 26, 4, 2048, 1024), (3, 26, 4, 2048, 1024)])
 @pytest.mark.parametrize("renormalize", [True, False])
 def test_against_the_formula(T, E, k, H, I, renormalize):
     check(T, E, k, H, I, T + E + k, renormalize, bf16=renormalize)
