@@ -37,8 +37,8 @@ enum sgemm_type { SGEMM_F32 = 0, SGEMM_BF16 = 1 };
  * numbers follow those of enum sgemm_variant, whose NONE and SCALE are reported too). */
 enum sgemm_fp8_variant {
     SGEMM_VARIANT_FP8_PAIR = 32,  /* CTA pairs, 256 x tile_n tiles (tile_n 64, 128 or 256), 128 k per tile */
-    SGEMM_VARIANT_FP8_SHORT = 33  /* one CTA per 128 x tile_n tile (128 along the longer of M and N, tile_n <= 128
-                                     along the other), K shared by a cluster of split_k CTAs */
+    SGEMM_VARIANT_FP8_SHORT = 33  /* one CTA per 128 x tile_n tile (128 along the longer of M and N, tile_n 16, 32,
+                                     64 or 128 along the other), K shared by a cluster of split_k CTAs */
 };
 
 /* A stored 8-bit matrix (its row and column counts come from the call). */

@@ -108,25 +108,54 @@ int64_t repack_bytes(const Operand& o) {
   return aligned(o.m->data, 16) && o.m->ld % 16 == 0 ? 0 : round256(o.rows * repack_ld(o));
 }
 
-// Pair kernel: the tile width whose rounds of tiles over the clusters cost least.  A group of 128 k
-// costs a tile tile_n / 256 of the tensor cores' time plus what does not shrink with it (the rows
-// of A, the barriers' round trips).
-constexpr int kPairFixedCols = 64;
-int pair_tile_n(int64_t M, int64_t N, int64_t clusters) {
-  int best = 256;
-  int64_t best_cost = INT64_MAX;
-  for (int n : kFp8PairTiles) {
-    const int64_t rounds = ceil_div(ceil_div(M, 256) * ceil_div(N, n), clusters);
-    const int64_t cost = rounds * (n + kPairFixedCols);
-    if (cost < best_cost) {
-      best_cost = cost;
-      best = n;
+// Times in ns that the choice of kernel goes by (measured on a GB300, to a few per cent): a group of
+// 128 k and the rest of a tile in the pair kernel, by tile width; a group in a short-side CTA that has
+// its SM to itself; and what a launch takes apart from its groups.
+struct TileCost {
+  int tile, group_ns, tile_ns;
+};
+constexpr TileCost kPairCost[] = {{256, 430, 1000}, {128, 310, 600}, {64, 270, 400}};
+constexpr TileCost kPairColsCost[] = {{256, 680, 1500}, {128, 440, 900}, {64, 310, 600}};  // B scaled by column
+constexpr TileCost kShortCost[] = {{16, 310, 0}, {32, 330, 0}, {64, 460, 0}, {128, 680, 0}};
+constexpr double kPairLaunchNs = 4000, kShortLaunchNs = 4500;
+constexpr double kSmBytesPerNs = 44.7;  // an SM's share of the memory bandwidth
+
+int64_t short_ring(int tile) { return (tile == 128 ? 2 : 1) * 98 * 1024; }  // stages of two CTAs (one) per SM
+int short_ctas_per_sm(int tile) { return tile == 128 ? 1 : 2; }
+
+struct Choice {
+  int variant = 0, tile = 0, split = 1;
+  double ns = 1e30;
+};
+
+// The cheapest launch of a product, among the variant, tile and split that are forced (0: any).
+Choice choose(const Product& pr, int64_t clusters, int sm_count, int variant, int tile, int split) {
+  const int64_t groups = ceil_div(pr.K, 128), S = std::min(pr.M, pr.N), L = std::max(pr.M, pr.N);
+  Choice best;
+  const auto offer = [&](int v, int n, int k, double ns) {
+    if (ns < best.ns) best = Choice{v, n, k, ns};
+  };
+  if (variant != SGEMM_VARIANT_FP8_SHORT)
+    for (const TileCost& c : pr.b.scales.shift == 0 ? kPairColsCost : kPairCost) {
+      if (tile != 0 && tile != c.tile) continue;
+      const int64_t rounds = ceil_div(ceil_div(pr.M, 256) * ceil_div(pr.N, c.tile), clusters);
+      offer(SGEMM_VARIANT_FP8_PAIR, c.tile, 1, kPairLaunchNs + (double)rounds * (groups * c.group_ns + c.tile_ns));
     }
-  }
+  if (variant != SGEMM_VARIANT_FP8_PAIR)
+    for (const TileCost& c : kShortCost) {
+      if (tile != 0 ? tile != c.tile : c.tile < 128 && S > c.tile) continue;  // the narrowest that holds the short side
+      const int64_t tiles = ceil_div(L, 128) * ceil_div(S, c.tile), slots = (int64_t)sm_count * short_ctas_per_sm(c.tile);
+      for (int k = 1; k <= 8; k *= 2) {
+        if (split != 0 ? split != k : k > 1 && groups < 2 * k) continue;  // two groups per CTA at least
+        const double on_sm = std::min((double)short_ctas_per_sm(c.tile), std::max(1.0, (double)tiles * k / sm_count));
+        const double group = std::max<double>(c.group_ns, on_sm * (16384 + 64 * c.tile) / kSmBytesPerNs);
+        offer(SGEMM_VARIANT_FP8_SHORT, c.tile, k,
+              kShortLaunchNs + (double)ceil_div(tiles * k, slots) * ceil_div(groups, k) * group);
+      }
+      if (tile == 0) break;
+    }
   return best;
 }
-
-constexpr int64_t kShortRing = 108 * 1024;  // two CTAs per SM
 
 int plan_product(const Product& pr, int sm_count, int pair_clusters, sgemm_plan_t* plan) {
   *plan = sgemm_plan_t{};
@@ -146,9 +175,8 @@ int plan_product(const Product& pr, int sm_count, int pair_clusters, sgemm_plan_
   const int64_t clusters = pair_clusters > 0 ? pair_clusters : std::max(1, sm_count / 2);
   const int64_t groups = ceil_div(pr.K, 128);
   const int64_t S = std::min(pr.M, pr.N), L = std::max(pr.M, pr.N);
-  int variant = g_force_variant.load();
-  if (variant == SGEMM_VARIANT_AUTO) variant = S <= 128 ? SGEMM_VARIANT_FP8_SHORT : SGEMM_VARIANT_FP8_PAIR;
-  const int force_tile = g_force_tile.load(), force_split = g_force_split.load();
+  const Choice choice = choose(pr, clusters, sm_count, g_force_variant.load(), g_force_tile.load(), g_force_split.load());
+  const int variant = choice.variant;
   plan->variant = variant;
   plan->tile_k = 128;
   plan->kernel_launches = 1;
@@ -157,7 +185,7 @@ int plan_product(const Product& pr, int sm_count, int pair_clusters, sgemm_plan_
   int64_t tiles;
   if (variant == SGEMM_VARIANT_FP8_PAIR) {
     plan->tile_m = 256;
-    plan->tile_n = force_tile ? force_tile : pair_tile_n(pr.M, pr.N, clusters);
+    plan->tile_n = choice.tile;
     plan->stages = kFp8PairStages;
     plan->threads = kFp8PairThreads;
     plan->smem_bytes = fp8_pair_smem(pr.b.scales.shift == 0);
@@ -165,20 +193,15 @@ int plan_product(const Product& pr, int sm_count, int pair_clusters, sgemm_plan_
     plan->grid_x = 2 * std::min<int64_t>(tiles, clusters);
   } else {
     const Operand& s_op = pr.M <= pr.N ? pr.a : pr.b;
-    const int64_t tiles_s = ceil_div(S, kFp8ShortMaxTile);
     plan->tile_m = 128;
-    plan->tile_n = force_tile ? force_tile : (int)(ceil_div(ceil_div(S, tiles_s), 16) * 16);
+    plan->tile_n = choice.tile;
     tiles = ceil_div(L, 128) * ceil_div(S, plan->tile_n);
-    // K shares: as many CTAs as the device holds at two per SM, at least two groups each
-    int split = 1;
-    while (split < 8 && tiles * split * 2 <= 2 * sm_count && groups >= 4 * split) split *= 2;
-    if (force_split) split = force_split;
-    plan->split_k = split;
+    plan->split_k = choice.split;
     const int64_t stage = 16384 + (s_op.mn_major ? 16384 : plan->tile_n * 128);
-    plan->stages = (int)std::min<int64_t>(kFp8ShortMaxStages, kShortRing / stage);
-    plan->threads = 192;
+    plan->stages = (int)std::min<int64_t>(kFp8ShortMaxStages, short_ring(plan->tile_n) / stage);
+    plan->threads = kFp8ShortThreads;
     plan->smem_bytes = (int64_t)fp8_short_smem(plan->tile_n, plan->stages, (int)stage);
-    plan->grid_x = tiles * split;
+    plan->grid_x = tiles * choice.split;
   }
   plan->dp_tiles = tiles;
   plan->grid_y = 1;
@@ -348,10 +371,8 @@ int sgemm_fp8_set_override(int variant, int tile_n, int split) {
   if (variant != SGEMM_VARIANT_AUTO && variant != SGEMM_VARIANT_FP8_PAIR && variant != SGEMM_VARIANT_FP8_SHORT)
     return -1;
   const bool is_short = variant == SGEMM_VARIANT_FP8_SHORT;
-  const bool known = is_short ? tile_n > 0 && tile_n <= kFp8ShortMaxTile && tile_n % 16 == 0
-                              : variant == SGEMM_VARIANT_FP8_PAIR &&
-                                    std::find(std::begin(kFp8PairTiles), std::end(kFp8PairTiles), tile_n) !=
-                                        std::end(kFp8PairTiles);
+  const auto is_in = [&](const auto& tiles) { return std::find(std::begin(tiles), std::end(tiles), tile_n) != std::end(tiles); };
+  const bool known = is_short ? is_in(kFp8ShortTiles) : variant == SGEMM_VARIANT_FP8_PAIR && is_in(kFp8PairTiles);
   if (tile_n != 0 && !known) return -2;
   if ((split != 0 && !is_short) || (split != 0 && split != 1 && split != 2 && split != 4 && split != 8)) return -3;
   g_force_variant.store(variant);

@@ -124,7 +124,8 @@ struct Fp8ShortParams {
   unsigned* fault = nullptr;
 };
 cudaError_t prepare_fp8_short();
-constexpr int kFp8ShortMaxTile = 128, kFp8ShortMaxStages = 12;
+constexpr int kFp8ShortTiles[] = {16, 32, 64, 128};  // the tile widths there are kernels for
+constexpr int kFp8ShortMaxStages = 12, kFp8ShortThreads = 256;
 size_t fp8_short_smem(int tile_s, int stages, int stage_bytes);
 cudaError_t launch_fp8_short(const CUtensorMap& mapL, const CUtensorMap& mapS, const Fp8ShortParams& p,
                              cudaStream_t stream);

@@ -3,7 +3,7 @@
 //
 // The same sum as kernel_fp8_pair.cuh for products whose time is that of reading the long operand
 // (the weights of a decoding step).  The long side runs along the 128 rows of the tensor core, the
-// short one along its columns (tile_s <= 128, a multiple of 16), so a row of one token costs a
+// short one along its columns (tile_s 16, 32, 64 or 128), so a row of one token costs a
 // 128 x 16 tile and not a 256-row one; when the short side is M the tile is D transposed and is
 // written along the long side all the same.  One CTA per tile and K share: a cluster of `split`
 // CTAs (1, 2, 4 or 8) divides the groups of 128 k of a tile, each folds its groups into FP32 sums
@@ -11,7 +11,9 @@
 // order, each CTA a part of the tile read from its peers' shared memory: no workspace, one launch,
 // and the same result every time.
 //
-// Warp 0 loads (TMA; as many stages as fit twice per SM), warp 1 issues the products, warps 2-5 fold.
+// Warp 0 loads (TMA), warp 1 issues the products, warp 2 loads scales a chunk of 8 groups ahead, warps
+// 4-7 fold.  tile_s is a template argument (16, 32, 64 or 128): the fold's branches cost as much as its
+// work otherwise.  Two CTAs per SM share its memory (one at 128 columns, whose sums need the registers).
 #include "fp8_gemm.cuh"
 
 namespace sgemm_impl {
@@ -21,17 +23,16 @@ namespace {
 using namespace tc;
 
 constexpr int BL = 128, BK = 128;
-constexpr int kFoldThreads = 128;
-constexpr int kThreads = 64 + kFoldThreads;
-constexpr int kMaxStages = 12;
-constexpr int kMaxS = 128;
+constexpr int kFirstFold = 4, kFoldWarps = 4;
+constexpr int kThreads = 32 * (kFirstFold + kFoldWarps);
+constexpr int kMaxStages = kFp8ShortMaxStages;
+static_assert(kThreads == kFp8ShortThreads, "the plan's figure");
 constexpr int kMaxSmem = 220 * 1024;
-constexpr int kPitch = BL + 1;  // words between the columns of a share: lanes along rows or columns both hit 32 banks
+constexpr int kPitch = BL + 1;   // words between the columns of a share: lanes along rows or columns both hit 32 banks
+constexpr int kChunkGroups = 8;  // groups whose scales are loaded together
+constexpr int kChunks = 2;       // in shared memory
 
-__device__ __forceinline__ void tma_load(uint32_t dst, const CUtensorMap* map, uint32_t bar, int32_t inner,
-                                         int32_t outer) {
-  tma_load_3d(dst, map, bar, inner, outer, 0);
-}
+__host__ __device__ constexpr int chunk_floats(int tile_s) { return kChunkGroups * (BL + tile_s); }
 
 __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   float v;
@@ -39,57 +40,64 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
   return v;
 }
 
-__device__ __forceinline__ void fold_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
-
-// MAXS: the largest tile_s this form holds sums for (32 columns leave registers for more CTAs).
-template <int MAXS>
-__global__ void __launch_bounds__(kThreads, 2) fp8_short_kernel(const __grid_constant__ CUtensorMap mapL,
-                                                                const __grid_constant__ CUtensorMap mapS,
-                                                                const __grid_constant__ Fp8ShortParams p) {
+template <int TS>
+__global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
+    fp8_short_kernel(const __grid_constant__ CUtensorMap mapL, const __grid_constant__ CUtensorMap mapS,
+                     const __grid_constant__ Fp8ShortParams p) {
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
-  __shared__ __align__(8) uint64_t acc_full[2], acc_empty[2];
+  __shared__ __align__(8) uint64_t full[kMaxStages], done[kMaxStages];
+  __shared__ __align__(8) uint64_t acc_empty[2];
+  __shared__ __align__(8) uint64_t scale_full[kChunks], scale_empty[kChunks];
   __shared__ uint32_t tmem_slot;
-  __shared__ __align__(16) float col_scale[2][kMaxS];
 
   const uint32_t raw_addr = smem_addr(smem_raw);
   const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
   const uint32_t sbase = raw_addr + pad;
   float* share = reinterpret_cast<float*>(smem_raw + pad);  // over the ring, once it is drained
+  float* chunks = reinterpret_cast<float*>(smem_raw + pad + p.stages * p.stage_bytes);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)blockIdx.x % p.split;  // of the cluster: blocks of a cluster are consecutive
   const int tile = (int)blockIdx.x / p.split;
-  const int l0 = (tile / p.tiles_s) * BL, s0 = (tile % p.tiles_s) * p.tile_s;
+  const int l0 = (tile / p.tiles_s) * BL, s0 = (tile % p.tiles_s) * TS;
   const int groups = (p.K + BK - 1) / BK;
   const int g0 = (int)((int64_t)groups * rank / p.split), g1 = (int)((int64_t)groups * (rank + 1) / p.split);
   const int units = g1 - g0;
-  const uint32_t tmem_cols = p.tile_s <= 32 ? 64u : p.tile_s <= 64 ? 128u : 256u;  // two accumulators
+  constexpr uint32_t kAccCols = TS < 32 ? 32u : (uint32_t)TS;
+  constexpr uint32_t kTmemCols = 2 * kAccCols;
 
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
+    prefetch_tensormap(&mapL);
+    prefetch_tensormap(&mapS);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
-      mbar_init(smem_addr(&empty[s]), 1);
+      mbar_init(smem_addr(&done[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) {
-      mbar_init(smem_addr(&acc_full[b]), 1);
-      mbar_init(smem_addr(&acc_empty[b]), kFoldThreads / 32);
+    for (int b = 0; b < 2; ++b) mbar_init(smem_addr(&acc_empty[b]), kFoldWarps);
+    for (int c = 0; c < kChunks; ++c) {
+      mbar_init(smem_addr(&scale_full[c]), 32);
+      mbar_init(smem_addr(&scale_empty[c]), kFoldWarps);
     }
     fence_mbar_init();
   }
-  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), tmem_cols);
+  if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
   tmem_fence_before_sync();
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_slot;
-  const uint32_t acc_step = tmem_cols / 2;
+  // launched as a programmatic dependent: what the stream's kernel before this one wrote is read, and
+  // what it read is written, only from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
 
+  float2 sum[TS / 2];
+  const int row = 32 * (warp & 3) + lane;  // of the tile, of a fold thread
   if (warp == 0) {
     // ------------------------------------------------ loads
-    const uint32_t bytes = (uint32_t)(BL * BK + (p.s_mn ? 128 * BK : p.tile_s * BK));
+    const uint32_t bytes = (uint32_t)(BL * BK + (p.s_mn ? 128 * BK : TS * BK));
     int t = 0, s = 0;
     uint32_t lap = 0;
     for (; t < units; ++t) {
-      if (lap > 0 && !poll_wait(smem_addr(&empty[s]), (lap - 1) & 1u, p.timeout_ns)) {
+      if (lap > 0 && !poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
         if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
         break;
       }
@@ -97,8 +105,8 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_short_kernel(const __grid_con
         const int k0 = (g0 + t) * BK;
         const uint32_t bar = smem_addr(&full[s]), a = sbase + (uint32_t)(s * p.stage_bytes);
         mbar_arrive_expect_tx(bar, bytes);
-        tma_load(a, &mapL, bar, p.l_mn ? l0 : k0, p.l_mn ? k0 : l0);
-        tma_load(a + BL * BK, &mapS, bar, p.s_mn ? s0 : k0, p.s_mn ? k0 : s0);
+        tma_load_3d(a, &mapL, bar, p.l_mn ? l0 : k0, p.l_mn ? k0 : l0, 0);
+        tma_load_3d(a + BL * BK, &mapS, bar, p.s_mn ? s0 : k0, p.s_mn ? k0 : s0, 0);
       }
       if (++s == p.stages) {
         s = 0;
@@ -111,7 +119,7 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_short_kernel(const __grid_con
         atomicOr(p.fault, (unsigned)kFaultDrainWait);
   } else if (warp == 1) {
     // ------------------------------------------------ products
-    const uint32_t lstep = step_of(p.l_mn), sstep = step_of(p.s_mn);
+    const uint32_t lstep = step_of(p.l_mn), sstep = step_of(p.s_mn), desc0 = desc_lo(sbase);
     int t = 0, s = 0;
     uint32_t lap = 0;
     for (; t < units; ++t) {
@@ -123,15 +131,12 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_short_kernel(const __grid_con
       }
       tmem_fence_after_sync();
       if (elect_one()) {
-        const uint32_t a = sbase + (uint32_t)(s * p.stage_bytes);
-        const uint32_t ld = desc_lo(a), sd = desc_lo(a + BL * BK);
+        const uint32_t ld = desc0 + (uint32_t)(s * (p.stage_bytes >> 4)), sd = ld + ((BL * BK) >> 4);
 #pragma unroll
-        for (int ks = 0; ks < BK / 32; ++ks)
-          mma_f8(tmem + (uint32_t)b * acc_step, make_desc(ld + (uint32_t)ks * lstep),
-                 make_desc(sd + (uint32_t)ks * sstep), p.idesc,
+        for (uint32_t ks = 0; ks < BK / 32; ++ks)
+          mma_f8(tmem + (uint32_t)b * kAccCols, make_desc(ld + ks * lstep), make_desc(sd + ks * sstep), p.idesc,
                  ks == 0 ? 0u : 1u);
-        mma_commit(smem_addr(&empty[s]));
-        mma_commit(smem_addr(&acc_full[b]));
+        mma_commit(smem_addr(&done[s]));  // the stage is free, the accumulator holds group t
       }
       __syncwarp();
       if (++s == p.stages) {
@@ -139,67 +144,88 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_short_kernel(const __grid_con
         ++lap;
       }
     }
-    // leave only when every product has completed and its commits have landed
+    // leave only when every product has completed and its commit has landed
     bool ok = true;
     for (int u = t > p.stages ? t - p.stages : 0; u < t; ++u)
-      ok = ok && poll_wait(smem_addr(&empty[u % p.stages]), (uint32_t)(u / p.stages) & 1u, p.timeout_ns);
-    for (int u = t > 2 ? t - 2 : 0; u < t; ++u)
-      ok = ok && poll_wait(smem_addr(&acc_full[u & 1]), (uint32_t)(u / 2) & 1u, p.timeout_ns);
+      ok = ok && poll_wait(smem_addr(&done[u % p.stages]), (uint32_t)(u / p.stages) & 1u, p.timeout_ns);
     if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultDrainWait);
-  }
-
-  // ------------------------------------------------ folders: row 32q + lane of the tile, all its columns
-  float2 sum[MAXS / 2];
-  const int row = 32 * (warp & 3) + lane;  // warps 2, 3, 4, 5: TMEM lane quarters 2, 3, 0, 1
-  bool ok = true;
-  if (warp >= 2) {
-    const int q = warp & 3;
-    const int fid = (int)threadIdx.x - 64;
-    const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16);
+  } else if (warp == 2) {
+    // ------------------------------------------------ scales of the tile's rows and columns
+    const uint32_t ring = smem_addr(chunks);
+    int c = 0;
+    uint32_t lap = 0;
+    for (int t = 0; t < units; t += kChunkGroups) {
+      if (lap > 0 && !poll_wait(smem_addr(&scale_empty[c]), (lap - 1) & 1u, p.timeout_ns)) {
+        if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+        break;
+      }
+      const int count = min(kChunkGroups, units - t);
+      const uint32_t dst = ring + 4u * (uint32_t)(c * chunk_floats(TS));
+      for (int j = lane; j < BL + TS; j += 32) {
+        const Fp8Scales& sc = j < BL ? p.sl : p.ss;
+        const int64_t at = j < BL ? min(l0 + j, p.L - 1) : min(s0 + j - BL, p.S - 1);
+        const float* src = sc.p + (at >> sc.shift) * sc.si + (int64_t)(g0 + t) * sc.sk;
+        for (int g = 0; g < count; ++g) copy4_async(dst + 4u * (uint32_t)(g * (BL + TS) + j), src + (int64_t)g * sc.sk);
+      }
+      copies_arrive(smem_addr(&scale_full[c]));
+      if (++c == kChunks) {
+        c = 0;
+        ++lap;
+      }
+    }
+    copies_wait_all();
+  } else if (warp >= kFirstFold) {
+    // ------------------------------------------------ folders: a row of the tile each, all its columns
+    const uint32_t tq = tmem + ((uint32_t)(32 * (warp & 3)) << 16);
 #pragma unroll
-    for (int e = 0; e < MAXS / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
-    const float* sl = p.sl.p + (int64_t)(min(l0 + row, p.L - 1) >> p.sl.shift) * p.sl.si + (int64_t)g0 * p.sl.sk;
-    const float* ss = p.ss.p + (int64_t)(min(s0 + min(fid, p.tile_s - 1), p.S - 1) >> p.ss.shift) * p.ss.si +
-                      (int64_t)g0 * p.ss.sk;
-    float l_next = units > 0 ? __ldg(sl) : 0.0f, s_next = units > 0 ? __ldg(ss) : 0.0f;
+    for (int e = 0; e < TS / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
+    bool ok = true;
+    int s = 0, c = 0;
+    uint32_t s_lap = 0, c_lap = 0;
     for (int t = 0; t < units; ++t) {
-      const int b = t & 1;
-      const float l_cur = l_next;
-      col_scale[b][fid] = s_next;  // last read two groups ago: one barrier per group suffices
-      if (t + 1 < units) {
-        l_next = __ldg(sl + (int64_t)(t + 1) * p.sl.sk);
-        s_next = __ldg(ss + (int64_t)(t + 1) * p.ss.sk);
+      const int b = t & 1, in_chunk = t & (kChunkGroups - 1);
+      if (in_chunk == 0) ok = poll_wait(smem_addr(&scale_full[c]), c_lap & 1u, p.timeout_ns);
+      ok = ok && poll_wait(smem_addr(&done[s]), s_lap & 1u, p.timeout_ns);
+      if (!ok) {
+        if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+        break;
       }
-      fold_barrier();
-      if (ok) {  // a warp that gave up keeps meeting the others at the barrier
-        ok = poll_wait(smem_addr(&acc_full[b]), (uint32_t)(t / 2) & 1u, p.timeout_ns);
-        if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
-      }
-      if (!ok) continue;
       tmem_fence_after_sync();
-      const float2 l2 = make_float2(l_cur, l_cur);
+      const float* sc = chunks + c * chunk_floats(TS) + in_chunk * (BL + TS);
+      const float l = sc[row];
+      const float2 l2 = make_float2(l, l);
+      constexpr int kCols = TS < 32 ? TS : 32;
 #pragma unroll
-      for (int c = 0; c < MAXS / 16; ++c) {
-        if (16 * c < p.tile_s) {
-          float v[16];
-          tmem_ld16(tq + (uint32_t)b * acc_step + (uint32_t)(16 * c), v);
-          tmem_wait_ld();
-          if (16 * (c + 1) >= p.tile_s) {
-            tmem_fence_before_sync();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&acc_empty[b]));
-          }
-          tmem_ld_ready(v);
-          const float4* cs = reinterpret_cast<const float4*>(&col_scale[b][16 * c]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float4 w = cs[e];
-            float2& m0 = sum[8 * c + 2 * e];
-            float2& m1 = sum[8 * c + 2 * e + 1];
-            m0 = __ffma2_rn(__fmul2_rn(make_float2(v[4 * e], v[4 * e + 1]), make_float2(w.x, w.y)), l2, m0);
-            m1 = __ffma2_rn(__fmul2_rn(make_float2(v[4 * e + 2], v[4 * e + 3]), make_float2(w.z, w.w)), l2, m1);
-          }
+      for (int j0 = 0; j0 < TS; j0 += kCols) {
+        float v[kCols];
+        tmem_ld<kCols>(tq + (uint32_t)b * kAccCols + (uint32_t)j0, v);
+        tmem_wait_ld();
+        if (j0 + kCols == TS) {
+          tmem_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_addr(&acc_empty[b]));
         }
+#pragma unroll
+        for (int j = 0; j < kCols; ++j) asm volatile("" : "+f"(v[j]));  // used behind the wait only
+#pragma unroll
+        for (int j = 0; j < kCols; j += 4) {
+          const float4 w = *reinterpret_cast<const float4*>(sc + BL + j0 + j);
+          float2* m = &sum[(j0 + j) / 2];
+          m[0] = __ffma2_rn(__fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(w.x, w.y)), l2, m[0]);
+          m[1] = __ffma2_rn(__fmul2_rn(make_float2(v[j + 2], v[j + 3]), make_float2(w.z, w.w)), l2, m[1]);
+        }
+      }
+      if (in_chunk == kChunkGroups - 1) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_addr(&scale_empty[c]));
+        if (++c == kChunks) {
+          c = 0;
+          ++c_lap;
+        }
+      }
+      if (++s == p.stages) {
+        s = 0;
+        ++s_lap;
       }
     }
   }
@@ -208,30 +234,28 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_short_kernel(const __grid_con
   tmem_fence_before_sync();
   __syncthreads();  // the ring is drained: loads have landed and the products that read it are done
   tmem_fence_after_sync();
-  if (warp == 1) tmem_dealloc(tmem, tmem_cols);
-  if (warp >= 2) {
+  if (warp == 1) tmem_dealloc(tmem, kTmemCols);
+  if (warp >= kFirstFold) {
 #pragma unroll
-    for (int c = 0; c < MAXS / 16; ++c)
-      if (16 * c < p.tile_s)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          share[(16 * c + 2 * e) * kPitch + row] = sum[8 * c + e].x;
-          share[(16 * c + 2 * e + 1) * kPitch + row] = sum[8 * c + e].y;
-        }
+    for (int e = 0; e < TS / 2; ++e) {
+      share[2 * e * kPitch + row] = sum[e].x;
+      share[(2 * e + 1) * kPitch + row] = sum[e].y;
+    }
   }
+  __syncthreads();
   if (p.split > 1) cluster_sync();
-  else __syncthreads();
   // this CTA's part of the tile: its share of the columns (D transposed: lanes along the long side)
   // or of the rows (lanes along the short side, the columns of D)
-  const int nl = min(BL, p.L - l0), ns = min(p.tile_s, p.S - s0);
-  const uint32_t share_addr = sbase;
+  const int nl = min(BL, p.L - l0), ns = min(TS, p.S - s0);
   const int parts = p.trans ? ns : nl;
   const int b0 = parts * rank / p.split, b1 = parts * (rank + 1) / p.split;
-  const int inner = p.trans ? nl : ns;
-  for (int i = (int)threadIdx.x; i < (b1 - b0) * inner; i += kThreads) {
-    const int outer_i = b0 + i / inner, inner_i = i % inner;
+  const int inner = p.trans ? BL : TS;  // powers of two
+  const int shift = 31 - __clz(inner);
+  for (int i = (int)threadIdx.x; i < (b1 - b0) << shift; i += kThreads) {
+    const int outer_i = b0 + (i >> shift), inner_i = i & (inner - 1);
     const int l = p.trans ? inner_i : outer_i, s = p.trans ? outer_i : inner_i;
-    const uint32_t at = share_addr + 4u * (uint32_t)(s * kPitch + l);
+    if (l >= nl || s >= ns) continue;
+    const uint32_t at = sbase + 4u * (uint32_t)(s * kPitch + l);
     float v = 0.0f;
     if (p.split == 1) {
       v = share[s * kPitch + l];
@@ -251,6 +275,18 @@ __global__ void __launch_bounds__(kThreads, 2) fp8_short_kernel(const __grid_con
     __syncthreads();
     cluster_sync();  // no CTA leaves while a peer may read its share
   }
+}
+
+// f(kernel) for a tile width.
+template <typename F>
+cudaError_t with_short_kernel(int tile_s, const F& f) {
+  switch (tile_s) {
+    case 16: return f(fp8_short_kernel<16>);
+    case 32: return f(fp8_short_kernel<32>);
+    case 64: return f(fp8_short_kernel<64>);
+    case 128: return f(fp8_short_kernel<128>);
+  }
+  return cudaErrorInvalidValue;
 }
 
 __global__ void __launch_bounds__(256) repack_kernel(const uint8_t* __restrict__ src, int64_t ld, int64_t rows,
@@ -283,16 +319,19 @@ __global__ void __launch_bounds__(256) scale_kernel(const Fp8Out o) {
 }  // namespace f8
 
 size_t fp8_short_smem(int tile_s, int stages, int stage_bytes) {
-  const size_t ring = (size_t)stages * stage_bytes, share = (size_t)tile_s * f8::kPitch * 4;
+  const size_t ring = (size_t)stages * stage_bytes + (size_t)f8::kChunks * f8::chunk_floats(tile_s) * 4;
+  const size_t share = (size_t)tile_s * f8::kPitch * 4;
   return (ring > share ? ring : share) + 1024;
 }
 
 cudaError_t prepare_fp8_short() {
-  cudaError_t e = cudaFuncSetAttribute(f8::fp8_short_kernel<32>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                       f8::kMaxSmem);
-  if (e == cudaSuccess)
-    e = cudaFuncSetAttribute(f8::fp8_short_kernel<128>, cudaFuncAttributeMaxDynamicSharedMemorySize, f8::kMaxSmem);
-  return e;
+  for (int tile_s : kFp8ShortTiles) {
+    const cudaError_t e = f8::with_short_kernel(tile_s, [](auto kernel) {
+      return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, f8::kMaxSmem);
+    });
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 cudaError_t launch_fp8_short(const CUtensorMap& mapL, const CUtensorMap& mapS, const Fp8ShortParams& p,
@@ -302,15 +341,17 @@ cudaError_t launch_fp8_short(const CUtensorMap& mapL, const CUtensorMap& mapS, c
   cfg.blockDim = dim3(f8::kThreads);
   cfg.dynamicSmemBytes = fp8_short_smem(p.tile_s, p.stages, p.stage_bytes);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
   attr[0].val.clusterDim.x = (unsigned)p.split;
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
+  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return p.tile_s <= 32 ? cudaLaunchKernelEx(&cfg, f8::fp8_short_kernel<32>, mapL, mapS, p)
-                        : cudaLaunchKernelEx(&cfg, f8::fp8_short_kernel<128>, mapL, mapS, p);
+  cfg.numAttrs = 2;
+  return f8::with_short_kernel(p.tile_s,
+                               [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, mapL, mapS, p); });
 }
 
 cudaError_t launch_fp8_repack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t ldd,

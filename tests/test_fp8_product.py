@@ -138,7 +138,7 @@ def test_short_splits(force, split, M, N, K):
 
 
 @pytest.mark.gpu
-@pytest.mark.parametrize("tile", range(16, 129, 16))
+@pytest.mark.parametrize("tile", [16, 32, 64, 128])
 def test_short_tiles(force, tile):
     force("FP8_SHORT", tile, 2)
     for ops in OPS:
@@ -351,7 +351,7 @@ def test_refusals():
     refused(-13, "NT", 8, 8, 128, beta=1.0, C=FAKE, ldc=9, ldd=8)  # C in place has one stride
     refused(-14, "NT", 8, 8, 128, type=2)
     refused(4, "NT", 1 << 31, 8, 128)
-    for bad in (("FP8_PAIR", 16, 0), ("FP8_PAIR", 96, 0), ("FP8_PAIR", 288, 0), ("FP8_SHORT", 144, 0), ("AUTO", 32, 0)):
+    for bad in (("FP8_PAIR", 16, 0), ("FP8_PAIR", 96, 0), ("FP8_PAIR", 288, 0), ("FP8_SHORT", 144, 0), ("FP8_SHORT", 48, 0), ("AUTO", 32, 0)):
         with pytest.raises(sg.SgemmError):
             sg.sgemm_fp8_set_override(*bad)
     for bad in (("FP8_PAIR", 0, 2), ("FP8_SHORT", 0, 3)):
