@@ -168,7 +168,7 @@ enum Output {
 template <bool BF16>
 __device__ __forceinline__ void store_aligned_rows(const Fp8Out& o, int64_t row, int64_t col, const float* v,
                                                    int pitch) {
-  constexpr int kBatch = 4;
+  constexpr int kBatch = 8;  // all of them: each batch waits for C once
   using T = typename std::conditional<BF16, uint2, float4>::type;  // 4 elements
   constexpr int kSize = BF16 ? 2 : 4;
   char* d = static_cast<char*>(o.D) + (row * o.ldd + col) * kSize;
@@ -206,6 +206,26 @@ __device__ __forceinline__ void store_aligned_rows(const Fp8Out& o, int64_t row,
   }
 }
 
+// One column of a piece, element by element: `rows` rows from row0, what C holds kBatch rows at a time.
+template <typename T, int kBatch>
+__device__ __forceinline__ void store_rows_any(const Fp8Out& o, int row0, int col, int rows, bool add, const float* v,
+                                               int pitch) {
+  T* d = static_cast<T*>(o.D) + (int64_t)row0 * o.ldd + col;
+  const T* c = static_cast<const T*>(o.C) + (add ? (int64_t)row0 * o.ldc + col : 0);
+#pragma unroll 1
+  for (int r0 = 0; r0 < rows; r0 += kBatch) {
+    T old[kBatch];
+    if (add) {
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k, c += o.ldc)
+        if (r0 + k < rows) old[k] = *c;
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k, v += pitch, d += o.ldd)
+      if (r0 + k < rows) from_float(d, add ? fmaf(o.alpha, *v, o.beta * to_float(old[k])) : o.alpha * *v);
+  }
+}
+
 // A 32-row x 32-column piece of D from its sums in shared memory (`piece`, `pitch` words from row to
 // row), by one warp.  With aligned rows eight lanes hold 32 consecutive columns (128 bytes of FP32, 64
 // of BF16) of 4 rows at a time, otherwise (and at D's edges) a row is written by lanes with one element
@@ -224,25 +244,9 @@ __device__ __forceinline__ void store_piece(const Fp8Out& o, int row0, int col0,
   if (col >= o.N) return;
   const bool add = OUT == kOutAdd || o.beta != 0.0f;
   const int rows = min(32, o.M - row0);
-#pragma unroll 1
-  for (int r0 = 0; r0 < rows; r0 += 8) {
-    float c[8];
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      c[k] = 0.0f;
-      if (add && r0 + k < rows) c[k] = read_c(o, (int64_t)(row0 + r0 + k) * o.ldc + col);
-    }
-#pragma unroll
-    for (int k = 0; k < 8; ++k) {
-      const float v = piece[(r0 + k) * pitch + lane];
-      const float x = add ? fmaf(o.alpha, v, o.beta * c[k]) : o.alpha * v;
-      const int64_t i = (int64_t)(row0 + r0 + k) * o.ldd + col;
-      if (r0 + k < rows) {
-        if (o.bf16) static_cast<__nv_bfloat16*>(o.D)[i] = __float2bfloat16_rn(x);
-        else        static_cast<float*>(o.D)[i] = x;
-      }
-    }
-  }
+  constexpr int kBatch = OUT == kOutAny ? 32 : 8;  // (at the edges only, where registers are short)
+  if (o.bf16) store_rows_any<__nv_bfloat16, kBatch>(o, row0, col, rows, add, piece + lane, pitch);
+  else        store_rows_any<float, kBatch>(o, row0, col, rows, add, piece + lane, pitch);
 }
 
 }  // namespace f8
