@@ -341,19 +341,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int e = 0; e < 8; ++e) asm volatile("" : "+f"(x[e]));  // used behind the wait only
             float2* m = &sum[(kFirst + k) / 2];
-            if (COLS) {
-              const float4* w = reinterpret_cast<const float4*>(scb + kFirst + k);
-              const float4 w0 = w[0], w1 = w[1];
-              const float2 sa2 = make_float2(sa, sa);
-              m[0] = __ffma2_rn(__fmul2_rn(make_float2(x[0], x[1]), make_float2(w0.x, w0.y)), sa2, m[0]);
-              m[1] = __ffma2_rn(__fmul2_rn(make_float2(x[2], x[3]), make_float2(w0.z, w0.w)), sa2, m[1]);
-              m[2] = __ffma2_rn(__fmul2_rn(make_float2(x[4], x[5]), make_float2(w1.x, w1.y)), sa2, m[2]);
-              m[3] = __ffma2_rn(__fmul2_rn(make_float2(x[6], x[7]), make_float2(w1.z, w1.w)), sa2, m[3]);
-            } else {
-              const float2 w2 = make_float2(s0, s0);
+            const float2 w2 = make_float2(s0, s0);
 #pragma unroll
-              for (int e = 0; e < 4; ++e) m[e] = __ffma2_rn(make_float2(x[2 * e], x[2 * e + 1]), w2, m[e]);
-            }
+            for (int e = 0; e < 4; ++e) m[e] = __ffma2_rn(make_float2(x[2 * e], x[2 * e + 1]), w2, m[e]);
           }
         };
         const auto load = [&](auto first, float* v) {
@@ -369,30 +359,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         constexpr std::integral_constant<int, kLoadCols> c_1{};
         constexpr std::integral_constant<int, 2 * kLoadCols> c_2{};
         constexpr std::integral_constant<int, 3 * kLoadCols> c_3{};
-        float va[kLoadCols], vb[kLoadCols];
-        load(c_0, va);
-        sa = sc[in_chunk * BMC + 32 * q + lane];
-        if (!COLS) s0 = sa * scb[0];
-        tmem_wait_ld();
-        if constexpr (cols > c_1) load(c_1, vb);
-        else release();
-        add(c_0, va);
-        if constexpr (cols > c_1) {
+        if constexpr (COLS) {
+          // the columns' scales come from shared memory while the accumulator's columns do from TMEM (with
+          // the next columns' registers as well there would be too few)
+          sa = sc[in_chunk * BMC + 32 * q + lane];
+          const float2 sa2 = make_float2(sa, sa);
+          const auto scaled = [&](auto first) {
+            constexpr int kFirst = decltype(first)::value;
+            float v[kLoadCols];
+            float4 w[kLoadCols / 4];
+            load(first, v);
+#pragma unroll
+            for (int k = 0; k < kLoadCols / 4; ++k) w[k] = *reinterpret_cast<const float4*>(scb + kFirst + 4 * k);
+            tmem_wait_ld();
+            if (kFirst + kLoadCols == cols) release();
+#pragma unroll
+            for (int k = 0; k < kLoadCols / 4; ++k) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) asm volatile("" : "+f"(v[4 * k + e]));  // used behind the wait only
+              float2* m = &sum[kFirst / 2 + 2 * k];
+              m[0] = __ffma2_rn(__fmul2_rn(make_float2(v[4 * k], v[4 * k + 1]), make_float2(w[k].x, w[k].y)), sa2, m[0]);
+              m[1] = __ffma2_rn(__fmul2_rn(make_float2(v[4 * k + 2], v[4 * k + 3]), make_float2(w[k].z, w[k].w)), sa2, m[1]);
+            }
+          };
+          scaled(c_0);
+          if constexpr (cols > c_1) scaled(c_1);
+          if constexpr (cols > c_2) scaled(c_2);
+          if constexpr (cols > c_3) scaled(c_3);
+        } else {
+          float va[kLoadCols], vb[kLoadCols];
+          load(c_0, va);
+          s0 = sc[in_chunk * BMC + 32 * q + lane] * scb[0];
           tmem_wait_ld();
-          if constexpr (cols > c_2) load(c_2, va);
+          if constexpr (cols > c_1) load(c_1, vb);
           else release();
-          add(c_1, vb);
-        }
-        if constexpr (cols > c_2) {
-          tmem_wait_ld();
-          if constexpr (cols > c_3) load(c_3, vb);
-          else release();
-          add(c_2, va);
-        }
-        if constexpr (cols > c_3) {
-          tmem_wait_ld();
-          release();
-          add(c_3, vb);
+          add(c_0, va);
+          if constexpr (cols > c_1) {
+            tmem_wait_ld();
+            if constexpr (cols > c_2) load(c_2, va);
+            else release();
+            add(c_1, vb);
+          }
+          if constexpr (cols > c_2) {
+            tmem_wait_ld();
+            if constexpr (cols > c_3) load(c_3, vb);
+            else release();
+            add(c_2, va);
+          }
+          if constexpr (cols > c_3) {
+            tmem_wait_ld();
+            release();
+            add(c_3, vb);
+          }
         }
         if (in_chunk == kChunk - 1 || g == groups - 1) {
           __syncwarp();
