@@ -414,7 +414,6 @@ int sgemm_fp8_quantize(int64_t rows, int64_t cols, const void* X, int type, int6
   p.lds = lds;
   p.format = format;
   p.x_vec = rows16(X, ldx, type_size(type));
-  p.q_vec = aligned(codes, 8) && ldq % 8 == 0;
   return launch_status(launch_fp8_quantize(type, block_rows, block_cols, p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -465,7 +464,7 @@ int sgemm_fp8_rmsnorm(int64_t rows, int64_t cols, int type, const void* X, int64
   p.lds = lds;
   p.rstd = rstd;
   p.vec = rows16(X, ldx, size) && rows16(R, ldr, size) && rows16(W, 0, size) && rows16(H, ldh, size) &&
-          rows16(Y, ldy, size) && (!codes || (aligned(codes, 8) && ldq % 8 == 0));
+          rows16(Y, ldy, size) && cols % 8 == 0;
   return launch_status(launch_fp8_rmsnorm(type, p, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -511,8 +510,10 @@ int sgemm_fp8_rmsnorm_backward(int64_t rows, int64_t cols, int type, const void*
   p.lddx = lddx;
   p.dw = dW;
   p.vec = rows16(dY, lddy, size) && rows16(H, ldh, size) && rows16(W, 0, size) && rows16(dH, lddh, size) &&
-          rows16(dX, lddx, size);
-  const int grid = fp8_rmsnorm_backward_grid(type, rows, (int)cols, dev.sm_count);
+          rows16(dX, lddx, size) && cols % 8 == 0;
+  p.timeout_ns = wait_timeout_ns();
+  p.fault = dev.fault;
+  const int grid = fp8_rmsnorm_backward_grid(type, rows, (int)cols, p.vec != 0, dev.sm_count);
   if (dW) {
     void* ws = nullptr;
     cudaError_t e = cudaMallocFromPoolAsync(&ws, (size_t)grid * cols * 4, dev.pool, stream);

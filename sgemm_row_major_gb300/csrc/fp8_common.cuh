@@ -90,45 +90,104 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void from_float(float* p, float x) { *p = x; }
 __device__ __forceinline__ void from_float(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// Elements [0, n) of a chunk of V at p (zeros beyond n); `vec`: p is 16-byte aligned.
+// A matrix that chunks are loaded from: `end` is past its last element.
 template <typename T>
-__device__ __forceinline__ Chunk<T> load_chunk(const T* p, int64_t n, bool vec) {
-  constexpr int V = Chunk<T>::V;
-  Chunk<T> c;
-  c.raw = make_uint4(0u, 0u, 0u, 0u);
-  if (vec && n >= V) {
-    c.raw = *reinterpret_cast<const uint4*>(p);
-  } else if (n > 0) {
-    float v[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) v[i] = i < n ? to_float(p[i]) : 0.0f;
-    c.put(v);  // exact: every value came from T
-  }
-  return c;
-}
+struct Rows {
+  const T *base, *end;
+  __device__ __forceinline__ Rows(const void* p, int64_t rows, int64_t ld, int64_t cols)
+      : base(static_cast<const T*>(p)), end(static_cast<const T*>(p) + (rows - 1) * ld + cols) {}
+};
 
-template <typename T>
-__device__ __forceinline__ void store_chunk(T* p, const float* v, int64_t n, bool vec) {
+// A chunk of elements [0, n) at p, zeros beyond n, in two steps: load() sends for it, get() waits for it
+// (so that several are on their way at once).  VEC: p is 16-byte aligned and n is 0 or >= V.  Otherwise
+// any p that is aligned to its type (rows of an odd number of columns begin anywhere): FP32 element by
+// element; BF16 as the 16-byte units that p lies in, where they are inside the matrix, shifted into place
+// (element by element the norm of 8192 x 4095 took 113 us, so 66 us).
+template <typename T, bool VEC>
+struct Loading {
+  static constexpr int V = Chunk<T>::V;
+  uint4 a, b;
+  uint32_t off;  // bytes to shift by
+  int left;
+  __device__ __forceinline__ void load(const T* p, int64_t n, const Rows<T>& m) {
+    a = b = make_uint4(0u, 0u, 0u, 0u);
+    if (VEC) {
+      if (n > 0) a = *reinterpret_cast<const uint4*>(p);
+      return;
+    }
+    left = (int)max((int64_t)0, min((int64_t)V, n));
+    if (sizeof(T) == 4) {
+      const uint32_t* e = reinterpret_cast<const uint32_t*>(p);
+      a.x = left > 0 ? e[0] : 0u;
+      a.y = left > 1 ? e[1] : 0u;
+      a.z = left > 2 ? e[2] : 0u;
+      a.w = left > 3 ? e[3] : 0u;
+      return;
+    }
+    const uintptr_t at = reinterpret_cast<uintptr_t>(p), unit = at & ~(uintptr_t)15;
+    off = (uint32_t)(at - unit);
+    if (left == 0) return;
+    const bool two = off + left * sizeof(T) > 16u;
+    if (unit >= reinterpret_cast<uintptr_t>(m.base) && unit + (two ? 32 : 16) <= reinterpret_cast<uintptr_t>(m.end)) {
+      a = *reinterpret_cast<const uint4*>(unit);
+      if (two) b = *reinterpret_cast<const uint4*>(unit + 16);
+    } else {
+      float v[V];
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[i] = i < left ? to_float(p[i]) : 0.0f;
+      Chunk<T> c;
+      c.put(v);  // exact: every value came from T
+      a = c.raw;
+      off = 0u;
+    }
+  }
+  __device__ __forceinline__ Chunk<T> get() const {
+    Chunk<T> c;
+    if (VEC || sizeof(T) == 4) {
+      c.raw = a;
+      return c;
+    }
+    uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = off & 8u ? w[i + 2] : w[i];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = off & 4u ? w[i + 1] : w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __funnelshift_r(w[i], w[i + 1], 8u * (off & 2u));
+    if (left < V) {
+      constexpr int kPer = 4 / sizeof(T);  // elements per word
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int here = left - i * kPer;
+        w[i] = here <= 0 ? 0u : here < kPer ? w[i] & 0xFFFFu : w[i];
+      }
+    }
+    c.raw = make_uint4(w[0], w[1], w[2], w[3]);
+    return c;
+  }
+};
+
+template <typename T, bool VEC>
+__device__ __forceinline__ void store_chunk(T* p, const float* v, int64_t n) {
   constexpr int V = Chunk<T>::V;
-  if (vec && n >= V) {
+  if (VEC ? n > 0 : n >= V && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
     Chunk<T> c;
     c.put(v);
     *reinterpret_cast<uint4*>(p) = c.raw;
-  } else {
+  } else if (!VEC) {
 #pragma unroll
     for (int i = 0; i < V; ++i)
       if (i < n) from_float(p + i, v[i]);
   }
 }
 
-// V codes (4 or 8) of one chunk, value i times inv[i]; `vec`: p is aligned to V bytes.
+// V codes (4 or 8) of one chunk, value i times inv[i].
 template <int V, bool CHECK>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float* v, const float* inv, int64_t n, bool vec,
-                                            bool e5m2) {
+__device__ __forceinline__ void store_codes(uint8_t* p, const float* v, const float* inv, int64_t n, bool e5m2) {
   uint32_t u[V / 4];
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) u[i] = codes4<CHECK>(v + 4 * i, inv + 4 * i, e5m2);
-  if (vec && n >= V) {
+  if (n >= V && (reinterpret_cast<uintptr_t>(p) & (V - 1)) == 0) {
     if (V == 4) *reinterpret_cast<uint32_t*>(p) = u[0];
     else        *reinterpret_cast<uint2*>(p) = make_uint2(u[0], u[V / 4 - 1]);
   } else {

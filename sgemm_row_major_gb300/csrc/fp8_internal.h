@@ -27,7 +27,7 @@ struct QuantParams {
   float* s = nullptr;
   int64_t lds = 0;
   int format = 0;
-  int x_vec = 0, q_vec = 0;  // 1: rows of X start at multiples of 16 bytes, of codes at multiples of 8
+  int x_vec = 0;  // 1: rows of X start at multiples of 16 bytes
 };
 cudaError_t launch_fp8_quantize(int type, int block_rows, int block_cols, const QuantParams& p, cudaStream_t stream);
 
@@ -44,7 +44,7 @@ struct NormParams {
   int64_t ldq = 0;
   float *s = nullptr, *rstd = nullptr;
   int64_t lds = 0;
-  int vec = 0;  // 1: every matrix row is aligned to its 8-element chunks
+  int vec = 0;  // 1: rows of all matrices start at multiples of 16 bytes and hold whole chunks of 8
 };
 cudaError_t launch_fp8_rmsnorm(int type, const NormParams& p, cudaStream_t stream);
 
@@ -59,11 +59,13 @@ struct NormGradParams {
   float* partial = nullptr;  // [grid][cols] sums of dW; nullptr: dW is not wanted
   float* dw = nullptr;
   int vec = 0;
+  uint64_t timeout_ns = 0;
+  unsigned* fault = nullptr;
 };
 constexpr int kNormGradMaxCols = 49152;  // the wide form keeps a row of dW sums in shared memory
 cudaError_t prepare_fp8_norm();
 // CTAs of the gradient kernel (its partial sums of dW take grid * cols floats).
-int fp8_rmsnorm_backward_grid(int type, int64_t rows, int cols, int sm_count);
+int fp8_rmsnorm_backward_grid(int type, int64_t rows, int cols, bool vec, int sm_count);
 cudaError_t launch_fp8_rmsnorm_backward(int type, const NormGradParams& p, int grid, cudaStream_t stream);
 
 // ---- product (kernel_fp8_pair.cuh, kernel_fp8_short.cu)

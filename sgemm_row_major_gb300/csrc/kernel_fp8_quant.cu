@@ -23,8 +23,7 @@ template <typename T>
 constexpr int kCtas = sizeof(T) == 2 ? 3 : 2;  // per SM: about 100 KB of loads in flight
 
 // What the threads of a CTA share of a tile: its place, and (128 x 1, 128 x 128) the partial maxima.
-// VEC: rows of X start at multiples of 16 bytes and hold whole chunks of V elements; otherwise
-// elements are loaded one by one.
+// VEC: rows of X start at multiples of 16 bytes and hold whole chunks of V elements.
 template <typename T, int G, bool VEC>
 struct Quant {
   static constexpr int V = Chunk<T>::V;
@@ -46,19 +45,16 @@ struct Quant {
     Chunk<T> c[kPasses];
     {
       const T* x = static_cast<const T*>(p.x) + (rt * kTile + lr) * p.ldx + col;
+      const Rows<T> all(p.x, p.rows, p.ldx, p.cols);
+      constexpr int kBatch = VEC ? kPasses : 4;  // chunks on their way at once
 #pragma unroll
-      for (int i = 0; i < kPasses; ++i, x += kRowsPerPass * p.ldx) {
-        c[i].raw = make_uint4(0u, 0u, 0u, 0u);
-        if (i * kRowsPerPass < rows && left > 0) {
-          if (VEC) {
-            c[i].raw = *reinterpret_cast<const uint4*>(x);
-          } else {
-            float v[V];
+      for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
+        Loading<T, VEC> l[kBatch];
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = e < left ? to_float(x[e]) : 0.0f;
-            c[i].put(v);
-          }
-        }
+        for (int i = 0; i < kBatch; ++i, x += kRowsPerPass * p.ldx)
+          l[i].load(x, (i0 + i) * kRowsPerPass < rows ? left : 0, all);
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) c[i0 + i] = l[i].get();
       }
     }
     bool again = false;
@@ -130,7 +126,7 @@ struct Quant {
         float f[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) f[e] = inv[G == kCol ? e : 0];
-        store_codes<V, CHECK>(q, v, f, left, p.q_vec != 0, e5m2);
+        store_codes<V, CHECK>(q, v, f, left, e5m2);
       }
     }
     return again;

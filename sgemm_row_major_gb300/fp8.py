@@ -4,7 +4,8 @@ An ``Fp8Matrix`` is a 2-D tensor of 8-bit codes with the scales of its groups of
 1x128, 128x1 or 128x128 elements.  ``quantize_fp8`` makes one from an FP32 or
 BF16 matrix, ``rmsnorm_fp8`` makes one from a layer's input, ``matmul_fp8``
 multiplies two, ``moe_fp8`` runs a mixture-of-experts layer on one.  Outputs
-that a call allocates belong to the stream it runs on.
+that a call allocates belong to the stream it runs on; rows of codes start at
+multiples of 16 elements and rows of the norm's outputs at multiples of 8.
 """
 from __future__ import annotations
 
@@ -118,6 +119,14 @@ def _empty(shape, dtype, like, stream):
         stream = _T.cuda.ExternalStream(int(stream), device=like.device) if stream else _T.cuda.default_stream(like.device)
     with _T.cuda.stream(stream):
         return _T.empty(shape, dtype=dtype, device=like.device)
+
+
+def _empty_rows(rows, cols, like, stream):
+    """(tensor, row stride): an uninitialised rows x cols tensor of like's type whose rows start at multiples of 16
+    bytes, as the kernels write them fastest."""
+    ld = (cols + 7) // 8 * 8
+    x = _empty((rows, ld), like.dtype, like, stream)
+    return (x if ld == cols else x[:, :cols]), ld or 1
 
 
 class Fp8Matrix:
@@ -276,19 +285,19 @@ def rmsnorm_fp8(x, weight, eps=1e-6, residual=None, *, codes=True, y=False, stre
     rows, cols, ldx = _rows(x, "x")
     dtype = x.dtype
     _vector(weight, "weight", cols, dtype)
-    h, r_ptr, ldr, h_ptr = x, None, 0, None
+    h, r_ptr, ldr, h_ptr, ldh = x, None, 0, None, cols or 1
     if residual is not None:
         rrows, rcols, ldr = _rows(residual, "residual")
         if rrows != rows or rcols != cols or residual.dtype is not dtype:
             raise ValueError("residual must have x's shape and type")
-        h = _empty((rows, cols), dtype, x, stream)
+        h, ldh = _empty_rows(rows, cols, x, stream)
         r_ptr, h_ptr = residual.data_ptr(), h.data_ptr()
-    out = _empty((rows, cols), dtype, x, stream) if y else None
+    out, ldy = _empty_rows(rows, cols, x, stream) if y else (None, cols or 1)
     rstd = _empty((rows,), _T.float32, x, stream)
     q = _new_matrix(rows, cols, ROW, 0, x, stream) if codes else None
     c = q._struct if codes else _NO_MATRIX
-    st = lib.sgemm_fp8_rmsnorm(rows, cols, t, x.data_ptr(), ldx, r_ptr, ldr, weight.data_ptr(), eps, h_ptr, cols or 1,
-                               out.data_ptr() if y else None, cols or 1, c.data, c.ld, c.scale, c.lds, rstd.data_ptr(), _on(stream, x))
+    st = lib.sgemm_fp8_rmsnorm(rows, cols, t, x.data_ptr(), ldx, r_ptr, ldr, weight.data_ptr(), eps, h_ptr, ldh,
+                               out.data_ptr() if y else None, ldy, c.data, c.ld, c.scale, c.lds, rstd.data_ptr(), _on(stream, x))
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_rmsnorm")
     return NormOutput(q, h, out, rstd)
@@ -312,10 +321,10 @@ def rmsnorm_fp8_backward(dy, h, weight, rstd, dh=None, *, stream=None):
         if drows != rows or dcols != cols or dh.dtype is not dtype:
             raise ValueError("dh must have dy's shape and type")
         dh_ptr = dh.data_ptr()
-    dx = _empty((rows, cols), dtype, dy, stream)
+    dx, lddx = _empty_rows(rows, cols, dy, stream)
     dw = _empty((cols,), _T.float32, dy, stream)
     st = lib.sgemm_fp8_rmsnorm_backward(rows, cols, t, dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), rstd.data_ptr(),
-                                        dh_ptr, lddh, dx.data_ptr(), cols or 1, dw.data_ptr(), _on(stream, dy))
+                                        dh_ptr, lddh, dx.data_ptr(), lddx, dw.data_ptr(), _on(stream, dy))
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_rmsnorm_backward")
     return dx, dw
