@@ -102,7 +102,7 @@ def _rows(x, name):
     ld, inner = x.stride()
     if inner != 1 and cols > 1:
         raise TypeError(f"{name}: the last dimension must be contiguous")
-    if rows <= 1 or ld < 1:
+    if rows <= 1 or cols == 0:
         ld = cols or 1
     return rows, cols, ld
 

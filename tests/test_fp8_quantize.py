@@ -114,6 +114,17 @@ def test_empty():
         assert tuple(m.shape) == shape
 
 
+@pytest.mark.gpu
+def test_rows_without_a_stride_are_refused():
+    """An expanded tensor's rows share memory: no leading dimension describes it."""
+    import torch
+    x = torch.zeros(1, 256, device="cuda").expand(5, 256)
+    with pytest.raises(sg.SgemmError):
+        sg.quantize_fp8(x)
+    with pytest.raises(sg.SgemmError):
+        sg.rmsnorm_fp8(x, torch.ones(256, device="cuda"))
+
+
 def call(*a):
     from sgemm_row_major_gb300 import fp8
     return fp8._lib().sgemm_fp8_quantize(*a)
