@@ -122,6 +122,21 @@ __device__ __forceinline__ void tma_out(const CUtensorMap& map, uint8_t* buf, co
   }
 }
 
+// One warp: asks for what C holds of rows row0 .. row1 - 1 and `cols` columns to be brought to L2 while
+// the tile's products run (the memory is hardly used then; when D is written, by all SMs at once, it is
+// what they wait for).
+__device__ __forceinline__ void prefetch_c(const Fp8Out& o, int row0, int row1, int col0, int cols) {
+  if (o.beta == 0.0f) return;
+  const int size = o.bf16 ? 2 : 4;
+  const int64_t bytes = (int64_t)min(cols, o.N - col0) * size;
+  for (int r = row0 + (threadIdx.x & 31); r < min(row1, o.M); r += 32) {
+    const uintptr_t first = reinterpret_cast<uintptr_t>(o.C) + (uintptr_t)(((int64_t)r * o.ldc + col0) * size);
+    const uintptr_t from = (first + 15) & ~(uintptr_t)15, to = (first + (uintptr_t)bytes) & ~(uintptr_t)15;
+    if (from < to)
+      asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(to - from)) : "memory");
+  }
+}
+
 // TN: the tile's columns.  COLS: B has one scale per column (weight gradients), else one per 128
 // columns.  Both are template arguments because the fold runs once per group in 16 warps: with the
 // tile's width at run time its branches made it 2.5 times as long.
@@ -289,6 +304,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int g = 0; g < count; ++g) copy4_async(dst + 4u * (uint32_t)(g * pitch + j), src + (int64_t)g * sc.sk);
           }
           copies_arrive(smem_addr(&scale_full[c]));
+          if (OUT != kOutPlain && rows) {  // the rows in equal parts, one with each chunk
+            const int chunks = (groups + kChunk - 1) / kChunk, at = g0 / kChunk;
+            prefetch_c(p.out, first + BMC * at / chunks, first + BMC * (at + 1) / chunks, tn * TN, TN);
+          }
           if (++c == Sc::kChunks) {
             c = 0;
             ++lap;
