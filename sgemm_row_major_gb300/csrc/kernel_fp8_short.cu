@@ -28,7 +28,11 @@ constexpr int kThreads = 32 * (kFirstFold + kFoldWarps);
 constexpr int kMaxStages = kFp8ShortMaxStages;
 static_assert(kThreads == kFp8ShortThreads, "the plan's figure");
 constexpr int kMaxSmem = 220 * 1024;
-constexpr int kPitch = BL + 1;   // words between the columns of a share: lanes along rows or columns both hit 32 banks
+// A share lies in shared memory in the order in which it is read, along the long side (D transposed) or
+// the short one: peers' reads of 32 consecutive words are one access, at any other step 32 (a product of
+// 1000 x 300 x 900 took 25 us and not 8).  The odd pitch keeps the folders' writes free of conflicts.
+__host__ __device__ constexpr int share_pitch(bool trans, int tile_s) { return trans ? BL + 1 : tile_s + 1; }
+__host__ __device__ constexpr int share_words(int tile_s) { return BL * tile_s + (BL > tile_s ? BL : tile_s); }
 constexpr int kChunkGroups = 8;  // groups whose scales are loaded together
 constexpr int kChunks = 2;       // in shared memory
 
@@ -236,10 +240,11 @@ __global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
   tmem_fence_after_sync();
   if (warp == 1) tmem_dealloc(tmem, kTmemCols);
   if (warp >= kFirstFold) {
+    const int sl = p.trans ? 1 : share_pitch(false, TS), ss = p.trans ? share_pitch(true, TS) : 1;
 #pragma unroll
     for (int e = 0; e < TS / 2; ++e) {
-      share[2 * e * kPitch + row] = sum[e].x;
-      share[(2 * e + 1) * kPitch + row] = sum[e].y;
+      share[2 * e * ss + row * sl] = sum[e].x;
+      share[(2 * e + 1) * ss + row * sl] = sum[e].y;
     }
   }
   __syncthreads();
@@ -255,10 +260,11 @@ __global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
     const int outer_i = b0 + (i >> shift), inner_i = i & (inner - 1);
     const int l = p.trans ? inner_i : outer_i, s = p.trans ? outer_i : inner_i;
     if (l >= nl || s >= ns) continue;
-    const uint32_t at = sbase + 4u * (uint32_t)(s * kPitch + l);
+    const int word = outer_i * share_pitch(p.trans, TS) + inner_i;
+    const uint32_t at = sbase + 4u * (uint32_t)word;
     float v = 0.0f;
     if (p.split == 1) {
-      v = share[s * kPitch + l];
+      v = share[word];
     } else {
       float u[8];
 #pragma unroll
@@ -320,7 +326,7 @@ __global__ void __launch_bounds__(256) scale_kernel(const Fp8Out o) {
 
 size_t fp8_short_smem(int tile_s, int stages, int stage_bytes) {
   const size_t ring = (size_t)stages * stage_bytes + (size_t)f8::kChunks * f8::chunk_floats(tile_s) * 4;
-  const size_t share = (size_t)tile_s * f8::kPitch * 4;
+  const size_t share = (size_t)f8::share_words(tile_s) * 4;
   return (ring > share ? ring : share) + 1024;
 }
 
