@@ -108,17 +108,29 @@ int64_t repack_bytes(const Operand& o) {
   return aligned(o.m->data, 16) && o.m->ld % 16 == 0 ? 0 : round256(o.rows * repack_ld(o));
 }
 
-// Times in ns that the choice of kernel goes by (measured on a GB300, to a few per cent): a group of
-// 128 k and the rest of a tile in the pair kernel, by tile width; a group in a short-side CTA that has
-// its SM to itself; and what a launch takes apart from its groups.
-struct TileCost {
+// Times in ns that the choice of kernel goes by, fitted to 700 launches of 44 products (M, N, K from 1
+// to 16384) forced to each kernel, tile and split on a GB300: they give those launches' times to about
+// 15%, and for 34 further products the launch they choose took 4% longer than the fastest on average, 33%
+// at most.  In the pair kernel, by tile width: a group of 128 k, and the rest of a tile.  On the short
+// side: a group in a CTA that has its SM to itself, the rest of a tile, and what joining a tile's shares
+// adds to it.
+struct PairCost {
   int tile, group_ns, tile_ns;
 };
-constexpr TileCost kPairCost[] = {{256, 430, 1000}, {128, 310, 600}, {64, 270, 400}};
-constexpr TileCost kPairColsCost[] = {{256, 680, 1500}, {128, 440, 900}, {64, 310, 600}};  // B scaled by column
-constexpr TileCost kShortCost[] = {{16, 310, 0}, {32, 330, 0}, {64, 460, 0}, {128, 680, 0}};
-constexpr double kPairLaunchNs = 4000, kShortLaunchNs = 4500;
-constexpr double kSmBytesPerNs = 44.7;  // an SM's share of the memory bandwidth
+constexpr PairCost kPairCost[] = {{256, 390, 3200}, {128, 325, 1850}, {64, 295, 950}};
+constexpr PairCost kPairColsCost[] = {{256, 605, 3450}, {128, 490, 1650}, {64, 430, 1000}};  // B scaled by column
+struct ShortCost {
+  int tile, group_ns, tile_ns, join_ns;
+};
+constexpr ShortCost kShortCost[] = {{16, 310, 1500, 800}, {32, 330, 2400, 500}, {64, 445, 4100, 650}, {128, 545, 7300, 1550}};
+constexpr double kPairLaunchNs = 4950, kShortLaunchNs = 2750;
+constexpr double kSharedSm = 0.3;        // a group takes this much longer with a second CTA on the SM
+constexpr double kSmBytesPerNs = 44.7;   // an SM's share of the memory bandwidth
+
+// SMs that clusters of `split` CTAs can use at a time: groups of 4 or 8 do not fill every part of the chip.
+int64_t cluster_sms(int sm_count, int split) {
+  return split <= 2 ? sm_count : std::max(1, split == 4 ? sm_count * 18 / 19 : sm_count * 16 / 19);
+}
 
 int64_t short_ring(int tile) { return (tile == 128 ? 2 : 1) * 98 * 1024; }  // stages of two CTAs (one) per SM
 int short_ctas_per_sm(int tile) { return tile == 128 ? 1 : 2; }
@@ -136,23 +148,24 @@ Choice choose(const Product& pr, int64_t clusters, int sm_count, int variant, in
     if (ns < best.ns) best = Choice{v, n, k, ns};
   };
   if (variant != SGEMM_VARIANT_FP8_SHORT)
-    for (const TileCost& c : pr.b.scales.shift == 0 ? kPairColsCost : kPairCost) {
+    for (const PairCost& c : pr.b.scales.shift == 0 ? kPairColsCost : kPairCost) {
       if (tile != 0 && tile != c.tile) continue;
       const int64_t rounds = ceil_div(ceil_div(pr.M, 256) * ceil_div(pr.N, c.tile), clusters);
       offer(SGEMM_VARIANT_FP8_PAIR, c.tile, 1, kPairLaunchNs + (double)rounds * (groups * c.group_ns + c.tile_ns));
     }
   if (variant != SGEMM_VARIANT_FP8_PAIR)
-    for (const TileCost& c : kShortCost) {
-      if (tile != 0 ? tile != c.tile : c.tile < 128 && S > c.tile) continue;  // the narrowest that holds the short side
-      const int64_t tiles = ceil_div(L, 128) * ceil_div(S, c.tile), slots = (int64_t)sm_count * short_ctas_per_sm(c.tile);
+    for (const ShortCost& c : kShortCost) {
+      if (tile != 0 ? tile != c.tile : c.tile > 16 && c.tile >= 2 * S) continue;
+      const int64_t tiles = ceil_div(L, 128) * ceil_div(S, c.tile);
       for (int k = 1; k <= 8; k *= 2) {
         if (split != 0 ? split != k : k > 1 && groups < 2 * k) continue;  // two groups per CTA at least
-        const double on_sm = std::min((double)short_ctas_per_sm(c.tile), std::max(1.0, (double)tiles * k / sm_count));
-        const double group = std::max<double>(c.group_ns, on_sm * (16384 + 64 * c.tile) / kSmBytesPerNs);
+        const int per_sm = short_ctas_per_sm(c.tile);
+        const double on_sm = std::min((double)per_sm, std::max(1.0, (double)tiles * k / sm_count));
+        const double group = std::max(c.group_ns * (1.0 + kSharedSm * (on_sm - 1.0)), on_sm * (16384 + 64 * c.tile) / kSmBytesPerNs);
+        const double rounds = (double)ceil_div(tiles * k, cluster_sms(sm_count, k) * per_sm);
         offer(SGEMM_VARIANT_FP8_SHORT, c.tile, k,
-              kShortLaunchNs + (double)ceil_div(tiles * k, slots) * ceil_div(groups, k) * group);
+              kShortLaunchNs + rounds * (ceil_div(groups, k) * group + c.tile_ns + (k > 1 ? c.join_ns : 0)));
       }
-      if (tile == 0) break;
     }
   return best;
 }
