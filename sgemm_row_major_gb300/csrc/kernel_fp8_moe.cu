@@ -28,6 +28,12 @@
 // Both: one CTA per SM with as many 16 KB weight tiles in flight as half its shared memory holds; warp 0
 // loads (TMA), warp 1 issues the products, warp 2 loads scales a chunk of groups ahead, warps 4-7 fold
 // the accumulators (two alternate) into FP32 sums in registers.
+//
+// What bounds it: the weights' bytes.  32 tokens, 64 experts of 2048 x 1024, 8 each (397 MB): 100 us,
+// 4.0 TB/s; the routing and the first loads take 6 us, the first kernel's last round of tiles is part empty,
+// and while one kernel runs out the other has half of an SM's shared memory.  One token (50 MB): 26 us,
+// of which the launch, the routing, the two streams of about 4 us each, the wait between the kernels
+// and the last sums follow one another.
 #include <algorithm>
 
 #include "fp8_gemm.cuh"
