@@ -53,6 +53,19 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 
+// Whether a barrier phase is complete, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+  uint32_t done;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(done)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return done != 0;
+}
+
 // Bounded wait of a whole warp for a barrier phase, for waits that are short: every lane polls (each
 // has its own acquire), the clock is read only now and then, and nothing is called, so the sums that
 // the fold keeps in registers stay there.  Warp-uniform.
@@ -121,6 +134,22 @@ __device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
     if constexpr (N >= 16) tmem_ld16(taddr, *reinterpret_cast<float(*)[16]>(v));
     if constexpr (N % 16 == 8) tmem_ld8(taddr + (N >= 16 ? 16u : 0u), v + (N >= 16 ? 16 : 0));
   }
+}
+
+// 16 rows x 32 columns of this warp's TMEM lanes from taddr's lane on, as the tensor cores' own fragments
+// lie: thread t receives of rows t / 4 and t / 4 + 8, for each 8 columns, columns 2 (t % 4) and the next
+// (v[4 j], v[4 j + 1] of the first row, v[4 j + 2], v[4 j + 3] of the second).
+__device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, float* v) {
+  uint32_t r[16];
+  asm volatile(
+      "tcgen05.ld.sync.aligned.16x256b.x4.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
 // 4 bytes from global to shared memory, asynchronously.

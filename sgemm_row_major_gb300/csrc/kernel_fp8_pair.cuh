@@ -12,11 +12,11 @@
 //
 // What bounds it: at tile_n = 256 the tensor cores need 512 cycles for a group, the folders 256 cycles of
 // the FMA pipes (512 with a scale per column) and as many of the TMEM's reading width, and both run at the
-// same time.  A group takes 740 cycles all the same (1200 with a scale per column): with two accumulators
+// same time.  A group takes 740 cycles all the same (1080 with a scale per column): with two accumulators
 // in the TMEM the chain of handing one over (the commit's arrival, the folders' first load, the last load,
 // the arrival at the issuer) is longer than the other's products.  Without the fold it would be 540.
 // Measured: 8192^3 with BF16 output 390 us, 2.8 PFLOP/s; 4096^3 63 us; the gradient 4096 x 4096 x 8192 of
-// both operands with column groups, added to FP32, 182 us.  Narrower tiles need 325 ns (128) and 295 ns
+// both operands with column groups, added to FP32, 171 us.  Narrower tiles need 325 ns (128) and 295 ns
 // (64) for a group of a half and a quarter of the products, and pay where the last round of 256-wide tiles
 // would be far from full.
 //
@@ -46,8 +46,9 @@ constexpr int kStages = kFp8PairStages;
 constexpr int kChunk = 8;                 // groups whose scales are loaded together
 constexpr int kOutPitch = 36;             // words between the rows of a warp's 32 x 32 piece of D (16-byte accesses
                                           // by row and by column both hit 32 banks)
+constexpr int kOutPitchFragments = 40;    // the same where a lane holds pairs of columns of 4 rows (8-byte accesses)
 constexpr int kOutBytes = 5 * 1024;       // of shared memory per folding warp (pieces for TMA: 4 KB, 1024-byte aligned)
-static_assert(32 * kOutPitch * 4 <= kOutBytes, "a piece of D");
+static_assert(32 * kOutPitch * 4 <= kOutBytes && 32 * kOutPitchFragments * 4 <= kOutBytes, "a piece of D");
 constexpr int kFirstFold = 4;             // warps 0-3: loads, products, scales of A, scales of B
 constexpr int kFoldWarps = 8;
 constexpr int kThreads = 32 * (kFirstFold + kFoldWarps);
@@ -85,7 +86,8 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
 // columns at a time in D's type, rows of 64 (BF16) or 128 bytes with the swizzle of that width, so that
 // the lanes' 16-byte stores to shared memory hit different banks.  Two BF16 pieces or one of FP32 fit
 // in the warp's buffer; a piece is written when the copy that read its place before is done reading.
-template <bool BF16, int N>
+// FRAGMENTS: a lane holds pairs of columns of 4 rows instead (tmem_ld_fragments).
+template <bool BF16, bool FRAGMENTS, int N>
 __device__ __forceinline__ void tma_out(const CUtensorMap& map, uint8_t* buf, const Fp8Out& o, int row0, int col0,
                                         const float2 (&sum)[N]) {
   const int lane = threadIdx.x & 31;
@@ -99,24 +101,38 @@ __device__ __forceinline__ void tma_out(const CUtensorMap& map, uint8_t* buf, co
       else      asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     }
     __syncwarp();
+    if constexpr (FRAGMENTS) {
 #pragma unroll
-    for (int e = 0; e < (BF16 ? 4 : 8); ++e) {  // 16 bytes
-      uint4 u;
-      if constexpr (BF16) {
-        uint32_t w[4];
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float2 x = __fmul2_rn(sum[16 * piece + 4 * e + k], alpha);
-          const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
-          w[k] = *reinterpret_cast<const uint32_t*>(&b);
+      for (int e = 0; e < 16; ++e) {  // 2 columns
+        const int row = (lane >> 2) + 8 * (e % 4), col = 8 * (e / 4) + 2 * (lane & 3);
+        const float2 x = __fmul2_rn(sum[16 * piece + e], alpha);
+        if constexpr (BF16) {
+          *reinterpret_cast<__nv_bfloat162*>(at + row * 64 + 16 * ((col >> 3) ^ ((row >> 1) & 3)) + 2 * (col & 7)) =
+              __floats2bfloat162_rn(x.x, x.y);
+        } else {
+          *reinterpret_cast<float2*>(at + row * 128 + 16 * ((col >> 2) ^ (row & 7)) + 4 * (col & 3)) = x;
         }
-        u = make_uint4(w[0], w[1], w[2], w[3]);
-      } else {
-        const float2 x = __fmul2_rn(sum[16 * piece + 2 * e], alpha), y = __fmul2_rn(sum[16 * piece + 2 * e + 1], alpha);
-        u = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
       }
-      const int chunk = BF16 ? e ^ ((lane >> 1) & 3) : e ^ (lane & 7);
-      *reinterpret_cast<uint4*>(at + lane * (BF16 ? 64 : 128) + 16 * chunk) = u;
+    } else {
+#pragma unroll
+      for (int e = 0; e < (BF16 ? 4 : 8); ++e) {  // 16 bytes
+        uint4 u;
+        if constexpr (BF16) {
+          uint32_t w[4];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 x = __fmul2_rn(sum[16 * piece + 4 * e + k], alpha);
+            const __nv_bfloat162 b = __floats2bfloat162_rn(x.x, x.y);
+            w[k] = *reinterpret_cast<const uint32_t*>(&b);
+          }
+          u = make_uint4(w[0], w[1], w[2], w[3]);
+        } else {
+          const float2 x = __fmul2_rn(sum[16 * piece + 2 * e], alpha), y = __fmul2_rn(sum[16 * piece + 2 * e + 1], alpha);
+          u = make_uint4(__float_as_uint(x.x), __float_as_uint(x.y), __float_as_uint(y.x), __float_as_uint(y.y));
+        }
+        const int chunk = BF16 ? e ^ ((lane >> 1) & 3) : e ^ (lane & 7);
+        *reinterpret_cast<uint4*>(at + lane * (BF16 ? 64 : 128) + 16 * chunk) = u;
+      }
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -339,6 +355,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
     for (int e = 0; e < cols / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
     bool ok = true;
+    bool seen = false;                      // the group's products were done when last looked at (COLS)
     int s = 0, b = 0, c = 0;                // stage, accumulator and scale chunk of the next group
     uint32_t s_lap = 0, c_lap = 0;
     for (int i = 0; ok && i < my_tiles; ++i) {
@@ -350,7 +367,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       for (int g = 0; g < groups; ++g) {
         const int in_chunk = g & (kChunk - 1);
         if (in_chunk == 0) ok = poll_wait(smem_addr(&scale_full[c]), c_lap & 1u, p.timeout_ns);
-        ok = ok && poll_wait(smem_addr(&done[s]), s_lap & 1u, p.timeout_ns);
+        if (!COLS || !__all_sync(0xffffffffu, seen)) ok = ok && poll_wait(smem_addr(&done[s]), s_lap & 1u, p.timeout_ns);
         if (!ok) {
           if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
           break;
@@ -359,7 +376,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const uint32_t acc = tq + (uint32_t)(b * TN);
         const float* sc = scales + c * Sc::kFloats;
         const float* scb = sc + kChunk * BMC + in_chunk * Sc::kB + b_at;
-        float sa = 0.0f, s0 = 0.0f;
+        float s0 = 0.0f;
         // 32 columns at a time, the next ones on their way while these are added
         const auto add = [&](auto first, float* v) {
           constexpr int kFirst = decltype(first)::value, kCount = cols - kFirst < kLoadCols ? cols - kFirst : kLoadCols;
@@ -378,6 +395,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           constexpr int kFirst = decltype(first)::value, kCount = cols - kFirst < kLoadCols ? cols - kFirst : kLoadCols;
           tmem_ld<kCount>(acc + (uint32_t)kFirst, v);
         };
+        // With a scale per column the fold takes longer than the products: the next group's are then done
+        // before this one's last columns are added, and asking beforehand saves the wait's latency (182 to
+        // 171 us for 4096 x 4096 x 8192; where the fold waits for the products it costs 4%).
+        const auto look = [&] {
+          const int ns = s + 1 == kStages ? 0 : s + 1;
+          seen = mbar_test(smem_addr(&done[ns]), (s_lap + (ns == 0)) & 1u);
+        };
         const auto release = [&] {  // the whole accumulator is in registers: hand it back to the issuer
           tmem_fence_before_sync();
           __syncwarp();
@@ -388,32 +412,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         constexpr std::integral_constant<int, 2 * kLoadCols> c_2{};
         constexpr std::integral_constant<int, 3 * kLoadCols> c_3{};
         if constexpr (COLS) {
-          // the columns' scales come from shared memory while the accumulator's columns do from TMEM (with
-          // the next columns' registers as well there would be too few)
-          sa = sc[in_chunk * BMC + 32 * q + lane];
-          const float2 sa2 = make_float2(sa, sa);
-          const auto scaled = [&](auto first) {
+          // as fragments a lane holds 2 of 8 columns and 4 of 32 rows: 32 column scales to read and not 128
+          float va[kLoadCols], vb[kLoadCols];
+          float2 wa[kLoadCols / 8], wb[kLoadCols / 8];
+          float rs[4];
+          const auto fetch = [&](auto first, float* v, float2* w) {
             constexpr int kFirst = decltype(first)::value;
-            float v[kLoadCols];
-            float4 w[kLoadCols / 4];
-            load(first, v);
+            tmem_ld_fragments(acc + (uint32_t)kFirst, v);
+            tmem_ld_fragments(acc + (uint32_t)kFirst + (16u << 16), v + kLoadCols / 2);
 #pragma unroll
-            for (int k = 0; k < kLoadCols / 4; ++k) w[k] = *reinterpret_cast<const float4*>(scb + kFirst + 4 * k);
-            tmem_wait_ld();
-            if (kFirst + kLoadCols == cols) release();
-#pragma unroll
-            for (int k = 0; k < kLoadCols / 4; ++k) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) asm volatile("" : "+f"(v[4 * k + e]));  // used behind the wait only
-              float2* m = &sum[kFirst / 2 + 2 * k];
-              m[0] = __ffma2_rn(__fmul2_rn(make_float2(v[4 * k], v[4 * k + 1]), make_float2(w[k].x, w[k].y)), sa2, m[0]);
-              m[1] = __ffma2_rn(__fmul2_rn(make_float2(v[4 * k + 2], v[4 * k + 3]), make_float2(w[k].z, w[k].w)), sa2, m[1]);
-            }
+            for (int j = 0; j < kLoadCols / 8; ++j)
+              w[j] = *reinterpret_cast<const float2*>(scb + kFirst + 8 * j + 2 * (lane & 3));
           };
-          scaled(c_0);
-          if constexpr (cols > c_1) scaled(c_1);
-          if constexpr (cols > c_2) scaled(c_2);
-          if constexpr (cols > c_3) scaled(c_3);
+          const auto scaled = [&](auto first, float* v, const float2* w) {
+            constexpr int kFirst = decltype(first)::value;
+#pragma unroll
+            for (int e = 0; e < kLoadCols; ++e) asm volatile("" : "+f"(v[e]));  // used behind the wait only
+#pragma unroll
+            for (int j = 0; j < kLoadCols / 8; ++j)
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {  // rows lane / 4 + 8 k
+                const float* x = v + (k / 2) * (kLoadCols / 2) + 4 * j + 2 * (k % 2);
+                float2& m = sum[kFirst / 2 + 4 * j + k];
+                m = __ffma2_rn(__fmul2_rn(make_float2(x[0], x[1]), w[j]), make_float2(rs[k], rs[k]), m);
+              }
+          };
+          fetch(c_0, va, wa);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) rs[k] = sc[in_chunk * BMC + 32 * q + (lane >> 2) + 8 * k];
+          tmem_wait_ld();
+          if constexpr (cols > c_1) fetch(c_1, vb, wb);
+          else release();
+          scaled(c_0, va, wa);
+          if constexpr (cols > c_1) {
+            tmem_wait_ld();
+            if constexpr (cols > c_2) fetch(c_2, va, wa);
+            else release();
+            scaled(c_1, vb, wb);
+          }
+          if constexpr (cols > c_2) {
+            tmem_wait_ld();
+            fetch(c_3, vb, wb);
+            scaled(c_2, va, wa);
+            tmem_wait_ld();
+            release();
+            look();
+            scaled(c_3, vb, wb);
+          }
         } else {
           float va[kLoadCols], vb[kLoadCols];
           load(c_0, va);
@@ -459,19 +504,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const int row0 = tm * BM + BMC * (int)rank + 32 * q;
       if (ok && OUT == kOutPlain) {
         // in D's type and the order TMA reads, which writes the piece (as far as it is in D) by itself
-        if (p.out.bf16) tma_out<true>(mapD, out, p.out, row0, c0, sum);
-        else            tma_out<false>(mapD, out, p.out, row0, c0, sum);
+        if (p.out.bf16) tma_out<true, COLS>(mapD, out, p.out, row0, c0, sum);
+        else            tma_out<false, COLS>(mapD, out, p.out, row0, c0, sum);
       } else if (ok) {
-        float4* mine = reinterpret_cast<float4*>(out) + lane * (kOutPitch / 4);
+        constexpr int pitch = COLS ? kOutPitchFragments : kOutPitch;
+        float* piece = reinterpret_cast<float*>(out);
 #pragma unroll
         for (int at = 0; at < cols; at += 32) {
           __syncwarp();
+          if constexpr (COLS) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e)
-            mine[e] = make_float4(sum[at / 2 + 2 * e].x, sum[at / 2 + 2 * e].y, sum[at / 2 + 2 * e + 1].x,
-                                  sum[at / 2 + 2 * e + 1].y);
+            for (int e = 0; e < 16; ++e)
+              *reinterpret_cast<float2*>(piece + ((lane >> 2) + 8 * (e % 4)) * pitch + 8 * (e / 4) + 2 * (lane & 3)) =
+                  sum[at / 2 + e];
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+              *reinterpret_cast<float4*>(piece + lane * pitch + 4 * e) =
+                  make_float4(sum[at / 2 + 2 * e].x, sum[at / 2 + 2 * e].y, sum[at / 2 + 2 * e + 1].x,
+                              sum[at / 2 + 2 * e + 1].y);
+          }
           __syncwarp();
-          store_piece<OUT>(p.out, row0, c0 + at, reinterpret_cast<const float*>(out), kOutPitch);
+          store_piece<OUT>(p.out, row0, c0 + at, piece, pitch);
         }
       }
 #pragma unroll
