@@ -27,7 +27,7 @@
 //
 // Both: one CTA per SM with as many 16 KB weight tiles in flight as half its shared memory holds; warp 0
 // loads (TMA), warp 1 issues the products, warp 2 loads scales a chunk of groups ahead, warps 4-7 fold
-// the accumulators (two alternate) into FP32 sums in registers.
+// the accumulators (several alternate) into FP32 sums in registers.
 //
 // What bounds it: the weights' bytes.  32 tokens, 64 experts of 2048 x 1024, 8 each (397 MB): 100 us,
 // 4.0 TB/s; the routing and the first loads take 6 us, the first kernel's last round of tiles is part empty,
@@ -306,7 +306,12 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
                                                              const __grid_constant__ MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], done[kMaxStages];
-  __shared__ __align__(8) uint64_t acc_empty[2];
+  // accumulators: as many as 128 columns hold, so that products and loads go on while an item's sums are
+  // worked into h; no more than stages, as a stage's second commit must not precede the folders' look at
+  // its first
+  constexpr int kBufs = 128 / NC;
+  const int bufs = kBufs <= 2 ? kBufs : min(kBufs, p.up_stages);  // (there are 2 stages at least)
+  __shared__ __align__(8) uint64_t acc_empty[kBufs];
   __shared__ __align__(8) uint64_t scale_full[kChunks], scale_empty[kChunks];
   __shared__ uint32_t tmem_slot;
 
@@ -329,7 +334,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&done[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) mbar_init(smem_addr(&acc_empty[b]), kFoldWarps);
+    for (int b = 0; b < kBufs; ++b) mbar_init(smem_addr(&acc_empty[b]), kFoldWarps);
     for (int c = 0; c < kChunks; ++c) {
       mbar_init(smem_addr(&scale_full[c]), 32);
       mbar_init(smem_addr(&scale_empty[c]), kFoldWarps);
@@ -393,11 +398,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
     constexpr uint32_t step = 32u >> 4;
     const uint32_t desc0 = desc_lo(sbase);
     const int units = my_items * groups;
-    int t = 0, s = 0;
-    uint32_t lap = 0;
+    int t = 0, s = 0, b = 0;
+    uint32_t lap = 0, b_lap = 0;
     for (; t < units; ++t) {
-      const int b = t & 1;
-      if ((t >= 2 && !poll_wait(smem_addr(&acc_empty[b]), (uint32_t)((t / 2) - 1) & 1u, p.timeout_ns)) ||
+      if ((b_lap > 0 && !poll_wait(smem_addr(&acc_empty[b]), (b_lap - 1) & 1u, p.timeout_ns)) ||
           !poll_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns)) {
         if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
         break;
@@ -407,11 +411,15 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
         const uint32_t wd = desc0 + (uint32_t)(s * (stage_bytes >> 4)), xd = wd + (kWTile >> 4);
 #pragma unroll
         for (uint32_t ks = 0; ks < BK / 32; ++ks)
-          mma_f8(tmem + (uint32_t)b * 64u, make_desc(wd + ks * step), make_desc(xd + ks * step), moe_idesc(NC),
+          mma_f8(tmem + (uint32_t)(b * NC), make_desc(wd + ks * step), make_desc(xd + ks * step), moe_idesc(NC),
                  ks == 0 ? 0u : 1u);
         mma_commit(smem_addr(&done[s]));  // the stage is free, the accumulator holds group t
       }
       __syncwarp();
+      if (++b == bufs) {
+        b = 0;
+        ++b_lap;
+      }
       if (++s == p.up_stages) {
         s = 0;
         ++lap;
@@ -480,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
         for (int j0 = 0; j0 < NC; j0 += 32) {
           constexpr int kCols = NC < 32 ? NC : 32;
           float v[kCols];
-          tmem_ld<kCols>(tq + (uint32_t)(64 * b + j0), v);
+          tmem_ld<kCols>(tq + (uint32_t)(b * NC + j0), v);
           tmem_wait_ld();
           if (j0 + kCols == NC) {
             tmem_fence_before_sync();
@@ -505,7 +513,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
             ++c_lap;
           }
         }
-        b ^= 1;
+        if (++b == bufs) b = 0;
         if (++s == p.up_stages) {
           s = 0;
           ++s_lap;
@@ -573,7 +581,6 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
                                                                const __grid_constant__ MoeParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], done[kMaxStages];
-  __shared__ __align__(8) uint64_t acc_empty[2];
   __shared__ __align__(8) uint64_t scale_full[kChunks], scale_empty[kChunks];
   __shared__ uint32_t tmem_slot;
   __shared__ int last_tiles[2], n_last;  // tiles whose last sums are this CTA's (of two that it shares at most)
@@ -584,8 +591,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
   constexpr int stage_bytes = kWTile + 2 * NC * BK;
   constexpr int kChunkFloats = 2 * kChunkGroups * NC + kChunkGroups;  // slots' scales of 16 halves, weights' of 8 units
   constexpr uint32_t kHalfCols = 2 * NC, kAccCols = 4 * NC;           // of an accumulator: a unit's two halves
-  constexpr int kBufs = NC == 64 ? 1 : 2;
-  constexpr uint32_t kTmemCols = kBufs * kAccCols;  // at most 256: 128 of an SM's 512 are the first kernel's
+  constexpr uint32_t kTmemCols = 256;               // 128 of an SM's 512 are the first kernel's
+  constexpr int kBufs = kTmemCols / kAccCols;
+  const int bufs = kBufs <= 2 ? kBufs : min(kBufs, p.down_stages);  // as in the first kernel
+  __shared__ __align__(8) uint64_t acc_empty[kBufs];
   float* chunks = reinterpret_cast<float*>(smem_raw + pad + p.down_stages * stage_bytes);
   float* ysum = chunks + kChunks * kChunkFloats;  // [tokens][128]
   const Route r = route_at(p, ysum + p.tokens * 128);
@@ -601,7 +610,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&done[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) mbar_init(smem_addr(&acc_empty[b]), kFoldWarps);
+    for (int b = 0; b < kBufs; ++b) mbar_init(smem_addr(&acc_empty[b]), kFoldWarps);
     for (int c = 0; c < kChunks; ++c) {
       mbar_init(smem_addr(&scale_full[c]), 32);
       mbar_init(smem_addr(&scale_empty[c]), kFoldWarps);
@@ -693,12 +702,11 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
     // a unit's two halves of 64 inner columns have scales, and so columns of the accumulator, of their own
     constexpr uint32_t step = 32u >> 4;
     const uint32_t desc0 = desc_lo(sbase);
-    int t = 0, s = 0;
+    int t = 0, s = 0, b = 0;
     Place u = first;
-    uint32_t lap = 0;
+    uint32_t lap = 0, b_lap = 0;
     for (; t < mine; ++t, next(&u)) {
-      const int b = t % kBufs;
-      if ((t >= kBufs && !poll_wait(smem_addr(&acc_empty[b]), (uint32_t)((t / kBufs) - 1) & 1u, p.timeout_ns)) ||
+      if ((b_lap > 0 && !poll_wait(smem_addr(&acc_empty[b]), (b_lap - 1) & 1u, p.timeout_ns)) ||
           !poll_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns)) {
         if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
         break;
@@ -714,6 +722,10 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
         mma_commit(smem_addr(&done[s]));  // the stage is free, the accumulator holds unit t
       }
       __syncwarp();
+      if (++b == bufs) {
+        b = 0;
+        ++b_lap;
+      }
       if (++s == p.down_stages) {
         s = 0;
         ++lap;
@@ -815,7 +827,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
               if (w2 != 0.0f) sum[j0 + j] = fmaf(v1 * f1[j], w2, sum[j0 + j]);
             }
           }
-          if (++b == kBufs) b = 0;
+          if (++b == bufs) b = 0;
           if (++s == p.down_stages) {
             s = 0;
             ++s_lap;
