@@ -17,7 +17,7 @@
 //
 // What bounds it: a stream of the long operand, but a CTA starts, folds and joins in 4 us and takes 310 ns
 // (16 columns) to 545 ns (128) for a group, where its 16 KB are 370 ns of an SM's share of the memory's
-// bandwidth: 1 x 4096 x 4096 (17 MB) 6.8 us, 64 x 4096 x 16384 (68 MB) 19.3 us, 3.6 TB/s.  More shares
+// bandwidth: 1 x 4096 x 4096 (17 MB) 6.2 us, 64 x 4096 x 16384 (68 MB) 19.3 us, 3.6 TB/s.  More shares
 // shorten the groups' part and lengthen the joining.
 #include "fp8_gemm.cuh"
 
@@ -55,7 +55,11 @@ __global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
                      const __grid_constant__ Fp8ShortParams p) {
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t full[kMaxStages], done[kMaxStages];
-  __shared__ __align__(8) uint64_t acc_empty[2];
+  // accumulators: 4 where two CTAs' fit, no more than stages (a stage's second commit must not precede the
+  // folders' look at its first)
+  constexpr int kBufs = TS == 128 ? 2 : 4;
+  const int bufs = min(kBufs, p.stages);
+  __shared__ __align__(8) uint64_t acc_empty[kBufs];
   __shared__ __align__(8) uint64_t scale_full[kChunks], scale_empty[kChunks];
   __shared__ uint32_t tmem_slot;
 
@@ -72,7 +76,7 @@ __global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
   const int g0 = (int)((int64_t)groups * rank / p.split), g1 = (int)((int64_t)groups * (rank + 1) / p.split);
   const int units = g1 - g0;
   constexpr uint32_t kAccCols = TS < 32 ? 32u : (uint32_t)TS;
-  constexpr uint32_t kTmemCols = 2 * kAccCols;
+  constexpr uint32_t kTmemCols = kBufs * kAccCols;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
@@ -82,7 +86,7 @@ __global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&done[s]), 1);
     }
-    for (int b = 0; b < 2; ++b) mbar_init(smem_addr(&acc_empty[b]), kFoldWarps);
+    for (int b = 0; b < kBufs; ++b) mbar_init(smem_addr(&acc_empty[b]), kFoldWarps);
     for (int c = 0; c < kChunks; ++c) {
       mbar_init(smem_addr(&scale_full[c]), 32);
       mbar_init(smem_addr(&scale_empty[c]), kFoldWarps);
@@ -129,11 +133,10 @@ __global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
   } else if (warp == 1) {
     // ------------------------------------------------ products
     const uint32_t lstep = step_of(p.l_mn), sstep = step_of(p.s_mn), desc0 = desc_lo(sbase);
-    int t = 0, s = 0;
-    uint32_t lap = 0;
+    int t = 0, s = 0, b = 0;
+    uint32_t lap = 0, b_lap = 0;
     for (; t < units; ++t) {
-      const int b = t & 1;
-      if ((t >= 2 && !poll_wait(smem_addr(&acc_empty[b]), (uint32_t)((t / 2) - 1) & 1u, p.timeout_ns)) ||
+      if ((b_lap > 0 && !poll_wait(smem_addr(&acc_empty[b]), (b_lap - 1) & 1u, p.timeout_ns)) ||
           !poll_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns)) {
         if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
         break;
@@ -148,6 +151,10 @@ __global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
         mma_commit(smem_addr(&done[s]));  // the stage is free, the accumulator holds group t
       }
       __syncwarp();
+      if (++b == bufs) {
+        b = 0;
+        ++b_lap;
+      }
       if (++s == p.stages) {
         s = 0;
         ++lap;
@@ -189,10 +196,10 @@ __global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
 #pragma unroll
     for (int e = 0; e < TS / 2; ++e) sum[e] = make_float2(0.0f, 0.0f);
     bool ok = true;
-    int s = 0, c = 0;
+    int s = 0, c = 0, b = 0;
     uint32_t s_lap = 0, c_lap = 0;
     for (int t = 0; t < units; ++t) {
-      const int b = t & 1, in_chunk = t & (kChunkGroups - 1);
+      const int in_chunk = t & (kChunkGroups - 1);
       if (in_chunk == 0) ok = poll_wait(smem_addr(&scale_full[c]), c_lap & 1u, p.timeout_ns);
       ok = ok && poll_wait(smem_addr(&done[s]), s_lap & 1u, p.timeout_ns);
       if (!ok) {
@@ -232,6 +239,7 @@ __global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
           ++c_lap;
         }
       }
+      if (++b == bufs) b = 0;
       if (++s == p.stages) {
         s = 0;
         ++s_lap;
