@@ -111,22 +111,23 @@ def _ld(x) -> int:
     return _rows(x, "tensor")[2]
 
 
-def _empty(shape, dtype, like, stream):
-    """Uninitialised memory that belongs to the stream the call runs on."""
+def _empty(shape, dtype, like, stream, ld=None):
+    """Uninitialised memory that belongs to the stream the call runs on; ld: the row stride where it is not the width."""
     if stream is None:
+        if ld is not None:
+            return _T.empty_strided(shape, (ld, 1), dtype=dtype, device=like.device)
         return _T.empty(shape, dtype=dtype, device=like.device)
     if not hasattr(stream, "cuda_stream"):
         stream = _T.cuda.ExternalStream(int(stream), device=like.device) if stream else _T.cuda.default_stream(like.device)
     with _T.cuda.stream(stream):
-        return _T.empty(shape, dtype=dtype, device=like.device)
+        return _empty(shape, dtype, like, None, ld)
 
 
 def _empty_rows(rows, cols, like, stream):
     """(tensor, row stride): an uninitialised rows x cols tensor of like's type whose rows start at multiples of 16
     bytes, as the kernels write them fastest."""
     ld = (cols + 7) // 8 * 8
-    x = _empty((rows, ld), like.dtype, like, stream)
-    return (x if ld == cols else x[:, :cols]), ld or 1
+    return _empty((rows, cols), like.dtype, like, stream, None if ld == cols else ld), ld or 1
 
 
 class Fp8Matrix:
@@ -159,9 +160,7 @@ def _new_matrix(rows, cols, block, fmt, like, stream):
     """An Fp8Matrix of uninitialised codes and scales; rows start at multiples of 16 bytes."""
     dtype = _T.float8_e5m2 if fmt else _T.float8_e4m3fn
     ld = (cols + 15) // 16 * 16
-    data = _empty((rows, ld), dtype, like, stream)
-    if ld != cols:
-        data = data[:, :cols]
+    data = _empty((rows, cols), dtype, like, stream, None if ld == cols else ld)
     br, bc = block
     scols = -(-cols // bc)
     m = Fp8Matrix.__new__(Fp8Matrix)

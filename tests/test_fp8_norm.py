@@ -217,3 +217,41 @@ def test_refusals():
         assert lib.sgemm_fp8_rmsnorm_backward(*bad) == -index, (index, value)
     wide = [4, 49153, 0, FAKE, 49153, FAKE, 49153, FAKE, FAKE, None, 0, FAKE, 49153, FAKE, None]
     assert lib.sgemm_fp8_rmsnorm_backward(*wide) == 4  # SGEMM_ERR_UNSUPPORTED, before the device is looked at
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("cols", [1, 130, 1000, 1001])
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("pad", [0, 1, 16])
+def test_nothing_is_written_between_rows(cols, dtype, pad):
+    """What lies between an output's rows, and behind its last one, keeps its value."""
+    import torch
+    from sgemm_row_major_gb300 import fp8
+    lib, t = fp8._lib(), getattr(torch, dtype)
+    code = {"float32": 0, "bfloat16": 1}[dtype]
+    rows, ld = 3, -(-cols // 16) * 16 + pad
+    groups = -(-cols // 128)
+    g = torch.Generator(device="cuda").manual_seed(cols)
+    x, r, w = (torch.randn(n, cols, device="cuda", generator=g).to(t) for n in (rows, rows, 1))
+    stream = torch.cuda.current_stream().cuda_stream
+
+    def padded(dtype):
+        return torch.full((rows + 1, ld), 7.0, device="cuda").to(dtype)
+
+    def kept(out):
+        flat = out.float()
+        return bool((flat[:rows, cols:] == 7.0).all()) and bool((flat[rows:] == 7.0).all())
+
+    h, y, dx, q, codes = padded(t), padded(t), padded(t), padded(torch.float8_e4m3fn), padded(torch.float8_e4m3fn)
+    s, s2 = (torch.full((rows + 1, groups + 1), 7.0, device="cuda") for _ in range(2))
+    rstd, dw = torch.full((rows + 1,), 7.0, device="cuda"), torch.full((cols + 1,), 7.0, device="cuda")
+    assert lib.sgemm_fp8_rmsnorm(rows, cols, code, x.data_ptr(), cols, r.data_ptr(), cols, w.data_ptr(), 1e-6, h.data_ptr(), ld,
+                                 y.data_ptr(), ld, q.data_ptr(), ld, s.data_ptr(), groups + 1, rstd.data_ptr(), stream) == 0
+    assert lib.sgemm_fp8_rmsnorm_backward(rows, cols, code, x.data_ptr(), cols, h.data_ptr(), ld, w.data_ptr(), rstd.data_ptr(),
+                                          r.data_ptr(), cols, dx.data_ptr(), ld, dw.data_ptr(), stream) == 0
+    assert lib.sgemm_fp8_quantize(rows, cols, x.data_ptr(), code, cols, 0, 1, 128, codes.data_ptr(), ld, s2.data_ptr(), groups + 1,
+                                  stream) == 0
+    torch.cuda.synchronize()
+    assert all(kept(o) for o in (h, y, dx, q, codes))
+    assert all(bool((o[:rows, groups:] == 7.0).all()) and bool((o[rows:] == 7.0).all()) for o in (s, s2))
+    assert float(rstd[rows]) == 7.0 and float(dw[cols]) == 7.0
