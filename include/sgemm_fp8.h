@@ -70,8 +70,11 @@ typedef struct sgemm_fp8_matrix_t {
  *   - Errors per element, against the sum taken exactly: at most
  *     (K + 2) 2^-24 (|alpha| sum|a b| + |beta c|), then one rounding to `type`.
  *     NaN codes, E5M2 infinities and non-finite scales give the values the
- *     formula gives, except that a pair of scales whose product is beyond
- *     FLT_MAX is used as +-Inf (0 * Inf = NaN).
+ *     formula gives.  The two scales of a pair are multiplied first, in FP32:
+ *     a product beyond FLT_MAX is +-Inf (0 * Inf = NaN), one below 2^-126 has
+ *     the bits of a subnormal number or is 0.  The bound is for elements whose
+ *     pairs' products are zero or in between, and whose sum (before alpha) and
+ *     its terms are.
  *   - Fast where both code arrays are 16-byte aligned with ld % 16 == 0; others
  *     are first copied to aligned rows (in the workspace).
  * Arguments: 1 transA, 2 transB, 3 M, 4 N, 5 K, 6 alpha, 7 A, 8 B, 9 beta, 10 C,

@@ -434,7 +434,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               for (int k = 0; k < 4; ++k) {  // rows lane / 4 + 8 k
                 const float* x = v + (k / 2) * (kLoadCols / 2) + 4 * j + 2 * (k % 2);
                 float2& m = sum[kFirst / 2 + 4 * j + k];
-                m = __ffma2_rn(__fmul2_rn(make_float2(x[0], x[1]), w[j]), make_float2(rs[k], rs[k]), m);
+                // the two scales first: either alone may be far from 1
+                m = __ffma2_rn(make_float2(x[0], x[1]), __fmul2_rn(w[j], make_float2(rs[k], rs[k])), m);
               }
           };
           fetch(c_0, va, wa);

@@ -227,8 +227,9 @@ __global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
         for (int j = 0; j < kCols; j += 4) {
           const float4 w = *reinterpret_cast<const float4*>(sc + BL + j0 + j);
           float2* m = &sum[(j0 + j) / 2];
-          m[0] = __ffma2_rn(__fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(w.x, w.y)), l2, m[0]);
-          m[1] = __ffma2_rn(__fmul2_rn(make_float2(v[j + 2], v[j + 3]), make_float2(w.z, w.w)), l2, m[1]);
+          // the two scales first: either alone may be far from 1
+          m[0] = __ffma2_rn(make_float2(v[j], v[j + 1]), __fmul2_rn(make_float2(w.x, w.y), l2), m[0]);
+          m[1] = __ffma2_rn(make_float2(v[j + 2], v[j + 3]), __fmul2_rn(make_float2(w.z, w.w), l2), m[1]);
         }
       }
       if (in_chunk == kChunkGroups - 1) {

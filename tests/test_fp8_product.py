@@ -220,6 +220,31 @@ def test_wide_range_of_scales():
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kernel,tile", [("FP8_PAIR", 64), ("FP8_PAIR", 256), ("FP8_SHORT", 16), ("FP8_SHORT", 64), ("FP8_SHORT", 128)])
+@pytest.mark.parametrize("ops,ga,gb", [("NT", 1, 128), ("TN", 1, 1), ("NN", 128, 128), ("TT", 128, 1)])
+@pytest.mark.parametrize("swap", [False, True])
+def test_each_scale_may_be_extreme(force, kernel, tile, ops, ga, gb, swap):
+    """Scales from 2^-126 to 2^120 on either side whose products are ordinary.  A group's sum times one of them alone would
+    be beyond FP32 (codes up to 448), or lose its bits (three products of codes of at most 7 2^-9)."""
+    import torch
+    force(kernel, tile)
+    for M, N, K in ((130, 140, 200), (140, 130, 200), (130, 140, 3), (140, 130, 3)):  # either side along the tensor core's rows
+        a, b = operands(ops, M, N, K, ga, gb, "e4m3", "e4m3", 91)
+        for m, down in ((a, ops[0] == "T"), (b, ops[1] == "N")):  # k along dimension 0 where `down`
+            codes, scale = m.data.view(torch.uint8), m.scale if down else m.scale.T
+            if K == 3:
+                codes.bitwise_and_(0x87)
+            else:
+                codes.bitwise_or_(0x70)
+                codes[(codes & 0x7F) == 0x7F] = 0x7E
+            low = (m is a) != swap
+            scale[0].mul_(2.0 ** -125 if low else 2.0 ** 119)
+            scale[1:].mul_(2.0 ** 119 if low else 2.0 ** -125)
+        ref, mag, _ = reference(ops, a, b)
+        check(sg.matmul_fp8(a, b, transA=ops[0], transB=ops[1]), ref, mag, K, what=(M, N, K))
+
+
+@pytest.mark.gpu
 def test_nothing_is_read_that_need_not_be():
     import torch
     a, b = operands("NT", 20, 30, 128, 1, 128, "e4m3", "e4m3", 61)
