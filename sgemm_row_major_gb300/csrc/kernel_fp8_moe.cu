@@ -501,8 +501,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
           for (int j = 0; j < kCols; j += 4) {
             const float4 x = *reinterpret_cast<const float4*>(sc + j0 + j);
             float2* m = &sum[(j0 + j) / 2];
-            m[0] = __ffma2_rn(__fmul2_rn(make_float2(v[j], v[j + 1]), make_float2(x.x, x.y)), w2, m[0]);
-            m[1] = __ffma2_rn(__fmul2_rn(make_float2(v[j + 2], v[j + 3]), make_float2(x.z, x.w)), w2, m[1]);
+            // the two scales first: either alone may be far from 1
+            m[0] = __ffma2_rn(make_float2(v[j], v[j + 1]), __fmul2_rn(make_float2(x.x, x.y), w2), m[0]);
+            m[1] = __ffma2_rn(make_float2(v[j + 2], v[j + 3]), __fmul2_rn(make_float2(x.z, x.w), w2), m[1]);
           }
         }
         if (in_chunk == kChunkGroups - 1 || g == groups - 1) {
@@ -823,8 +824,8 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
             for (int j = 0; j < 8; ++j) {
               const float v0 = fmaf(x[0][2 * j + 1], 1.0f / kLoScale, x[0][2 * j]);
               const float v1 = fmaf(x[1][2 * j + 1], 1.0f / kLoScale, x[1][2 * j]);
-              sum[j0 + j] = fmaf(v0 * f0[j], w, sum[j0 + j]);
-              if (w2 != 0.0f) sum[j0 + j] = fmaf(v1 * f1[j], w2, sum[j0 + j]);
+              sum[j0 + j] = fmaf(v0, f0[j] * w, sum[j0 + j]);
+              if (w2 != 0.0f) sum[j0 + j] = fmaf(v1, f1[j] * w2, sum[j0 + j]);
             }
           }
           if (++b == bufs) b = 0;

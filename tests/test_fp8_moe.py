@@ -90,6 +90,43 @@ def test_against_the_formula(T, E, k, H, I, renormalize):
     check(T, E, k, H, I, T + E + k, renormalize, bf16=renormalize)
 
 
+def largest_codes(data, scale, ref, block):
+    """Every code replaced by the largest one of the same sign."""
+    import torch
+    data.view(torch.uint8).bitwise_or_(0x7E).bitwise_and_(0xFE)
+    s = scale.double().cpu().numpy().reshape(-1, *scale.shape[-2:])
+    ref[:] = np.copysign(448.0 * np.stack([spread(m, block, ref.shape[-2:]) for m in s]).reshape(ref.shape), ref)
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k,H,I", [(3, 6, 2, 256, 256), (40, 6, 3, 256, 160)])
+def test_each_scale_may_be_extreme(T, E, k, H, I):
+    """Scales far from 1 on either side of a product whose value is ordinary: x against gate and up, and inner values
+    of 2^118 against down.  A group's sum times one of them alone would be beyond FP32."""
+    import torch
+    big, small = 2.0 ** 118, 2.0 ** -118
+    for inner_big in (False, True):
+        x, xr, lg, ws, wr = layer(T, E, H, I, 11)
+        if inner_big:
+            largest_codes(*ws[2], wr[2], (128, 128))
+            ws[1][1].mul_(big)
+            wr[1] *= big
+            ws[2][1].mul_(small)
+            wr[2] *= small
+        else:
+            largest_codes(x.data, x.scale, xr, (1, 128))
+            for m, m_ref, f in ((x.scale, xr, big), (ws[0][1], wr[0], small), (ws[1][1], wr[1], small)):
+                m[..., 0].mul_(f)
+                m_ref[..., :128] *= f
+                m[..., 1].mul_(1 / f)
+                m_ref[..., 128:] *= 1 / f
+        got = sg.moe_fp8(x, torch.from_numpy(lg).cuda(), k, *ws, out_dtype=torch.float32)
+        y, tol = reference(xr, lg, k, wr, True)
+        assert np.isfinite(y).all()
+        err = np.abs(got.double().cpu().numpy() - y)
+        assert np.all(err <= tol + U * np.abs(y)), (inner_big, float(np.nanmax(err / tol)), int((~np.isfinite(err)).sum()))
+
+
 @pytest.mark.gpu
 def test_every_token_to_one_expert():
     """All tokens on the same experts (a full tile of columns), and each token on an expert of its own."""
