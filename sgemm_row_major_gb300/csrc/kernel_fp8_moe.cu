@@ -798,7 +798,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
           tmem_fence_after_sync();
           const uint32_t acc = tq + (uint32_t)b * kAccCols;
           const float w = chunks[c * kChunkFloats + 2 * kChunkGroups * NC + i];
-          const float w2 = 2 * (u.g + i) + 1 < p.h_groups ? w : 0.0f;  // the second half may be past the end
+          const bool two = 2 * (u.g + i) + 1 < p.h_groups;  // the second half may be past the end, its scales not loaded
 #pragma unroll
           for (int j0 = 0; j0 < NS; j0 += 8) {  // 8 slots of both halves: hi, lo, hi, lo, ...
             float x[2][16];
@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
               const float v0 = fmaf(x[0][2 * j + 1], 1.0f / kLoScale, x[0][2 * j]);
               const float v1 = fmaf(x[1][2 * j + 1], 1.0f / kLoScale, x[1][2 * j]);
               sum[j0 + j] = fmaf(v0, f0[j] * w, sum[j0 + j]);
-              if (w2 != 0.0f) sum[j0 + j] = fmaf(v1, f1[j] * w2, sum[j0 + j]);
+              if (two) sum[j0 + j] = fmaf(v1, f1[j] * w, sum[j0 + j]);
             }
           }
           if (++b == bufs) b = 0;

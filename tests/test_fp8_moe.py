@@ -90,6 +90,25 @@ def test_against_the_formula(T, E, k, H, I, renormalize):
     check(T, E, k, H, I, T + E + k, renormalize, bf16=renormalize)
 
 
+@pytest.mark.gpu
+@pytest.mark.parametrize("inner", [3, 70, 133, 200])
+@pytest.mark.parametrize("I", [208, 256])
+def test_nan_inner_value_under_a_zero_scale(inner, I):
+    """A NaN inner value times weights whose scale is 0 is NaN, in whichever half of a group of 128 it lies."""
+    import torch
+    x, xr, lg, ws, wr = layer(3, 4, 256, I, 12)
+    ws[0][0].view(torch.uint8)[:2, inner] = 0x7F
+    wr[0][:2, inner] = np.nan
+    ws[2][1][..., inner // 128] = 0.0
+    wr[2][..., 128 * (inner // 128): 128 * (inner // 128) + 128] *= 0.0
+    lg[0], lg[1] = [9, 8, 1, 2], [1, 2, 9, 8]
+    got = sg.moe_fp8(x, torch.from_numpy(lg).cuda(), 2, *ws, out_dtype=torch.float32).cpu().numpy()
+    y, tol = reference(xr, lg, 2, wr, True)
+    assert np.isnan(y[0]).all() and np.isfinite(y[1]).all()
+    assert np.array_equal(np.isnan(got), np.isnan(y)), (np.isnan(got).sum(1), np.isnan(y).sum(1))
+    assert np.all(np.abs(got[1] - y[1]) <= tol[1] + U * np.abs(y[1]))
+
+
 def largest_codes(data, scale, ref, block):
     """Every code replaced by the largest one of the same sign."""
     import torch
