@@ -5,7 +5,8 @@ An ``Fp8Matrix`` is a 2-D tensor of 8-bit codes with the scales of its groups of
 BF16 matrix, ``rmsnorm_fp8`` makes one from a layer's input, ``matmul_fp8``
 multiplies two, ``moe_fp8`` runs a mixture-of-experts layer on one.  Outputs
 that a call allocates belong to the stream it runs on; rows of codes start at
-multiples of 16 elements and rows of the norm's outputs at multiples of 8.
+multiples of 16 elements and rows of the norm's outputs at multiples of 8.  A
+call's tensors are on one device, which is the current one (ValueError otherwise).
 """
 from __future__ import annotations
 
@@ -35,11 +36,12 @@ _T = None          # torch, imported with the first call
 _CODES = {}        # torch dtype -> enum sgemm_fp8_format
 _TYPES = {}        # torch dtype -> enum sgemm_type
 _raw_stream = None
+_current_device = None
 
 
 def _lib():
     """The compiled library with the C signatures of this file's entry points."""
-    global _functions, _T, _raw_stream
+    global _functions, _T, _raw_stream, _current_device
     if _functions is None:
         import torch
         lib = load()
@@ -61,14 +63,24 @@ def _lib():
         _TYPES.update({torch.float32: 0, torch.bfloat16: 1})
         # the handle alone: torch.cuda.current_stream() builds an object, which costs as much as a launch
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
         _T, _functions = torch, lib
     return _functions
 
 
-def _on(stream, x):
-    """The stream handle a call on tensor x runs on."""
+def _on(stream, x, *others):
+    """The stream handle a call on these tensors (None: not given) runs on.  The library launches on the current device:
+    tensors or a stream of another one are refused."""
+    device = x.get_device()
+    for t in others:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"tensors on cuda:{device} and cuda:{t.get_device()}: all must be on one device")
+    if device != _current_device():
+        raise ValueError(f"tensors are on cuda:{device}, the current device is cuda:{_current_device()}")
     if stream is None and _raw_stream is not None:
-        return _raw_stream(x.get_device())
+        return _raw_stream(device)
+    if getattr(getattr(stream, "device", None), "index", device) != device:
+        raise ValueError(f"tensors are on cuda:{device}, the stream on {stream.device}")
     return _stream(stream)
 
 
@@ -147,6 +159,8 @@ class Fp8Matrix:
             raise TypeError(f"scale must be float32, got {scale.dtype}")
         rows, cols, ld = _rows(data, "data")
         srows, scols, lds = _rows(scale, "scale")
+        if scale.get_device() != data.get_device():
+            raise ValueError(f"data is on cuda:{data.get_device()}, scale on cuda:{scale.get_device()}")
         br, bc = block
         if (br, bc) not in GROUPS:
             raise ValueError("block must be (1, 128), (128, 1) or (128, 128)")
@@ -183,9 +197,10 @@ def quantize_fp8(x, block=ROW, format="e4m3", stream=None) -> Fp8Matrix:
     block = tuple(block)
     if block not in GROUPS:
         raise ValueError("block must be (1, 128), (128, 1) or (128, 128)")
+    handle = _on(stream, x)
     m = _new_matrix(rows, cols, block, fmt, x, stream)
     c = m._struct
-    st = lib.sgemm_fp8_quantize(rows, cols, x.data_ptr(), t, ldx, fmt, block[0], block[1], c.data, c.ld, c.scale, c.lds, _on(stream, x))
+    st = lib.sgemm_fp8_quantize(rows, cols, x.data_ptr(), t, ldx, fmt, block[0], block[1], c.data, c.ld, c.scale, c.lds, handle)
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_quantize")
     return m
@@ -226,6 +241,7 @@ def matmul_fp8(A: Fp8Matrix, B: Fp8Matrix, C=None, transA="N", transB="N", alpha
         c_ptr = C.data_ptr()
     elif beta != 0.0:
         raise ValueError("beta != 0 needs C")
+    handle = _on(stream, A.data, B.data, C, d)
     if d is None:
         d = _empty((M, N), out_dtype or _T.float32, A.data, stream)
     elif out_dtype is not None and d.dtype is not out_dtype:
@@ -234,7 +250,7 @@ def matmul_fp8(A: Fp8Matrix, B: Fp8Matrix, C=None, transA="N", transB="N", alpha
     rows, cols, ldd = _rows(d, "out")
     if rows != M or cols != N:
         raise ValueError("out has the wrong shape")
-    st = lib.sgemm_fp8(opa, opb, M, N, K, alpha, A._struct, B._struct, beta, c_ptr, ldc, d.data_ptr(), ldd, t, _on(stream, d))
+    st = lib.sgemm_fp8(opa, opb, M, N, K, alpha, A._struct, B._struct, beta, c_ptr, ldc, d.data_ptr(), ldd, t, handle)
     if st != 0:
         raise SgemmError(st, "sgemm_fp8")
     return d
@@ -284,6 +300,7 @@ def rmsnorm_fp8(x, weight, eps=1e-6, residual=None, *, codes=True, y=False, stre
     rows, cols, ldx = _rows(x, "x")
     dtype = x.dtype
     _vector(weight, "weight", cols, dtype)
+    handle = _on(stream, x, weight, residual)
     h, r_ptr, ldr, h_ptr, ldh = x, None, 0, None, cols or 1
     if residual is not None:
         rrows, rcols, ldr = _rows(residual, "residual")
@@ -296,7 +313,7 @@ def rmsnorm_fp8(x, weight, eps=1e-6, residual=None, *, codes=True, y=False, stre
     q = _new_matrix(rows, cols, ROW, 0, x, stream) if codes else None
     c = q._struct if codes else _NO_MATRIX
     st = lib.sgemm_fp8_rmsnorm(rows, cols, t, x.data_ptr(), ldx, r_ptr, ldr, weight.data_ptr(), eps, h_ptr, ldh,
-                               out.data_ptr() if y else None, ldy, c.data, c.ld, c.scale, c.lds, rstd.data_ptr(), _on(stream, x))
+                               out.data_ptr() if y else None, ldy, c.data, c.ld, c.scale, c.lds, rstd.data_ptr(), handle)
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_rmsnorm")
     return NormOutput(q, h, out, rstd)
@@ -320,10 +337,11 @@ def rmsnorm_fp8_backward(dy, h, weight, rstd, dh=None, *, stream=None):
         if drows != rows or dcols != cols or dh.dtype is not dtype:
             raise ValueError("dh must have dy's shape and type")
         dh_ptr = dh.data_ptr()
+    handle = _on(stream, dy, h, weight, rstd, dh)
     dx, lddx = _empty_rows(rows, cols, dy, stream)
     dw = _empty((cols,), _T.float32, dy, stream)
     st = lib.sgemm_fp8_rmsnorm_backward(rows, cols, t, dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), rstd.data_ptr(),
-                                        dh_ptr, lddh, dx.data_ptr(), lddx, dw.data_ptr(), _on(stream, dy))
+                                        dh_ptr, lddh, dx.data_ptr(), lddx, dw.data_ptr(), handle)
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_rmsnorm_backward")
     return dx, dw
@@ -361,6 +379,7 @@ def moe_fp8(x: Fp8Matrix, logits, top_k, gate, up, down, *, renormalize=True, ou
     g = _experts(gate, "gate", experts, inner, hidden)
     u = _experts(up, "up", experts, inner, hidden)
     d = _experts(down, "down", experts, hidden, inner)
+    handle = _on(stream, x.data, logits, *gate, *up, *down, out)
     y = out if out is not None else _empty((tokens, hidden), out_dtype or _T.bfloat16, x.data, stream)
     yrows, ycols, ldy = _rows(y, "out")
     if yrows != tokens or ycols != hidden:
@@ -369,7 +388,7 @@ def moe_fp8(x: Fp8Matrix, logits, top_k, gate, up, down, *, renormalize=True, ou
     if out_dtype is not None and y.dtype is not out_dtype:
         raise TypeError(f"out is {y.dtype}, not {out_dtype}")
     st = lib.sgemm_fp8_moe(tokens, hidden, inner, experts, top_k, x._struct, logits.data_ptr(), ldl, 1 if renormalize else 0, g, u, d,
-                           y.data_ptr(), ldy, t, _on(stream, y))
+                           y.data_ptr(), ldy, t, handle)
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_moe")
     return y
