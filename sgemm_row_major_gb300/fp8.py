@@ -68,19 +68,26 @@ def _lib():
     return _functions
 
 
-def _on(stream, x, *others):
-    """The stream handle a call on these tensors (None: not given) runs on.  The library launches on the current device:
-    tensors or a stream of another one are refused."""
-    device = x.get_device()
+def _not_cuda():
+    return TypeError("operands must be CUDA tensors")
+
+
+def _on(stream, device, *others):
+    """The stream handle a call on the current device runs on.  device: that of the first operand, others: further tensors
+    or device numbers (None: not given); the library launches on the current device, so another one is refused."""
     for t in others:
-        if t is not None and t.get_device() != device:
-            raise ValueError(f"tensors on cuda:{device} and cuda:{t.get_device()}: all must be on one device")
+        if t is not None:
+            d = t if type(t) is int else t.get_device()
+            if d != device:
+                raise ValueError(f"operands on cuda:{device} and cuda:{d}: all must be on one device") if d >= 0 else _not_cuda()
+    if device < 0:
+        raise _not_cuda()
     if device != _current_device():
-        raise ValueError(f"tensors are on cuda:{device}, the current device is cuda:{_current_device()}")
+        raise ValueError(f"operands are on cuda:{device}, the current device is cuda:{_current_device()}")
     if stream is None and _raw_stream is not None:
         return _raw_stream(device)
     if getattr(getattr(stream, "device", None), "index", device) != device:
-        raise ValueError(f"tensors are on cuda:{device}, the stream on {stream.device}")
+        raise ValueError(f"operands are on cuda:{device}, the stream on {stream.device}")
     return _stream(stream)
 
 
@@ -92,8 +99,6 @@ def _type(x, name) -> int:
 
 
 def _check(x, name, dims=2, dtype=None):
-    if not x.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
     if x.dim() != dims:
         raise TypeError(f"{name} must have {dims} dimension(s)")
     if dtype is not None and x.dtype != dtype:
@@ -104,9 +109,7 @@ def _check(x, name, dims=2, dtype=None):
 
 
 def _rows(x, name):
-    """(rows, columns, row stride) of a 2-D CUDA tensor with contiguous rows (a single row has no stride of its own)."""
-    if not x.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
+    """(rows, columns, row stride) of a 2-D tensor with contiguous rows (a single row has no stride of its own)."""
     shape = x.shape
     if len(shape) != 2:
         raise TypeError(f"{name} must have 2 dimensions")
@@ -146,9 +149,15 @@ class Fp8Matrix:
     """A stored matrix of 8-bit codes: ``data`` (2-D, float8_e4m3fn or float8_e5m2, rows contiguous), ``scale``
     (float32, one per group, rows contiguous) and ``block``, the elements (rows, columns) of a group.
 
-    Element (r, c) is ``data[r, c] * scale[r // block[0], c // block[1]]``."""
+    Element (r, c) is ``data[r, c] * scale[r // block[0], c // block[1]]``.  The attributes are fixed; the tensors' values
+    may change between calls, and so may their memory (``tensor.data = other``) as long as the shapes stay."""
 
-    __slots__ = ("data", "scale", "block", "shape", "_struct")
+    __slots__ = ("_data", "_scale", "_block", "_shape", "_struct", "_at", "_device")
+
+    data = property(lambda self: self._data)
+    scale = property(lambda self: self._scale)
+    block = property(lambda self: self._block)
+    shape = property(lambda self: self._shape)
 
     def __init__(self, data, scale, block=ROW):
         _lib()
@@ -159,15 +168,28 @@ class Fp8Matrix:
             raise TypeError(f"scale must be float32, got {scale.dtype}")
         rows, cols, ld = _rows(data, "data")
         srows, scols, lds = _rows(scale, "scale")
-        if scale.get_device() != data.get_device():
-            raise ValueError(f"data is on cuda:{data.get_device()}, scale on cuda:{scale.get_device()}")
+        device = data.get_device()
+        if device < 0:
+            raise _not_cuda()
+        if scale.get_device() != device:
+            raise ValueError(f"data is on cuda:{device}, scale on cuda:{scale.get_device()}")
         br, bc = block
         if (br, bc) not in GROUPS:
             raise ValueError("block must be (1, 128), (128, 1) or (128, 128)")
         if srows != -(-rows // br) or scols != -(-cols // bc):
             raise ValueError(f"scale must have shape {(-(-rows // br), -(-cols // bc))}, got {(srows, scols)}")
-        self.data, self.scale, self.block, self.shape = data, scale, (br, bc), data.shape
-        self._struct = MatrixStruct(data.data_ptr(), ld, scale.data_ptr(), lds, fmt, br, bc)
+        self._data, self._scale, self._block, self._shape = data, scale, (br, bc), data.shape
+        self._at, self._device = (data.data_ptr(), scale.data_ptr()), device
+        self._struct = MatrixStruct(self._at[0], ld, self._at[1], lds, fmt, br, bc)
+
+    def _c(self):
+        """The C structure; made again where a tensor's memory is no longer the one it was made for."""
+        if (self._data.data_ptr(), self._scale.data_ptr()) != self._at:
+            shape = self._shape
+            self.__init__(self._data, self._scale, self._block)
+            if self._shape != shape:
+                raise ValueError(f"data had shape {tuple(shape)}, has {tuple(self._shape)}")
+        return self._struct
 
 
 def _new_matrix(rows, cols, block, fmt, like, stream):
@@ -178,9 +200,11 @@ def _new_matrix(rows, cols, block, fmt, like, stream):
     br, bc = block
     scols = -(-cols // bc)
     m = Fp8Matrix.__new__(Fp8Matrix)
-    m.scale = scale = _empty((-(-rows // br), scols), _T.float32, like, stream)
-    m.data, m.block, m.shape = data, block, data.shape
-    m._struct = MatrixStruct(data.data_ptr(), ld or 1, scale.data_ptr(), scols or 1, fmt, br, bc)
+    m._scale = scale = _empty((-(-rows // br), scols), _T.float32, like, stream)
+    m._data, m._block, m._shape = data, block, data.shape
+    m._at = at = (data.data_ptr(), scale.data_ptr())
+    m._device = data.get_device()
+    m._struct = MatrixStruct(at[0], ld or 1, at[1], scols or 1, fmt, br, bc)
     return m
 
 
@@ -197,7 +221,7 @@ def quantize_fp8(x, block=ROW, format="e4m3", stream=None) -> Fp8Matrix:
     block = tuple(block)
     if block not in GROUPS:
         raise ValueError("block must be (1, 128), (128, 1) or (128, 128)")
-    handle = _on(stream, x)
+    handle = _on(stream, x.get_device())
     m = _new_matrix(rows, cols, block, fmt, x, stream)
     c = m._struct
     st = lib.sgemm_fp8_quantize(rows, cols, x.data_ptr(), t, ldx, fmt, block[0], block[1], c.data, c.ld, c.scale, c.lds, handle)
@@ -216,14 +240,15 @@ def matmul_fp8(A: Fp8Matrix, B: Fp8Matrix, C=None, transA="N", transB="N", alpha
     A and B are the stored matrices; both must have groups of 128 along the summed dimension.  The result goes to `out`, else
     to C in place, else to a new tensor of `out_dtype` (float32 unless given)."""
     lib = _lib()
+    a, b = A._c(), B._c()
     try:
         (ta, opa), (tb, opb) = _OPS[transA], _OPS[transB]
     except KeyError:
         raise ValueError(f"unknown operation {transA!r} or {transB!r}: N or T") from None
-    M, K = A.shape
+    M, K = A._shape
     if ta:
         M, K = K, M
-    kb, N = B.shape
+    kb, N = B._shape
     if tb:
         kb, N = N, kb
     if kb != K:
@@ -241,16 +266,16 @@ def matmul_fp8(A: Fp8Matrix, B: Fp8Matrix, C=None, transA="N", transB="N", alpha
         c_ptr = C.data_ptr()
     elif beta != 0.0:
         raise ValueError("beta != 0 needs C")
-    handle = _on(stream, A.data, B.data, C, d)
+    handle = _on(stream, A._device, B._device, C, d)
     if d is None:
-        d = _empty((M, N), out_dtype or _T.float32, A.data, stream)
+        d = _empty((M, N), out_dtype or _T.float32, A._data, stream)
     elif out_dtype is not None and d.dtype is not out_dtype:
         raise TypeError(f"out is {d.dtype}, not {out_dtype}")
     t = _type(d, "out")
     rows, cols, ldd = _rows(d, "out")
     if rows != M or cols != N:
         raise ValueError("out has the wrong shape")
-    st = lib.sgemm_fp8(opa, opb, M, N, K, alpha, A._struct, B._struct, beta, c_ptr, ldc, d.data_ptr(), ldd, t, handle)
+    st = lib.sgemm_fp8(opa, opb, M, N, K, alpha, a, b, beta, c_ptr, ldc, d.data_ptr(), ldd, t, handle)
     if st != 0:
         raise SgemmError(st, "sgemm_fp8")
     return d
@@ -281,8 +306,8 @@ _NO_MATRIX = MatrixStruct()
 
 
 def _vector(x, name, n, dtype):
-    if not x.is_cuda or x.dtype is not dtype:
-        raise TypeError(f"{name} must be a {dtype} CUDA tensor")
+    if x.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
     if x.shape != (n,):
         raise ValueError(f"{name} must have shape ({n},), got {tuple(x.shape)}")
     if n > 1 and x.stride(0) != 1:
@@ -300,7 +325,7 @@ def rmsnorm_fp8(x, weight, eps=1e-6, residual=None, *, codes=True, y=False, stre
     rows, cols, ldx = _rows(x, "x")
     dtype = x.dtype
     _vector(weight, "weight", cols, dtype)
-    handle = _on(stream, x, weight, residual)
+    handle = _on(stream, x.get_device(), weight, residual)
     h, r_ptr, ldr, h_ptr, ldh = x, None, 0, None, cols or 1
     if residual is not None:
         rrows, rcols, ldr = _rows(residual, "residual")
@@ -337,7 +362,7 @@ def rmsnorm_fp8_backward(dy, h, weight, rstd, dh=None, *, stream=None):
         if drows != rows or dcols != cols or dh.dtype is not dtype:
             raise ValueError("dh must have dy's shape and type")
         dh_ptr = dh.data_ptr()
-    handle = _on(stream, dy, h, weight, rstd, dh)
+    handle = _on(stream, dy.get_device(), h, weight, rstd, dh)
     dx, lddx = _empty_rows(rows, cols, dy, stream)
     dw = _empty((cols,), _T.float32, dy, stream)
     st = lib.sgemm_fp8_rmsnorm_backward(rows, cols, t, dy.data_ptr(), lddy, h.data_ptr(), ldh, weight.data_ptr(), rstd.data_ptr(),
@@ -369,7 +394,8 @@ def moe_fp8(x: Fp8Matrix, logits, top_k, gate, up, down, *, renormalize=True, ou
     weights are divided by their sum over the chosen experts with renormalize=True.  Returns bfloat16 unless out_dtype or
     out says otherwise."""
     lib = _lib()
-    tokens, hidden = x.shape
+    xs = x._c()
+    tokens, hidden = x._shape
     experts, inner = gate[0].shape[:2]
     lrows, lcols, ldl = _rows(logits, "logits")
     if logits.dtype is not _T.float32:
@@ -379,15 +405,15 @@ def moe_fp8(x: Fp8Matrix, logits, top_k, gate, up, down, *, renormalize=True, ou
     g = _experts(gate, "gate", experts, inner, hidden)
     u = _experts(up, "up", experts, inner, hidden)
     d = _experts(down, "down", experts, hidden, inner)
-    handle = _on(stream, x.data, logits, *gate, *up, *down, out)
-    y = out if out is not None else _empty((tokens, hidden), out_dtype or _T.bfloat16, x.data, stream)
+    handle = _on(stream, x._device, logits, *gate, *up, *down, out)
+    y = out if out is not None else _empty((tokens, hidden), out_dtype or _T.bfloat16, x._data, stream)
     yrows, ycols, ldy = _rows(y, "out")
     if yrows != tokens or ycols != hidden:
         raise ValueError("out has the wrong shape")
     t = _type(y, "out")
     if out_dtype is not None and y.dtype is not out_dtype:
         raise TypeError(f"out is {y.dtype}, not {out_dtype}")
-    st = lib.sgemm_fp8_moe(tokens, hidden, inner, experts, top_k, x._struct, logits.data_ptr(), ldl, 1 if renormalize else 0, g, u, d,
+    st = lib.sgemm_fp8_moe(tokens, hidden, inner, experts, top_k, xs, logits.data_ptr(), ldl, 1 if renormalize else 0, g, u, d,
                            y.data_ptr(), ldy, t, handle)
     if st != 0:
         raise SgemmError(st, "sgemm_fp8_moe")

@@ -83,3 +83,39 @@ def test_a_stream_of_another_device_is_refused(on_device_0):
         device = torch.device("cuda", 1)
     with pytest.raises(ValueError, match="stream"):
         sg.quantize_fp8(Stand((4, 256), torch.bfloat16), stream=Stream())
+
+
+def test_a_matrix_attributes_are_fixed():
+    """Codes or scales put in their place would not be the ones a call reads."""
+    import torch
+    fp8._lib()
+    m = sg.Fp8Matrix(Stand((8, 256), torch.float8_e4m3fn), Stand((8, 2), torch.float32))
+    for name in ("data", "scale", "block", "shape"):
+        with pytest.raises(AttributeError):
+            setattr(m, name, getattr(m, name))
+
+
+@pytest.mark.gpu
+def test_a_matrix_follows_its_tensors_memory():
+    """A tensor whose memory was exchanged after the matrix was made is read where it is now; another shape is refused."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x, w = (torch.randn(n, 256, generator=g, device="cuda") for n in (8, 128))
+    a, b = sg.quantize_fp8(x), sg.quantize_fp8(w, (128, 128))
+    want = sg.matmul_fp8(a, b, transB="T")
+    a.scale.data = a.scale * 2.0
+    assert torch.equal(sg.matmul_fp8(a, b, transB="T"), 2.0 * want)
+    b.data.data = b.data.view(torch.uint8).clone().bitwise_xor_(0x80).view(torch.float8_e4m3fn)
+    assert torch.equal(sg.matmul_fp8(a, b, transB="T"), -2.0 * want)
+    logits = torch.zeros(8, 2, device="cuda")
+    up = torch.stack([b.data.view(torch.uint8)] * 2).view(torch.float8_e4m3fn), torch.stack([b.scale] * 2)
+    d = sg.quantize_fp8(w.T.contiguous(), (128, 128))
+    down = torch.stack([d.data.view(torch.uint8)] * 2).view(torch.float8_e4m3fn), torch.stack([d.scale] * 2)
+    y = sg.moe_fp8(a, logits, 1, up, up, down)
+    fresh = sg.Fp8Matrix(a.data.clone(), a.scale.clone())
+    a.data.data = fresh.data.clone()
+    a.data.view(torch.uint8).zero_()
+    assert not torch.equal(sg.moe_fp8(a, logits, 1, up, up, down), y) and torch.equal(sg.moe_fp8(fresh, logits, 1, up, up, down), y)
+    a.data.data = torch.zeros(4, 256, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
+    with pytest.raises(ValueError):
+        sg.matmul_fp8(a, b, transB="T")
