@@ -124,8 +124,8 @@ int sgemm_fp8_quantize(int64_t rows, int64_t cols, const void *X, int type, int6
  * and y in E4M3 with 1 x 128 groups as sgemm_fp8_quantize() gives them.
  *   - X, R, W (cols values), H and Y have `type`.  H (NULL: not wanted) receives
  *     h, Y (NULL: not wanted) y, rstd (NULL: not wanted) a float per row;
- *     codes NULL: no 8-bit output.  H may be X or R.  The norm is of the
- *     unrounded sum.
+ *     codes NULL: no 8-bit output.  H may be X or R, with its row stride (-11
+ *     otherwise).  The norm is of the unrounded sum.
  * Arguments: 1 rows, 2 cols, 3 type, 4 X, 5 ldx, 6 R, 7 ldr, 8 W, 9 eps, 10 H,
  * 11 ldh, 12 Y, 13 ldy, 14 codes, 15 ldq, 16 scale, 17 lds, 18 rstd, 19 stream.
  */
@@ -141,8 +141,8 @@ int sgemm_fp8_rmsnorm(int64_t rows, int64_t cols, int type, const void *X, int64
  *     dw = sum over the rows of dy * h * rstd,
  * dh being the gradient that reaches h past the norm (NULL: none).  dx is the
  * gradient of both x and r.  dY, H, W, dH and dX have `type`, rstd and dW are
- * FP32 (dW NULL: not wanted).  dX may be dY or dH.  cols <= 49152, else
- * SGEMM_ERR_UNSUPPORTED.
+ * FP32 (dW NULL: not wanted).  dX may be dY or dH, with its row stride (-13
+ * otherwise).  cols <= 49152, else SGEMM_ERR_UNSUPPORTED.
  * Arguments: 1 rows, 2 cols, 3 type, 4 dY, 5 lddy, 6 H, 7 ldh, 8 W, 9 rstd,
  * 10 dH, 11 lddh, 12 dX, 13 lddx, 14 dW, 15 stream.
  */

@@ -24,6 +24,11 @@ bool known_format(int f) { return f == SGEMM_FP8_E4M3 || f == SGEMM_FP8_E5M2; }
 // Rows of 16-byte vectors: the base and the row stride in bytes are multiples of 16 (a NULL matrix is not read).
 bool rows16(const void* p, int64_t ld, int size) { return !p || (aligned(p, 16) && ld * size % 16 == 0); }
 
+// Whether an output in an input's place has rows of its own: it would overwrite rows that are still to be read.
+bool other_stride(const void* out, int64_t ld_out, const void* in, int64_t ld_in, int64_t rows) {
+  return out == in && rows > 1 && ld_out != ld_in;
+}
+
 // ---------------------------------------------------------------- product
 
 std::atomic<int> g_force_variant{SGEMM_VARIANT_AUTO}, g_force_tile{0}, g_force_split{0};
@@ -446,7 +451,7 @@ int sgemm_fp8_rmsnorm(int64_t rows, int64_t cols, int type, const void* X, int64
   if (work && (!W || !aligned(W, size))) return -8;
   if (!(eps >= 0.0f)) return -9;
   if (H && !aligned(H, size)) return -10;
-  if (H && ldh < min_ld) return -11;
+  if (H && (ldh < min_ld || other_stride(H, ldh, X, ldx, rows) || other_stride(H, ldh, R, ldr, rows))) return -11;
   if (Y && !aligned(Y, size)) return -12;
   if (Y && ldy < min_ld) return -13;
   if (codes && ldq < min_ld) return -15;
@@ -500,6 +505,7 @@ int sgemm_fp8_rmsnorm_backward(int64_t rows, int64_t cols, int type, const void*
   if (dH && lddh < min_ld) return -11;
   if (work && (!dX || !aligned(dX, size))) return -12;
   if (lddx < min_ld) return -13;
+  if (work && (other_stride(dX, lddx, dY, lddy, rows) || other_stride(dX, lddx, dH, lddh, rows))) return -13;
   if (dW && !aligned(dW, 4)) return -14;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (cols == 0 || (rows == 0 && !dW)) return SGEMM_OK;

@@ -255,3 +255,39 @@ def test_nothing_is_written_between_rows(cols, dtype, pad):
     assert all(kept(o) for o in (h, y, dx, q, codes))
     assert all(bool((o[:rows, groups:] == 7.0).all()) and bool((o[rows:] == 7.0).all()) for o in (s, s2))
     assert float(rstd[rows]) == 7.0 and float(dw[cols]) == 7.0
+
+
+def test_in_place_with_another_stride_is_refused():
+    """An output in an input's place has that input's row stride: with another it would overwrite rows still to be read.
+    (No launch: the addresses are not memory.)"""
+    from sgemm_row_major_gb300 import fp8
+    lib = fp8._lib()
+    a, b, c = FAKE, 2 * FAKE, 3 * FAKE
+    for h, ldx, ldr, ldh in ((a, 264, 256, 256), (a, 256, 256, 264), (b, 256, 264, 256), (b, 264, 256, 264)):
+        assert lib.sgemm_fp8_rmsnorm(4, 256, 1, a, ldx, b, ldr, c, 1e-6, h, ldh, None, 0, None, 0, None, 0, None, None) == -11
+    for dx, lddy, lddh, lddx in ((a, 264, 256, 256), (a, 256, 256, 264), (b, 256, 264, 256), (b, 264, 256, 264)):
+        assert lib.sgemm_fp8_rmsnorm_backward(4, 256, 0, a, lddy, c, 256, c, c, b, lddh, dx, lddx, None, None) == -13
+
+
+@pytest.mark.gpu
+def test_gradient_may_overwrite_an_input():
+    """dX may be dY or dH, at any alignment and width; one row has no stride to differ in."""
+    import torch
+    from sgemm_row_major_gb300 import fp8
+    for rows, cols, pad in ((400, 1024, 0), (400, 1001, 3), (1, 520, 0), (5, 8200, 0)):
+        h, w, dh = (t.cuda() for t in data(rows, cols, 16, "float32", True))
+        dy = torch.randn(rows, cols, generator=torch.Generator().manual_seed(17)).cuda()
+        rstd = (h.square().mean(1) + EPS).rsqrt()
+        want, wdw = sg.rmsnorm_fp8_backward(dy, h, w, rstd, dh)
+        for over in (0, 1):
+            ins, dw = [strided(dy, pad), strided(dh, pad)], torch.empty(cols, device="cuda")
+            ld = cols + pad
+            st = fp8._lib().sgemm_fp8_rmsnorm_backward(rows, cols, 0, ins[0].data_ptr(), ld, h.data_ptr(), cols, w.data_ptr(), rstd.data_ptr(),
+                                                       ins[1].data_ptr(), ld, ins[over].data_ptr(), ld + 1 if rows == 1 else ld, dw.data_ptr(), None)
+            torch.cuda.synchronize()
+            assert st == 0
+            # (another alignment takes another kernel, whose sums are in another order)
+            ref, mag, rdw, mdw = grads(f64(dy), f64(h), f64(w), f64(rstd), f64(dh))
+            assert np.all(np.abs(f64(ins[over]) - ref) <= (cols + 8) * U * mag + U * np.abs(ref))
+            assert np.all(np.abs(f64(dw) - rdw) <= (rows + 8) * U * mdw)
+            assert pad or rows == 1 or (torch.equal(ins[over], want) and torch.equal(dw, wdw))
