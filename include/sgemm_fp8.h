@@ -75,8 +75,8 @@ typedef struct sgemm_fp8_matrix_t {
  *     the bits of a subnormal number or is 0.  The bound is for elements whose
  *     pairs' products are zero or in between, and whose sum (before alpha) and
  *     its terms are.
- *   - Fast where both code arrays are 16-byte aligned with ld % 16 == 0; others
- *     are first copied to aligned rows (in the workspace).
+ *   - Fast where both code arrays are 16-byte aligned with ld % 16 == 0 (or one
+ *     row); others are first copied to aligned rows (in the workspace).
  * Arguments: 1 transA, 2 transB, 3 M, 4 N, 5 K, 6 alpha, 7 A, 8 B, 9 beta, 10 C,
  * 11 ldc, 12 D, 13 ldd, 14 type, 15 stream.  An unusable field of *A or *B
  * gives -7 or -8 (data or scale NULL where read, ld or lds too small, unknown

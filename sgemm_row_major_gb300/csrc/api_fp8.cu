@@ -107,10 +107,11 @@ int check_product(char transA, char transB, int64_t M, int64_t N, int64_t K, flo
   return SGEMM_OK;
 }
 
-// TMA reads codes whose base and row stride are multiples of 16 bytes; others are copied first.
+// TMA reads codes whose base and row stride (of more than one row) are multiples of 16 bytes; others are
+// copied first.
 int64_t repack_ld(const Operand& o) { return ceil_div(o.cols, 16) * 16; }
 int64_t repack_bytes(const Operand& o) {
-  return aligned(o.m->data, 16) && o.m->ld % 16 == 0 ? 0 : round256(o.rows * repack_ld(o));
+  return aligned(o.m->data, 16) && (o.m->ld % 16 == 0 || o.rows == 1) ? 0 : round256(o.rows * repack_ld(o));
 }
 
 // Times in ns that the choice of kernel goes by, fitted to 700 launches of 44 products (M, N, K from 1
@@ -237,10 +238,10 @@ uint32_t instruction(const Operand& a, const Operand& b, int m, int n) {
 // at *ws where it needs that.
 cudaError_t operand_map(const Operand& o, int mn, uint8_t** ws, CUtensorMap* map, cudaStream_t stream) {
   const void* data = o.m->data;
-  int64_t ld = o.m->ld;
+  int64_t ld = o.rows == 1 ? repack_ld(o) : o.m->ld;  // (a map wants a stride even where it steps over nothing)
   const int64_t copy = repack_bytes(o);
   if (copy > 0) {
-    const cudaError_t e = launch_fp8_repack(data, ld, o.rows, o.cols, *ws, repack_ld(o), stream);
+    const cudaError_t e = launch_fp8_repack(data, o.m->ld, o.rows, o.cols, *ws, repack_ld(o), stream);
     if (e != cudaSuccess) return e;
     data = *ws;
     ld = repack_ld(o);

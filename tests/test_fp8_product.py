@@ -353,6 +353,28 @@ def test_planner():
     assert plan("NT", 8, 8, 8, alpha=0.0)["variant_name"] == "SCALE"
 
 
+def test_one_stored_row_is_read_in_place():
+    """A single aligned row needs no copy whatever its length and stride: the operand of a decoding step."""
+    w = struct(4096, 4095, (128, 128), ld=4096)
+    for ld in (4095, 4096, 4111):
+        p = plan("NT", 1, 4096, 4095, a=struct(1, 4095, ld=ld), b=w)
+        assert p["workspace_bytes"] == 0 and p["kernel_launches"] == 1, ld
+    assert plan("TN", 301, 40, 1, a=struct(1, 301, (128, 1)), b=struct(1, 40, (128, 128), ld=41))["workspace_bytes"] == 0
+    assert plan("NT", 1, 4096, 4095, a=struct(1, 4095, data=FAKE + 1), b=w)["workspace_bytes"] == 4096
+    assert plan("NT", 2, 4096, 4095, a=struct(2, 4095), b=w)["workspace_bytes"] == 2 * 4096
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_one_stored_row_of_any_length(force, kernel):
+    """Rows of odd lengths, read in place; what lies behind them is NaN."""
+    force(kernel)
+    for ops, M, N, K, pad in (("NT", 1, 300, 501, (11, 11)), ("NN", 1, 304, 127, (3, 0)), ("TN", 301, 40, 1, (5, 9)), ("TT", 33, 1, 1, (2, 7))):
+        a, b = operands(ops, M, N, K, 1, 128, "e4m3", "e4m3", 33, pad)
+        ref, mag, _ = reference(ops, a, b)
+        check(sg.matmul_fp8(a, b, transA=ops[0], transB=ops[1]), ref, mag, K, what=(ops, K))
+
+
 def test_refusals():
     def refused(code, *a, **kw):
         with pytest.raises(sg.SgemmError) as e:
