@@ -123,7 +123,8 @@ int sgemm_fp8_quantize(int64_t rows, int64_t cols, const void *X, int type, int6
  *     h = x + r,   rstd = (mean(h^2) + eps)^(-1/2),   y = h * rstd * w,
  * and y in E4M3 with 1 x 128 groups as sgemm_fp8_quantize() gives them.
  *   - X, R, W (cols values), H and Y have `type`.  H (NULL: not wanted) receives
- *     h, Y (NULL: not wanted) y, rstd (NULL: not wanted) a float per row;
+ *     h, Y (NULL: not wanted) y, rstd (NULL: not wanted) a float per row (NaN
+ *     where cols is 0);
  *     codes NULL: no 8-bit output.  H may be X or R, with its row stride (-11
  *     otherwise).  The norm is of the unrounded sum.
  * Arguments: 1 rows, 2 cols, 3 type, 4 X, 5 ldx, 6 R, 7 ldr, 8 W, 9 eps, 10 H,

@@ -459,11 +459,13 @@ int sgemm_fp8_rmsnorm(int64_t rows, int64_t cols, int type, const void* X, int64
   if (work && codes && (!scale || !aligned(scale, 4))) return -16;
   if (codes && lds < std::max<int64_t>(1, ceil_div(cols, 128))) return -17;
   if (rstd && !aligned(rstd, 4)) return -18;
-  if (!work) return SGEMM_OK;
+  if (rows == 0 || (cols == 0 && !rstd)) return SGEMM_OK;
   if (rows > kMaxDim || cols > kMaxDim) return SGEMM_ERR_UNSUPPORTED;
   CallDevice dev;
   const int s = call_device(&dev);
   if (s != SGEMM_OK) return s;
+  if (cols == 0)  // the mean of nothing: NaNs
+    return launch_status(cudaMemsetAsync(rstd, 0xFF, (size_t)rows * 4, reinterpret_cast<cudaStream_t>(stream)));
   NormParams p;
   p.rows = rows;
   p.cols = (int)cols;

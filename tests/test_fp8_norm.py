@@ -291,3 +291,17 @@ def test_gradient_may_overwrite_an_input():
             assert np.all(np.abs(f64(ins[over]) - ref) <= (cols + 8) * U * mag + U * np.abs(ref))
             assert np.all(np.abs(f64(dw) - rdw) <= (rows + 8) * U * mdw)
             assert pad or rows == 1 or (torch.equal(ins[over], want) and torch.equal(dw, wdw))
+
+
+@pytest.mark.gpu
+def test_rows_without_columns():
+    """Nothing to normalise: rstd is the root of a mean of nothing, NaN, and not what the memory held."""
+    import torch
+    for dtype in (torch.float32, torch.bfloat16):
+        x, w = torch.zeros(300, 0, dtype=dtype, device="cuda"), torch.zeros(0, dtype=dtype, device="cuda")
+        torch.full((300,), 7.0, device="cuda")  # leaves a value in the memory that the next call allocates
+        out = sg.rmsnorm_fp8(x, w, EPS, x, y=True)
+        assert tuple(out.q.shape) == tuple(out.h.shape) == tuple(out.y.shape) == (300, 0)
+        assert bool(torch.isnan(out.rstd).all())
+        dx, dw = sg.rmsnorm_fp8_backward(x, out.h, w, out.rstd)
+        assert tuple(dx.shape) == (300, 0) and tuple(dw.shape) == (0,)
