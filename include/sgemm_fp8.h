@@ -9,8 +9,8 @@
  * enqueued on `stream` of the current device, -(argument index) for an invalid
  * argument before anything is launched, SGEMM_ERR_* otherwise, workspace from
  * the library's stream-ordered pool.  Every call can be captured in a CUDA
- * graph after one eager call on the device.  Results are deterministic: no
- * sum's order depends on scheduling.
+ * graph after one eager call of this part on the device, which sets up its
+ * kernels.  Results are deterministic: no sum's order depends on scheduling.
  *
  * 8-bit matrices.  A stored R x C matrix has one code per element and one FP32
  * scale per group of block_rows x block_cols elements, 1 x 128, 128 x 1 or

@@ -63,6 +63,7 @@ std::atomic<int> g_override_split{0};
 struct DeviceState {
   std::mutex init_mutex;
   std::atomic<bool> ready{false};  // set once the set-up below has succeeded (a failed one is retried)
+  std::atomic<bool> fp8_ready{false};  // the same of the 8-bit kernels', which their first call makes
   int sm_count = 0;
   int pair_clusters = 0;  // co-resident clusters of the CTA-pair kernel; 0: pairs cannot run here
   unsigned* fault = nullptr;
@@ -105,12 +106,6 @@ int device_state(int* device_out, DeviceState** st_out) {
       if (err == cudaSuccess) err = prepare_tc_pair();
       if (err == cudaSuccess) err = prepare_presplit();
       if (err == cudaSuccess) err = prepare_skinny();
-      if (err == cudaSuccess) err = prepare_fp8_norm();
-      if (err == cudaSuccess) err = prepare_fp8_pair_plain();
-      if (err == cudaSuccess) err = prepare_fp8_pair_add();
-      if (err == cudaSuccess) err = prepare_fp8_pair_any();
-      if (err == cudaSuccess) err = prepare_fp8_short();
-      if (err == cudaSuccess) err = prepare_fp8_moe();
       if (err == cudaSuccess) st.pair_clusters = pair_clusters_or_none();
       if (err == cudaSuccess && !st.pool) {
         cudaMemPoolProps props = {};
@@ -882,6 +877,19 @@ int sgemm_impl::call_device(CallDevice* out) {
   DeviceState* st;
   const int s = device_state(&dev, &st);
   if (s != SGEMM_OK) return s;
+  if (!st->fp8_ready.load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(st->init_mutex);
+    if (!st->fp8_ready.load(std::memory_order_relaxed)) {
+      cudaError_t err = prepare_fp8_norm();
+      if (err == cudaSuccess) err = prepare_fp8_pair_plain();
+      if (err == cudaSuccess) err = prepare_fp8_pair_add();
+      if (err == cudaSuccess) err = prepare_fp8_pair_any();
+      if (err == cudaSuccess) err = prepare_fp8_short();
+      if (err == cudaSuccess) err = prepare_fp8_moe();
+      if (err != cudaSuccess) return cuda_fail(err);
+      st->fp8_ready.store(true, std::memory_order_release);
+    }
+  }
   out->sm_count = st->sm_count;
   out->pair_clusters = st->pair_clusters;
   out->fault = st->fault;

@@ -9,7 +9,8 @@
 
 namespace sgemm_impl {
 
-// What an entry point needs of the current device (set up by the first call on it; api.cu).
+// What an entry point needs of the current device (set up by the first call on it, the 8-bit kernels
+// by the first that needs them; api.cu).
 struct CallDevice {
   int sm_count = 0;
   int pair_clusters = 0;

@@ -1,0 +1,67 @@
+"""The 8-bit operators' one-time set-up on a device, with failing calls faked on the host: the library's own
+objects are linked again with one function replaced."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+import sgemm_row_major_gb300 as sg
+
+
+def linked_with(tmp_path, symbol, c_source):
+    """libsgemm with the function `symbol` (its mangled name) replaced by __wrap_<symbol> of `c_source`."""
+    from sgemm_row_major_gb300 import build, fp8
+    build.build()
+    objs = [os.path.join(build.BUILD_DIR, os.path.basename(s) + ".o") for s in build.sources()]
+    if not all(os.path.exists(o) for o in objs):
+        pytest.skip("the library's objects are not here")
+    src, out = str(tmp_path / "fake.c"), str(tmp_path / "libsgemm_fake.so")
+    with open(src, "w") as f:
+        f.write(c_source)
+    subprocess.run([build.nvcc(), *build.ARCH, "-shared", "-Xcompiler", "-fPIC", "-Xlinker", "--wrap=" + symbol, "-o", out, src, *objs,
+                    "-cudart", "static"], check=True, capture_output=True)
+    lib = sg._declare(ctypes.CDLL(out))
+    for name in ("sgemm_fp8", "sgemm_fp8_plan", "sgemm_fp8_quantize", "sgemm_fp8_set_override"):
+        getattr(lib, name).restype, getattr(lib, name).argtypes = ctypes.c_int, getattr(fp8._lib(), name).argtypes
+    return lib
+
+
+def product_of_ones(lib, n=64):
+    """The status of lib.sgemm() on n x n matrices of ones, and its result."""
+    import torch
+    a, c = torch.ones(n, n, device="cuda"), torch.zeros(n, n, device="cuda")
+    st = lib.sgemm(b"N", b"N", n, n, n, 1.0, a.data_ptr(), n, a.data_ptr(), n, 0.0, c.data_ptr(), n, None)
+    torch.cuda.synchronize()
+    return st, c
+
+
+def quantize(lib):
+    import torch
+    x = torch.full((4, 256), 448.0, device="cuda")
+    q, s = torch.zeros(4, 256, dtype=torch.uint8, device="cuda"), torch.zeros(4, 2, device="cuda")
+    st = lib.sgemm_fp8_quantize(4, 256, x.data_ptr(), 0, 256, 0, 1, 128, q.data_ptr(), 256, s.data_ptr(), 2, None)
+    torch.cuda.synchronize()
+    return st, s
+
+
+@pytest.mark.gpu
+def test_a_failed_setup_of_8_bit_kernels_leaves_the_others_alone(tmp_path):
+    """Only 8-bit calls set up 8-bit kernels: where that fails they report it, and are set up by a later call, while an
+    FP32 product neither waits for it nor fails with it."""
+    name = "_ZN10sgemm_impl17prepare_fp8_shortEv"
+    lib = linked_with(tmp_path, name, f"""
+        int fake_calls, fake_error = 1;
+        int __real_{name}(void);
+        int __wrap_{name}(void) {{ ++fake_calls; return fake_error ? fake_error : __real_{name}(); }}
+    """)
+    calls, error = ctypes.c_int.in_dll(lib, "fake_calls"), ctypes.c_int.in_dll(lib, "fake_error")
+    st, c = product_of_ones(lib)
+    assert st == 0 and bool((c == 64.0).all()) and calls.value == 0
+    assert quantize(lib)[0] == sg.STATUS["ERR_CUDA"] and lib.sgemm_last_cuda_error() == 1 and calls.value == 1
+    st, c = product_of_ones(lib)
+    assert st == 0 and bool((c == 64.0).all())
+    error.value = 0
+    for _ in range(2):
+        st, s = quantize(lib)
+        assert st == 0 and bool((s == 1.0).all()) and calls.value == 2
