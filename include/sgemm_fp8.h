@@ -81,7 +81,7 @@ typedef struct sgemm_fp8_matrix_t {
  * 11 ldc, 12 D, 13 ldd, 14 type, 15 stream.  An unusable field of *A or *B
  * gives -7 or -8 (data or scale NULL where read, ld or lds too small, unknown
  * format or groups).  SGEMM_ERR_UNSUPPORTED: a dimension or leading dimension
- * >= 2^31, or a device without clusters of two CTAs.
+ * >= 2^31, or a kernel forced that needs clusters of CTAs on a device without.
  */
 int sgemm_fp8(char transA, char transB, int64_t M, int64_t N, int64_t K, float alpha,
               const sgemm_fp8_matrix_t *A, const sgemm_fp8_matrix_t *B,

@@ -146,14 +146,15 @@ struct Choice {
   double ns = 1e30;
 };
 
-// The cheapest launch of a product, among the variant, tile and split that are forced (0: any).
+// The cheapest launch of a product, among the variant, tile and split that are forced (0: any); clusters:
+// CTA pairs that run at a time, 0 on a device without clusters, where only unshared tiles can run.
 Choice choose(const Product& pr, int64_t clusters, int sm_count, int variant, int tile, int split) {
   const int64_t groups = ceil_div(pr.K, 128), S = std::min(pr.M, pr.N), L = std::max(pr.M, pr.N);
   Choice best;
   const auto offer = [&](int v, int n, int k, double ns) {
     if (ns < best.ns) best = Choice{v, n, k, ns};
   };
-  if (variant != SGEMM_VARIANT_FP8_SHORT)
+  if (variant != SGEMM_VARIANT_FP8_SHORT && clusters > 0)
     for (const PairCost& c : pr.b.scales.shift == 0 ? kPairColsCost : kPairCost) {
       if (tile != 0 && tile != c.tile) continue;
       const int64_t rounds = ceil_div(ceil_div(pr.M, 256) * ceil_div(pr.N, c.tile), clusters);
@@ -164,6 +165,7 @@ Choice choose(const Product& pr, int64_t clusters, int sm_count, int variant, in
       if (tile != 0 ? tile != c.tile : c.tile > 16 && c.tile >= 2 * S) continue;
       const int64_t tiles = ceil_div(L, 128) * ceil_div(S, c.tile);
       for (int k = 1; k <= 8; k *= 2) {
+        if (clusters == 0 && k > 1) break;
         if (split != 0 ? split != k : k > 1 && groups < 2 * k) continue;  // two groups per CTA at least
         const int per_sm = short_ctas_per_sm(c.tile);
         const double on_sm = std::min((double)per_sm, std::max(1.0, (double)tiles * k / sm_count));
@@ -190,12 +192,13 @@ int plan_product(const Product& pr, int sm_count, int pair_clusters, sgemm_plan_
     plan->threads = 256;
     return SGEMM_OK;
   }
-  if (pr.a.m->ld > INT_MAX || pr.b.m->ld > INT_MAX || pair_clusters == 0) return SGEMM_ERR_UNSUPPORTED;
-  const int64_t clusters = pair_clusters > 0 ? pair_clusters : std::max(1, sm_count / 2);
+  if (pr.a.m->ld > INT_MAX || pr.b.m->ld > INT_MAX) return SGEMM_ERR_UNSUPPORTED;
+  const int64_t clusters = pair_clusters >= 0 ? pair_clusters : std::max(1, sm_count / 2);
   const int64_t groups = ceil_div(pr.K, 128);
   const int64_t S = std::min(pr.M, pr.N), L = std::max(pr.M, pr.N);
   const Choice choice = choose(pr, clusters, sm_count, g_force_variant.load(), g_force_tile.load(), g_force_split.load());
   const int variant = choice.variant;
+  if (variant == 0) return SGEMM_ERR_UNSUPPORTED;  // forced to what needs clusters
   plan->variant = variant;
   plan->tile_k = 128;
   plan->kernel_launches = 1;

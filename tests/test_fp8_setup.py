@@ -65,3 +65,28 @@ def test_a_failed_setup_of_8_bit_kernels_leaves_the_others_alone(tmp_path):
     for _ in range(2):
         st, s = quantize(lib)
         assert st == 0 and bool((s == 1.0).all()) and calls.value == 2
+
+
+@pytest.mark.gpu
+def test_a_product_without_clusters(tmp_path):
+    """Where no CTA pair can run, a product takes the short-side kernel with whole tiles; only forced pairs and shares
+    of K are refused."""
+    import torch
+    name = "_ZN10sgemm_impl20tc_pair_max_clustersEPi"
+    lib = linked_with(tmp_path, name, f"int __wrap_{name}(int *n) {{ *n = 0; return 1; }}")
+    from sgemm_row_major_gb300.fp8 import MatrixStruct
+    M, N, K = 300, 260, 1000
+    ones = torch.full((300, 1008), 0x38, dtype=torch.uint8, device="cuda")  # 1.0
+    sa, sb = torch.full((300, 8), 2.0, device="cuda"), torch.full((3, 8), 0.5, device="cuda")
+    a, b = MatrixStruct(ones.data_ptr(), 1008, sa.data_ptr(), 8, 0, 1, 128), MatrixStruct(ones.data_ptr(), 1008, sb.data_ptr(), 8, 0, 128, 128)
+    d = torch.zeros(M, N, device="cuda")
+    args = (b"N", b"T", M, N, K, 1.0, a, b, 0.0, None, N, d.data_ptr(), N, 0)
+    plan = sg.PlanStruct()
+    assert lib.sgemm_fp8_plan(*args, 0, ctypes.byref(plan)) == 0 and (plan.variant, plan.split_k) == (33, 1)
+    assert lib.sgemm_fp8(*args, None) == 0
+    torch.cuda.synchronize()
+    assert bool((d == float(K)).all())
+    for forced in ((32, 0, 0), (33, 0, 2)):
+        assert lib.sgemm_fp8_set_override(*forced) == 0
+        assert lib.sgemm_fp8(*args, None) == sg.STATUS["ERR_UNSUPPORTED"]
+    assert lib.sgemm_fp8_set_override(0, 0, 0) == 0
