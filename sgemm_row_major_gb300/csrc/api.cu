@@ -893,6 +893,7 @@ int sgemm_impl::call_device(CallDevice* out) {
   out->sm_count = st->sm_count;
   out->pair_clusters = st->pair_clusters;
   out->fault = st->fault;
+  out->bounds = st->bounds;
   out->pool = st->pool;
   return SGEMM_OK;
 }

@@ -239,12 +239,12 @@ uint32_t instruction(const Operand& a, const Operand& b, int m, int n) {
 
 // Tensor map of an operand's tiles (`mn` output rows each), after copying its codes to aligned rows
 // at *ws where it needs that.
-cudaError_t operand_map(const Operand& o, int mn, uint8_t** ws, CUtensorMap* map, cudaStream_t stream) {
+cudaError_t operand_map(const Operand& o, int mn, uint8_t** ws, CUtensorMap* map, const Guard& guard, cudaStream_t stream) {
   const void* data = o.m->data;
   int64_t ld = o.rows == 1 ? repack_ld(o) : o.m->ld;  // (a map wants a stride even where it steps over nothing)
   const int64_t copy = repack_bytes(o);
   if (copy > 0) {
-    const cudaError_t e = launch_fp8_repack(data, o.m->ld, o.rows, o.cols, *ws, repack_ld(o), stream);
+    const cudaError_t e = launch_fp8_repack(data, o.m->ld, o.rows, o.cols, *ws, repack_ld(o), guard, stream);
     if (e != cudaSuccess) return e;
     data = *ws;
     ld = repack_ld(o);
@@ -257,8 +257,8 @@ cudaError_t launch_product(const Product& pr, const sgemm_plan_t& plan, const Ca
                            cudaStream_t stream) {
   CUtensorMap ma, mb;
   if (plan.variant == SGEMM_VARIANT_FP8_PAIR) {
-    cudaError_t e = operand_map(pr.a, 128, &ws, &ma, stream);
-    if (e == cudaSuccess) e = operand_map(pr.b, plan.tile_n / 2, &ws, &mb, stream);
+    cudaError_t e = operand_map(pr.a, 128, &ws, &ma, pr.out.guard, stream);
+    if (e == cudaSuccess) e = operand_map(pr.b, plan.tile_n / 2, &ws, &mb, pr.out.guard, stream);
     if (e != cudaSuccess) return e;
     Fp8PairParams p;
     p.out = pr.out;
@@ -281,8 +281,8 @@ cudaError_t launch_product(const Product& pr, const sgemm_plan_t& plan, const Ca
   }
   const bool trans = pr.M <= pr.N;
   const Operand &l = trans ? pr.b : pr.a, &s = trans ? pr.a : pr.b;
-  cudaError_t e = operand_map(l, 128, &ws, &ma, stream);
-  if (e == cudaSuccess) e = operand_map(s, plan.tile_n, &ws, &mb, stream);
+  cudaError_t e = operand_map(l, 128, &ws, &ma, pr.out.guard, stream);
+  if (e == cudaSuccess) e = operand_map(s, plan.tile_n, &ws, &mb, pr.out.guard, stream);
   if (e != cudaSuccess) return e;
   Fp8ShortParams p;
   p.out = pr.out;
@@ -354,6 +354,7 @@ int sgemm_fp8(char transA, char transB, int64_t M, int64_t N, int64_t K, float a
   sgemm_plan_t plan;
   s = plan_product(pr, dev.sm_count, dev.pair_clusters, &plan);
   if (s != SGEMM_OK) return s;
+  pr.out.guard = {dev.fault, dev.bounds};
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (plan.variant == SGEMM_VARIANT_SCALE) return launch_status(launch_fp8_scale(pr.out, stream));
   void* ws = nullptr;
@@ -435,6 +436,7 @@ int sgemm_fp8_quantize(int64_t rows, int64_t cols, const void* X, int type, int6
   p.s = scale;
   p.lds = lds;
   p.format = format;
+  p.guard = {dev.fault, dev.bounds};
   p.x_vec = rows16(X, ldx, type_size(type));
   return launch_status(launch_fp8_quantize(type, block_rows, block_cols, p, reinterpret_cast<cudaStream_t>(stream)));
 }
@@ -487,6 +489,7 @@ int sgemm_fp8_rmsnorm(int64_t rows, int64_t cols, int type, const void* X, int64
   p.s = scale;
   p.lds = lds;
   p.rstd = rstd;
+  p.guard = {dev.fault, dev.bounds};
   p.vec = rows16(X, ldx, size) && rows16(R, ldr, size) && rows16(W, 0, size) && rows16(H, ldh, size) &&
           rows16(Y, ldy, size) && cols % 8 == 0;
   return launch_status(launch_fp8_rmsnorm(type, p, reinterpret_cast<cudaStream_t>(stream)));
@@ -538,6 +541,7 @@ int sgemm_fp8_rmsnorm_backward(int64_t rows, int64_t cols, int type, const void*
           rows16(dX, lddx, size) && cols % 8 == 0;
   p.timeout_ns = wait_timeout_ns();
   p.fault = dev.fault;
+  p.guard = {dev.fault, dev.bounds};
   const int grid = fp8_rmsnorm_backward_grid(type, rows, (int)cols, p.vec != 0, dev.sm_count);
   if (dW) {
     void* ws = nullptr;
@@ -617,6 +621,7 @@ int sgemm_fp8_moe(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts
   p.active_max = (int)std::min<int64_t>(experts, p.slots_max);
   p.timeout_ns = wait_timeout_ns();
   p.fault = dev.fault;
+  p.guard = {dev.fault, dev.bounds};
   shape_fp8_moe(&p, dev.sm_count);
   uint8_t* x_copy = nullptr;
   const auto place = [&](Pieces* w) {
@@ -639,7 +644,7 @@ int sgemm_fp8_moe(int64_t tokens, int64_t hidden, int64_t inner, int64_t experts
   w.base = static_cast<uint8_t*>(ws);
   place(&w);
   MoeMaps maps;
-  e = operand_map(x, tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64, &x_copy, &maps.x, stream);
+  e = operand_map(x, tokens <= 16 ? 16 : tokens <= 32 ? 32 : 64, &x_copy, &maps.x, p.guard, stream);
   if (e == cudaSuccess) e = experts_map(*gate, inner, hidden, experts, 64, &maps.gate);
   if (e == cudaSuccess) e = experts_map(*up, inner, hidden, experts, 64, &maps.up);
   if (e == cudaSuccess) e = experts_map(*down, hidden, inner, experts, 128, &maps.down);

@@ -7,6 +7,7 @@
 #include <cuda_fp8.h>
 
 #include "device_utils.cuh"
+#include "fp8_internal.h"
 #include "sgemm_fp8.h"
 
 namespace sgemm_impl {
@@ -15,6 +16,29 @@ namespace f8 {
 constexpr float kMaxE4M3 = 448.0f, kMaxE5M2 = 57344.0f;
 constexpr float kMaxFloat = 3.402823466e38f;
 constexpr float kMinScale = 1.17549435e-38f;  // 2^-126: the smallest scale, whose reciprocal is finite
+
+// What the debug build's checks report of an index outside its buffer (they follow enum BoundsSite).
+enum Fp8Site : unsigned {
+  kSiteIn = 16,      // X, R, W, dY, H, dH, C read
+  kSiteOut = 17,     // H, Y, dX, D, dW written
+  kSiteCodes = 18,   // codes written or copied
+  kSiteScale = 19,   // scales
+  kSiteRowStat = 20, // rstd
+  kSiteLogits = 21,  // logits
+  kSitePart = 22     // the workspace: partial sums, inner values, routing
+};
+
+// One element at index i of the n at p (the check is the constant true in the normal build).
+template <typename T>
+__device__ __forceinline__ T get_at(const Guard& g, unsigned site, const T* p, int64_t i, int64_t n) {
+  return in_range(g.fault, g.word, site, i, 1, n) ? p[i] : T();
+}
+template <typename T>
+__device__ __forceinline__ void put_at(const Guard& g, unsigned site, T* p, int64_t i, int64_t n, T v) {
+  if (in_range(g.fault, g.word, site, i, 1, n)) p[i] = v;
+}
+// Elements from the first to one past the last of a matrix.
+__device__ __forceinline__ int64_t extent(int64_t rows, int64_t ld, int64_t cols) { return (rows - 1) * ld + cols; }
 
 // |x| where it is finite, else 0: what counts towards a group's largest value.
 __device__ __forceinline__ float finite_abs(float x) {
@@ -90,12 +114,16 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ void from_float(float* p, float x) { *p = x; }
 __device__ __forceinline__ void from_float(__nv_bfloat16* p, float x) { *p = __float2bfloat16_rn(x); }
 
-// A matrix that chunks are loaded from: `end` is past its last element.
+// A matrix that chunks are loaded from or stored to: `end` is past its last element.
 template <typename T>
 struct Rows {
   const T *base, *end;
-  __device__ __forceinline__ Rows(const void* p, int64_t rows, int64_t ld, int64_t cols)
-      : base(static_cast<const T*>(p)), end(static_cast<const T*>(p) + (rows - 1) * ld + cols) {}
+  const Guard& guard;
+  __device__ __forceinline__ Rows(const void* p, int64_t rows, int64_t ld, int64_t cols, const Guard& g)
+      : base(static_cast<const T*>(p)), end(static_cast<const T*>(p) + extent(rows, ld, cols)), guard(g) {}
+  __device__ __forceinline__ bool holds(unsigned site, const T* p, int64_t n) const {
+    return n <= 0 || in_range(guard.fault, guard.word, site, p - base, n, end - base);
+  }
 };
 
 // A chunk of elements [0, n) at p, zeros beyond n, in two steps: load() sends for it, get() waits for it
@@ -111,6 +139,7 @@ struct Loading {
   int left;
   __device__ __forceinline__ void load(const T* p, int64_t n, const Rows<T>& m) {
     a = b = make_uint4(0u, 0u, 0u, 0u);
+    if (!m.holds(kSiteIn, p, VEC && n > 0 ? (int64_t)V : min((int64_t)V, n))) n = 0;
     if (VEC) {
       if (n > 0) a = *reinterpret_cast<const uint4*>(p);
       return;
@@ -168,8 +197,9 @@ struct Loading {
 };
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store_chunk(T* p, const float* v, int64_t n) {
+__device__ __forceinline__ void store_chunk(T* p, const float* v, int64_t n, const Rows<T>& m) {
   constexpr int V = Chunk<T>::V;
+  if (!m.holds(kSiteOut, p, VEC && n > 0 ? (int64_t)V : min((int64_t)V, n))) return;
   if (VEC ? n > 0 : n >= V && (reinterpret_cast<uintptr_t>(p) & 15u) == 0) {
     Chunk<T> c;
     c.put(v);
@@ -183,7 +213,9 @@ __device__ __forceinline__ void store_chunk(T* p, const float* v, int64_t n) {
 
 // V codes (4 or 8) of one chunk, value i times inv[i].
 template <int V, bool CHECK>
-__device__ __forceinline__ void store_codes(uint8_t* p, const float* v, const float* inv, int64_t n, bool e5m2) {
+__device__ __forceinline__ void store_codes(uint8_t* p, const float* v, const float* inv, int64_t n, bool e5m2,
+                                            const Rows<uint8_t>& m) {
+  if (!m.holds(kSiteCodes, p, min((int64_t)V, n))) return;
   uint32_t u[V / 4];
 #pragma unroll
   for (int i = 0; i < V / 4; ++i) u[i] = codes4<CHECK>(v + 4 * i, inv + 4 * i, e5m2);

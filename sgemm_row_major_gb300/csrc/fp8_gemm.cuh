@@ -152,8 +152,10 @@ __device__ __forceinline__ void tmem_ld_fragments(uint32_t taddr, float* v) {
   for (int i = 0; i < 16; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 4 bytes from global to shared memory, asynchronously.
-__device__ __forceinline__ void copy4_async(uint32_t dst, const float* src) {
+// Element i of the n at src from global to shared memory, asynchronously.
+__device__ __forceinline__ void copy4_async(const Guard& g, unsigned site, uint32_t dst, const float* src, int64_t i, int64_t n) {
+  if (!in_range(g.fault, g.word, site, i, 1, n)) return;
+  src += i;
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
 // Arrives on `bar` (one of the arrivals it counts) when this thread's copies so far have landed.
@@ -171,14 +173,30 @@ __device__ __forceinline__ void more_registers() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(REGS));
 }
 
-__device__ __forceinline__ float read_c(const Fp8Out& o, int64_t i) {
+// Scales that an operand of mn rows (columns) of op(X) has, from the first to one past the last.
+__device__ __forceinline__ int64_t extent(const Fp8Scales& s, int mn, int groups) {
+  return ((mn - 1) >> s.shift) * s.si + (groups - 1) * s.sk + 1;
+}
+
+// Whether `n` elements of C (D) from row `row`, column `col` on lie in it.
+__device__ __forceinline__ bool c_holds(const Fp8Out& o, int64_t row, int64_t col, int64_t n) {
+  return in_range(o.guard.fault, o.guard.word, kSiteIn, row * o.ldc + col, n, extent(o.M, o.ldc, o.N));
+}
+__device__ __forceinline__ bool d_holds(const Fp8Out& o, int64_t row, int64_t col, int64_t n) {
+  return in_range(o.guard.fault, o.guard.word, kSiteOut, row * o.ldd + col, n, extent(o.M, o.ldd, o.N));
+}
+
+__device__ __forceinline__ float read_c(const Fp8Out& o, int64_t row, int64_t col) {
+  if (!c_holds(o, row, col, 1)) return 0.0f;
+  const int64_t i = row * o.ldc + col;
   return o.bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(o.C)[i]) : static_cast<const float*>(o.C)[i];
 }
 
 // One element of D from its sum.
 __device__ __forceinline__ void store_one(const Fp8Out& o, int64_t row, int64_t col, float v) {
   float x = o.alpha * v;
-  if (o.beta != 0.0f) x = fmaf(o.alpha, v, o.beta * read_c(o, row * o.ldc + col));
+  if (o.beta != 0.0f) x = fmaf(o.alpha, v, o.beta * read_c(o, row, col));
+  if (!d_holds(o, row, col, 1)) return;
   const int64_t i = row * o.ldd + col;
   if (o.bf16) static_cast<__nv_bfloat16*>(o.D)[i] = __float2bfloat16_rn(x);
   else        static_cast<float*>(o.D)[i] = x;
@@ -203,6 +221,7 @@ __device__ __forceinline__ void store_aligned_rows(const Fp8Out& o, int64_t row,
   char* d = static_cast<char*>(o.D) + (row * o.ldd + col) * kSize;
   const char* c = static_cast<const char*>(o.C) + (row * o.ldc + col) * kSize;
   const int64_t dstep = 4 * o.ldd * kSize, cstep = 4 * o.ldc * kSize;
+  if (!c_holds(o, row, col, 28 * o.ldc + 4) || !d_holds(o, row, col, 28 * o.ldd + 4)) return;
 #pragma unroll
   for (int r0 = 0; r0 < 8; r0 += kBatch) {
     float4 x[kBatch];
@@ -241,6 +260,7 @@ __device__ __forceinline__ void store_rows_any(const Fp8Out& o, int row0, int co
                                                int pitch) {
   T* d = static_cast<T*>(o.D) + (int64_t)row0 * o.ldd + col;
   const T* c = static_cast<const T*>(o.C) + (add ? (int64_t)row0 * o.ldc + col : 0);
+  if (rows > 0 && ((add && !c_holds(o, row0, col, (rows - 1) * o.ldc + 1)) || !d_holds(o, row0, col, (rows - 1) * o.ldd + 1))) return;
 #pragma unroll 1
   for (int r0 = 0; r0 < rows; r0 += kBatch) {
     T old[kBatch];

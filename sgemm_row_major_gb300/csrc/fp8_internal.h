@@ -15,9 +15,16 @@ struct CallDevice {
   int sm_count = 0;
   int pair_clusters = 0;
   unsigned* fault = nullptr;
+  unsigned long long* bounds = nullptr;
   cudaMemPool_t pool = nullptr;
 };
 int call_device(CallDevice* out);  // an sgemm_status
+
+// Where the debug build records an index that falls outside its buffer (in_range, device_utils.cuh).
+struct Guard {
+  unsigned* fault = nullptr;
+  unsigned long long* word = nullptr;
+};
 
 // ---- quantiser (kernel_fp8_quant.cu)
 struct QuantParams {
@@ -29,6 +36,7 @@ struct QuantParams {
   int64_t lds = 0;
   int format = 0;
   int x_vec = 0;  // 1: rows of X start at multiples of 16 bytes
+  Guard guard;
 };
 cudaError_t launch_fp8_quantize(int type, int block_rows, int block_cols, const QuantParams& p, cudaStream_t stream);
 
@@ -46,6 +54,7 @@ struct NormParams {
   float *s = nullptr, *rstd = nullptr;
   int64_t lds = 0;
   int vec = 0;  // 1: rows of all matrices start at multiples of 16 bytes and hold whole chunks of 8
+  Guard guard;
 };
 cudaError_t launch_fp8_rmsnorm(int type, const NormParams& p, cudaStream_t stream);
 
@@ -62,6 +71,7 @@ struct NormGradParams {
   int vec = 0;
   uint64_t timeout_ns = 0;
   unsigned* fault = nullptr;
+  Guard guard;
 };
 constexpr int kNormGradMaxCols = 49152;  // the wide form keeps a row of dW sums in shared memory
 cudaError_t prepare_fp8_norm();
@@ -88,6 +98,7 @@ struct Fp8Out {
   int64_t ldc = 0, ldd = 0;
   int bf16 = 0;  // type of C and D
   int vec = 0;   // 1: rows of C and D start at multiples of 16 bytes
+  Guard guard;
 };
 
 struct Fp8PairParams {
@@ -156,6 +167,7 @@ struct MoeParams {
   int dense = 0;                          // 1: nearly every expert will have a token
   int* route = nullptr;                   // the routing, left by the first kernel where `many`
   int active_max = 0, slots_max = 0;      // bounds of the routing arrays
+  Guard guard;
   uint64_t timeout_ns = 0;
   unsigned* fault = nullptr;
 };
@@ -179,7 +191,7 @@ cudaError_t encode_fp8_maps(const void* base, int64_t inner, int64_t outer, int6
                             int64_t stride, int box_outer, CUtensorMap* map);
 // Rows of `cols` codes copied to rows `ldd` apart (any alignment of the source).
 cudaError_t launch_fp8_repack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t ldd,
-                              cudaStream_t stream);
+                              const Guard& guard, cudaStream_t stream);
 // D = beta * C (alpha == 0 or K == 0).
 cudaError_t launch_fp8_scale(const Fp8Out& o, cudaStream_t stream);
 

@@ -125,13 +125,12 @@ __host__ __device__ inline size_t down_smem(const MoeParams& p) {
 template <int PER>
 __device__ __forceinline__ bool load_keys(const MoeParams& p, int t, uint32_t (&keys)[PER]) {
   const int lane = threadIdx.x & 31;
-  const float* row = p.logits + (int64_t)t * p.ldl;
   bool bad = false;
 #pragma unroll
   for (int i = 0; i < PER; ++i) {
     keys[i] = 0u;
     if (32 * i + lane < p.experts) {
-      const float x = row[32 * i + lane];
+      const float x = get_at(p.guard, kSiteLogits, p.logits, (int64_t)t * p.ldl + 32 * i + lane, extent(p.tokens, p.ldl, p.experts));
       if (!(x < INFINITY)) bad = true;
       else if (x > -INFINITY) keys[i] = order_key(x + 0.0f);  // -0 counts as 0
     }
@@ -274,10 +273,15 @@ __device__ __forceinline__ void route(const MoeParams& p, const Route& r) {
   __syncthreads();
 }
 
+__device__ __forceinline__ int64_t route_words(const MoeParams& p) {
+  return 2 + 2 * (int64_t)p.active_max + 2 * (int64_t)p.slots_max + p.tokens;
+}
+
 // What the second kernel needs of it, to (store) or from the workspace, by `threads` threads.
 __device__ __forceinline__ void copy_route(const MoeParams& p, const Route& r, bool store, int thread, int threads) {
   const auto copy = [&](int* shared, int* global, int n) {
     for (int i = thread; i < n; i += threads) {
+      if (!in_range(p.guard.fault, p.guard.word, kSitePart, global + i - p.route, 1, route_words(p))) continue;
       if (store) global[i] = shared[i];
       else       shared[i] = global[i];
     }
@@ -289,6 +293,11 @@ __device__ __forceinline__ void copy_route(const MoeParams& p, const Route& r, b
   copy(r.slot_token, g += p.active_max, p.slots_max);
   copy(reinterpret_cast<int*>(r.slot_weight), g += p.slots_max, p.slots_max);
   copy(r.poisoned, g + p.slots_max, p.tokens);
+}
+
+// Scales that stored matrices of `rows` rows and `groups` groups of columns have, all experts'.
+__device__ __forceinline__ int64_t expert_scales(int experts, int64_t stride, int rows, int64_t ld, int groups) {
+  return (experts - 1) * stride + extent((rows + 127) / 128, ld, groups);
 }
 
 // A box of a tensor map into L2.
@@ -359,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
   const uint32_t tmem = tmem_slot;
 
   if (blockIdx.x == gridDim.x - 1 && warp == 3) {  // by a warp with nothing else to do
-    for (int i = lane; i < (p.hidden + 127) / 128; i += 32) p.arrived[i] = 0;
+    for (int i = lane; i < (p.hidden + 127) / 128; i += 32) put_at(p.guard, kSitePart, p.arrived, i, (p.hidden + 127) / 128, 0);
     if (p.many) copy_route(p, r, true, lane, 32);
   }
   const int items = r.counts[0] * col_tiles;
@@ -437,8 +446,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
     for (int i = 0; ok && i < my_items; ++i) {
       const int item = (int)blockIdx.x + i * (int)gridDim.x;
       const int e = r.expert[item / col_tiles], rb = (item % col_tiles) * kUpCols >> 7;
-      const float* sg = p.sg + (int64_t)e * p.stride_sg + (int64_t)rb * p.ldsg;
-      const float* su = p.su + (int64_t)e * p.stride_su + (int64_t)rb * p.ldsu;
+      const int64_t sg = (int64_t)e * p.stride_sg + (int64_t)rb * p.ldsg, su = (int64_t)e * p.stride_su + (int64_t)rb * p.ldsu;
       for (int g0 = 0; g0 < groups; g0 += kChunkGroups) {
         if (lap > 0 && !poll_wait(smem_addr(&scale_empty[c]), (lap - 1) & 1u, p.timeout_ns)) {
           if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
@@ -448,8 +456,13 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
         const uint32_t dst = ring + 4u * (uint32_t)(c * kChunkFloats);
         const int count = min(kChunkGroups, groups - g0);
         for (int j = lane; j < NC + 2; j += 32) {
-          const float* src = j < NC ? p.sx + (int64_t)min(j, p.tokens - 1) * p.ldsx : j == NC ? sg : su;
-          for (int g = 0; g < count; ++g) copy4_async(dst + 4u * (uint32_t)(g * (NC + 4) + j), src + g0 + g);
+          const float* src = j < NC ? p.sx : j == NC ? p.sg : p.su;
+          const int64_t at = (j < NC ? (int64_t)min(j, p.tokens - 1) * p.ldsx : j == NC ? sg : su) + g0;
+          const int64_t n = j < NC    ? extent(p.tokens, p.ldsx, groups)
+                            : j == NC ? expert_scales(p.experts, p.stride_sg, p.inner, p.ldsg, groups)
+                                      : expert_scales(p.experts, p.stride_su, p.inner, p.ldsu, groups);
+          for (int g = 0; g < count; ++g)
+            copy4_async(p.guard, kSiteScale, dst + 4u * (uint32_t)(g * (NC + 4) + j), src, at + g, n);
         }
         copies_arrive(smem_addr(&scale_full[c]));
         if (++c == kChunks) {
@@ -554,10 +567,14 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
         const int col = c0 + 2 * lane;
         const int64_t slot = r.base[a] + j;
         if (col < p.inner) {  // inner is even
-          *reinterpret_cast<uint16_t*>(p.h + 2 * slot * p.inner + col) = (uint16_t)hi;
-          *reinterpret_cast<uint16_t*>(p.h + (2 * slot + 1) * p.inner + col) = (uint16_t)lo;
+          uint16_t* pairs = reinterpret_cast<uint16_t*>(p.h);
+          const int64_t n = (int64_t)p.slots_max * p.inner;
+          const int64_t at = slot * p.inner + (col >> 1);
+          put_at(p.guard, kSitePart, pairs, at, n, (uint16_t)hi);
+          put_at(p.guard, kSitePart, pairs, at + (p.inner >> 1), n, (uint16_t)lo);
         }
-        if (lane == 0) p.sh[slot * p.h_groups + c0 / kUpCols] = scale;
+        if (lane == 0)
+          put_at(p.guard, kSitePart, p.sh, slot * p.h_groups + c0 / kUpCols, (int64_t)p.slots_max * p.h_groups, scale);
       }
     }
   }
@@ -567,10 +584,13 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
   if (warp == 1) tmem_dealloc(tmem, 128);
 }
 
+__device__ __forceinline__ int64_t part_words(const MoeParams& p) { return 2 * (int64_t)p.down_grid * p.tokens * 128; }
+
 __device__ __forceinline__ void store_y(const MoeParams& p, int tok, int col, int poisoned, float v) {
   if (col >= p.hidden) return;
   if (poisoned) v = __int_as_float(0x7FFFFFFF);
   const int64_t o = (int64_t)tok * p.ldy + col;
+  if (!in_range(p.guard.fault, p.guard.word, kSiteOut, o, 1, extent(p.tokens, p.ldy, p.hidden))) return;
   if (p.bf16) static_cast<__nv_bfloat16*>(p.y)[o] = __float2bfloat16_rn(v);
   else        static_cast<float*>(p.y)[o] = v;
 }
@@ -752,12 +772,14 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
       const uint32_t dst = ring + 4u * (uint32_t)(c * kChunkFloats);
       const int n = slots_of(u.a), halves = min(2 * count, p.h_groups - 2 * u.g);
       for (int j = lane; j < n; j += 32) {
-        const float* src = p.sh + (int64_t)(base[u.a] + j) * p.h_groups + 2 * u.g;
-        for (int h = 0; h < halves; ++h) copy4_async(dst + 4u * (uint32_t)(h * NC + j), src + h);
+        const int64_t src = (int64_t)(base[u.a] + j) * p.h_groups + 2 * u.g;
+        for (int h = 0; h < halves; ++h)
+          copy4_async(p.guard, kSitePart, dst + 4u * (uint32_t)(h * NC + j), p.sh, src + h, (int64_t)p.slots_max * p.h_groups);
       }
       if (lane < count)
-        copy4_async(dst + 4u * (uint32_t)(2 * kChunkGroups * NC + lane),
-                    p.sd + (int64_t)expert[u.a] * p.stride_sd + (int64_t)u.tile * p.ldsd + u.g + lane);
+        copy4_async(p.guard, kSiteScale, dst + 4u * (uint32_t)(2 * kChunkGroups * NC + lane), p.sd,
+                    (int64_t)expert[u.a] * p.stride_sd + (int64_t)u.tile * p.ldsd + u.g + lane,
+                    expert_scales(p.experts, p.stride_sd, p.hidden, p.ldsd, groups));
       copies_arrive(smem_addr(&scale_full[c]));
       t += count;
       u.g += count - 1;
@@ -881,11 +903,12 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
           // CTAs c0 .. c1 share the tile; one that began before it uses its first slot for it, one that began
           // in it its second
           const int c0 = (int)(((t0 + 1) * ctas + total - 1) / total - 1), c1 = (int)((t1 * ctas + total - 1) / total - 1);
-          float* to = p.part + (2 * (int64_t)blockIdx.x + (u0 < t0 ? 0 : 1)) * p.tokens * 128 + row;
-          for (int tok = 0; tok < p.tokens; ++tok) to[tok * 128] = ysum[tok * 128 + row];
+          const int64_t to = (2 * (int64_t)blockIdx.x + (u0 < t0 ? 0 : 1)) * p.tokens * 128 + row;
+          for (int tok = 0; tok < p.tokens; ++tok)
+            put_at(p.guard, kSitePart, p.part, to + tok * 128, part_words(p), ysum[tok * 128 + row]);
           __threadfence();
           fold_barrier();
-          if (threadIdx.x == kFirstFold * 32 && atomicAdd(&p.arrived[at.tile], 1) == c1 - c0)
+          if (threadIdx.x == kFirstFold * 32 && in_range(p.guard.fault, p.guard.word, kSitePart, at.tile, 1, tiles) && atomicAdd(&p.arrived[at.tile], 1) == c1 - c0)
             last_tiles[n_last++] = at.tile;  // the others' sums are there
         }
         for (int tok = 0; tok < p.tokens; ++tok) ysum[tok * 128 + row] = 0.0f;
@@ -905,7 +928,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
     const int64_t t0 = tile * per_tile, t1 = t0 + per_tile;
     const int c0 = (int)(((t0 + 1) * ctas + total - 1) / total - 1), c1 = (int)((t1 * ctas + total - 1) / total - 1);
     const int64_t slot = (int64_t)p.tokens * 128;
-    const float* from = p.part + (2 * (int64_t)c0 + 1) * slot + 4 * lane;
+    const int64_t from = (2 * (int64_t)c0 + 1) * slot + 4 * lane;
     const int64_t back = bound(c0) < t0 ? -slot : 0;  // only c0 can have begun before the tile
     for (int tok0 = warp; tok0 < p.tokens; tok0 += 2 * (kThreads / 32)) {
       float4 v[2];
@@ -918,8 +941,9 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
           for (int k = 0; k < 8; ++k) {
             const int tok = tok0 + q * (kThreads / 32);
             x[q][k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-            if (k0 + k <= c1 - c0 && tok < p.tokens)
-              x[q][k] = __ldcg(reinterpret_cast<const float4*>(from + 2 * (k0 + k) * slot + (k0 + k == 0 ? back : 0) + tok * 128));
+            const int64_t word = from + 2 * (k0 + k) * slot + (k0 + k == 0 ? back : 0) + tok * 128;
+            if (k0 + k <= c1 - c0 && tok < p.tokens && in_range(p.guard.fault, p.guard.word, kSitePart, word, 4, part_words(p)))
+              x[q][k] = __ldcg(reinterpret_cast<const float4*>(p.part + word));
           }
 #pragma unroll
         for (int q = 0; q < 2; ++q)

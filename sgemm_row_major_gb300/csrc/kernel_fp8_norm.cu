@@ -44,10 +44,10 @@ struct Chunk8 {
 };
 
 template <typename T, bool VEC>
-__device__ __forceinline__ void store8(T* p, const float* v, int n) {
+__device__ __forceinline__ void store8(T* p, const float* v, int n, const Rows<T>& m) {
 #pragma unroll
   for (int i = 0; i < kChunk / Chunk<T>::V; ++i)
-    store_chunk<T, VEC>(p + i * Chunk<T>::V, v + i * Chunk<T>::V, (int64_t)(n - i * Chunk<T>::V));
+    store_chunk<T, VEC>(p + i * Chunk<T>::V, v + i * Chunk<T>::V, (int64_t)(n - i * Chunk<T>::V), m);
 }
 
 // Sum over the CTA of one float per thread; `slot` is used by one call at a time.
@@ -66,23 +66,26 @@ __device__ __forceinline__ void emit(const NormParams& p, int64_t row, int col, 
   float y[kChunk];
   {
     Chunk8<T, VEC> w;
-    w.load(static_cast<const T*>(p.w) + col, left, Rows<T>(p.w, 1, 0, p.cols));
+    w.load(static_cast<const T*>(p.w) + col, left, Rows<T>(p.w, 1, 0, p.cols, p.guard));
     w.get(y);
   }
 #pragma unroll
   for (int e = 0; e < kChunk; ++e) y[e] = h[e] * rstd * y[e];  // columns past the end: h = 0
-  if (p.y && left > 0) store8<T, VEC>(static_cast<T*>(p.y) + row * p.ldy + col, y, left);
+  if (p.y && left > 0)
+    store8<T, VEC>(static_cast<T*>(p.y) + row * p.ldy + col, y, left, Rows<T>(p.y, p.rows, p.ldy, p.cols, p.guard));
   if (p.q) {
     float m = 0.0f;
 #pragma unroll
     for (int e = 0; e < kChunk; ++e) m = fmaxf(m, finite_abs(y[e]));
     const float s = group_scale(lanes_max<16>(m), kMaxE4M3);
     if (left > 0) {
-      if (col % 128 == 0) p.s[row * p.lds + col / 128] = s;
+      if (col % 128 == 0)
+        put_at(p.guard, kSiteScale, p.s, row * p.lds + col / 128, extent(p.rows, p.lds, (p.cols - 1) / 128 + 1), s);
       float inv[kChunk];
 #pragma unroll
       for (int e = 0; e < kChunk; ++e) inv[e] = __frcp_rn(s);
-      store_codes<kChunk, true>(p.q + row * p.ldq + col, y, inv, left, false);
+      store_codes<kChunk, true>(p.q + row * p.ldq + col, y, inv, left, false,
+                                Rows<uint8_t>(p.q, p.rows, p.ldq, p.cols, p.guard));
     }
   }
 }
@@ -93,8 +96,8 @@ struct Sum8 {
   Chunk8<T, VEC> x, r;
   __device__ __forceinline__ void load(const NormParams& p, int64_t row, int col) {
     const int left = p.cols - col;
-    x.load(static_cast<const T*>(p.x) + row * p.ldx + col, left, Rows<T>(p.x, p.rows, p.ldx, p.cols));
-    if (p.r) r.load(static_cast<const T*>(p.r) + row * p.ldr + col, left, Rows<T>(p.r, p.rows, p.ldr, p.cols));
+    x.load(static_cast<const T*>(p.x) + row * p.ldx + col, left, Rows<T>(p.x, p.rows, p.ldx, p.cols, p.guard));
+    if (p.r) r.load(static_cast<const T*>(p.r) + row * p.ldr + col, left, Rows<T>(p.r, p.rows, p.ldr, p.cols, p.guard));
   }
   __device__ __forceinline__ void get(const NormParams& p, float* h) const {
     x.get(h);
@@ -136,11 +139,12 @@ __global__ void __launch_bounds__(1024) rmsnorm_kernel(const __grid_constant__ N
     ss += a;
   }
   const float rstd = __frsqrt_rn(cta_sum(ss, slot) / (float)p.cols + p.eps);
-  if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+  if (p.rstd && threadIdx.x == 0) put_at(p.guard, kSiteRowStat, p.rstd, row, p.rows, rstd);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int col = kChunk * (j * (int)blockDim.x + (int)threadIdx.x);
-    if (p.h && col < p.cols) store8<T, VEC>(static_cast<T*>(p.h) + row * p.ldh + col, h[j], p.cols - col);
+    if (p.h && col < p.cols)
+      store8<T, VEC>(static_cast<T*>(p.h) + row * p.ldh + col, h[j], p.cols - col, Rows<T>(p.h, p.rows, p.ldh, p.cols, p.guard));
     emit<T, VEC>(p, row, col, h[j], rstd);
   }
 }
@@ -165,7 +169,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_wide_kernel(const __grid_constan
     ss += a;
   }
   const float rstd = __frsqrt_rn(cta_sum(ss, slot) / (float)p.cols + p.eps);
-  if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+  if (p.rstd && threadIdx.x == 0) put_at(p.guard, kSiteRowStat, p.rstd, row, p.rows, rstd);
   for (int64_t c0 = 0; c0 < p.cols; c0 += step) {
     float h[kChunk];
     // every lane stays in the loop (the groups' shuffles); past the end it works on no columns
@@ -174,7 +178,8 @@ __global__ void __launch_bounds__(1024) rmsnorm_wide_kernel(const __grid_constan
     in.load(p, row, col);
     in.get(p, h);
     // h may overwrite x or r: only this thread reads these columns, and it has
-    if (p.h && col < p.cols) store8<T, VEC>(static_cast<T*>(p.h) + row * p.ldh + col, h, p.cols - col);
+    if (p.h && col < p.cols)
+      store8<T, VEC>(static_cast<T*>(p.h) + row * p.ldh + col, h, p.cols - col, Rows<T>(p.h, p.rows, p.ldh, p.cols, p.guard));
     emit<T, VEC>(p, row, col, h, rstd);
   }
 }
@@ -196,20 +201,25 @@ cudaError_t launch_forward(const NormParams& p, cudaStream_t stream) {
 
 // ------------------------------------------------------------------ backward
 
+// A column of this CTA's sums of dW.
+__device__ __forceinline__ void put_partial(const NormGradParams& p, int col, float v) {
+  put_at(p.guard, kSitePart, p.partial, (int64_t)blockIdx.x * p.cols + col, (int64_t)gridDim.x * p.cols, v);
+}
+
 template <typename T, int NV, bool VEC>
 struct GradRow {  // a thread's chunks of dy, h and dh of one row
   Chunk8<T, VEC> dy[NV], h[NV], dh[NV];
   float rstd;
   __device__ __forceinline__ void load(const NormGradParams& p, int64_t row) {
-    rstd = p.rstd[row];
+    rstd = get_at(p.guard, kSiteRowStat, p.rstd, row, p.rows);
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int col = kChunk * (j * (int)blockDim.x + (int)threadIdx.x), left = p.cols - col;
-      dy[j].load(static_cast<const T*>(p.dy) + row * p.lddy + col, left, Rows<T>(p.dy, p.rows, p.lddy, p.cols));
-      h[j].load(static_cast<const T*>(p.h) + row * p.ldh + col, left, Rows<T>(p.h, p.rows, p.ldh, p.cols));
+      dy[j].load(static_cast<const T*>(p.dy) + row * p.lddy + col, left, Rows<T>(p.dy, p.rows, p.lddy, p.cols, p.guard));
+      h[j].load(static_cast<const T*>(p.h) + row * p.ldh + col, left, Rows<T>(p.h, p.rows, p.ldh, p.cols, p.guard));
       if (p.dh)
         dh[j].load(static_cast<const T*>(p.dh) + row * p.lddh + col, left,
-                                 Rows<T>(p.dh, p.rows, p.lddh, p.cols));
+                                 Rows<T>(p.dh, p.rows, p.lddh, p.cols, p.guard));
     }
   }
 };
@@ -233,7 +243,8 @@ __device__ __forceinline__ void grad_chunk(const NormGradParams& p, int64_t row,
 #pragma unroll
     for (int e = 0; e < kChunk; ++e) dx[e] += dh[e];
   }
-  if (col < p.cols) store8<T, VEC>(static_cast<T*>(p.dx) + row * p.lddx + col, dx, p.cols - col);
+  if (col < p.cols)
+    store8<T, VEC>(static_cast<T*>(p.dx) + row * p.lddx + col, dx, p.cols - col, Rows<T>(p.dx, p.rows, p.lddx, p.cols, p.guard));
 }
 
 template <typename T, bool VEC>
@@ -254,7 +265,7 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_kernel(const __grid_constant
   for (int j = 0; j < NV; ++j) {
     const int col = kChunk * (j * (int)blockDim.x + (int)threadIdx.x);
     Chunk8<T, VEC> c;
-    c.load(static_cast<const T*>(p.w) + col, p.cols - col, Rows<T>(p.w, 1, 0, p.cols));
+    c.load(static_cast<const T*>(p.w) + col, p.cols - col, Rows<T>(p.w, 1, 0, p.cols, p.guard));
     c.get(w[j]);
 #pragma unroll
     for (int e = 0; e < kChunk; ++e) acc[j][e] = 0.0f;
@@ -283,7 +294,7 @@ __global__ void __launch_bounds__(512) rmsnorm_grad_kernel(const __grid_constant
       const int col = kChunk * (j * (int)blockDim.x + (int)threadIdx.x);
 #pragma unroll
       for (int e = 0; e < kChunk; ++e)
-        if (col + e < p.cols) p.partial[(int64_t)blockIdx.x * p.cols + col + e] = acc[j][e];
+        if (col + e < p.cols) put_partial(p, col + e, acc[j][e]);
     }
   }
 }
@@ -307,9 +318,13 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_ring_kernel(const __grid_
   const auto load = [&](int s, int64_t row) {  // one thread
     const uint32_t bar = smem_addr(&full[s]), dst = smem_addr(ring) + (uint32_t)s * slot_bytes;
     mbar_arrive_expect_tx(bar, parts * row_bytes);
-    bulk_load(dst, static_cast<const T*>(p.dy) + row * p.lddy, row_bytes, bar);
-    bulk_load(dst + row_bytes, static_cast<const T*>(p.h) + row * p.ldh, row_bytes, bar);
-    if (p.dh) bulk_load(dst + 2 * row_bytes, static_cast<const T*>(p.dh) + row * p.lddh, row_bytes, bar);
+    const auto part = [&](int i, const void* base, int64_t ld) {
+      const T* src = static_cast<const T*>(base) + row * ld;
+      if (Rows<T>(base, p.rows, ld, p.cols, p.guard).holds(kSiteIn, src, p.cols)) bulk_load(dst + i * row_bytes, src, row_bytes, bar);
+    };
+    part(0, p.dy, p.lddy);
+    part(1, p.h, p.ldh);
+    if (p.dh) part(2, p.dh, p.lddh);
   };
   if (threadIdx.x == 0) {
     for (int s = 0; s < depth; ++s) mbar_init(smem_addr(&full[s]), 1);
@@ -322,7 +337,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_ring_kernel(const __grid_
   for (int j = 0; j < NV; ++j) {
     const int col = kChunk * (j * (int)blockDim.x + (int)threadIdx.x);
     Chunk8<T, true> c;
-    c.load(static_cast<const T*>(p.w) + col, p.cols - col, Rows<T>(p.w, 1, 0, p.cols));
+    c.load(static_cast<const T*>(p.w) + col, p.cols - col, Rows<T>(p.w, 1, 0, p.cols, p.guard));
     c.get(w[j]);
 #pragma unroll
     for (int e = 0; e < kChunk; ++e) acc[j][e] = 0.0f;
@@ -333,7 +348,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_ring_kernel(const __grid_
   bool ok = true;  // the same in every thread: each waits for the same phases
   int it = 0;
   for (int64_t row = blockIdx.x; row < p.rows; row += gridDim.x, ++it) {
-    const float rstd = p.rstd[row];
+    const float rstd = get_at(p.guard, kSiteRowStat, p.rstd, row, p.rows);
     ok = ok && mbar_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns);
     if (!ok && threadIdx.x == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
     const T* base = reinterpret_cast<const T*>(ring + (size_t)s * slot_bytes);
@@ -342,7 +357,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_ring_kernel(const __grid_
 #pragma unroll
     for (int j = 0; j < NV; ++j) {
       const int col = kChunk * (j * (int)blockDim.x + (int)threadIdx.x), left = p.cols - col;
-      const Rows<T> in(base, 1, 0, 3 * p.cols);
+      const Rows<T> in(base, 1, 0, 3 * p.cols, p.guard);
       dy[j].load(base + col, left, in);
       h[j].load(base + p.cols + col, left, in);
       if (p.dh) dh[j].load(base + 2 * p.cols + col, left, in);
@@ -365,7 +380,7 @@ __global__ void __launch_bounds__(512, 1) rmsnorm_grad_ring_kernel(const __grid_
       const int col = kChunk * (j * (int)blockDim.x + (int)threadIdx.x);
 #pragma unroll
       for (int e = 0; e < kChunk; ++e)
-        if (col + e < p.cols) p.partial[(int64_t)blockIdx.x * p.cols + col + e] = acc[j][e];
+        if (col + e < p.cols) put_partial(p, col + e, acc[j][e]);
     }
   }
 }
@@ -388,12 +403,12 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_wide_kernel(const NormGradP
     float w[kChunk], dot = 0.0f;
     const auto load = [&](int col, bool with_dh) {
       const int left = p.cols - col;
-      cdy.load(static_cast<const T*>(p.dy) + row * p.lddy + col, left, Rows<T>(p.dy, p.rows, p.lddy, p.cols));
-      ch.load(static_cast<const T*>(p.h) + row * p.ldh + col, left, Rows<T>(p.h, p.rows, p.ldh, p.cols));
-      cw.load(static_cast<const T*>(p.w) + col, left, Rows<T>(p.w, 1, 0, p.cols));
+      cdy.load(static_cast<const T*>(p.dy) + row * p.lddy + col, left, Rows<T>(p.dy, p.rows, p.lddy, p.cols, p.guard));
+      ch.load(static_cast<const T*>(p.h) + row * p.ldh + col, left, Rows<T>(p.h, p.rows, p.ldh, p.cols, p.guard));
+      cw.load(static_cast<const T*>(p.w) + col, left, Rows<T>(p.w, 1, 0, p.cols, p.guard));
       if (with_dh)
         cdh.load(static_cast<const T*>(p.dh) + row * p.lddh + col, left,
-                                 Rows<T>(p.dh, p.rows, p.lddh, p.cols));
+                                 Rows<T>(p.dh, p.rows, p.lddh, p.cols, p.guard));
       cw.get(w);
     };
     for (int col = col0; col < p.cols; col += step) {
@@ -401,7 +416,7 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_wide_kernel(const NormGradP
       dot += grad_dot<T, false>(cdy, ch, w);
     }
     dot = cta_sum(dot, slot[it & 1]);
-    const float rstd = p.rstd[row];
+    const float rstd = get_at(p.guard, kSiteRowStat, p.rstd, row, p.rows);
     const float c = rstd * rstd * (dot / (float)p.cols);
     for (int col = col0; col < p.cols; col += step) {
       load(col, p.dh != nullptr);
@@ -418,13 +433,13 @@ __global__ void __launch_bounds__(1024) rmsnorm_grad_wide_kernel(const NormGradP
     for (int col = col0; col < p.cols; col += step)
 #pragma unroll
       for (int e = 0; e < kChunk; ++e)
-        if (col + e < p.cols) p.partial[(int64_t)blockIdx.x * p.cols + col + e] = acc_s[col + e];
+        if (col + e < p.cols) put_partial(p, col + e, acc_s[col + e]);
 }
 
 // dw = the CTAs' sums in CTA order: 32 columns per CTA, warp i adds a fixed share of the rows of
 // `partial`, then the 32 warps' sums are added in warp order.
 __global__ void __launch_bounds__(1024) grad_reduce_kernel(const float* __restrict__ partial, int n, int cols,
-                                                           float* __restrict__ dw) {
+                                                           float* __restrict__ dw, const Guard guard) {
   __shared__ float part[32][33];
   asm volatile("griddepcontrol.wait;" ::: "memory");  // a programmatic dependent of the kernel above
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -432,14 +447,14 @@ __global__ void __launch_bounds__(1024) grad_reduce_kernel(const float* __restri
   const int each = (n + 31) / 32;
   float a = 0.0f;
   if (col < cols)
-    for (int i = warp * each; i < min(n, (warp + 1) * each); ++i) a += partial[(int64_t)i * cols + col];
+    for (int i = warp * each; i < min(n, (warp + 1) * each); ++i) a += get_at(guard, kSitePart, partial, (int64_t)i * cols + col, (int64_t)n * cols);
   part[warp][lane] = a;
   __syncthreads();
   if (warp == 0 && col < cols) {
     float s = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) s += part[i][lane];
-    dw[col] = s;
+    put_at(guard, kSiteOut, dw, col, cols, s);
   }
 }
 
@@ -486,7 +501,7 @@ cudaError_t launch_backward(int type, const NormGradParams& p, int grid, cudaStr
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     const float* partial = p.partial;
-    e = cudaLaunchKernelEx(&cfg, grad_reduce_kernel, partial, grid, p.cols, p.dw);
+    e = cudaLaunchKernelEx(&cfg, grad_reduce_kernel, partial, grid, p.cols, p.dw, p.guard);
   }
   return e;
 }

@@ -157,7 +157,7 @@ __device__ __forceinline__ void prefetch_c(const Fp8Out& o, int row0, int row1, 
   for (int r = row0 + (threadIdx.x & 31); r < min(row1, o.M); r += 32) {
     const uintptr_t first = reinterpret_cast<uintptr_t>(o.C) + (uintptr_t)(((int64_t)r * o.ldc + col0) * size);
     const uintptr_t from = (first + 15) & ~(uintptr_t)15, to = (first + (uintptr_t)bytes) & ~(uintptr_t)15;
-    if (from < to)
+    if (from < to && c_holds(o, r, col0, bytes / size))
       asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(from), "r"((uint32_t)(to - from)) : "memory");
   }
 }
@@ -325,8 +325,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           const int count = min(kChunk, groups - g0);
           for (int j = lane; j < n; j += 32) {
             const int64_t at = rows || COLS ? min(first + j, last) >> sc.shift : min((first >> 7) + j, last >> 7);
-            const float* src = sc.p + at * sc.si + (int64_t)g0 * sc.sk;
-            for (int g = 0; g < count; ++g) copy4_async(dst + 4u * (uint32_t)(g * pitch + j), src + (int64_t)g * sc.sk);
+            const int64_t src = at * sc.si + (int64_t)g0 * sc.sk, held = extent(sc, last + 1, groups);
+            for (int g = 0; g < count; ++g)
+              copy4_async(p.out.guard, kSiteScale, dst + 4u * (uint32_t)(g * pitch + j), sc.p, src + (int64_t)g * sc.sk, held);
           }
           copies_arrive(smem_addr(&scale_full[c]));
           if (OUT != kOutPlain && rows) {  // the rows in equal parts, one with each chunk

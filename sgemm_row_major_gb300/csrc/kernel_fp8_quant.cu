@@ -48,7 +48,7 @@ struct Quant {
     Chunk<T> c[kPasses];
     {
       const T* x = static_cast<const T*>(p.x) + (rt * kTile + lr) * p.ldx + col;
-      const Rows<T> all(p.x, p.rows, p.ldx, p.cols);
+      const Rows<T> all(p.x, p.rows, p.ldx, p.cols, p.guard);
       constexpr int kBatch = VEC ? kPasses : 4;  // chunks on their way at once
 #pragma unroll
       for (int i0 = 0; i0 < kPasses; i0 += kBatch) {
@@ -60,6 +60,7 @@ struct Quant {
         for (int i = 0; i < kBatch; ++i) c[i0 + i] = l[i].get();
       }
     }
+    const int64_t scales = extent(G == kRow ? p.rows : (p.rows + kTile - 1) / kTile, p.lds, G == kCol ? p.cols : (p.cols + kTile - 1) / kTile);
     bool again = false;
     float inv[G == kCol ? V : 1];
     if (G != kRow) {
@@ -85,7 +86,7 @@ struct Quant {
         for (int i = 1; i < kQuantThreads / 32; ++i) a = fmaxf(a, part[0][i]);
         again = !CHECK && a > kMaxFloat;
         const float s = group_scale(a, top);
-        if (threadIdx.x == 0) p.s[rt * p.lds + ct] = s;
+        if (threadIdx.x == 0) put_at(p.guard, kSiteScale, p.s, rt * p.lds + ct, scales, s);
         inv[0] = __frcp_rn(s);
       } else {
 #pragma unroll
@@ -98,7 +99,7 @@ struct Quant {
           const float s = group_scale(a, top);
           part[0][threadIdx.x] = s;
           const int64_t at = (int64_t)ct * kTile + threadIdx.x;
-          if (at < p.cols) p.s[rt * p.lds + at] = s;
+          if (at < p.cols) put_at(p.guard, kSiteScale, p.s, rt * p.lds + at, scales, s);
         }
         __syncthreads();
 #pragma unroll
@@ -110,6 +111,7 @@ struct Quant {
       }
     }
     uint8_t* q = p.q + (rt * kTile + lr) * p.ldq + col;
+    const Rows<uint8_t> codes(p.q, p.rows, p.ldq, p.cols, p.guard);
 #pragma unroll
     for (int i = 0; i < kPasses; ++i, q += kRowsPerPass * p.ldq) {
       const bool in = i * kRowsPerPass < rows;
@@ -123,13 +125,13 @@ struct Quant {
         again = again || (!CHECK && m > kMaxFloat);
         const float s = group_scale(m, top);
         inv[0] = __frcp_rn(s);
-        if (lc == 0 && in) p.s[(rt * kTile + lr + i * kRowsPerPass) * p.lds + ct] = s;
+        if (lc == 0 && in) put_at(p.guard, kSiteScale, p.s, (rt * kTile + lr + i * kRowsPerPass) * p.lds + ct, scales, s);
       }
       if (in) {
         float f[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) f[e] = inv[G == kCol ? e : 0];
-        store_codes<V, CHECK>(q, v, f, left, e5m2);
+        store_codes<V, CHECK>(q, v, f, left, e5m2, codes);
       }
     }
     return again;

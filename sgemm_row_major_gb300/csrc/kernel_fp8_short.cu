@@ -180,8 +180,9 @@ __global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
       for (int j = lane; j < BL + TS; j += 32) {
         const Fp8Scales& sc = j < BL ? p.sl : p.ss;
         const int64_t at = j < BL ? min(l0 + j, p.L - 1) : min(s0 + j - BL, p.S - 1);
-        const float* src = sc.p + (at >> sc.shift) * sc.si + (int64_t)(g0 + t) * sc.sk;
-        for (int g = 0; g < count; ++g) copy4_async(dst + 4u * (uint32_t)(g * (BL + TS) + j), src + (int64_t)g * sc.sk);
+        const int64_t src = (at >> sc.shift) * sc.si + (int64_t)(g0 + t) * sc.sk, n = extent(sc, j < BL ? p.L : p.S, groups);
+        for (int g = 0; g < count; ++g)
+          copy4_async(p.out.guard, kSiteScale, dst + 4u * (uint32_t)(g * (BL + TS) + j), sc.p, src + (int64_t)g * sc.sk, n);
       }
       copies_arrive(smem_addr(&scale_full[c]));
       if (++c == kChunks) {
@@ -310,17 +311,18 @@ cudaError_t with_short_kernel(int tile_s, const F& f) {
 }
 
 __global__ void __launch_bounds__(256) repack_kernel(const uint8_t* __restrict__ src, int64_t ld, int64_t rows,
-                                                     int64_t cols, uint8_t* __restrict__ dst, int64_t ldd) {
+                                                     int64_t cols, uint8_t* __restrict__ dst, int64_t ldd,
+                                                     const Guard guard) {
   const int64_t chunks = ldd / 16, total = rows * chunks;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t r = i / chunks, c = (i - r * chunks) * 16;
-    const uint8_t* s = src + r * ld + c;
+    const int64_t s = r * ld + c;
     const int n = (int)min((int64_t)16, cols - c);
     uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int k = 0; k < 16; ++k)
-      if (k < n) w[k / 4] |= (uint32_t)s[k] << (8 * (k % 4));
-    *reinterpret_cast<uint4*>(dst + r * ldd + c) = make_uint4(w[0], w[1], w[2], w[3]);
+      if (k < n) w[k / 4] |= (uint32_t)get_at(guard, kSiteCodes, src, s + k, extent(rows, ld, cols)) << (8 * (k % 4));
+    put_at(guard, kSitePart, reinterpret_cast<uint4*>(dst), i, total, make_uint4(w[0], w[1], w[2], w[3]));
   }
 }
 
@@ -328,7 +330,8 @@ __global__ void __launch_bounds__(256) scale_kernel(const Fp8Out o) {
   const int64_t total = (int64_t)o.M * o.N;
   for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < total; i += (int64_t)gridDim.x * blockDim.x) {
     const int64_t row = i / o.N, col = i - row * o.N;
-    const float x = o.beta == 0.0f ? 0.0f : o.beta * read_c(o, row * o.ldc + col);
+    const float x = o.beta == 0.0f ? 0.0f : o.beta * read_c(o, row, col);
+    if (!d_holds(o, row, col, 1)) continue;
     const int64_t d = row * o.ldd + col;
     if (o.bf16) static_cast<__nv_bfloat16*>(o.D)[d] = __float2bfloat16_rn(x);
     else        static_cast<float*>(o.D)[d] = x;
@@ -375,10 +378,10 @@ cudaError_t launch_fp8_short(const CUtensorMap& mapL, const CUtensorMap& mapS, c
 }
 
 cudaError_t launch_fp8_repack(const void* src, int64_t ld, int64_t rows, int64_t cols, void* dst, int64_t ldd,
-                              cudaStream_t stream) {
+                              const Guard& guard, cudaStream_t stream) {
   const int64_t blocks = (rows * (ldd / 16) + 255) / 256;
   f8::repack_kernel<<<(unsigned)(blocks < 8192 ? blocks : 8192), 256, 0, stream>>>(
-      static_cast<const uint8_t*>(src), ld, rows, cols, static_cast<uint8_t*>(dst), ldd);
+      static_cast<const uint8_t*>(src), ld, rows, cols, static_cast<uint8_t*>(dst), ldd, guard);
   return cudaGetLastError();
 }
 

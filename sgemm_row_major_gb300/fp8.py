@@ -39,26 +39,30 @@ _raw_stream = None
 _current_device = None
 
 
+def _declare(lib):
+    """C signatures of this file's entry points."""
+    i64, f32, vp, ci = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_int
+    mp, ep, ch = ctypes.POINTER(MatrixStruct), ctypes.POINTER(ExpertsStruct), ctypes.c_char
+    for name, args in {
+        "sgemm_fp8": [ch, ch, i64, i64, i64, f32, mp, mp, f32, vp, i64, vp, i64, ci, vp],
+        "sgemm_fp8_plan": [ch, ch, i64, i64, i64, f32, mp, mp, f32, vp, i64, vp, i64, ci, ci, ctypes.POINTER(PlanStruct)],
+        "sgemm_fp8_set_override": [ci, ci, ci],
+        "sgemm_fp8_moe": [i64, i64, i64, i64, ci, mp, vp, i64, ci, ep, ep, ep, vp, i64, ci, vp],
+        "sgemm_fp8_quantize": [i64, i64, vp, ci, i64, ci, ci, ci, vp, i64, vp, i64, vp],
+        "sgemm_fp8_rmsnorm": [i64, i64, ci, vp, i64, vp, i64, vp, f32, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp],
+        "sgemm_fp8_rmsnorm_backward": [i64, i64, ci, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp],
+    }.items():
+        f = getattr(lib, name)
+        f.restype, f.argtypes = ci, args
+    return lib
+
+
 def _lib():
     """The compiled library with the C signatures of this file's entry points."""
     global _functions, _T, _raw_stream, _current_device
     if _functions is None:
         import torch
-        lib = load()
-        i64, f32, vp, ci = ctypes.c_int64, ctypes.c_float, ctypes.c_void_p, ctypes.c_int
-        mp, ep, ch = ctypes.POINTER(MatrixStruct), ctypes.POINTER(ExpertsStruct), ctypes.c_char
-        lib.sgemm_fp8_plan.restype = ci
-        lib.sgemm_fp8_plan.argtypes = [ch, ch, i64, i64, i64, f32, mp, mp, f32, vp, i64, vp, i64, ci, ci, ctypes.POINTER(PlanStruct)]
-        for name, args in {
-            "sgemm_fp8": [ch, ch, i64, i64, i64, f32, mp, mp, f32, vp, i64, vp, i64, ci, vp],
-            "sgemm_fp8_set_override": [ci, ci, ci],
-            "sgemm_fp8_moe": [i64, i64, i64, i64, ci, mp, vp, i64, ci, ep, ep, ep, vp, i64, ci, vp],
-            "sgemm_fp8_quantize": [i64, i64, vp, ci, i64, ci, ci, ci, vp, i64, vp, i64, vp],
-            "sgemm_fp8_rmsnorm": [i64, i64, ci, vp, i64, vp, i64, vp, f32, vp, i64, vp, i64, vp, i64, vp, i64, vp, vp],
-            "sgemm_fp8_rmsnorm_backward": [i64, i64, ci, vp, i64, vp, i64, vp, vp, vp, i64, vp, i64, vp, vp],
-        }.items():
-            f = getattr(lib, name)
-            f.restype, f.argtypes = ci, args
+        lib = _declare(load())
         _CODES.update({torch.float8_e4m3fn: 0, torch.float8_e5m2: 1})
         _TYPES.update({torch.float32: 0, torch.bfloat16: 1})
         # the handle alone: torch.cuda.current_stream() builds an object, which costs as much as a launch

@@ -21,10 +21,7 @@ def linked_with(tmp_path, symbol, c_source):
         f.write(c_source)
     subprocess.run([build.nvcc(), *build.ARCH, "-shared", "-Xcompiler", "-fPIC", "-Xlinker", "--wrap=" + symbol, "-o", out, src, *objs,
                     "-cudart", "static"], check=True, capture_output=True)
-    lib = sg._declare(ctypes.CDLL(out))
-    for name in ("sgemm_fp8", "sgemm_fp8_plan", "sgemm_fp8_quantize", "sgemm_fp8_set_override"):
-        getattr(lib, name).restype, getattr(lib, name).argtypes = ctypes.c_int, getattr(fp8._lib(), name).argtypes
-    return lib
+    return fp8._declare(sg._declare(ctypes.CDLL(out)))
 
 
 def product_of_ones(lib, n=64):
