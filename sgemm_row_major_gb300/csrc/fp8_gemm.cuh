@@ -114,26 +114,12 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
   for (int i = 0; i < 32; ++i) v[i] = __uint_as_float(r[i]);
 }
 
-// 8 consecutive 32-bit columns of this thread's TMEM lane.
-__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float* v) {
-  uint32_t r[8];
-  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
-               : "r"(taddr)
-               : "memory");
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(r[i]);
-}
-
-// N (a multiple of 8, up to 32) consecutive columns.
+// N (16 or 32) consecutive columns.
 template <int N>
-__device__ __forceinline__ void tmem_ld(uint32_t taddr, float* v) {
-  if constexpr (N == 32) {
-    tmem_ld32(taddr, v);
-  } else {
-    if constexpr (N >= 16) tmem_ld16(taddr, *reinterpret_cast<float(*)[16]>(v));
-    if constexpr (N % 16 == 8) tmem_ld8(taddr + (N >= 16 ? 16u : 0u), v + (N >= 16 ? 16 : 0));
-  }
+__device__ __forceinline__ void tmem_ld(uint32_t taddr, float (&v)[N]) {
+  static_assert(N == 16 || N == 32, "columns at a time");
+  if constexpr (N == 32) tmem_ld32(taddr, v);
+  else                   tmem_ld16(taddr, v);
 }
 
 // 16 rows x 32 columns of this warp's TMEM lanes from taddr's lane on, as the tensor cores' own fragments

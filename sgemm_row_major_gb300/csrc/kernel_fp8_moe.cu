@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
         for (int j0 = 0; j0 < NC; j0 += 32) {
           constexpr int kCols = NC < 32 ? NC : 32;
           float v[kCols];
-          tmem_ld<kCols>(tq + (uint32_t)(b * NC + j0), v);
+          tmem_ld(tq + (uint32_t)(b * NC + j0), v);
           tmem_wait_ld();
           if (j0 + kCols == NC) {
             tmem_fence_before_sync();

@@ -60,7 +60,7 @@ constexpr int kMoverRegs = 40, kFoldRegs = 232;
 static_assert(128 * kMoverRegs + 32 * kFoldWarps * kFoldRegs <= kThreads * 168, "registers at launch");
 constexpr int kMaxBufs = 4;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kLoadCols = 32;             // accumulator columns a folder thread loads at a time, at most
+constexpr int kLoadCols = 32;             // accumulator columns a folder thread loads at a time
 
 // Scales of a chunk of groups: of the CTA's 128 rows, and of the tile's columns (COLS) or its two or
 // three column blocks.
@@ -347,7 +347,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // ------------------------------------------------ folders, then D (both CTAs)
     const int q = warp & 3;                     // TMEM lane quarter this warp may access
     const int part = (warp - kFirstFold) >> 2;  // which half of the tile's columns
-    constexpr int cols = TN / 2;                // a multiple of 16
+    constexpr int cols = TN / 2;
+    static_assert(cols % kLoadCols == 0, "whole loads");
     static_assert(cols <= 128 && 128 % cols == 0, "a thread's columns lie in one column block");
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(cols * part);
     uint8_t* out = smem_raw + pad + kStages * kStageBytes + (warp - kFirstFold) * kOutBytes;
@@ -380,9 +381,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         float s0 = 0.0f;
         // 32 columns at a time, the next ones on their way while these are added
         const auto add = [&](auto first, float* v) {
-          constexpr int kFirst = decltype(first)::value, kCount = cols - kFirst < kLoadCols ? cols - kFirst : kLoadCols;
+          constexpr int kFirst = decltype(first)::value;
 #pragma unroll
-          for (int k = 0; k < kCount; k += 8) {
+          for (int k = 0; k < kLoadCols; k += 8) {
             float* x = v + k;
 #pragma unroll
             for (int e = 0; e < 8; ++e) asm volatile("" : "+f"(x[e]));  // used behind the wait only
@@ -392,10 +393,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             for (int e = 0; e < 4; ++e) m[e] = __ffma2_rn(make_float2(x[2 * e], x[2 * e + 1]), w2, m[e]);
           }
         };
-        const auto load = [&](auto first, float* v) {
-          constexpr int kFirst = decltype(first)::value, kCount = cols - kFirst < kLoadCols ? cols - kFirst : kLoadCols;
-          tmem_ld<kCount>(acc + (uint32_t)kFirst, v);
-        };
+        const auto load = [&](auto first, float (&v)[kLoadCols]) { tmem_ld(acc + (uint32_t)decltype(first)::value, v); };
         // With a scale per column the fold takes longer than the products: the next group's are then done
         // before this one's last columns are added, and asking beforehand saves the wait's latency (182 to
         // 171 us for 4096 x 4096 x 8192; where the fold waits for the products it costs 4%).

@@ -63,7 +63,7 @@ struct Quant {
     const int64_t scales = extent(G == kRow ? p.rows : (p.rows + kTile - 1) / kTile, p.lds, G == kCol ? p.cols : (p.cols + kTile - 1) / kTile);
     bool again = false;
     float inv[G == kCol ? V : 1];
-    if (G != kRow) {
+    if constexpr (G != kRow) {
       float m[G == kCol ? V : 1];
 #pragma unroll
       for (int e = 0; e < (G == kCol ? V : 1); ++e) m[e] = 0.0f;
@@ -77,7 +77,7 @@ struct Quant {
           x = fmaxf(x, mag(v[e]));
         }
       }
-      if (G == kBlock) {
+      if constexpr (G == kBlock) {
         const float w = lanes_max<32>(m[0]);
         if ((threadIdx.x & 31) == 0) part[0][threadIdx.x >> 5] = w;
         __syncthreads();
@@ -90,7 +90,7 @@ struct Quant {
         inv[0] = __frcp_rn(s);
       } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) part[lr][lc * V + e] = m[G == kCol ? e : 0];
+        for (int e = 0; e < V; ++e) part[lr][lc * V + e] = m[e];
         __syncthreads();
         if (threadIdx.x < kTile) {
           float a = 0.0f;
@@ -103,7 +103,7 @@ struct Quant {
         }
         __syncthreads();
 #pragma unroll
-        for (int e = 0; e < (G == kCol ? V : 1); ++e) {
+        for (int e = 0; e < V; ++e) {
           const float s = part[0][lc * V + e];
           again = again || (!CHECK && s > kMaxFloat);
           inv[e] = __frcp_rn(s);

@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, TS == 128 ? 1 : 2)
 #pragma unroll
       for (int j0 = 0; j0 < TS; j0 += kCols) {
         float v[kCols];
-        tmem_ld<kCols>(tq + (uint32_t)b * kAccCols + (uint32_t)j0, v);
+        tmem_ld(tq + (uint32_t)b * kAccCols + (uint32_t)j0, v);
         tmem_wait_ld();
         if (j0 + kCols == TS) {
           tmem_fence_before_sync();

@@ -102,10 +102,10 @@ def _type(x, name) -> int:
     return t
 
 
-def _check(x, name, dims=2, dtype=None):
+def _check(x, name, dims, dtype):
     if x.dim() != dims:
-        raise TypeError(f"{name} must have {dims} dimension(s)")
-    if dtype is not None and x.dtype != dtype:
+        raise TypeError(f"{name} must have {dims} dimensions")
+    if x.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
     if x.shape[-1] > 1 and x.stride(-1) != 1:
         raise TypeError(f"{name}: the last dimension must be contiguous")
@@ -124,10 +124,6 @@ def _rows(x, name):
     if rows <= 1 or cols == 0:
         ld = cols or 1
     return rows, cols, ld
-
-
-def _ld(x) -> int:
-    return _rows(x, "tensor")[2]
 
 
 def _empty(shape, dtype, like, stream, ld=None):
