@@ -1020,10 +1020,15 @@ cudaError_t prepare_fp8_moe() {
 void shape_fp8_moe(MoeParams* p, int sm_count) {
   const int64_t units = (int64_t)p->active_max * ((p->inner + 127) / 128) * ((p->hidden + 127) / 128);
   p->down_grid = (int)std::min<int64_t>(sm_count, units);
-  // Few units per CTA: half the shared memory each, so that the second kernel's ring is filled while the
-  // first runs.  Many: all of it, as the bytes in flight decide (32 tokens, 64 experts of 2048 x 1024: the
-  // second kernel ran at 3.5 TB/s with 4 stages).
-  const bool many = units > 20 * (int64_t)sm_count;
+  // Half the shared memory each, so that the second kernel routes and fills its ring while the first runs, or
+  // all of it for one after the other, whose bytes in flight pay where there are many units per SM, the sooner
+  // the more tokens' inner values a stage holds.  Measured over 90 layers (us beside / after, at units per SM):
+  //   16 columns:  13.5 38.8 / 44.8,  54 83.5 / 87.9,  81 110.8 / 110.9,  162 143 / 145,  216 254 / 244
+  //   32 columns:  13.5 47.5 / 52.0,  54 98.5 / 101.6,  61 105.6 / 106.4,  81 135.9 / 132.2,  108 165.9 / 159.0
+  //   64 columns:  10 53.3 / 57.7,  20 70.8 / 73.4 and 82.5 / 79.3,  27 91.4 / 85.2,  54 145 / 132
+  // The form that this rule takes is at most 5% slower than the other.
+  const int cols = f8::token_cols(*p);
+  const bool many = units > (cols == 16 ? 160 : cols == 32 ? 64 : 24) * (int64_t)sm_count;
   const size_t most = many ? f8::kMaxSmem : f8::kHalfSmem;
   // Twice as many choices as experts: few experts stay without a token, so their weights are sent for
   // before the routing is known.

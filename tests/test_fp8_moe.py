@@ -147,6 +147,48 @@ def test_each_scale_may_be_extreme(T, E, k, H, I):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("T,E,k,H,I", [(16, 256, 16, 2048, 784), (20, 100, 8, 2048, 784), (40, 40, 4, 2048, 784),   # one kernel after the other
+                                       (16, 128, 16, 2048, 784), (20, 60, 8, 2048, 784), (40, 24, 4, 2048, 784)])  # beside each other
+def test_both_launch_forms(T, E, k, H, I):
+    """Layers with many weights per SM, in which the kernels run one after the other, and with fewer."""
+    import torch
+    g = torch.Generator(device="cuda").manual_seed(E)
+
+    def stack(rows, cols):
+        codes = torch.randint(0x18, 0x58, (E, rows, cols), generator=g, device="cuda", dtype=torch.uint8)  # 2^-4 .. 15
+        codes |= torch.randint(0, 2, (E, rows, cols), generator=g, device="cuda", dtype=torch.uint8) << 7
+        return codes.view(torch.float8_e4m3fn), (torch.rand(E, -(-rows // 128), -(-cols // 128), generator=g, device="cuda") + 0.5) * (0.25 / cols ** 0.5)
+
+    def real(w, e):
+        return w[0][e].double() * w[1][e].double().repeat_interleave(128, 0)[: w[0].shape[1]].repeat_interleave(128, 1)[:, : w[0].shape[2]]
+    x = sg.quantize_fp8(torch.randn(T, H, generator=g, device="cuda"))
+    xr = x.data.double() * x.scale.double().repeat_interleave(128, 1)
+    logits = torch.randn(T, E, generator=g, device="cuda")
+    ws = [stack(I, H), stack(I, H), stack(H, I)]
+    got = sg.moe_fp8(x, logits, k, *ws, out_dtype=torch.float32)
+    assert torch.equal(sg.moe_fp8(x, logits, k, *ws, out_dtype=torch.float32), got)
+    assert sg.sgemm_sync_status(torch.cuda.current_stream()) == 0
+    p, at = logits.double().softmax(1).topk(k, 1)
+    p /= p.sum(1, keepdim=True)
+    y, tol = torch.zeros(2, T, H, dtype=torch.float64, device="cuda")
+    for e in range(E):
+        t, j = (at == e).nonzero(as_tuple=True)
+        if not t.numel():
+            continue
+        w1, w3, w2 = (real(w, e) for w in ws)
+        gate, up, mg, mu = xr[t] @ w1.T, xr[t] @ w3.T, xr[t].abs() @ w1.abs().T, xr[t].abs() @ w3.abs().T
+        s = torch.sigmoid(gate)
+        h = gate * s * up
+        big = torch.nn.functional.pad(h.abs(), (0, -I % 64)).view(len(t), -1, 64).amax(2).repeat_interleave(64, 1)[:, :I]
+        dh = (H + 4) * U * (1.1 * mg * up.abs() + (gate * s).abs() * mu) + 8 * U * h.abs() + 2.0 ** -9.8 * big * (1 + 2.0 ** -6)
+        c = p[t, j][:, None]
+        y[t] += c * (h @ w2.T)
+        tol[t] += c * ((dh + (2 * I + E + 8) * U * h.abs()) @ w2.abs().T)
+    err = (got.double() - y).abs()
+    assert bool((err <= tol + U * y.abs()).all()), float((err / tol).max())
+
+
+@pytest.mark.gpu
 def test_every_token_to_one_expert():
     """All tokens on the same experts (a full tile of columns), and each token on an expert of its own."""
     def same(lg):
