@@ -164,7 +164,6 @@ struct MoeParams {
   int* arrived = nullptr;                 // [ceil(hidden / 128)] CTAs whose sums are in `part`
   float* part = nullptr;                  // [2 * down_grid][tokens][128]
   int many = 0;                           // 1: many units per CTA: the kernels run one after the other
-  int dense = 0;                          // 1: nearly every expert will have a token
   int* route = nullptr;                   // the routing, left by the first kernel where `many`
   int active_max = 0, slots_max = 0;      // bounds of the routing arrays
   Guard guard;

@@ -53,7 +53,6 @@ constexpr float kLoScale = 16.0f;
 constexpr int kPitch = 129;
 constexpr int kChunkGroups = 8;   // groups of 128 k whose scales are loaded together
 constexpr int kChunks = 3;        // in shared memory
-constexpr int kPrefetch = 16;     // weight tiles a CTA sends for before it knows the routing, at most (40 MB in all)
 
 __device__ __forceinline__ void fold_barrier() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
@@ -300,13 +299,6 @@ __device__ __forceinline__ int64_t expert_scales(int experts, int64_t stride, in
   return (experts - 1) * stride + extent((rows + 127) / 128, ld, groups);
 }
 
-// A box of a tensor map into L2.
-__device__ __forceinline__ void prefetch_box(const CUtensorMap* map, int32_t inner, int32_t outer, int32_t product) {
-  asm volatile("cp.async.bulk.prefetch.tensor.3d.L2.global [%0, {%1, %2, %3}];" ::"l"(reinterpret_cast<uint64_t>(map)),
-               "r"(inner), "r"(outer), "r"(product)
-               : "memory");
-}
-
 // NC: columns of the product, the tokens rounded up to 16, 32 or 64.
 template <int NC>
 __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_constant__ CUtensorMap mapX,
@@ -351,13 +343,6 @@ __global__ void __launch_bounds__(kThreads, 2) moe_up_kernel(const __grid_consta
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), 128);
-  if (warp == 3 && p.dense) {  // the first item's weights if every expert is active, on their way to L2 while the routing runs
-    const int e = (int)blockIdx.x / col_tiles, c0 = ((int)blockIdx.x % col_tiles) * kUpCols;
-    for (int g = lane; e < p.experts && g < min(groups, kPrefetch); g += 32) {
-      prefetch_box(&mapG, g * BK, c0, e);
-      prefetch_box(&mapU, g * BK, c0, e);
-    }
-  }
   // what the stream's kernel before this one wrote; the second kernel may begin once that is there
   // too, as it reads the logits on its own
   asm volatile("griddepcontrol.wait;" ::: "memory");
@@ -639,11 +624,6 @@ __global__ void __launch_bounds__(kThreads, 2) moe_down_kernel(const __grid_cons
     fence_mbar_init();
   }
   if (warp == 1) tmem_alloc(smem_addr(&tmem_slot), kTmemCols);
-  if (warp == 3 && p.dense) {  // as in the first kernel
-    const int64_t all = (int64_t)p.experts * groups, u = all * tiles * blockIdx.x / gridDim.x;
-    for (int64_t v = u + lane; v < min(u + kPrefetch, all * tiles); v += 32)
-      prefetch_box(&mapD, (int)(v % groups) * BK, (int)(v / all) * 128, (int)(v % all / groups));
-  }
   for (int i = (int)threadIdx.x; i < p.tokens * 128; i += kThreads) ysum[i] = 0.0f;
   tmem_fence_before_sync();
   if (p.many) {
@@ -1030,10 +1010,7 @@ void shape_fp8_moe(MoeParams* p, int sm_count) {
   const int cols = f8::token_cols(*p);
   const bool many = units > (cols == 16 ? 160 : cols == 32 ? 64 : 24) * (int64_t)sm_count;
   const size_t most = many ? f8::kMaxSmem : f8::kHalfSmem;
-  // Twice as many choices as experts: few experts stay without a token, so their weights are sent for
-  // before the routing is known.
   p->many = many;
-  p->dense = many && p->slots_max >= 2 * p->experts;
   for (p->up_stages = f8::kMaxStages; p->up_stages > 2 && f8::up_smem(*p) > most;) --p->up_stages;
   for (p->down_stages = f8::kMaxStages; p->down_stages > 2 && f8::down_smem(*p) > most;) --p->down_stages;
 }
