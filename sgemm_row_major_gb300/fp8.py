@@ -102,16 +102,6 @@ def _type(x, name) -> int:
     return t
 
 
-def _check(x, name, dims, dtype):
-    if x.dim() != dims:
-        raise TypeError(f"{name} must have {dims} dimensions")
-    if x.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
-    if x.shape[-1] > 1 and x.stride(-1) != 1:
-        raise TypeError(f"{name}: the last dimension must be contiguous")
-    return x
-
-
 def _rows(x, name):
     """(rows, columns, row stride) of a 2-D tensor with contiguous rows (a single row has no stride of its own)."""
     shape = x.shape
@@ -372,16 +362,24 @@ def rmsnorm_fp8_backward(dy, h, weight, rstd, dh=None, *, stream=None):
     return dx, dw
 
 
+def _stack(x, name, shape, dtype):
+    """(stride between matrices, row stride) of a 3-D tensor of `shape` with contiguous rows."""
+    if len(x.shape) != 3:
+        raise TypeError(f"{name} must have 3 dimensions")
+    if x.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {x.dtype}")
+    if x.shape != shape:
+        raise ValueError(f"{name} must have shape {shape}, got {tuple(x.shape)}")
+    stride, ld, inner = x.stride()
+    if inner != 1 and shape[2] > 1:
+        raise TypeError(f"{name}: the last dimension must be contiguous")
+    return stride, ld
+
+
 def _experts(w, name, experts, rows, cols) -> ExpertsStruct:
     data, scale = w
-    _check(data, name, 3, _T.float8_e4m3fn)
-    _check(scale, name + " scales", 3, _T.float32)
-    if data.shape != (experts, rows, cols):
-        raise ValueError(f"{name} must have shape {(experts, rows, cols)}, got {tuple(data.shape)}")
-    if scale.shape != (experts, -(-rows // 128), -(-cols // 128)):
-        raise ValueError(f"{name} scales must have shape {(experts, -(-rows // 128), -(-cols // 128))}, got {tuple(scale.shape)}")
-    stride, ld, _ = data.stride()
-    sstride, lds, _ = scale.stride()
+    stride, ld = _stack(data, name, (experts, rows, cols), _T.float8_e4m3fn)
+    sstride, lds = _stack(scale, name + " scales", (experts, -(-rows // 128), -(-cols // 128)), _T.float32)
     return ExpertsStruct(data.data_ptr(), ld, stride, scale.data_ptr(), lds or 1, sstride)
 
 

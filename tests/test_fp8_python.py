@@ -119,3 +119,30 @@ def test_a_matrix_follows_its_tensors_memory():
     a.data.data = torch.zeros(4, 256, dtype=torch.uint8, device="cuda").view(torch.float8_e4m3fn)
     with pytest.raises(ValueError):
         sg.matmul_fp8(a, b, transB="T")
+
+
+def test_experts_refusals(on_device_0):
+    """Weights of another shape, type or order than the layer's."""
+    import torch
+    f32, e4 = torch.float32, torch.float8_e4m3fn
+    x = sg.Fp8Matrix(Stand((2, 256), e4), Stand((2, 2), f32))
+
+    def call(error, **kw):
+        w = dict(gate=(Stand((4, 128, 256), e4), Stand((4, 1, 2), f32)), up=(Stand((4, 128, 256), e4), Stand((4, 1, 2), f32)),
+                 down=(Stand((4, 256, 128), e4), Stand((4, 2, 1), f32)))
+        w.update(kw)
+        with pytest.raises(error):
+            sg.moe_fp8(x, Stand((2, 4), f32), 2, w["gate"], w["up"], w["down"])
+
+    class Columns(Stand):
+        def stride(self, i=None):
+            return (self.shape[1] * self.shape[2], 1, self.shape[1])
+    good = Stand((4, 1, 2), f32)
+    call(AssertionError)
+    call(TypeError, up=(Stand((4 * 128, 256), e4), good))
+    call(TypeError, up=(Stand((4, 128, 256), torch.float8_e5m2), good))
+    call(TypeError, up=(Stand((4, 128, 256), e4), Stand((4, 1, 2), torch.bfloat16)))
+    call(TypeError, up=(Columns((4, 128, 256), e4), good))
+    call(ValueError, up=(Stand((4, 256, 256), e4), good))
+    call(ValueError, up=(Stand((4, 128, 256), e4), Stand((4, 2, 2), f32)))
+    call(ValueError, down=(Stand((4, 128, 256), e4), good))
