@@ -69,6 +69,9 @@ typedef struct sgemm_fp8_matrix_t {
  *     not read and may be NULL.  alpha == 0 or K == 0: A and B are not read.
  *   - Errors per element, against the sum taken exactly: at most
  *     (K + 2) 2^-24 (|alpha| sum|a b| + |beta c|), then one rounding to `type`.
+ *     In sum|a b| a subnormal code (below 2^-6 in E4M3, 2^-14 in E5M2, and not
+ *     0) counts as the smallest normal one: the tensor cores align the products
+ *     that they add by the codes' exponents.
  *     NaN codes, E5M2 infinities and non-finite scales give the values the
  *     formula gives.  The two scales of a pair are multiplied first, in FP32:
  *     a product beyond FLT_MAX is +-Inf (0 * Inf = NaN), one below 2^-126 has

@@ -208,6 +208,35 @@ def test_special_values(force, kernel):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("fa", ["e4m3", "e5m2"])
+@pytest.mark.parametrize("fb", ["e4m3", "e5m2"])
+def test_whole_range_of_codes(force, kernel, fa, fb):
+    """Codes of every finite value, and sums in which the product of the largest code with the smallest subnormal one leads.
+    A product of codes m 2^e is aligned by e, and a subnormal code's e is the smallest normal one's, so the bound counts such
+    a code as the smallest normal one (the sums of magnitudes alone were exceeded by a third)."""
+    import torch
+    force(kernel)
+    least, rng = {"e4m3": 2.0 ** -6, "e5m2": 2.0 ** -14}, np.random.default_rng(101)
+    for K, lead, positive in [(K, lead, positive) for K in (2, 3, 4, 8, 16, 40, 128, 300) for lead in (0, 1, 2) for positive in (False, True)]:
+        codes = []
+        for i, fmt in enumerate((fa, fb)):
+            v = code_values(fmt)
+            usable = np.flatnonzero(np.isfinite(v) & ((np.abs(v) < 2.0 ** -3) if lead else True) & (np.signbit(v) <= (not positive)))
+            c = rng.choice(usable, (150, K)).astype(np.uint8)
+            if lead:
+                c[:, 0] = np.nanargmax(np.where(np.isfinite(v), v, np.nan)) if lead == i + 1 else 1  # the largest one, 1: the smallest
+            codes.append(c)
+        ms, vs, ws = [], [], []
+        for c, fmt in zip(codes, (fa, fb)):
+            buf = torch.from_numpy(np.pad(c, ((0, 0), (0, -K % 16)))).cuda()[:, :K]
+            ms.append(sg.Fp8Matrix(buf.view(torch.float8_e4m3fn if fmt == "e4m3" else torch.float8_e5m2), torch.ones(150, -(-K // 128), device="cuda")))
+            vs.append(code_values(fmt)[c])
+            ws.append(np.where(vs[-1] == 0, 0.0, np.maximum(np.abs(vs[-1]), least[fmt])))
+        check(sg.matmul_fp8(*ms, transB="T"), vs[0] @ vs[1].T, ws[0] @ ws[1].T, K, what=(K, lead, positive))
+
+
+@pytest.mark.gpu
 def test_wide_range_of_scales():
     """Scales from the smallest to large ones: products of two scales that FP32 holds."""
     import torch
