@@ -174,10 +174,12 @@ typedef struct sgemm_fp8_experts_t {
  *     hidden per expert; down (W2): hidden x inner per expert.
  *   - The weights of the experts that some token chose are read once.  The
  *     products' sums are FP32; the inner values are kept as two 8-bit terms
- *     with a common scale (relative to a group's largest value at most 2^-9.8
- *     off, about as far as BF16).
+ *     with a common scale (relative to the largest of 64 at most 2^-9.8 off,
+ *     about as far as BF16) whatever `type` is.  The codes have no infinity:
+ *     an inner value beyond FP32 counts as NaN.
  *   - An expert whose logit is -Inf is not chosen; a row whose logits are all
- *     -Inf gives zeros.  A row with a NaN or +Inf logit gives NaNs.
+ *     -Inf gives zeros.  A row with a NaN or +Inf logit gives NaNs.  top_k == 0
+ *     or inner == 0: zeros, and nothing is read.
  *   - tokens <= 64, experts <= 1024, top_k <= 16, hidden and inner multiples of 16
  *     (SGEMM_ERR_UNSUPPORTED otherwise; top_k <= experts, else -5).
  * Arguments: 1 tokens, 2 hidden, 3 inner, 4 experts, 5 top_k, 6 X, 7 logits,

@@ -20,20 +20,24 @@
 // moe_down_kernel shares the (128 rows of the hidden side, expert, 128 inner columns) units evenly, in
 // that order; a CTA folds its units per expert in FP32 registers and adds them weighted into its tokens'
 // sums in shared memory.  Rows of one CTA go to Y; the others' sums go to slots of the workspace, and the
-// last CTA of such rows to arrive adds them in CTA order (which CTA that is does not matter).  A CTA of
-// each kernel fits on an SM beside one of the other, and the second kernel is launched when the first
-// has begun: it routes and fills its ring with W2 meanwhile, and waits for the first kernel only
-// before it loads h (one token: its 17 MB of W2 are then nearly all on chip).
+// last CTA of such rows to arrive adds them in CTA order (which CTA that is does not matter).  Unless there
+// are many units per SM (shape_fp8_moe) a CTA of each kernel fits on an SM beside one of the other, and the
+// second kernel is launched when the first has begun: it routes and fills its ring with W2 meanwhile, and
+// waits for the first kernel only before it loads h (one token: 12 of its 17 MB of W2 are then on chip).
 //
-// Both: one CTA per SM with as many 16 KB weight tiles in flight as half its shared memory holds; warp 0
-// loads (TMA), warp 1 issues the products, warp 2 loads scales a chunk of groups ahead, warps 4-7 fold
-// the accumulators (several alternate) into FP32 sums in registers.
+// Both: one CTA per SM with as many 16 KB weight tiles in flight as half its shared memory holds (all of it,
+// where the kernels run one after the other); warp 0 loads (TMA), warp 1 issues the products, warp 2 loads
+// scales a chunk of groups ahead, warps 4-7 fold the accumulators (several alternate) into FP32 sums in
+// registers.
 //
-// What bounds it: the weights' bytes.  32 tokens, 64 experts of 2048 x 1024, 8 each (397 MB): 100 us,
-// 4.0 TB/s; the routing and the first loads take 6 us, the first kernel's last round of tiles is part empty,
-// and while one kernel runs out the other has half of an SM's shared memory.  One token (50 MB): 26 us,
-// of which the launch, the routing, the two streams of about 4 us each, the wait between the kernels
-// and the last sums follow one another.
+// What bounds it: up to 32 tokens the fold and the weights' bytes about equally, beyond that the fold.
+// 32 tokens, 64 experts of 2048 x 1024, 8 each (397 MB): 98.6 us, 4.0 TB/s.  While it runs, the first kernel
+// takes 820 cycles for a tile of 16 KB (5.8 TB/s at 1.9 GHz), of which the issuer waits 230 for an
+// accumulator and 240 for operands; about 20 us are the routing, the first loads, the first kernel's part
+// empty last round of tiles and the second's start and joining.  64 tokens: 132 us, 1050 cycles, 480 of them
+// for an accumulator and 190 for operands.  One token (50 MB): 26 us, of which the launch, the routing, the
+// first kernel's stream (9 us from its first wait to its last product), the wait between the kernels, the
+// second stream and the last sums follow one another.
 #include <algorithm>
 
 #include "fp8_gemm.cuh"

@@ -5,8 +5,9 @@
 // chunks of h in registers between the sum and the output, so x and r are read once and h and the
 // codes written once (an HBM stream: 7 bytes per element of a BF16 row with a residual).  16
 // neighbouring threads hold one group of 128 columns, so a group's largest value is a shuffle away.
-// BF16 16384 x 4096 with a residual: 79 us, 6.0 TB/s of 6.8 measured for a copy (FP32 8192 x 4096 0.97 of
-// it); one row of 4096: 3.2 us, which is a launch and one memory latency.
+// BF16 16384 x 4096 with a residual: 80 us, 5.9 TB/s of 6.8 measured for a copy (FP32 8192 x 4096 68 us,
+// 6.4 TB/s); one row of 4096: 3.1 us, which is a launch and one memory latency.  Rows that begin anywhere
+// take more instructions per byte (fp8_common.cuh, Loading): 8192 x 4095 BF16 66 us, 3.6 TB/s, FP32 112 us.
 //
 // Backward:   dx = rstd (dy w - h rstd^2 mean(dy w h)) + dh,   dw = sum_rows dy h rstd.
 // A persistent grid: a CTA takes rows blockIdx.x, blockIdx.x + gridDim.x, ..., its threads own
@@ -14,8 +15,8 @@
 // costs no traffic per row; the CTAs' sums go to `partial` and a second kernel adds them in CTA
 // order.  Rows that begin at multiples of 16 bytes are copied to a ring in shared memory by bulk copies
 // several rows ahead (192 KB in flight per SM), others are loaded one row ahead into registers.
-// BF16 8192 x 4096 with dh: 49 us, 5.5 TB/s (62 us with loads one row ahead); the second kernel and the
-// first rows' latency are about 5 us of it.
+// BF16 8192 x 4096 with dh: 50 us, 5.4 TB/s (62 us with loads one row ahead); the second kernel and the
+// first rows' latency are about 5 us of it.  8192 x 4095, one row ahead: BF16 89 us, FP32 119 us.
 #include <algorithm>
 
 #include "fp8_common.cuh"

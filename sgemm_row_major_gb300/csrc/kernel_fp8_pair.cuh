@@ -15,8 +15,9 @@
 // same time.  A group takes 740 cycles all the same (1080 with a scale per column): with two accumulators
 // in the TMEM the chain of handing one over (the commit's arrival, the folders' first load, the last load,
 // the arrival at the issuer) is longer than the other's products.  Without the fold it would be 540.
-// Measured: 8192^3 with BF16 output 390 us, 2.8 PFLOP/s; 4096^3 63 us; the gradient 4096 x 4096 x 8192 of
-// both operands with column groups, added to FP32, 171 us.  Narrower tiles need 325 ns (128) and 295 ns
+// Measured: 8192^3 with BF16 output 390 us, 2.8 PFLOP/s, in a short run and 444 us in a long one (the power
+// limit); 4096^3 62 us; the gradient 4096 x 4096 x 8192 of both operands with column groups, added to FP32,
+// 173 us.  Narrower tiles need 325 ns (128) and 295 ns
 // (64) for a group of a half and a quarter of the products, and pay where the last round of 256-wide tiles
 // would be far from full.
 //

@@ -8,8 +8,8 @@
 // registers, find the groups' largest values -- across the lanes of a row (1 x 128), down the
 // thread's own columns and then across the warps through shared memory (128 x 1, 128 x 128) -- and
 // write the codes of their own elements.  So X is read once and the pass is an HBM stream: FP32 4096 x
-// 4096 in 128 x 128 groups 16.0 us (5.2 TB/s of 6.8 measured for a copy), BF16 16384 x 4096 in 128 x 1
-// groups 37 us (5.5 TB/s), FP32 8192 x 4096 28 us (5.9 TB/s); what is missing is the start and the end,
+// 4096 in 128 x 128 groups 15.4 us (5.5 TB/s of 6.8 measured for a copy), BF16 16384 x 4096 in 128 x 1
+// or 1 x 128 groups 38 us (5.3 TB/s), FP32 8192 x 4096 28 us (5.9 TB/s); what is missing is the start and the end,
 // when not all SMs load.  Rows that do not begin at multiples of 16 bytes: BF16 8192 x 4095 26 to 32 us.
 #include "fp8_common.cuh"
 #include "fp8_internal.h"

@@ -17,7 +17,7 @@
 //
 // What bounds it: a stream of the long operand, but a CTA starts, folds and joins in 4 us and takes 310 ns
 // (16 columns) to 545 ns (128) for a group, where its 16 KB are 370 ns of an SM's share of the memory's
-// bandwidth: 1 x 4096 x 4096 (17 MB) 6.2 us, 64 x 4096 x 16384 (68 MB) 19.3 us, 3.6 TB/s.  More shares
+// bandwidth: 1 x 4096 x 4096 (17 MB) 7.0 us, 64 x 4096 x 16384 (68 MB) 19.1 us, 3.6 TB/s.  More shares
 // shorten the groups' part and lengthen the joining.
 #include "fp8_gemm.cuh"
 

@@ -201,7 +201,8 @@ def _new_matrix(rows, cols, block, fmt, like, stream):
 def quantize_fp8(x, block=ROW, format="e4m3", stream=None) -> Fp8Matrix:
     """Codes and scales of a 2-D float32 or bfloat16 tensor in groups of `block` elements: (1, 128), (128, 1) or
     (128, 128).  For each group the scale is max(amax / top, 2**-126) and the code of x is x * (1 / scale) rounded
-    to nearest even (sgemm_fp8_quantize)."""
+    to nearest even (sgemm_fp8_quantize).  Rows of the codes start at multiples of 16 elements: where the width is not one,
+    ``data`` is not contiguous."""
     lib = _lib()
     rows, cols, ldx = _rows(x, "x")
     fmt = FORMATS.get(format)
@@ -309,7 +310,8 @@ def rmsnorm_fp8(x, weight, eps=1e-6, residual=None, *, codes=True, y=False, stre
     (sgemm_fp8_rmsnorm).
 
     Returns (q, h, y, rstd): `q` the E4M3 codes and scales of y in groups of (1, 128) (None with codes=False), `h` the sum
-    (x itself without a residual), `y` in x's type when y=True (else None), `rstd` float32 of one value per row."""
+    (x itself without a residual), `y` in x's type when y=True (else None), `rstd` float32 of one value per row.  Where the
+    width is no multiple of 8, `h` and `y` are not contiguous (their rows start at multiples of 8 elements)."""
     lib = _lib()
     t = _type(x, "x")
     rows, cols, ldx = _rows(x, "x")
@@ -336,7 +338,8 @@ def rmsnorm_fp8(x, weight, eps=1e-6, residual=None, *, codes=True, y=False, stre
 
 def rmsnorm_fp8_backward(dy, h, weight, rstd, dh=None, *, stream=None):
     """(dx, dweight) of rmsnorm_fp8: `dy` the gradient of y, `h` and `rstd` as the forward pass returned them, `dh` the
-    gradient that reaches h past the norm.  dx is the gradient of x and of the residual; dweight is float32."""
+    gradient that reaches h past the norm.  dx is the gradient of x and of the residual, not contiguous where the width is no
+    multiple of 8; dweight is float32."""
     lib = _lib()
     t = _type(dy, "dy")
     rows, cols, lddy = _rows(dy, "dy")
