@@ -175,10 +175,9 @@ class Fp8Matrix:
     def _c(self):
         """The C structure; made again where a tensor's memory is no longer the one it was made for."""
         if (self._data.data_ptr(), self._scale.data_ptr()) != self._at:
-            shape = self._shape
+            if self._data.shape != self._shape:
+                raise ValueError(f"data had shape {tuple(self._shape)}, has {tuple(self._data.shape)}")
             self.__init__(self._data, self._scale, self._block)
-            if self._shape != shape:
-                raise ValueError(f"data had shape {tuple(shape)}, has {tuple(self._shape)}")
         return self._struct
 
 

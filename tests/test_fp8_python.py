@@ -146,3 +146,16 @@ def test_experts_refusals(on_device_0):
     call(ValueError, up=(Stand((4, 256, 256), e4), good))
     call(ValueError, up=(Stand((4, 128, 256), e4), Stand((4, 2, 2), f32)))
     call(ValueError, down=(Stand((4, 128, 256), e4), good))
+
+
+def test_a_matrix_of_another_shape_stays_refused(on_device_0):
+    """Memory and shape of a matrix's tensor exchanged: every call is refused, not only the first."""
+    import torch
+    a = sg.Fp8Matrix(Stand((8, 256), torch.float8_e4m3fn), Stand((8, 2), torch.float32))
+    b = sg.Fp8Matrix(Stand((16, 256), torch.float8_e4m3fn), Stand((1, 2), torch.float32), (128, 128))
+    a.data.shape, a.data.data_ptr = (8, 128), lambda: 1 << 21
+    a.scale.shape = (8, 1)
+    for _ in range(2):
+        with pytest.raises(ValueError, match="had shape"):
+            sg.matmul_fp8(a, b, transB="T")
+    assert tuple(a.shape) == (8, 256)
