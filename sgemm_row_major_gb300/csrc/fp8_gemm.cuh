@@ -191,7 +191,7 @@ __device__ __forceinline__ void store_one(const Fp8Out& o, int64_t row, int64_t 
 // How the output is written, known where the kernel is chosen (the caller holds 128 sums in registers
 // meanwhile; all cases in one kernel cost 9% at 8192^3).
 enum Output {
-  kOutPlain = 0,  // beta == 0, aligned rows: TMA
+  kOutPlain = 0,  // beta == 0, aligned rows of whole 16 bytes: TMA
   kOutAdd = 1,    // beta != 0, aligned rows
   kOutAny = 2     // any alignment and beta
 };

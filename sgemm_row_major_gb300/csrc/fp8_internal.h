@@ -114,8 +114,8 @@ struct Fp8PairParams {
 constexpr int kFp8PairStages = 5, kFp8PairThreads = 384;
 int64_t fp8_pair_smem(bool cols);  // dynamic shared memory; cols: B has a scale per column
 constexpr int kFp8PairTiles[] = {256, 128, 64};  // the tile widths there are kernels for
-// One translation unit per form of the output: beta == 0 and aligned rows, beta != 0 and aligned
-// rows, anything.
+// One translation unit per form of the output: beta == 0 and aligned rows of whole 16 bytes, beta != 0 and
+// aligned rows, anything.
 #define SGEMM_DECLARE_FP8_PAIR(name)                                                               \
   cudaError_t prepare_fp8_pair_##name();                                                           \
   cudaError_t launch_fp8_pair_##name(int tile_n, const CUtensorMap& mapA, const CUtensorMap& mapB, \
@@ -182,8 +182,8 @@ cudaError_t launch_fp8_moe(const MoeMaps& maps, const MoeParams& p, int sm_count
 // codes x box_outer rows, 128-byte swizzle, zeros outside.
 cudaError_t encode_fp8_map(const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer,
                            CUtensorMap* map);
-// Map over D (`rows` x `cols` FP32 or BF16, row stride ld elements, 16-byte aligned rows): boxes of 32 x 32,
-// swizzled by their rows' width.
+// Map over D (`rows` x `cols` FP32 or BF16, row stride ld elements, 16-byte aligned rows of whole 16 bytes, as
+// TMA writes the rest of a unit too): boxes of 32 x 32, swizzled by their rows' width.
 cudaError_t encode_out_map(const void* base, int64_t cols, int64_t rows, int64_t ld, bool bf16, CUtensorMap* map);
 // The same as encode_fp8_map over `products` such matrices `stride` bytes apart (a multiple of 16).
 cudaError_t encode_fp8_maps(const void* base, int64_t inner, int64_t outer, int64_t ld, int64_t products,

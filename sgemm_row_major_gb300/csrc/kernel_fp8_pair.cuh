@@ -86,7 +86,8 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
 // One warp's 32 rows x 2N columns of D, from a row's sums in each lane, to global memory by TMA: 32
 // columns at a time in D's type, rows of 64 (BF16) or 128 bytes with the swizzle of that width, so that
 // the lanes' 16-byte stores to shared memory hit different banks.  Two BF16 pieces or one of FP32 fit
-// in the warp's buffer; a piece is written when the copy that read its place before is done reading.
+// in the warp's buffer; a piece is written when the copy that read its place before is done reading.  (Columns
+// past D's, which TMA leaves out, begin at a multiple of 16 bytes: it writes whole units.)
 // FRAGMENTS: a lane holds pairs of columns of 4 rows instead (tmem_ld_fragments).
 template <bool BF16, bool FRAGMENTS, int N>
 __device__ __forceinline__ void tma_out(const CUtensorMap& map, uint8_t* buf, const Fp8Out& o, int row0, int col0,

@@ -1,4 +1,4 @@
-// kernel_fp8_pair_plain.cu -- the CTA-pair 8-bit product, output form: beta == 0, aligned rows.
+// kernel_fp8_pair_plain.cu -- the CTA-pair 8-bit product, output form: beta == 0, aligned rows of whole 16 bytes.
 #include "kernel_fp8_pair.cuh"
 
 namespace sgemm_impl {

@@ -171,6 +171,31 @@ def test_alpha_beta_types_and_strides(force, kernel, bf16, ldc_pad):
 
 
 @pytest.mark.gpu
+@pytest.mark.parametrize("kernel,tile", [("FP8_PAIR", 64), ("FP8_PAIR", 128), ("FP8_PAIR", 256), ("FP8_SHORT", 0)])
+@pytest.mark.parametrize("bf16", [False, True])
+@pytest.mark.parametrize("gb", [1, 128])
+def test_nothing_is_written_beside_d(force, kernel, tile, bf16, gb):
+    """D as columns of a wider matrix whose rows are aligned, at every width modulo 16 bytes: its neighbours on both sides,
+    and what lies behind the last row, keep their values."""
+    import torch
+    force(kernel, tile)
+    t = torch.bfloat16 if bf16 else torch.float32
+    for M, N in [(150, n) for n in (1, 2, 3, 5, 6, 7, 31, 33, 100, 129, 255, 257, 300, 514, 515, 516, 517, 518, 519)] + [(1, 130), (700, 61)]:
+        K = 160
+        a, b = operands("NT", M, N, K, 1, gb, "e4m3", "e4m3", N)
+        ref, mag, _ = reference("NT", a, b)
+        ld = -(-N // 8) * 8 + 16
+        big = torch.full((M + 1, ld), 7.0, dtype=t, device="cuda")
+        d = big[:M, 8:8 + N]
+        for beta in (0.0, 1.0):
+            big[:M, 8:8 + N] = 3.0
+            c = d if beta else None
+            got = sg.matmul_fp8(a, b, c, "N", "T", 1.0, beta, out=d)
+            check(got, ref + 3.0 * beta, mag + 3.0 * beta, K, bf16, what=(M, N, beta))
+            assert bool((big[:M, :8] == 7.0).all()) and bool((big[:M, 8 + N:] == 7.0).all()) and bool((big[M] == 7.0).all()), (M, N, beta)
+
+
+@pytest.mark.gpu
 @pytest.mark.parametrize("ops", OPS)
 @pytest.mark.parametrize("pad,offset", [((16, 32), 0), ((0, 0), 0), ((3, 5), 0), ((16, 16), 1)])
 def test_alignment(ops, pad, offset):
