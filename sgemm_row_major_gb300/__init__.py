@@ -430,3 +430,9 @@ from .fp8 import (Fp8Matrix, matmul_fp8, moe_fp8, quantize_fp8, rmsnorm_fp8, rms
 
 __all__ += ["Fp8Matrix", "matmul_fp8", "moe_fp8", "quantize_fp8", "rmsnorm_fp8", "rmsnorm_fp8_backward", "sgemm_fp8_plan",
             "sgemm_fp8_set_override"]
+
+from .linear import (gated_bf16, gated_bf16_backward, linear_bf16, linear_bf16_backward, sgemm_linear_plan,  # noqa: E402
+                     sgemm_linear_set_override)
+
+__all__ += ["gated_bf16", "gated_bf16_backward", "linear_bf16", "linear_bf16_backward", "sgemm_linear_plan",
+            "sgemm_linear_set_override"]

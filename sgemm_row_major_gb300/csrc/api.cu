@@ -13,6 +13,7 @@
 #include <mutex>
 
 #include "fp8_internal.h"
+#include "linear_internal.h"
 #include "kernel_small.h"
 #include "kernel_tma.cuh"
 #include "sgemm.h"
@@ -64,11 +65,20 @@ struct DeviceState {
   std::mutex init_mutex;
   std::atomic<bool> ready{false};  // set once the set-up below has succeeded (a failed one is retried)
   std::atomic<bool> fp8_ready{false};  // the same of the 8-bit kernels', which their first call makes
+  std::atomic<bool> linear_ready{false};  // and of the BF16 layers' kernels
   int sm_count = 0;
   int pair_clusters = 0;  // co-resident clusters of the CTA-pair kernel; 0: pairs cannot run here
   unsigned* fault = nullptr;
   unsigned long long* bounds = nullptr;  // debug build: first bounds violation
   cudaMemPool_t pool = nullptr;
+
+  void describe(CallDevice* out) const {
+    out->sm_count = sm_count;
+    out->pair_clusters = pair_clusters;
+    out->fault = fault;
+    out->bounds = bounds;
+    out->pool = pool;
+  }
 };
 DeviceState g_devices[kMaxDevices];
 
@@ -890,11 +900,25 @@ int sgemm_impl::call_device(CallDevice* out) {
       st->fp8_ready.store(true, std::memory_order_release);
     }
   }
-  out->sm_count = st->sm_count;
-  out->pair_clusters = st->pair_clusters;
-  out->fault = st->fault;
-  out->bounds = st->bounds;
-  out->pool = st->pool;
+  st->describe(out);
+  return SGEMM_OK;
+}
+
+int sgemm_impl::linear_device(CallDevice* out) {
+  int dev;
+  DeviceState* st;
+  const int s = device_state(&dev, &st);
+  if (s != SGEMM_OK) return s;
+  if (!st->linear_ready.load(std::memory_order_acquire)) {
+    std::lock_guard<std::mutex> lock(st->init_mutex);
+    if (!st->linear_ready.load(std::memory_order_relaxed)) {
+      cudaError_t err = prepare_linear_pair();
+      if (err == cudaSuccess) err = prepare_linear_short();
+      if (err != cudaSuccess) return cuda_fail(err);
+      st->linear_ready.store(true, std::memory_order_release);
+    }
+  }
+  st->describe(out);
   return SGEMM_OK;
 }
 

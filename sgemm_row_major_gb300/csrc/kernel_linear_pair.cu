@@ -1,0 +1,590 @@
+// kernel_linear_pair.cu -- products of BF16 matrices on CTA pairs for sm_103a, with what a layer does to the sums.
+//
+//     linear:        Y = act(X W^T + bias) + R          gated:  H = act(X G^T) * (X U^T)
+//     gradients:     D = A0 B0 (+ A1 B1)                two products that share B: D0 = A0 B, D1 = A1 B
+//
+// Clusters of two CTAs on one TPC compute 256 x TN tiles (TN 64, 128 or 256) with tcgen05.mma.cta_group::2.kind::f16,
+// M = 256, N = TN, K = 16, both operands from shared memory: each CTA holds 128 rows of A and half of the tile's columns of
+// B.  A gated tile has TN / 2 columns of each product: the even CTA's half of B is gate's rows, the odd one's up's, so every
+// thread that reads the accumulator finds both products of an element in its own lane.  Sums of 512 k (kFold) leave the
+// tensor memory for FP32 registers, as the tensor cores' own accumulation drifts; the last ones are added back there, and the
+// epilogue runs over the accumulator 32 columns at a time while the next tile's products fill the other one.
+//
+// Either operand may be stored along K or across it: the tensor core reads both orders, so a gradient's product takes the
+// weights and activations as the forward pass left them.
+//
+// Warp 0 loads (TMA, 5 stages of 32 KB), warp 1 of the even CTA issues the products, warps 4-11 fold and write.  Persistent
+// clusters take tiles round robin in an order that keeps 8 rows of tiles together (their A and B panels stay in L2).
+#include "linear_common.cuh"
+
+namespace sgemm_impl {
+namespace lin {
+namespace {
+
+using namespace tc;
+
+constexpr int BM = 256, BMC = 128, BK = 64;
+constexpr int kPart = 128 * BK * 2;       // 16 KB: one operand's tile in one CTA
+constexpr int kStageBytes = 2 * kPart;
+constexpr int kStages = kLinearPairStages;
+constexpr int kOutBytes = 8 * 1024;       // of shared memory per folding warp: 4 pieces of 32 x 32 BF16, or 2 of FP32
+constexpr int kFirstFold = 4;             // warps 0 and 1: loads, products
+constexpr int kFoldWarps = 8;
+constexpr int kThreads = 32 * (kFirstFold + kFoldWarps);
+static_assert(kThreads == kLinearPairThreads, "the plan's figure");
+// 384 threads are launched with 168 registers each; the four warps that move data give most of theirs to the folders:
+// 128 x 40 + 256 x 232 = 384 x 168.
+constexpr int kMoverRegs = 40, kFoldRegs = 232;
+static_assert(128 * kMoverRegs + 32 * kFoldWarps * kFoldRegs <= kThreads * 168, "registers at launch");
+constexpr int kMaxBufs = 4;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kSmem = kStages * kStageBytes + kFoldWarps * kOutBytes + 1024;
+static_assert(kSmem + 1024 + 256 <= 232448, "shared memory per CTA");
+
+__device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster, int32_t inner, int32_t outer) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cluster), "r"(inner), "r"(outer), "r"(0)
+      : "memory");
+}
+
+// 128 (64, 32) output rows of an operand from row mn0 on and 64 k from k0 on.
+__device__ __forceinline__ void load_part(uint32_t dst, const CUtensorMap* map, uint32_t bar, bool mn_major, int mn0, int k0, int rows) {
+  if (mn_major) {
+    tma_load_pair(dst, map, bar, mn0, k0);
+    if (rows > 64) tma_load_pair(dst + kBlockBytes, map, bar, mn0 + 64, k0);
+  } else {
+    tma_load_pair(dst, map, bar, k0, mn0);
+  }
+}
+// Bytes that it loads.
+__host__ __device__ constexpr uint32_t part_bytes(bool mn_major, int rows) {
+  return mn_major ? (rows > 64 ? 2u : 1u) * kBlockBytes : (uint32_t)rows * BK * 2;
+}
+
+// A folding warp's pieces of an output, 32 rows x 32 columns each: written to shared memory in the output's type, in rows of
+// 64 (BF16) or 128 bytes with the swizzle of that width, then by TMA, or by the lanes where TMA cannot (rows that are not
+// aligned or end inside 16 bytes).
+struct Pieces {
+  uint8_t* buf;
+  int at;     // the next piece's place
+  bool wide;  // places of 4 KB (an FP32 output), else of 2 KB
+  __device__ __forceinline__ uint8_t* next() {
+    uint8_t* p = buf + at * (wide ? 4096 : 2048);
+    at = (at + 1) & (wide ? 1 : 3);
+    // the copy that read this place before is done reading
+    if ((threadIdx.x & 31) == 0) {
+      if (wide) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
+      else      asm volatile("cp.async.bulk.wait_group.read 3;" ::: "memory");
+    }
+    __syncwarp();
+    return p;
+  }
+};
+
+template <bool F32>
+__device__ __forceinline__ void emit(Pieces& pieces, const CUtensorMap* map, bool tma, void* base, int64_t ld, const LinearOut& o,
+                                     unsigned site, int row0, int col0, const float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+  uint8_t* at = pieces.next();
+  if constexpr (F32) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      *reinterpret_cast<float4*>(at + lane * 128 + 16 * (e ^ (lane & 7))) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<uint4*>(at + lane * 64 + 16 * (e ^ ((lane >> 1) & 3))) =
+          make_uint4(pack2(v[8 * e], v[8 * e + 1]), pack2(v[8 * e + 2], v[8 * e + 3]), pack2(v[8 * e + 4], v[8 * e + 5]),
+                     pack2(v[8 * e + 6], v[8 * e + 7]));
+  }
+  if (tma) {
+    fence_proxy_async_smem();
+    __syncwarp();
+    if (lane == 0) {
+      if (row0 < o.M && col0 < o.N)
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
+                         reinterpret_cast<uint64_t>(map)),
+                     "r"(smem_addr(at)), "r"(col0), "r"(row0), "r"(0)
+                     : "memory");
+    }
+  } else {
+    __syncwarp();
+    const int rows = min(32, o.M - row0);
+    if (col0 + lane < o.N && rows > 0 &&
+        in_range(o.guard.fault, o.guard.word, site, (int64_t)row0 * ld + col0 + lane, (rows - 1) * ld + 1, extent(o.M, ld, o.N))) {
+      const int64_t first = (int64_t)row0 * ld + col0 + lane;
+      if constexpr (F32) {
+        float* d = static_cast<float*>(base) + first;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r, d += ld) *d = *reinterpret_cast<const float*>(at + r * 128 + 16 * ((lane >> 2) ^ (r & 7)) + 4 * (lane & 3));
+      } else {
+        uint16_t* d = static_cast<uint16_t*>(base) + first;
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r, d += ld)
+          *d = *reinterpret_cast<const uint16_t*>(at + r * 64 + 16 * ((lane >> 3) ^ ((r >> 1) & 3)) + 2 * (lane & 7));
+      }
+    }
+  }
+  // (a group without a copy where TMA wrote nothing: places and groups advance together)
+  if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  __syncwarp();
+}
+
+// bias[col0 ..] is added to 32 sums.
+__device__ __forceinline__ void add_bias(const LinearOut& o, int col0, float (&v)[32]) {
+  const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(o.bias);
+  if (o.bias_vec && col0 + 32 <= o.N) {
+    if (!in_range(o.guard.fault, o.guard.word, f8::kSiteIn, col0, 32, o.N)) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      Chunk<__nv_bfloat16> c;
+      float x[8];
+      c.raw = __ldg(reinterpret_cast<const uint4*>(b + col0) + e);
+      c.get(x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[8 * e + k] += x[k];
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 32; ++e)
+    if (col0 + e < o.N) v[e] += __bfloat162float(get_at(o.guard, f8::kSiteIn, b, col0 + e, o.N));
+}
+
+// The residual's 32 values of one row, sent for before the sums are waited for.
+template <bool VEC>
+struct Residual {
+  f8::Loading<__nv_bfloat16, VEC> c[4];
+  __device__ __forceinline__ void load(const LinearOut& o, int row, int col0) {
+    const f8::Rows<__nv_bfloat16> m(o.residual, o.M, o.ldr, o.N, o.guard);
+    const __nv_bfloat16* p = m.base + (int64_t)row * o.ldr + col0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int n = row < o.M ? max(0, min(8, o.N - col0 - 8 * e)) : 0;
+      c[e].load(p + 8 * e, VEC && n < 8 ? 0 : n, m);
+    }
+  }
+  __device__ __forceinline__ void add(float (&v)[32]) const {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      float x[8];
+      c[e].get().get(x);
+#pragma unroll
+      for (int k = 0; k < 8; ++k) v[8 * e + k] += x[k];
+    }
+  }
+};
+
+// 32 codes of one row.
+__device__ __forceinline__ void put_codes(const LinearOut& o, int which, int row, int col0, const float (&v)[32], float inv) {
+  if (row >= o.M || col0 >= o.N) return;
+  const LinearKept& k = o.kept[which];
+  uint32_t u[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e)
+    u[e] = f8::codes2<true>(v[4 * e] * inv, v[4 * e + 1] * inv, false) | (f8::codes2<true>(v[4 * e + 2] * inv, v[4 * e + 3] * inv, false) << 16);
+  const int n = min(32, o.N - col0);
+  if (!kept_ok(o, which, row, col0, n)) return;
+  uint8_t* d = static_cast<uint8_t*>(k.data) + (int64_t)row * k.ld + col0;
+  if (k.vec && n == 32) {
+    reinterpret_cast<uint4*>(d)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+    reinterpret_cast<uint4*>(d)[1] = make_uint4(u[4], u[5], u[6], u[7]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (e < n) d[e] = (uint8_t)(u[e / 4] >> (8 * (e % 4)));
+  }
+}
+
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+  const float(&a)[16] = *reinterpret_cast<const float(*)[16]>(&v[0]);
+  const float(&b)[16] = *reinterpret_cast<const float(*)[16]>(&v[16]);
+  tmem_st16(taddr, a);
+  tmem_st16(taddr + 16u, b);
+}
+
+// TN: the accumulator's columns.  GATED: half of them are gate's, half up's.
+template <int TN, bool GATED>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
+    linear_pair_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearPairParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  constexpr int halfn = TN / 2;   // columns of B this CTA loads
+  constexpr int TD = GATED ? TN / 2 : TN;  // the tile's columns of D
+  constexpr int bufs = (int)kTmemCols / TN < kMaxBufs ? (int)kTmemCols / TN : kMaxBufs;
+  __shared__ __align__(8) uint64_t full[kStages], done[kStages];
+  __shared__ __align__(8) uint64_t acc_full[bufs], acc_empty[bufs];
+  // a group of 128 columns held by two warps: the second one's largest values, and then both's
+  __shared__ __align__(8) uint64_t max_asked[4], max_told[4];
+  __shared__ float largest[GATED ? 2 : 1][BMC];
+  __shared__ __align__(8) uint64_t fin;
+  __shared__ uint32_t tmem_slot;
+
+  const uint32_t raw_addr = smem_addr(smem_raw);
+  const uint32_t pad = (1024u - (raw_addr & 1023u)) & 1023u;
+  const uint32_t sbase = raw_addr + pad;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_rank();
+  const int cl = (int)cluster_id_x();
+  const int kt = p.k_tiles * p.segments;
+  const int chunks = (kt + kFold - 1) / kFold;
+  const int product_tiles = p.tiles_m * p.tiles_n, tiles = product_tiles * p.products;
+  const int my_tiles = cl < tiles ? (tiles - cl + p.clusters - 1) / p.clusters : 0;
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(smem_addr(&full[s]), 1);
+      mbar_init(smem_addr(&done[s]), 1);
+    }
+    for (int b = 0; b < bufs; ++b) {
+      mbar_init(smem_addr(&acc_full[b]), 1);
+      mbar_init(smem_addr(&acc_empty[b]), 2 * kFoldWarps);
+    }
+    for (int q = 0; q < 4; ++q) {
+      mbar_init(smem_addr(&max_asked[q]), 1);
+      mbar_init(smem_addr(&max_told[q]), 1);
+    }
+    mbar_init(smem_addr(&fin), 1);
+    fence_mbar_init();
+  }
+  if (warp == 1) tmem_alloc_pair(smem_addr(&tmem_slot), kTmemCols);
+  tmem_fence_before_sync();
+  cluster_sync();
+  tmem_fence_after_sync();
+  const uint32_t tmem = tmem_slot;
+  // launched as a programmatic dependent: what the stream's kernel before this one wrote is read, and what it read is
+  // written, only from here on
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (warp < kFirstFold) {
+    f8::fewer_registers<kMoverRegs>();
+    if (warp == 0) {
+      // ------------------------------------------------ loads (each CTA: its rows of A, its columns of B)
+      if (lane == 0) {
+        prefetch_tensormap(&maps.a[0]);
+        prefetch_tensormap(&maps.b[GATED ? rank : 0]);
+      }
+      __syncwarp();
+      const uint32_t bytes = 2u * (part_bytes(p.a_mn, BMC) + part_bytes(p.b_mn, halfn));  // both CTAs'
+      const uint32_t full0 = map_to_rank(smem_addr(&full[0]), 0);
+      int t = 0, s = 0;
+      uint32_t lap = 0;
+      bool ok = true;
+      for (int i = 0; ok && i < my_tiles; ++i) {
+        const int tile = cl + i * p.clusters, product = tile >= product_tiles;
+        int tm, tn;
+        tile_coords(tile - product * product_tiles, p.tiles_m, p.tiles_n, tm, tn);
+        const int m0 = tm * BM + BMC * (int)rank, n0 = GATED ? tn * TD : tn * TN + halfn * (int)rank;
+        for (int g = 0, k = 0, segment = 0; g < kt; ++g, ++t, ++k) {
+          if (k == p.k_tiles) {
+            k = 0;
+            segment = 1;
+          }
+          if (lap > 0 && !poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
+            if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
+            // both CTAs' loads complete on the even CTA's barrier, which expects all their bytes
+            const uint32_t fb = full0 + 8u * (uint32_t)s;
+            if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), bytes);
+            const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
+            load_part(a, &maps.a[segment | product], fb, p.a_mn, m0, k * BK, BMC);
+            load_part(a + kPart, &maps.b[GATED ? (int)rank : segment], fb, p.b_mn, n0, k * BK, halfn);
+          }
+          if (++s == kStages) {
+            s = 0;
+            ++lap;
+          }
+        }
+      }
+      // leave only when every copy into shared memory has landed (the odd CTA's warp 1 waits for the products that read its
+      // last stages)
+      if (rank == 0)
+        for (int u = t > kStages ? t - kStages : 0; u < t; ++u)
+          if (!poll_wait(smem_addr(&full[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns) && lane == 0)
+            atomicOr(p.fault, (unsigned)kFaultDrainWait);
+    } else if (warp == 1) {
+      int t = 0;  // K tiles whose products have been issued (odd CTA: will be)
+      const int units = my_tiles * kt;
+      if (rank != 0) {
+        t = units;
+      } else {
+        // ---------------------------------------------- products (even CTA)
+        const uint32_t astep = step_of(p.a_mn), bstep = step_of(p.b_mn);
+        const uint32_t desc0 = desc_lo(sbase);
+        int s = 0, b = 0, g = 0;
+        uint32_t s_lap = 0, b_lap = 0;
+        bool ok = true;
+        while (ok && t < units) {
+          // a chunk: the K tiles of one accumulator
+          const int n = min(kFold, kt - g);
+          ok = b_lap == 0 || poll_wait(smem_addr(&acc_empty[b]), (b_lap - 1) & 1u, p.timeout_ns);
+          tmem_fence_after_sync();
+          for (int j = 0; ok && j < n; ++j) {
+            ok = poll_wait(smem_addr(&full[s]), s_lap & 1u, p.timeout_ns);
+            if (!ok) break;
+            tmem_fence_after_sync();
+            if (elect_one()) {
+              const uint32_t acc = tmem + (uint32_t)(b * TN);
+              const uint32_t ad = desc0 + (uint32_t)(s * (kStageBytes >> 4)), bd = ad + (kPart >> 4);
+#pragma unroll
+              for (uint32_t ks = 0; ks < BK / 16; ++ks)
+                mma_bf16_pair(acc, make_desc(ad + ks * astep), make_desc(bd + ks * bstep), p.idesc, j == 0 && ks == 0 ? 0u : 1u);
+              mma_commit_pair(smem_addr(&done[s]));  // in both CTAs: stage s is free
+              if (j == n - 1) mma_commit_pair(smem_addr(&acc_full[b]));
+            }
+            __syncwarp();
+            ++t;
+            if (++s == kStages) {
+              s = 0;
+              ++s_lap;
+            }
+          }
+          g = g + n == kt ? 0 : g + n;
+          if (++b == bufs) {
+            b = 0;
+            ++b_lap;
+          }
+        }
+        if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+      }
+      // leave only when every product has completed and its commits have landed in this CTA
+      for (int u = t > kStages ? t - kStages : 0; u < t; ++u)
+        if (!poll_wait(smem_addr(&done[u % kStages]), (uint32_t)(u / kStages) & 1u, p.timeout_ns)) {
+          if (lane == 0) atomicOr(p.fault, (unsigned)kFaultDrainWait);
+          break;
+        }
+    }
+  } else {
+    f8::more_registers<kFoldRegs>();
+    // ------------------------------------------------ folders, then the epilogue (both CTAs)
+    const LinearOut& o = p.out;
+    const int q = warp & 3;                     // TMEM lane quarter this warp may access
+    const int part = (warp - kFirstFold) >> 2;  // which half of the tile's columns
+    constexpr int cols = TD / 2;                // of D, per thread
+    constexpr int loads = TN / 64;              // 32 accumulator columns at a time
+    const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(cols * part);
+    // the accumulator column of load e: gated, the first half of the loads are gate's columns, the others up's
+    const auto column = [](int e) { return GATED && e >= loads / 2 ? TN / 2 + 32 * (e - loads / 2) : 32 * e; };
+    Pieces pieces{smem_raw + pad + kStages * kStageBytes + (warp - kFirstFold) * kOutBytes, 0, o.f32 != 0};
+    float sum[TN / 2];
+    bool ok = true;
+    int b = 0;
+    uint32_t b_lap = 0;
+    for (int i = 0; ok && i < my_tiles; ++i) {
+      const int tile = cl + i * p.clusters, product = tile >= product_tiles;
+      int tm, tn;
+      tile_coords(tile - product * product_tiles, p.tiles_m, p.tiles_n, tm, tn);
+      const int row0 = tm * BM + BMC * (int)rank + 32 * q, row = row0 + lane;
+      const int c0 = tn * TD + cols * part;  // this thread's first column of D
+#pragma unroll
+      for (int e = 0; e < TN / 2; ++e) sum[e] = 0.0f;
+      for (int ch = 0; ch < chunks; ++ch) {
+        ok = poll_wait(smem_addr(&acc_full[b]), b_lap & 1u, p.timeout_ns);
+        if (!ok) {
+          if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+          break;
+        }
+        tmem_fence_after_sync();
+        const uint32_t acc = tq + (uint32_t)(b * TN);
+        const auto release = [&] {  // the accumulator has been read: hand it back to the issuer
+          tmem_fence_before_sync();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_remote(smem_addr(&acc_empty[b]), 0);
+        };
+        if (ch < chunks - 1) {
+#pragma unroll
+          for (int e = 0; e < loads; ++e) {
+            float v[32];
+            tmem_ld32(acc + (uint32_t)column(e), v);
+            tmem_wait_ld();
+            if (e == loads - 1) release();
+            tmem_ld_ready(v);
+#pragma unroll
+            for (int k = 0; k < 32; ++k) sum[32 * e + k] += v[k];
+          }
+        } else {
+          if (chunks > 1) {
+#pragma unroll
+            for (int e = 0; e < loads; ++e) {
+              float v[32];
+              tmem_ld32(acc + (uint32_t)column(e), v);
+              tmem_wait_ld();
+              tmem_ld_ready(v);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) v[k] += sum[32 * e + k];
+              tmem_st32(acc + (uint32_t)column(e), v);
+            }
+            tmem_wait_st();
+          }
+          // -------------------------------------------- epilogue
+          constexpr uint32_t up = TN / 2;  // gated: from a column of gate to up's
+          float scale[2] = {1.0f, 1.0f};
+          if (o.keep == 2) {
+            float m[2] = {0.0f, 0.0f};
+#pragma unroll 1
+            for (int c = 0; c < cols; c += 32) {
+              float v[32];
+              tmem_ld32(acc + (uint32_t)c, v);
+              tmem_wait_ld();
+              tmem_ld_ready(v);
+              if (!GATED && o.bias) add_bias(o, c0 + c, v);
+#pragma unroll
+              for (int k = 0; k < 32; ++k) m[0] = fmaxf(m[0], f8::finite_abs(v[k]));
+              if constexpr (GATED) {
+                tmem_ld32(acc + up + (uint32_t)c, v);
+                tmem_wait_ld();
+                tmem_ld_ready(v);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) m[1] = fmaxf(m[1], f8::finite_abs(v[k]));
+              }
+            }
+            if (cols < 128) {  // the other half of the group is with the warp of the other column half
+              float* at = &largest[0][32 * q + lane];
+              constexpr int kUp = GATED ? BMC : 0;
+              if (part == 1) {
+                at[0] = m[0];
+                if (GATED) at[kUp] = m[1];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&max_asked[q]));
+              }
+              ok = poll_wait(smem_addr(part == 1 ? &max_told[q] : &max_asked[q]), (uint32_t)(i & 1), p.timeout_ns);
+              if (!ok) {
+                if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+                break;
+              }
+              m[0] = fmaxf(m[0], at[0]);
+              if (GATED) m[1] = fmaxf(m[1], at[kUp]);
+              if (part == 0) {
+                at[0] = m[0];
+                if (GATED) at[kUp] = m[1];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&max_told[q]));
+              }
+            }
+#pragma unroll
+            for (int w = 0; w < (GATED ? 2 : 1); ++w) {
+              scale[w] = f8::group_scale(m[w], kMaxE4M3);
+              if (row < o.M && c0 < o.N && c0 % 128 == 0) put_scale(o, w, row, c0 >> 7, scale[w]);
+              scale[w] = __fdiv_rn(1.0f, scale[w]);
+            }
+          }
+#pragma unroll 1
+          for (int c = 0; c < cols; c += 32) {
+            float v[32];
+            tmem_ld32(acc + (uint32_t)c, v);
+            if constexpr (GATED) {
+              float u[32];
+              tmem_ld32(acc + up + (uint32_t)c, u);
+              tmem_wait_ld();
+              if (c + 32 == cols) release();
+              tmem_ld_ready(v);
+              tmem_ld_ready(u);
+              if (o.keep == 1) {
+                emit<false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, f8::kSiteCodes, row0, c0 + c, v);
+                emit<false>(pieces, &maps.kept[1], o.kept[1].vec, o.kept[1].data, o.kept[1].ld, o, f8::kSiteCodes, row0, c0 + c, u);
+              } else if (o.keep == 2) {
+                put_codes(o, 0, row, c0 + c, v, scale[0]);
+                put_codes(o, 1, row, c0 + c, u, scale[1]);
+              }
+              with_act(o.act, [&](auto act) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = act_of<decltype(act)::value>(v[k]) * u[k];
+              });
+              emit<false>(pieces, &maps.d[0], o.d_tma[0], o.d[0], o.ldd[0], o, f8::kSiteOut, row0, c0 + c, v);
+            } else {
+              Residual<true> ra;
+              Residual<false> rb;
+              if (o.residual) {
+                if (o.r_vec && c0 + c + 32 <= o.N) ra.load(o, row, c0 + c);
+                else                               rb.load(o, row, c0 + c);
+              }
+              tmem_wait_ld();
+              if (c + 32 == cols) release();
+              tmem_ld_ready(v);
+              if (o.bias) add_bias(o, c0 + c, v);
+              if (o.keep == 1) emit<false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, f8::kSiteCodes, row0, c0 + c, v);
+              else if (o.keep == 2) put_codes(o, 0, row, c0 + c, v, scale[0]);
+              with_act(o.act, [&](auto act) {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = act_of<decltype(act)::value>(v[k]);
+              });
+              if (o.residual) {
+                if (o.r_vec && c0 + c + 32 <= o.N) ra.add(v);
+                else                               rb.add(v);
+              }
+              if (o.f32) emit<true>(pieces, &maps.d[product], o.d_tma[product], o.d[product], o.ldd[product], o, f8::kSiteOut, row0, c0 + c, v);
+              else       emit<false>(pieces, &maps.d[product], o.d_tma[product], o.d[product], o.ldd[product], o, f8::kSiteOut, row0, c0 + c, v);
+            }
+          }
+        }
+        if (!ok) break;
+        if (++b == bufs) {
+          b = 0;
+          ++b_lap;
+        }
+      }
+    }
+    if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
+    __syncwarp();
+  }
+
+  tmem_fence_before_sync();
+  __syncthreads();
+  // Bounded handshake of the two CTAs: neither releases its TMEM or exits while the other may still arrive on its barriers
+  // or have products read its shared memory and TMEM.
+  if (threadIdx.x == 0) {
+    mbar_arrive_remote(smem_addr(&fin), rank ^ 1u);
+    if (!mbar_wait(smem_addr(&fin), 0u, p.timeout_ns)) atomicOr(p.fault, (unsigned)kFaultDrainWait);
+  }
+  __syncthreads();
+  tmem_fence_after_sync();
+  if (warp == 1) tmem_dealloc_pair(tmem, kTmemCols);
+}
+
+// f(kernel) for a tile width and form.
+template <typename F>
+cudaError_t with_kernel(int tile_n, bool gated, const F& f) {
+  switch (tile_n) {
+    case 256: return gated ? f(linear_pair_kernel<256, true>) : f(linear_pair_kernel<256, false>);
+    case 128: return gated ? f(linear_pair_kernel<128, true>) : f(linear_pair_kernel<128, false>);
+    case 64: return gated ? cudaErrorInvalidValue : f(linear_pair_kernel<64, false>);
+  }
+  return cudaErrorInvalidValue;
+}
+
+}  // namespace
+}  // namespace lin
+
+int64_t linear_pair_smem() { return lin::kSmem; }
+
+cudaError_t prepare_linear_pair() {
+  for (int tile_n : kLinearPairTiles)
+    for (int gated = 0; gated < 2; ++gated) {
+      if (gated && tile_n == 64) continue;
+      const cudaError_t e = lin::with_kernel(tile_n, gated != 0, [](auto kernel) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kSmem);
+      });
+      if (e != cudaSuccess) return e;
+    }
+  return cudaSuccess;
+}
+
+cudaError_t launch_linear_pair(int tile_n, bool gated, const LinearMaps& maps, const LinearPairParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2u * (unsigned)p.clusters);
+  cfg.blockDim = dim3(lin::kThreads);
+  cfg.dynamicSmemBytes = lin::kSmem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return lin::with_kernel(tile_n, gated, [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, maps, p); });
+}
+
+}  // namespace sgemm_impl

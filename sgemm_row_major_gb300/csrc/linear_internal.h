@@ -1,0 +1,112 @@
+// linear_internal.h -- host-side declarations of the operators on BF16 layers (sgemm_linear.h).
+#pragma once
+
+#include <cstdint>
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include "fp8_internal.h"
+#include "sgemm_linear.h"
+
+namespace sgemm_impl {
+
+// What an entry point of this part needs of the current device (its kernels are set up by the first call; api.cu).
+int linear_device(CallDevice* out);  // an sgemm_status
+
+// What happens to a product's sums: bias, activation, residual, the output and what is kept of the sums.
+struct LinearKept {
+  void* data = nullptr;
+  float* scale = nullptr;
+  int64_t ld = 0, lds = 0;
+  int vec = 0;                   // BF16: TMA writes it; 8-bit: rows start at multiples of 16 bytes
+};
+struct LinearOut {
+  int M = 0, N = 0;              // rows and columns of the output (of each of two products, of H)
+  void* d[2] = {nullptr, nullptr};
+  int64_t ldd[2] = {0, 0};
+  int d_tma[2] = {0, 0};         // 1: aligned rows of whole 16 bytes, which TMA writes
+  int f32 = 0;                   // type of d
+  const void* bias = nullptr;    // N values or nullptr
+  const void* residual = nullptr;
+  int64_t ldr = 0;
+  int act = 0;
+  int keep = 0;                  // 0: nothing, 1: BF16, 2: 8-bit
+  LinearKept kept[2];            // of A and B
+  int bias_vec = 0, r_vec = 0;   // 1: 16-byte aligned (rows)
+  int d_vec[2] = {0, 0};         // 1: rows of d start at multiples of 8 bytes (BF16) or 16 bytes (FP32)
+  int kept_vec8[2] = {0, 0};     // 1: rows of a BF16 kept matrix start at multiples of 8 bytes
+  Guard guard;
+};
+
+// D = A0 B0 (+ A1 B1 with two segments); with two products D0 = A0 B0, D1 = A1 B0; gated: B0 and B1 are gate and up.
+struct LinearMaps {
+  CUtensorMap a[2], b[2], d[2], kept[2];
+};
+
+struct LinearPairParams {
+  LinearOut out;
+  int k_tiles = 0;               // of 64 k, per segment
+  int segments = 1, products = 1;
+  int a_mn = 0, b_mn = 0;        // 1: the stored rows run along M (N), not along K
+  uint32_t idesc = 0;
+  int tiles_m = 0, tiles_n = 0, clusters = 0;
+  uint64_t timeout_ns = 0;
+  unsigned* fault = nullptr;
+};
+constexpr int kLinearPairStages = 5, kLinearPairThreads = 384;
+constexpr int kLinearPairTiles[] = {256, 128, 64};
+int64_t linear_pair_smem();
+cudaError_t prepare_linear_pair();
+cudaError_t launch_linear_pair(int tile_n, bool gated, const LinearMaps& maps, const LinearPairParams& p, cudaStream_t stream);
+
+// The columns of D run along the tensor core's rows (B's tile of 128), its rows along the columns.
+struct LinearShortParams {
+  LinearOut out;
+  int k_tiles = 0, segments = 1;
+  int l_mn = 0, s_mn = 0;        // order of B and of A
+  uint32_t idesc = 0;
+  int tile_s = 0, tiles_l = 0, tiles_s = 0, split = 1, stages = 0, stage_bytes = 0;
+  uint64_t timeout_ns = 0;
+  unsigned* fault = nullptr;
+};
+constexpr int kLinearShortTiles[] = {16, 32, 64, 128};
+constexpr int kLinearShortMaxStages = 12, kLinearShortThreads = 256;
+int64_t linear_short_smem(int tile_s, bool gated, int stages, int stage_bytes);
+cudaError_t prepare_linear_short();
+cudaError_t launch_linear_short(bool gated, const LinearMaps& maps, const LinearShortParams& p, cudaStream_t stream);
+
+// The elementwise part of the backward passes (kernel_linear_grad.cu).
+struct LinearKeptIn {
+  const void* data = nullptr;    // nullptr: not read
+  const float* scale = nullptr;  // nullptr: BF16
+  int64_t ld = 0, lds = 0;
+  int vec = 0;                   // 1: chunks of 8 elements can be read at once
+};
+struct LinearGradParams {
+  int64_t rows = 0;
+  int cols = 0;
+  const void* dy = nullptr;
+  int64_t lddy = 0;
+  int dy_vec = 0;
+  LinearKeptIn a, b;             // b: gated
+  int act = 0;
+  void *da = nullptr, *db = nullptr, *h = nullptr;  // nullptr: not wanted (da and db: aligned rows)
+  int64_t ldd = 0, ldh = 0;
+  int h_vec = 0;
+  float* partial = nullptr;      // [row blocks][cols] sums of dA (nullptr: dbias is not wanted)
+  float* dbias = nullptr;
+  int row_blocks = 0;
+  Guard guard;
+};
+int linear_grad_row_blocks(int64_t rows, int cols, int sm_count);
+cudaError_t launch_linear_grad(const LinearGradParams& p, cudaStream_t stream);
+
+// A stored matrix as aligned BF16 rows (ldd a multiple of 8): BF16 of any alignment copied, 8-bit values times their scales.
+cudaError_t launch_linear_expand(const LinearKeptIn& m, int64_t rows, int64_t cols, void* dst, int64_t ldd, const Guard& guard,
+                                 cudaStream_t stream);
+
+// Map over `outer` rows of `inner` BF16 values (row stride ld elements, a multiple of 8): boxes of 64 x box_outer,
+// 128-byte swizzle, zeros outside.
+cudaError_t encode_linear_map(const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer, CUtensorMap* map);
+
+}  // namespace sgemm_impl

@@ -8,6 +8,7 @@
 #include <mutex>
 
 #include "fp8_internal.h"
+#include "linear_internal.h"
 #include "sgemm_internal.h"
 
 namespace sgemm_impl {
@@ -86,6 +87,22 @@ cudaError_t encode_bf16_map(const void* base, int64_t K, int64_t rows, int64_t l
   const cuuint64_t dims[3] = {(cuuint64_t)K, (cuuint64_t)rows, 1};
   const cuuint64_t strides[2] = {(cuuint64_t)ldk * 2u, (cuuint64_t)(rows * ldk) * 2u};
   const cuuint32_t box[3] = {64u, 128u, 1u};
+  const cuuint32_t estr[3] = {1, 1, 1};
+  CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                  CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                  CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t encode_linear_map(const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer, CUtensorMap* map) {
+  cudaError_t e = bind_primary_context();
+  if (e != cudaSuccess) return e;
+  EncodeTiledFn fn = nullptr;
+  e = encode_fn(&fn);
+  if (e != cudaSuccess) return e;
+  const cuuint64_t dims[3] = {(cuuint64_t)inner, (cuuint64_t)outer, 1};
+  const cuuint64_t strides[2] = {(cuuint64_t)ld * 2u, (cuuint64_t)ld * 2u};  // one matrix: the second is not used
+  const cuuint32_t box[3] = {64u, (cuuint32_t)box_outer, 1u};
   const cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
