@@ -42,8 +42,10 @@ std::atomic<int> g_force_variant{SGEMM_VARIANT_AUTO}, g_force_tile{0}, g_force_s
 // A product: M x N over `segments` times K.
 struct Shape {
   int64_t M = 0, N = 0, K = 0;
-  int segments = 1, products = 1;
+  int segments = 1;
   bool gated = false, kept8 = false;
+  int64_t k_tiles() const { return ceil_div(K, 64) * segments; }
+  int64_t pair_tiles(int tile) const { return ceil_div(M, 256) * ceil_div(N, gated ? tile / 2 : tile); }
 };
 
 // Times in ns that the choice of kernel goes by.  In the pair kernel, by tile width: a K tile of 64, and the rest of a tile.
@@ -77,82 +79,74 @@ struct Choice {
   double ns = 1e30;
 };
 
-// The cheapest launch, among the variant, tile and split that are forced (0: any); clusters: CTA pairs that run at a time, 0
-// on a device without clusters, where only unshared tiles can run.
-Choice choose(const Shape& s, int64_t clusters, int sm_count, int variant, int tile, int split) {
-  const int64_t kt = ceil_div(s.K, 64) * s.segments;
+// The pair kernel's time for up to three products in one launch: that of the cluster with the most work (tiles are dealt round
+// robin; a cluster has one more of a product's tiles where the deal of its last round starts, so one of these has the most).
+double pair_ns(const Shape* s, int n, const PairCost& c, int64_t clusters) {
+  double most = 0.0;
+  int64_t start = 0;
+  for (int i = 0; i < n; start += s[i++].pair_tiles(c.tile)) {
+    const int64_t at = (start + s[i].pair_tiles(c.tile) / clusters * clusters) % clusters;
+    double ns = 0.0;
+    int64_t first = 0;
+    for (int k = 0; k < n; first += s[k++].pair_tiles(c.tile)) {
+      // tiles of product k that cluster `at` gets: those in [first, first + tiles) that are `at` modulo the clusters
+      const int64_t skip = ((at - first) % clusters + clusters) % clusters, tiles = s[k].pair_tiles(c.tile);
+      const int64_t mine = tiles > skip ? (tiles - skip - 1) / clusters + 1 : 0;
+      ns += (double)mine * (s[k].k_tiles() * c.k_ns + c.tile_ns);
+    }
+    most = std::max(most, ns);
+  }
+  return kPairLaunchNs + most;
+}
+
+// The cheapest launch of one product (several: in one launch of the pair kernel), among the variant, tile and split that are
+// forced (0: any); clusters: CTA pairs that run at a time, 0 on a device without clusters, where only unshared tiles can run.
+Choice choose(const Shape* s, int n, int64_t clusters, int sm_count, int variant, int tile, int split) {
   Choice best;
-  const auto offer = [&](int v, int n, int k, double ns) {
-    if (ns < best.ns) best = Choice{v, n, k, ns};
+  const auto offer = [&](int v, int t, int k, double ns) {
+    if (ns < best.ns) best = Choice{v, t, k, ns};
   };
   const auto forced_here = [&](const auto& tiles, const auto& fits) {
     return std::any_of(std::begin(tiles), std::end(tiles), [&](int t) { return t == tile && fits(t); });
   };
   if (variant != SGEMM_VARIANT_LINEAR_SHORT && clusters > 0) {
-    const bool only = forced_here(kLinearPairTiles, [&](int t) { return pair_tile_fits(t, s); });
-    for (const PairCost& c : kPairCost) {
-      if (!pair_tile_fits(c.tile, s) || (only && c.tile != tile)) continue;
-      const int64_t tiles = ceil_div(s.M, 256) * ceil_div(s.N, s.gated ? c.tile / 2 : c.tile) * s.products;
-      offer(SGEMM_VARIANT_LINEAR_PAIR, c.tile, 1, kPairLaunchNs + (double)ceil_div(tiles, clusters) * (kt * c.k_ns + c.tile_ns));
-    }
+    const bool only = forced_here(kLinearPairTiles, [&](int t) { return pair_tile_fits(t, s[0]); });
+    for (const PairCost& c : kPairCost)
+      if (pair_tile_fits(c.tile, s[0]) && (!only || c.tile == tile)) offer(SGEMM_VARIANT_LINEAR_PAIR, c.tile, 1, pair_ns(s, n, c, clusters));
   }
-  if (variant != SGEMM_VARIANT_LINEAR_PAIR) {
-    const auto fits = [&](int t) { return !s.gated || t < 128; };
+  if (variant != SGEMM_VARIANT_LINEAR_PAIR && n == 1) {
+    const int64_t kt = s->k_tiles();
+    const bool gated = s->gated;
+    const auto fits = [&](int t) { return !gated || t < 128; };
     const bool only = forced_here(kLinearShortTiles, fits);
     for (const ShortCost& c : kShortCost) {
-      if (!fits(c.tile) || (only ? c.tile != tile : c.tile > 16 && c.tile >= 2 * s.M)) continue;
-      const int64_t tiles = ceil_div(s.N, 128) * ceil_div(s.M, c.tile);
+      if (!fits(c.tile) || (only ? c.tile != tile : c.tile > 16 && c.tile >= 2 * s->M)) continue;
+      const int64_t tiles = ceil_div(s->N, 128) * ceil_div(s->M, c.tile);
       if (tiles * 8 > INT_MAX) continue;
-      const int wide = s.gated ? 2 : 1;
+      const int wide = gated ? 2 : 1;
       for (int k = 1; k <= 8; k *= 2) {
         if (clusters == 0 && k > 1) break;
         if (split != 0 ? split != k : k > 1 && kt < 2 * k) continue;  // two K tiles per CTA at least
-        const int per_sm = short_alone(c.tile, s.gated) ? 1 : 2;
+        const int per_sm = short_alone(c.tile, gated) ? 1 : 2;
         const double on_sm = std::min((double)per_sm, std::max(1.0, (double)tiles * k / sm_count));
         const double one = std::max(c.k_ns * wide * (1.0 + kSharedSm * (on_sm - 1.0)), on_sm * (16384 * wide + 64 * c.tile) / kSmBytesPerNs);
         const double rounds = (double)ceil_div(tiles * k, cluster_sms(sm_count, k) * per_sm);
         offer(SGEMM_VARIANT_LINEAR_SHORT, c.tile, k,
-              s.products * (kShortLaunchNs + rounds * (ceil_div(kt, k) * one + c.tile_ns + (k > 1 ? c.join_ns : 0))));
+              kShortLaunchNs + rounds * (ceil_div(kt, k) * one + c.tile_ns + (k > 1 ? c.join_ns : 0)));
       }
     }
   }
   return best;
 }
 
-int plan_shape(const Shape& s, bool s_mn, int sm_count, int pair_clusters, sgemm_plan_t* plan) {
-  *plan = sgemm_plan_t{};
-  plan->split_k = 1;
+Choice choose(const Shape* s, int n, int sm_count, int pair_clusters) {
   const int64_t clusters = pair_clusters >= 0 ? pair_clusters : std::max(1, sm_count / 2);
-  const Choice c = choose(s, clusters, sm_count, g_force_variant.load(), g_force_tile.load(), g_force_split.load());
-  if (c.variant == 0) return SGEMM_ERR_UNSUPPORTED;  // forced to what needs clusters
-  plan->variant = c.variant;
-  plan->tile_k = 64;
-  plan->kernel_launches = 1;
-  plan->grid_y = 1;
-  int64_t tiles;
-  if (c.variant == SGEMM_VARIANT_LINEAR_PAIR) {
-    plan->tile_m = 256;
-    plan->tile_n = c.tile;
-    plan->stages = kLinearPairStages;
-    plan->threads = kLinearPairThreads;
-    plan->smem_bytes = linear_pair_smem();
-    tiles = ceil_div(s.M, 256) * ceil_div(s.N, s.gated ? c.tile / 2 : c.tile) * s.products;
-    plan->grid_x = 2 * std::min<int64_t>(tiles, clusters);
-    if (ceil_div(tiles, clusters) * ceil_div(s.K, 64) * s.segments > INT_MAX) return SGEMM_ERR_UNSUPPORTED;
-  } else {
-    plan->tile_m = 128;
-    plan->tile_n = c.tile;
-    plan->split_k = c.split;
-    plan->kernel_launches = s.products;
-    tiles = ceil_div(s.N, 128) * ceil_div(s.M, c.tile);
-    const int64_t stage = (s.gated ? 2 : 1) * 16384 + (s_mn ? std::max(1, c.tile / 64) * 8192 : c.tile * 128);
-    plan->stages = (int)std::min<int64_t>(kLinearShortMaxStages, short_ring(c.tile, s.gated) / stage);
-    plan->threads = kLinearShortThreads;
-    plan->smem_bytes = linear_short_smem(c.tile, s.gated, plan->stages, (int)stage);
-    plan->grid_x = tiles * c.split;
-  }
-  plan->dp_tiles = tiles;
-  return tiles > INT_MAX || plan->grid_x > INT_MAX ? SGEMM_ERR_UNSUPPORTED : SGEMM_OK;
+  return choose(s, n, clusters, sm_count, g_force_variant.load(), g_force_tile.load(), g_force_split.load());
+}
+
+int64_t short_stage(int tile, bool gated, bool s_mn) { return (gated ? 2 : 1) * 16384 + (s_mn ? std::max(1, tile / 64) * 8192 : tile * 128); }
+int short_stages(int tile, bool gated, bool s_mn) {
+  return (int)std::min<int64_t>(kLinearShortMaxStages, short_ring(tile, gated) / short_stage(tile, gated, s_mn));
 }
 
 // ---------------------------------------------------------------- operands and workspace
@@ -173,12 +167,11 @@ struct Pieces {
 struct Operand {
   LinearKeptIn m;
   int64_t rows = 0, cols = 0;  // stored
-  int mn = 0;                  // the stored rows run along the output, not along k
   void* copy = nullptr;
   bool copied = false;
 
   Operand() = default;
-  Operand(const void* p, int64_t ld, const float* scale, int64_t lds, int64_t rows_, int64_t cols_, int mn_) : rows(rows_), cols(cols_), mn(mn_) {
+  Operand(const void* p, int64_t ld, const float* scale, int64_t lds, int64_t rows_, int64_t cols_) : rows(rows_), cols(cols_) {
     m.data = p;
     m.ld = ld;
     m.scale = scale;
@@ -196,7 +189,7 @@ struct Operand {
   }
   cudaError_t map(int box_rows, CUtensorMap* out) const {
     const int64_t ld = copied || rows == 1 ? round8(cols) : m.ld;  // (a map wants a stride even where it steps over nothing)
-    return encode_linear_map(copied ? copy : m.data, cols, rows, ld, mn ? 64 : box_rows, out);
+    return encode_linear_map(copied ? copy : m.data, cols, rows, ld, box_rows, out);
   }
 };
 
@@ -206,94 +199,139 @@ uint32_t instruction(int a_mn, int b_mn, int m, int n) {
          ((uint32_t)(m >> 4) << 24);
 }
 
+// A product with its operands and output.  mn: an operand's stored rows run along the output, not along k.
 struct Product {
   Shape shape;
-  Operand *a[2] = {nullptr, nullptr}, *b[2] = {nullptr, nullptr};  // the second of each: as the kernel's maps
-  LinearOut out;
+  const Operand *a[2] = {nullptr, nullptr}, *b[2] = {nullptr, nullptr};
+  int a_mn = 0, b_mn = 0;
+  void* d = nullptr;
+  int64_t ldd = 0;
+  bool f32 = false;
 };
 
-bool tma_writes(const void* p, int64_t ld, int64_t cols, int size) { return rows_at(p, ld, size, 16) && cols * size % 16 == 0; }
+// K tiles that are summed in one accumulator: FP32 values that leave the kernel are to be about as exact as FP32 sums.
+constexpr int kFoldF32 = 8, kFoldKept8 = 16, kFoldNone = 1 << 30;
 
-cudaError_t launch_product(Product& pr, const sgemm_plan_t& plan, const CallDevice& dev, cudaStream_t stream) {
-  LinearOut& o = pr.out;
-  const Shape& s = pr.shape;
-  o.M = (int)s.M;
-  o.N = (int)s.N;
-  o.guard = {dev.fault, dev.bounds};
-  o.bias_vec = aligned(o.bias, 16);
-  const int size = o.f32 ? 4 : 2;
-  const bool pair = plan.variant == SGEMM_VARIANT_LINEAR_PAIR;
-  o.r_vec = rows_at(o.residual, o.ldr, 2, 16);
-  LinearMaps maps = {};
-  cudaError_t e = cudaSuccess;
-  for (int i = 0; i < 2; ++i) {
-    if (o.d[i]) {
-      o.d_tma[i] = tma_writes(o.d[i], o.ldd[i], s.N, size);
-      o.d_vec[i] = rows_at(o.d[i], o.ldd[i], size, 4 * size);
-      if (pair && o.d_tma[i] && e == cudaSuccess) e = encode_out_map(o.d[i], s.N, s.M, o.ldd[i], !o.f32, &maps.d[i]);
+// One launch of the products: of one with a choice of either kernel, of several with the pair kernel.
+struct Launch {
+  Product pr[kLinearJobs];
+  int n = 0;
+  LinearOut out;
+
+  Product& add() { return pr[n++]; }
+
+  int run(const CallDevice& dev, cudaStream_t stream, cudaError_t* e) {
+    Shape s[kLinearJobs];
+    for (int i = 0; i < n; ++i) s[i] = pr[i].shape;
+    Choice c = choose(s, n, dev.sm_count, dev.pair_clusters);
+    if (n > 1) {
+      // each by itself where that is cheaper: a short one among long ones, or no clusters
+      Choice one[kLinearJobs];
+      double ns = 0.0;
+      for (int i = 0; i < n; ++i) {
+        one[i] = choose(s + i, 1, dev.sm_count, dev.pair_clusters);
+        ns += one[i].ns;
+      }
+      if (ns < c.ns) {
+        for (int i = 0; i < n && *e == cudaSuccess; ++i) {
+          if (one[i].variant == 0) return SGEMM_ERR_UNSUPPORTED;
+          const int st = launch(&pr[i], 1, one[i], dev, stream, e);
+          if (st != SGEMM_OK) return st;
+        }
+        return SGEMM_OK;
+      }
     }
-    LinearKept& k = o.kept[i];
-    if (k.data) {
-      k.vec = o.keep == 2 ? rows_at(k.data, k.ld, 1, 16) : tma_writes(k.data, k.ld, s.N, 2);
-      o.kept_vec8[i] = rows_at(k.data, k.ld, 2, 8);
-      if (pair && o.keep == 1 && k.vec && e == cudaSuccess) e = encode_out_map(k.data, s.N, s.M, k.ld, true, &maps.kept[i]);
-    }
-    const int tile = plan.tile_n;
-    if (pr.a[i] && e == cudaSuccess) e = pr.a[i]->map(pair ? 128 : tile, &maps.a[i]);
-    if (pr.b[i] && e == cudaSuccess) e = pr.b[i]->map(pair ? tile / 2 : 128, &maps.b[i]);
+    if (c.variant == 0) return SGEMM_ERR_UNSUPPORTED;  // forced to what needs clusters
+    return launch(pr, n, c, dev, stream, e);
   }
-  if (e != cudaSuccess) return e;
-  if (pair) {
+
+ private:
+  int launch(const Product* list, int count, const Choice& c, const CallDevice& dev, cudaStream_t stream, cudaError_t* e) {
+    const bool pair = c.variant == SGEMM_VARIANT_LINEAR_PAIR, gated = list[0].shape.gated;
+    out.guard = {dev.fault, dev.bounds};
+    out.bias_vec = aligned(out.bias, 16);
+    out.r_vec = rows_at(out.residual, out.ldr, 2, 16);
+    LinearMaps maps;
     LinearPairParams p;
-    p.out = o;
-    p.k_tiles = (int)ceil_div(s.K, 64);
-    p.segments = s.segments;
-    p.products = s.products;
-    p.a_mn = pr.a[0]->mn;
-    p.b_mn = pr.b[0]->mn;
-    p.idesc = instruction(p.a_mn, p.b_mn, 256, plan.tile_n);
-    p.tiles_m = (int)ceil_div(s.M, 256);
-    p.tiles_n = (int)ceil_div(s.N, s.gated ? plan.tile_n / 2 : plan.tile_n);
-    p.clusters = (int)(plan.grid_x / 2);
-    p.timeout_ns = wait_timeout_ns();
-    p.fault = dev.fault;
-    return launch_linear_pair(plan.tile_n, s.gated, maps, p, stream);
-  }
-  LinearShortParams p;
-  p.out = o;
-  p.k_tiles = (int)ceil_div(s.K, 64);
-  p.segments = s.segments;
-  p.l_mn = pr.b[0]->mn;
-  p.s_mn = pr.a[0]->mn;
-  p.idesc = instruction(p.l_mn, p.s_mn, 128, plan.tile_n);
-  p.tile_s = plan.tile_n;
-  p.tiles_l = (int)ceil_div(s.N, 128);
-  p.tiles_s = (int)ceil_div(s.M, plan.tile_n);
-  p.split = plan.split_k;
-  p.stages = plan.stages;
-  p.stage_bytes = (s.gated ? 2 : 1) * 16384 + (p.s_mn ? std::max(1, plan.tile_n / 64) * 8192 : plan.tile_n * 128);
-  p.timeout_ns = wait_timeout_ns();
-  p.fault = dev.fault;
-  for (int i = 0; i < s.products && e == cudaSuccess; ++i) {
-    if (i == 1) {  // its own A and output, the same B
-      maps.a[0] = maps.a[1];
-      p.out.d[0] = o.d[1];
-      p.out.ldd[0] = o.ldd[1];
-      p.out.d_vec[0] = o.d_vec[1];
+    const Operand* known[6];
+    int box[6], maps_used = 0;
+    const auto map_of = [&](const Operand* o, int rows) {  // an operand's map, made once
+      for (int i = 0; i < maps_used; ++i)
+        if (known[i] == o && box[i] == rows) return i;
+      known[maps_used] = o;
+      box[maps_used] = rows;
+      if (*e == cudaSuccess) *e = o->map(rows, &maps.op[maps_used]);
+      return maps_used++;
+    };
+    int64_t tiles = 0, steps = 0;
+    for (int i = 0; i < count; ++i) {
+      const Product& r = list[i];
+      LinearJob& j = p.job[i];
+      const int size = r.f32 ? 4 : 2;
+      j.M = (int)r.shape.M;
+      j.N = (int)r.shape.N;
+      j.d = r.d;
+      j.ldd = r.ldd;
+      j.f32 = r.f32;
+      j.d_tma = tma_writes(r.d, r.ldd, r.shape.N, size);
+      j.d_vec = rows_at(r.d, r.ldd, size, 4 * size);
+      j.k_tiles = (int)ceil_div(r.shape.K, 64);
+      j.segments = r.shape.segments;
+      j.fold = r.f32 ? kFoldF32 : out.keep == 2 ? kFoldKept8 : kFoldNone;
+      j.a_mn = r.a_mn;
+      j.b_mn = r.b_mn;
+      if (pair) {
+        j.tiles_m = (int)ceil_div(r.shape.M, 256);
+        j.tiles_n = (int)ceil_div(r.shape.N, gated ? c.tile / 2 : c.tile);
+        j.idesc = instruction(r.a_mn, r.b_mn, 256, c.tile);
+        if (j.d_tma && *e == cudaSuccess) *e = encode_out_map(r.d, r.shape.N, r.shape.M, r.ldd, !r.f32, &maps.d[i]);
+      } else {
+        j.tiles_m = (int)ceil_div(r.shape.M, c.tile);
+        j.tiles_n = (int)ceil_div(r.shape.N, 128);
+        j.idesc = instruction(r.b_mn, r.a_mn, 128, c.tile);
+      }
+      for (int k = 0; k < 2; ++k) {
+        if (r.a[k]) j.a[k] = map_of(r.a[k], r.a_mn || pair ? 64 : std::min(64, c.tile));
+        if (r.b[k]) j.b[k] = map_of(r.b[k], r.b_mn || !pair ? 64 : std::min(64, c.tile / 2));
+      }
+      tiles += (int64_t)j.tiles_m * j.tiles_n;
+      steps += (int64_t)j.tiles_m * j.tiles_n * r.shape.k_tiles();
     }
-    e = launch_linear_short(s.gated, maps, p, stream);
+    for (int i = 0; i < 2; ++i) {
+      LinearKept& k = out.kept[i];
+      if (!k.data) continue;
+      k.vec = out.keep == 2 ? rows_at(k.data, k.ld, 1, 16) : tma_writes(k.data, k.ld, list[0].shape.N, 2);
+      out.kept_vec8[i] = rows_at(k.data, k.ld, 2, 8);
+      if (pair && out.keep == 1 && k.vec && *e == cudaSuccess) *e = encode_out_map(k.data, list[0].shape.N, list[0].shape.M, k.ld, true, &maps.kept[i]);
+    }
+    if (*e != cudaSuccess) return SGEMM_OK;
+    if (pair) {
+      const int64_t clusters = std::min<int64_t>(tiles, dev.pair_clusters);
+      if (tiles > INT_MAX || steps / clusters > INT_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
+      p.out = out;
+      p.jobs = count;
+      p.clusters = (int)clusters;
+      p.timeout_ns = wait_timeout_ns();
+      p.fault = dev.fault;
+      *e = launch_linear_pair(c.tile, gated, maps, p, stream);
+      return SGEMM_OK;
+    }
+    LinearShortParams q;
+    q.out = out;
+    q.job = p.job[0];
+    q.tile_s = c.tile;
+    q.split = c.split;
+    q.stages = short_stages(c.tile, gated, list[0].a_mn != 0);
+    q.stage_bytes = (int)short_stage(c.tile, gated, list[0].a_mn != 0);
+    q.timeout_ns = wait_timeout_ns();
+    q.fault = dev.fault;
+    if (tiles * c.split > INT_MAX) return SGEMM_ERR_UNSUPPORTED;
+    *e = launch_linear_short(gated, maps, q, stream);
+    return SGEMM_OK;
   }
-  return e;
-}
 
-// Plans a product, and launches it.
-int run_product(Product& pr, const CallDevice& dev, cudaStream_t stream, cudaError_t* e) {
-  sgemm_plan_t plan;
-  const int s = plan_shape(pr.shape, pr.a[0]->mn != 0, dev.sm_count, dev.pair_clusters, &plan);
-  if (s != SGEMM_OK) return s;
-  *e = launch_product(pr, plan, dev, stream);
-  return SGEMM_OK;
-}
+  static bool tma_writes(const void* p, int64_t ld, int64_t cols, int size) { return rows_at(p, ld, size, 16) && cols * size % 16 == 0; }
+};
 
 // What is kept, as the kernels take it: 0 nothing, 1 BF16, 2 8-bit.
 int keep_of(const sgemm_kept_t* k, LinearKept* out) {
@@ -352,21 +390,21 @@ bool too_large(std::initializer_list<int64_t> v) {
 
 // The forward products: X (W0, gated: W1)^T with their epilogue.
 int forward(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, int64_t ldx, const void* W0, int64_t ldw0, const void* W1,
-            int64_t ldw1, Product& pr, cudaStream_t stream) {
+            int64_t ldw1, Launch& launch, cudaStream_t stream) {
+  Product& pr = launch.pr[0];
   CallDevice dev;
   const int s = linear_device(&dev);
   if (s != SGEMM_OK) return s;
-  const bool gated = W1 != nullptr || pr.shape.gated;
+  const bool gated = pr.shape.gated;
   const bool empty = inputs == 0;  // a sum of nothing: 8 zeros per row instead
   const int64_t K = empty ? 8 : inputs;
   void* zeros = nullptr;
-  Operand x(X, ldx, nullptr, 0, tokens, K, 0), w0(W0, ldw0, nullptr, 0, outputs, K, 0), w1(W1, ldw1, nullptr, 0, outputs, K, 0);
+  Operand x(X, ldx, nullptr, 0, tokens, K), w0(W0, ldw0, nullptr, 0, outputs, K), w1(W1, ldw1, nullptr, 0, outputs, K);
   if (empty) x.copied = w0.copied = w1.copied = false;
   pr.shape.M = tokens;
   pr.shape.N = outputs;
   pr.shape.K = K;
-  pr.shape.gated = gated;
-  pr.shape.kept8 = pr.out.keep == 2;
+  pr.shape.kept8 = launch.out.keep == 2;
   pr.a[0] = &x;
   pr.b[0] = &w0;
   if (gated) pr.b[1] = &w1;
@@ -387,8 +425,40 @@ int forward(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, int6
         if (*e == cudaSuccess) *e = x.make(g, stream);
         if (*e == cudaSuccess) *e = w0.make(g, stream);
         if (*e == cudaSuccess && gated) *e = w1.make(g, stream);
-        return *e == cudaSuccess ? run_product(pr, dev, stream, e) : SGEMM_OK;
+        return *e == cudaSuccess ? launch.run(dev, stream, e) : SGEMM_OK;
       });
+}
+
+// tokens x inputs over the outputs (twice them with two gradients and weights).
+Product input_gradient(int64_t tokens, int64_t inputs, int64_t outputs, const Operand* d0, const Operand* d1, const Operand* w0, const Operand* w1,
+                       void* dX, int64_t lddx) {
+  Product r;
+  r.shape.M = tokens;
+  r.shape.N = inputs;
+  r.shape.K = outputs;
+  r.shape.segments = d1 ? 2 : 1;
+  r.a[0] = d0;
+  r.a[1] = d1;
+  r.b[0] = w0;
+  r.b[1] = w1;
+  r.b_mn = 1;
+  r.d = dX;
+  r.ldd = lddx;
+  return r;
+}
+// outputs x inputs over the tokens.
+Product weight_gradient(int64_t tokens, int64_t inputs, int64_t outputs, const Operand* d, const Operand* x, void* dW, int64_t lddw, int type) {
+  Product r;
+  r.shape.M = outputs;
+  r.shape.N = inputs;
+  r.shape.K = tokens;
+  r.a[0] = d;
+  r.b[0] = x;
+  r.a_mn = r.b_mn = 1;
+  r.d = dW;
+  r.ldd = lddw;
+  r.f32 = type == SGEMM_F32;
+  return r;
 }
 
 }  // namespace
@@ -416,16 +486,18 @@ int sgemm_linear(int64_t tokens, int64_t inputs, int64_t outputs, const void* X,
   if (!wide_enough(ldy, outputs) || (work && Y == R && tokens > 1 && ldy != ldr)) return -14;
   if (!work) return SGEMM_OK;
   if (too_large({tokens, inputs, outputs, ldx, ldw, ldy, R ? ldr : 0})) return SGEMM_ERR_UNSUPPORTED;
-  Product pr;
-  pr.out.d[0] = Y;
-  pr.out.ldd[0] = ldy;
-  pr.out.f32 = type == SGEMM_F32;
-  pr.out.bias = bias;
-  pr.out.residual = R;
-  pr.out.ldr = ldr;
-  pr.out.act = activation;
-  pr.out.keep = keep_of(kept, &pr.out.kept[0]);
-  return forward(tokens, inputs, outputs, X, ldx, W, ldw, nullptr, 0, pr, reinterpret_cast<cudaStream_t>(stream));
+  Launch launch;
+  Product& pr = launch.add();
+  pr.d = Y;
+  pr.ldd = ldy;
+  pr.f32 = type == SGEMM_F32;
+  LinearOut& o = launch.out;
+  o.bias = bias;
+  o.residual = R;
+  o.ldr = ldr;
+  o.act = activation;
+  o.keep = keep_of(kept, &o.kept[0]);
+  return forward(tokens, inputs, outputs, X, ldx, W, ldw, nullptr, 0, launch, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int sgemm_gated(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, int64_t ldx, const void* gate, int64_t ldg, const void* up,
@@ -448,14 +520,16 @@ int sgemm_gated(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, 
   if (!wide_enough(ldh, outputs)) return -14;
   if (!work) return SGEMM_OK;
   if (too_large({tokens, inputs, outputs, ldx, ldg, ldu, ldh})) return SGEMM_ERR_UNSUPPORTED;
-  Product pr;
+  Launch launch;
+  Product& pr = launch.add();
   pr.shape.gated = true;
-  pr.out.d[0] = H;
-  pr.out.ldd[0] = ldh;
-  pr.out.act = activation;
-  pr.out.keep = keep_of(kept_gate, &pr.out.kept[0]);
-  keep_of(kept_up, &pr.out.kept[1]);
-  return forward(tokens, inputs, outputs, X, ldx, gate, ldg, up, ldu, pr, reinterpret_cast<cudaStream_t>(stream));
+  pr.d = H;
+  pr.ldd = ldh;
+  LinearOut& o = launch.out;
+  o.act = activation;
+  o.keep = keep_of(kept_gate, &o.kept[0]);
+  keep_of(kept_up, &o.kept[1]);
+  return forward(tokens, inputs, outputs, X, ldx, gate, ldg, up, ldu, launch, reinterpret_cast<cudaStream_t>(stream));
 }
 
 int sgemm_linear_backward(int64_t tokens, int64_t inputs, int64_t outputs, const void* dY, int64_t lddy, const sgemm_kept_t* X,
@@ -507,10 +581,10 @@ int sgemm_linear_backward(int64_t tokens, int64_t inputs, int64_t outputs, const
   g.guard = {dev.fault, dev.bounds};
   g.row_blocks = linear_grad_row_blocks(tokens, (int)outputs, dev.sm_count);
   // dA: dY itself where it can be read as it is and there is no activation
-  Operand d_n(dY, lddy, nullptr, 0, tokens, outputs, 0);
-  const bool write = products && (act || d_n.copied);
-  Operand w(W, ldw, nullptr, 0, outputs, inputs, 1);
-  Operand x(X ? X->data : nullptr, X ? X->ld : 1, X ? X->scale : nullptr, X ? X->lds : 1, tokens, inputs, 1);
+  Operand d(dY, lddy, nullptr, 0, tokens, outputs);
+  const bool write = products && (act || d.copied);
+  Operand w(W, ldw, nullptr, 0, outputs, inputs);
+  Operand x(X ? X->data : nullptr, X ? X->ld : 1, X ? X->scale : nullptr, X ? X->lds : 1, tokens, inputs);
   const int64_t ldd = round8(outputs);
   return with_workspace(
       dev, stream,
@@ -525,34 +599,12 @@ int sgemm_linear_backward(int64_t tokens, int64_t inputs, int64_t outputs, const
         if (write || dbias) *e = launch_linear_grad(g, stream);
         if (*e == cudaSuccess && dX) *e = w.make(g.guard, stream);
         if (*e == cudaSuccess && dW) *e = x.make(g.guard, stream);
-        if (write) d_n = Operand(g.da, ldd, nullptr, 0, tokens, outputs, 0);
-        int st = SGEMM_OK;
-        if (*e == cudaSuccess && dX) {  // tokens x inputs over outputs
-          Product pr;
-          pr.shape.M = tokens;
-          pr.shape.N = inputs;
-          pr.shape.K = outputs;
-          pr.a[0] = &d_n;
-          pr.b[0] = &w;
-          pr.out.d[0] = dX;
-          pr.out.ldd[0] = lddx;
-          st = run_product(pr, dev, stream, e);
-        }
-        if (*e == cudaSuccess && st == SGEMM_OK && dW) {  // outputs x inputs over tokens
-          Operand d_t = d_n;
-          d_t.mn = 1;
-          Product pr;
-          pr.shape.M = outputs;
-          pr.shape.N = inputs;
-          pr.shape.K = tokens;
-          pr.a[0] = &d_t;
-          pr.b[0] = &x;
-          pr.out.d[0] = dW;
-          pr.out.ldd[0] = lddw;
-          pr.out.f32 = dw_type == SGEMM_F32;
-          st = run_product(pr, dev, stream, e);
-        }
-        return st;
+        if (*e != cudaSuccess) return (int)SGEMM_OK;
+        if (write) d = Operand(g.da, ldd, nullptr, 0, tokens, outputs);
+        Launch launch;
+        if (dX) launch.add() = input_gradient(tokens, inputs, outputs, &d, nullptr, &w, nullptr, dX, lddx);
+        if (dW) launch.add() = weight_gradient(tokens, inputs, outputs, &d, &x, dW, lddw, dw_type);
+        return launch.n ? launch.run(dev, stream, e) : (int)SGEMM_OK;
       });
 }
 
@@ -614,8 +666,8 @@ int sgemm_gated_backward(int64_t tokens, int64_t inputs, int64_t outputs, const 
   g.h_vec = rows_at(H, ldh, 2, 16);
   g.guard = {dev.fault, dev.bounds};
   g.row_blocks = linear_grad_row_blocks(tokens, (int)outputs, dev.sm_count);
-  Operand wg(gate, ldg, nullptr, 0, outputs, inputs, 1), wu(up, ldu, nullptr, 0, outputs, inputs, 1);
-  Operand x(X ? X->data : nullptr, X ? X->ld : 1, X ? X->scale : nullptr, X ? X->lds : 1, tokens, inputs, 1);
+  Operand wg(gate, ldg, nullptr, 0, outputs, inputs), wu(up, ldu, nullptr, 0, outputs, inputs);
+  Operand x(X ? X->data : nullptr, X ? X->ld : 1, X ? X->scale : nullptr, X ? X->lds : 1, tokens, inputs);
   const int64_t ldd = round8(outputs);
   return with_workspace(
       dev, stream,
@@ -634,40 +686,13 @@ int sgemm_gated_backward(int64_t tokens, int64_t inputs, int64_t outputs, const 
         if (*e == cudaSuccess && dX) *e = wg.make(g.guard, stream);
         if (*e == cudaSuccess && dX) *e = wu.make(g.guard, stream);
         if (*e == cudaSuccess && dG) *e = x.make(g.guard, stream);
-        Operand da(g.da, ldd, nullptr, 0, tokens, outputs, 0), db(g.db, ldd, nullptr, 0, tokens, outputs, 0);
-        int st = SGEMM_OK;
-        if (*e == cudaSuccess && dX) {  // tokens x inputs, two sums over outputs
-          Product pr;
-          pr.shape.M = tokens;
-          pr.shape.N = inputs;
-          pr.shape.K = outputs;
-          pr.shape.segments = 2;
-          pr.a[0] = &da;
-          pr.a[1] = &db;
-          pr.b[0] = &wg;
-          pr.b[1] = &wu;
-          pr.out.d[0] = dX;
-          pr.out.ldd[0] = lddx;
-          st = run_product(pr, dev, stream, e);
-        }
-        if (*e == cudaSuccess && st == SGEMM_OK && dG) {  // twice outputs x inputs over tokens
-          da.mn = db.mn = 1;
-          Product pr;
-          pr.shape.M = outputs;
-          pr.shape.N = inputs;
-          pr.shape.K = tokens;
-          pr.shape.products = 2;
-          pr.a[0] = &da;
-          pr.a[1] = &db;
-          pr.b[0] = &x;
-          pr.out.d[0] = dG;
-          pr.out.ldd[0] = lddg;
-          pr.out.d[1] = dU;
-          pr.out.ldd[1] = lddu;
-          pr.out.f32 = dw_type == SGEMM_F32;
-          st = run_product(pr, dev, stream, e);
-        }
-        return st;
+        if (*e != cudaSuccess) return (int)SGEMM_OK;
+        Operand da(g.da, ldd, nullptr, 0, tokens, outputs), db(g.db, ldd, nullptr, 0, tokens, outputs);
+        Launch launch;
+        if (dX) launch.add() = input_gradient(tokens, inputs, outputs, &da, &db, &wg, &wu, dX, lddx);
+        if (dG) launch.add() = weight_gradient(tokens, inputs, outputs, &da, &x, dG, lddg, dw_type);
+        if (dG) launch.add() = weight_gradient(tokens, inputs, outputs, &db, &x, dU, lddu, dw_type);
+        return launch.n ? launch.run(dev, stream, e) : (int)SGEMM_OK;
       });
 }
 
@@ -690,7 +715,24 @@ int sgemm_linear_plan(int64_t rows, int64_t cols, int64_t K, int gated, int kept
   s.K = K;
   s.gated = gated != 0;
   s.kept8 = kept8 != 0;
-  return plan_shape(s, false, dev.sm_count, dev.pair_clusters, plan);
+  const Choice c = choose(&s, 1, dev.sm_count, dev.pair_clusters);
+  if (c.variant == 0) return SGEMM_ERR_UNSUPPORTED;
+  const bool pair = c.variant == SGEMM_VARIANT_LINEAR_PAIR;
+  *plan = sgemm_plan_t{};
+  plan->variant = c.variant;
+  plan->tile_m = pair ? 256 : 128;
+  plan->tile_n = c.tile;
+  plan->tile_k = 64;
+  plan->stages = pair ? linear_pair_stages(c.tile) : short_stages(c.tile, s.gated, false);
+  plan->threads = pair ? kLinearPairThreads : kLinearShortThreads;
+  plan->split_k = c.split;
+  plan->kernel_launches = 1;
+  plan->dp_tiles = pair ? s.pair_tiles(c.tile) : ceil_div(cols, 128) * ceil_div(rows, c.tile);
+  const int64_t clusters = dev.pair_clusters >= 0 ? dev.pair_clusters : std::max(1, dev.sm_count / 2);
+  plan->grid_x = pair ? 2 * std::min(plan->dp_tiles, clusters) : plan->dp_tiles * c.split;
+  plan->grid_y = 1;
+  plan->smem_bytes = pair ? linear_pair_smem(c.tile) : linear_short_smem(c.tile, s.gated, plan->stages, (int)short_stage(c.tile, s.gated, false));
+  return SGEMM_OK;
 }
 
 int sgemm_linear_set_override(int variant, int tile_n, int split) {

@@ -116,12 +116,13 @@ __global__ void __launch_bounds__(kThreads) linear_grad_kernel(const LinearGradP
           b[GATED ? k : 0].get(u);
           with_act(p.act, [&](auto act) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              float f, df;
-              act_grad<decltype(act)::value>(x[e], f, df);
-              d[e] = g[e] * u[e] * df;
-              du[e] = g[e] * f;
-              h[e] = f * u[e];
+            for (int e = 0; e < 8; e += 2) {
+              const float2 ge = make_float2(g[e], g[e + 1]), ue = make_float2(u[e], u[e + 1]);
+              float2 f, df;
+              act_grad<decltype(act)::value>(make_float2(x[e], x[e + 1]), f, df);
+              *reinterpret_cast<float2*>(&d[e]) = mul(mul(ge, ue), df);
+              *reinterpret_cast<float2*>(&du[e]) = mul(ge, f);
+              *reinterpret_cast<float2*>(&h[e]) = mul(f, ue);
             }
           });
           if (p.da) {
@@ -134,10 +135,10 @@ __global__ void __launch_bounds__(kThreads) linear_grad_kernel(const LinearGradP
             a[k].get(x);
             with_act(p.act, [&](auto act) {
 #pragma unroll
-              for (int e = 0; e < 8; ++e) {
-                float f, df;
-                act_grad<decltype(act)::value>(x[e], f, df);
-                d[e] = g[e] * df;
+              for (int e = 0; e < 8; e += 2) {
+                float2 f, df;
+                act_grad<decltype(act)::value>(make_float2(x[e], x[e + 1]), f, df);
+                *reinterpret_cast<float2*>(&d[e]) = mul(make_float2(g[e], g[e + 1]), df);
               }
             });
           } else {

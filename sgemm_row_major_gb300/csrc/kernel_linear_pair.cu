@@ -1,19 +1,25 @@
 // kernel_linear_pair.cu -- products of BF16 matrices on CTA pairs for sm_103a, with what a layer does to the sums.
 //
 //     linear:        Y = act(X W^T + bias) + R          gated:  H = act(X G^T) * (X U^T)
-//     gradients:     D = A0 B0 (+ A1 B1)                two products that share B: D0 = A0 B, D1 = A1 B
+//     gradients:     D = A0 B0 (+ A1 B1)
+//
+// Up to three such products (jobs) run in one launch, their tiles one behind the other: a backward pass's products together
+// fill the rounds of tiles better than each alone.
 //
 // Clusters of two CTAs on one TPC compute 256 x TN tiles (TN 64, 128 or 256) with tcgen05.mma.cta_group::2.kind::f16,
 // M = 256, N = TN, K = 16, both operands from shared memory: each CTA holds 128 rows of A and half of the tile's columns of
 // B.  A gated tile has TN / 2 columns of each product: the even CTA's half of B is gate's rows, the odd one's up's, so every
-// thread that reads the accumulator finds both products of an element in its own lane.  Sums of 512 k (kFold) leave the
-// tensor memory for FP32 registers, as the tensor cores' own accumulation drifts; the last ones are added back there, and the
-// epilogue runs over the accumulator 32 columns at a time while the next tile's products fill the other one.
+// thread that reads the accumulator finds both products of an element in its own lane.  The epilogue runs over an accumulator
+// 32 columns at a time while the next tile's products fill the other one.  The tensor cores' own accumulation is not
+// round-to-nearest and drifts by about 1.2e-8 of the sum per instruction of 16 k.  Where FP32 values leave the kernel (an FP32
+// output, the scales of 8-bit values) only `fold` K tiles are summed in one accumulator, and these sums in FP32 registers;
+// BF16 outputs take whole sums from the tensor memory (1e-5 off at 16384 terms, where their own rounding is 2e-3), which
+// leaves the next tile's products a whole tile's time to overlap with the epilogue.
 //
 // Either operand may be stored along K or across it: the tensor core reads both orders, so a gradient's product takes the
 // weights and activations as the forward pass left them.
 //
-// Warp 0 loads (TMA, 5 stages of 32 KB), warp 1 of the even CTA issues the products, warps 4-11 fold and write.  Persistent
+// Warp 0 loads (TMA, 5 stages of 32 KB or 8 of 24), warp 1 of the even CTA issues the products, warps 4-11 fold and write.  Persistent
 // clusters take tiles round robin in an order that keeps 8 rows of tiles together (their A and B panels stay in L2).
 #include "linear_common.cuh"
 
@@ -24,10 +30,7 @@ namespace {
 using namespace tc;
 
 constexpr int BM = 256, BMC = 128, BK = 64;
-constexpr int kPart = 128 * BK * 2;       // 16 KB: one operand's tile in one CTA
-constexpr int kStageBytes = 2 * kPart;
-constexpr int kStages = kLinearPairStages;
-constexpr int kOutBytes = 8 * 1024;       // of shared memory per folding warp: 4 pieces of 32 x 32 BF16, or 2 of FP32
+constexpr int kPart = 128 * BK * 2;       // 16 KB: A's tile in one CTA
 constexpr int kFirstFold = 4;             // warps 0 and 1: loads, products
 constexpr int kFoldWarps = 8;
 constexpr int kThreads = 32 * (kFirstFold + kFoldWarps);
@@ -38,8 +41,17 @@ constexpr int kMoverRegs = 40, kFoldRegs = 232;
 static_assert(128 * kMoverRegs + 32 * kFoldWarps * kFoldRegs <= kThreads * 168, "registers at launch");
 constexpr int kMaxBufs = 4;
 constexpr uint32_t kTmemCols = 512;
-constexpr int kSmem = kStages * kStageBytes + kFoldWarps * kOutBytes + 1024;
-static_assert(kSmem + 1024 + 256 <= 232448, "shared memory per CTA");
+
+// Shared memory by the tile's width: narrow tiles take less of it per K tile and as long to arrive, so they get more stages.
+template <int TN>
+struct Ring {
+  static constexpr int kPartB = TN == 256 ? kPart : kPart / 2;  // (64 columns across K are copied as a block of 64)
+  static constexpr int kStageBytes = kPart + kPartB;
+  static constexpr int kStages = TN == 256 ? 5 : 8;
+  static constexpr int kOutBytes = TN == 256 ? 8 * 1024 : 4 * 1024;  // per folding warp: pieces of 2 KB (BF16) or 4 KB (FP32)
+  static constexpr int kSmem = kStages * kStageBytes + kFoldWarps * kOutBytes + 1024;
+  static_assert(kSmem + 1536 <= 232448, "shared memory per CTA");
+};
 
 __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* map, uint32_t bar_cluster, int32_t inner, int32_t outer) {
   asm volatile(
@@ -49,43 +61,38 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-// 128 (64, 32) output rows of an operand from row mn0 on and 64 k from k0 on.
-__device__ __forceinline__ void load_part(uint32_t dst, const CUtensorMap* map, uint32_t bar, bool mn_major, int mn0, int k0, int rows) {
-  if (mn_major) {
-    tma_load_pair(dst, map, bar, mn0, k0);
-    if (rows > 64) tma_load_pair(dst + kBlockBytes, map, bar, mn0 + 64, k0);
-  } else {
-    tma_load_pair(dst, map, bar, k0, mn0);
-  }
-}
-// Bytes that it loads.
-__host__ __device__ constexpr uint32_t part_bytes(bool mn_major, int rows) {
-  return mn_major ? (rows > 64 ? 2u : 1u) * kBlockBytes : (uint32_t)rows * BK * 2;
-}
-
 // A folding warp's pieces of an output, 32 rows x 32 columns each: written to shared memory in the output's type, in rows of
 // 64 (BF16) or 128 bytes with the swizzle of that width, then by TMA, or by the lanes where TMA cannot (rows that are not
 // aligned or end inside 16 bytes).
+template <int BYTES>
 struct Pieces {
   uint8_t* buf;
   int at;     // the next piece's place
   bool wide;  // places of 4 KB (an FP32 output), else of 2 KB
+  __device__ __forceinline__ void set(bool f32) {
+    if (f32 == wide) return;
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+    __syncwarp();
+    wide = f32;
+    at = 0;
+  }
   __device__ __forceinline__ uint8_t* next() {
+    constexpr int kNarrow = BYTES / 2048, kWide = BYTES / 4096;
     uint8_t* p = buf + at * (wide ? 4096 : 2048);
-    at = (at + 1) & (wide ? 1 : 3);
+    at = (at + 1) & (wide ? kWide - 1 : kNarrow - 1);
     // the copy that read this place before is done reading
     if ((threadIdx.x & 31) == 0) {
-      if (wide) asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-      else      asm volatile("cp.async.bulk.wait_group.read 3;" ::: "memory");
+      if (wide) asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kWide - 1) : "memory");
+      else      asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(kNarrow - 1) : "memory");
     }
     __syncwarp();
     return p;
   }
 };
 
-template <bool F32>
-__device__ __forceinline__ void emit(Pieces& pieces, const CUtensorMap* map, bool tma, void* base, int64_t ld, const LinearOut& o,
-                                     unsigned site, int row0, int col0, const float (&v)[32]) {
+template <bool F32, int BYTES>
+__device__ __forceinline__ void emit(Pieces<BYTES>& pieces, const CUtensorMap* map, bool tma, void* base, int64_t ld, const LinearOut& o,
+                                     const LinearJob& j, unsigned site, int row0, int col0, const float (&v)[32]) {
   const int lane = threadIdx.x & 31;
   uint8_t* at = pieces.next();
   if constexpr (F32) {
@@ -103,7 +110,7 @@ __device__ __forceinline__ void emit(Pieces& pieces, const CUtensorMap* map, boo
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
-      if (row0 < o.M && col0 < o.N)
+      if (row0 < j.M && col0 < j.N)
         asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
                          reinterpret_cast<uint64_t>(map)),
                      "r"(smem_addr(at)), "r"(col0), "r"(row0), "r"(0)
@@ -111,9 +118,9 @@ __device__ __forceinline__ void emit(Pieces& pieces, const CUtensorMap* map, boo
     }
   } else {
     __syncwarp();
-    const int rows = min(32, o.M - row0);
-    if (col0 + lane < o.N && rows > 0 &&
-        in_range(o.guard.fault, o.guard.word, site, (int64_t)row0 * ld + col0 + lane, (rows - 1) * ld + 1, extent(o.M, ld, o.N))) {
+    const int rows = min(32, j.M - row0);
+    if (col0 + lane < j.N && rows > 0 &&
+        in_range(o.guard.fault, o.guard.word, site, (int64_t)row0 * ld + col0 + lane, (rows - 1) * ld + 1, extent(j.M, ld, j.N))) {
       const int64_t first = (int64_t)row0 * ld + col0 + lane;
       if constexpr (F32) {
         float* d = static_cast<float*>(base) + first;
@@ -132,37 +139,46 @@ __device__ __forceinline__ void emit(Pieces& pieces, const CUtensorMap* map, boo
   __syncwarp();
 }
 
-// bias[col0 ..] is added to 32 sums.
-__device__ __forceinline__ void add_bias(const LinearOut& o, int col0, float (&v)[32]) {
+template <int N>
+__device__ __forceinline__ void add_to(float* v, const float* x) {
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    const float2 s = add(make_float2(v[k], v[k + 1]), make_float2(x[k], x[k + 1]));
+    v[k] = s.x;
+    v[k + 1] = s.y;
+  }
+}
+
+// bias[col0 ..] is added to 32 sums of N.
+__device__ __forceinline__ void add_bias(const LinearOut& o, int N, int col0, float (&v)[32]) {
   const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(o.bias);
-  if (o.bias_vec && col0 + 32 <= o.N) {
-    if (!in_range(o.guard.fault, o.guard.word, f8::kSiteIn, col0, 32, o.N)) return;
+  if (o.bias_vec && col0 + 32 <= N) {
+    if (!in_range(o.guard.fault, o.guard.word, f8::kSiteIn, col0, 32, N)) return;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       Chunk<__nv_bfloat16> c;
       float x[8];
       c.raw = __ldg(reinterpret_cast<const uint4*>(b + col0) + e);
       c.get(x);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[8 * e + k] += x[k];
+      add_to<8>(&v[8 * e], x);
     }
     return;
   }
 #pragma unroll
   for (int e = 0; e < 32; ++e)
-    if (col0 + e < o.N) v[e] += __bfloat162float(get_at(o.guard, f8::kSiteIn, b, col0 + e, o.N));
+    if (col0 + e < N) v[e] += __bfloat162float(get_at(o.guard, f8::kSiteIn, b, col0 + e, N));
 }
 
 // The residual's 32 values of one row, sent for before the sums are waited for.
 template <bool VEC>
 struct Residual {
   f8::Loading<__nv_bfloat16, VEC> c[4];
-  __device__ __forceinline__ void load(const LinearOut& o, int row, int col0) {
-    const f8::Rows<__nv_bfloat16> m(o.residual, o.M, o.ldr, o.N, o.guard);
+  __device__ __forceinline__ void load(const LinearOut& o, const LinearJob& j, int row, int col0) {
+    const f8::Rows<__nv_bfloat16> m(o.residual, j.M, o.ldr, j.N, o.guard);
     const __nv_bfloat16* p = m.base + (int64_t)row * o.ldr + col0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int n = row < o.M ? max(0, min(8, o.N - col0 - 8 * e)) : 0;
+      const int n = row < j.M ? max(0, min(8, j.N - col0 - 8 * e)) : 0;
       c[e].load(p + 8 * e, VEC && n < 8 ? 0 : n, m);
     }
   }
@@ -171,22 +187,24 @@ struct Residual {
     for (int e = 0; e < 4; ++e) {
       float x[8];
       c[e].get().get(x);
-#pragma unroll
-      for (int k = 0; k < 8; ++k) v[8 * e + k] += x[k];
+      add_to<8>(&v[8 * e], x);
     }
   }
 };
 
-// 32 codes of one row.
-__device__ __forceinline__ void put_codes(const LinearOut& o, int which, int row, int col0, const float (&v)[32], float inv) {
-  if (row >= o.M || col0 >= o.N) return;
+// 32 codes of one row.  CHECK: some value may be infinite.
+template <bool CHECK>
+__device__ __forceinline__ void put_codes(const LinearOut& o, const LinearJob& j, int which, int row, int col0, const float (&v)[32], float inv) {
   const LinearKept& k = o.kept[which];
   uint32_t u[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e)
-    u[e] = f8::codes2<true>(v[4 * e] * inv, v[4 * e + 1] * inv, false) | (f8::codes2<true>(v[4 * e + 2] * inv, v[4 * e + 3] * inv, false) << 16);
-  const int n = min(32, o.N - col0);
-  if (!kept_ok(o, which, row, col0, n)) return;
+  for (int e = 0; e < 8; ++e) {
+    const float2 a = mul(make_float2(v[4 * e], v[4 * e + 1]), both(inv)), b = mul(make_float2(v[4 * e + 2], v[4 * e + 3]), both(inv));
+    u[e] = f8::codes2<CHECK>(a.x, a.y, false) | (f8::codes2<CHECK>(b.x, b.y, false) << 16);
+  }
+  if (row >= j.M || col0 >= j.N) return;
+  const int n = min(32, j.N - col0);
+  if (!kept_ok(o, j, which, row, col0, n)) return;
   uint8_t* d = static_cast<uint8_t*>(k.data) + (int64_t)row * k.ld + col0;
   if (k.vec && n == 32) {
     reinterpret_cast<uint4*>(d)[0] = make_uint4(u[0], u[1], u[2], u[3]);
@@ -198,6 +216,23 @@ __device__ __forceinline__ void put_codes(const LinearOut& o, int which, int row
   }
 }
 
+// The largest finite |v| so far (a NaN is never the larger one; infinities are looked for only where there are some).
+__device__ __forceinline__ float largest_of(float m, const float (&v)[32]) {
+  float x = 0.0f, y = 0.0f;
+#pragma unroll
+  for (int k = 0; k < 32; k += 2) {
+    x = fmaxf(x, fabsf(v[k]));
+    y = fmaxf(y, fabsf(v[k + 1]));
+  }
+  x = fmaxf(x, y);
+  if (x > f8::kMaxFloat) {
+    x = 0.0f;
+#pragma unroll
+    for (int k = 0; k < 32; ++k) x = fmaxf(x, f8::finite_abs(v[k]));
+  }
+  return fmaxf(m, x);
+}
+
 __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
   const float(&a)[16] = *reinterpret_cast<const float(*)[16]>(&v[0]);
   const float(&b)[16] = *reinterpret_cast<const float(*)[16]>(&v[16]);
@@ -205,11 +240,22 @@ __device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) 
   tmem_st16(taddr + 16u, b);
 }
 
+// The job of a tile and the tile's place in it.
+struct Place {
+  int job, tm, tn;
+  __device__ __forceinline__ Place(const LinearPairParams& p, int tile) : job(0) {
+    while (tile >= p.job[job].tiles_m * p.job[job].tiles_n) tile -= p.job[job].tiles_m * p.job[job].tiles_n, ++job;
+    tile_coords(tile, p.job[job].tiles_m, p.job[job].tiles_n, tm, tn);
+  }
+};
+
 // TN: the accumulator's columns.  GATED: half of them are gate's, half up's.
 template <int TN, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearPairParams p) {
   extern __shared__ uint8_t smem_raw[];
+  using R = Ring<TN>;
+  constexpr int kStages = R::kStages, kStageBytes = R::kStageBytes;
   constexpr int halfn = TN / 2;   // columns of B this CTA loads
   constexpr int TD = GATED ? TN / 2 : TN;  // the tile's columns of D
   constexpr int bufs = (int)kTmemCols / TN < kMaxBufs ? (int)kTmemCols / TN : kMaxBufs;
@@ -227,10 +273,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint32_t rank = cluster_rank();
   const int cl = (int)cluster_id_x();
-  const int kt = p.k_tiles * p.segments;
-  const int chunks = (kt + kFold - 1) / kFold;
-  const int product_tiles = p.tiles_m * p.tiles_n, tiles = product_tiles * p.products;
-  const int my_tiles = cl < tiles ? (tiles - cl + p.clusters - 1) / p.clusters : 0;
+  int tiles = 0;
+  for (int n = 0; n < p.jobs; ++n) tiles += p.job[n].tiles_m * p.job[n].tiles_n;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
@@ -262,41 +306,41 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     if (warp == 0) {
       // ------------------------------------------------ loads (each CTA: its rows of A, its columns of B)
       if (lane == 0) {
-        prefetch_tensormap(&maps.a[0]);
-        prefetch_tensormap(&maps.b[GATED ? rank : 0]);
+        prefetch_tensormap(&maps.op[p.job[0].a[0]]);
+        prefetch_tensormap(&maps.op[p.job[0].b[GATED ? rank : 0]]);
       }
       __syncwarp();
-      const uint32_t bytes = 2u * (part_bytes(p.a_mn, BMC) + part_bytes(p.b_mn, halfn));  // both CTAs'
       const uint32_t full0 = map_to_rank(smem_addr(&full[0]), 0);
       int t = 0, s = 0;
       uint32_t lap = 0;
       bool ok = true;
-      for (int i = 0; ok && i < my_tiles; ++i) {
-        const int tile = cl + i * p.clusters, product = tile >= product_tiles;
-        int tm, tn;
-        tile_coords(tile - product * product_tiles, p.tiles_m, p.tiles_n, tm, tn);
-        const int m0 = tm * BM + BMC * (int)rank, n0 = GATED ? tn * TD : tn * TN + halfn * (int)rank;
-        for (int g = 0, k = 0, segment = 0; g < kt; ++g, ++t, ++k) {
-          if (k == p.k_tiles) {
-            k = 0;
-            segment = 1;
-          }
-          if (lap > 0 && !poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
-            if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
-            ok = false;
-            break;
-          }
-          if (elect_one()) {
-            // both CTAs' loads complete on the even CTA's barrier, which expects all their bytes
-            const uint32_t fb = full0 + 8u * (uint32_t)s;
-            if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), bytes);
-            const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
-            load_part(a, &maps.a[segment | product], fb, p.a_mn, m0, k * BK, BMC);
-            load_part(a + kPart, &maps.b[GATED ? (int)rank : segment], fb, p.b_mn, n0, k * BK, halfn);
-          }
-          if (++s == kStages) {
-            s = 0;
-            ++lap;
+      for (int tile = cl; ok && tile < tiles; tile += p.clusters) {
+        const Place at(p, tile);
+        const LinearJob& j = p.job[at.job];
+        const uint32_t bytes = 2u * (part_bytes(j.a_mn, BMC) + part_bytes(j.b_mn, halfn));  // both CTAs'
+        const int m0 = at.tm * BM + BMC * (int)rank, n0 = GATED ? at.tn * TD : at.tn * TN + halfn * (int)rank;
+        const int a_mn = j.a_mn, b_mn = j.b_mn, kt = j.k_tiles;
+        for (int segment = 0; ok && segment < j.segments; ++segment) {
+          const CUtensorMap *ma = &maps.op[j.a[segment]], *mb = &maps.op[j.b[GATED ? (int)rank : segment]];
+          for (int k = 0; k < kt; ++k, ++t) {
+            if (lap > 0 && !poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
+              if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+              ok = false;
+              break;
+            }
+            if (elect_one()) {
+              // both CTAs' loads complete on the even CTA's barrier, which expects all their bytes
+              const uint32_t fb = full0 + 8u * (uint32_t)s;
+              if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), bytes);
+              const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
+              const auto load = [&](uint32_t dst, const CUtensorMap* map, int inner, int outer) { tma_load_pair(dst, map, fb, inner, outer); };
+              load_part(load, a, ma, a_mn, m0, k * BK, BMC);
+              load_part(load, a + kPart, mb, b_mn, n0, k * BK, halfn);
+            }
+            if (++s == kStages) {
+              s = 0;
+              ++lap;
+            }
           }
         }
       }
@@ -308,45 +352,50 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             atomicOr(p.fault, (unsigned)kFaultDrainWait);
     } else if (warp == 1) {
       int t = 0;  // K tiles whose products have been issued (odd CTA: will be)
-      const int units = my_tiles * kt;
       if (rank != 0) {
-        t = units;
+        for (int tile = cl; tile < tiles; tile += p.clusters) {
+          const LinearJob& j = p.job[Place(p, tile).job];
+          t += j.k_tiles * j.segments;
+        }
       } else {
         // ---------------------------------------------- products (even CTA)
-        const uint32_t astep = step_of(p.a_mn), bstep = step_of(p.b_mn);
         const uint32_t desc0 = desc_lo(sbase);
-        int s = 0, b = 0, g = 0;
+        int s = 0, b = 0;
         uint32_t s_lap = 0, b_lap = 0;
         bool ok = true;
-        while (ok && t < units) {
-          // a chunk: the K tiles of one accumulator
-          const int n = min(kFold, kt - g);
-          ok = b_lap == 0 || poll_wait(smem_addr(&acc_empty[b]), (b_lap - 1) & 1u, p.timeout_ns);
-          tmem_fence_after_sync();
-          for (int j = 0; ok && j < n; ++j) {
-            ok = poll_wait(smem_addr(&full[s]), s_lap & 1u, p.timeout_ns);
-            if (!ok) break;
+        for (int tile = cl; ok && tile < tiles; tile += p.clusters) {
+          const LinearJob& j = p.job[Place(p, tile).job];
+          const uint32_t astep = step_of(j.a_mn), bstep = step_of(j.b_mn), idesc = j.idesc;
+          const int kt = j.k_tiles * j.segments, fold = j.fold;
+          for (int g = 0; ok && g < kt; g += fold) {
+            // a chunk: the K tiles of one accumulator
+            const int n = min(fold, kt - g);
+            ok = b_lap == 0 || poll_wait(smem_addr(&acc_empty[b]), (b_lap - 1) & 1u, p.timeout_ns);
             tmem_fence_after_sync();
-            if (elect_one()) {
-              const uint32_t acc = tmem + (uint32_t)(b * TN);
-              const uint32_t ad = desc0 + (uint32_t)(s * (kStageBytes >> 4)), bd = ad + (kPart >> 4);
+            for (int i = 0; ok && i < n; ++i) {
+              ok = poll_wait(smem_addr(&full[s]), s_lap & 1u, p.timeout_ns);
+              if (!ok) break;
+              tmem_fence_after_sync();
+              if (elect_one()) {
+                const uint32_t acc = tmem + (uint32_t)(b * TN);
+                const uint32_t ad = desc0 + (uint32_t)(s * (kStageBytes >> 4)), bd = ad + (kPart >> 4);
 #pragma unroll
-              for (uint32_t ks = 0; ks < BK / 16; ++ks)
-                mma_bf16_pair(acc, make_desc(ad + ks * astep), make_desc(bd + ks * bstep), p.idesc, j == 0 && ks == 0 ? 0u : 1u);
-              mma_commit_pair(smem_addr(&done[s]));  // in both CTAs: stage s is free
-              if (j == n - 1) mma_commit_pair(smem_addr(&acc_full[b]));
+                for (uint32_t ks = 0; ks < BK / 16; ++ks)
+                  mma_bf16_pair(acc, make_desc(ad + ks * astep), make_desc(bd + ks * bstep), idesc, i == 0 && ks == 0 ? 0u : 1u);
+                mma_commit_pair(smem_addr(&done[s]));  // in both CTAs: stage s is free
+                if (i == n - 1) mma_commit_pair(smem_addr(&acc_full[b]));
+              }
+              __syncwarp();
+              ++t;
+              if (++s == kStages) {
+                s = 0;
+                ++s_lap;
+              }
             }
-            __syncwarp();
-            ++t;
-            if (++s == kStages) {
-              s = 0;
-              ++s_lap;
+            if (++b == bufs) {
+              b = 0;
+              ++b_lap;
             }
-          }
-          g = g + n == kt ? 0 : g + n;
-          if (++b == bufs) {
-            b = 0;
-            ++b_lap;
           }
         }
         if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
@@ -369,33 +418,40 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     const uint32_t tq = tmem + ((uint32_t)(32 * q) << 16) + (uint32_t)(cols * part);
     // the accumulator column of load e: gated, the first half of the loads are gate's columns, the others up's
     const auto column = [](int e) { return GATED && e >= loads / 2 ? TN / 2 + 32 * (e - loads / 2) : 32 * e; };
-    Pieces pieces{smem_raw + pad + kStages * kStageBytes + (warp - kFirstFold) * kOutBytes, 0, o.f32 != 0};
+    Pieces<R::kOutBytes> pieces{smem_raw + pad + kStages * kStageBytes + (warp - kFirstFold) * R::kOutBytes, 0, false};
     float sum[TN / 2];
     bool ok = true;
     int b = 0;
-    uint32_t b_lap = 0;
-    for (int i = 0; ok && i < my_tiles; ++i) {
-      const int tile = cl + i * p.clusters, product = tile >= product_tiles;
-      int tm, tn;
-      tile_coords(tile - product * product_tiles, p.tiles_m, p.tiles_n, tm, tn);
-      const int row0 = tm * BM + BMC * (int)rank + 32 * q, row = row0 + lane;
-      const int c0 = tn * TD + cols * part;  // this thread's first column of D
-#pragma unroll
-      for (int e = 0; e < TN / 2; ++e) sum[e] = 0.0f;
-      for (int ch = 0; ch < chunks; ++ch) {
+    uint32_t b_lap = 0, asked = 0;  // tiles whose largest values have been exchanged
+    for (int tile = cl; ok && tile < tiles; tile += p.clusters) {
+      const Place at(p, tile);
+      const LinearJob& j = p.job[at.job];
+      const int row0 = at.tm * BM + BMC * (int)rank + 32 * q, row = row0 + lane;
+      const int c0 = at.tn * TD + cols * part;  // this thread's first column of D
+      const int kt = j.k_tiles * j.segments, fold = j.fold;
+      uint32_t acc;
+      const auto next = [&] {  // waits for the next accumulator
         ok = poll_wait(smem_addr(&acc_full[b]), b_lap & 1u, p.timeout_ns);
-        if (!ok) {
-          if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
-          break;
-        }
+        if (!ok && lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
         tmem_fence_after_sync();
-        const uint32_t acc = tq + (uint32_t)(b * TN);
-        const auto release = [&] {  // the accumulator has been read: hand it back to the issuer
-          tmem_fence_before_sync();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_remote(smem_addr(&acc_empty[b]), 0);
-        };
-        if (ch < chunks - 1) {
+        acc = tq + (uint32_t)(b * TN);
+        return ok;
+      };
+      const auto release = [&] {  // the accumulator has been read: hand it back to the issuer
+        tmem_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_remote(smem_addr(&acc_empty[b]), 0);
+        if (++b == bufs) {
+          b = 0;
+          ++b_lap;
+        }
+      };
+      if (kt > fold) {
+        // several accumulators: all but the last are added in registers, and these sums to the last one where it lies
+#pragma unroll
+        for (int e = 0; e < TN / 2; ++e) sum[e] = 0.0f;
+        for (int g = 0; g + fold < kt; g += fold) {
+          if (!next()) break;
 #pragma unroll
           for (int e = 0; e < loads; ++e) {
             float v[32];
@@ -403,128 +459,136 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             tmem_wait_ld();
             if (e == loads - 1) release();
             tmem_ld_ready(v);
-#pragma unroll
-            for (int k = 0; k < 32; ++k) sum[32 * e + k] += v[k];
-          }
-        } else {
-          if (chunks > 1) {
-#pragma unroll
-            for (int e = 0; e < loads; ++e) {
-              float v[32];
-              tmem_ld32(acc + (uint32_t)column(e), v);
-              tmem_wait_ld();
-              tmem_ld_ready(v);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) v[k] += sum[32 * e + k];
-              tmem_st32(acc + (uint32_t)column(e), v);
-            }
-            tmem_wait_st();
-          }
-          // -------------------------------------------- epilogue
-          constexpr uint32_t up = TN / 2;  // gated: from a column of gate to up's
-          float scale[2] = {1.0f, 1.0f};
-          if (o.keep == 2) {
-            float m[2] = {0.0f, 0.0f};
-#pragma unroll 1
-            for (int c = 0; c < cols; c += 32) {
-              float v[32];
-              tmem_ld32(acc + (uint32_t)c, v);
-              tmem_wait_ld();
-              tmem_ld_ready(v);
-              if (!GATED && o.bias) add_bias(o, c0 + c, v);
-#pragma unroll
-              for (int k = 0; k < 32; ++k) m[0] = fmaxf(m[0], f8::finite_abs(v[k]));
-              if constexpr (GATED) {
-                tmem_ld32(acc + up + (uint32_t)c, v);
-                tmem_wait_ld();
-                tmem_ld_ready(v);
-#pragma unroll
-                for (int k = 0; k < 32; ++k) m[1] = fmaxf(m[1], f8::finite_abs(v[k]));
-              }
-            }
-            if (cols < 128) {  // the other half of the group is with the warp of the other column half
-              float* at = &largest[0][32 * q + lane];
-              constexpr int kUp = GATED ? BMC : 0;
-              if (part == 1) {
-                at[0] = m[0];
-                if (GATED) at[kUp] = m[1];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&max_asked[q]));
-              }
-              ok = poll_wait(smem_addr(part == 1 ? &max_told[q] : &max_asked[q]), (uint32_t)(i & 1), p.timeout_ns);
-              if (!ok) {
-                if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
-                break;
-              }
-              m[0] = fmaxf(m[0], at[0]);
-              if (GATED) m[1] = fmaxf(m[1], at[kUp]);
-              if (part == 0) {
-                at[0] = m[0];
-                if (GATED) at[kUp] = m[1];
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&max_told[q]));
-              }
-            }
-#pragma unroll
-            for (int w = 0; w < (GATED ? 2 : 1); ++w) {
-              scale[w] = f8::group_scale(m[w], kMaxE4M3);
-              if (row < o.M && c0 < o.N && c0 % 128 == 0) put_scale(o, w, row, c0 >> 7, scale[w]);
-              scale[w] = __fdiv_rn(1.0f, scale[w]);
-            }
-          }
-#pragma unroll 1
-          for (int c = 0; c < cols; c += 32) {
-            float v[32];
-            tmem_ld32(acc + (uint32_t)c, v);
-            if constexpr (GATED) {
-              float u[32];
-              tmem_ld32(acc + up + (uint32_t)c, u);
-              tmem_wait_ld();
-              if (c + 32 == cols) release();
-              tmem_ld_ready(v);
-              tmem_ld_ready(u);
-              if (o.keep == 1) {
-                emit<false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, f8::kSiteCodes, row0, c0 + c, v);
-                emit<false>(pieces, &maps.kept[1], o.kept[1].vec, o.kept[1].data, o.kept[1].ld, o, f8::kSiteCodes, row0, c0 + c, u);
-              } else if (o.keep == 2) {
-                put_codes(o, 0, row, c0 + c, v, scale[0]);
-                put_codes(o, 1, row, c0 + c, u, scale[1]);
-              }
-              with_act(o.act, [&](auto act) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = act_of<decltype(act)::value>(v[k]) * u[k];
-              });
-              emit<false>(pieces, &maps.d[0], o.d_tma[0], o.d[0], o.ldd[0], o, f8::kSiteOut, row0, c0 + c, v);
-            } else {
-              Residual<true> ra;
-              Residual<false> rb;
-              if (o.residual) {
-                if (o.r_vec && c0 + c + 32 <= o.N) ra.load(o, row, c0 + c);
-                else                               rb.load(o, row, c0 + c);
-              }
-              tmem_wait_ld();
-              if (c + 32 == cols) release();
-              tmem_ld_ready(v);
-              if (o.bias) add_bias(o, c0 + c, v);
-              if (o.keep == 1) emit<false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, f8::kSiteCodes, row0, c0 + c, v);
-              else if (o.keep == 2) put_codes(o, 0, row, c0 + c, v, scale[0]);
-              with_act(o.act, [&](auto act) {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = act_of<decltype(act)::value>(v[k]);
-              });
-              if (o.residual) {
-                if (o.r_vec && c0 + c + 32 <= o.N) ra.add(v);
-                else                               rb.add(v);
-              }
-              if (o.f32) emit<true>(pieces, &maps.d[product], o.d_tma[product], o.d[product], o.ldd[product], o, f8::kSiteOut, row0, c0 + c, v);
-              else       emit<false>(pieces, &maps.d[product], o.d_tma[product], o.d[product], o.ldd[product], o, f8::kSiteOut, row0, c0 + c, v);
-            }
+            add_to<32>(&sum[32 * e], v);
           }
         }
-        if (!ok) break;
-        if (++b == bufs) {
-          b = 0;
-          ++b_lap;
+        if (!ok || !next()) break;
+#pragma unroll
+        for (int e = 0; e < loads; ++e) {
+          float v[32];
+          tmem_ld32(acc + (uint32_t)column(e), v);
+          tmem_wait_ld();
+          tmem_ld_ready(v);
+          add_to<32>(v, &sum[32 * e]);
+          tmem_st32(acc + (uint32_t)column(e), v);
+        }
+        tmem_wait_st();
+      } else if (!next()) {
+        break;
+      }
+      // ---------------------------------------------- epilogue
+      constexpr uint32_t up = TN / 2;  // gated: from a column of gate to up's
+      pieces.set(j.f32 != 0);
+      float inv[2] = {1.0f, 1.0f};     // of the scales of what is kept in 8 bits
+      bool bias = !GATED && o.bias;    // still to be added
+      if (o.keep == 2) {
+        float m[2] = {0.0f, 0.0f};
+#pragma unroll 1
+        for (int c = 0; c < cols; c += 32) {
+          float v[32];
+          tmem_ld32(acc + (uint32_t)c, v);
+          tmem_wait_ld();
+          tmem_ld_ready(v);
+          if (bias) {
+            add_bias(o, j.N, c0 + c, v);
+            tmem_st32(acc + (uint32_t)c, v);
+          }
+          m[0] = largest_of(m[0], v);
+          if constexpr (GATED) {
+            tmem_ld32(acc + up + (uint32_t)c, v);
+            tmem_wait_ld();
+            tmem_ld_ready(v);
+            m[1] = largest_of(m[1], v);
+          }
+        }
+        if (bias) tmem_wait_st();
+        bias = false;
+        if (cols < 128) {  // the other half of the group is with the warp of the other column half
+          float* slot = &largest[0][32 * q + lane];
+          constexpr int kUp = GATED ? BMC : 0;
+          if (part == 1) {
+            slot[0] = m[0];
+            if (GATED) slot[kUp] = m[1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&max_asked[q]));
+          }
+          ok = poll_wait(smem_addr(part == 1 ? &max_told[q] : &max_asked[q]), asked & 1u, p.timeout_ns);
+          ++asked;
+          if (!ok) {
+            if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+            break;
+          }
+          m[0] = fmaxf(m[0], slot[0]);
+          if (GATED) m[1] = fmaxf(m[1], slot[kUp]);
+          if (part == 0) {
+            slot[0] = m[0];
+            if (GATED) slot[kUp] = m[1];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&max_told[q]));
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < (GATED ? 2 : 1); ++w) {
+          const float scale = f8::group_scale(m[w], kMaxE4M3);
+          if (row < j.M && c0 < j.N && c0 % 128 == 0) put_scale(o, j, w, row, c0 >> 7, scale);
+          inv[w] = __fdiv_rn(1.0f, scale);
+        }
+      }
+#pragma unroll 1
+      for (int c = 0; c < cols; c += 32) {
+        const bool last = c + 32 == cols;
+        float v[32];
+        tmem_ld32(acc + (uint32_t)c, v);
+        if constexpr (GATED) {
+          float u[32];
+          tmem_ld32(acc + up + (uint32_t)c, u);
+          tmem_wait_ld();
+          if (last) release();
+          tmem_ld_ready(v);
+          tmem_ld_ready(u);
+          if (o.keep == 1) {
+            emit<false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
+            emit<false>(pieces, &maps.kept[1], o.kept[1].vec, o.kept[1].data, o.kept[1].ld, o, j, f8::kSiteCodes, row0, c0 + c, u);
+          } else if (o.keep == 2) {
+            put_codes<true>(o, j, 0, row, c0 + c, v, inv[0]);
+            put_codes<true>(o, j, 1, row, c0 + c, u, inv[1]);
+          }
+          with_act(o.act, [&](auto act) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 h = mul(act_of<decltype(act)::value>(make_float2(v[k], v[k + 1])), make_float2(u[k], u[k + 1]));
+              v[k] = h.x;
+              v[k + 1] = h.y;
+            }
+          });
+          emit<false>(pieces, &maps.d[0], j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
+        } else {
+          Residual<true> ra;
+          Residual<false> rb;
+          if (o.residual) {
+            if (o.r_vec && c0 + c + 32 <= j.N) ra.load(o, j, row, c0 + c);
+            else                               rb.load(o, j, row, c0 + c);
+          }
+          tmem_wait_ld();
+          if (last) release();
+          tmem_ld_ready(v);
+          if (bias) add_bias(o, j.N, c0 + c, v);
+          if (o.keep == 1) emit<false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
+          else if (o.keep == 2) put_codes<true>(o, j, 0, row, c0 + c, v, inv[0]);
+          with_act(o.act, [&](auto act) {
+#pragma unroll
+            for (int k = 0; k < 32; k += 2) {
+              const float2 f = act_of<decltype(act)::value>(make_float2(v[k], v[k + 1]));
+              v[k] = f.x;
+              v[k + 1] = f.y;
+            }
+          });
+          if (o.residual) {
+            if (o.r_vec && c0 + c + 32 <= j.N) ra.add(v);
+            else                               rb.add(v);
+          }
+          if (j.f32) emit<true>(pieces, &maps.d[at.job], j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
+          else       emit<false>(pieces, &maps.d[at.job], j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
         }
       }
     }
@@ -559,14 +623,15 @@ cudaError_t with_kernel(int tile_n, bool gated, const F& f) {
 }  // namespace
 }  // namespace lin
 
-int64_t linear_pair_smem() { return lin::kSmem; }
+int linear_pair_stages(int tile_n) { return tile_n == 256 ? lin::Ring<256>::kStages : lin::Ring<128>::kStages; }
+int64_t linear_pair_smem(int tile_n) { return tile_n == 256 ? lin::Ring<256>::kSmem : lin::Ring<128>::kSmem; }
 
 cudaError_t prepare_linear_pair() {
   for (int tile_n : kLinearPairTiles)
     for (int gated = 0; gated < 2; ++gated) {
       if (gated && tile_n == 64) continue;
-      const cudaError_t e = lin::with_kernel(tile_n, gated != 0, [](auto kernel) {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, lin::kSmem);
+      const cudaError_t e = lin::with_kernel(tile_n, gated != 0, [&](auto kernel) {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)linear_pair_smem(tile_n));
       });
       if (e != cudaSuccess) return e;
     }
@@ -577,7 +642,7 @@ cudaError_t launch_linear_pair(int tile_n, bool gated, const LinearMaps& maps, c
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)p.clusters);
   cfg.blockDim = dim3(lin::kThreads);
-  cfg.dynamicSmemBytes = lin::kSmem;
+  cfg.dynamicSmemBytes = (size_t)linear_pair_smem(tile_n);
   cfg.stream = stream;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -7,8 +7,7 @@
 // order, each CTA the tokens of its part, read from its peers' shared memory: no workspace, one launch, and the same result
 // every time.  A warp writes 128 columns of one token at a time, which are one group of what is kept in 8 bits.
 //
-// Warp 0 loads (TMA), warp 1 issues the products, warps 4-7 take the sums of 512 k at a time to FP32 registers, all warps join
-// the shares.  Two CTAs share an SM where their sums leave room.
+// Warp 0 loads (TMA), warp 1 issues the products, warps 4-7 take the accumulators to FP32 registers, all warps join the shares.  Two CTAs share an SM where their sums leave room.
 #include "linear_common.cuh"
 
 namespace sgemm_impl {
@@ -30,15 +29,6 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   float4 v;
   asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(addr) : "memory");
   return v;
-}
-
-__device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* map, uint32_t bar, bool mn_major, int mn0, int k0, int rows) {
-  if (mn_major) {
-    tma_load_3d(dst, map, bar, mn0, k0, 0);
-    if (rows > 64) tma_load_3d(dst + kBlockBytes, map, bar, mn0 + 64, k0, 0);
-  } else {
-    tma_load_3d(dst, map, bar, k0, mn0, 0);
-  }
 }
 
 // Four elements of a BF16 row, n of them there.
@@ -65,10 +55,10 @@ __device__ __forceinline__ void put4(__nv_bfloat16* p, int n, bool vec, const fl
 }
 
 // What is kept of 4 columns of a token; all lanes of the warp, which hold 128 columns (n < 1: none here).
-__device__ __forceinline__ void keep4(const LinearOut& o, int which, int row, int col, int n, const float (&v)[4]) {
+__device__ __forceinline__ void keep4(const LinearOut& o, const LinearJob& j, int which, int row, int col, int n, const float (&v)[4]) {
   const LinearKept& k = o.kept[which];
   if (o.keep == 1) {
-    if (n > 0 && kept_ok(o, which, row, col, n)) put4(static_cast<__nv_bfloat16*>(k.data) + (int64_t)row * k.ld + col, n, o.kept_vec8[which], v);
+    if (n > 0 && kept_ok(o, j, which, row, col, n)) put4(static_cast<__nv_bfloat16*>(k.data) + (int64_t)row * k.ld + col, n, o.kept_vec8[which], v);
     return;
   }
   float m = 0.0f;
@@ -76,9 +66,9 @@ __device__ __forceinline__ void keep4(const LinearOut& o, int which, int row, in
   for (int e = 0; e < 4; ++e) m = fmaxf(m, e < n ? f8::finite_abs(v[e]) : 0.0f);
   const float scale = f8::group_scale(f8::lanes_max<32>(m), kMaxE4M3), inv = __fdiv_rn(1.0f, scale);
   if (n <= 0) return;
-  if (col % 128 == 0) put_scale(o, which, row, col >> 7, scale);
+  if (col % 128 == 0) put_scale(o, j, which, row, col >> 7, scale);
   const uint32_t u = f8::codes2<true>(v[0] * inv, v[1] * inv, false) | (f8::codes2<true>(v[2] * inv, v[3] * inv, false) << 16);
-  if (!kept_ok(o, which, row, col, n)) return;
+  if (!kept_ok(o, j, which, row, col, n)) return;
   uint8_t* d = static_cast<uint8_t*>(k.data) + (int64_t)row * k.ld + col;
   if (k.vec && n == 4) {
     *reinterpret_cast<uint32_t*>(d) = u;
@@ -108,16 +98,17 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = (int)blockIdx.x % p.split;  // of the cluster: blocks of a cluster are consecutive
   const int tile = (int)blockIdx.x / p.split;
-  const int l0 = (tile / p.tiles_s) * BL, s0 = (tile % p.tiles_s) * TS;
-  const int kt = p.k_tiles * p.segments;
+  const LinearJob& j = p.job;
+  const int l0 = (tile / j.tiles_m) * BL, s0 = (tile % j.tiles_m) * TS;
+  const int kt = j.k_tiles * j.segments;
   const int g0 = (int)((int64_t)kt * rank / p.split), g1 = (int)((int64_t)kt * (rank + 1) / p.split);
   const int units = g1 - g0;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
-    prefetch_tensormap(&maps.a[0]);
-    prefetch_tensormap(&maps.b[0]);
-    if (GATED) prefetch_tensormap(&maps.b[1]);
+    prefetch_tensormap(&maps.op[j.a[0]]);
+    prefetch_tensormap(&maps.op[j.b[0]]);
+    if (GATED) prefetch_tensormap(&maps.op[j.b[1]]);
     for (int s = 0; s < p.stages; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
       mbar_init(smem_addr(&done[s]), 1);
@@ -148,12 +139,13 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
         break;
       }
       if (elect_one()) {
-        const int segment = g0 + t >= p.k_tiles, k0 = (g0 + t - segment * p.k_tiles) * BK;
+        const int segment = g0 + t >= j.k_tiles, k0 = (g0 + t - segment * j.k_tiles) * BK;
         const uint32_t bar = smem_addr(&full[s]), l = sbase + (uint32_t)(s * p.stage_bytes);
+        const auto load = [&](uint32_t dst, const CUtensorMap* map, int inner, int outer) { tma_load_3d(dst, map, bar, inner, outer, 0); };
         mbar_arrive_expect_tx(bar, (uint32_t)p.stage_bytes);
-        load_rows(l, &maps.b[segment], bar, p.l_mn, l0, k0, BL);
-        if (GATED) load_rows(l + BL * BK * 2, &maps.b[1], bar, p.l_mn, l0, k0, BL);
-        load_rows(l + kParts * BL * BK * 2, &maps.a[segment], bar, p.s_mn, s0, k0, TS);
+        load_part(load, l, &maps.op[j.b[GATED ? 0 : segment]], j.b_mn, l0, k0, BL);
+        if (GATED) load_part(load, l + BL * BK * 2, &maps.op[j.b[1]], j.b_mn, l0, k0, BL);
+        load_part(load, l + kParts * BL * BK * 2, &maps.op[j.a[segment]], j.a_mn, s0, k0, TS);
       }
       if (++s == p.stages) {
         s = 0;
@@ -166,15 +158,15 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
         atomicOr(p.fault, (unsigned)kFaultDrainWait);
   } else if (warp == 1) {
     // ------------------------------------------------ products
-    const uint32_t lstep = step_of(p.l_mn), sstep = step_of(p.s_mn), desc0 = desc_lo(sbase);
+    const uint32_t lstep = step_of(j.b_mn), sstep = step_of(j.a_mn), desc0 = desc_lo(sbase);
     int t = 0, s = 0, b = 0;
     uint32_t lap = 0, b_lap = 0;
     bool ok = true;
     while (ok && t < units) {
-      const int n = min(kFold, units - t);
+      const int n = min(j.fold, units - t);
       ok = b_lap == 0 || poll_wait(smem_addr(&acc_empty[b]), (b_lap - 1) & 1u, p.timeout_ns);
       tmem_fence_after_sync();
-      for (int j = 0; ok && j < n; ++j) {
+      for (int i = 0; ok && i < n; ++i) {
         ok = poll_wait(smem_addr(&full[s]), lap & 1u, p.timeout_ns);
         if (!ok) break;
         tmem_fence_after_sync();
@@ -186,9 +178,9 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
 #pragma unroll
             for (uint32_t ks = 0; ks < BK / 16; ++ks)
               mma_bf16(tmem + (uint32_t)(b * kParts + w) * kAccCols, make_desc(ld + (uint32_t)(w * (BL * BK * 2 >> 4)) + ks * lstep),
-                       make_desc(sd + ks * sstep), p.idesc, j == 0 && ks == 0 ? 0u : 1u);
+                       make_desc(sd + ks * sstep), j.idesc, i == 0 && ks == 0 ? 0u : 1u);
           f8::mma_commit(smem_addr(&done[s]));
-          if (j == n - 1) f8::mma_commit(smem_addr(&acc_full[b]));
+          if (i == n - 1) f8::mma_commit(smem_addr(&acc_full[b]));
         }
         __syncwarp();
         ++t;
@@ -215,7 +207,7 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
     for (int e = 0; e < kParts * TS; ++e) sum[e] = 0.0f;
     int b = 0;
     uint32_t b_lap = 0;
-    for (int t = 0; t < units; t += kFold) {
+    for (int t = 0; t < units; t += j.fold) {
       if (!poll_wait(smem_addr(&acc_full[b]), b_lap & 1u, p.timeout_ns)) {
         if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
         break;
@@ -236,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
           }
           tmem_ld_ready(v);
 #pragma unroll
-          for (int j = 0; j < kCols; ++j) sum[w * TS + j0 + j] += v[j];
+          for (int k = 0; k < kCols; ++k) sum[w * TS + j0 + k] += v[k];
         }
       if (++b == kBufs) {
         b = 0;
@@ -259,9 +251,9 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
   if (p.split > 1) cluster_sync();
   // this CTA's tokens of the tile: a warp per token, 4 columns per lane
   const LinearOut& o = p.out;
-  const int ns = min(TS, o.M - s0);
+  const int ns = min(TS, j.M - s0);
   const int b0 = ns * rank / p.split, b1 = ns * (rank + 1) / p.split;
-  const int col = l0 + 4 * lane, n = min(4, o.N - col);
+  const int col = l0 + 4 * lane, n = min(4, j.N - col);
   for (int s = b0 + warp; s < b1; s += kThreads / 32) {
     float v[kParts][4];
 #pragma unroll
@@ -281,31 +273,36 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
       v[w][3] = x.w;
     }
     const int row = s0 + s;
-    if (!GATED && o.bias && n > 0 && in_range(o.guard.fault, o.guard.word, f8::kSiteIn, col, n, o.N)) {
+    if (!GATED && o.bias && n > 0 && in_range(o.guard.fault, o.guard.word, f8::kSiteIn, col, n, j.N)) {
       float x[4];
       get4(static_cast<const __nv_bfloat16*>(o.bias) + col, n, o.bias_vec, x);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[0][e] += x[e];
     }
     if (o.keep) {
-      keep4(o, 0, row, col, n, v[0]);
-      if constexpr (GATED) keep4(o, 1, row, col, n, v[kParts - 1]);
+      keep4(o, j, 0, row, col, n, v[0]);
+      if constexpr (GATED) keep4(o, j, 1, row, col, n, v[kParts - 1]);
     }
     if (n <= 0) continue;
     with_act(o.act, [&](auto act) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) v[0][e] = act_of<decltype(act)::value>(v[0][e]) * (GATED ? v[kParts - 1][e] : 1.0f);
+      for (int e = 0; e < 4; e += 2) {
+        float2 f = act_of<decltype(act)::value>(make_float2(v[0][e], v[0][e + 1]));
+        if (GATED) f = mul(f, make_float2(v[kParts - 1][e], v[kParts - 1][e + 1]));
+        v[0][e] = f.x;
+        v[0][e + 1] = f.y;
+      }
     });
-    if (!GATED && o.residual && r_ok(o, row, col, n)) {
+    if (!GATED && o.residual && r_ok(o, j, row, col, n)) {
       float x[4];
       get4(static_cast<const __nv_bfloat16*>(o.residual) + (int64_t)row * o.ldr + col, n, o.r_vec, x);
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[0][e] += x[e];
     }
-    if (!d_ok(o, 0, row, col, n)) continue;
-    if (o.f32) {
-      float* d = static_cast<float*>(o.d[0]) + (int64_t)row * o.ldd[0] + col;
-      if (o.d_vec[0] && n == 4) {
+    if (!d_ok(o, j, row, col, n)) continue;
+    if (j.f32) {
+      float* d = static_cast<float*>(j.d) + (int64_t)row * j.ldd + col;
+      if (j.d_vec && n == 4) {
         *reinterpret_cast<float4*>(d) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
       } else {
 #pragma unroll
@@ -313,7 +310,7 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
           if (e < n) d[e] = v[0][e];
       }
     } else {
-      put4(static_cast<__nv_bfloat16*>(o.d[0]) + (int64_t)row * o.ldd[0] + col, n, o.d_vec[0], v[0]);
+      put4(static_cast<__nv_bfloat16*>(j.d) + (int64_t)row * j.ldd + col, n, j.d_vec, v[0]);
     }
   }
   if (p.split > 1) {
@@ -356,7 +353,7 @@ cudaError_t prepare_linear_short() {
 
 cudaError_t launch_linear_short(bool gated, const LinearMaps& maps, const LinearShortParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(p.tiles_l * p.tiles_s * p.split));
+  cfg.gridDim = dim3((unsigned)(p.job.tiles_n * p.job.tiles_m * p.split));
   cfg.blockDim = dim3(lin::kThreads);
   cfg.dynamicSmemBytes = (size_t)linear_short_smem(p.tile_s, gated, p.stages, p.stage_bytes);
   cfg.stream = stream;

@@ -21,16 +21,64 @@ using f8::poll_wait;
 using f8::put_at;
 using f8::tmem_ld32;
 
-// ---- activations, in FP32
+// ---- activations, in FP32, two values at a time (packed arithmetic: the epilogues and the gradient kernel are bound by the
+// number of instructions as much as by the memory)
 //
-// exp(-a) is expf(), whose infinity for a below -88 makes the quotients 0; a quotient of a finite value and an infinity is
-// 0 with the fast division too (2 ulp; its result is 0 for divisors above 2^126, where the true one is below 2^-100 of a).
+// The exponential is ex2.approx.ftz (2^-22 of its result; 0 or infinity beyond its range), the reciprocal rcp.approx.ftz (1 ulp,
+// 0 for an infinity), so a quotient of a finite value and an infinity is 0.
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 both(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 ex2(float2 x) { return make_float2(ex2(x.x), ex2(x.y)); }
+__device__ __forceinline__ float2 rcp(float2 x) { return make_float2(rcp(x.x), rcp(x.y)); }
+__device__ __forceinline__ float2 mul(float2 a, float2 b) { return __fmul2_rn(a, b); }
+__device__ __forceinline__ float2 add(float2 a, float2 b) { return __fadd2_rn(a, b); }
+__device__ __forceinline__ float2 fma(float2 a, float2 b, float2 c) { return __ffma2_rn(a, b, c); }
+// c where k is 0, else x
+__device__ __forceinline__ float2 unless0(float2 k, float2 c, float2 x) { return make_float2(k.x == 0.0f ? c.x : x.x, k.y == 0.0f ? c.y : x.y); }
+
+// e = exp(-a^2 / 2) and Phi(a).  Phi(-|a|) = e P(t), t = 1 / (1 + 0.28284273 |a|), with P of degree 9 fitted to
+// exp(a^2 / 2) Phi(-|a|) over all a (least maximum of the relative error, 1.3e-7; 4.4e-7 evaluated in FP32), so that small
+// values of Phi keep their relative accuracy.
+__device__ __forceinline__ float2 normal_integral(float2 a, float2& e) {
+  const float2 m = make_float2(fabsf(a.x), fabsf(a.y));
+  const float2 t = rcp(fma(m, both(0.28284273f), both(1.0f)));
+  e = ex2(mul(mul(a, both(-0.72134752f)), a));
+  float2 q = both(0.025131345f);
+  q = fma(q, t, both(-0.09145177f));
+  q = fma(q, t, both(0.08454426f));
+  q = fma(q, t, both(-0.00280497f));
+  q = fma(q, t, both(0.070716225f));
+  q = fma(q, t, both(0.08427088f));
+  q = fma(q, t, both(0.10392137f));
+  q = fma(q, t, both(0.112834804f));
+  q = fma(q, t, both(0.11283793f));
+  q = mul(mul(q, t), e);
+  return make_float2(a.x >= 0.0f ? 1.0f - q.x : q.x, a.y >= 0.0f ? 1.0f - q.y : q.y);
+}
+
+// 1 / (1 + exp(-a)) and, for GELU's tanh form, 1 / (1 + exp(-2 u))
+__device__ __forceinline__ float2 sigmoid(float2 a) { return rcp(add(ex2(mul(a, both(-1.44269504f))), both(1.0f))); }
+__device__ __forceinline__ float2 sigmoid_2u(float2 a, float2 a2) {
+  return rcp(add(ex2(mul(a, fma(a2, both(-0.10294324f), both(-2.3022082f)))), both(1.0f)));
+}
+
 template <int ACT>
-__device__ __forceinline__ float act_of(float a) {
-  if constexpr (ACT == SGEMM_ACT_RELU) return a < 0.0f ? 0.0f : a;
-  else if constexpr (ACT == SGEMM_ACT_SILU) return __fdividef(a, 1.0f + expf(-a));
-  else if constexpr (ACT == SGEMM_ACT_GELU) return a * (0.5f * erfcf(a * -0.70710678f));  // Phi(a) without cancellation for a < 0
-  else if constexpr (ACT == SGEMM_ACT_GELU_TANH) return __fdividef(a, 1.0f + expf(-1.59576912f * fmaf(0.044715f * a * a, a, a)));
+__device__ __forceinline__ float2 act_of(float2 a) {
+  if constexpr (ACT == SGEMM_ACT_RELU) return make_float2(a.x < 0.0f ? 0.0f : a.x, a.y < 0.0f ? 0.0f : a.y);
+  else if constexpr (ACT == SGEMM_ACT_SILU) return mul(a, sigmoid(a));
+  else if constexpr (ACT == SGEMM_ACT_GELU) {
+    float2 e;
+    return mul(a, normal_integral(a, e));
+  } else if constexpr (ACT == SGEMM_ACT_GELU_TANH) return mul(a, sigmoid_2u(a, mul(a, a)));
   else return a;
 }
 
@@ -49,28 +97,27 @@ __device__ __forceinline__ void with_act(int act, const F& f) {
 // The activation f and its derivative df.  Where a factor of a product has become 0 the product's limit is taken (a s (1 - s)
 // and a phi(a) are 0 for a beyond their range, infinite a among them).
 template <int ACT>
-__device__ __forceinline__ void act_grad(float a, float& f, float& df) {
+__device__ __forceinline__ void act_grad(float2 a, float2& f, float2& df) {
   if constexpr (ACT == SGEMM_ACT_RELU) {
-    f = a < 0.0f ? 0.0f : a;
-    df = a > 0.0f ? 1.0f : a <= 0.0f ? 0.0f : a;  // NaN stays NaN
+    f = act_of<ACT>(a);
+    df = make_float2(a.x > 0.0f ? 1.0f : a.x <= 0.0f ? 0.0f : a.x, a.y > 0.0f ? 1.0f : a.y <= 0.0f ? 0.0f : a.y);  // NaN stays NaN
   } else if constexpr (ACT == SGEMM_ACT_SILU) {
-    const float s = __fdividef(1.0f, 1.0f + expf(-a));
-    const float t = s * (1.0f - s);
-    f = a * s;
-    df = t == 0.0f ? s : fmaf(a, t, s);
+    const float2 s = sigmoid(a), t = fma(make_float2(-s.x, -s.y), s, s);
+    f = mul(a, s);
+    df = unless0(t, s, fma(a, t, s));
   } else if constexpr (ACT == SGEMM_ACT_GELU) {
-    const float c = 0.5f * erfcf(a * -0.70710678f), phi = 0.39894228f * expf(-0.5f * a * a);
-    f = a * c;
-    df = phi == 0.0f ? c : fmaf(a, phi, c);
+    float2 e;
+    const float2 c = normal_integral(a, e);
+    f = mul(a, c);
+    df = unless0(e, c, fma(mul(a, both(0.39894228f)), e, c));
   } else if constexpr (ACT == SGEMM_ACT_GELU_TANH) {
-    const float a2 = a * a;
-    const float s = __fdividef(1.0f, 1.0f + expf(-1.59576912f * fmaf(0.044715f * a2, a, a)));
-    const float t = s * (1.0f - s);
-    f = a * s;
-    df = t == 0.0f ? s : fmaf(a * t, 1.59576912f * fmaf(0.134145f, a2, 1.0f), s);
+    const float2 a2 = mul(a, a);
+    const float2 s = sigmoid_2u(a, a2), t = fma(make_float2(-s.x, -s.y), s, s);
+    f = mul(a, s);
+    df = unless0(t, s, fma(mul(a, t), fma(a2, both(0.21406445f), both(1.5957691f)), s));
   } else {
     f = a;
-    df = 1.0f;
+    df = both(1.0f);
   }
 }
 
@@ -108,9 +155,16 @@ __device__ __forceinline__ void mma_bf16(uint32_t d_tmem, uint64_t adesc, uint64
       : "memory");
 }
 
-// K tiles summed in one accumulator before they are added to sums in FP32 registers: the tensor cores' own accumulation is not
-// round-to-nearest and drifts by about 1.2e-8 of the sum per instruction of 16 k; 32 of them stay below 4e-7.
-constexpr int kFold = 8;
+// Copies one operand's tile of `rows` output rows (at most 128) and 64 k: boxes of 64 output rows in either order, one 8 KB
+// block behind the other.
+template <typename Load>
+__device__ __forceinline__ void load_part(const Load& load, uint32_t dst, const CUtensorMap* map, int mn_major, int mn0, int k0, int rows) {
+#pragma unroll
+  for (int i = 0; i < (rows > 64 ? 2 : 1); ++i)
+    load(dst + (uint32_t)(i * kBlockBytes), map, mn_major ? mn0 + 64 * i : k0, mn_major ? k0 : mn0 + 64 * i);
+}
+// Bytes that it copies.
+__host__ __device__ constexpr uint32_t part_bytes(int mn_major, int rows) { return mn_major ? (rows > 64 ? 2u : 1u) * kBlockBytes : (uint32_t)rows * 128u; }
 
 // ---- what an epilogue reads and writes
 
@@ -120,19 +174,19 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
-__device__ __forceinline__ bool d_ok(const LinearOut& o, int which, int64_t row, int64_t col, int64_t n) {
-  return in_range(o.guard.fault, o.guard.word, f8::kSiteOut, row * o.ldd[which] + col, n, extent(o.M, o.ldd[which], o.N));
+__device__ __forceinline__ bool d_ok(const LinearOut& o, const LinearJob& j, int64_t row, int64_t col, int64_t n) {
+  return in_range(o.guard.fault, o.guard.word, f8::kSiteOut, row * j.ldd + col, n, extent(j.M, j.ldd, j.N));
 }
-__device__ __forceinline__ bool r_ok(const LinearOut& o, int64_t row, int64_t col, int64_t n) {
-  return in_range(o.guard.fault, o.guard.word, f8::kSiteIn, row * o.ldr + col, n, extent(o.M, o.ldr, o.N));
+__device__ __forceinline__ bool r_ok(const LinearOut& o, const LinearJob& j, int64_t row, int64_t col, int64_t n) {
+  return in_range(o.guard.fault, o.guard.word, f8::kSiteIn, row * o.ldr + col, n, extent(j.M, o.ldr, j.N));
 }
-__device__ __forceinline__ bool kept_ok(const LinearOut& o, int which, int64_t row, int64_t col, int64_t n) {
-  return in_range(o.guard.fault, o.guard.word, f8::kSiteCodes, row * o.kept[which].ld + col, n, extent(o.M, o.kept[which].ld, o.N));
+__device__ __forceinline__ bool kept_ok(const LinearOut& o, const LinearJob& j, int which, int64_t row, int64_t col, int64_t n) {
+  return in_range(o.guard.fault, o.guard.word, f8::kSiteCodes, row * o.kept[which].ld + col, n, extent(j.M, o.kept[which].ld, j.N));
 }
 // The scale of group `group` of a row of a kept 8-bit matrix.
-__device__ __forceinline__ void put_scale(const LinearOut& o, int which, int64_t row, int64_t group, float s) {
+__device__ __forceinline__ void put_scale(const LinearOut& o, const LinearJob& j, int which, int64_t row, int64_t group, float s) {
   const LinearKept& k = o.kept[which];
-  if (in_range(o.guard.fault, o.guard.word, f8::kSiteScale, row * k.lds + group, 1, extent(o.M, k.lds, (o.N + 127) / 128)))
+  if (in_range(o.guard.fault, o.guard.word, f8::kSiteScale, row * k.lds + group, 1, extent(j.M, k.lds, (j.N + 127) / 128)))
     k.scale[row * k.lds + group] = s;
 }
 

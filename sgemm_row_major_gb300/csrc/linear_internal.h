@@ -21,11 +21,6 @@ struct LinearKept {
   int vec = 0;                   // BF16: TMA writes it; 8-bit: rows start at multiples of 16 bytes
 };
 struct LinearOut {
-  int M = 0, N = 0;              // rows and columns of the output (of each of two products, of H)
-  void* d[2] = {nullptr, nullptr};
-  int64_t ldd[2] = {0, 0};
-  int d_tma[2] = {0, 0};         // 1: aligned rows of whole 16 bytes, which TMA writes
-  int f32 = 0;                   // type of d
   const void* bias = nullptr;    // N values or nullptr
   const void* residual = nullptr;
   int64_t ldr = 0;
@@ -33,39 +28,49 @@ struct LinearOut {
   int keep = 0;                  // 0: nothing, 1: BF16, 2: 8-bit
   LinearKept kept[2];            // of A and B
   int bias_vec = 0, r_vec = 0;   // 1: 16-byte aligned (rows)
-  int d_vec[2] = {0, 0};         // 1: rows of d start at multiples of 8 bytes (BF16) or 16 bytes (FP32)
   int kept_vec8[2] = {0, 0};     // 1: rows of a BF16 kept matrix start at multiples of 8 bytes
   Guard guard;
 };
 
-// D = A0 B0 (+ A1 B1 with two segments); with two products D0 = A0 B0, D1 = A1 B0; gated: B0 and B1 are gate and up.
+// One product of a launch: D = A0 B0 (+ A1 B1 with two segments of K); gated: B0 and B1 are gate and up, D is H.
+struct LinearJob {
+  int M = 0, N = 0;              // rows and columns of D
+  void* d = nullptr;
+  int64_t ldd = 0;
+  int d_tma = 0;                 // 1: aligned rows of whole 16 bytes, which TMA writes
+  int d_vec = 0;                 // 1: rows start at multiples of 8 bytes (BF16) or 16 bytes (FP32)
+  int f32 = 0;
+  int tiles_m = 0, tiles_n = 0;
+  int k_tiles = 0, segments = 1; // of 64 k, per segment
+  int fold = 0;                  // K tiles that are summed in one accumulator
+  int a_mn = 0, b_mn = 0;        // 1: the stored rows run along M (N), not along K
+  uint32_t idesc = 0;
+  int a[2] = {0, 0}, b[2] = {0, 0};  // maps of the operands
+};
+constexpr int kLinearJobs = 3;
 struct LinearMaps {
-  CUtensorMap a[2], b[2], d[2], kept[2];
+  CUtensorMap op[6], d[kLinearJobs], kept[2];
 };
 
 struct LinearPairParams {
   LinearOut out;
-  int k_tiles = 0;               // of 64 k, per segment
-  int segments = 1, products = 1;
-  int a_mn = 0, b_mn = 0;        // 1: the stored rows run along M (N), not along K
-  uint32_t idesc = 0;
-  int tiles_m = 0, tiles_n = 0, clusters = 0;
+  LinearJob job[kLinearJobs];    // their tiles one behind the other
+  int jobs = 1, clusters = 0;
   uint64_t timeout_ns = 0;
   unsigned* fault = nullptr;
 };
-constexpr int kLinearPairStages = 5, kLinearPairThreads = 384;
+constexpr int kLinearPairThreads = 384;
 constexpr int kLinearPairTiles[] = {256, 128, 64};
-int64_t linear_pair_smem();
+int linear_pair_stages(int tile_n);
+int64_t linear_pair_smem(int tile_n);
 cudaError_t prepare_linear_pair();
 cudaError_t launch_linear_pair(int tile_n, bool gated, const LinearMaps& maps, const LinearPairParams& p, cudaStream_t stream);
 
 // The columns of D run along the tensor core's rows (B's tile of 128), its rows along the columns.
 struct LinearShortParams {
   LinearOut out;
-  int k_tiles = 0, segments = 1;
-  int l_mn = 0, s_mn = 0;        // order of B and of A
-  uint32_t idesc = 0;
-  int tile_s = 0, tiles_l = 0, tiles_s = 0, split = 1, stages = 0, stage_bytes = 0;
+  LinearJob job;
+  int tile_s = 0, split = 1, stages = 0, stage_bytes = 0;
   uint64_t timeout_ns = 0;
   unsigned* fault = nullptr;
 };

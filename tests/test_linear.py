@@ -195,9 +195,11 @@ def test_empty():
     done()
 
 
-def test_only_what_is_wanted():
+def test_only_what_is_wanted(force):
+    """Each output alone: the same values where the kernel is the same, None for the others."""
     import torch
     T, I, O = 70, 200, 136
+    force("LINEAR_PAIR", 128)
     dy, x, w, u, a, b = rand(1, T, O), rand(2, T, I), rand(3, O, I), rand(4, O, I), rand(5, T, O), rand(6, T, O)
     full = sg.linear_bf16_backward(dy, x, w, a, "gelu", dbias=True)
     only = [sg.linear_bf16_backward(dy, None, w, a, "gelu", dweight=False), sg.linear_bf16_backward(dy, x, None, a, "gelu", dx=False),
@@ -212,6 +214,8 @@ def test_only_what_is_wanted():
     assert torch.equal(one.dgate, full.dgate) and torch.equal(one.dup, full.dup) and one.dx is None and one.h is None
     one = sg.gated_bf16_backward(dy, None, None, None, a, b, dx=False, dweights=False, h=True)
     assert torch.equal(one.h, full.h) and one[:3] == (None, None, None)
+    force()
+    check_all(sg.gated_bf16_backward(dy, None, w, u, a, b, dweights=False), gated_grad_ref(dy, x, w, u, a, b, "silu"), ["dx"])
     done()
 
 
