@@ -182,16 +182,28 @@ struct Operand {
   void place(Pieces* w) {
     if (copied) copy = w->take<uint16_t>(rows * round8(cols));
   }
-  // Copies it where it needs that; an operand that several products read is copied once.
-  cudaError_t make(const Guard& g, cudaStream_t stream) {
-    if (!copied) return cudaSuccess;
-    return launch_linear_expand(m, rows, cols, copy, round8(cols), g, stream);
-  }
   cudaError_t map(int box_rows, CUtensorMap* out) const {
     const int64_t ld = copied || rows == 1 ? round8(cols) : m.ld;  // (a map wants a stride even where it steps over nothing)
     return encode_linear_map(copied ? copy : m.data, cols, rows, ld, box_rows, out);
   }
 };
+
+// Makes the copies that operands (up to three) need, in one launch.
+cudaError_t make_copies(std::initializer_list<const Operand*> list, const Guard& g, cudaStream_t stream) {
+  LinearExpandParams p;
+  p.guard = g;
+  int n = 0;
+  for (const Operand* o : list) {
+    if (!o || !o->copied) continue;
+    LinearExpand& e = p.part[n++];
+    e.m = o->m;
+    e.rows = o->rows;
+    e.cols = (int)o->cols;
+    e.dst = o->copy;
+    e.ldd = round8(o->cols);
+  }
+  return n ? launch_linear_expand(p, stream) : cudaSuccess;
+}
 
 // Tensor-core instruction descriptor, kind::f16: FP32 accumulator, BF16 operands, their orders (1: MN-major), N and M.
 uint32_t instruction(int a_mn, int b_mn, int m, int n) {
@@ -209,8 +221,10 @@ struct Product {
   bool f32 = false;
 };
 
-// K tiles that are summed in one accumulator: FP32 values that leave the kernel are to be about as exact as FP32 sums.
-constexpr int kFoldF32 = 8, kFoldKept8 = 16, kFoldNone = 1 << 30;
+// K tiles of 64 that the pair kernel sums in one accumulator where FP32 values leave it (an FP32 output, scales): sums of 8 are
+// about as exact as FP32 sums (kernel_linear_pair.cu); the first 16 together leave the epilogue of the tile before more time
+// (4.2 us) before the folding starts again.
+constexpr int kFoldFirst = 16, kFold = 8, kFoldNone = 1 << 30;
 
 // One launch of the products: of one with a choice of either kernel, of several with the pair kernel.
 struct Launch {
@@ -277,7 +291,8 @@ struct Launch {
       j.d_vec = rows_at(r.d, r.ldd, size, 4 * size);
       j.k_tiles = (int)ceil_div(r.shape.K, 64);
       j.segments = r.shape.segments;
-      j.fold = r.f32 ? kFoldF32 : out.keep == 2 ? kFoldKept8 : kFoldNone;
+      j.fold0 = r.f32 || out.keep == 2 ? kFoldFirst : kFoldNone;
+      j.fold = kFold;
       j.a_mn = r.a_mn;
       j.b_mn = r.b_mn;
       if (pair) {
@@ -422,9 +437,7 @@ int forward(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, int6
           for (Operand* o : {&x, &w0, &w1}) o->m.data = zeros, o->m.ld = 8;
           *e = cudaMemsetAsync(zeros, 0, (size_t)std::max(tokens, outputs) * 16, stream);
         }
-        if (*e == cudaSuccess) *e = x.make(g, stream);
-        if (*e == cudaSuccess) *e = w0.make(g, stream);
-        if (*e == cudaSuccess && gated) *e = w1.make(g, stream);
+        if (*e == cudaSuccess) *e = make_copies({&x, &w0, gated ? &w1 : nullptr}, g, stream);
         return *e == cudaSuccess ? launch.run(dev, stream, e) : SGEMM_OK;
       });
 }
@@ -574,12 +587,12 @@ int sgemm_linear_backward(int64_t tokens, int64_t inputs, int64_t outputs, const
   g.cols = (int)outputs;
   g.dy = dY;
   g.lddy = lddy;
-  g.dy_vec = rows_at(dY, lddy, 2, 16);
   if (act) g.a = kept_in(kept);
   g.act = activation;
   g.dbias = dbias;
   g.guard = {dev.fault, dev.bounds};
-  g.row_blocks = linear_grad_row_blocks(tokens, (int)outputs, dev.sm_count);
+  g.row_blocks = linear_grad_row_blocks(tokens, (int)outputs, dbias != nullptr, dev.pair_clusters > 0, dev.sm_count);
+  g.vec = outputs % 8 == 0 && rows_at(dY, lddy, 2, 16) && (!act || g.a.vec);
   // dA: dY itself where it can be read as it is and there is no activation
   Operand d(dY, lddy, nullptr, 0, tokens, outputs);
   const bool write = products && (act || d.copied);
@@ -590,15 +603,13 @@ int sgemm_linear_backward(int64_t tokens, int64_t inputs, int64_t outputs, const
       dev, stream,
       [&](Pieces* p) {
         g.da = write ? p->take<uint16_t>(tokens * ldd) : nullptr;
-        g.partial = dbias && g.row_blocks > 1 ? p->take<float>((int64_t)g.row_blocks * outputs) : nullptr;
         if (dX) w.place(p);
         if (dW) x.place(p);
       },
       [&](cudaError_t* e) {
         g.ldd = ldd;
         if (write || dbias) *e = launch_linear_grad(g, stream);
-        if (*e == cudaSuccess && dX) *e = w.make(g.guard, stream);
-        if (*e == cudaSuccess && dW) *e = x.make(g.guard, stream);
+        if (*e == cudaSuccess) *e = make_copies({dX ? &w : nullptr, dW ? &x : nullptr}, g.guard, stream);
         if (*e != cudaSuccess) return (int)SGEMM_OK;
         if (write) d = Operand(g.da, ldd, nullptr, 0, tokens, outputs);
         Launch launch;
@@ -657,15 +668,14 @@ int sgemm_gated_backward(int64_t tokens, int64_t inputs, int64_t outputs, const 
   g.cols = (int)outputs;
   g.dy = dH;
   g.lddy = lddh;
-  g.dy_vec = rows_at(dH, lddh, 2, 16);
   g.a = kept_in(kept_gate);
   g.b = kept_in(kept_up);
   g.act = activation;
   g.h = H;
   g.ldh = ldh;
-  g.h_vec = rows_at(H, ldh, 2, 16);
   g.guard = {dev.fault, dev.bounds};
-  g.row_blocks = linear_grad_row_blocks(tokens, (int)outputs, dev.sm_count);
+  g.row_blocks = linear_grad_row_blocks(tokens, (int)outputs, false, true, dev.sm_count);
+  g.vec = outputs % 8 == 0 && rows_at(dH, lddh, 2, 16) && g.a.vec && g.b.vec && (!H || rows_at(H, ldh, 2, 16));
   Operand wg(gate, ldg, nullptr, 0, outputs, inputs), wu(up, ldu, nullptr, 0, outputs, inputs);
   Operand x(X ? X->data : nullptr, X ? X->ld : 1, X ? X->scale : nullptr, X ? X->lds : 1, tokens, inputs);
   const int64_t ldd = round8(outputs);
@@ -683,9 +693,7 @@ int sgemm_gated_backward(int64_t tokens, int64_t inputs, int64_t outputs, const 
       [&](cudaError_t* e) {
         g.ldd = ldd;
         *e = launch_linear_grad(g, stream);
-        if (*e == cudaSuccess && dX) *e = wg.make(g.guard, stream);
-        if (*e == cudaSuccess && dX) *e = wu.make(g.guard, stream);
-        if (*e == cudaSuccess && dG) *e = x.make(g.guard, stream);
+        if (*e == cudaSuccess) *e = make_copies({dX ? &wg : nullptr, dX ? &wu : nullptr, dG ? &x : nullptr}, g.guard, stream);
         if (*e != cudaSuccess) return (int)SGEMM_OK;
         Operand da(g.da, ldd, nullptr, 0, tokens, outputs), db(g.db, ldd, nullptr, 0, tokens, outputs);
         Launch launch;

@@ -5,264 +5,260 @@
 //     gated:  dA = dH * B * act'(A),  dB = dH * act(A),  H = act(A) * B
 //
 // A and B as the forward pass kept them: BF16, or 8-bit codes times the scale of their group of 128.  One pass over the data,
-// bound by the memory; a thread takes 8 columns of a row (16 bytes of BF16, 8 of codes), and rows 8 apart with all its loads
-// of two rows on their way before either is used.  Column sums are held per thread in FP32 over the rows of a block, joined in
-// shared memory in a fixed order, and the blocks' sums are added by a second kernel in a fixed order.
+// bound by the memory and nearly as much by the instructions of an activation's derivative (two values at a time in packed
+// arithmetic).  A thread takes 8 columns of a row (16 bytes of BF16, 8 of codes), eight threads a line of 128 bytes, and has all
+// its loads of two rows on their way before either is used.  Column sums are held per thread in FP32, joined within the CTA and
+// then by a cluster of up to 8 CTAs that share the rows of a strip of 64 columns, both in a fixed order: no second kernel.
 #include "linear_common.cuh"
 
 namespace sgemm_impl {
 namespace lin {
 namespace {
 
-constexpr int kThreads = 256, kWarps = kThreads / 32, kStrip = 256;  // columns of a CTA: 8 per lane
+constexpr int kThreads = 256, kStrip = 64, kLanes = kStrip / 8, kRowLanes = kThreads / kLanes;
+constexpr int kBatch = 2;         // rows whose loads are on their way together
+constexpr int kExpandChunks = 4;  // the same of the copies, in chunks of 8 columns
 
-// 8 consecutive values of a kept matrix, sent for and then waited for.
-template <bool CODES>
+// 8 consecutive values, n of them there, sent for and then waited for.  VEC: n is 8 or 0, and they can be read at once.
+template <bool CODES, bool VEC>
 struct KeptLoad;
-template <>
-struct KeptLoad<false> {
-  f8::Loading<__nv_bfloat16, true> v;
-  f8::Loading<__nv_bfloat16, false> u;
-  bool vec;
+template <bool VEC>
+struct KeptLoad<false, VEC> {
+  f8::Loading<__nv_bfloat16, VEC> v;
   __device__ __forceinline__ void load(const LinearKeptIn& k, int64_t rows, int cols, int64_t row, int col, int n, const Guard& g) {
     const f8::Rows<__nv_bfloat16> m(k.data, rows, k.ld, cols, g);
-    const __nv_bfloat16* p = m.base + row * k.ld + col;
-    vec = k.vec && n == 8;
-    if (vec) v.load(p, 8, m);
-    else     u.load(p, n, m);
+    v.load(m.base + row * k.ld + col, n, m);
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
-    if (vec) v.get().get(x);
-    else     u.get().get(x);
-  }
+  __device__ __forceinline__ void get(float2 (&x)[4]) const { v.get().get(&x[0].x); }
 };
-template <>
-struct KeptLoad<true> {
-  uint32_t c[2];
+template <bool VEC>
+struct KeptLoad<true, VEC> {
+  uint2 c;
   float s;
   __device__ __forceinline__ void load(const LinearKeptIn& k, int64_t rows, int cols, int64_t row, int col, int n, const Guard& g) {
-    c[0] = c[1] = 0u;
+    c = make_uint2(0u, 0u);
     s = 0.0f;
     if (n <= 0) return;
     const uint8_t* base = static_cast<const uint8_t*>(k.data);
     const int64_t at = row * k.ld + col;
     if (!in_range(g.fault, g.word, f8::kSiteCodes, at, n, extent(rows, k.ld, cols))) return;
     s = get_at(g, f8::kSiteScale, k.scale, row * k.lds + (col >> 7), extent(rows, k.lds, (cols + 127) / 128));
-    if (k.vec && n == 8) {
-      const uint2 u = *reinterpret_cast<const uint2*>(base + at);
-      c[0] = u.x;
-      c[1] = u.y;
+    if (VEC) {
+      c = *reinterpret_cast<const uint2*>(base + at);
     } else {
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (e < n) c[e / 4] |= (uint32_t)base[at + e] << (8 * (e % 4));
+        if (e < n) (e < 4 ? c.x : c.y) |= (uint32_t)base[at + e] << (8 * (e % 4));
     }
   }
-  __device__ __forceinline__ void get(float (&x)[8]) const {
+  __device__ __forceinline__ void get(float2 (&x)[4]) const {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c[e / 2] >> (16 * (e % 2))), __NV_E4M3);
-      const float2 f = __half22float2(__half2(h));
-      x[2 * e] = f.x * s;
-      x[2 * e + 1] = f.y * s;
+      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((e < 2 ? c.x : c.y) >> (16 * (e % 2))), __NV_E4M3);
+      x[e] = mul(__half22float2(__half2(h)), both(s));
     }
   }
 };
 
-// 8 values of BF16, n of them there, to a row of an aligned (VEC) or any other matrix.
-__device__ __forceinline__ void put8(void* base, int64_t ld, int64_t rows, int cols, int64_t row, int col, int n, bool vec, const float (&x)[8],
-                                     const Guard& g) {
+// 8 values as BF16, n of them there, to a row of an aligned (VEC) or any other matrix.
+template <bool VEC>
+__device__ __forceinline__ void put8(void* base, int64_t ld, int64_t rows, int cols, int64_t row, int col, int n, const float2 (&x)[4], const Guard& g) {
   const f8::Rows<__nv_bfloat16> m(base, rows, ld, cols, g);
-  __nv_bfloat16* p = static_cast<__nv_bfloat16*>(base) + row * ld + col;
-  if (vec && n == 8) f8::store_chunk<__nv_bfloat16, true>(p, x, 8, m);
-  else               f8::store_chunk<__nv_bfloat16, false>(p, x, n, m);
+  f8::store_chunk<__nv_bfloat16, VEC>(static_cast<__nv_bfloat16*>(base) + row * ld + col, &x[0].x, n, m);
 }
 
-template <bool GATED, bool CODES, bool SUMS>
-__global__ void __launch_bounds__(kThreads) linear_grad_kernel(const LinearGradParams p) {
+// ACT: the activation (one kernel for each: the branch around eight values' work cost as much as the work).
+template <int ACT, bool GATED, bool CODES, bool VEC, bool SUMS>
+__global__ void __launch_bounds__(kThreads) linear_grad_kernel(const __grid_constant__ LinearGradParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  constexpr int kRows = 2;  // whose loads are on their way together
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = (int)blockIdx.x * kStrip + 8 * lane;
+  const int col = (int)blockIdx.x * kStrip + 8 * (int)(threadIdx.x % kLanes);
   const int n = max(0, min(8, p.cols - col));
   const int64_t r0 = p.rows * blockIdx.y / p.row_blocks, r1 = p.rows * (blockIdx.y + 1) / p.row_blocks;
-  float sum[SUMS ? 8 : 1];
+  const LinearKeptIn y{p.dy, nullptr, p.lddy, 0, 0};
+  constexpr bool kAct = ACT != SGEMM_ACT_NONE || GATED;  // A is read
+  float2 sum[4];
 #pragma unroll
-  for (int e = 0; e < (SUMS ? 8 : 1); ++e) sum[e] = 0.0f;
+  for (int e = 0; e < 4; ++e) sum[e] = both(0.0f);
   if (n > 0) {
-    for (int64_t r = r0 + warp; r < r1; r += kRows * kWarps) {
-      KeptLoad<false> dy[kRows];
-      KeptLoad<CODES> a[kRows], b[GATED ? kRows : 1];
-      const LinearKeptIn y{p.dy, nullptr, p.lddy, 0, p.dy_vec};
+    for (int64_t r = r0 + threadIdx.x / kLanes; r < r1; r += kBatch * kRowLanes) {
+      KeptLoad<false, VEC> dy[kBatch];
+      KeptLoad<CODES, VEC> a[kBatch], b[kBatch];
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const int64_t row = r + k * kWarps;
-        const int here = row < r1 ? n : 0;
-        const int64_t at = row < r1 ? row : r;
-        dy[k].load(y, p.rows, p.cols, at, col, here, p.guard);
-        if (GATED || p.a.data) a[k].load(p.a, p.rows, p.cols, at, col, here, p.guard);
-        if (GATED) b[GATED ? k : 0].load(p.b, p.rows, p.cols, at, col, here, p.guard);
+      for (int k = 0; k < kBatch; ++k) {
+        const bool there = r + k * kRowLanes < r1;
+        const int64_t row = there ? r + k * kRowLanes : r;
+        const int here = there ? n : 0;
+        dy[k].load(y, p.rows, p.cols, row, col, here, p.guard);
+        if (kAct) a[k].load(p.a, p.rows, p.cols, row, col, here, p.guard);
+        if (GATED) b[k].load(p.b, p.rows, p.cols, row, col, here, p.guard);
       }
 #pragma unroll
-      for (int k = 0; k < kRows; ++k) {
-        const int64_t row = r + k * kWarps;
+      for (int k = 0; k < kBatch; ++k) {
+        const int64_t row = r + k * kRowLanes;
         if (row >= r1) break;
-        float g[8], x[8], d[8];
+        float2 g[4], x[4], d[4];
         dy[k].get(g);
+        if (kAct) a[k].get(x);
         if (GATED) {
-          float u[8], du[8], h[8];
-          a[k].get(x);
-          b[GATED ? k : 0].get(u);
-          with_act(p.act, [&](auto act) {
+          float2 u[4], du[4], h[4];
+          b[k].get(u);
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-              const float2 ge = make_float2(g[e], g[e + 1]), ue = make_float2(u[e], u[e + 1]);
-              float2 f, df;
-              act_grad<decltype(act)::value>(make_float2(x[e], x[e + 1]), f, df);
-              *reinterpret_cast<float2*>(&d[e]) = mul(mul(ge, ue), df);
-              *reinterpret_cast<float2*>(&du[e]) = mul(ge, f);
-              *reinterpret_cast<float2*>(&h[e]) = mul(f, ue);
-            }
-          });
+          for (int e = 0; e < 4; ++e) {
+            float2 f, df;
+            act_grad<ACT>(x[e], f, df);
+            d[e] = mul(mul(g[e], u[e]), df);
+            du[e] = mul(g[e], f);
+            h[e] = mul(f, u[e]);
+          }
           if (p.da) {
-            put8(p.da, p.ldd, p.rows, p.cols, row, col, n, true, d, p.guard);
-            put8(p.db, p.ldd, p.rows, p.cols, row, col, n, true, du, p.guard);
+            put8<VEC>(p.da, p.ldd, p.rows, p.cols, row, col, n, d, p.guard);
+            put8<VEC>(p.db, p.ldd, p.rows, p.cols, row, col, n, du, p.guard);
           }
-          if (p.h) put8(p.h, p.ldh, p.rows, p.cols, row, col, n, p.h_vec, h, p.guard);
+          if (p.h) put8<VEC>(p.h, p.ldh, p.rows, p.cols, row, col, n, h, p.guard);
         } else {
-          if (p.a.data) {
-            a[k].get(x);
-            with_act(p.act, [&](auto act) {
 #pragma unroll
-              for (int e = 0; e < 8; e += 2) {
-                float2 f, df;
-                act_grad<decltype(act)::value>(make_float2(x[e], x[e + 1]), f, df);
-                *reinterpret_cast<float2*>(&d[e]) = mul(make_float2(g[e], g[e + 1]), df);
-              }
-            });
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) d[e] = g[e];
+          for (int e = 0; e < 4; ++e) {
+            float2 f, df;
+            if (kAct) act_grad<ACT>(x[e], f, df);
+            d[e] = kAct ? mul(g[e], df) : g[e];
+            if (SUMS) sum[e] = add(sum[e], d[e]);
           }
-          if (p.da) put8(p.da, p.ldd, p.rows, p.cols, row, col, n, true, d, p.guard);
-          if (SUMS) {
-#pragma unroll
-            for (int e = 0; e < (SUMS ? 8 : 1); ++e) sum[e] += d[e];
-          }
+          if (p.da) put8<VEC>(p.da, p.ldd, p.rows, p.cols, row, col, n, d, p.guard);
         }
       }
     }
   }
   if constexpr (SUMS) {
-    __shared__ float part[kWarps][kStrip];
+    __shared__ float warps[kThreads / 32][kStrip], strip[kStrip];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) part[warp][8 * lane + e] = sum[e];
+    for (int e = 0; e < 4; ++e) {  // over the warp's four rows
+#pragma unroll
+      for (int m = kLanes; m < 32; m *= 2)
+        sum[e] = add(sum[e], make_float2(__shfl_xor_sync(0xffffffffu, sum[e].x, m), __shfl_xor_sync(0xffffffffu, sum[e].y, m)));
+      if (threadIdx.x % 32 < kLanes) *reinterpret_cast<float2*>(&warps[threadIdx.x / 32][8 * (threadIdx.x % kLanes) + 2 * e]) = sum[e];
+    }
     __syncthreads();
+    float s = 0.0f;
+    if (threadIdx.x < kStrip) {
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) s += warps[w][threadIdx.x];
+      strip[threadIdx.x] = s;
+    }
     const int c = (int)blockIdx.x * kStrip + (int)threadIdx.x;
-    if (c < p.cols) {
-      float s = 0.0f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) s += part[w][threadIdx.x];
-      if (p.row_blocks == 1) put_at(p.guard, f8::kSiteOut, p.dbias, c, p.cols, s);
-      else put_at(p.guard, f8::kSitePart, p.partial, (int64_t)blockIdx.y * p.cols + c, (int64_t)p.row_blocks * p.cols, s);
+    tc::cluster_sync();
+    if (blockIdx.y == 0 && threadIdx.x < kStrip && c < p.cols) {
+      for (int k = 1; k < p.row_blocks; ++k) {  // (the row blocks are the cluster)
+        float v;
+        asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::map_to_rank(smem_addr(&strip[threadIdx.x]), (uint32_t)k)) : "memory");
+        s += v;
+      }
+      put_at(p.guard, f8::kSiteOut, p.dbias, c, p.cols, s);
     }
+    tc::cluster_sync();  // no CTA leaves while its sums may be read
   }
 }
 
-// dbias from the row blocks' sums, a column per lane, 8 warps over the blocks.
-__global__ void __launch_bounds__(kThreads) linear_bias_kernel(const LinearGradParams p) {
+// Up to three matrices one behind the other, in chunks of 8 columns.
+__global__ void __launch_bounds__(kThreads) linear_expand_kernel(const __grid_constant__ LinearExpandParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  __shared__ float part[kWarps][32];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int c = (int)blockIdx.x * 32 + lane;
-  float s = 0.0f;
-  if (c < p.cols)
-    for (int b = warp; b < p.row_blocks; b += kWarps)
-      s += get_at(p.guard, f8::kSitePart, p.partial, (int64_t)b * p.cols + c, (int64_t)p.row_blocks * p.cols);
-  part[warp][lane] = s;
-  __syncthreads();
-  if (warp == 0 && c < p.cols) {
-    s = 0.0f;
+  int which = 0;
+  int64_t block = blockIdx.x;
+  while (block >= p.part[which].blocks) block -= p.part[which++].blocks;
+  const LinearExpand& m = p.part[which];
+  const int chunks = (m.cols + 7) / 8;
+  const int64_t total = m.rows * chunks;
+  const auto run = [&](auto codes) {
+    constexpr int kChunks = kExpandChunks;
+    KeptLoad<decltype(codes)::value, false> v[kChunks];
+    int64_t row[kChunks];
+    int col[kChunks], n[kChunks];
 #pragma unroll
-    for (int w = 0; w < kWarps; ++w) s += part[w][lane];
-    put_at(p.guard, f8::kSiteOut, p.dbias, c, p.cols, s);
-  }
-}
-
-template <bool CODES>
-__global__ void __launch_bounds__(kThreads) linear_expand_kernel(const LinearKeptIn m, int64_t rows, int cols, void* dst, int64_t ldd,
-                                                                 const Guard guard) {
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int chunks = (cols + 7) / 8;
-  const int64_t total = rows * chunks, step = (int64_t)gridDim.x * kThreads;
-  constexpr int kBatch = 4;
-  for (int64_t i = (int64_t)blockIdx.x * kThreads + threadIdx.x; i < total; i += kBatch * step) {
-    KeptLoad<CODES> v[kBatch];
-#pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int64_t j = i + k * step, row = j < total ? j / chunks : 0;
-      const int col = (int)(j - row * chunks) * 8;
-      v[k].load(m, rows, cols, row, j < total ? col : 0, j < total ? min(8, cols - col) : 0, guard);
+    for (int k = 0; k < kChunks; ++k) {
+      const int64_t i = (block * kChunks + k) * kThreads + threadIdx.x, j = i < total ? i : 0;
+      row[k] = total <= 0x7fffffff ? (uint32_t)j / (uint32_t)chunks : j / chunks;
+      col[k] = (int)(j - row[k] * chunks) * 8;
+      n[k] = i < total ? min(8, m.cols - col[k]) : 0;
+      v[k].load(m.m, m.rows, m.cols, row[k], col[k], n[k], p.guard);
     }
 #pragma unroll
-    for (int k = 0; k < kBatch; ++k) {
-      const int64_t j = i + k * step;
-      if (j >= total) break;
-      const int64_t row = j / chunks;
-      const int col = (int)(j - row * chunks) * 8;
-      float x[8];
+    for (int k = 0; k < kChunks; ++k) {
+      float2 x[4];
       v[k].get(x);
-      put8(dst, ldd, rows, cols, row, col, min(8, cols - col), true, x, guard);
+      // (whole chunks: rows of the copy have room for them, and nothing reads behind their ends)
+      if (n[k] > 0 && in_range(p.guard.fault, p.guard.word, f8::kSitePart, row[k] * m.ldd + col[k], 8, m.rows * m.ldd)) {
+        Chunk<__nv_bfloat16> c;
+        c.put(&x[0].x);
+        *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(m.dst) + row[k] * m.ldd + col[k]) = c.raw;
+      }
     }
-  }
+  };
+  if (m.m.scale) run(std::true_type{});
+  else           run(std::false_type{});
 }
 
-template <typename... Args>
-cudaError_t launch(void (*kernel)(Args...), dim3 grid, cudaStream_t stream, Args... args) {
+template <typename P>
+cudaError_t launch(void (*kernel)(P), dim3 grid, int cluster_y, const P& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(kThreads);
   cfg.stream = stream;
-  cudaLaunchAttribute attr[1];
+  cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = 1;
+  attr[1].val.clusterDim.y = (unsigned)cluster_y;
+  attr[1].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
+  cfg.numAttrs = cluster_y > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <bool GATED, bool CODES, bool VEC, bool SUMS>
+cudaError_t launch_act(const LinearGradParams& p, cudaStream_t stream) {
+  const dim3 grid((unsigned)((p.cols + kStrip - 1) / kStrip), (unsigned)p.row_blocks);
+  cudaError_t e = cudaErrorInvalidValue;
+  with_act(p.act, [&](auto act) { e = launch(linear_grad_kernel<decltype(act)::value, GATED, CODES, VEC, SUMS>, grid, SUMS ? p.row_blocks : 1, p, stream); });
+  return e;
+}
+template <bool VEC>
+cudaError_t launch_form(const LinearGradParams& p, cudaStream_t stream) {
+  const bool codes = p.a.scale != nullptr;
+  if (p.b.data) return codes ? launch_act<true, true, VEC, false>(p, stream) : launch_act<true, false, VEC, false>(p, stream);
+  if (p.dbias) return codes ? launch_act<false, true, VEC, true>(p, stream) : launch_act<false, false, VEC, true>(p, stream);
+  return codes ? launch_act<false, true, VEC, false>(p, stream) : launch_act<false, false, VEC, false>(p, stream);
 }
 
 }  // namespace
 }  // namespace lin
 
-int linear_grad_row_blocks(int64_t rows, int cols, int sm_count) {
-  // four CTAs per SM, no fewer than 32 rows each
+int linear_grad_row_blocks(int64_t rows, int cols, bool sums, bool clusters, int sm_count) {
+  if (sums && !clusters) return 1;
   const int64_t strips = (cols + lin::kStrip - 1) / lin::kStrip;
-  int64_t blocks = (8 * (int64_t)sm_count + strips - 1) / strips;
-  if (blocks > (rows + 31) / 32) blocks = (rows + 31) / 32;
-  return (int)(blocks < 1 ? 1 : blocks > 65535 ? 65535 : blocks);
+  // eight CTAs per SM, of no fewer rows than two batches
+  const int64_t want = (8 * (int64_t)sm_count + strips - 1) / strips, most = (rows + 2 * lin::kBatch * lin::kRowLanes - 1) / (2 * lin::kBatch * lin::kRowLanes);
+  int64_t blocks = want < most ? want : most;
+  if (!sums) return (int)(blocks < 1 ? 1 : blocks > 65535 ? 65535 : blocks);
+  int n = 8;  // a cluster
+  while (n > 1 && n > most) n /= 2;
+  return n;
 }
 
 cudaError_t launch_linear_grad(const LinearGradParams& p, cudaStream_t stream) {
-  using namespace lin;
-  const dim3 grid((unsigned)((p.cols + kStrip - 1) / kStrip), (unsigned)p.row_blocks);
-  const bool codes = p.a.scale != nullptr, sums = p.dbias != nullptr;
-  cudaError_t e;
-  if (p.b.data) e = launch(codes ? linear_grad_kernel<true, true, false> : linear_grad_kernel<true, false, false>, grid, stream, p);
-  else if (sums) e = launch(codes ? linear_grad_kernel<false, true, true> : linear_grad_kernel<false, false, true>, grid, stream, p);
-  else e = launch(codes ? linear_grad_kernel<false, true, false> : linear_grad_kernel<false, false, false>, grid, stream, p);
-  if (e == cudaSuccess && sums && p.row_blocks > 1) e = launch(linear_bias_kernel, dim3((unsigned)((p.cols + 31) / 32)), stream, p);
-  return e;
+  return p.vec ? lin::launch_form<true>(p, stream) : lin::launch_form<false>(p, stream);
 }
 
-cudaError_t launch_linear_expand(const LinearKeptIn& m, int64_t rows, int64_t cols, void* dst, int64_t ldd, const Guard& guard,
-                                 cudaStream_t stream) {
-  const int64_t blocks = (rows * ((cols + 7) / 8) + 4 * lin::kThreads - 1) / (4 * lin::kThreads);
-  const dim3 grid((unsigned)(blocks < 2048 ? blocks : 2048));
-  return lin::launch(m.scale ? lin::linear_expand_kernel<true> : lin::linear_expand_kernel<false>, grid, stream, m, rows, (int)cols, dst, ldd,
-                     guard);
+cudaError_t launch_linear_expand(LinearExpandParams& p, cudaStream_t stream) {
+  int64_t blocks = 0;
+  for (LinearExpand& m : p.part) {
+    m.blocks = (m.rows * ((m.cols + 7) / 8) + lin::kExpandChunks * lin::kThreads - 1) / (lin::kExpandChunks * lin::kThreads);
+    blocks += m.blocks;
+  }
+  if (blocks == 0) return cudaSuccess;
+  if (blocks > 0x7fffffff) return cudaErrorInvalidValue;
+  return lin::launch(lin::linear_expand_kernel, dim3((unsigned)blocks), 1, p, stream);
 }
 
 }  // namespace sgemm_impl

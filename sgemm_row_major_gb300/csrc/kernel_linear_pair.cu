@@ -90,12 +90,13 @@ struct Pieces {
   }
 };
 
-template <bool F32, int BYTES>
+// RESIDUAL: its rows are not aligned, so it is added where lanes run along them (the piece is then FP32 until it is written).
+template <bool F32, bool RESIDUAL = false, int BYTES>
 __device__ __forceinline__ void emit(Pieces<BYTES>& pieces, const CUtensorMap* map, bool tma, void* base, int64_t ld, const LinearOut& o,
                                      const LinearJob& j, unsigned site, int row0, int col0, const float (&v)[32]) {
   const int lane = threadIdx.x & 31;
   uint8_t* at = pieces.next();
-  if constexpr (F32) {
+  if constexpr (F32 || RESIDUAL) {
 #pragma unroll
     for (int e = 0; e < 8; ++e)
       *reinterpret_cast<float4*>(at + lane * 128 + 16 * (e ^ (lane & 7))) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
@@ -106,7 +107,7 @@ __device__ __forceinline__ void emit(Pieces<BYTES>& pieces, const CUtensorMap* m
           make_uint4(pack2(v[8 * e], v[8 * e + 1]), pack2(v[8 * e + 2], v[8 * e + 3]), pack2(v[8 * e + 4], v[8 * e + 5]),
                      pack2(v[8 * e + 6], v[8 * e + 7]));
   }
-  if (tma) {
+  if (!RESIDUAL && tma) {
     fence_proxy_async_smem();
     __syncwarp();
     if (lane == 0) {
@@ -120,17 +121,30 @@ __device__ __forceinline__ void emit(Pieces<BYTES>& pieces, const CUtensorMap* m
     __syncwarp();
     const int rows = min(32, j.M - row0);
     if (col0 + lane < j.N && rows > 0 &&
-        in_range(o.guard.fault, o.guard.word, site, (int64_t)row0 * ld + col0 + lane, (rows - 1) * ld + 1, extent(j.M, ld, j.N))) {
+        in_range(o.guard.fault, o.guard.word, site, (int64_t)row0 * ld + col0 + lane, (rows - 1) * ld + 1, extent(j.M, ld, j.N)) &&
+        (!RESIDUAL || r_ok(o, j, row0, col0 + lane, (rows - 1) * o.ldr + 1))) {
       const int64_t first = (int64_t)row0 * ld + col0 + lane;
-      if constexpr (F32) {
-        float* d = static_cast<float*>(base) + first;
-#pragma unroll 8
-        for (int r = 0; r < rows; ++r, d += ld) *d = *reinterpret_cast<const float*>(at + r * 128 + 16 * ((lane >> 2) ^ (r & 7)) + 4 * (lane & 3));
+      const auto f32_at = [&](int r) { return *reinterpret_cast<const float*>(at + r * 128 + 16 * ((lane >> 2) ^ (r & 7)) + 4 * (lane & 3)); };
+      using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+      T* d = static_cast<T*>(base) + first;
+      if constexpr (RESIDUAL) {
+        const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(o.residual) + (int64_t)row0 * o.ldr + col0 + lane;
+#pragma unroll 1
+        for (int r0 = 0; r0 < rows; r0 += 16) {  // 16 rows' values on their way together
+          __nv_bfloat16 u[16];
+#pragma unroll
+          for (int k = 0; k < 16; ++k, x += o.ldr)
+            if (r0 + k < rows) u[k] = *x;
+#pragma unroll
+          for (int k = 0; k < 16; ++k, d += ld)
+            if (r0 + k < rows) f8::from_float(d, f32_at(r0 + k) + __bfloat162float(u[k]));
+        }
       } else {
-        uint16_t* d = static_cast<uint16_t*>(base) + first;
 #pragma unroll 8
-        for (int r = 0; r < rows; ++r, d += ld)
-          *d = *reinterpret_cast<const uint16_t*>(at + r * 64 + 16 * ((lane >> 3) ^ ((r >> 1) & 3)) + 2 * (lane & 7));
+        for (int r = 0; r < rows; ++r, d += ld) {
+          if constexpr (F32) *d = f32_at(r);
+          else               *d = *reinterpret_cast<const T*>(at + r * 64 + 16 * ((lane >> 3) ^ ((r >> 1) & 3)) + 2 * (lane & 7));
+        }
       }
     }
   }
@@ -149,44 +163,62 @@ __device__ __forceinline__ void add_to(float* v, const float* x) {
   }
 }
 
-// bias[col0 ..] is added to 32 sums of N.
-__device__ __forceinline__ void add_bias(const LinearOut& o, int N, int col0, float (&v)[32]) {
-  const __nv_bfloat16* b = static_cast<const __nv_bfloat16*>(o.bias);
-  if (o.bias_vec && col0 + 32 <= N) {
-    if (!in_range(o.guard.fault, o.guard.word, f8::kSiteIn, col0, 32, N)) return;
+// 32 values of the bias, and of one row of the residual (aligned rows): sent for before the sums are waited for.
+struct Bias {
+  uint4 c[4];
+  __device__ __forceinline__ static bool whole(const LinearOut& o, int N, int col0) { return o.bias_vec && col0 + 32 <= N; }
+  __device__ __forceinline__ void load(const LinearOut& o, int N, int col0) {
+    if (whole(o, N, col0) && in_range(o.guard.fault, o.guard.word, f8::kSiteIn, col0, 32, N)) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      Chunk<__nv_bfloat16> c;
-      float x[8];
-      c.raw = __ldg(reinterpret_cast<const uint4*>(b + col0) + e);
-      c.get(x);
-      add_to<8>(&v[8 * e], x);
+      for (int e = 0; e < 4; ++e) c[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(o.bias) + col0) + e);
     }
-    return;
   }
+  __device__ __forceinline__ void add(const LinearOut& o, int N, int col0, float (&v)[32]) const {
+    if (whole(o, N, col0)) {
 #pragma unroll
-  for (int e = 0; e < 32; ++e)
-    if (col0 + e < N) v[e] += __bfloat162float(get_at(o.guard, f8::kSiteIn, b, col0 + e, N));
-}
+      for (int e = 0; e < 4; ++e) {
+        Chunk<__nv_bfloat16> b;
+        float x[8];
+        b.raw = c[e];
+        b.get(x);
+        add_to<8>(&v[8 * e], x);
+      }
+      return;
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e)
+      if (col0 + e < N) v[e] += __bfloat162float(get_at(o.guard, f8::kSiteIn, static_cast<const __nv_bfloat16*>(o.bias), col0 + e, N));
+  }
+};
 
-// The residual's 32 values of one row, sent for before the sums are waited for.
-template <bool VEC>
 struct Residual {
-  f8::Loading<__nv_bfloat16, VEC> c[4];
+  uint4 c[4];
   __device__ __forceinline__ void load(const LinearOut& o, const LinearJob& j, int row, int col0) {
-    const f8::Rows<__nv_bfloat16> m(o.residual, j.M, o.ldr, j.N, o.guard);
-    const __nv_bfloat16* p = m.base + (int64_t)row * o.ldr + col0;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const int n = row < j.M ? max(0, min(8, j.N - col0 - 8 * e)) : 0;
-      c[e].load(p + 8 * e, VEC && n < 8 ? 0 : n, m);
+      c[e] = make_uint4(0u, 0u, 0u, 0u);
+      const int n = min(8, j.N - col0 - 8 * e);
+      if (row >= j.M || n <= 0 || !r_ok(o, j, row, col0 + 8 * e, n)) continue;
+      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(o.residual) + (int64_t)row * o.ldr + col0 + 8 * e;
+      if (n == 8) {
+        c[e] = *reinterpret_cast<const uint4*>(p);
+      } else {
+        float x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) x[k] = k < n ? __bfloat162float(p[k]) : 0.0f;
+        Chunk<__nv_bfloat16> b;
+        b.put(x);  // exact: every value was BF16
+        c[e] = b.raw;
+      }
     }
   }
   __device__ __forceinline__ void add(float (&v)[32]) const {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
+      Chunk<__nv_bfloat16> b;
       float x[8];
-      c[e].get().get(x);
+      b.raw = c[e];
+      b.get(x);
       add_to<8>(&v[8 * e], x);
     }
   }
@@ -216,8 +248,9 @@ __device__ __forceinline__ void put_codes(const LinearOut& o, const LinearJob& j
   }
 }
 
-// The largest finite |v| so far (a NaN is never the larger one; infinities are looked for only where there are some).
-__device__ __forceinline__ float largest_of(float m, const float (&v)[32]) {
+// The largest finite |v| so far (a NaN is never the larger one; infinities are looked for only where there are some, and
+// remembered).
+__device__ __forceinline__ float largest_of(float m, bool& infinite, const float (&v)[32]) {
   float x = 0.0f, y = 0.0f;
 #pragma unroll
   for (int k = 0; k < 32; k += 2) {
@@ -226,6 +259,7 @@ __device__ __forceinline__ float largest_of(float m, const float (&v)[32]) {
   }
   x = fmaxf(x, y);
   if (x > f8::kMaxFloat) {
+    infinite = true;
     x = 0.0f;
 #pragma unroll
     for (int k = 0; k < 32; ++k) x = fmaxf(x, f8::finite_abs(v[k]));
@@ -366,10 +400,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         for (int tile = cl; ok && tile < tiles; tile += p.clusters) {
           const LinearJob& j = p.job[Place(p, tile).job];
           const uint32_t astep = step_of(j.a_mn), bstep = step_of(j.b_mn), idesc = j.idesc;
-          const int kt = j.k_tiles * j.segments, fold = j.fold;
-          for (int g = 0; ok && g < kt; g += fold) {
-            // a chunk: the K tiles of one accumulator
-            const int n = min(fold, kt - g);
+          const int kt = j.k_tiles * j.segments;
+          int n = j.fold0;  // a chunk: the K tiles of one accumulator
+          for (int g = 0; ok && g < kt; g += n, n = j.fold) {
+            n = min(n, kt - g);
             ok = b_lap == 0 || poll_wait(smem_addr(&acc_empty[b]), (b_lap - 1) & 1u, p.timeout_ns);
             tmem_fence_after_sync();
             for (int i = 0; ok && i < n; ++i) {
@@ -428,7 +462,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const LinearJob& j = p.job[at.job];
       const int row0 = at.tm * BM + BMC * (int)rank + 32 * q, row = row0 + lane;
       const int c0 = at.tn * TD + cols * part;  // this thread's first column of D
-      const int kt = j.k_tiles * j.segments, fold = j.fold;
+      const int kt = j.k_tiles * j.segments;
       uint32_t acc;
       const auto next = [&] {  // waits for the next accumulator
         ok = poll_wait(smem_addr(&acc_full[b]), b_lap & 1u, p.timeout_ns);
@@ -446,31 +480,32 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++b_lap;
         }
       };
-      if (kt > fold) {
+      if (kt > j.fold0) {
         // several accumulators: all but the last are added in registers, and these sums to the last one where it lies
 #pragma unroll
         for (int e = 0; e < TN / 2; ++e) sum[e] = 0.0f;
-        for (int g = 0; g + fold < kt; g += fold) {
+        for (int g = j.fold0; g < kt; g += j.fold) {  // (g: K tiles up to this accumulator's end)
           if (!next()) break;
 #pragma unroll
-          for (int e = 0; e < loads; ++e) {
-            float v[32];
-            tmem_ld32(acc + (uint32_t)column(e), v);
+          for (int e = 0; e < 2 * loads; ++e) {
+            float v[16];
+            tmem_ld16(acc + (uint32_t)(column(e / 2) + 16 * (e % 2)), v);
             tmem_wait_ld();
-            if (e == loads - 1) release();
+            if (e == 2 * loads - 1) release();
             tmem_ld_ready(v);
-            add_to<32>(&sum[32 * e], v);
+            add_to<16>(&sum[16 * e], v);
           }
         }
         if (!ok || !next()) break;
 #pragma unroll
-        for (int e = 0; e < loads; ++e) {
-          float v[32];
-          tmem_ld32(acc + (uint32_t)column(e), v);
+        for (int e = 0; e < 2 * loads; ++e) {
+          const uint32_t at16 = acc + (uint32_t)(column(e / 2) + 16 * (e % 2));
+          float v[16];
+          tmem_ld16(at16, v);
           tmem_wait_ld();
           tmem_ld_ready(v);
-          add_to<32>(v, &sum[32 * e]);
-          tmem_st32(acc + (uint32_t)column(e), v);
+          add_to<16>(v, &sum[16 * e]);
+          tmem_st16(at16, v);
         }
         tmem_wait_st();
       } else if (!next()) {
@@ -478,31 +513,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       // ---------------------------------------------- epilogue
       constexpr uint32_t up = TN / 2;  // gated: from a column of gate to up's
-      pieces.set(j.f32 != 0);
+      pieces.set(j.f32 != 0 || (!GATED && o.residual && !o.r_vec));
       float inv[2] = {1.0f, 1.0f};     // of the scales of what is kept in 8 bits
-      bool bias = !GATED && o.bias;    // still to be added
+      bool odd = false;                // an infinity among them
+      bool add_bias = !GATED && o.bias;  // still to be done
       if (o.keep == 2) {
         float m[2] = {0.0f, 0.0f};
 #pragma unroll 1
         for (int c = 0; c < cols; c += 32) {
           float v[32];
+          Bias bias;
           tmem_ld32(acc + (uint32_t)c, v);
+          if (add_bias) bias.load(o, j.N, c0 + c);
           tmem_wait_ld();
           tmem_ld_ready(v);
-          if (bias) {
-            add_bias(o, j.N, c0 + c, v);
+          if (add_bias) {
+            bias.add(o, j.N, c0 + c, v);
             tmem_st32(acc + (uint32_t)c, v);
           }
-          m[0] = largest_of(m[0], v);
+          m[0] = largest_of(m[0], odd, v);
           if constexpr (GATED) {
             tmem_ld32(acc + up + (uint32_t)c, v);
             tmem_wait_ld();
             tmem_ld_ready(v);
-            m[1] = largest_of(m[1], v);
+            m[1] = largest_of(m[1], odd, v);
           }
         }
-        if (bias) tmem_wait_st();
-        bias = false;
+        if (add_bias) tmem_wait_st();
+        add_bias = false;
+        odd = __any_sync(0xffffffffu, odd);
         if (cols < 128) {  // the other half of the group is with the warp of the other column half
           float* slot = &largest[0][32 * q + lane];
           constexpr int kUp = GATED ? BMC : 0;
@@ -534,11 +573,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           inv[w] = __fdiv_rn(1.0f, scale);
         }
       }
+      Residual following;  // of the next 32 columns
+      const bool direct = !GATED && o.residual && o.r_vec;
+      if (direct) following.load(o, j, row, c0);
 #pragma unroll 1
       for (int c = 0; c < cols; c += 32) {
         const bool last = c + 32 == cols;
         float v[32];
         tmem_ld32(acc + (uint32_t)c, v);
+        const auto codes = [&](int which, const float (&x)[32]) {
+          if (odd) put_codes<true>(o, j, which, row, c0 + c, x, inv[which]);
+          else     put_codes<false>(o, j, which, row, c0 + c, x, inv[which]);
+        };
         if constexpr (GATED) {
           float u[32];
           tmem_ld32(acc + up + (uint32_t)c, u);
@@ -550,8 +596,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             emit<false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
             emit<false>(pieces, &maps.kept[1], o.kept[1].vec, o.kept[1].data, o.kept[1].ld, o, j, f8::kSiteCodes, row0, c0 + c, u);
           } else if (o.keep == 2) {
-            put_codes<true>(o, j, 0, row, c0 + c, v, inv[0]);
-            put_codes<true>(o, j, 1, row, c0 + c, u, inv[1]);
+            codes(0, v);
+            codes(1, u);
           }
           with_act(o.act, [&](auto act) {
 #pragma unroll
@@ -563,18 +609,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           });
           emit<false>(pieces, &maps.d[0], j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
         } else {
-          Residual<true> ra;
-          Residual<false> rb;
-          if (o.residual) {
-            if (o.r_vec && c0 + c + 32 <= j.N) ra.load(o, j, row, c0 + c);
-            else                               rb.load(o, j, row, c0 + c);
-          }
+          const Residual residual = following;
+          if (direct && !last) following.load(o, j, row, c0 + c + 32);
+          Bias bias;
+          if (add_bias) bias.load(o, j.N, c0 + c);
           tmem_wait_ld();
           if (last) release();
           tmem_ld_ready(v);
-          if (bias) add_bias(o, j.N, c0 + c, v);
+          if (add_bias) bias.add(o, j.N, c0 + c, v);
           if (o.keep == 1) emit<false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
-          else if (o.keep == 2) put_codes<true>(o, j, 0, row, c0 + c, v, inv[0]);
+          else if (o.keep == 2) codes(0, v);
           with_act(o.act, [&](auto act) {
 #pragma unroll
             for (int k = 0; k < 32; k += 2) {
@@ -583,12 +627,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               v[k + 1] = f.y;
             }
           });
-          if (o.residual) {
-            if (o.r_vec && c0 + c + 32 <= j.N) ra.add(v);
-            else                               rb.add(v);
+          if (direct) residual.add(v);
+          const auto write = [&](auto f32, auto with_residual) {
+            emit<decltype(f32)::value, decltype(with_residual)::value>(pieces, &maps.d[at.job], j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0,
+                                                                       c0 + c, v);
+          };
+          constexpr std::true_type yes{};
+          constexpr std::false_type no{};
+          if (o.residual && !direct) {
+            if (j.f32) write(yes, yes);
+            else       write(no, yes);
+          } else {
+            if (j.f32) write(yes, no);
+            else       write(no, no);
           }
-          if (j.f32) emit<true>(pieces, &maps.d[at.job], j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
-          else       emit<false>(pieces, &maps.d[at.job], j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
         }
       }
     }

@@ -22,6 +22,7 @@ constexpr int kThreads = 32 * (kFirstFold + kFoldWarps);
 constexpr int kMaxStages = kLinearShortMaxStages;
 static_assert(kThreads == kLinearShortThreads, "the plan's figure");
 constexpr int kMaxSmem = 220 * 1024;
+constexpr int kFold = 8;  // K tiles that are summed in one accumulator (their sums drift: kernel_linear_pair.cu)
 constexpr int kPitch = BL + 4;  // words from token to token of a share: reads and writes of 32 lanes hit different banks
 __host__ __device__ constexpr int share_bytes(int tile_s, bool gated) { return (gated ? 2 : 1) * tile_s * kPitch * 4; }
 
@@ -163,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
     uint32_t lap = 0, b_lap = 0;
     bool ok = true;
     while (ok && t < units) {
-      const int n = min(j.fold, units - t);
+      const int n = min(kFold, units - t);
       ok = b_lap == 0 || poll_wait(smem_addr(&acc_empty[b]), (b_lap - 1) & 1u, p.timeout_ns);
       tmem_fence_after_sync();
       for (int i = 0; ok && i < n; ++i) {
@@ -207,7 +208,7 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
     for (int e = 0; e < kParts * TS; ++e) sum[e] = 0.0f;
     int b = 0;
     uint32_t b_lap = 0;
-    for (int t = 0; t < units; t += j.fold) {
+    for (int t = 0; t < units; t += kFold) {
       if (!poll_wait(smem_addr(&acc_full[b]), b_lap & 1u, p.timeout_ns)) {
         if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
         break;

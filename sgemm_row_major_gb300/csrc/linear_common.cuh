@@ -84,7 +84,7 @@ __device__ __forceinline__ float2 act_of(float2 a) {
 
 // f(the activation as a constant): one branch around a loop over elements, whose steps then overlap.
 template <typename F>
-__device__ __forceinline__ void with_act(int act, const F& f) {
+__host__ __device__ __forceinline__ void with_act(int act, const F& f) {
   switch (act) {
     case SGEMM_ACT_RELU: return f(std::integral_constant<int, SGEMM_ACT_RELU>{});
     case SGEMM_ACT_SILU: return f(std::integral_constant<int, SGEMM_ACT_SILU>{});

@@ -42,7 +42,7 @@ struct LinearJob {
   int f32 = 0;
   int tiles_m = 0, tiles_n = 0;
   int k_tiles = 0, segments = 1; // of 64 k, per segment
-  int fold = 0;                  // K tiles that are summed in one accumulator
+  int fold0 = 0, fold = 1;       // K tiles that are summed in the first accumulator, and in each further one
   int a_mn = 0, b_mn = 0;        // 1: the stored rows run along M (N), not along K
   uint32_t idesc = 0;
   int a[2] = {0, 0}, b[2] = {0, 0};  // maps of the operands
@@ -92,23 +92,32 @@ struct LinearGradParams {
   int cols = 0;
   const void* dy = nullptr;
   int64_t lddy = 0;
-  int dy_vec = 0;
   LinearKeptIn a, b;             // b: gated
   int act = 0;
   void *da = nullptr, *db = nullptr, *h = nullptr;  // nullptr: not wanted (da and db: aligned rows)
   int64_t ldd = 0, ldh = 0;
-  int h_vec = 0;
-  float* partial = nullptr;      // [row blocks][cols] sums of dA (nullptr: dbias is not wanted)
-  float* dbias = nullptr;
+  float* dbias = nullptr;        // nullptr: not wanted
   int row_blocks = 0;
+  int vec = 0;                   // 1: whole chunks of 8 columns, all of which can be read and written at once
   Guard guard;
 };
-int linear_grad_row_blocks(int64_t rows, int cols, int sm_count);
+int linear_grad_row_blocks(int64_t rows, int cols, bool sums, bool clusters, int sm_count);
 cudaError_t launch_linear_grad(const LinearGradParams& p, cudaStream_t stream);
 
-// A stored matrix as aligned BF16 rows (ldd a multiple of 8): BF16 of any alignment copied, 8-bit values times their scales.
-cudaError_t launch_linear_expand(const LinearKeptIn& m, int64_t rows, int64_t cols, void* dst, int64_t ldd, const Guard& guard,
-                                 cudaStream_t stream);
+// Stored matrices as aligned BF16 rows (ldd a multiple of 8): BF16 of any alignment copied, 8-bit values times their scales.
+struct LinearExpand {
+  LinearKeptIn m;
+  int64_t rows = 0;
+  int cols = 0;
+  void* dst = nullptr;
+  int64_t ldd = 0;
+  int64_t blocks = 0;            // of the launch
+};
+struct LinearExpandParams {
+  LinearExpand part[3];
+  Guard guard;
+};
+cudaError_t launch_linear_expand(LinearExpandParams& p, cudaStream_t stream);
 
 // Map over `outer` rows of `inner` BF16 values (row stride ld elements, a multiple of 8): boxes of 64 x box_outer,
 // 128-byte swizzle, zeros outside.
