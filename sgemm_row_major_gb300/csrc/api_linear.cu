@@ -278,6 +278,8 @@ struct Launch {
       return maps_used++;
     };
     int64_t tiles = 0, steps = 0;
+    bool fold = false;
+    for (int i = 0; i < count; ++i) fold |= fold_first(list[i]) < list[i].shape.k_tiles();
     for (int i = 0; i < count; ++i) {
       const Product& r = list[i];
       LinearJob& j = p.job[i];
@@ -291,7 +293,7 @@ struct Launch {
       j.d_vec = rows_at(r.d, r.ldd, size, 4 * size);
       j.k_tiles = (int)ceil_div(r.shape.K, 64);
       j.segments = r.shape.segments;
-      j.fold0 = r.f32 || out.keep == 2 ? kFoldFirst : kFoldNone;
+      j.fold0 = fold_first(r);
       j.fold = kFold;
       j.a_mn = r.a_mn;
       j.b_mn = r.b_mn;
@@ -299,7 +301,7 @@ struct Launch {
         j.tiles_m = (int)ceil_div(r.shape.M, 256);
         j.tiles_n = (int)ceil_div(r.shape.N, gated ? c.tile / 2 : c.tile);
         j.idesc = instruction(r.a_mn, r.b_mn, 256, c.tile);
-        if (j.d_tma && *e == cudaSuccess) *e = encode_out_map(r.d, r.shape.N, r.shape.M, r.ldd, !r.f32, &maps.d[i]);
+        if (j.d_tma && *e == cudaSuccess) *e = encode_linear_out_map(r.d, r.shape.N, r.shape.M, r.ldd, !r.f32, r.f32 ? 32 : linear_pair_box(c.tile, gated, fold), &maps.d[i]);
       } else {
         j.tiles_m = (int)ceil_div(r.shape.M, c.tile);
         j.tiles_n = (int)ceil_div(r.shape.N, 128);
@@ -317,7 +319,8 @@ struct Launch {
       if (!k.data) continue;
       k.vec = out.keep == 2 ? rows_at(k.data, k.ld, 1, 16) : tma_writes(k.data, k.ld, list[0].shape.N, 2);
       out.kept_vec8[i] = rows_at(k.data, k.ld, 2, 8);
-      if (pair && out.keep == 1 && k.vec && *e == cudaSuccess) *e = encode_out_map(k.data, list[0].shape.N, list[0].shape.M, k.ld, true, &maps.kept[i]);
+      if (pair && out.keep == 1 && k.vec && *e == cudaSuccess)
+        *e = encode_linear_out_map(k.data, list[0].shape.N, list[0].shape.M, k.ld, true, linear_pair_box(c.tile, gated, fold), &maps.kept[i]);
     }
     if (*e != cudaSuccess) return SGEMM_OK;
     if (pair) {
@@ -328,7 +331,7 @@ struct Launch {
       p.clusters = (int)clusters;
       p.timeout_ns = wait_timeout_ns();
       p.fault = dev.fault;
-      *e = launch_linear_pair(c.tile, gated, maps, p, stream);
+      *e = launch_linear_pair(c.tile, gated, fold, maps, p, stream);
       return SGEMM_OK;
     }
     LinearShortParams q;
@@ -345,6 +348,7 @@ struct Launch {
     return SGEMM_OK;
   }
 
+  int fold_first(const Product& r) const { return r.f32 || out.keep == 2 ? kFoldFirst : kFoldNone; }
   static bool tma_writes(const void* p, int64_t ld, int64_t cols, int size) { return rows_at(p, ld, size, 16) && cols * size % 16 == 0; }
 };
 

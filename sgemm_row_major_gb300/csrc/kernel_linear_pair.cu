@@ -10,7 +10,7 @@
 // M = 256, N = TN, K = 16, both operands from shared memory: each CTA holds 128 rows of A and half of the tile's columns of
 // B.  A gated tile has TN / 2 columns of each product: the even CTA's half of B is gate's rows, the odd one's up's, so every
 // thread that reads the accumulator finds both products of an element in its own lane.  The epilogue runs over an accumulator
-// 32 columns at a time while the next tile's products fill the other one.  The tensor cores' own accumulation is not
+// 64 columns at a time while the next tile's products fill the other one.  The tensor cores' own accumulation is not
 // round-to-nearest and drifts by about 1.2e-8 of the sum per instruction of 16 k.  Where FP32 values leave the kernel (an FP32
 // output, the scales of 8-bit values) only `fold` K tiles are summed in one accumulator, and these sums in FP32 registers;
 // BF16 outputs take whole sums from the tensor memory (1e-5 off at 16384 terms, where their own rounding is 2e-3), which
@@ -61,19 +61,29 @@ __device__ __forceinline__ void tma_load_pair(uint32_t dst, const CUtensorMap* m
       : "memory");
 }
 
-// A folding warp's pieces of an output, 32 rows x 32 columns each: written to shared memory in the output's type, in rows of
-// 64 (BF16) or 128 bytes with the swizzle of that width, then by TMA, or by the lanes where TMA cannot (rows that are not
-// aligned or end inside 16 bytes).
+template <int N>
+__device__ __forceinline__ void add_to(float* v, const float* x) {
+#pragma unroll
+  for (int k = 0; k < N; k += 2) {
+    const float2 s = add(make_float2(v[k], v[k + 1]), make_float2(x[k], x[k + 1]));
+    v[k] = s.x;
+    v[k + 1] = s.y;
+  }
+}
+
+// A folding warp's pieces of an output, 32 rows each: written to shared memory in the output's type, in rows of 64 (32 columns of
+// BF16) or 128 bytes (64 of BF16, 32 of FP32) with the swizzle of that width, then by TMA, or by the lanes where TMA cannot
+// (rows that are not aligned or end inside 16 bytes).  Rows of 128 bytes halve what the copy engine has to do for a tile.
 template <int BYTES>
 struct Pieces {
   uint8_t* buf;
   int at;     // the next piece's place
-  bool wide;  // places of 4 KB (an FP32 output), else of 2 KB
-  __device__ __forceinline__ void set(bool f32) {
-    if (f32 == wide) return;
+  bool wide;  // places of 4 KB, else of 2 KB
+  __device__ __forceinline__ void set(bool w) {
+    if (w == wide) return;
     if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
     __syncwarp();
-    wide = f32;
+    wide = w;
     at = 0;
   }
   __device__ __forceinline__ uint8_t* next() {
@@ -88,95 +98,114 @@ struct Pieces {
     __syncwarp();
     return p;
   }
-};
-
-// RESIDUAL: its rows are not aligned, so it is added where lanes run along them (the piece is then FP32 until it is written).
-template <bool F32, bool RESIDUAL = false, int BYTES>
-__device__ __forceinline__ void emit(Pieces<BYTES>& pieces, const CUtensorMap* map, bool tma, void* base, int64_t ld, const LinearOut& o,
-                                     const LinearJob& j, unsigned site, int row0, int col0, const float (&v)[32]) {
-  const int lane = threadIdx.x & 31;
-  uint8_t* at = pieces.next();
-  if constexpr (F32 || RESIDUAL) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-      *reinterpret_cast<float4*>(at + lane * 128 + 16 * (e ^ (lane & 7))) = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      *reinterpret_cast<uint4*>(at + lane * 64 + 16 * (e ^ ((lane >> 1) & 3))) =
-          make_uint4(pack2(v[8 * e], v[8 * e + 1]), pack2(v[8 * e + 2], v[8 * e + 3]), pack2(v[8 * e + 4], v[8 * e + 5]),
-                     pack2(v[8 * e + 6], v[8 * e + 7]));
-  }
-  if (!RESIDUAL && tma) {
+  // Sends a piece off (a group without a copy where it lies outside: places and groups advance together).
+  __device__ __forceinline__ void copy(const uint8_t* p, const CUtensorMap* map, bool inside, int row0, int col0) {
     fence_proxy_async_smem();
     __syncwarp();
-    if (lane == 0) {
-      if (row0 < j.M && col0 < j.N)
-        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(
-                         reinterpret_cast<uint64_t>(map)),
-                     "r"(smem_addr(at)), "r"(col0), "r"(row0), "r"(0)
+    if ((threadIdx.x & 31) == 0) {
+      if (inside)
+        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                     "r"(smem_addr(p)), "r"(col0), "r"(row0), "r"(0)
                      : "memory");
+      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
     }
-  } else {
+  }
+  __device__ __forceinline__ void written() {  // by the lanes
     __syncwarp();
-    const int rows = min(32, j.M - row0);
-    if (col0 + lane < j.N && rows > 0 &&
-        in_range(o.guard.fault, o.guard.word, site, (int64_t)row0 * ld + col0 + lane, (rows - 1) * ld + 1, extent(j.M, ld, j.N)) &&
-        (!RESIDUAL || r_ok(o, j, row0, col0 + lane, (rows - 1) * o.ldr + 1))) {
-      const int64_t first = (int64_t)row0 * ld + col0 + lane;
-      const auto f32_at = [&](int r) { return *reinterpret_cast<const float*>(at + r * 128 + 16 * ((lane >> 2) ^ (r & 7)) + 4 * (lane & 3)); };
-      using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
-      T* d = static_cast<T*>(base) + first;
-      if constexpr (RESIDUAL) {
-        const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(o.residual) + (int64_t)row0 * o.ldr + col0 + lane;
+    if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+  }
+};
+
+// W columns (32 or 64) of this lane's row of D (or of what is kept) go out.  RESIDUAL: the residual's rows are not aligned, so it
+// is added where lanes run along them (the pieces are then FP32 until they are written).
+template <bool F32, bool RESIDUAL, int W, int BYTES>
+__device__ __forceinline__ void emit(Pieces<BYTES>& pieces, const CUtensorMap* map, bool tma, void* base, int64_t ld, const LinearOut& o,
+                                     const LinearJob& j, unsigned site, int row0, int col0, const float (&v)[W]) {
+  const int lane = threadIdx.x & 31;
+  const int rows = min(32, j.M - row0);
+  using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
+  // the rows of this lane's column `col` (one of D's) that it may write
+  const auto mine = [&](int col) {
+    return col < j.N && rows > 0 && in_range(o.guard.fault, o.guard.word, site, (int64_t)row0 * ld + col, (rows - 1) * ld + 1, extent(j.M, ld, j.N));
+  };
+  if constexpr (F32 || RESIDUAL) {
+#pragma unroll
+    for (int h = 0; h < W / 32; ++h) {
+      uint8_t* at = pieces.next();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float* x = v + 32 * h + 4 * e;
+        *reinterpret_cast<float4*>(at + lane * 128 + 16 * (e ^ (lane & 7))) = make_float4(x[0], x[1], x[2], x[3]);
+      }
+      const int first = col0 + 32 * h, col = first + lane;
+      if (!RESIDUAL && tma) {
+        pieces.copy(at, map, row0 < j.M && first < j.N, row0, first);
+        continue;
+      }
+      __syncwarp();
+      if (mine(col) && (!RESIDUAL || r_ok(o, j, row0, col, (rows - 1) * o.ldr + 1))) {
+        const auto f32_at = [&](int r) { return *reinterpret_cast<const float*>(at + r * 128 + 16 * ((lane >> 2) ^ (r & 7)) + 4 * (lane & 3)); };
+        T* d = static_cast<T*>(base) + (int64_t)row0 * ld + col;
+        if constexpr (RESIDUAL) {
+          const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(o.residual) + (int64_t)row0 * o.ldr + col;
 #pragma unroll 1
-        for (int r0 = 0; r0 < rows; r0 += 16) {  // 16 rows' values on their way together
-          __nv_bfloat16 u[16];
+          for (int r0 = 0; r0 < rows; r0 += 16) {  // 16 rows' values on their way together
+            __nv_bfloat16 u[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k, x += o.ldr)
-            if (r0 + k < rows) u[k] = *x;
+            for (int k = 0; k < 16; ++k, x += o.ldr)
+              if (r0 + k < rows) u[k] = *x;
 #pragma unroll
-          for (int k = 0; k < 16; ++k, d += ld)
-            if (r0 + k < rows) f8::from_float(d, f32_at(r0 + k) + __bfloat162float(u[k]));
-        }
-      } else {
+            for (int k = 0; k < 16; ++k, d += ld)
+              if (r0 + k < rows) f8::from_float(d, f32_at(r0 + k) + __bfloat162float(u[k]));
+          }
+        } else {
 #pragma unroll 8
-        for (int r = 0; r < rows; ++r, d += ld) {
-          if constexpr (F32) *d = f32_at(r);
-          else               *d = *reinterpret_cast<const T*>(at + r * 64 + 16 * ((lane >> 3) ^ ((r >> 1) & 3)) + 2 * (lane & 7));
+          for (int r = 0; r < rows; ++r, d += ld) f8::from_float(d, f32_at(r));
         }
       }
+      pieces.written();
     }
-  }
-  // (a group without a copy where TMA wrote nothing: places and groups advance together)
-  if (lane == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-  __syncwarp();
-}
-
-template <int N>
-__device__ __forceinline__ void add_to(float* v, const float* x) {
+  } else {
+    uint8_t* at = pieces.next();
+    // 16-byte unit e of row r
+    const auto unit = [&](int r, int e) { return at + r * 2 * W + 16 * (W == 64 ? e ^ (r & 7) : e ^ ((r >> 1) & 3)); };
 #pragma unroll
-  for (int k = 0; k < N; k += 2) {
-    const float2 s = add(make_float2(v[k], v[k + 1]), make_float2(x[k], x[k + 1]));
-    v[k] = s.x;
-    v[k + 1] = s.y;
+    for (int e = 0; e < W / 8; ++e) {
+      const float* x = v + 8 * e;
+      *reinterpret_cast<uint4*>(unit(lane, e)) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+    }
+    if (tma) {
+      pieces.copy(at, map, row0 < j.M && col0 < j.N, row0, col0);
+      return;
+    }
+    __syncwarp();
+#pragma unroll
+    for (int h = 0; h < W / 32; ++h) {
+      const int col = col0 + 32 * h + lane;
+      if (!mine(col)) continue;
+      T* d = static_cast<T*>(base) + (int64_t)row0 * ld + col;
+#pragma unroll 8
+      for (int r = 0; r < rows; ++r, d += ld) *d = *reinterpret_cast<const T*>(unit(r, 4 * h + (lane >> 3)) + 2 * (lane & 7));
+    }
+    pieces.written();
   }
 }
 
-// 32 values of the bias, and of one row of the residual (aligned rows): sent for before the sums are waited for.
+// W values of the bias, and of one row of the residual (aligned rows): sent for before the sums are waited for.
+template <int W>
 struct Bias {
-  uint4 c[4];
-  __device__ __forceinline__ static bool whole(const LinearOut& o, int N, int col0) { return o.bias_vec && col0 + 32 <= N; }
+  uint4 c[W / 8];
+  __device__ __forceinline__ static bool whole(const LinearOut& o, int N, int col0) { return o.bias_vec && col0 + W <= N; }
   __device__ __forceinline__ void load(const LinearOut& o, int N, int col0) {
-    if (whole(o, N, col0) && in_range(o.guard.fault, o.guard.word, f8::kSiteIn, col0, 32, N)) {
+    if (whole(o, N, col0) && in_range(o.guard.fault, o.guard.word, f8::kSiteIn, col0, W, N)) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) c[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(o.bias) + col0) + e);
+      for (int e = 0; e < W / 8; ++e) c[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(o.bias) + col0) + e);
     }
   }
-  __device__ __forceinline__ void add(const LinearOut& o, int N, int col0, float (&v)[32]) const {
+  __device__ __forceinline__ void add(const LinearOut& o, int N, int col0, float (&v)[W]) const {
     if (whole(o, N, col0)) {
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
+      for (int e = 0; e < W / 8; ++e) {
         Chunk<__nv_bfloat16> b;
         float x[8];
         b.raw = c[e];
@@ -186,35 +215,35 @@ struct Bias {
       return;
     }
 #pragma unroll
-    for (int e = 0; e < 32; ++e)
+    for (int e = 0; e < W; ++e)
       if (col0 + e < N) v[e] += __bfloat162float(get_at(o.guard, f8::kSiteIn, static_cast<const __nv_bfloat16*>(o.bias), col0 + e, N));
   }
 };
 
+template <int W>
 struct Residual {
-  uint4 c[4];
+  uint4 c[W / 8];
   __device__ __forceinline__ void load(const LinearOut& o, const LinearJob& j, int row, int col0) {
+    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(o.residual) + (int64_t)row * o.ldr + col0;
+    if (row < j.M && col0 + W <= j.N && r_ok(o, j, row, col0, W)) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      c[e] = make_uint4(0u, 0u, 0u, 0u);
-      const int n = min(8, j.N - col0 - 8 * e);
-      if (row >= j.M || n <= 0 || !r_ok(o, j, row, col0 + 8 * e, n)) continue;
-      const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(o.residual) + (int64_t)row * o.ldr + col0 + 8 * e;
-      if (n == 8) {
-        c[e] = *reinterpret_cast<const uint4*>(p);
-      } else {
-        float x[8];
+      for (int e = 0; e < W / 8; ++e) c[e] = reinterpret_cast<const uint4*>(p)[e];
+      return;
+    }
 #pragma unroll
-        for (int k = 0; k < 8; ++k) x[k] = k < n ? __bfloat162float(p[k]) : 0.0f;
-        Chunk<__nv_bfloat16> b;
-        b.put(x);  // exact: every value was BF16
-        c[e] = b.raw;
-      }
+    for (int e = 0; e < W / 8; ++e) {
+      float x[8];
+      const int n = row < j.M ? j.N - col0 - 8 * e : 0;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[k] = k < n && r_ok(o, j, row, col0 + 8 * e + k, 1) ? __bfloat162float(p[8 * e + k]) : 0.0f;
+      Chunk<__nv_bfloat16> b;
+      b.put(x);  // exact: every value was BF16
+      c[e] = b.raw;
     }
   }
-  __device__ __forceinline__ void add(float (&v)[32]) const {
+  __device__ __forceinline__ void add(float (&v)[W]) const {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < W / 8; ++e) {
       Chunk<__nv_bfloat16> b;
       float x[8];
       b.raw = c[e];
@@ -224,9 +253,18 @@ struct Residual {
   }
 };
 
+// Asks for `cols` values of the residual in one row to be brought to L2, while the tile's products run.
+__device__ __forceinline__ void prefetch_residual(const LinearOut& o, const LinearJob& j, int row, int col0, int cols) {
+  const int n = min(cols, j.N - col0);
+  if (row >= j.M || n <= 0 || !r_ok(o, j, row, col0, n)) return;
+  const char* p = reinterpret_cast<const char*>(static_cast<const __nv_bfloat16*>(o.residual) + (int64_t)row * o.ldr + col0);
+  for (int at = 0; at < 2 * n; at += 128) asm volatile("prefetch.global.L2 [%0];" ::"l"(p + at));
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p + 2 * n - 2));
+}
+
 // 32 codes of one row.  CHECK: some value may be infinite.
 template <bool CHECK>
-__device__ __forceinline__ void put_codes(const LinearOut& o, const LinearJob& j, int which, int row, int col0, const float (&v)[32], float inv) {
+__device__ __forceinline__ void put_codes(const LinearOut& o, const LinearJob& j, int which, int row, int col0, const float* v, float inv) {
   const LinearKept& k = o.kept[which];
   uint32_t u[8];
 #pragma unroll
@@ -250,10 +288,11 @@ __device__ __forceinline__ void put_codes(const LinearOut& o, const LinearJob& j
 
 // The largest finite |v| so far (a NaN is never the larger one; infinities are looked for only where there are some, and
 // remembered).
-__device__ __forceinline__ float largest_of(float m, bool& infinite, const float (&v)[32]) {
+template <int W>
+__device__ __forceinline__ float largest_of(float m, bool& infinite, const float (&v)[W]) {
   float x = 0.0f, y = 0.0f;
 #pragma unroll
-  for (int k = 0; k < 32; k += 2) {
+  for (int k = 0; k < W; k += 2) {
     x = fmaxf(x, fabsf(v[k]));
     y = fmaxf(y, fabsf(v[k + 1]));
   }
@@ -262,16 +301,21 @@ __device__ __forceinline__ float largest_of(float m, bool& infinite, const float
     infinite = true;
     x = 0.0f;
 #pragma unroll
-    for (int k = 0; k < 32; ++k) x = fmaxf(x, f8::finite_abs(v[k]));
+    for (int k = 0; k < W; ++k) x = fmaxf(x, f8::finite_abs(v[k]));
   }
   return fmaxf(m, x);
 }
 
-__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
-  const float(&a)[16] = *reinterpret_cast<const float(*)[16]>(&v[0]);
-  const float(&b)[16] = *reinterpret_cast<const float(*)[16]>(&v[16]);
-  tmem_st16(taddr, a);
-  tmem_st16(taddr + 16u, b);
+// W columns of this thread's TMEM lane.
+template <int W>
+__device__ __forceinline__ void tmem_get(uint32_t taddr, float (&v)[W]) {
+#pragma unroll
+  for (int h = 0; h < W; h += 32) tmem_ld32(taddr + (uint32_t)h, v + h);
+}
+template <int W>
+__device__ __forceinline__ void tmem_put(uint32_t taddr, const float (&v)[W]) {
+#pragma unroll
+  for (int h = 0; h < W; h += 16) tmem_st16(taddr + (uint32_t)h, *reinterpret_cast<const float(*)[16]>(&v[h]));
 }
 
 // The job of a tile and the tile's place in it.
@@ -283,8 +327,9 @@ struct Place {
   }
 };
 
-// TN: the accumulator's columns.  GATED: half of them are gate's, half up's.
-template <int TN, bool GATED>
+// TN: the accumulator's columns.  GATED: half of them are gate's, half up's.  FOLD: some job adds several accumulators in
+// registers (without that the epilogue can take 64 columns at a time everywhere).
+template <int TN, bool GATED, bool FOLD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearPairParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -453,7 +498,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     // the accumulator column of load e: gated, the first half of the loads are gate's columns, the others up's
     const auto column = [](int e) { return GATED && e >= loads / 2 ? TN / 2 + 32 * (e - loads / 2) : 32 * e; };
     Pieces<R::kOutBytes> pieces{smem_raw + pad + kStages * kStageBytes + (warp - kFirstFold) * R::kOutBytes, 0, false};
-    float sum[TN / 2];
     bool ok = true;
     int b = 0;
     uint32_t b_lap = 0, asked = 0;  // tiles whose largest values have been exchanged
@@ -480,168 +524,174 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           ++b_lap;
         }
       };
-      if (kt > j.fold0) {
-        // several accumulators: all but the last are added in registers, and these sums to the last one where it lies
+      bool several = false;
+      if constexpr (FOLD) {
+        several = kt > j.fold0;
+        if (several) {
+          // several accumulators: all but the last are added in registers, and these sums to the last one where it lies
+          float sum[TN / 2];
 #pragma unroll
-        for (int e = 0; e < TN / 2; ++e) sum[e] = 0.0f;
-        for (int g = j.fold0; g < kt; g += j.fold) {  // (g: K tiles up to this accumulator's end)
-          if (!next()) break;
+          for (int e = 0; e < TN / 2; ++e) sum[e] = 0.0f;
+          for (int g = j.fold0; g < kt; g += j.fold) {  // (g: K tiles up to this accumulator's end)
+            if (!next()) break;
+#pragma unroll
+            for (int e = 0; e < 2 * loads; ++e) {
+              float v[16];
+              tmem_ld16(acc + (uint32_t)(column(e / 2) + 16 * (e % 2)), v);
+              tmem_wait_ld();
+              if (e == 2 * loads - 1) release();
+              tmem_ld_ready(v);
+              add_to<16>(&sum[16 * e], v);
+            }
+          }
+          if (!ok || !next()) break;
 #pragma unroll
           for (int e = 0; e < 2 * loads; ++e) {
+            const uint32_t at16 = acc + (uint32_t)(column(e / 2) + 16 * (e % 2));
             float v[16];
-            tmem_ld16(acc + (uint32_t)(column(e / 2) + 16 * (e % 2)), v);
+            tmem_ld16(at16, v);
             tmem_wait_ld();
-            if (e == 2 * loads - 1) release();
             tmem_ld_ready(v);
-            add_to<16>(&sum[16 * e], v);
+            add_to<16>(v, &sum[16 * e]);
+            tmem_st16(at16, v);
           }
+          tmem_wait_st();
         }
-        if (!ok || !next()) break;
-#pragma unroll
-        for (int e = 0; e < 2 * loads; ++e) {
-          const uint32_t at16 = acc + (uint32_t)(column(e / 2) + 16 * (e % 2));
-          float v[16];
-          tmem_ld16(at16, v);
-          tmem_wait_ld();
-          tmem_ld_ready(v);
-          add_to<16>(v, &sum[16 * e]);
-          tmem_st16(at16, v);
-        }
-        tmem_wait_st();
-      } else if (!next()) {
-        break;
       }
-      // ---------------------------------------------- epilogue
+      if (!several && !next()) break;
+      // ---------------------------------------------- epilogue, W columns at a time
+      constexpr int W = linear_pair_box(TN, GATED, FOLD);
       constexpr uint32_t up = TN / 2;  // gated: from a column of gate to up's
-      pieces.set(j.f32 != 0 || (!GATED && o.residual && !o.r_vec));
-      float inv[2] = {1.0f, 1.0f};     // of the scales of what is kept in 8 bits
-      bool odd = false;                // an infinity among them
+      const bool direct = !GATED && o.residual && o.r_vec;  // the residual is read by rows
+      pieces.set(W == 64 || j.f32 != 0 || (!GATED && o.residual && !direct));
+      const CUtensorMap* map_d = &maps.d[at.job];
+      float inv[2] = {1.0f, 1.0f};       // of the scales of what is kept in 8 bits
+      bool odd = false;                  // an infinity among them
       bool add_bias = !GATED && o.bias;  // still to be done
-      if (o.keep == 2) {
+      if (o.keep) {
+        // what is kept in BF16, or the largest values of what is kept in 8 bits; the bias is added where the sums lie
         float m[2] = {0.0f, 0.0f};
 #pragma unroll 1
-        for (int c = 0; c < cols; c += 32) {
-          float v[32];
-          Bias bias;
-          tmem_ld32(acc + (uint32_t)c, v);
+        for (int c = 0; c < cols; c += W) {
+          float v[W];
+          Bias<W> bias;
+          tmem_get(acc + (uint32_t)c, v);
           if (add_bias) bias.load(o, j.N, c0 + c);
           tmem_wait_ld();
           tmem_ld_ready(v);
           if (add_bias) {
             bias.add(o, j.N, c0 + c, v);
-            tmem_st32(acc + (uint32_t)c, v);
+            tmem_put(acc + (uint32_t)c, v);
           }
-          m[0] = largest_of(m[0], odd, v);
+          if (o.keep == 1) emit<false, false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
+          else             m[0] = largest_of(m[0], odd, v);
           if constexpr (GATED) {
-            tmem_ld32(acc + up + (uint32_t)c, v);
+            tmem_get(acc + up + (uint32_t)c, v);
             tmem_wait_ld();
             tmem_ld_ready(v);
-            m[1] = largest_of(m[1], odd, v);
+            if (o.keep == 1) emit<false, false>(pieces, &maps.kept[1], o.kept[1].vec, o.kept[1].data, o.kept[1].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
+            else             m[1] = largest_of(m[1], odd, v);
           }
         }
         if (add_bias) tmem_wait_st();
         add_bias = false;
-        odd = __any_sync(0xffffffffu, odd);
-        if (cols < 128) {  // the other half of the group is with the warp of the other column half
-          float* slot = &largest[0][32 * q + lane];
-          constexpr int kUp = GATED ? BMC : 0;
-          if (part == 1) {
-            slot[0] = m[0];
-            if (GATED) slot[kUp] = m[1];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&max_asked[q]));
+        if (o.keep == 2) {
+          odd = __any_sync(0xffffffffu, odd);
+          if (cols < 128) {  // the other half of the group is with the warp of the other column half
+            float* slot = &largest[0][32 * q + lane];
+            constexpr int kUp = GATED ? BMC : 0;
+            if (part == 1) {
+              slot[0] = m[0];
+              if (GATED) slot[kUp] = m[1];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_addr(&max_asked[q]));
+            }
+            ok = poll_wait(smem_addr(part == 1 ? &max_told[q] : &max_asked[q]), asked & 1u, p.timeout_ns);
+            ++asked;
+            if (!ok) {
+              if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
+              break;
+            }
+            m[0] = fmaxf(m[0], slot[0]);
+            if (GATED) m[1] = fmaxf(m[1], slot[kUp]);
+            if (part == 0) {
+              slot[0] = m[0];
+              if (GATED) slot[kUp] = m[1];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_addr(&max_told[q]));
+            }
           }
-          ok = poll_wait(smem_addr(part == 1 ? &max_told[q] : &max_asked[q]), asked & 1u, p.timeout_ns);
-          ++asked;
-          if (!ok) {
-            if (lane == 0) atomicOr(p.fault, (unsigned)kFaultFullWait);
-            break;
-          }
-          m[0] = fmaxf(m[0], slot[0]);
-          if (GATED) m[1] = fmaxf(m[1], slot[kUp]);
-          if (part == 0) {
-            slot[0] = m[0];
-            if (GATED) slot[kUp] = m[1];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_addr(&max_told[q]));
-          }
-        }
 #pragma unroll
-        for (int w = 0; w < (GATED ? 2 : 1); ++w) {
-          const float scale = f8::group_scale(m[w], kMaxE4M3);
-          if (row < j.M && c0 < j.N && c0 % 128 == 0) put_scale(o, j, w, row, c0 >> 7, scale);
-          inv[w] = __fdiv_rn(1.0f, scale);
+          for (int w = 0; w < (GATED ? 2 : 1); ++w) {
+            const float scale = f8::group_scale(m[w], kMaxE4M3);
+            if (row < j.M && c0 < j.N && c0 % 128 == 0) put_scale(o, j, w, row, c0 >> 7, scale);
+            inv[w] = __fdiv_rn(1.0f, scale);
+          }
         }
       }
-      Residual following;  // of the next 32 columns
-      const bool direct = !GATED && o.residual && o.r_vec;
-      if (direct) following.load(o, j, row, c0);
 #pragma unroll 1
-      for (int c = 0; c < cols; c += 32) {
-        const bool last = c + 32 == cols;
-        float v[32];
-        tmem_ld32(acc + (uint32_t)c, v);
-        const auto codes = [&](int which, const float (&x)[32]) {
-          if (odd) put_codes<true>(o, j, which, row, c0 + c, x, inv[which]);
-          else     put_codes<false>(o, j, which, row, c0 + c, x, inv[which]);
+      for (int c = 0; c < cols; c += W) {
+        const bool last = c + W == cols;
+        const auto codes = [&](int which, const float (&x)[W]) {
+#pragma unroll
+          for (int h = 0; h < W; h += 32) {
+            if (odd) put_codes<true>(o, j, which, row, c0 + c + h, x + h, inv[which]);
+            else     put_codes<false>(o, j, which, row, c0 + c + h, x + h, inv[which]);
+          }
         };
+        float v[W];
+        tmem_get(acc + (uint32_t)c, v);
         if constexpr (GATED) {
-          float u[32];
-          tmem_ld32(acc + up + (uint32_t)c, u);
+          float u[W];
+          tmem_get(acc + up + (uint32_t)c, u);
           tmem_wait_ld();
           if (last) release();
           tmem_ld_ready(v);
           tmem_ld_ready(u);
-          if (o.keep == 1) {
-            emit<false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
-            emit<false>(pieces, &maps.kept[1], o.kept[1].vec, o.kept[1].data, o.kept[1].ld, o, j, f8::kSiteCodes, row0, c0 + c, u);
-          } else if (o.keep == 2) {
+          if (o.keep == 2) {
             codes(0, v);
             codes(1, u);
           }
           with_act(o.act, [&](auto act) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
+            for (int k = 0; k < W; k += 2) {
               const float2 h = mul(act_of<decltype(act)::value>(make_float2(v[k], v[k + 1])), make_float2(u[k], u[k + 1]));
               v[k] = h.x;
               v[k + 1] = h.y;
             }
           });
-          emit<false>(pieces, &maps.d[0], j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
+          emit<false, false>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
         } else {
-          const Residual residual = following;
-          if (direct && !last) following.load(o, j, row, c0 + c + 32);
-          Bias bias;
+          Residual<W> residual;
+          if (direct) residual.load(o, j, row, c0 + c);
+          Bias<W> bias;
           if (add_bias) bias.load(o, j.N, c0 + c);
           tmem_wait_ld();
           if (last) release();
           tmem_ld_ready(v);
           if (add_bias) bias.add(o, j.N, c0 + c, v);
-          if (o.keep == 1) emit<false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
-          else if (o.keep == 2) codes(0, v);
+          if (o.keep == 2) codes(0, v);
           with_act(o.act, [&](auto act) {
 #pragma unroll
-            for (int k = 0; k < 32; k += 2) {
+            for (int k = 0; k < W; k += 2) {
               const float2 f = act_of<decltype(act)::value>(make_float2(v[k], v[k + 1]));
               v[k] = f.x;
               v[k + 1] = f.y;
             }
           });
           if (direct) residual.add(v);
-          const auto write = [&](auto f32, auto with_residual) {
-            emit<decltype(f32)::value, decltype(with_residual)::value>(pieces, &maps.d[at.job], j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0,
-                                                                       c0 + c, v);
-          };
-          constexpr std::true_type yes{};
-          constexpr std::false_type no{};
           if (o.residual && !direct) {
-            if (j.f32) write(yes, yes);
-            else       write(no, yes);
+            if (j.f32) emit<true, true>(pieces, map_d, false, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
+            else       emit<false, true>(pieces, map_d, false, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
           } else {
-            if (j.f32) write(yes, no);
-            else       write(no, no);
+            if (j.f32) emit<true, false>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
+            else       emit<false, false>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
           }
         }
+      }
+      if (!GATED && o.residual && tile + p.clusters < tiles) {  // the next tile's (here its place need not be held during the sums)
+        const Place to(p, tile + p.clusters);
+        prefetch_residual(o, p.job[to.job], to.tm * BM + BMC * (int)rank + 32 * q + lane, to.tn * TD + cols * part, cols);
       }
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
@@ -662,14 +712,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // f(kernel) for a tile width and form.
-template <typename F>
-cudaError_t with_kernel(int tile_n, bool gated, const F& f) {
+template <bool FOLD, typename F>
+cudaError_t with_form(int tile_n, bool gated, const F& f) {
   switch (tile_n) {
-    case 256: return gated ? f(linear_pair_kernel<256, true>) : f(linear_pair_kernel<256, false>);
-    case 128: return gated ? f(linear_pair_kernel<128, true>) : f(linear_pair_kernel<128, false>);
-    case 64: return gated ? cudaErrorInvalidValue : f(linear_pair_kernel<64, false>);
+    case 256: return gated ? f(linear_pair_kernel<256, true, FOLD>) : f(linear_pair_kernel<256, false, FOLD>);
+    case 128: return gated ? f(linear_pair_kernel<128, true, false>) : f(linear_pair_kernel<128, false, FOLD>);  // (gated: BF16 alone)
+    case 64: return gated ? cudaErrorInvalidValue : f(linear_pair_kernel<64, false, FOLD>);
   }
   return cudaErrorInvalidValue;
+}
+template <typename F>
+cudaError_t with_kernel(int tile_n, bool gated, bool fold, const F& f) {
+  return fold ? with_form<true>(tile_n, gated, f) : with_form<false>(tile_n, gated, f);
 }
 
 }  // namespace
@@ -680,9 +734,10 @@ int64_t linear_pair_smem(int tile_n) { return tile_n == 256 ? lin::Ring<256>::kS
 
 cudaError_t prepare_linear_pair() {
   for (int tile_n : kLinearPairTiles)
-    for (int gated = 0; gated < 2; ++gated) {
+    for (int form = 0; form < 4; ++form) {
+      const bool gated = form / 2 != 0, fold = form % 2 != 0;
       if (gated && tile_n == 64) continue;
-      const cudaError_t e = lin::with_kernel(tile_n, gated != 0, [&](auto kernel) {
+      const cudaError_t e = lin::with_kernel(tile_n, gated, fold, [&](auto kernel) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)linear_pair_smem(tile_n));
       });
       if (e != cudaSuccess) return e;
@@ -690,7 +745,7 @@ cudaError_t prepare_linear_pair() {
   return cudaSuccess;
 }
 
-cudaError_t launch_linear_pair(int tile_n, bool gated, const LinearMaps& maps, const LinearPairParams& p, cudaStream_t stream) {
+cudaError_t launch_linear_pair(int tile_n, bool gated, bool fold, const LinearMaps& maps, const LinearPairParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)p.clusters);
   cfg.blockDim = dim3(lin::kThreads);
@@ -701,7 +756,7 @@ cudaError_t launch_linear_pair(int tile_n, bool gated, const LinearMaps& maps, c
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return lin::with_kernel(tile_n, gated, [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, maps, p); });
+  return lin::with_kernel(tile_n, gated, fold, [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, maps, p); });
 }
 
 }  // namespace sgemm_impl

@@ -61,10 +61,16 @@ struct LinearPairParams {
 };
 constexpr int kLinearPairThreads = 384;
 constexpr int kLinearPairTiles[] = {256, 128, 64};
+// Columns of the pieces of D that TMA writes (BF16; FP32: 32), which the epilogue takes at a time.  With the 128 sums of a
+// 256-wide tile in registers 64 columns at a time spill.
+constexpr int linear_pair_box(int tile_n, bool gated, bool fold) {
+  return tile_n / (gated ? 4 : 2) >= 64 && !(fold && !gated && tile_n == 256) ? 64 : 32;
+}
 int linear_pair_stages(int tile_n);
 int64_t linear_pair_smem(int tile_n);
 cudaError_t prepare_linear_pair();
-cudaError_t launch_linear_pair(int tile_n, bool gated, const LinearMaps& maps, const LinearPairParams& p, cudaStream_t stream);
+// fold: some job sums K tiles in more than one accumulator.
+cudaError_t launch_linear_pair(int tile_n, bool gated, bool fold, const LinearMaps& maps, const LinearPairParams& p, cudaStream_t stream);
 
 // The columns of D run along the tensor core's rows (B's tile of 128), its rows along the columns.
 struct LinearShortParams {
@@ -122,5 +128,9 @@ cudaError_t launch_linear_expand(LinearExpandParams& p, cudaStream_t stream);
 // Map over `outer` rows of `inner` BF16 values (row stride ld elements, a multiple of 8): boxes of 64 x box_outer,
 // 128-byte swizzle, zeros outside.
 cudaError_t encode_linear_map(const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer, CUtensorMap* map);
+
+// Map over D (`rows` x `cols` BF16 or FP32, row stride ld elements, 16-byte aligned rows of whole 16 bytes): boxes of box_cols x
+// 32, rows of 64 or 128 bytes with the swizzle of that width.
+cudaError_t encode_linear_out_map(const void* base, int64_t cols, int64_t rows, int64_t ld, bool bf16, int box_cols, CUtensorMap* map);
 
 }  // namespace sgemm_impl
