@@ -188,7 +188,7 @@ struct Operand {
   }
 };
 
-// Makes the copies that operands (up to three) need, in one launch.
+// Makes the copies that operands (up to three of them) need, in one launch.
 cudaError_t make_copies(std::initializer_list<const Operand*> list, const Guard& g, cudaStream_t stream) {
   LinearExpandParams p;
   p.guard = g;
@@ -234,33 +234,35 @@ struct Launch {
 
   Product& add() { return pr[n++]; }
 
-  int run(const CallDevice& dev, cudaStream_t stream, cudaError_t* e) {
+  Choice choice(const CallDevice& dev) const {
     Shape s[kLinearJobs];
     for (int i = 0; i < n; ++i) s[i] = pr[i].shape;
-    Choice c = choose(s, n, dev.sm_count, dev.pair_clusters);
+    return choose(s, n, dev.sm_count, dev.pair_clusters);
+  }
+
+  int run(const CallDevice& dev, cudaStream_t stream, cudaError_t* e) {
+    const Choice c = choice(dev);
     if (n > 1) {
       // each by itself where that is cheaper: a short one among long ones, or no clusters
       Choice one[kLinearJobs];
       double ns = 0.0;
       for (int i = 0; i < n; ++i) {
-        one[i] = choose(s + i, 1, dev.sm_count, dev.pair_clusters);
+        one[i] = choose(&pr[i].shape, 1, dev.sm_count, dev.pair_clusters);
         ns += one[i].ns;
       }
       if (ns < c.ns) {
         for (int i = 0; i < n && *e == cudaSuccess; ++i) {
-          if (one[i].variant == 0) return SGEMM_ERR_UNSUPPORTED;
           const int st = launch(&pr[i], 1, one[i], dev, stream, e);
           if (st != SGEMM_OK) return st;
         }
         return SGEMM_OK;
       }
     }
-    if (c.variant == 0) return SGEMM_ERR_UNSUPPORTED;  // forced to what needs clusters
     return launch(pr, n, c, dev, stream, e);
   }
 
- private:
   int launch(const Product* list, int count, const Choice& c, const CallDevice& dev, cudaStream_t stream, cudaError_t* e) {
+    if (c.variant == 0) return SGEMM_ERR_UNSUPPORTED;  // forced to what needs clusters
     const bool pair = c.variant == SGEMM_VARIANT_LINEAR_PAIR, gated = list[0].shape.gated;
     out.guard = {dev.fault, dev.bounds};
     out.bias_vec = aligned(out.bias, 16);
@@ -278,8 +280,8 @@ struct Launch {
       return maps_used++;
     };
     int64_t tiles = 0, steps = 0;
-    bool fold = false;
-    for (int i = 0; i < count; ++i) fold |= fold_first(list[i]) < list[i].shape.k_tiles();
+    bool fold = out.keep == 2;
+    for (int i = 0; i < count; ++i) fold |= list[i].f32;
     for (int i = 0; i < count; ++i) {
       const Product& r = list[i];
       LinearJob& j = p.job[i];
@@ -301,7 +303,7 @@ struct Launch {
         j.tiles_m = (int)ceil_div(r.shape.M, 256);
         j.tiles_n = (int)ceil_div(r.shape.N, gated ? c.tile / 2 : c.tile);
         j.idesc = instruction(r.a_mn, r.b_mn, 256, c.tile);
-        if (j.d_tma && *e == cudaSuccess) *e = encode_linear_out_map(r.d, r.shape.N, r.shape.M, r.ldd, !r.f32, r.f32 ? 32 : linear_pair_box(c.tile, gated, fold), &maps.d[i]);
+        if (j.d_tma && *e == cudaSuccess) *e = encode_linear_out_map(r.d, r.shape.N / (16 / size) * (16 / size), r.shape.M, r.ldd, !r.f32, r.f32 ? 32 : linear_pair_box(c.tile, gated, fold), &maps.d[i]);
       } else {
         j.tiles_m = (int)ceil_div(r.shape.M, c.tile);
         j.tiles_n = (int)ceil_div(r.shape.N, 128);
@@ -320,7 +322,7 @@ struct Launch {
       k.vec = out.keep == 2 ? rows_at(k.data, k.ld, 1, 16) : tma_writes(k.data, k.ld, list[0].shape.N, 2);
       out.kept_vec8[i] = rows_at(k.data, k.ld, 2, 8);
       if (pair && out.keep == 1 && k.vec && *e == cudaSuccess)
-        *e = encode_linear_out_map(k.data, list[0].shape.N, list[0].shape.M, k.ld, true, linear_pair_box(c.tile, gated, fold), &maps.kept[i]);
+        *e = encode_linear_out_map(k.data, list[0].shape.N / 8 * 8, list[0].shape.M, k.ld, true, linear_pair_box(c.tile, gated, fold), &maps.kept[i]);
     }
     if (*e != cudaSuccess) return SGEMM_OK;
     if (pair) {
@@ -348,8 +350,9 @@ struct Launch {
     return SGEMM_OK;
   }
 
+ private:
   int fold_first(const Product& r) const { return r.f32 || out.keep == 2 ? kFoldFirst : kFoldNone; }
-  static bool tma_writes(const void* p, int64_t ld, int64_t cols, int size) { return rows_at(p, ld, size, 16) && cols * size % 16 == 0; }
+  static bool tma_writes(const void* p, int64_t ld, int64_t cols, int size) { return rows_at(p, ld, size, 16) && cols * size >= 16; }
 };
 
 // What is kept, as the kernels take it: 0 nothing, 1 BF16, 2 8-bit.
@@ -427,6 +430,12 @@ int forward(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, int6
   pr.a[0] = &x;
   pr.b[0] = &w0;
   if (gated) pr.b[1] = &w1;
+  // the pair kernel's lanes read a row of the residual each, 16 bytes at a time; rows that lie anywhere are copied first
+  // (reading them along the rows in its epilogue took longer than the copy and the epilogue together)
+  const Choice choice = launch.choice(dev);
+  LinearOut& out = launch.out;
+  Operand r(out.residual, out.ldr, nullptr, 0, tokens, outputs);
+  r.copied = out.residual && choice.variant == SGEMM_VARIANT_LINEAR_PAIR && !rows_at(out.residual, out.ldr, 2, 16);
   return with_workspace(
       dev, stream,
       [&](Pieces* w) {
@@ -434,6 +443,7 @@ int forward(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, int6
         x.place(w);
         w0.place(w);
         if (gated) w1.place(w);
+        r.place(w);
       },
       [&](cudaError_t* e) {
         const Guard g{dev.fault, dev.bounds};
@@ -441,8 +451,9 @@ int forward(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, int6
           for (Operand* o : {&x, &w0, &w1}) o->m.data = zeros, o->m.ld = 8;
           *e = cudaMemsetAsync(zeros, 0, (size_t)std::max(tokens, outputs) * 16, stream);
         }
-        if (*e == cudaSuccess) *e = make_copies({&x, &w0, gated ? &w1 : nullptr}, g, stream);
-        return *e == cudaSuccess ? launch.run(dev, stream, e) : SGEMM_OK;
+        if (*e == cudaSuccess) *e = make_copies({&x, &w0, gated ? &w1 : nullptr, &r}, g, stream);
+        if (r.copied) out.residual = r.copy, out.ldr = round8(outputs);
+        return *e == cudaSuccess ? launch.launch(launch.pr, 1, choice, dev, stream, e) : SGEMM_OK;
       });
 }
 

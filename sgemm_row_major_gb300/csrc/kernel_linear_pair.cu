@@ -72,8 +72,8 @@ __device__ __forceinline__ void add_to(float* v, const float* x) {
 }
 
 // A folding warp's pieces of an output, 32 rows each: written to shared memory in the output's type, in rows of 64 (32 columns of
-// BF16) or 128 bytes (64 of BF16, 32 of FP32) with the swizzle of that width, then by TMA, or by the lanes where TMA cannot
-// (rows that are not aligned or end inside 16 bytes).  Rows of 128 bytes halve what the copy engine has to do for a tile.
+// BF16) or 128 bytes (64 of BF16, 32 of FP32) with the swizzle of that width, then by TMA
+// or by the lanes.  Rows of 128 bytes halve what the copy engine has to do for a tile.
 template <int BYTES>
 struct Pieces {
   uint8_t* buf;
@@ -102,96 +102,59 @@ struct Pieces {
   __device__ __forceinline__ void copy(const uint8_t* p, const CUtensorMap* map, bool inside, int row0, int col0) {
     fence_proxy_async_smem();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) {
-      if (inside)
-        asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
-                     "r"(smem_addr(p)), "r"(col0), "r"(row0), "r"(0)
-                     : "memory");
-      asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-    }
+    if ((threadIdx.x & 31) == 0 && inside)
+      asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(reinterpret_cast<uint64_t>(map)),
+                   "r"(smem_addr(p)), "r"(col0), "r"(row0), "r"(0)
+                   : "memory");
+    commit();
   }
-  __device__ __forceinline__ void written() {  // by the lanes
-    __syncwarp();
+  __device__ __forceinline__ void commit() {
     if ((threadIdx.x & 31) == 0) asm volatile("cp.async.bulk.commit_group;" ::: "memory");
   }
 };
 
-// W columns (32 or 64) of this lane's row of D (or of what is kept) go out.  RESIDUAL: the residual's rows are not aligned, so it
-// is added where lanes run along them (the pieces are then FP32 until they are written).
-template <bool F32, bool RESIDUAL, int W, int BYTES>
+// W columns (32 or 64) of this lane's row of D (or of what is kept) go out.  TMA writes whole 16 bytes of a row; what is left of
+// it, and everything where rows are not aligned (tma: 0), is written by lanes that run along the rows.
+template <bool F32, int W, int BYTES>
 __device__ __forceinline__ void emit(Pieces<BYTES>& pieces, const CUtensorMap* map, bool tma, void* base, int64_t ld, const LinearOut& o,
                                      const LinearJob& j, unsigned site, int row0, int col0, const float (&v)[W]) {
-  const int lane = threadIdx.x & 31;
-  const int rows = min(32, j.M - row0);
   using T = typename std::conditional<F32, float, __nv_bfloat16>::type;
-  // the rows of this lane's column `col` (one of D's) that it may write
-  const auto mine = [&](int col) {
-    return col < j.N && rows > 0 && in_range(o.guard.fault, o.guard.word, site, (int64_t)row0 * ld + col, (rows - 1) * ld + 1, extent(j.M, ld, j.N));
-  };
-  if constexpr (F32 || RESIDUAL) {
+  constexpr int kCols = F32 ? 32 : W, kBytes = kCols * (int)sizeof(T);  // of a piece's row
+  const int lane = threadIdx.x & 31;
+  const int by_tma = tma ? j.N & ~(16 / (int)sizeof(T) - 1) : 0;
 #pragma unroll
-    for (int h = 0; h < W / 32; ++h) {
-      uint8_t* at = pieces.next();
+  for (int h = 0; h < W / kCols; ++h) {
+    uint8_t* at = pieces.next();
+    const int first = col0 + kCols * h;
+    // 16-byte unit e of row r
+    const auto unit = [&](int r, int e) { return at + r * kBytes + 16 * (e ^ (kBytes == 128 ? r & 7 : (r >> 1) & 3)); };
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float* x = v + 32 * h + 4 * e;
-        *reinterpret_cast<float4*>(at + lane * 128 + 16 * (e ^ (lane & 7))) = make_float4(x[0], x[1], x[2], x[3]);
-      }
-      const int first = col0 + 32 * h, col = first + lane;
-      if (!RESIDUAL && tma) {
-        pieces.copy(at, map, row0 < j.M && first < j.N, row0, first);
-        continue;
+    for (int e = 0; e < kBytes / 16; ++e) {
+      const float* x = v + kCols * h + 16 / (int)sizeof(T) * e;
+      if constexpr (F32)
+        *reinterpret_cast<float4*>(unit(lane, e)) = make_float4(x[0], x[1], x[2], x[3]);
+      else
+        *reinterpret_cast<uint4*>(unit(lane, e)) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+    }
+    if (tma) pieces.copy(at, map, row0 < j.M && first < by_tma, row0, first);
+    else     __syncwarp();
+    if (first + kCols > by_tma && by_tma < j.N && row0 < j.M) {
+      const int rows = min(32, j.M - row0);
+#pragma unroll 1
+      for (int c = max(first, by_tma) + lane; c < min(first + kCols, j.N); c += 32) {
+        if (!in_range(o.guard.fault, o.guard.word, site, (int64_t)row0 * ld + c, (rows - 1) * ld + 1, extent(j.M, ld, j.N))) continue;
+        T* d = static_cast<T*>(base) + (int64_t)row0 * ld + c;
+        const int byte = (c - first) * (int)sizeof(T);
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r, d += ld) *d = *reinterpret_cast<const T*>(unit(r, byte >> 4) + (byte & 15));
       }
       __syncwarp();
-      if (mine(col) && (!RESIDUAL || r_ok(o, j, row0, col, (rows - 1) * o.ldr + 1))) {
-        const auto f32_at = [&](int r) { return *reinterpret_cast<const float*>(at + r * 128 + 16 * ((lane >> 2) ^ (r & 7)) + 4 * (lane & 3)); };
-        T* d = static_cast<T*>(base) + (int64_t)row0 * ld + col;
-        if constexpr (RESIDUAL) {
-          const __nv_bfloat16* x = static_cast<const __nv_bfloat16*>(o.residual) + (int64_t)row0 * o.ldr + col;
-#pragma unroll 1
-          for (int r0 = 0; r0 < rows; r0 += 16) {  // 16 rows' values on their way together
-            __nv_bfloat16 u[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k, x += o.ldr)
-              if (r0 + k < rows) u[k] = *x;
-#pragma unroll
-            for (int k = 0; k < 16; ++k, d += ld)
-              if (r0 + k < rows) f8::from_float(d, f32_at(r0 + k) + __bfloat162float(u[k]));
-          }
-        } else {
-#pragma unroll 8
-          for (int r = 0; r < rows; ++r, d += ld) f8::from_float(d, f32_at(r));
-        }
-      }
-      pieces.written();
     }
-  } else {
-    uint8_t* at = pieces.next();
-    // 16-byte unit e of row r
-    const auto unit = [&](int r, int e) { return at + r * 2 * W + 16 * (W == 64 ? e ^ (r & 7) : e ^ ((r >> 1) & 3)); };
-#pragma unroll
-    for (int e = 0; e < W / 8; ++e) {
-      const float* x = v + 8 * e;
-      *reinterpret_cast<uint4*>(unit(lane, e)) = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
-    }
-    if (tma) {
-      pieces.copy(at, map, row0 < j.M && col0 < j.N, row0, col0);
-      return;
-    }
-    __syncwarp();
-#pragma unroll
-    for (int h = 0; h < W / 32; ++h) {
-      const int col = col0 + 32 * h + lane;
-      if (!mine(col)) continue;
-      T* d = static_cast<T*>(base) + (int64_t)row0 * ld + col;
-#pragma unroll 8
-      for (int r = 0; r < rows; ++r, d += ld) *d = *reinterpret_cast<const T*>(unit(r, 4 * h + (lane >> 3)) + 2 * (lane & 7));
-    }
-    pieces.written();
+    if (!tma) pieces.commit();
   }
 }
 
-// W values of the bias, and of one row of the residual (aligned rows): sent for before the sums are waited for.
+// W values of the bias, and of one row of the residual (whose rows are aligned): sent for before the sums are waited for.
 template <int W>
 struct Bias {
   uint4 c[W / 8];
@@ -327,8 +290,9 @@ struct Place {
   }
 };
 
-// TN: the accumulator's columns.  GATED: half of them are gate's, half up's.  FOLD: some job adds several accumulators in
-// registers (without that the epilogue can take 64 columns at a time everywhere).
+// TN: the accumulator's columns.  GATED: half of them are gate's, half up's.  FOLD: FP32 values leave the kernel (an FP32
+// output, scales of 8-bit values), so a job may add several accumulators in registers; without that the epilogue has room for
+// 64 columns at a time everywhere.
 template <int TN, bool GATED, bool FOLD>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearPairParams p) {
@@ -562,8 +526,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       // ---------------------------------------------- epilogue, W columns at a time
       constexpr int W = linear_pair_box(TN, GATED, FOLD);
       constexpr uint32_t up = TN / 2;  // gated: from a column of gate to up's
-      const bool direct = !GATED && o.residual && o.r_vec;  // the residual is read by rows
-      pieces.set(W == 64 || j.f32 != 0 || (!GATED && o.residual && !direct));
+      pieces.set(W == 64 || (FOLD && j.f32 != 0));
       const CUtensorMap* map_d = &maps.d[at.job];
       float inv[2] = {1.0f, 1.0f};       // of the scales of what is kept in 8 bits
       bool odd = false;                  // an infinity among them
@@ -583,19 +546,19 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
             bias.add(o, j.N, c0 + c, v);
             tmem_put(acc + (uint32_t)c, v);
           }
-          if (o.keep == 1) emit<false, false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
-          else             m[0] = largest_of(m[0], odd, v);
+          if (!FOLD || o.keep == 1) emit<false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
+          else                      m[0] = largest_of(m[0], odd, v);
           if constexpr (GATED) {
             tmem_get(acc + up + (uint32_t)c, v);
             tmem_wait_ld();
             tmem_ld_ready(v);
-            if (o.keep == 1) emit<false, false>(pieces, &maps.kept[1], o.kept[1].vec, o.kept[1].data, o.kept[1].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
-            else             m[1] = largest_of(m[1], odd, v);
+            if (!FOLD || o.keep == 1) emit<false>(pieces, &maps.kept[1], o.kept[1].vec, o.kept[1].data, o.kept[1].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
+            else                      m[1] = largest_of(m[1], odd, v);
           }
         }
         if (add_bias) tmem_wait_st();
         add_bias = false;
-        if (o.keep == 2) {
+        if (FOLD && o.keep == 2) {
           odd = __any_sync(0xffffffffu, odd);
           if (cols < 128) {  // the other half of the group is with the warp of the other column half
             float* slot = &largest[0][32 * q + lane];
@@ -648,7 +611,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           if (last) release();
           tmem_ld_ready(v);
           tmem_ld_ready(u);
-          if (o.keep == 2) {
+          if (FOLD && o.keep == 2) {
             codes(0, v);
             codes(1, u);
           }
@@ -660,17 +623,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               v[k + 1] = h.y;
             }
           });
-          emit<false, false>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
+          emit<false>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
         } else {
           Residual<W> residual;
-          if (direct) residual.load(o, j, row, c0 + c);
+          if (o.residual) residual.load(o, j, row, c0 + c);
           Bias<W> bias;
           if (add_bias) bias.load(o, j.N, c0 + c);
           tmem_wait_ld();
           if (last) release();
           tmem_ld_ready(v);
           if (add_bias) bias.add(o, j.N, c0 + c, v);
-          if (o.keep == 2) codes(0, v);
+          if (FOLD && o.keep == 2) codes(0, v);
           with_act(o.act, [&](auto act) {
 #pragma unroll
             for (int k = 0; k < W; k += 2) {
@@ -679,14 +642,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               v[k + 1] = f.y;
             }
           });
-          if (direct) residual.add(v);
-          if (o.residual && !direct) {
-            if (j.f32) emit<true, true>(pieces, map_d, false, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
-            else       emit<false, true>(pieces, map_d, false, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
-          } else {
-            if (j.f32) emit<true, false>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
-            else       emit<false, false>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
-          }
+          if (o.residual) residual.add(v);
+          if (FOLD && j.f32) emit<true>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
+          else               emit<false>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
         }
       }
       if (!GATED && o.residual && tile + p.clusters < tiles) {  // the next tile's (here its place need not be held during the sums)

@@ -18,7 +18,7 @@ struct LinearKept {
   void* data = nullptr;
   float* scale = nullptr;
   int64_t ld = 0, lds = 0;
-  int vec = 0;                   // BF16: TMA writes it; 8-bit: rows start at multiples of 16 bytes
+  int vec = 0;                   // 1: rows start at multiples of 16 bytes
 };
 struct LinearOut {
   const void* bias = nullptr;    // N values or nullptr
@@ -37,7 +37,7 @@ struct LinearJob {
   int M = 0, N = 0;              // rows and columns of D
   void* d = nullptr;
   int64_t ldd = 0;
-  int d_tma = 0;                 // 1: aligned rows of whole 16 bytes, which TMA writes
+  int d_tma = 0;                 // 1: rows start at multiples of 16 bytes: TMA writes the whole 16 bytes of them
   int d_vec = 0;                 // 1: rows start at multiples of 8 bytes (BF16) or 16 bytes (FP32)
   int f32 = 0;
   int tiles_m = 0, tiles_n = 0;
@@ -69,7 +69,7 @@ constexpr int linear_pair_box(int tile_n, bool gated, bool fold) {
 int linear_pair_stages(int tile_n);
 int64_t linear_pair_smem(int tile_n);
 cudaError_t prepare_linear_pair();
-// fold: some job sums K tiles in more than one accumulator.
+// fold: some job has an FP32 output or keeps 8-bit values.
 cudaError_t launch_linear_pair(int tile_n, bool gated, bool fold, const LinearMaps& maps, const LinearPairParams& p, cudaStream_t stream);
 
 // The columns of D run along the tensor core's rows (B's tile of 128), its rows along the columns.
@@ -129,8 +129,8 @@ cudaError_t launch_linear_expand(LinearExpandParams& p, cudaStream_t stream);
 // 128-byte swizzle, zeros outside.
 cudaError_t encode_linear_map(const void* base, int64_t inner, int64_t outer, int64_t ld, int box_outer, CUtensorMap* map);
 
-// Map over D (`rows` x `cols` BF16 or FP32, row stride ld elements, 16-byte aligned rows of whole 16 bytes): boxes of box_cols x
-// 32, rows of 64 or 128 bytes with the swizzle of that width.
+// Map over D (`rows` x `cols` BF16 or FP32, row stride ld elements, rows that start at multiples of 16 bytes; what a row holds
+// beyond whole 16 bytes is left out, as TMA would write behind it): boxes of box_cols x 32, rows of 64 or 128 bytes with the swizzle of that width.
 cudaError_t encode_linear_out_map(const void* base, int64_t cols, int64_t rows, int64_t ld, bool bf16, int box_cols, CUtensorMap* map);
 
 }  // namespace sgemm_impl
