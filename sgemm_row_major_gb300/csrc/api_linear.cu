@@ -606,8 +606,8 @@ int sgemm_linear_backward(int64_t tokens, int64_t inputs, int64_t outputs, const
   g.act = activation;
   g.dbias = dbias;
   g.guard = {dev.fault, dev.bounds};
-  g.row_blocks = linear_grad_row_blocks(tokens, (int)outputs, dbias != nullptr, dev.pair_clusters > 0, dev.sm_count);
-  g.vec = outputs % 8 == 0 && rows_at(dY, lddy, 2, 16) && (!act || g.a.vec);
+  shape_linear_grad(&g, dev.pair_clusters > 0, dev.sm_count);
+  g.vec = rows_at(dY, lddy, 2, 16) && (!act || g.a.vec);
   // dA: dY itself where it can be read as it is and there is no activation
   Operand d(dY, lddy, nullptr, 0, tokens, outputs);
   const bool write = products && (act || d.copied);
@@ -618,6 +618,7 @@ int sgemm_linear_backward(int64_t tokens, int64_t inputs, int64_t outputs, const
       dev, stream,
       [&](Pieces* p) {
         g.da = write ? p->take<uint16_t>(tokens * ldd) : nullptr;
+        g.partial = dbias && !g.joined ? p->take<float>((int64_t)g.row_blocks * outputs) : nullptr;
         if (dX) w.place(p);
         if (dW) x.place(p);
       },
@@ -689,8 +690,8 @@ int sgemm_gated_backward(int64_t tokens, int64_t inputs, int64_t outputs, const 
   g.h = H;
   g.ldh = ldh;
   g.guard = {dev.fault, dev.bounds};
-  g.row_blocks = linear_grad_row_blocks(tokens, (int)outputs, false, true, dev.sm_count);
-  g.vec = outputs % 8 == 0 && rows_at(dH, lddh, 2, 16) && g.a.vec && g.b.vec && (!H || rows_at(H, ldh, 2, 16));
+  shape_linear_grad(&g, dev.pair_clusters > 0, dev.sm_count);
+  g.vec = rows_at(dH, lddh, 2, 16) && g.a.vec && g.b.vec && (!H || rows_at(H, ldh, 2, 16));
   Operand wg(gate, ldg, nullptr, 0, outputs, inputs), wu(up, ldu, nullptr, 0, outputs, inputs);
   Operand x(X ? X->data : nullptr, X ? X->ld : 1, X ? X->scale : nullptr, X ? X->lds : 1, tokens, inputs);
   const int64_t ldd = round8(outputs);

@@ -6,33 +6,47 @@
 //
 // A and B as the forward pass kept them: BF16, or 8-bit codes times the scale of their group of 128.  One pass over the data,
 // bound by the memory and nearly as much by the instructions of an activation's derivative (two values at a time in packed
-// arithmetic).  A thread takes 8 columns of a row (16 bytes of BF16, 8 of codes), eight threads a line of 128 bytes, and has all
-// its loads of two rows on their way before either is used.  Column sums are held per thread in FP32, joined within the CTA and
-// then by a cluster of up to 8 CTAs that share the rows of a strip of 64 columns, both in a fixed order: no second kernel.
+// arithmetic).  A thread takes 8 columns of a row (16 bytes of BF16, 8 of codes); what it
+// reads of its next four rows is on its way to shared memory while it works on one (in registers the loads of two rows covered
+// half of the memory's latency).  Column sums are held per thread in FP32 and joined within the CTA, then
+// by a cluster of up to 8 CTAs that share the rows of a strip, or (many rows and columns, where a cluster's CTAs are too few to
+// fill the chip) by a second kernel; always in a fixed order.
+#include <algorithm>
+
 #include "linear_common.cuh"
 
 namespace sgemm_impl {
 namespace lin {
 namespace {
 
-constexpr int kThreads = 256, kStrip = 64, kLanes = kStrip / 8, kRowLanes = kThreads / kLanes;
-constexpr int kBatch = 2;         // rows whose loads are on their way together
+constexpr int kThreads = 256, kWide = 256, kNarrow = 64;  // columns of a strip
+constexpr int kStages = 4;        // rows ahead per thread
+constexpr int kBatch = 2;         // without alignment: rows whose loads are on their way together
 constexpr int kExpandChunks = 4;  // the same of the copies, in chunks of 8 columns
 
-// 8 consecutive values, n of them there, sent for and then waited for.  VEC: n is 8 or 0, and they can be read at once.
-template <bool CODES, bool VEC>
+// 8 consecutive values of codes and their scale.
+__device__ __forceinline__ void decode(uint2 c, float scale, float2 (&x)[4]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((e < 2 ? c.x : c.y) >> (16 * (e % 2))), __NV_E4M3);
+    x[e] = mul(__half22float2(__half2(h)), both(scale));
+  }
+}
+
+// 8 consecutive values at any alignment, n of them there, sent for and then waited for.
+template <bool CODES>
 struct KeptLoad;
-template <bool VEC>
-struct KeptLoad<false, VEC> {
-  f8::Loading<__nv_bfloat16, VEC> v;
+template <>
+struct KeptLoad<false> {
+  f8::Loading<__nv_bfloat16, false> v;
   __device__ __forceinline__ void load(const LinearKeptIn& k, int64_t rows, int cols, int64_t row, int col, int n, const Guard& g) {
     const f8::Rows<__nv_bfloat16> m(k.data, rows, k.ld, cols, g);
     v.load(m.base + row * k.ld + col, n, m);
   }
   __device__ __forceinline__ void get(float2 (&x)[4]) const { v.get().get(&x[0].x); }
 };
-template <bool VEC>
-struct KeptLoad<true, VEC> {
+template <>
+struct KeptLoad<true> {
   uint2 c;
   float s;
   __device__ __forceinline__ void load(const LinearKeptIn& k, int64_t rows, int cols, int64_t row, int col, int n, const Guard& g) {
@@ -43,21 +57,46 @@ struct KeptLoad<true, VEC> {
     const int64_t at = row * k.ld + col;
     if (!in_range(g.fault, g.word, f8::kSiteCodes, at, n, extent(rows, k.ld, cols))) return;
     s = get_at(g, f8::kSiteScale, k.scale, row * k.lds + (col >> 7), extent(rows, k.lds, (cols + 127) / 128));
-    if (VEC) {
-      c = *reinterpret_cast<const uint2*>(base + at);
-    } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (e < n) (e < 4 ? c.x : c.y) |= (uint32_t)base[at + e] << (8 * (e % 4));
-    }
+    for (int e = 0; e < 8; ++e)
+      if (e < n) (e < 4 ? c.x : c.y) |= (uint32_t)base[at + e] << (8 * (e % 4));
   }
-  __device__ __forceinline__ void get(float2 (&x)[4]) const {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)((e < 2 ? c.x : c.y) >> (16 * (e % 2))), __NV_E4M3);
-      x[e] = mul(__half22float2(__half2(h)), both(s));
-    }
+  __device__ __forceinline__ void get(float2 (&x)[4]) const { decode(c, s, x); }
+};
+
+template <int BYTES>
+__device__ __forceinline__ void copy_async(void* dst, const void* src) {
+  if constexpr (BYTES == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+  else                       asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_addr(dst)), "l"(src), "n"(BYTES) : "memory");
+}
+
+// 8 consecutive values that can be read at once, copied to shared memory ahead: a place per thread and stage, which no other
+// thread reads.
+template <bool CODES>
+struct KeptRing;
+template <>
+struct KeptRing<false> {
+  uint4 v[kStages][kThreads];
+  __device__ __forceinline__ void copy(int s, const LinearKeptIn& k, int64_t rows, int cols, int64_t row, int col, const Guard& g) {
+    const int64_t at = row * k.ld + col;
+    if (in_range(g.fault, g.word, f8::kSiteIn, at, 8, extent(rows, k.ld, cols))) copy_async<16>(&v[s][threadIdx.x], static_cast<const __nv_bfloat16*>(k.data) + at);
   }
+  __device__ __forceinline__ void get(int s, float2 (&x)[4]) const {
+    Chunk<__nv_bfloat16> c;
+    c.raw = v[s][threadIdx.x];
+    c.get(&x[0].x);
+  }
+};
+template <>
+struct KeptRing<true> {
+  uint2 c[kStages][kThreads];
+  float scale[kStages][kThreads];
+  __device__ __forceinline__ void copy(int s, const LinearKeptIn& k, int64_t rows, int cols, int64_t row, int col, const Guard& g) {
+    const int64_t at = row * k.ld + col, group = row * k.lds + (col >> 7);
+    if (in_range(g.fault, g.word, f8::kSiteCodes, at, 8, extent(rows, k.ld, cols))) copy_async<8>(&c[s][threadIdx.x], static_cast<const uint8_t*>(k.data) + at);
+    if (in_range(g.fault, g.word, f8::kSiteScale, group, 1, extent(rows, k.lds, (cols + 127) / 128))) copy_async<4>(&scale[s][threadIdx.x], k.scale + group);
+  }
+  __device__ __forceinline__ void get(int s, float2 (&x)[4]) const { decode(c[s][threadIdx.x], scale[s][threadIdx.x], x); }
 };
 
 // 8 values as BF16, n of them there, to a row of an aligned (VEC) or any other matrix.
@@ -67,27 +106,89 @@ __device__ __forceinline__ void put8(void* base, int64_t ld, int64_t rows, int c
   f8::store_chunk<__nv_bfloat16, VEC>(static_cast<__nv_bfloat16*>(base) + row * ld + col, &x[0].x, n, m);
 }
 
-// ACT: the activation (one kernel for each: the branch around eight values' work cost as much as the work).
+// ACT: the activation (one kernel for each: the branch around eight values' work cost as much as the work).  VEC: chunks of 8
+// columns can be read and written at once (but for one that a row ends in).
 template <int ACT, bool GATED, bool CODES, bool VEC, bool SUMS>
-__global__ void __launch_bounds__(kThreads) linear_grad_kernel(const __grid_constant__ LinearGradParams p) {
+__global__ void __launch_bounds__(kThreads, VEC ? 3 : 2) linear_grad_kernel(const __grid_constant__ LinearGradParams p) {
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   asm volatile("griddepcontrol.wait;" ::: "memory");
-  const int col = (int)blockIdx.x * kStrip + 8 * (int)(threadIdx.x % kLanes);
+  const int lanes = p.strip / 8, at = (int)threadIdx.x % lanes, step = kThreads / lanes;  // (8 or 32 threads to a row)
+  const int col = (int)blockIdx.x * p.strip + 8 * at;
   const int n = max(0, min(8, p.cols - col));
-  const int64_t r0 = p.rows * blockIdx.y / p.row_blocks, r1 = p.rows * (blockIdx.y + 1) / p.row_blocks;
+  const int64_t r0 = p.rows * blockIdx.y / p.row_blocks + threadIdx.x / lanes, r1 = p.rows * (blockIdx.y + 1) / p.row_blocks;
   const LinearKeptIn y{p.dy, nullptr, p.lddy, 0, 0};
   constexpr bool kAct = ACT != SGEMM_ACT_NONE || GATED;  // A is read
   float2 sum[4];
 #pragma unroll
   for (int e = 0; e < 4; ++e) sum[e] = both(0.0f);
-  if (n > 0) {
-    for (int64_t r = r0 + threadIdx.x / kLanes; r < r1; r += kBatch * kRowLanes) {
-      KeptLoad<false, VEC> dy[kBatch];
-      KeptLoad<CODES, VEC> a[kBatch], b[kBatch];
+  // the work on 8 values of row r
+  const auto work = [&](auto vec, int64_t row, const float2 (&g)[4], const float2 (&x)[4], const float2 (&u)[4]) {
+    constexpr bool kVec = decltype(vec)::value;
+    float2 d[4];
+    if constexpr (GATED) {
+      float2 du[4], h[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float2 f, df;
+        act_grad<ACT>(x[e], f, df);
+        d[e] = mul(mul(g[e], u[e]), df);
+        du[e] = mul(g[e], f);
+        h[e] = mul(f, u[e]);
+      }
+      if (p.da) {
+        put8<kVec>(p.da, p.ldd, p.rows, p.cols, row, col, n, d, p.guard);
+        put8<kVec>(p.db, p.ldd, p.rows, p.cols, row, col, n, du, p.guard);
+      }
+      if (p.h) put8<kVec>(p.h, p.ldh, p.rows, p.cols, row, col, n, h, p.guard);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        float2 f, df;
+        if (kAct) act_grad<ACT>(x[e], f, df);
+        d[e] = kAct ? mul(g[e], df) : g[e];
+        if (SUMS) sum[e] = add(sum[e], d[e]);
+      }
+      if (p.da) put8<kVec>(p.da, p.ldd, p.rows, p.cols, row, col, n, d, p.guard);
+    }
+  };
+  if constexpr (VEC) {
+    struct None {};
+    __shared__ KeptRing<false> ring_y;
+    __shared__ typename std::conditional<kAct, KeptRing<CODES>, None>::type ring_a;
+    __shared__ typename std::conditional<GATED, KeptRing<CODES>, None>::type ring_b;
+    if (n == 8) {
+      const auto copy = [&](int s, int64_t row) {
+        if (row < r1) {
+          ring_y.copy(s, y, p.rows, p.cols, row, col, p.guard);
+          if constexpr (kAct) ring_a.copy(s, p.a, p.rows, p.cols, row, col, p.guard);
+          if constexpr (GATED) ring_b.copy(s, p.b, p.rows, p.cols, row, col, p.guard);
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+      };
+#pragma unroll
+      for (int s = 0; s < kStages; ++s) copy(s, r0 + s * step);
+      int s = 0;
+      for (int64_t row = r0; row < r1; row += step) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+        float2 g[4], x[4], u[4];
+        ring_y.get(s, g);
+        if constexpr (kAct) ring_a.get(s, x);
+        if constexpr (GATED) ring_b.get(s, u);
+        work(std::true_type{}, row, g, x, u);
+        copy(s, row + kStages * step);
+        s = s + 1 == kStages ? 0 : s + 1;
+      }
+      asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+  }
+  if (VEC ? n > 0 && n < 8 : n > 0) {
+    for (int64_t r = r0; r < r1; r += kBatch * step) {
+      KeptLoad<false> dy[kBatch];
+      KeptLoad<CODES> a[kBatch], b[kBatch];
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const bool there = r + k * kRowLanes < r1;
-        const int64_t row = there ? r + k * kRowLanes : r;
+        const bool there = r + k * step < r1;
+        const int64_t row = there ? r + k * step : r;
         const int here = there ? n : 0;
         dy[k].load(y, p.rows, p.cols, row, col, here, p.guard);
         if (kAct) a[k].load(p.a, p.rows, p.cols, row, col, here, p.guard);
@@ -95,59 +196,39 @@ __global__ void __launch_bounds__(kThreads) linear_grad_kernel(const __grid_cons
       }
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
-        const int64_t row = r + k * kRowLanes;
-        if (row >= r1) break;
-        float2 g[4], x[4], d[4];
+        if (r + k * step >= r1) break;
+        float2 g[4], x[4], u[4];
         dy[k].get(g);
         if (kAct) a[k].get(x);
-        if (GATED) {
-          float2 u[4], du[4], h[4];
-          b[k].get(u);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float2 f, df;
-            act_grad<ACT>(x[e], f, df);
-            d[e] = mul(mul(g[e], u[e]), df);
-            du[e] = mul(g[e], f);
-            h[e] = mul(f, u[e]);
-          }
-          if (p.da) {
-            put8<VEC>(p.da, p.ldd, p.rows, p.cols, row, col, n, d, p.guard);
-            put8<VEC>(p.db, p.ldd, p.rows, p.cols, row, col, n, du, p.guard);
-          }
-          if (p.h) put8<VEC>(p.h, p.ldh, p.rows, p.cols, row, col, n, h, p.guard);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            float2 f, df;
-            if (kAct) act_grad<ACT>(x[e], f, df);
-            d[e] = kAct ? mul(g[e], df) : g[e];
-            if (SUMS) sum[e] = add(sum[e], d[e]);
-          }
-          if (p.da) put8<VEC>(p.da, p.ldd, p.rows, p.cols, row, col, n, d, p.guard);
-        }
+        if (GATED) b[k].get(u);
+        work(std::false_type{}, r + k * step, g, x, u);
       }
     }
   }
   if constexpr (SUMS) {
-    __shared__ float warps[kThreads / 32][kStrip], strip[kStrip];
+    __shared__ __align__(16) float warps[kThreads / 32][kWide];
+    __shared__ float strip[kWide];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {  // over the warp's four rows
+    for (int e = 0; e < 4; ++e) {
+      if (lanes == 8)  // over the warp's four rows
 #pragma unroll
-      for (int m = kLanes; m < 32; m *= 2)
-        sum[e] = add(sum[e], make_float2(__shfl_xor_sync(0xffffffffu, sum[e].x, m), __shfl_xor_sync(0xffffffffu, sum[e].y, m)));
-      if (threadIdx.x % 32 < kLanes) *reinterpret_cast<float2*>(&warps[threadIdx.x / 32][8 * (threadIdx.x % kLanes) + 2 * e]) = sum[e];
+        for (int m = 8; m < 32; m *= 2)
+          sum[e] = add(sum[e], make_float2(__shfl_xor_sync(0xffffffffu, sum[e].x, m), __shfl_xor_sync(0xffffffffu, sum[e].y, m)));
+      if ((int)threadIdx.x % 32 < lanes) *reinterpret_cast<float2*>(&warps[threadIdx.x / 32][8 * at + 2 * e]) = sum[e];
     }
     __syncthreads();
+    const int c = (int)blockIdx.x * p.strip + (int)threadIdx.x;
+    const bool mine = (int)threadIdx.x < p.strip && c < p.cols;
     float s = 0.0f;
-    if (threadIdx.x < kStrip) {
+    if (mine) {
 #pragma unroll
       for (int w = 0; w < kThreads / 32; ++w) s += warps[w][threadIdx.x];
       strip[threadIdx.x] = s;
+      if (p.partial) put_at(p.guard, f8::kSitePart, p.partial, (int64_t)blockIdx.y * p.cols + c, (int64_t)p.row_blocks * p.cols, s);
     }
-    const int c = (int)blockIdx.x * kStrip + (int)threadIdx.x;
+    if (p.partial) return;
     tc::cluster_sync();
-    if (blockIdx.y == 0 && threadIdx.x < kStrip && c < p.cols) {
+    if (blockIdx.y == 0 && mine) {
       for (int k = 1; k < p.row_blocks; ++k) {  // (the row blocks are the cluster)
         float v;
         asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(tc::map_to_rank(smem_addr(&strip[threadIdx.x]), (uint32_t)k)) : "memory");
@@ -156,6 +237,28 @@ __global__ void __launch_bounds__(kThreads) linear_grad_kernel(const __grid_cons
       put_at(p.guard, f8::kSiteOut, p.dbias, c, p.cols, s);
     }
     tc::cluster_sync();  // no CTA leaves while its sums may be read
+  }
+}
+
+// dbias from the row blocks' sums: a column per lane, the warps share the blocks.
+__global__ void __launch_bounds__(kThreads) linear_bias_kernel(const __grid_constant__ LinearGradParams p) {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  constexpr int kWarps = kThreads / 32;
+  __shared__ float part[kWarps][32];
+  const int warp = (int)threadIdx.x / 32, lane = (int)threadIdx.x % 32, c = (int)blockIdx.x * 32 + lane;
+  float s = 0.0f;
+  if (c < p.cols)
+#pragma unroll 4
+    for (int b = warp; b < p.row_blocks; b += kWarps)
+      s += get_at(p.guard, f8::kSitePart, p.partial, (int64_t)b * p.cols + c, (int64_t)p.row_blocks * p.cols);
+  part[warp][lane] = s;
+  __syncthreads();
+  if (warp == 0 && c < p.cols) {
+    s = 0.0f;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) s += part[w][lane];
+    put_at(p.guard, f8::kSiteOut, p.dbias, c, p.cols, s);
   }
 }
 
@@ -171,7 +274,7 @@ __global__ void __launch_bounds__(kThreads) linear_expand_kernel(const __grid_co
   const int64_t total = m.rows * chunks;
   const auto run = [&](auto codes) {
     constexpr int kChunks = kExpandChunks;
-    KeptLoad<decltype(codes)::value, false> v[kChunks];
+    KeptLoad<decltype(codes)::value> v[kChunks];
     int64_t row[kChunks];
     int col[kChunks], n[kChunks];
 #pragma unroll
@@ -218,9 +321,10 @@ cudaError_t launch(void (*kernel)(P), dim3 grid, int cluster_y, const P& p, cuda
 
 template <bool GATED, bool CODES, bool VEC, bool SUMS>
 cudaError_t launch_act(const LinearGradParams& p, cudaStream_t stream) {
-  const dim3 grid((unsigned)((p.cols + kStrip - 1) / kStrip), (unsigned)p.row_blocks);
+  const dim3 grid((unsigned)((p.cols + p.strip - 1) / p.strip), (unsigned)p.row_blocks);
   cudaError_t e = cudaErrorInvalidValue;
-  with_act(p.act, [&](auto act) { e = launch(linear_grad_kernel<decltype(act)::value, GATED, CODES, VEC, SUMS>, grid, SUMS ? p.row_blocks : 1, p, stream); });
+  with_act(p.act, [&](auto act) { e = launch(linear_grad_kernel<decltype(act)::value, GATED, CODES, VEC, SUMS>, grid, SUMS && !p.partial ? p.row_blocks : 1, p, stream); });
+  if (SUMS && p.partial && e == cudaSuccess) e = launch(linear_bias_kernel, dim3((unsigned)((p.cols + 31) / 32)), 1, p, stream);
   return e;
 }
 template <bool VEC>
@@ -234,16 +338,21 @@ cudaError_t launch_form(const LinearGradParams& p, cudaStream_t stream) {
 }  // namespace
 }  // namespace lin
 
-int linear_grad_row_blocks(int64_t rows, int cols, bool sums, bool clusters, int sm_count) {
-  if (sums && !clusters) return 1;
-  const int64_t strips = (cols + lin::kStrip - 1) / lin::kStrip;
-  // eight CTAs per SM, of no fewer rows than two batches
-  const int64_t want = (8 * (int64_t)sm_count + strips - 1) / strips, most = (rows + 2 * lin::kBatch * lin::kRowLanes - 1) / (2 * lin::kBatch * lin::kRowLanes);
-  int64_t blocks = want < most ? want : most;
-  if (!sums) return (int)(blocks < 1 ? 1 : blocks > 65535 ? 65535 : blocks);
-  int n = 8;  // a cluster
-  while (n > 1 && n > most) n /= 2;
-  return n;
+void shape_linear_grad(LinearGradParams* p, bool clusters, int sm_count) {
+  // strips of 512 bytes of a row (64 of 128 bytes read and wrote at half the memory's rate in the gated form), or of 128 bytes
+  // where there would be too few of them
+  const int64_t wide = (p->cols + lin::kWide - 1) / lin::kWide, most = (p->rows + 31) / 32;
+  p->strip = wide * std::min<int64_t>(8, most) >= sm_count ? lin::kWide : lin::kNarrow;
+  const int64_t strips = (p->cols + p->strip - 1) / p->strip;
+  p->joined = p->dbias && p->strip == lin::kNarrow;
+  if (p->joined) {
+    int n = clusters ? 8 : 1;  // a cluster's CTAs
+    while (n > 1 && n > most) n /= 2;
+    p->row_blocks = n;
+  } else {
+    const int64_t want = (8 * (int64_t)sm_count + strips - 1) / strips;  // eight CTAs per SM, of no fewer than 32 rows
+    p->row_blocks = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 65535));
+  }
 }
 
 cudaError_t launch_linear_grad(const LinearGradParams& p, cudaStream_t stream) {

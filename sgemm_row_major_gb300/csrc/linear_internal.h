@@ -103,11 +103,13 @@ struct LinearGradParams {
   void *da = nullptr, *db = nullptr, *h = nullptr;  // nullptr: not wanted (da and db: aligned rows)
   int64_t ldd = 0, ldh = 0;
   float* dbias = nullptr;        // nullptr: not wanted
-  int row_blocks = 0;
-  int vec = 0;                   // 1: whole chunks of 8 columns, all of which can be read and written at once
+  int strip = 0, row_blocks = 0; // columns of a CTA; CTAs that share the rows
+  int joined = 0;                // dbias: 1: a cluster's CTAs add their sums, 0: a second kernel those in `partial`
+  float* partial = nullptr;      // [row_blocks][cols]
+  int vec = 0;                   // 1: chunks of 8 columns can be read and written at once
   Guard guard;
 };
-int linear_grad_row_blocks(int64_t rows, int cols, bool sums, bool clusters, int sm_count);
+void shape_linear_grad(LinearGradParams* p, bool clusters, int sm_count);  // fills strip, row_blocks and joined
 cudaError_t launch_linear_grad(const LinearGradParams& p, cudaStream_t stream);
 
 // Stored matrices as aligned BF16 rows (ldd a multiple of 8): BF16 of any alignment copied, 8-bit values times their scales.
