@@ -48,23 +48,28 @@ struct Shape {
   int64_t pair_tiles(int tile) const { return ceil_div(M, 256) * ceil_div(N, gated ? tile / 2 : tile); }
 };
 
-// Times in ns that the choice of kernel goes by.  In the pair kernel, by tile width: a K tile of 64, and the rest of a tile.
-// On the short side: a K tile in a CTA that has its SM to itself, the rest of a tile, and what joining a tile's shares adds.
+// Times in ns that the choice of kernel goes by, fitted to 640 launches of 54 products (1 to 4096 tokens, gradients and gated ones
+// among them) forced to each kernel, tile and split on a GB300: they give those launches' times to about 12%, and the launch they
+// choose takes 3% longer than the fastest on average.  In the pair kernel, by tile width: a K tile of 64, and the rest of a tile,
+// and the rate at which few clusters read.  On the short side: a K tile in a CTA that has its SM to itself, the rest of a tile, and
+// what joining a tile's shares adds.
 struct PairCost {
   int tile, k_ns, tile_ns;
 };
-constexpr PairCost kPairCost[] = {{256, 290, 1500}, {128, 190, 1200}, {64, 150, 1000}};
+constexpr PairCost kPairCost[] = {{256, 294, 2020}, {128, 215, 1060}, {64, 209, 740}};
 struct ShortCost {
   int tile, k_ns, tile_ns, join_ns;
 };
-constexpr ShortCost kShortCost[] = {{16, 160, 1200, 800}, {32, 170, 1600, 600}, {64, 220, 2400, 650}, {128, 300, 4000, 1200}};
-constexpr double kPairLaunchNs = 4500, kShortLaunchNs = 2750;
-constexpr double kSharedSm = 0.3;        // a K tile takes this much longer with a second CTA on the SM
-constexpr double kSmBytesPerNs = 44.7;   // an SM's share of the memory bandwidth
+constexpr ShortCost kShortCost[] = {{16, 267, 2730, 570}, {32, 298, 3580, 85}, {64, 328, 4530, 5}, {128, 154, 6330, 0}};
+constexpr double kPairLaunchNs = 3000, kShortLaunchNs = 790;
+constexpr double kPairBytesPerNs = 3490;
+constexpr double kSharedSm = 0.34;       // a K tile takes this much longer with a second CTA on the SM
+constexpr double kGatedK = 1.19, kGatedTile = 1.36;  // a gated tile's K tiles and rest against a plain one's
+constexpr double kSmBytesPerNs = 89.0;   // an SM's largest share of the memory bandwidth
 
 // SMs that clusters of `split` CTAs can use at a time: groups of 4 or 8 do not fill every part of the chip.
 int64_t cluster_sms(int sm_count, int split) {
-  return split <= 2 ? sm_count : std::max(1, split == 4 ? sm_count * 18 / 19 : sm_count * 16 / 19);
+  return split <= 2 ? sm_count : std::max(1, split == 4 ? sm_count * 18 / 19 : sm_count * 15 / 19);
 }
 
 bool short_alone(int tile, bool gated) { return gated || tile == 128; }  // one CTA per SM
@@ -82,7 +87,9 @@ struct Choice {
 // The pair kernel's time for up to three products in one launch: that of the cluster with the most work (tiles are dealt round
 // robin; a cluster has one more of a product's tiles where the deal of its last round starts, so one of these has the most).
 double pair_ns(const Shape* s, int n, const PairCost& c, int64_t clusters) {
-  double most = 0.0;
+  double most = 0.0, bytes = 0.0;
+  for (int i = 0; i < n; ++i)
+    bytes += 2.0 * ((double)s[i].M * s[i].K * s[i].segments + (double)s[i].N * s[i].K * s[i].segments * (s[i].gated ? 2 : 1) + (double)s[i].M * s[i].N);
   int64_t start = 0;
   for (int i = 0; i < n; start += s[i++].pair_tiles(c.tile)) {
     const int64_t at = (start + s[i].pair_tiles(c.tile) / clusters * clusters) % clusters;
@@ -96,7 +103,7 @@ double pair_ns(const Shape* s, int n, const PairCost& c, int64_t clusters) {
     }
     most = std::max(most, ns);
   }
-  return kPairLaunchNs + most;
+  return kPairLaunchNs + std::max(most, bytes / kPairBytesPerNs);
 }
 
 // The cheapest launch of one product (several: in one launch of the pair kernel), among the variant, tile and split that are
@@ -129,10 +136,10 @@ Choice choose(const Shape* s, int n, int64_t clusters, int sm_count, int variant
         if (split != 0 ? split != k : k > 1 && kt < 2 * k) continue;  // two K tiles per CTA at least
         const int per_sm = short_alone(c.tile, gated) ? 1 : 2;
         const double on_sm = std::min((double)per_sm, std::max(1.0, (double)tiles * k / sm_count));
-        const double one = std::max(c.k_ns * wide * (1.0 + kSharedSm * (on_sm - 1.0)), on_sm * (16384 * wide + 64 * c.tile) / kSmBytesPerNs);
+        const double one = std::max(c.k_ns * (gated ? kGatedK : 1.0) * (1.0 + kSharedSm * (on_sm - 1.0)), on_sm * (16384 * wide + 64 * c.tile) / kSmBytesPerNs);
         const double rounds = (double)ceil_div(tiles * k, cluster_sms(sm_count, k) * per_sm);
         offer(SGEMM_VARIANT_LINEAR_SHORT, c.tile, k,
-              kShortLaunchNs + rounds * (ceil_div(kt, k) * one + c.tile_ns + (k > 1 ? c.join_ns : 0)));
+              kShortLaunchNs + rounds * (ceil_div(kt, k) * one + c.tile_ns * (gated ? kGatedTile : 1.0) + (k > 1 ? c.join_ns : 0)));
       }
     }
   }
