@@ -67,9 +67,10 @@ constexpr double kSharedSm = 0.34;       // a K tile takes this much longer with
 constexpr double kGatedK = 1.19, kGatedTile = 1.36;  // a gated tile's K tiles and rest against a plain one's
 constexpr double kSmBytesPerNs = 89.0;   // an SM's largest share of the memory bandwidth
 
-// SMs that clusters of `split` CTAs can use at a time: groups of 4 or 8 do not fill every part of the chip.
-int64_t cluster_sms(int sm_count, int split) {
-  return split <= 2 ? sm_count : std::max(1, split == 4 ? sm_count * 18 / 19 : sm_count * 15 / 19);
+// CTAs that run at a time in clusters of `split` with `per_sm` to an SM: groups of 4 or 8 do not fill every part of the chip.
+int64_t cluster_ctas(int sm_count, int split, int per_sm) {
+  const int of19 = split <= 2 ? 19 : split == 4 ? 18 : per_sm > 1 ? 17 : 15;
+  return std::max<int64_t>(split, (int64_t)sm_count * per_sm * of19 / 19);
 }
 
 bool short_alone(int tile, bool gated) { return gated || tile == 128; }  // one CTA per SM
@@ -137,7 +138,7 @@ Choice choose(const Shape* s, int n, int64_t clusters, int sm_count, int variant
         const int per_sm = short_alone(c.tile, gated) ? 1 : 2;
         const double on_sm = std::min((double)per_sm, std::max(1.0, (double)tiles * k / sm_count));
         const double one = std::max(c.k_ns * (gated ? kGatedK : 1.0) * (1.0 + kSharedSm * (on_sm - 1.0)), on_sm * (16384 * wide + 64 * c.tile) / kSmBytesPerNs);
-        const double rounds = (double)ceil_div(tiles * k, cluster_sms(sm_count, k) * per_sm);
+        const double rounds = (double)ceil_div(tiles * k, cluster_ctas(sm_count, k, per_sm));
         offer(SGEMM_VARIANT_LINEAR_SHORT, c.tile, k,
               kShortLaunchNs + rounds * (ceil_div(kt, k) * one + c.tile_ns * (gated ? kGatedTile : 1.0) + (k > 1 ? c.join_ns : 0)));
       }

@@ -154,54 +154,27 @@ __device__ __forceinline__ void emit(Pieces<BYTES>& pieces, const CUtensorMap* m
   }
 }
 
-// W values of the bias, and of one row of the residual (whose rows are aligned): sent for before the sums are waited for.
+// W values of the bias, or of one row of the residual (whose rows are aligned), sent for before the sums are waited for: 8 at a
+// time where they are aligned (vec), at a row's end and otherwise one by one.
 template <int W>
-struct Bias {
+struct Ahead {
   uint4 c[W / 8];
-  __device__ __forceinline__ static bool whole(const LinearOut& o, int N, int col0) { return o.bias_vec && col0 + W <= N; }
-  __device__ __forceinline__ void load(const LinearOut& o, int N, int col0) {
-    if (whole(o, N, col0) && in_range(o.guard.fault, o.guard.word, f8::kSiteIn, col0, W, N)) {
-#pragma unroll
-      for (int e = 0; e < W / 8; ++e) c[e] = __ldg(reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(o.bias) + col0) + e);
-    }
-  }
-  __device__ __forceinline__ void add(const LinearOut& o, int N, int col0, float (&v)[W]) const {
-    if (whole(o, N, col0)) {
-#pragma unroll
-      for (int e = 0; e < W / 8; ++e) {
-        Chunk<__nv_bfloat16> b;
-        float x[8];
-        b.raw = c[e];
-        b.get(x);
-        add_to<8>(&v[8 * e], x);
-      }
-      return;
-    }
-#pragma unroll
-    for (int e = 0; e < W; ++e)
-      if (col0 + e < N) v[e] += __bfloat162float(get_at(o.guard, f8::kSiteIn, static_cast<const __nv_bfloat16*>(o.bias), col0 + e, N));
-  }
-};
-
-template <int W>
-struct Residual {
-  uint4 c[W / 8];
-  __device__ __forceinline__ void load(const LinearOut& o, const LinearJob& j, int row, int col0) {
-    const __nv_bfloat16* p = static_cast<const __nv_bfloat16*>(o.residual) + (int64_t)row * o.ldr + col0;
-    if (row < j.M && col0 + W <= j.N && r_ok(o, j, row, col0, W)) {
-#pragma unroll
-      for (int e = 0; e < W / 8; ++e) c[e] = reinterpret_cast<const uint4*>(p)[e];
-      return;
-    }
+  // p: the first of them, of which `left` are there, at element `at` of the `size` of its buffer
+  __device__ __forceinline__ void load(const Guard& g, const __nv_bfloat16* p, bool vec, int left, int64_t at, int64_t size) {
 #pragma unroll
     for (int e = 0; e < W / 8; ++e) {
-      float x[8];
-      const int n = row < j.M ? j.N - col0 - 8 * e : 0;
+      const int n = min(8, left - 8 * e);
+      c[e] = make_uint4(0u, 0u, 0u, 0u);
+      if (n <= 0 || !in_range(g.fault, g.word, f8::kSiteIn, at + 8 * e, n, size)) continue;
+      if (vec && n == 8) {
+        c[e] = reinterpret_cast<const uint4*>(p)[e];
+      } else {
+        uint32_t w[4] = {0u, 0u, 0u, 0u};
 #pragma unroll
-      for (int k = 0; k < 8; ++k) x[k] = k < n && r_ok(o, j, row, col0 + 8 * e + k, 1) ? __bfloat162float(p[8 * e + k]) : 0.0f;
-      Chunk<__nv_bfloat16> b;
-      b.put(x);  // exact: every value was BF16
-      c[e] = b.raw;
+        for (int k = 0; k < 8; ++k)
+          if (k < n) w[k / 2] |= (uint32_t)reinterpret_cast<const uint16_t*>(p)[8 * e + k] << (16 * (k % 2));
+        c[e] = make_uint4(w[0], w[1], w[2], w[3]);
+      }
     }
   }
   __device__ __forceinline__ void add(float (&v)[W]) const {
@@ -213,6 +186,13 @@ struct Residual {
       b.get(x);
       add_to<8>(&v[8 * e], x);
     }
+  }
+  __device__ __forceinline__ void bias(const LinearOut& o, const LinearJob& j, int col0) {
+    load(o.guard, static_cast<const __nv_bfloat16*>(o.bias) + col0, o.bias_vec, j.N - col0, col0, j.N);
+  }
+  __device__ __forceinline__ void residual(const LinearOut& o, const LinearJob& j, int row, int col0) {
+    const int64_t at = (int64_t)row * o.ldr + col0;
+    load(o.guard, static_cast<const __nv_bfloat16*>(o.residual) + at, true, row < j.M ? j.N - col0 : 0, at, extent(j.M, o.ldr, j.N));
   }
 };
 
@@ -465,6 +445,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     bool ok = true;
     int b = 0;
     uint32_t b_lap = 0, asked = 0;  // tiles whose largest values have been exchanged
+    const auto fetch = [&](int tile) {  // has a tile's residual brought to L2
+      if (GATED || !o.residual || tile >= tiles) return;
+      const Place to(p, tile);
+      prefetch_residual(o, p.job[to.job], to.tm * BM + BMC * (int)rank + 32 * q + lane, to.tn * TD + cols * part, cols);
+    };
+    fetch(cl);
+    fetch(cl + p.clusters);
     for (int tile = cl; ok && tile < tiles; tile += p.clusters) {
       const Place at(p, tile);
       const LinearJob& j = p.job[at.job];
@@ -537,13 +524,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll 1
         for (int c = 0; c < cols; c += W) {
           float v[W];
-          Bias<W> bias;
+          Ahead<W> bias;
           tmem_get(acc + (uint32_t)c, v);
-          if (add_bias) bias.load(o, j.N, c0 + c);
+          if (add_bias) bias.bias(o, j, c0 + c);
           tmem_wait_ld();
           tmem_ld_ready(v);
           if (add_bias) {
-            bias.add(o, j.N, c0 + c, v);
+            bias.add(v);
             tmem_put(acc + (uint32_t)c, v);
           }
           if (!FOLD || o.keep == 1) emit<false>(pieces, &maps.kept[0], o.kept[0].vec, o.kept[0].data, o.kept[0].ld, o, j, f8::kSiteCodes, row0, c0 + c, v);
@@ -625,14 +612,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           });
           emit<false>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
         } else {
-          Residual<W> residual;
-          if (o.residual) residual.load(o, j, row, c0 + c);
-          Bias<W> bias;
-          if (add_bias) bias.load(o, j.N, c0 + c);
+          Ahead<W> residual, bias;
+          if (o.residual) residual.residual(o, j, row, c0 + c);
+          if (add_bias) bias.bias(o, j, c0 + c);
           tmem_wait_ld();
           if (last) release();
           tmem_ld_ready(v);
-          if (add_bias) bias.add(o, j.N, c0 + c, v);
+          if (add_bias) bias.add(v);
           if (FOLD && o.keep == 2) codes(0, v);
           with_act(o.act, [&](auto act) {
 #pragma unroll
@@ -647,10 +633,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           else               emit<false>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
         }
       }
-      if (!GATED && o.residual && tile + p.clusters < tiles) {  // the next tile's (here its place need not be held during the sums)
-        const Place to(p, tile + p.clusters);
-        prefetch_residual(o, p.job[to.job], to.tm * BM + BMC * (int)rank + 32 * q + lane, to.tn * TD + cols * part, cols);
-      }
+      fetch(tile + 2 * p.clusters);  // (its place need not be held during the sums here)
     }
     if (lane == 0) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
     __syncwarp();
