@@ -13,7 +13,7 @@ import ctypes
 from collections import namedtuple
 
 from . import PlanStruct, SgemmError, fp8
-from .fp8 import ROW, Fp8Matrix, _empty, _new_matrix, _on, _rows, _type
+from .fp8 import ROW, Fp8Matrix, _empty, _new_matrix, _on, _rows
 
 ACTIVATIONS = {None: 0, "relu": 1, "silu": 2, "gelu": 3, "gelu_tanh": 4}
 VARIANTS = {0: "AUTO", 40: "LINEAR_PAIR", 41: "LINEAR_SHORT"}
@@ -61,6 +61,14 @@ def _matrix(x, name, rows=None, cols=None):
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{name} must have shape ({'any' if rows is None else rows}, {'any' if cols is None else cols}), got ({r}, {c})")
     return r, c, ld
+
+
+def _code(dtype, name) -> int:
+    """enum sgemm_type of an output's type (None: bfloat16)."""
+    t = 1 if dtype is None else fp8._TYPES.get(dtype)
+    if t is None:
+        raise TypeError(f"{name} must be float32 or bfloat16, got {dtype}")
+    return t
 
 
 def _act(activation) -> int:
@@ -129,17 +137,17 @@ def linear_bf16(x, weight, bias=None, activation=None, residual=None, *, save=No
     if residual is not None:
         ldr = _matrix(residual, "residual", tokens, outputs)[2]
         r_ptr = residual.data_ptr()
-    handle = _on(stream, x.get_device(), weight, bias, residual, out)
-    if out is None:
-        y, ldy = _alloc(tokens, outputs, out_dtype or _bf16, x, stream)
-    else:
-        y = out
-        if out_dtype is not None and y.dtype is not out_dtype:
-            raise TypeError(f"out is {y.dtype}, not {out_dtype}")
-        rows, cols, ldy = _rows(y, "out")
+    if out is not None:
+        rows, cols, ldy = _rows(out, "out")
         if rows != tokens or cols != outputs:
             raise ValueError("out has the wrong shape")
-    t = _type(y, "out")
+        if out_dtype is not None and out.dtype is not out_dtype:
+            raise TypeError(f"out is {out.dtype}, not {out_dtype}")
+    t = _code(out_dtype if out is None else out.dtype, "out")
+    handle = _on(stream, x.get_device(), weight, bias, residual, out)
+    y = out
+    if y is None:
+        y, ldy = _alloc(tokens, outputs, out_dtype or _bf16, x, stream)
     pre, kept = _keep(save, tokens, outputs, x, stream)
     st = lib.sgemm_linear(tokens, inputs, outputs, x.data_ptr(), ldx, weight.data_ptr(), ldw, None if bias is None else bias.data_ptr(), act,
                           r_ptr, ldr, kept, y.data_ptr(), ldy, t, handle)
@@ -172,10 +180,10 @@ def linear_bf16_backward(dy, x, weight, pre=None, activation=None, *, dx=True, d
         if pre is None:
             raise ValueError("an activation's gradient needs pre")
         ks, kt = _kept(pre, "pre", tokens, outputs)
+    t = _code(dweight_dtype, "dweight")
     handle = _on(stream, dy.get_device(), w, xt, kt)
     gx, lddx = _alloc(tokens, inputs, _bf16, dy, stream) if dx else (None, 1)
     gw, lddw = _alloc(outputs, inputs, dweight_dtype or _bf16, dy, stream) if dweight else (None, 1)
-    t = _type(gw, "dweight") if dweight else 1
     gb = _empty((outputs,), _f32, dy, stream) if dbias else None
     st = lib.sgemm_linear_backward(tokens, inputs, outputs, dy.data_ptr(), lddy, xs, w_ptr, ldw, act, ks, gx.data_ptr() if dx else None, lddx,
                                    gw.data_ptr() if dweight else None, lddw, t, gb.data_ptr() if dbias else None, handle)
@@ -195,11 +203,12 @@ def gated_bf16(x, gate, up, activation="silu", *, save=None, out=None, stream=No
     ldu = _matrix(up, "up", outputs, inputs)[2]
     act = _act(activation)
     _check_keep(save)
+    if out is not None:
+        ldh = _matrix(out, "out", tokens, outputs)[2]
     handle = _on(stream, x.get_device(), gate, up, out)
-    if out is None:
+    h = out
+    if h is None:
         h, ldh = _alloc(tokens, outputs, _bf16, x, stream)
-    else:
-        h, ldh = out, _matrix(out, "out", tokens, outputs)[2]
     (a, ka), (b, kb) = _keep(save, tokens, outputs, x, stream), _keep(save, tokens, outputs, x, stream)
     st = lib.sgemm_gated(tokens, inputs, outputs, x.data_ptr(), ldx, gate.data_ptr(), ldg, up.data_ptr(), ldu, act, ka, kb, h.data_ptr(), ldh,
                          handle)
@@ -230,10 +239,10 @@ def gated_bf16_backward(dh, x, gate, up, gate_pre, up_pre, activation="silu", *,
     (ka, ta), (kb, tb) = _kept(gate_pre, "gate_pre", tokens, outputs), _kept(up_pre, "up_pre", tokens, outputs)
     if isinstance(gate_pre, Fp8Matrix) != isinstance(up_pre, Fp8Matrix):
         raise TypeError("gate_pre and up_pre must be kept alike")
+    t = _code(dweight_dtype, "dgate and dup")
     handle = _on(stream, dh.get_device(), *w, xt, ta, tb)
     gx, lddx = _alloc(tokens, inputs, _bf16, dh, stream) if dx else (None, 1)
     (dg, lddg), (du, lddu) = (_alloc(outputs, inputs, dweight_dtype or _bf16, dh, stream) if dweights else (None, 1) for _ in range(2))
-    t = _type(dg, "dgate") if dweights else 1
     ho, ldh = _alloc(tokens, outputs, _bf16, dh, stream) if h else (None, 1)
     ptr = [None if v is None else v.data_ptr() for v in (gx, dg, du, ho)]
     st = lib.sgemm_gated_backward(tokens, inputs, outputs, dh.data_ptr(), lddh, xs, g_ptr, ldg, u_ptr, ldu, act, ka, kb, ptr[0], lddx, ptr[1], lddg,
