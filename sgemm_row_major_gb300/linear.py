@@ -54,13 +54,19 @@ def _lib():
 
 
 def _matrix(x, name, rows=None, cols=None):
-    """(rows, columns, row stride) of a bfloat16 matrix of the given shape."""
+    """(rows, columns, row stride) of a bfloat16 matrix of the given shape with contiguous rows."""
+    shape = x.shape
     if x.dtype is not _bf16:
         raise TypeError(f"{name} must be bfloat16, got {x.dtype}")
-    r, c, ld = _rows(x, name)
+    if len(shape) != 2:
+        raise TypeError(f"{name} must have 2 dimensions")
+    r, c = shape
+    ld, inner = x.stride()
+    if inner != 1 and c > 1:
+        raise TypeError(f"{name}: the last dimension must be contiguous")
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{name} must have shape ({'any' if rows is None else rows}, {'any' if cols is None else cols}), got ({r}, {c})")
-    return r, c, ld
+    return r, c, ld if r > 1 and c else c or 1
 
 
 def _code(dtype, name) -> int:
@@ -79,21 +85,20 @@ def _act(activation) -> int:
 
 
 def _kept(k, name, rows, cols):
-    """(structure, a tensor of it) of a matrix that was kept: bfloat16, or an Fp8Matrix of E4M3 codes in groups of (1, 128)."""
-    if isinstance(k, Fp8Matrix):
+    """(structure, device number) of a matrix that was kept: bfloat16, or an Fp8Matrix of E4M3 codes in groups of (1, 128)."""
+    if type(k) is Fp8Matrix:
         c = k._c()
-        if tuple(k._shape) != (rows, cols):
+        if k._shape != (rows, cols):
             raise ValueError(f"{name} must have shape ({rows}, {cols}), got {tuple(k._shape)}")
         if k._block != ROW or c.format != 0:
             raise ValueError(f"{name} must have E4M3 codes and groups of (1, 128)")
         return KeptStruct(c.data, c.ld, c.scale, c.lds), k._device
-    ld = _matrix(k, name, rows, cols)[2]
-    return KeptStruct(k.data_ptr(), ld, None, 1), k
+    return KeptStruct(k.data_ptr(), _matrix(k, name, rows, cols)[2], None, 1), k.get_device()
 
 
 def _alloc(rows, cols, dtype, like, stream):
     """(tensor, row stride): uninitialised, its rows at multiples of 8 elements, as the kernels write them fastest."""
-    ld = (cols + 7) // 8 * 8
+    ld = (cols + 7) & ~7
     return _empty((rows, cols), dtype, like, stream, None if ld == cols else ld), ld or 1
 
 
@@ -237,7 +242,7 @@ def gated_bf16_backward(dh, x, gate, up, gate_pre, up_pre, activation="silu", *,
             inputs = x.shape[1]
         xs, xt = _kept(x, "x", tokens, inputs)
     (ka, ta), (kb, tb) = _kept(gate_pre, "gate_pre", tokens, outputs), _kept(up_pre, "up_pre", tokens, outputs)
-    if isinstance(gate_pre, Fp8Matrix) != isinstance(up_pre, Fp8Matrix):
+    if (type(gate_pre) is Fp8Matrix) != (type(up_pre) is Fp8Matrix):
         raise TypeError("gate_pre and up_pre must be kept alike")
     t = _code(dweight_dtype, "dgate and dup")
     handle = _on(stream, dh.get_device(), *w, xt, ta, tb)
