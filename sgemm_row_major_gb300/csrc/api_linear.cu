@@ -16,7 +16,9 @@ namespace {
 constexpr int64_t kMaxDim = INT_MAX - 1024;  // indices of the kernels' last tiles stay below 2^31
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
-int64_t round8(int64_t n) { return ceil_div(n, 8) * 8; }
+// The row stride of copies and of what lies in the workspace: whole lines of 128 bytes (rows of 4112 bytes, which the tensor
+// cores' copies can read too, cost a fifth more per K tile, as each 128 bytes of them lie in two lines).
+int64_t whole_lines(int64_t n) { return ceil_div(n, 64) * 64; }
 bool aligned(const void* p, size_t n) { return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0; }
 int type_size(int type) { return type == SGEMM_BF16 ? 2 : 4; }
 bool known_type(int type) { return type == SGEMM_F32 || type == SGEMM_BF16; }
@@ -188,10 +190,10 @@ struct Operand {
     copied = scale || !aligned(p, 16) || (ld % 8 != 0 && rows > 1);
   }
   void place(Pieces* w) {
-    if (copied) copy = w->take<uint16_t>(rows * round8(cols));
+    if (copied) copy = w->take<uint16_t>(rows * whole_lines(cols));
   }
   cudaError_t map(int box_rows, CUtensorMap* out) const {
-    const int64_t ld = copied || rows == 1 ? round8(cols) : m.ld;  // (a map wants a stride even where it steps over nothing)
+    const int64_t ld = copied || rows == 1 ? whole_lines(cols) : m.ld;  // (a map wants a stride even where it steps over nothing)
     return encode_linear_map(copied ? copy : m.data, cols, rows, ld, box_rows, out);
   }
 };
@@ -208,7 +210,7 @@ cudaError_t make_copies(std::initializer_list<const Operand*> list, const Guard&
     e.rows = o->rows;
     e.cols = (int)o->cols;
     e.dst = o->copy;
-    e.ldd = round8(o->cols);
+    e.ldd = whole_lines(o->cols);
   }
   return n ? launch_linear_expand(p, stream) : cudaSuccess;
 }
@@ -230,9 +232,10 @@ struct Product {
 };
 
 // K tiles of 64 that the pair kernel sums in one accumulator where FP32 values leave it (an FP32 output, scales): sums of 8 are
-// about as exact as FP32 sums (kernel_linear_pair.cu); the first 16 together leave the epilogue of the tile before more time
-// (4.2 us) before the folding starts again.
-constexpr int kFoldFirst = 16, kFold = 8, kFoldNone = 1 << 30;
+// about as exact as FP32 sums (kernel_linear_pair.cu).  The more the first takes, the more time the epilogue of the tile before
+// has before the folding starts again: 16 are 4.7 us, about an FP32 output's; the epilogue that keeps 8-bit values takes up to 8 and
+// gets 24 where they are at most half of a sum (8192 x 4096 x 16384 with GELU's tanh form 647 -> 612 us).
+constexpr int kFoldFirst = 16, kFoldFirstKept8 = 24, kFold = 8, kFoldNone = 1 << 30;
 
 // One launch of the products: of one with a choice of either kernel, of several with the pair kernel.
 struct Launch {
@@ -359,7 +362,10 @@ struct Launch {
   }
 
  private:
-  int fold_first(const Product& r) const { return r.f32 || out.keep == 2 ? kFoldFirst : kFoldNone; }
+  int fold_first(const Product& r) const {
+    if (out.keep == 2 && !r.f32 && r.shape.k_tiles() >= 2 * kFoldFirstKept8) return kFoldFirstKept8;
+    return r.f32 || out.keep == 2 ? kFoldFirst : kFoldNone;
+  }
   static bool tma_writes(const void* p, int64_t ld, int64_t cols, int size) { return rows_at(p, ld, size, 16) && cols * size >= 16; }
 };
 
@@ -460,7 +466,7 @@ int forward(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, int6
           *e = cudaMemsetAsync(zeros, 0, (size_t)std::max(tokens, outputs) * 16, stream);
         }
         if (*e == cudaSuccess) *e = make_copies({&x, &w0, gated ? &w1 : nullptr, &r}, g, stream);
-        if (r.copied) out.residual = r.copy, out.ldr = round8(outputs);
+        if (r.copied) out.residual = r.copy, out.ldr = whole_lines(outputs);
         return *e == cudaSuccess ? launch.launch(launch.pr, 1, choice, dev, stream, e) : SGEMM_OK;
       });
 }
@@ -621,7 +627,7 @@ int sgemm_linear_backward(int64_t tokens, int64_t inputs, int64_t outputs, const
   const bool write = products && (act || d.copied);
   Operand w(W, ldw, nullptr, 0, outputs, inputs);
   Operand x(X ? X->data : nullptr, X ? X->ld : 1, X ? X->scale : nullptr, X ? X->lds : 1, tokens, inputs);
-  const int64_t ldd = round8(outputs);
+  const int64_t ldd = whole_lines(outputs);
   return with_workspace(
       dev, stream,
       [&](Pieces* p) {
@@ -702,7 +708,7 @@ int sgemm_gated_backward(int64_t tokens, int64_t inputs, int64_t outputs, const 
   g.vec = rows_at(dH, lddh, 2, 16) && g.a.vec && g.b.vec && (!H || rows_at(H, ldh, 2, 16));
   Operand wg(gate, ldg, nullptr, 0, outputs, inputs), wu(up, ldu, nullptr, 0, outputs, inputs);
   Operand x(X ? X->data : nullptr, X ? X->ld : 1, X ? X->scale : nullptr, X ? X->lds : 1, tokens, inputs);
-  const int64_t ldd = round8(outputs);
+  const int64_t ldd = whole_lines(outputs);
   return with_workspace(
       dev, stream,
       [&](Pieces* p) {
