@@ -104,8 +104,6 @@ def _alloc(rows, cols, dtype, like, stream):
 
 def _keep(how, rows, cols, like, stream):
     """(what a forward pass returns, its structure) for values that are kept."""
-    if how is None:
-        return None, None
     if how == "fp8":
         m = _new_matrix(rows, cols, ROW, 0, like, stream)
         c = m._struct
@@ -153,7 +151,9 @@ def linear_bf16(x, weight, bias=None, activation=None, residual=None, *, save=No
     y = out
     if y is None:
         y, ldy = _alloc(tokens, outputs, out_dtype or _bf16, x, stream)
-    pre, kept = _keep(save, tokens, outputs, x, stream)
+    pre = kept = None
+    if save is not None:
+        pre, kept = _keep(save, tokens, outputs, x, stream)
     st = lib.sgemm_linear(tokens, inputs, outputs, x.data_ptr(), ldx, weight.data_ptr(), ldw, None if bias is None else bias.data_ptr(), act,
                           r_ptr, ldr, kept, y.data_ptr(), ldy, t, handle)
     if st != 0:
@@ -172,26 +172,34 @@ def linear_bf16_backward(dy, x, weight, pre=None, activation=None, *, dx=True, d
     lib = _lib()
     tokens, outputs, lddy = _matrix(dy, "dy")
     act = _act(activation)
-    inputs, w_ptr, ldw, xs, xt, w = 0, None, 1, None, None, None
+    inputs, w_ptr, ldw, xs, x_dev, ks, k_dev = 0, None, 1, None, None, None, None
     if dx:
-        inputs, ldw = _matrix(weight, "weight", outputs)[1:]
-        w, w_ptr = weight, weight.data_ptr()
+        _, inputs, ldw = _matrix(weight, "weight", outputs)
+        w_ptr = weight.data_ptr()
+    else:
+        weight = None
     if dweight:
         if not dx:
             inputs = x.shape[1]
-        xs, xt = _kept(x, "x", tokens, inputs)
-    ks, kt = None, None
+        xs, x_dev = _kept(x, "x", tokens, inputs)
     if act:
         if pre is None:
             raise ValueError("an activation's gradient needs pre")
-        ks, kt = _kept(pre, "pre", tokens, outputs)
+        ks, k_dev = _kept(pre, "pre", tokens, outputs)
     t = _code(dweight_dtype, "dweight")
-    handle = _on(stream, dy.get_device(), w, xt, kt)
-    gx, lddx = _alloc(tokens, inputs, _bf16, dy, stream) if dx else (None, 1)
-    gw, lddw = _alloc(outputs, inputs, dweight_dtype or _bf16, dy, stream) if dweight else (None, 1)
-    gb = _empty((outputs,), _f32, dy, stream) if dbias else None
-    st = lib.sgemm_linear_backward(tokens, inputs, outputs, dy.data_ptr(), lddy, xs, w_ptr, ldw, act, ks, gx.data_ptr() if dx else None, lddx,
-                                   gw.data_ptr() if dweight else None, lddw, t, gb.data_ptr() if dbias else None, handle)
+    handle = _on(stream, dy.get_device(), weight, x_dev, k_dev)
+    gx = gw = gb = gx_ptr = gw_ptr = gb_ptr = None
+    lddx = lddw = 1
+    if dx:
+        gx, lddx = _alloc(tokens, inputs, _bf16, dy, stream)
+        gx_ptr = gx.data_ptr()
+    if dweight:
+        gw, lddw = _alloc(outputs, inputs, dweight_dtype or _bf16, dy, stream)
+        gw_ptr = gw.data_ptr()
+    if dbias:
+        gb = _empty((outputs,), _f32, dy, stream)
+        gb_ptr = gb.data_ptr()
+    st = lib.sgemm_linear_backward(tokens, inputs, outputs, dy.data_ptr(), lddy, xs, w_ptr, ldw, act, ks, gx_ptr, lddx, gw_ptr, lddw, t, gb_ptr, handle)
     if st != 0:
         raise SgemmError(st, "sgemm_linear_backward")
     return LinearGradients(gx, gw, gb)
@@ -214,7 +222,10 @@ def gated_bf16(x, gate, up, activation="silu", *, save=None, out=None, stream=No
     h = out
     if h is None:
         h, ldh = _alloc(tokens, outputs, _bf16, x, stream)
-    (a, ka), (b, kb) = _keep(save, tokens, outputs, x, stream), _keep(save, tokens, outputs, x, stream)
+    a = b = ka = kb = None
+    if save is not None:
+        a, ka = _keep(save, tokens, outputs, x, stream)
+        b, kb = _keep(save, tokens, outputs, x, stream)
     st = lib.sgemm_gated(tokens, inputs, outputs, x.data_ptr(), ldx, gate.data_ptr(), ldg, up.data_ptr(), ldu, act, ka, kb, h.data_ptr(), ldh,
                          handle)
     if st != 0:
@@ -232,26 +243,38 @@ def gated_bf16_backward(dh, x, gate, up, gate_pre, up_pre, activation="silu", *,
     lib = _lib()
     tokens, outputs, lddh = _matrix(dh, "dh")
     act = _act(activation)
-    inputs, ldg, ldu, g_ptr, u_ptr, xs, xt, w = 0, 1, 1, None, None, None, None, (None, None)
+    inputs, ldg, ldu, g_ptr, u_ptr, xs, x_dev = 0, 1, 1, None, None, None, None
     if dx:
-        inputs, ldg = _matrix(gate, "gate", outputs)[1:]
-        ldu = _matrix(up, "up", outputs, inputs)[2]
-        w, g_ptr, u_ptr = (gate, up), gate.data_ptr(), up.data_ptr()
+        _, inputs, ldg = _matrix(gate, "gate", outputs)
+        _, _, ldu = _matrix(up, "up", outputs, inputs)
+        g_ptr, u_ptr = gate.data_ptr(), up.data_ptr()
+    else:
+        gate = up = None
     if dweights:
         if not dx:
             inputs = x.shape[1]
-        xs, xt = _kept(x, "x", tokens, inputs)
-    (ka, ta), (kb, tb) = _kept(gate_pre, "gate_pre", tokens, outputs), _kept(up_pre, "up_pre", tokens, outputs)
+        xs, x_dev = _kept(x, "x", tokens, inputs)
+    ka, a_dev = _kept(gate_pre, "gate_pre", tokens, outputs)
+    kb, b_dev = _kept(up_pre, "up_pre", tokens, outputs)
     if (type(gate_pre) is Fp8Matrix) != (type(up_pre) is Fp8Matrix):
         raise TypeError("gate_pre and up_pre must be kept alike")
     t = _code(dweight_dtype, "dgate and dup")
-    handle = _on(stream, dh.get_device(), *w, xt, ta, tb)
-    gx, lddx = _alloc(tokens, inputs, _bf16, dh, stream) if dx else (None, 1)
-    (dg, lddg), (du, lddu) = (_alloc(outputs, inputs, dweight_dtype or _bf16, dh, stream) if dweights else (None, 1) for _ in range(2))
-    ho, ldh = _alloc(tokens, outputs, _bf16, dh, stream) if h else (None, 1)
-    ptr = [None if v is None else v.data_ptr() for v in (gx, dg, du, ho)]
-    st = lib.sgemm_gated_backward(tokens, inputs, outputs, dh.data_ptr(), lddh, xs, g_ptr, ldg, u_ptr, ldu, act, ka, kb, ptr[0], lddx, ptr[1], lddg,
-                                  ptr[2], lddu, t, ptr[3], ldh, handle)
+    handle = _on(stream, dh.get_device(), gate, up, x_dev, a_dev, b_dev)
+    gx = dg = du = ho = gx_ptr = dg_ptr = du_ptr = ho_ptr = None
+    lddx = ldw = ldh = 1
+    if dx:
+        gx, lddx = _alloc(tokens, inputs, _bf16, dh, stream)
+        gx_ptr = gx.data_ptr()
+    if dweights:
+        dtype = dweight_dtype or _bf16
+        dg, ldw = _alloc(outputs, inputs, dtype, dh, stream)
+        du, _ = _alloc(outputs, inputs, dtype, dh, stream)
+        dg_ptr, du_ptr = dg.data_ptr(), du.data_ptr()
+    if h:
+        ho, ldh = _alloc(tokens, outputs, _bf16, dh, stream)
+        ho_ptr = ho.data_ptr()
+    st = lib.sgemm_gated_backward(tokens, inputs, outputs, dh.data_ptr(), lddh, xs, g_ptr, ldg, u_ptr, ldu, act, ka, kb, gx_ptr, lddx, dg_ptr, ldw,
+                                  du_ptr, ldw, t, ho_ptr, ldh, handle)
     if st != 0:
         raise SgemmError(st, "sgemm_gated_backward")
     return GatedGradients(gx, dg, du, ho)
