@@ -299,7 +299,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   int tiles = 0;
   for (int n = 0; n < p.jobs; ++n) tiles += p.job[n].tiles_m * p.job[n].tiles_n;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
       mbar_init(smem_addr(&full[s]), 1);
@@ -321,6 +320,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   cluster_sync();
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_slot;
+  // (not before this CTA has its tensor memory: a dependent that took it first would wait for this grid, and this grid for it)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // launched as a programmatic dependent: what the stream's kernel before this one wrote is read, and what it read is
   // written, only from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -105,7 +105,6 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
   const int g0 = (int)((int64_t)kt * rank / p.split), g1 = (int)((int64_t)kt * (rank + 1) / p.split);
   const int units = g1 - g0;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (threadIdx.x == 0) {
     prefetch_tensormap(&maps.op[j.a[0]]);
     prefetch_tensormap(&maps.op[j.b[0]]);
@@ -125,6 +124,10 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
   __syncthreads();
   tmem_fence_after_sync();
   const uint32_t tmem = tmem_slot;
+  // Not before this CTA has its tensor memory: a dependent that took it first would wait for this grid, and this grid for it.
+  // (As a dependent itself it takes at most 256 columns: no kernel of the library that needs more than the others leaves its
+  // shared memory.)
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   // launched as a programmatic dependent: what the stream's kernel before this one wrote is read, and what it read is
   // written, only from here on
   asm volatile("griddepcontrol.wait;" ::: "memory");
