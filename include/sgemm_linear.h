@@ -42,7 +42,8 @@ enum sgemm_activation {
 
 /* Kernel variants of this part (sgemm_plan_t.variant). */
 enum sgemm_linear_variant {
-    SGEMM_VARIANT_LINEAR_PAIR = 40,  /* CTA pairs, 256 x tile_n tiles (tile_n 64, 128 or 256), 64 k per tile */
+    SGEMM_VARIANT_LINEAR_PAIR = 40,  /* CTA pairs, 256 x tile_n tiles (tile_n 64, 128 or 256), 64 k per tile; with split_k > 1
+                                        the K tiles of a tile are shared and a second kernel adds the sums */
     SGEMM_VARIANT_LINEAR_SHORT = 41  /* one CTA per tile_n x 128 tile (tile_n 16, 32, 64 or 128 rows, 128 columns), K
                                         shared by a cluster of split_k CTAs */
 };
@@ -136,9 +137,11 @@ int sgemm_linear_plan(int64_t rows, int64_t cols, int64_t K, int gated, int kept
 /*
  * Process-wide override of this part's choice of kernel, for tests and
  * benchmarks: variant = SGEMM_VARIANT_AUTO (0) restores it.  tile_n = 0 and
- * split = 0 keep the planner's own; a forced split (SHORT: 1, 2, 4 or 8) may
- * give a CTA no work at all, and a tile that a call cannot use (64 columns where a gated pair or 8-bit values want more,
- * 128 rows of a gated short one) is left to the planner.  -1, -2, -3: an argument that names no kernel, tile or split.
+ * split = 0 keep the planner's own; a forced split (SHORT: 1, 2, 4 or 8; PAIR: 1
+ * to 32, where the call can share K) may give a CTA of the short-side kernel no
+ * work at all.  A tile that a call cannot use (64 columns where a gated pair or
+ * 8-bit values want more, 128 rows of a gated short one) is left to the
+ * planner.  -1, -2, -3: an argument that names no kernel, tile or split.
  */
 int sgemm_linear_set_override(int variant, int tile_n, int split);
 

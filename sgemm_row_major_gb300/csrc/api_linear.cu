@@ -65,6 +65,8 @@ struct ShortCost {
 constexpr ShortCost kShortCost[] = {{16, 267, 2730, 570}, {32, 298, 3580, 85}, {64, 328, 4530, 5}, {128, 154, 6330, 0}};
 constexpr double kPairLaunchNs = 3000, kShortLaunchNs = 790;
 constexpr double kPairBytesPerNs = 3490;
+constexpr int kLeastShare = 8;  // K tiles of a unit that shares a tile
+constexpr double kJoinNs = 4000, kJoinBytesPerNs = 4000;
 constexpr double kSharedSm = 0.34;       // a K tile takes this much longer with a second CTA on the SM
 constexpr double kGatedK = 1.19, kGatedTile = 1.36;  // a gated tile's K tiles and rest against a plain one's
 constexpr double kSmBytesPerNs = 89.0;   // an SM's largest share of the memory bandwidth
@@ -83,30 +85,69 @@ bool pair_tile_fits(int tile, const Shape& s) {
 }
 
 struct Choice {
-  int variant = 0, tile = 0, split = 1;
+  int variant = 0, tile = 0, split = 1;            // split: of the short-side kernel
+  int splits[kLinearJobs] = {1, 1, 1};             // of each product in the pair kernel
   double ns = 1e30;
 };
 
-// The pair kernel's time for up to three products in one launch: that of the cluster with the most work (tiles are dealt round
-// robin; a cluster has one more of a product's tiles where the deal of its last round starts, so one of these has the most).
-double pair_ns(const Shape* s, int n, const PairCost& c, int64_t clusters) {
-  double most = 0.0, bytes = 0.0;
-  for (int i = 0; i < n; ++i)
+// The pair kernel's time for up to three products in one launch, the K tiles of each tile of product i shared by splits[i] units:
+// that of the cluster with the most work (units are dealt round robin; a cluster has one more of a product's where the deal of
+// its last round starts, so one of these has the most), and of joining the shares.
+double pair_ns(const Shape* s, int n, const PairCost& c, int64_t clusters, const int* splits) {
+  double most = 0.0, bytes = 0.0, joined = 0.0;
+  int64_t units[kLinearJobs];
+  for (int i = 0; i < n; ++i) {
+    units[i] = s[i].pair_tiles(c.tile) * splits[i];
     bytes += 2.0 * ((double)s[i].M * s[i].K * s[i].segments + (double)s[i].N * s[i].K * s[i].segments * (s[i].gated ? 2 : 1) + (double)s[i].M * s[i].N);
+    if (splits[i] > 1) joined += 4.0 * s[i].M * s[i].N * (2 * splits[i] + 1);
+  }
   int64_t start = 0;
-  for (int i = 0; i < n; start += s[i++].pair_tiles(c.tile)) {
-    const int64_t at = (start + s[i].pair_tiles(c.tile) / clusters * clusters) % clusters;
+  for (int i = 0; i < n; start += units[i++]) {
+    const int64_t at = (start + units[i] / clusters * clusters) % clusters;
     double ns = 0.0;
     int64_t first = 0;
-    for (int k = 0; k < n; first += s[k++].pair_tiles(c.tile)) {
-      // tiles of product k that cluster `at` gets: those in [first, first + tiles) that are `at` modulo the clusters
-      const int64_t skip = ((at - first) % clusters + clusters) % clusters, tiles = s[k].pair_tiles(c.tile);
-      const int64_t mine = tiles > skip ? (tiles - skip - 1) / clusters + 1 : 0;
-      ns += (double)mine * (s[k].k_tiles() * c.k_ns + c.tile_ns);
+    for (int k = 0; k < n; first += units[k++]) {
+      // units of product k that cluster `at` gets: those in [first, first + units) that are `at` modulo the clusters
+      const int64_t skip = ((at - first) % clusters + clusters) % clusters;
+      const int64_t mine = units[k] > skip ? (units[k] - skip - 1) / clusters + 1 : 0;
+      ns += (double)mine * (ceil_div(s[k].k_tiles(), splits[k]) * c.k_ns + c.tile_ns);
     }
     most = std::max(most, ns);
   }
-  return kPairLaunchNs + std::max(most, bytes / kPairBytesPerNs);
+  return kPairLaunchNs + std::max(most, bytes / kPairBytesPerNs) + (joined > 0.0 ? kJoinNs + joined / kJoinBytesPerNs : 0.0);
+}
+
+// The pair kernel's launch with K shared where that is worth it: units of about equal length, as many as clusters or twice that.
+void offer_pair(const Shape* s, int n, const PairCost& c, int64_t clusters, int forced, Choice* best) {
+  const auto offer = [&](const int* splits) {
+    const double ns = pair_ns(s, n, c, clusters, splits);
+    if (ns >= best->ns) return;
+    *best = Choice{SGEMM_VARIANT_LINEAR_PAIR, c.tile, 1, {1, 1, 1}, ns};
+    std::copy(splits, splits + n, best->splits);
+  };
+  int splits[kLinearJobs] = {1, 1, 1};
+  int64_t tiles = 0, steps = 0, longest = 0;
+  for (int i = 0; i < n; ++i) {
+    tiles += s[i].pair_tiles(c.tile);
+    steps += s[i].pair_tiles(c.tile) * s[i].k_tiles();
+    longest = std::max(longest, s[i].k_tiles());
+  }
+  const bool can = !s[0].gated && !s[0].kept8;  // (the joining kernel has no second product and no groups)
+  if (forced > 0 && can) {
+    for (int i = 0; i < n; ++i) splits[i] = (int)std::min<int64_t>(forced, s[i].k_tiles());
+    return offer(splits);
+  }
+  offer(splits);
+  if (!can || forced > 0 || tiles >= 2 * clusters || longest < 2 * kLeastShare) return;
+  for (int rounds = 1; rounds <= 2; ++rounds) {
+    const double length = std::max((double)kLeastShare, (double)steps / (double)(rounds * clusters));
+    bool any = false;
+    for (int i = 0; i < n; ++i) {
+      splits[i] = (int)std::max<int64_t>(1, std::min<int64_t>(kLinearMostShares, (int64_t)((double)s[i].k_tiles() / length + 0.25)));
+      any |= splits[i] > 1;
+    }
+    if (any) offer(splits);
+  }
 }
 
 // The cheapest launch of one product (several: in one launch of the pair kernel), among the variant, tile and split that are
@@ -114,7 +155,7 @@ double pair_ns(const Shape* s, int n, const PairCost& c, int64_t clusters) {
 Choice choose(const Shape* s, int n, int64_t clusters, int sm_count, int variant, int tile, int split) {
   Choice best;
   const auto offer = [&](int v, int t, int k, double ns) {
-    if (ns < best.ns) best = Choice{v, t, k, ns};
+    if (ns < best.ns) best = Choice{v, t, k, {1, 1, 1}, ns};
   };
   const auto forced_here = [&](const auto& tiles, const auto& fits) {
     return std::any_of(std::begin(tiles), std::end(tiles), [&](int t) { return t == tile && fits(t); });
@@ -122,7 +163,7 @@ Choice choose(const Shape* s, int n, int64_t clusters, int sm_count, int variant
   if (variant != SGEMM_VARIANT_LINEAR_SHORT && clusters > 0) {
     const bool only = forced_here(kLinearPairTiles, [&](int t) { return pair_tile_fits(t, s[0]); });
     for (const PairCost& c : kPairCost)
-      if (pair_tile_fits(c.tile, s[0]) && (!only || c.tile == tile)) offer(SGEMM_VARIANT_LINEAR_PAIR, c.tile, 1, pair_ns(s, n, c, clusters));
+      if (pair_tile_fits(c.tile, s[0]) && (!only || c.tile == tile)) offer_pair(s, n, c, clusters, variant == SGEMM_VARIANT_LINEAR_PAIR ? split : 0, &best);
   }
   if (variant != SGEMM_VARIANT_LINEAR_PAIR && n == 1) {
     const int64_t kt = s->k_tiles();
@@ -245,34 +286,54 @@ struct Launch {
 
   Product& add() { return pr[n++]; }
 
-  Choice choice(const CallDevice& dev) const {
+  // How it runs: all in one launch of the pair kernel; or the first by itself, where that is cheaper (a product of few rows
+  // beside long ones), and the others in one; or (no clusters) each by itself.
+  struct Group {
+    int first, count;
+    Choice choice;
+  };
+  Group group[kLinearJobs];
+  int groups = 0;
+  float* sums[kLinearJobs] = {nullptr, nullptr, nullptr};  // of products whose K is shared
+
+  void plan(const CallDevice& dev) {
     Shape s[kLinearJobs];
     for (int i = 0; i < n; ++i) s[i] = pr[i].shape;
-    return choose(s, n, dev.sm_count, dev.pair_clusters);
+    const auto of = [&](int first, int count) { return Group{first, count, choose(s + first, count, dev.sm_count, dev.pair_clusters)}; };
+    group[0] = of(0, n);
+    groups = 1;
+    if (n == 1) return;
+    const Group one = of(0, 1), rest = of(1, n - 1);
+    if (rest.choice.variant == 0) {
+      for (groups = 0; groups < n; ++groups) group[groups] = of(groups, 1);
+    } else if (one.choice.ns + rest.choice.ns < group[0].choice.ns) {
+      group[0] = one;
+      group[1] = rest;
+      groups = 2;
+    }
+  }
+  bool by_pairs() const { return n == 1 && group[0].choice.variant == SGEMM_VARIANT_LINEAR_PAIR; }
+  bool shares_k() const { return group[0].choice.splits[0] > 1; }
+
+  static int64_t sums_ld(const Shape& s) { return ceil_div(s.N, 32) * 32; }
+  static int64_t rows_apart(const Shape& s) { return ceil_div(s.M, 256) * 256; }
+  void place(Pieces* w) {
+    for (int g = 0; g < groups; ++g)
+      for (int i = 0; i < group[g].count; ++i) {
+        const int split = group[g].choice.splits[i], at = group[g].first + i;
+        if (split > 1) sums[at] = w->take<float>(split * rows_apart(pr[at].shape) * sums_ld(pr[at].shape));
+      }
   }
 
   int run(const CallDevice& dev, cudaStream_t stream, cudaError_t* e) {
-    const Choice c = choice(dev);
-    if (n > 1) {
-      // each by itself where that is cheaper: a short one among long ones, or no clusters
-      Choice one[kLinearJobs];
-      double ns = 0.0;
-      for (int i = 0; i < n; ++i) {
-        one[i] = choose(&pr[i].shape, 1, dev.sm_count, dev.pair_clusters);
-        ns += one[i].ns;
-      }
-      if (ns < c.ns) {
-        for (int i = 0; i < n && *e == cudaSuccess; ++i) {
-          const int st = launch(&pr[i], 1, one[i], dev, stream, e);
-          if (st != SGEMM_OK) return st;
-        }
-        return SGEMM_OK;
-      }
-    }
-    return launch(pr, n, c, dev, stream, e);
+    int st = SGEMM_OK;
+    for (int g = 0; g < groups && st == SGEMM_OK && *e == cudaSuccess; ++g) st = launch(group[g].first, group[g].count, group[g].choice, dev, stream, e);
+    return st;
   }
 
-  int launch(const Product* list, int count, const Choice& c, const CallDevice& dev, cudaStream_t stream, cudaError_t* e) {
+ private:
+  int launch(int first, int count, const Choice& c, const CallDevice& dev, cudaStream_t stream, cudaError_t* e) {
+    const Product* list = pr + first;
     if (c.variant == 0) return SGEMM_ERR_UNSUPPORTED;  // forced to what needs clusters
     const bool pair = c.variant == SGEMM_VARIANT_LINEAR_PAIR, gated = list[0].shape.gated;
     out.guard = {dev.fault, dev.bounds};
@@ -280,6 +341,8 @@ struct Launch {
     out.r_vec = rows_at(out.residual, out.ldr, 2, 16);
     LinearMaps maps;
     LinearPairParams p;
+    LinearJoinParams join;
+    bool joins = false;
     const Operand* known[6];
     int box[6], maps_used = 0;
     const auto map_of = [&](const Operand* o, int rows) {  // an operand's map, made once
@@ -292,7 +355,7 @@ struct Launch {
     };
     int64_t tiles = 0, steps = 0;
     bool fold = out.keep == 2;
-    for (int i = 0; i < count; ++i) fold |= list[i].f32;
+    for (int i = 0; i < count; ++i) fold |= list[i].f32 || c.splits[i] > 1;
     for (int i = 0; i < count; ++i) {
       const Product& r = list[i];
       LinearJob& j = p.job[i];
@@ -314,7 +377,25 @@ struct Launch {
         j.tiles_m = (int)ceil_div(r.shape.M, 256);
         j.tiles_n = (int)ceil_div(r.shape.N, gated ? c.tile / 2 : c.tile);
         j.idesc = instruction(r.a_mn, r.b_mn, 256, c.tile);
-        if (j.d_tma && *e == cudaSuccess) *e = encode_linear_out_map(r.d, r.shape.N / (16 / size) * (16 / size), r.shape.M, r.ldd, !r.f32, r.f32 ? 32 : linear_pair_box(c.tile, gated, fold), &maps.d[i]);
+        if (c.splits[i] > 1) {  // the units' sums are what the kernel writes
+          LinearJoin& t = join.part[i];
+          t.sums = sums[first + i];
+          t.ld = sums_ld(r.shape);
+          t.split = c.splits[i];
+          t.rows_apart = (int)rows_apart(r.shape);
+          t.job = j;
+          joins = true;
+          if ((int64_t)t.split * t.rows_apart > kMaxDim) return SGEMM_ERR_UNSUPPORTED;
+          j.split = t.split;
+          j.rows_apart = t.rows_apart;
+          j.M = t.split * t.rows_apart;
+          j.N = (int)t.ld;
+          j.d = sums[first + i];
+          j.ldd = t.ld;
+          j.f32 = j.d_tma = 1;
+          j.fold0 = kFoldFirst;
+          if (*e == cudaSuccess) *e = encode_linear_out_map(j.d, t.ld, j.M, t.ld, false, 32, &maps.d[i]);
+        } else if (j.d_tma && *e == cudaSuccess) *e = encode_linear_out_map(r.d, r.shape.N / (16 / size) * (16 / size), r.shape.M, r.ldd, !r.f32, r.f32 ? 32 : linear_pair_box(c.tile, gated, fold), &maps.d[i]);
       } else {
         j.tiles_m = (int)ceil_div(r.shape.M, c.tile);
         j.tiles_n = (int)ceil_div(r.shape.N, 128);
@@ -324,7 +405,7 @@ struct Launch {
         if (r.a[k]) j.a[k] = map_of(r.a[k], r.a_mn || pair ? 64 : std::min(64, c.tile));
         if (r.b[k]) j.b[k] = map_of(r.b[k], r.b_mn || !pair ? 64 : std::min(64, c.tile / 2));
       }
-      tiles += (int64_t)j.tiles_m * j.tiles_n;
+      tiles += (int64_t)j.tiles_m * j.tiles_n * j.split;
       steps += (int64_t)j.tiles_m * j.tiles_n * r.shape.k_tiles();
     }
     for (int i = 0; i < 2; ++i) {
@@ -340,11 +421,19 @@ struct Launch {
       const int64_t clusters = std::min<int64_t>(tiles, dev.pair_clusters);
       if (tiles > INT_MAX || steps / clusters > INT_MAX / 2) return SGEMM_ERR_UNSUPPORTED;
       p.out = out;
+      if (joins && count == 1) {  // the epilogue is the joining kernel's
+        p.out.bias = p.out.residual = nullptr;
+        p.out.act = p.out.keep = 0;
+      }
       p.jobs = count;
       p.clusters = (int)clusters;
       p.timeout_ns = wait_timeout_ns();
       p.fault = dev.fault;
       *e = launch_linear_pair(c.tile, gated, fold, maps, p, stream);
+      if (joins && *e == cudaSuccess) {
+        join.out = out;
+        *e = launch_linear_join(join, stream);
+      }
       return SGEMM_OK;
     }
     LinearShortParams q;
@@ -361,7 +450,6 @@ struct Launch {
     return SGEMM_OK;
   }
 
- private:
   int fold_first(const Product& r) const {
     if (out.keep == 2 && !r.f32 && r.shape.k_tiles() >= 2 * kFoldFirstKept8) return kFoldFirstKept8;
     return r.f32 || out.keep == 2 ? kFoldFirst : kFoldNone;
@@ -446,10 +534,10 @@ int forward(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, int6
   if (gated) pr.b[1] = &w1;
   // the pair kernel's lanes read a row of the residual each, 16 bytes at a time; rows that lie anywhere are copied first
   // (reading them along the rows in its epilogue took longer than the copy and the epilogue together)
-  const Choice choice = launch.choice(dev);
+  launch.plan(dev);
   LinearOut& out = launch.out;
   Operand r(out.residual, out.ldr, nullptr, 0, tokens, outputs);
-  r.copied = out.residual && choice.variant == SGEMM_VARIANT_LINEAR_PAIR && !rows_at(out.residual, out.ldr, 2, 16);
+  r.copied = out.residual && launch.by_pairs() && !launch.shares_k() && !rows_at(out.residual, out.ldr, 2, 16);
   return with_workspace(
       dev, stream,
       [&](Pieces* w) {
@@ -458,6 +546,7 @@ int forward(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, int6
         w0.place(w);
         if (gated) w1.place(w);
         r.place(w);
+        launch.place(w);
       },
       [&](cudaError_t* e) {
         const Guard g{dev.fault, dev.bounds};
@@ -467,7 +556,7 @@ int forward(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, int6
         }
         if (*e == cudaSuccess) *e = make_copies({&x, &w0, gated ? &w1 : nullptr, &r}, g, stream);
         if (r.copied) out.residual = r.copy, out.ldr = whole_lines(outputs);
-        return *e == cudaSuccess ? launch.launch(launch.pr, 1, choice, dev, stream, e) : SGEMM_OK;
+        return *e == cudaSuccess ? launch.run(dev, stream, e) : SGEMM_OK;
       });
 }
 
@@ -628,6 +717,10 @@ int sgemm_linear_backward(int64_t tokens, int64_t inputs, int64_t outputs, const
   Operand w(W, ldw, nullptr, 0, outputs, inputs);
   Operand x(X ? X->data : nullptr, X ? X->ld : 1, X ? X->scale : nullptr, X ? X->lds : 1, tokens, inputs);
   const int64_t ldd = whole_lines(outputs);
+  Launch launch;
+  if (dX) launch.add() = input_gradient(tokens, inputs, outputs, &d, nullptr, &w, nullptr, dX, lddx);
+  if (dW) launch.add() = weight_gradient(tokens, inputs, outputs, &d, &x, dW, lddw, dw_type);
+  if (launch.n) launch.plan(dev);
   return with_workspace(
       dev, stream,
       [&](Pieces* p) {
@@ -635,6 +728,7 @@ int sgemm_linear_backward(int64_t tokens, int64_t inputs, int64_t outputs, const
         g.partial = dbias && !g.joined ? p->take<float>((int64_t)g.row_blocks * outputs) : nullptr;
         if (dX) w.place(p);
         if (dW) x.place(p);
+        launch.place(p);
       },
       [&](cudaError_t* e) {
         g.ldd = ldd;
@@ -642,9 +736,6 @@ int sgemm_linear_backward(int64_t tokens, int64_t inputs, int64_t outputs, const
         if (*e == cudaSuccess) *e = make_copies({dX ? &w : nullptr, dW ? &x : nullptr}, g.guard, stream);
         if (*e != cudaSuccess) return (int)SGEMM_OK;
         if (write) d = Operand(g.da, ldd, nullptr, 0, tokens, outputs);
-        Launch launch;
-        if (dX) launch.add() = input_gradient(tokens, inputs, outputs, &d, nullptr, &w, nullptr, dX, lddx);
-        if (dW) launch.add() = weight_gradient(tokens, inputs, outputs, &d, &x, dW, lddw, dw_type);
         return launch.n ? launch.run(dev, stream, e) : (int)SGEMM_OK;
       });
 }
@@ -709,6 +800,12 @@ int sgemm_gated_backward(int64_t tokens, int64_t inputs, int64_t outputs, const 
   Operand wg(gate, ldg, nullptr, 0, outputs, inputs), wu(up, ldu, nullptr, 0, outputs, inputs);
   Operand x(X ? X->data : nullptr, X ? X->ld : 1, X ? X->scale : nullptr, X ? X->lds : 1, tokens, inputs);
   const int64_t ldd = whole_lines(outputs);
+  Operand da, db;
+  Launch launch;
+  if (dX) launch.add() = input_gradient(tokens, inputs, outputs, &da, &db, &wg, &wu, dX, lddx);
+  if (dG) launch.add() = weight_gradient(tokens, inputs, outputs, &da, &x, dG, lddg, dw_type);
+  if (dG) launch.add() = weight_gradient(tokens, inputs, outputs, &db, &x, dU, lddu, dw_type);
+  if (launch.n) launch.plan(dev);
   return with_workspace(
       dev, stream,
       [&](Pieces* p) {
@@ -719,17 +816,15 @@ int sgemm_gated_backward(int64_t tokens, int64_t inputs, int64_t outputs, const 
           wu.place(p);
         }
         if (dG) x.place(p);
+        launch.place(p);
       },
       [&](cudaError_t* e) {
         g.ldd = ldd;
         *e = launch_linear_grad(g, stream);
         if (*e == cudaSuccess) *e = make_copies({dX ? &wg : nullptr, dX ? &wu : nullptr, dG ? &x : nullptr}, g.guard, stream);
         if (*e != cudaSuccess) return (int)SGEMM_OK;
-        Operand da(g.da, ldd, nullptr, 0, tokens, outputs), db(g.db, ldd, nullptr, 0, tokens, outputs);
-        Launch launch;
-        if (dX) launch.add() = input_gradient(tokens, inputs, outputs, &da, &db, &wg, &wu, dX, lddx);
-        if (dG) launch.add() = weight_gradient(tokens, inputs, outputs, &da, &x, dG, lddg, dw_type);
-        if (dG) launch.add() = weight_gradient(tokens, inputs, outputs, &db, &x, dU, lddu, dw_type);
+        da = Operand(g.da, ldd, nullptr, 0, tokens, outputs);
+        db = Operand(g.db, ldd, nullptr, 0, tokens, outputs);
         return launch.n ? launch.run(dev, stream, e) : (int)SGEMM_OK;
       });
 }
@@ -763,11 +858,12 @@ int sgemm_linear_plan(int64_t rows, int64_t cols, int64_t K, int gated, int kept
   plan->tile_k = 64;
   plan->stages = pair ? linear_pair_stages(c.tile) : short_stages(c.tile, s.gated, false);
   plan->threads = pair ? kLinearPairThreads : kLinearShortThreads;
-  plan->split_k = c.split;
-  plan->kernel_launches = 1;
+  plan->split_k = pair ? c.splits[0] : c.split;
+  plan->kernel_launches = plan->split_k > 1 && pair ? 2 : 1;
   plan->dp_tiles = pair ? s.pair_tiles(c.tile) : ceil_div(cols, 128) * ceil_div(rows, c.tile);
   const int64_t clusters = dev.pair_clusters >= 0 ? dev.pair_clusters : std::max(1, dev.sm_count / 2);
-  plan->grid_x = pair ? 2 * std::min(plan->dp_tiles, clusters) : plan->dp_tiles * c.split;
+  plan->grid_x = pair ? 2 * std::min(plan->dp_tiles * plan->split_k, clusters) : plan->dp_tiles * c.split;
+  plan->workspace_bytes = pair && plan->split_k > 1 ? round256(4 * plan->split_k * Launch::rows_apart(s) * Launch::sums_ld(s)) : 0;
   plan->grid_y = 1;
   plan->smem_bytes = pair ? linear_pair_smem(c.tile) : linear_short_smem(c.tile, s.gated, plan->stages, (int)short_stage(c.tile, s.gated, false));
   return SGEMM_OK;
@@ -779,7 +875,8 @@ int sgemm_linear_set_override(int variant, int tile_n, int split) {
   const auto is_in = [&](const auto& tiles) { return std::find(std::begin(tiles), std::end(tiles), tile_n) != std::end(tiles); };
   const bool known = is_short ? is_in(kLinearShortTiles) : variant == SGEMM_VARIANT_LINEAR_PAIR && is_in(kLinearPairTiles);
   if (tile_n != 0 && !known) return -2;
-  if ((split != 0 && !is_short) || (split != 0 && split != 1 && split != 2 && split != 4 && split != 8)) return -3;
+  if (variant == SGEMM_VARIANT_AUTO ? split != 0 : is_short ? split != 0 && split != 1 && split != 2 && split != 4 && split != 8 : split < 0 || split > kLinearMostShares)
+    return -3;
   g_force_variant.store(variant);
   g_force_tile.store(tile_n);
   g_force_split.store(split);

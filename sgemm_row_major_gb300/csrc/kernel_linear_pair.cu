@@ -4,7 +4,8 @@
 //     gradients:     D = A0 B0 (+ A1 B1)
 //
 // Up to three such products (jobs) run in one launch, their tiles one behind the other: a backward pass's products together
-// fill the rounds of tiles better than each alone.
+// fill the rounds of tiles better than each alone.  Where tiles are few and K is long, the K tiles of a tile are shared by
+// several units, whose FP32 sums kernel_linear_join.cu adds.
 //
 // Clusters of two CTAs on one TPC compute 256 x TN tiles (TN 64, 128 or 256) with tcgen05.mma.cta_group::2.kind::f16,
 // M = 256, N = TN, K = 16, both operands from shared memory: each CTA holds 128 rows of A and half of the tile's columns of
@@ -261,12 +262,21 @@ __device__ __forceinline__ void tmem_put(uint32_t taddr, const float (&v)[W]) {
   for (int h = 0; h < W; h += 16) tmem_st16(taddr + (uint32_t)h, *reinterpret_cast<const float(*)[16]>(&v[h]));
 }
 
-// The job of a tile and the tile's place in it.
+// The job of a unit of work, the tile and the K tiles [g0, g1) (over both segments) it takes.
 struct Place {
-  int job, tm, tn;
-  __device__ __forceinline__ Place(const LinearPairParams& p, int tile) : job(0) {
-    while (tile >= p.job[job].tiles_m * p.job[job].tiles_n) tile -= p.job[job].tiles_m * p.job[job].tiles_n, ++job;
-    tile_coords(tile, p.job[job].tiles_m, p.job[job].tiles_n, tm, tn);
+  int job, tm, tn, slice, g0, g1;
+  __device__ __forceinline__ static int units(const LinearJob& j) { return j.tiles_m * j.tiles_n * j.split; }
+  __device__ __forceinline__ Place(const LinearPairParams& p, int unit) : job(0), slice(0), g0(0) {
+    while (unit >= units(p.job[job])) unit -= units(p.job[job]), ++job;
+    const LinearJob& j = p.job[job];
+    g1 = j.k_tiles * j.segments;
+    if (j.split > 1) {  // the units of a tile one behind the other
+      slice = unit % j.split;
+      unit /= j.split;
+      g0 = (int)((int64_t)g1 * slice / j.split);
+      g1 = (int)((int64_t)g1 * (slice + 1) / j.split);
+    }
+    tile_coords(unit, j.tiles_m, j.tiles_n, tm, tn);
   }
 };
 
@@ -297,7 +307,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   const int cl = (int)cluster_id_x();
   int tiles = 0;
-  for (int n = 0; n < p.jobs; ++n) tiles += p.job[n].tiles_m * p.job[n].tiles_n;
+  for (int n = 0; n < p.jobs; ++n) tiles += Place::units(p.job[n]);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -343,28 +353,26 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         const LinearJob& j = p.job[at.job];
         const uint32_t bytes = 2u * (part_bytes(j.a_mn, BMC) + part_bytes(j.b_mn, halfn));  // both CTAs'
         const int m0 = at.tm * BM + BMC * (int)rank, n0 = GATED ? at.tn * TD : at.tn * TN + halfn * (int)rank;
-        const int a_mn = j.a_mn, b_mn = j.b_mn, kt = j.k_tiles;
-        for (int segment = 0; ok && segment < j.segments; ++segment) {
-          const CUtensorMap *ma = &maps.op[j.a[segment]], *mb = &maps.op[j.b[GATED ? (int)rank : segment]];
-          for (int k = 0; k < kt; ++k, ++t) {
-            if (lap > 0 && !poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
-              if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
-              ok = false;
-              break;
-            }
-            if (elect_one()) {
-              // both CTAs' loads complete on the even CTA's barrier, which expects all their bytes
-              const uint32_t fb = full0 + 8u * (uint32_t)s;
-              if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), bytes);
-              const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
-              const auto load = [&](uint32_t dst, const CUtensorMap* map, int inner, int outer) { tma_load_pair(dst, map, fb, inner, outer); };
-              load_part(load, a, ma, a_mn, m0, k * BK, BMC);
-              load_part(load, a + kPart, mb, b_mn, n0, k * BK, halfn);
-            }
-            if (++s == kStages) {
-              s = 0;
-              ++lap;
-            }
+        const int a_mn = j.a_mn, b_mn = j.b_mn;
+        for (int g = at.g0; g < at.g1; ++g, ++t) {
+          const int segment = g >= j.k_tiles, k0 = (g - segment * j.k_tiles) * BK;
+          if (lap > 0 && !poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
+            if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+            ok = false;
+            break;
+          }
+          if (elect_one()) {
+            // both CTAs' loads complete on the even CTA's barrier, which expects all their bytes
+            const uint32_t fb = full0 + 8u * (uint32_t)s;
+            if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), bytes);
+            const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
+            const auto load = [&](uint32_t dst, const CUtensorMap* map, int inner, int outer) { tma_load_pair(dst, map, fb, inner, outer); };
+            load_part(load, a, &maps.op[j.a[segment]], a_mn, m0, k0, BMC);
+            load_part(load, a + kPart, &maps.op[j.b[GATED ? (int)rank : segment]], b_mn, n0, k0, halfn);
+          }
+          if (++s == kStages) {
+            s = 0;
+            ++lap;
           }
         }
       }
@@ -378,8 +386,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int t = 0;  // K tiles whose products have been issued (odd CTA: will be)
       if (rank != 0) {
         for (int tile = cl; tile < tiles; tile += p.clusters) {
-          const LinearJob& j = p.job[Place(p, tile).job];
-          t += j.k_tiles * j.segments;
+          const Place at(p, tile);
+          t += at.g1 - at.g0;
         }
       } else {
         // ---------------------------------------------- products (even CTA)
@@ -388,9 +396,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t s_lap = 0, b_lap = 0;
         bool ok = true;
         for (int tile = cl; ok && tile < tiles; tile += p.clusters) {
-          const LinearJob& j = p.job[Place(p, tile).job];
+          const Place at(p, tile);
+          const LinearJob& j = p.job[at.job];
           const uint32_t astep = step_of(j.a_mn), bstep = step_of(j.b_mn), idesc = j.idesc;
-          const int kt = j.k_tiles * j.segments;
+          const int kt = at.g1 - at.g0;
           int n = j.fold0;  // a chunk: the K tiles of one accumulator
           for (int g = 0; ok && g < kt; g += n, n = j.fold) {
             n = min(n, kt - g);
@@ -454,11 +463,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fetch(cl);
     fetch(cl + p.clusters);
     for (int tile = cl; ok && tile < tiles; tile += p.clusters) {
-      const Place at(p, tile);
-      const LinearJob& j = p.job[at.job];
-      const int row0 = at.tm * BM + BMC * (int)rank + 32 * q, row = row0 + lane;
-      const int c0 = at.tn * TD + cols * part;  // this thread's first column of D
-      const int kt = j.k_tiles * j.segments;
+      int kt, fold0, fold;
+      {
+        const Place at(p, tile);
+        kt = at.g1 - at.g0;
+        fold0 = p.job[at.job].fold0;
+        fold = p.job[at.job].fold;
+      }
       uint32_t acc;
       const auto next = [&] {  // waits for the next accumulator
         ok = poll_wait(smem_addr(&acc_full[b]), b_lap & 1u, p.timeout_ns);
@@ -478,13 +489,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       bool several = false;
       if constexpr (FOLD) {
-        several = kt > j.fold0;
+        several = kt > fold0;
         if (several) {
           // several accumulators: all but the last are added in registers, and these sums to the last one where it lies
           float sum[TN / 2];
 #pragma unroll
           for (int e = 0; e < TN / 2; ++e) sum[e] = 0.0f;
-          for (int g = j.fold0; g < kt; g += j.fold) {  // (g: K tiles up to this accumulator's end)
+          for (int g = fold0; g < kt; g += fold) {  // (g: K tiles up to this accumulator's end)
             if (!next()) break;
 #pragma unroll
             for (int e = 0; e < 2 * loads; ++e) {
@@ -512,6 +523,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!several && !next()) break;
       // ---------------------------------------------- epilogue, W columns at a time
+      const Place at(p, tile);  // (again: nothing of it is held while the sums are)
+      const LinearJob& j = p.job[at.job];
+      const int row0 = at.slice * j.rows_apart + at.tm * BM + BMC * (int)rank + 32 * q, row = row0 + lane;
+      const int c0 = at.tn * TD + cols * part;  // this thread's first column of D
       constexpr int W = linear_pair_box(TN, GATED, FOLD);
       constexpr uint32_t up = TN / 2;  // gated: from a column of gate to up's
       pieces.set(W == 64 || (FOLD && j.f32 != 0));
@@ -615,10 +630,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         } else {
           Ahead<W> residual, bias;
           if (o.residual) residual.residual(o, j, row, c0 + c);
-          if (add_bias) bias.bias(o, j, c0 + c);
+          if (!FOLD && add_bias) bias.bias(o, j, c0 + c);
           tmem_wait_ld();
           if (last) release();
           tmem_ld_ready(v);
+          if (FOLD && add_bias) bias.bias(o, j, c0 + c);  // (sent for earlier it spilled)
           if (add_bias) bias.add(v);
           if (FOLD && o.keep == 2) codes(0, v);
           with_act(o.act, [&](auto act) {

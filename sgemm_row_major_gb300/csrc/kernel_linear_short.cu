@@ -32,29 +32,6 @@ __device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
   return v;
 }
 
-// Four elements of a BF16 row, n of them there.
-__device__ __forceinline__ void get4(const __nv_bfloat16* p, int n, bool vec, float (&x)[4]) {
-  if (vec && n == 4) {
-    const uint2 u = *reinterpret_cast<const uint2*>(p);
-    x[0] = __uint_as_float(u.x << 16);
-    x[1] = __uint_as_float(u.x & 0xFFFF0000u);
-    x[2] = __uint_as_float(u.y << 16);
-    x[3] = __uint_as_float(u.y & 0xFFFF0000u);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) x[e] = e < n ? __bfloat162float(p[e]) : 0.0f;
-  }
-}
-__device__ __forceinline__ void put4(__nv_bfloat16* p, int n, bool vec, const float (&x)[4]) {
-  if (vec && n == 4) {
-    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
-  } else {
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      if (e < n) p[e] = __float2bfloat16_rn(x[e]);
-  }
-}
-
 // What is kept of 4 columns of a token; all lanes of the warp, which hold 128 columns (n < 1: none here).
 __device__ __forceinline__ void keep4(const LinearOut& o, const LinearJob& j, int which, int row, int col, int n, const float (&v)[4]) {
   const LinearKept& k = o.kept[which];
@@ -303,19 +280,7 @@ __global__ void __launch_bounds__(kThreads, GATED || TS == 128 ? 1 : 2)
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[0][e] += x[e];
     }
-    if (!d_ok(o, j, row, col, n)) continue;
-    if (j.f32) {
-      float* d = static_cast<float*>(j.d) + (int64_t)row * j.ldd + col;
-      if (j.d_vec && n == 4) {
-        *reinterpret_cast<float4*>(d) = make_float4(v[0][0], v[0][1], v[0][2], v[0][3]);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < n) d[e] = v[0][e];
-      }
-    } else {
-      put4(static_cast<__nv_bfloat16*>(j.d) + (int64_t)row * j.ldd + col, n, j.d_vec, v[0]);
-    }
+    put_row(o, j, row, col, n, v[0]);
   }
   if (p.split > 1) {
     __syncthreads();

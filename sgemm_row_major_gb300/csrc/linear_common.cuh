@@ -174,6 +174,29 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
   return *reinterpret_cast<const uint32_t*>(&v);
 }
 
+// Four elements of a BF16 row, n of them there.
+__device__ __forceinline__ void get4(const __nv_bfloat16* p, int n, bool vec, float (&x)[4]) {
+  if (vec && n == 4) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    x[0] = __uint_as_float(u.x << 16);
+    x[1] = __uint_as_float(u.x & 0xFFFF0000u);
+    x[2] = __uint_as_float(u.y << 16);
+    x[3] = __uint_as_float(u.y & 0xFFFF0000u);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = e < n ? __bfloat162float(p[e]) : 0.0f;
+  }
+}
+__device__ __forceinline__ void put4(__nv_bfloat16* p, int n, bool vec, const float (&x)[4]) {
+  if (vec && n == 4) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2(x[0], x[1]), pack2(x[2], x[3]));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      if (e < n) p[e] = __float2bfloat16_rn(x[e]);
+  }
+}
+
 __device__ __forceinline__ bool d_ok(const LinearOut& o, const LinearJob& j, int64_t row, int64_t col, int64_t n) {
   return in_range(o.guard.fault, o.guard.word, f8::kSiteOut, row * j.ldd + col, n, extent(j.M, j.ldd, j.N));
 }
@@ -188,6 +211,23 @@ __device__ __forceinline__ void put_scale(const LinearOut& o, const LinearJob& j
   const LinearKept& k = o.kept[which];
   if (in_range(o.guard.fault, o.guard.word, f8::kSiteScale, row * k.lds + group, 1, extent(j.M, k.lds, (j.N + 127) / 128)))
     k.scale[row * k.lds + group] = s;
+}
+
+// Four columns of a row of D, n of them there.
+__device__ __forceinline__ void put_row(const LinearOut& o, const LinearJob& j, int row, int col, int n, const float (&v)[4]) {
+  if (!d_ok(o, j, row, col, n)) return;
+  if (j.f32) {
+    float* d = static_cast<float*>(j.d) + (int64_t)row * j.ldd + col;
+    if (j.d_vec && n == 4) {
+      *reinterpret_cast<float4*>(d) = make_float4(v[0], v[1], v[2], v[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (e < n) d[e] = v[e];
+    }
+  } else {
+    put4(static_cast<__nv_bfloat16*>(j.d) + (int64_t)row * j.ldd + col, n, j.d_vec, v);
+  }
 }
 
 }  // namespace lin

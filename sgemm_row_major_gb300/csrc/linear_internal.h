@@ -46,6 +46,9 @@ struct LinearJob {
   int a_mn = 0, b_mn = 0;        // 1: the stored rows run along M (N), not along K
   uint32_t idesc = 0;
   int a[2] = {0, 0}, b[2] = {0, 0};  // maps of the operands
+  // split > 1 (pair kernel): the K tiles of a tile are shared by that many units, each of which writes its sums to an FP32
+  // matrix of its own, `rows_apart` rows below the one before (D then stands for all of them: M = split * rows_apart)
+  int split = 1, rows_apart = 0;
 };
 constexpr int kLinearJobs = 3;
 struct LinearMaps {
@@ -85,6 +88,22 @@ constexpr int kLinearShortMaxStages = 12, kLinearShortThreads = 256;
 int64_t linear_short_smem(int tile_s, bool gated, int stages, int stage_bytes);
 cudaError_t prepare_linear_short();
 cudaError_t launch_linear_short(bool gated, const LinearMaps& maps, const LinearShortParams& p, cudaStream_t stream);
+
+// The sums of products whose K was shared: each job's `split` matrices added in order, then the epilogue (of the first job).
+constexpr int kLinearMostShares = 32;  // units of a tile
+struct LinearJoin {
+  const float* sums = nullptr;
+  int64_t ld = 0;                // row stride of the sums
+  int split = 1, rows_apart = 0;
+  LinearJob job;                 // M, N and D of the product
+  int64_t blocks = 0;            // of the launch
+  int parts = 1;                 // threads that share the sums of an element
+};
+struct LinearJoinParams {
+  LinearJoin part[kLinearJobs];
+  LinearOut out;
+};
+cudaError_t launch_linear_join(LinearJoinParams& p, cudaStream_t stream);
 
 // The elementwise part of the backward passes (kernel_linear_grad.cu).
 struct LinearKeptIn {

@@ -8,7 +8,8 @@ from linear_util import ACTS, check_all, check_kept, close, gated_grad_ref, gate
 pytestmark = pytest.mark.gpu
 
 KERNELS = [("AUTO", 0, 0), ("LINEAR_SHORT", 16, 1), ("LINEAR_SHORT", 32, 2), ("LINEAR_SHORT", 64, 4), ("LINEAR_SHORT", 128, 8), ("LINEAR_SHORT", 16, 8),
-           ("LINEAR_PAIR", 64, 0), ("LINEAR_PAIR", 128, 0), ("LINEAR_PAIR", 256, 0)]
+           ("LINEAR_PAIR", 64, 0), ("LINEAR_PAIR", 128, 0), ("LINEAR_PAIR", 256, 0), ("LINEAR_PAIR", 64, 2), ("LINEAR_PAIR", 128, 5),
+           ("LINEAR_PAIR", 256, 32)]
 # tokens, inputs, outputs: ones, below and beyond a tile, a fold of 512 and more, odd everything
 SHAPES = [(1, 1, 1), (1, 64, 128), (3, 7, 5), (17, 129, 33), (64, 512, 256), (130, 520, 264), (257, 1100, 129), (300, 1304, 713)]
 

@@ -102,9 +102,9 @@ def test_planner(lib):
 
 def test_override(lib):
     try:
-        for v, t, k in ((0, 0, 0), (40, 256, 0), (40, 0, 0), (41, 16, 8), (41, 128, 1)):
+        for v, t, k in ((0, 0, 0), (40, 256, 0), (40, 0, 0), (41, 16, 8), (41, 128, 1), (40, 64, 2), (40, 0, 32)):
             assert lib.sgemm_linear_set_override(v, t, k) == 0
-        for args, status in (((32, 0, 0), -1), ((40, 16, 0), -2), ((41, 256, 0), -2), ((0, 64, 0), -2), ((40, 64, 2), -3), ((41, 16, 3), -3)):
+        for args, status in (((32, 0, 0), -1), ((40, 16, 0), -2), ((41, 256, 0), -2), ((0, 64, 0), -2), ((40, 64, 33), -3), ((40, 64, -1), -3), ((0, 0, 2), -3), ((41, 16, 3), -3)):
             assert lib.sgemm_linear_set_override(*args) == status
         sg.sgemm_linear_set_override("LINEAR_SHORT", 32, 2)
         p = sg.sgemm_linear_plan(1000, 1000, 1000, sm_count=152)
