@@ -429,7 +429,7 @@ struct Launch {
       p.clusters = (int)clusters;
       p.timeout_ns = wait_timeout_ns();
       p.fault = dev.fault;
-      *e = launch_linear_pair(c.tile, gated, fold, maps, p, stream);
+      *e = launch_linear_pair(c.tile, gated, joins ? LinearPairForm::kShared : fold ? LinearPairForm::kFold : LinearPairForm::kWhole, maps, p, stream);
       if (joins && *e == cudaSuccess) {
         join.out = out;
         *e = launch_linear_join(join, stream);

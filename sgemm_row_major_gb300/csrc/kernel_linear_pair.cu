@@ -262,15 +262,22 @@ __device__ __forceinline__ void tmem_put(uint32_t taddr, const float (&v)[W]) {
   for (int h = 0; h < W; h += 16) tmem_st16(taddr + (uint32_t)h, *reinterpret_cast<const float(*)[16]>(&v[h]));
 }
 
-// The job of a unit of work, the tile and the K tiles [g0, g1) (over both segments) it takes.
+// The job of a unit of work, the tile and the K tiles [g0, g1) (over both segments) it takes.  SHARED: some job's tiles are
+// several units.
+template <bool SHARED>
 struct Place {
   int job, tm, tn, slice, g0, g1;
-  __device__ __forceinline__ static int units(const LinearJob& j) { return j.tiles_m * j.tiles_n * j.split; }
+  __device__ __forceinline__ static int units(const LinearJob& j) { return j.tiles_m * j.tiles_n * (SHARED ? j.split : 1); }
   __device__ __forceinline__ Place(const LinearPairParams& p, int unit) : job(0), slice(0), g0(0) {
-    while (unit >= units(p.job[job])) unit -= units(p.job[job]), ++job;
+    // (written out: with a call of units() the 256-wide folding kernel spilled 176 bytes, so it spills 20)
+    if (SHARED) {
+      while (unit >= units(p.job[job])) unit -= units(p.job[job]), ++job;
+    } else {
+      while (unit >= p.job[job].tiles_m * p.job[job].tiles_n) unit -= p.job[job].tiles_m * p.job[job].tiles_n, ++job;
+    }
     const LinearJob& j = p.job[job];
     g1 = j.k_tiles * j.segments;
-    if (j.split > 1) {  // the units of a tile one behind the other
+    if (SHARED && j.split > 1) {  // the units of a tile one behind the other
       slice = unit % j.split;
       unit /= j.split;
       g0 = (int)((int64_t)g1 * slice / j.split);
@@ -282,8 +289,9 @@ struct Place {
 
 // TN: the accumulator's columns.  GATED: half of them are gate's, half up's.  FOLD: FP32 values leave the kernel (an FP32
 // output, scales of 8-bit values), so a job may add several accumulators in registers; without that the epilogue has room for
-// 64 columns at a time everywhere.
-template <int TN, bool GATED, bool FOLD>
+// 64 columns at a time everywhere.  SHARED: some job's K is shared by several units; sums are written and nothing else is done.
+// (A form of its own: with the sharing in all of them 16384 tokens, 256 -> 2048 gated, kept in 8 bits, took 59.4 us, not 56.3.)
+template <int TN, bool GATED, bool FOLD, bool SHARED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     linear_pair_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearPairParams p) {
   extern __shared__ uint8_t smem_raw[];
@@ -307,7 +315,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   const uint32_t rank = cluster_rank();
   const int cl = (int)cluster_id_x();
   int tiles = 0;
-  for (int n = 0; n < p.jobs; ++n) tiles += Place::units(p.job[n]);
+  for (int n = 0; n < p.jobs; ++n) tiles += Place<SHARED>::units(p.job[n]);
 
   if (threadIdx.x == 0) {
     for (int s = 0; s < kStages; ++s) {
@@ -349,30 +357,33 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       uint32_t lap = 0;
       bool ok = true;
       for (int tile = cl; ok && tile < tiles; tile += p.clusters) {
-        const Place at(p, tile);
+        const Place<SHARED> at(p, tile);
         const LinearJob& j = p.job[at.job];
         const uint32_t bytes = 2u * (part_bytes(j.a_mn, BMC) + part_bytes(j.b_mn, halfn));  // both CTAs'
         const int m0 = at.tm * BM + BMC * (int)rank, n0 = GATED ? at.tn * TD : at.tn * TN + halfn * (int)rank;
-        const int a_mn = j.a_mn, b_mn = j.b_mn;
-        for (int g = at.g0; g < at.g1; ++g, ++t) {
-          const int segment = g >= j.k_tiles, k0 = (g - segment * j.k_tiles) * BK;
-          if (lap > 0 && !poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
-            if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
-            ok = false;
-            break;
-          }
-          if (elect_one()) {
-            // both CTAs' loads complete on the even CTA's barrier, which expects all their bytes
-            const uint32_t fb = full0 + 8u * (uint32_t)s;
-            if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), bytes);
-            const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
-            const auto load = [&](uint32_t dst, const CUtensorMap* map, int inner, int outer) { tma_load_pair(dst, map, fb, inner, outer); };
-            load_part(load, a, &maps.op[j.a[segment]], a_mn, m0, k0, BMC);
-            load_part(load, a + kPart, &maps.op[j.b[GATED ? (int)rank : segment]], b_mn, n0, k0, halfn);
-          }
-          if (++s == kStages) {
-            s = 0;
-            ++lap;
+        const int a_mn = j.a_mn, b_mn = j.b_mn, kt = j.k_tiles;
+        for (int segment = 0; ok && segment < j.segments; ++segment) {
+          const CUtensorMap *ma = &maps.op[j.a[segment]], *mb = &maps.op[j.b[GATED ? (int)rank : segment]];
+          const int end = SHARED ? min(kt, at.g1 - segment * kt) : kt;
+          for (int k = SHARED ? max(0, at.g0 - segment * kt) : 0; k < end; ++k, ++t) {
+            if (lap > 0 && !poll_wait(smem_addr(&done[s]), (lap - 1) & 1u, p.timeout_ns)) {
+              if (lane == 0) atomicOr(p.fault, (unsigned)kFaultEmptyWait);
+              ok = false;
+              break;
+            }
+            if (elect_one()) {
+              // both CTAs' loads complete on the even CTA's barrier, which expects all their bytes
+              const uint32_t fb = full0 + 8u * (uint32_t)s;
+              if (rank == 0) mbar_arrive_expect_tx(smem_addr(&full[s]), bytes);
+              const uint32_t a = sbase + (uint32_t)(s * kStageBytes);
+              const auto load = [&](uint32_t dst, const CUtensorMap* map, int inner, int outer) { tma_load_pair(dst, map, fb, inner, outer); };
+              load_part(load, a, ma, a_mn, m0, k * BK, BMC);
+              load_part(load, a + kPart, mb, b_mn, n0, k * BK, halfn);
+            }
+            if (++s == kStages) {
+              s = 0;
+              ++lap;
+            }
           }
         }
       }
@@ -386,7 +397,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       int t = 0;  // K tiles whose products have been issued (odd CTA: will be)
       if (rank != 0) {
         for (int tile = cl; tile < tiles; tile += p.clusters) {
-          const Place at(p, tile);
+          const Place<SHARED> at(p, tile);
           t += at.g1 - at.g0;
         }
       } else {
@@ -396,7 +407,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
         uint32_t s_lap = 0, b_lap = 0;
         bool ok = true;
         for (int tile = cl; ok && tile < tiles; tile += p.clusters) {
-          const Place at(p, tile);
+          const Place<SHARED> at(p, tile);
           const LinearJob& j = p.job[at.job];
           const uint32_t astep = step_of(j.a_mn), bstep = step_of(j.b_mn), idesc = j.idesc;
           const int kt = at.g1 - at.g0;
@@ -456,20 +467,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     int b = 0;
     uint32_t b_lap = 0, asked = 0;  // tiles whose largest values have been exchanged
     const auto fetch = [&](int tile) {  // has a tile's residual brought to L2
-      if (GATED || !o.residual || tile >= tiles) return;
-      const Place to(p, tile);
+      if (GATED || SHARED || !o.residual || tile >= tiles) return;
+      const Place<SHARED> to(p, tile);
       prefetch_residual(o, p.job[to.job], to.tm * BM + BMC * (int)rank + 32 * q + lane, to.tn * TD + cols * part, cols);
     };
     fetch(cl);
     fetch(cl + p.clusters);
     for (int tile = cl; ok && tile < tiles; tile += p.clusters) {
-      int kt, fold0, fold;
-      {
-        const Place at(p, tile);
-        kt = at.g1 - at.g0;
-        fold0 = p.job[at.job].fold0;
-        fold = p.job[at.job].fold;
-      }
+      const Place<SHARED> at(p, tile);
+      const LinearJob& j = p.job[at.job];
+      const int row0 = (SHARED ? at.slice * j.rows_apart : 0) + at.tm * BM + BMC * (int)rank + 32 * q, row = row0 + lane;
+      const int c0 = at.tn * TD + cols * part;  // this thread's first column of D
+      const int kt = at.g1 - at.g0;
       uint32_t acc;
       const auto next = [&] {  // waits for the next accumulator
         ok = poll_wait(smem_addr(&acc_full[b]), b_lap & 1u, p.timeout_ns);
@@ -489,13 +498,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       };
       bool several = false;
       if constexpr (FOLD) {
-        several = kt > fold0;
+        several = kt > j.fold0;
         if (several) {
           // several accumulators: all but the last are added in registers, and these sums to the last one where it lies
           float sum[TN / 2];
 #pragma unroll
           for (int e = 0; e < TN / 2; ++e) sum[e] = 0.0f;
-          for (int g = fold0; g < kt; g += fold) {  // (g: K tiles up to this accumulator's end)
+          for (int g = j.fold0; g < kt; g += j.fold) {  // (g: K tiles up to this accumulator's end)
             if (!next()) break;
 #pragma unroll
             for (int e = 0; e < 2 * loads; ++e) {
@@ -523,18 +532,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       }
       if (!several && !next()) break;
       // ---------------------------------------------- epilogue, W columns at a time
-      const Place at(p, tile);  // (again: nothing of it is held while the sums are)
-      const LinearJob& j = p.job[at.job];
-      const int row0 = at.slice * j.rows_apart + at.tm * BM + BMC * (int)rank + 32 * q, row = row0 + lane;
-      const int c0 = at.tn * TD + cols * part;  // this thread's first column of D
       constexpr int W = linear_pair_box(TN, GATED, FOLD);
       constexpr uint32_t up = TN / 2;  // gated: from a column of gate to up's
       pieces.set(W == 64 || (FOLD && j.f32 != 0));
       const CUtensorMap* map_d = &maps.d[at.job];
       float inv[2] = {1.0f, 1.0f};       // of the scales of what is kept in 8 bits
       bool odd = false;                  // an infinity among them
-      bool add_bias = !GATED && o.bias;  // still to be done
-      if (o.keep) {
+      bool add_bias = !GATED && !SHARED && o.bias;  // still to be done
+      if (!SHARED && o.keep) {
         // what is kept in BF16, or the largest values of what is kept in 8 bits; the bias is added where the sums lie
         float m[2] = {0.0f, 0.0f};
 #pragma unroll 1
@@ -629,15 +634,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
           emit<false>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
         } else {
           Ahead<W> residual, bias;
-          if (o.residual) residual.residual(o, j, row, c0 + c);
-          if (!FOLD && add_bias) bias.bias(o, j, c0 + c);
+          if (!SHARED && o.residual) residual.residual(o, j, row, c0 + c);
+          if (add_bias) bias.bias(o, j, c0 + c);
           tmem_wait_ld();
           if (last) release();
           tmem_ld_ready(v);
-          if (FOLD && add_bias) bias.bias(o, j, c0 + c);  // (sent for earlier it spilled)
           if (add_bias) bias.add(v);
-          if (FOLD && o.keep == 2) codes(0, v);
-          with_act(o.act, [&](auto act) {
+          if (FOLD && !SHARED && o.keep == 2) codes(0, v);
+          if (!SHARED) with_act(o.act, [&](auto act) {
 #pragma unroll
             for (int k = 0; k < W; k += 2) {
               const float2 f = act_of<decltype(act)::value>(make_float2(v[k], v[k + 1]));
@@ -645,7 +649,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               v[k + 1] = f.y;
             }
           });
-          if (o.residual) residual.add(v);
+          if (!SHARED && o.residual) residual.add(v);
           if (FOLD && j.f32) emit<true>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
           else               emit<false>(pieces, map_d, j.d_tma, j.d, j.ldd, o, j, f8::kSiteOut, row0, c0 + c, v);
         }
@@ -670,18 +674,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 }
 
 // f(kernel) for a tile width and form.
-template <bool FOLD, typename F>
+template <bool FOLD, bool SHARED, typename F>
 cudaError_t with_form(int tile_n, bool gated, const F& f) {
+  constexpr bool kGated = !SHARED;  // (K of gated products is not shared)
+  if (gated && (tile_n == 64 || SHARED)) return cudaErrorInvalidValue;
   switch (tile_n) {
-    case 256: return gated ? f(linear_pair_kernel<256, true, FOLD>) : f(linear_pair_kernel<256, false, FOLD>);
-    case 128: return gated ? f(linear_pair_kernel<128, true, false>) : f(linear_pair_kernel<128, false, FOLD>);  // (gated: BF16 alone)
-    case 64: return gated ? cudaErrorInvalidValue : f(linear_pair_kernel<64, false, FOLD>);
+    case 256: return gated ? f(linear_pair_kernel<256, kGated, FOLD, SHARED>) : f(linear_pair_kernel<256, false, FOLD, SHARED>);
+    case 128: return gated ? f(linear_pair_kernel<128, kGated, FOLD && SHARED, SHARED>) : f(linear_pair_kernel<128, false, FOLD, SHARED>);  // (gated: BF16 alone)
+    case 64: return f(linear_pair_kernel<64, false, FOLD, SHARED>);
+    default: return cudaErrorInvalidValue;
   }
-  return cudaErrorInvalidValue;
 }
 template <typename F>
-cudaError_t with_kernel(int tile_n, bool gated, bool fold, const F& f) {
-  return fold ? with_form<true>(tile_n, gated, f) : with_form<false>(tile_n, gated, f);
+cudaError_t with_kernel(int tile_n, bool gated, LinearPairForm form, const F& f) {
+  switch (form) {
+    case LinearPairForm::kWhole: return with_form<false, false>(tile_n, gated, f);
+    case LinearPairForm::kFold: return with_form<true, false>(tile_n, gated, f);
+    default: return with_form<true, true>(tile_n, gated, f);
+  }
 }
 
 }  // namespace
@@ -692,10 +702,11 @@ int64_t linear_pair_smem(int tile_n) { return tile_n == 256 ? lin::Ring<256>::kS
 
 cudaError_t prepare_linear_pair() {
   for (int tile_n : kLinearPairTiles)
-    for (int form = 0; form < 4; ++form) {
-      const bool gated = form / 2 != 0, fold = form % 2 != 0;
-      if (gated && tile_n == 64) continue;
-      const cudaError_t e = lin::with_kernel(tile_n, gated, fold, [&](auto kernel) {
+    for (int n = 0; n < 6; ++n) {
+      const bool gated = n >= 3;
+      const LinearPairForm form = (LinearPairForm)(n % 3);
+      if (gated && (tile_n == 64 || form == LinearPairForm::kShared)) continue;
+      const cudaError_t e = lin::with_kernel(tile_n, gated, form, [&](auto kernel) {
         return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)linear_pair_smem(tile_n));
       });
       if (e != cudaSuccess) return e;
@@ -703,7 +714,7 @@ cudaError_t prepare_linear_pair() {
   return cudaSuccess;
 }
 
-cudaError_t launch_linear_pair(int tile_n, bool gated, bool fold, const LinearMaps& maps, const LinearPairParams& p, cudaStream_t stream) {
+cudaError_t launch_linear_pair(int tile_n, bool gated, LinearPairForm form, const LinearMaps& maps, const LinearPairParams& p, cudaStream_t stream) {
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2u * (unsigned)p.clusters);
   cfg.blockDim = dim3(lin::kThreads);
@@ -714,7 +725,7 @@ cudaError_t launch_linear_pair(int tile_n, bool gated, bool fold, const LinearMa
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return lin::with_kernel(tile_n, gated, fold, [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, maps, p); });
+  return lin::with_kernel(tile_n, gated, form, [&](auto kernel) { return cudaLaunchKernelEx(&cfg, kernel, maps, p); });
 }
 
 }  // namespace sgemm_impl
