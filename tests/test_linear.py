@@ -167,6 +167,46 @@ def test_residual_in_place(force, kernel, pad):
     done()
 
 
+def test_shared_k_as_chosen():
+    """Long K and few tiles, where the planner shares K: residuals in place and kept values with rows at any alignment, products
+    with and without shares in one launch, and two captured calls whose workspaces are in use at the same time."""
+    import torch
+    T, I, O = 4, 15527, 108
+    assert sg.sgemm_linear_plan(T, O, I)["kernel_launches"] == 2 and sg.sgemm_linear_plan(1024, 1024, 16384)["split_k"] > 1
+    x, w, b, r = rand(1, T, I), rand(2, O, I, std=I ** -0.5), rand(3, 1, O)[0], rand(4, T, O)
+    ref = linear_ref(x, w, b, "gelu", r)
+    want = sg.linear_bf16(x, w, b, "gelu", r, save="bf16")
+    check_all(want, ref, ["y"])
+    check_kept(want.pre, *ref["pre"])
+    for pad, offset in ((0, 0), (3, 1)):
+        stream = strided(r, pad, offset)
+        got = sg.linear_bf16(x, w, b, "gelu", stream, save="bf16", out=stream)
+        assert torch.equal(got.y, want.y) and torch.equal(got.pre, want.pre)
+        assert int(stream.as_strided((T * (O + pad),), (1,)).isnan().sum()) == T * pad
+    calls = []
+    for seed, (T, I, O) in enumerate(((16384, 1024, 256), (2, 128, 8413))):
+        dy, x, w, u = rand(seed, T, O, std=0.1), rand(seed + 1, T, I), rand(seed + 2, O, I, std=O ** -0.5), rand(seed + 3, O, I, std=O ** -0.5)
+        a, v = rand(seed + 4, T, O), rand(seed + 5, T, O)
+        check_all(sg.linear_bf16_backward(dy, x, w, a, "silu", dbias=True, dweight_dtype=torch.float32), linear_grad_ref(dy, x, w, a, "silu"))
+        calls.append(lambda dy=dy, x=x, w=w, u=u, a=a, v=v: sg.gated_bf16_backward(dy, x, w, u, a, v, "gelu", h=True))
+        check_all(calls[-1](), gated_grad_ref(dy, x, w, u, a, v, "gelu"))
+    want = [call() for call in calls]
+    graphs, got, streams = [], [], [torch.cuda.Stream(), torch.cuda.Stream()]
+    for call in calls:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(call())
+        graphs.append(g)
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for p, q in zip(want, got):
+        assert all(torch.equal(m, n) for m, n in zip(p, q))
+    done()
+
+
 def test_empty():
     """No tokens, no inputs, no outputs: empty results and sums of nothing."""
     import torch
