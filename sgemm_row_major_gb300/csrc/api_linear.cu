@@ -272,11 +272,19 @@ struct Product {
   bool f32 = false;
 };
 
-// K tiles of 64 that the pair kernel sums in one accumulator where FP32 values leave it (an FP32 output, scales): sums of 8 are
-// about as exact as FP32 sums (kernel_linear_pair.cu).  The more the first takes, the more time the epilogue of the tile before
-// has before the folding starts again: 16 are 4.7 us, about an FP32 output's; the epilogue that keeps 8-bit values takes up to 8 and
-// gets 24 where they are at most half of a sum (8192 x 4096 x 16384 with GELU's tanh form 647 -> 612 us).
-constexpr int kFoldFirst = 16, kFoldFirstKept8 = 24, kFold = 8, kFoldNone = 1 << 30;
+// K tiles of 64 that the pair kernel sums in one accumulator where FP32 values leave it (an FP32 output, scales): 8, but for the
+// first, which takes more the longer the sum is: the epilogue of the tile before has the first one's time, 294 ns per K tile of a
+// 256-wide tile, before the folding starts again.  An accumulator of n K tiles is off by 6.1e-8 n of its own sum (measured over 1 to
+// 256 of them), in that sum's direction.  The sums of several are independent and go by the square roots of their lengths n_i, so
+// together they are off by 6.1e-8 sqrt(sum(n_i^3) / sum(n_i)) of the whole.  The first is the longest that keeps this root at 13
+// (8e-7): n^3 - 64 n <= 105 K tiles.  (A first of 16 whatever the length, and of 24 for 8-bit values
+// of longer sums, were off by 1e-6 at some lengths.)
+constexpr int kFold = 8, kFoldMost = 32, kFoldNone = 1 << 30;
+int first_fold(int64_t k_tiles) {
+  int n = kFold;
+  while (n < kFoldMost && (int64_t)(n + 1) * ((n + 1) * (n + 1) - 64) <= 105 * k_tiles) ++n;
+  return n;
+}
 
 // One launch of the products: of one with a choice of either kernel, of several with the pair kernel.
 struct Launch {
@@ -393,7 +401,7 @@ struct Launch {
           j.d = sums[first + i];
           j.ldd = t.ld;
           j.f32 = j.d_tma = 1;
-          j.fold0 = kFoldFirst;
+          j.fold0 = first_fold(ceil_div(r.shape.k_tiles(), t.split));
           if (*e == cudaSuccess) *e = encode_linear_out_map(j.d, t.ld, j.M, t.ld, false, 32, &maps.d[i]);
         } else if (j.d_tma && *e == cudaSuccess) *e = encode_linear_out_map(r.d, r.shape.N / (16 / size) * (16 / size), r.shape.M, r.ldd, !r.f32, r.f32 ? 32 : linear_pair_box(c.tile, gated, fold), &maps.d[i]);
       } else {
@@ -451,8 +459,7 @@ struct Launch {
   }
 
   int fold_first(const Product& r) const {
-    if (out.keep == 2 && !r.f32 && r.shape.k_tiles() >= 2 * kFoldFirstKept8) return kFoldFirstKept8;
-    return r.f32 || out.keep == 2 ? kFoldFirst : kFoldNone;
+    return r.f32 || out.keep == 2 ? first_fold(r.shape.k_tiles()) : kFoldNone;
   }
   static bool tma_writes(const void* p, int64_t ld, int64_t cols, int size) { return rows_at(p, ld, size, 16) && cols * size >= 16; }
 };

@@ -207,6 +207,31 @@ def test_shared_k_as_chosen():
     done()
 
 
+@pytest.mark.parametrize("kernel", [("AUTO", 0, 0), ("LINEAR_PAIR", 256, 1), ("LINEAR_PAIR", 128, 0), ("LINEAR_PAIR", 128, 4), ("LINEAR_SHORT", 64, 1)], ids=str)
+def test_fp32_values_of_any_length(force, kernel):
+    """FP32 outputs and the scales of 8-bit values do not drift with K.  The tensor cores round each of the 4 steps of a K tile
+    towards zero: half a unit of the last place on average, which is 0.72 u of a value (u 2^-24; its mean over a binade), of
+    partial sums that are half of the whole one on average, so 4 * 0.72 / 2 = 1.44 u per K tile of an accumulator at most.
+    Measured it is 1.02 u, 6.1e-8, which is what the kernel's rule goes by: accumulators of n_i K tiles, whose sums are
+    independent and go by the roots of their lengths, are together off by 6.1e-8 sqrt(sum(n_i^3) / sum(n_i)) of the whole sum,
+    and the rule keeps the root at 13.  This test holds it to that, with u for the FP32 sums and a tenth of room.  (The guaranteed
+    bound, (K + 2) u sum|a b|, is the other tests'.)"""
+    import torch
+    force(*kernel)
+    tol = 1.1 * (13 * 6.1e-8 + 2.0 ** -24)  # 9.4e-7
+    worst = []
+    for kt in (1, 8, 12, 13, 14, 15, 16, 17, 20, 24, 32, 47, 49, 64, 100, 128, 200):
+        T, I, O = 300, 64 * kt, 256
+        x, w, u = rand(kt, T, I), rand(kt + 1, O, I, std=I ** -0.5), rand(kt + 2, O, I, std=I ** -0.5)
+        pre = x.double() @ w.double().T
+        scale = pre.abs().view(T, -1, 128).amax(2) / 448
+        off = lambda got, want: float((got.double() - want).norm() / want.norm())  # noqa: E731
+        worst.append(max(off(sg.linear_bf16(x, w, out_dtype=torch.float32).y, pre), off(sg.linear_bf16(x, w, save="fp8").pre.scale, scale),
+                         off(sg.gated_bf16(x, w, u, save="fp8").gate.scale, scale)))
+    assert max(worst) <= tol, worst
+    done()
+
+
 def test_empty():
     """No tokens, no inputs, no outputs: empty results and sums of nothing."""
     import torch
