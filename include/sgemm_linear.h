@@ -18,9 +18,12 @@
  * to aligned rows in the workspace), and outputs are written fastest there too.
  * No output may overlap an input or another output unless its call says so.
  *
- * Products are summed on the tensor cores in FP32, 512 terms at a time, and
- * these sums in FP32: an element is at most (K + 2) 2^-24 sum|a b| off before
- * its activation and its one rounding to the output's type.
+ * Products are summed on the tensor cores in FP32: an element is at most
+ * (K + 2) 2^-24 sum|a b| off before its activation and its one rounding to the
+ * output's type.  For FP32 outputs and the scales of 8-bit values long sums are
+ * made of several, which keeps random sums of up to 16384 terms within 1e-6; BF16 outputs
+ * take them whole.  So a result's last bits can depend on the other outputs
+ * that are wanted, as they can on the sizes.
  */
 #ifndef SGEMM_LINEAR_H
 #define SGEMM_LINEAR_H

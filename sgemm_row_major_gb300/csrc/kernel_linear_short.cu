@@ -7,7 +7,11 @@
 // order, each CTA the tokens of its part, read from its peers' shared memory: no workspace, one launch, and the same result
 // every time.  A warp writes 128 columns of one token at a time, which are one group of what is kept in 8 bits.
 //
-// Warp 0 loads (TMA), warp 1 issues the products, warps 4-7 take the accumulators to FP32 registers, all warps join the shares.  Two CTAs share an SM where their sums leave room.
+// Warp 0 loads (TMA), warp 1 issues the products, warps 4-7 take the accumulators to FP32 registers, all warps join the shares.  Two CTAs
+// share an SM where their sums leave room.
+//
+// Bound by reading the weights and, below about 20 us, by the start, the first loads and the joining: 64 x 16384 -> 4096 takes
+// 27.6 us, 4.9 TB/s; gated 1 x 4096 -> 8192 25.7 us, 5.2 TB/s; 1 x 4096 -> 4096 10.3 us, 3.3 TB/s.
 #include "linear_common.cuh"
 
 namespace sgemm_impl {
