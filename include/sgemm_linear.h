@@ -21,8 +21,9 @@
  * Products are summed on the tensor cores in FP32: an element is at most
  * (K + 2) 2^-24 sum|a b| off before its activation and its one rounding to the
  * output's type.  For FP32 outputs and the scales of 8-bit values long sums are
- * made of several, which keeps random sums of up to 16384 terms within 1e-6; BF16 outputs
- * take them whole.  So a result's last bits can depend on the other outputs
+ * made of several, which keeps random sums of up to 16384 terms within 1e-6; for
+ * BF16 outputs parts of up to 16384 terms are summed whole, which are up to
+ * 1e-4 too small where the terms have one sign.  So a result's last bits can depend on the other outputs
  * that are wanted, as they can on the sizes.
  */
 #ifndef SGEMM_LINEAR_H

@@ -41,12 +41,19 @@ bool usable_kept(const sgemm_kept_t* k, int64_t cols, bool work) {
 
 std::atomic<int> g_force_variant{SGEMM_VARIANT_AUTO}, g_force_tile{0}, g_force_split{0};
 
+// K tiles that a BF16 output's sum has in one accumulator of the pair kernel, at most.  The tensor cores truncate what they add:
+// the more, the larger the accumulator is against it, and where the terms have one sign all in one direction.  At this length
+// such a sum is 7.5e-5 too small, a twenty-sixth of a BF16 value's smallest half step; accumulators of 1024 K tiles were 3.8e-4 off
+// and whole sums of 16384 of them 6.6e-3, three half steps (measured; where signs are random 6.1e-8 per K tile).
+constexpr int kWholeMost = 256;
+
 // A product: M x N over `segments` times K.
 struct Shape {
   int64_t M = 0, N = 0, K = 0;
   int segments = 1;
   bool gated = false, kept8 = false;
   int64_t k_tiles() const { return ceil_div(K, 64) * segments; }
+  bool long_sum() const { return k_tiles() > kWholeMost; }
   int64_t pair_tiles(int tile) const { return ceil_div(M, 256) * ceil_div(N, gated ? tile / 2 : tile); }
 };
 
@@ -81,7 +88,7 @@ bool short_alone(int tile, bool gated) { return gated || tile == 128; }  // one 
 int64_t short_ring(int tile, bool gated) { return (short_alone(tile, gated) ? 2 : 1) * 98 * 1024; }
 
 bool pair_tile_fits(int tile, const Shape& s) {
-  return s.gated ? tile >= (s.kept8 ? 256 : 128) : tile >= (s.kept8 ? 128 : 64);
+  return s.gated ? tile >= (s.kept8 || s.long_sum() ? 256 : 128) : tile >= (s.kept8 ? 128 : 64);
 }
 
 struct Choice {
@@ -278,8 +285,8 @@ struct Product {
 // 256 of them), in that sum's direction.  The sums of several are independent and go by the square roots of their lengths n_i, so
 // together they are off by 6.1e-8 sqrt(sum(n_i^3) / sum(n_i)) of the whole.  The first is the longest that keeps this root at 13
 // (8e-7): n^3 - 64 n <= 105 K tiles.  (A first of 16 whatever the length, and of 24 for 8-bit values
-// of longer sums, were off by 1e-6 at some lengths.)
-constexpr int kFold = 8, kFoldMost = 32, kFoldNone = 1 << 30;
+// of longer sums, were off by 1e-6 at some lengths.  Sums of terms of one sign come out 7.3e-7 too small at most, by 1 to 1024 K tiles.)
+constexpr int kFold = 8, kFoldMost = 32;
 int first_fold(int64_t k_tiles) {
   int n = kFold;
   while (n < kFoldMost && (int64_t)(n + 1) * ((n + 1) * (n + 1) - 64) <= 105 * k_tiles) ++n;
@@ -363,7 +370,7 @@ struct Launch {
     };
     int64_t tiles = 0, steps = 0;
     bool fold = out.keep == 2;
-    for (int i = 0; i < count; ++i) fold |= list[i].f32 || c.splits[i] > 1;
+    for (int i = 0; i < count; ++i) fold |= list[i].f32 || c.splits[i] > 1 || list[i].shape.long_sum();
     for (int i = 0; i < count; ++i) {
       const Product& r = list[i];
       LinearJob& j = p.job[i];
@@ -377,8 +384,9 @@ struct Launch {
       j.d_vec = rows_at(r.d, r.ldd, size, 4 * size);
       j.k_tiles = (int)ceil_div(r.shape.K, 64);
       j.segments = r.shape.segments;
-      j.fold0 = fold_first(r);
-      j.fold = kFold;
+      const bool wide = r.f32 || out.keep == 2;  // FP32 values leave the kernel
+      j.fold0 = wide ? first_fold(r.shape.k_tiles()) : kWholeMost;
+      j.fold = wide ? kFold : kWholeMost;
       j.a_mn = r.a_mn;
       j.b_mn = r.b_mn;
       if (pair) {
@@ -402,6 +410,7 @@ struct Launch {
           j.ldd = t.ld;
           j.f32 = j.d_tma = 1;
           j.fold0 = first_fold(ceil_div(r.shape.k_tiles(), t.split));
+          j.fold = kFold;
           if (*e == cudaSuccess) *e = encode_linear_out_map(j.d, t.ld, j.M, t.ld, false, 32, &maps.d[i]);
         } else if (j.d_tma && *e == cudaSuccess) *e = encode_linear_out_map(r.d, r.shape.N / (16 / size) * (16 / size), r.shape.M, r.ldd, !r.f32, r.f32 ? 32 : linear_pair_box(c.tile, gated, fold), &maps.d[i]);
       } else {
@@ -458,9 +467,6 @@ struct Launch {
     return SGEMM_OK;
   }
 
-  int fold_first(const Product& r) const {
-    return r.f32 || out.keep == 2 ? first_fold(r.shape.k_tiles()) : kFoldNone;
-  }
   static bool tma_writes(const void* p, int64_t ld, int64_t cols, int size) { return rows_at(p, ld, size, 16) && cols * size >= 16; }
 };
 

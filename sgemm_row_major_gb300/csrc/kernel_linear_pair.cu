@@ -14,8 +14,9 @@
 // 64 columns at a time while the next tile's products fill the other one.  The tensor cores' own accumulation is not
 // round-to-nearest and drifts by about 1.2e-8 of the sum per instruction of 16 k.  Where FP32 values leave the kernel (an FP32
 // output, the scales of 8-bit values) only `fold` K tiles are summed in one accumulator, and these sums in FP32 registers;
-// BF16 outputs take whole sums from the tensor memory (1e-5 off at 16384 terms, where their own rounding is 2e-3), which
-// leaves the next tile's products a whole tile's time to overlap with the epilogue.
+// BF16 outputs take sums of up to 256 K tiles whole from the tensor memory (off by 1.6e-5 of the sum at that length where the terms'
+// signs are random and by 7.5e-5 where they have one sign; their own rounding is 2e-3), which leaves the next tile's products a whole
+// tile's time to overlap with the epilogue; longer ones are folded in parts of that many.
 //
 // Either operand may be stored along K or across it: the tensor core reads both orders, so a gradient's product takes the
 // weights and activations as the forward pass left them.
@@ -292,7 +293,7 @@ struct Place {
 };
 
 // TN: the accumulator's columns.  GATED: half of them are gate's, half up's.  FOLD: FP32 values leave the kernel (an FP32
-// output, scales of 8-bit values), so a job may add several accumulators in registers; without that the epilogue has room for
+// output, scales of 8-bit values) or a sum is long, so a job may add several accumulators in registers; without that the epilogue has room for
 // 64 columns at a time everywhere.  SHARED: some job's K is shared by several units; sums are written and nothing else is done.
 // (A form of its own: with the sharing in all of them 16384 tokens, 256 -> 2048 gated, kept in 8 bits, took 59.4 us, not 56.3.)
 template <int TN, bool GATED, bool FOLD, bool SHARED>
@@ -684,7 +685,7 @@ cudaError_t with_form(int tile_n, bool gated, const F& f) {
   if (gated && (tile_n == 64 || SHARED)) return cudaErrorInvalidValue;
   switch (tile_n) {
     case 256: return gated ? f(linear_pair_kernel<256, kGated, FOLD, SHARED>) : f(linear_pair_kernel<256, false, FOLD, SHARED>);
-    case 128: return gated ? f(linear_pair_kernel<128, kGated, FOLD && SHARED, SHARED>) : f(linear_pair_kernel<128, false, FOLD, SHARED>);  // (gated: BF16 alone)
+    case 128: return gated ? f(linear_pair_kernel<128, kGated, FOLD && SHARED, SHARED>) : f(linear_pair_kernel<128, false, FOLD, SHARED>);  // (gated: whole sums for BF16 alone)
     case 64: return f(linear_pair_kernel<64, false, FOLD, SHARED>);
     default: return cudaErrorInvalidValue;
   }

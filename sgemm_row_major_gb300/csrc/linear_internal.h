@@ -72,7 +72,7 @@ constexpr int linear_pair_box(int tile_n, bool gated, bool fold) {
 int linear_pair_stages(int tile_n);
 int64_t linear_pair_smem(int tile_n);
 cudaError_t prepare_linear_pair();
-// kFold: some job has an FP32 output or keeps 8-bit values.  kShared: some job's K is shared; nothing follows the products.
+// kFold: some job has an FP32 output, keeps 8-bit values or has a long sum.  kShared: some job's K is shared; nothing follows the products.
 enum class LinearPairForm { kWhole, kFold, kShared };
 cudaError_t launch_linear_pair(int tile_n, bool gated, LinearPairForm form, const LinearMaps& maps, const LinearPairParams& p, cudaStream_t stream);
 
