@@ -33,7 +33,7 @@ bool wide_enough(int64_t ld, int64_t cols) { return ld >= std::max<int64_t>(1, c
 // A kept matrix (checked as a whole: one argument).
 bool usable_kept(const sgemm_kept_t* k, int64_t cols, bool work) {
   if (!k) return true;
-  if (!wide_enough(k->ld, cols) || k->ld > kMaxDim || !usable(k->data, k->scale ? 1 : 2, work)) return false;
+  if (!wide_enough(k->ld, cols) || !usable(k->data, k->scale ? 1 : 2, work)) return false;
   return !k->scale || (aligned(k->scale, 4) && wide_enough(k->lds, ceil_div(cols, 128)));
 }
 
@@ -629,7 +629,7 @@ int sgemm_linear(int64_t tokens, int64_t inputs, int64_t outputs, const void* X,
   if (!usable(Y, type_size(type), work) || (work && Y == R && type != SGEMM_BF16)) return -13;
   if (!wide_enough(ldy, outputs) || (work && Y == R && tokens > 1 && ldy != ldr)) return -14;
   if (!work) return SGEMM_OK;
-  if (too_large({tokens, inputs, outputs, ldx, ldw, ldy, R ? ldr : 0})) return SGEMM_ERR_UNSUPPORTED;
+  if (too_large({tokens, inputs, outputs, ldx, ldw, ldy, R ? ldr : 0, kept ? kept->ld : 0})) return SGEMM_ERR_UNSUPPORTED;
   Launch launch;
   Product& pr = launch.add();
   pr.d = Y;
@@ -663,7 +663,7 @@ int sgemm_gated(int64_t tokens, int64_t inputs, int64_t outputs, const void* X, 
   if (!usable(H, 2, work)) return -13;
   if (!wide_enough(ldh, outputs)) return -14;
   if (!work) return SGEMM_OK;
-  if (too_large({tokens, inputs, outputs, ldx, ldg, ldu, ldh})) return SGEMM_ERR_UNSUPPORTED;
+  if (too_large({tokens, inputs, outputs, ldx, ldg, ldu, ldh, kept_gate ? kept_gate->ld : 0, kept_up ? kept_up->ld : 0})) return SGEMM_ERR_UNSUPPORTED;
   Launch launch;
   Product& pr = launch.add();
   pr.shape.gated = true;
@@ -696,7 +696,8 @@ int sgemm_linear_backward(int64_t tokens, int64_t inputs, int64_t outputs, const
   if (!usable(dW, type_size(dw_type), dW != nullptr)) return -13;
   if (dW && !wide_enough(lddw, inputs)) return -14;
   if (!usable(dbias, 4, dbias != nullptr)) return -16;
-  if (too_large({tokens, inputs, outputs, lddy, dX ? ldw : 0, dX ? lddx : 0, dW ? lddw : 0})) return SGEMM_ERR_UNSUPPORTED;
+  if (too_large({tokens, inputs, outputs, lddy, dX ? ldw : 0, dX ? lddx : 0, dW ? lddw : 0, dW ? X->ld : 0, activation != SGEMM_ACT_NONE ? kept->ld : 0}))
+    return SGEMM_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (tokens == 0 || inputs == 0 || outputs == 0) {  // nothing, or sums of nothing
     if (tokens == 0) {
@@ -780,7 +781,8 @@ int sgemm_gated_backward(int64_t tokens, int64_t inputs, int64_t outputs, const 
   if (dU && !wide_enough(lddu, inputs)) return -19;
   if (!usable(H, 2, H != nullptr)) return -21;
   if (H && !wide_enough(ldh, outputs)) return -22;
-  if (too_large({tokens, inputs, outputs, lddh, dX ? ldg : 0, dX ? ldu : 0, dX ? lddx : 0, dG ? lddg : 0, dU ? lddu : 0, H ? ldh : 0}))
+  if (too_large({tokens, inputs, outputs, lddh, dX ? ldg : 0, dX ? ldu : 0, dX ? lddx : 0, dG ? lddg : 0, dU ? lddu : 0, H ? ldh : 0, dG ? X->ld : 0,
+                 kept_gate->ld, kept_up->ld}))
     return SGEMM_ERR_UNSUPPORTED;
   cudaStream_t stream = reinterpret_cast<cudaStream_t>(stream_);
   if (tokens == 0 || inputs == 0 || outputs == 0) {  // nothing, or sums of nothing
