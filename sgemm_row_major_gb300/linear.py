@@ -53,11 +53,18 @@ def _lib():
     return lib
 
 
+def _no_tensor(x, name):
+    return TypeError(f"{name} must be a tensor, got {type(x).__name__}")
+
+
 def _matrix(x, name, rows=None, cols=None):
     """(rows, columns, row stride) of a bfloat16 matrix of the given shape with contiguous rows."""
-    shape = x.shape
-    if x.dtype is not _bf16:
-        raise TypeError(f"{name} must be bfloat16, got {x.dtype}")
+    try:
+        shape, dtype = x.shape, x.dtype
+    except AttributeError:
+        raise _no_tensor(x, name) from None
+    if dtype is not _bf16:
+        raise TypeError(f"{name} must be bfloat16, got {dtype}")
     if len(shape) != 2:
         raise TypeError(f"{name} must have 2 dimensions")
     r, c = shape
@@ -67,6 +74,14 @@ def _matrix(x, name, rows=None, cols=None):
     if (rows is not None and r != rows) or (cols is not None and c != cols):
         raise ValueError(f"{name} must have shape ({'any' if rows is None else rows}, {'any' if cols is None else cols}), got ({r}, {c})")
     return r, c, ld if r > 1 and c else c or 1
+
+
+def _columns(x, name):
+    """The columns of a matrix that _kept() then looks at."""
+    shape = getattr(x, "shape", ())
+    if len(shape) != 2:
+        raise TypeError(f"{name} must be a matrix")
+    return shape[1]
 
 
 def _code(dtype, name) -> int:
@@ -93,7 +108,8 @@ def _kept(k, name, rows, cols):
         if k._block != ROW or c.format != 0:
             raise ValueError(f"{name} must have E4M3 codes and groups of (1, 128)")
         return KeptStruct(c.data, c.ld, c.scale, c.lds), k._device
-    return KeptStruct(k.data_ptr(), _matrix(k, name, rows, cols)[2], None, 1), k.get_device()
+    ld = _matrix(k, name, rows, cols)[2]
+    return KeptStruct(k.data_ptr(), ld, None, 1), k.get_device()
 
 
 def _alloc(rows, cols, dtype, like, stream):
@@ -135,13 +151,19 @@ def linear_bf16(x, weight, bias=None, activation=None, residual=None, *, save=No
     act = _act(activation)
     _check_keep(save)
     if bias is not None:
-        fp8._vector(bias, "bias", outputs, _bf16)
+        try:
+            fp8._vector(bias, "bias", outputs, _bf16)
+        except AttributeError:
+            raise _no_tensor(bias, "bias") from None
     r_ptr, ldr = None, 0
     if residual is not None:
         ldr = _matrix(residual, "residual", tokens, outputs)[2]
         r_ptr = residual.data_ptr()
     if out is not None:
-        rows, cols, ldy = _rows(out, "out")
+        try:
+            rows, cols, ldy = _rows(out, "out")
+        except AttributeError:
+            raise _no_tensor(out, "out") from None
         if rows != tokens or cols != outputs:
             raise ValueError("out has the wrong shape")
         if out_dtype is not None and out.dtype is not out_dtype:
@@ -180,7 +202,7 @@ def linear_bf16_backward(dy, x, weight, pre=None, activation=None, *, dx=True, d
         weight = None
     if dweight:
         if not dx:
-            inputs = x.shape[1]
+            inputs = _columns(x, "x")
         xs, x_dev = _kept(x, "x", tokens, inputs)
     if act:
         if pre is None:
@@ -252,7 +274,7 @@ def gated_bf16_backward(dh, x, gate, up, gate_pre, up_pre, activation="silu", *,
         gate = up = None
     if dweights:
         if not dx:
-            inputs = x.shape[1]
+            inputs = _columns(x, "x")
         xs, x_dev = _kept(x, "x", tokens, inputs)
     ka, a_dev = _kept(gate_pre, "gate_pre", tokens, outputs)
     kb, b_dev = _kept(up_pre, "up_pre", tokens, outputs)
