@@ -9,8 +9,8 @@
 // arithmetic).  A thread takes 8 columns of a row (16 bytes of BF16, 8 of codes); what it
 // reads of its next four rows is on its way to shared memory while it works on one (in registers the loads of two rows covered
 // half of the memory's latency).  Column sums are held per thread in FP32 and joined within the CTA, then
-// by a cluster of up to 8 CTAs that share the rows of a strip, or (many rows and columns, where a cluster's CTAs are too few to
-// fill the chip) by a second kernel; always in a fixed order.
+// by a cluster of up to 8 CTAs that share the rows of a strip, or (many rows, where the clusters' CTAs are too few to fill the
+// chip, and wide strips) by a second kernel; always in a fixed order.
 // Gated, 4096 x 8192 values kept in BF16, with H: 58 us, 6.1 TB/s.
 #include <algorithm>
 
@@ -345,13 +345,24 @@ void shape_linear_grad(LinearGradParams* p, bool clusters, int sm_count) {
   const int64_t wide = (p->cols + lin::kWide - 1) / lin::kWide, most = (p->rows + 31) / 32;
   p->strip = wide * std::min<int64_t>(8, most) >= sm_count ? lin::kWide : lin::kNarrow;
   const int64_t strips = (p->cols + p->strip - 1) / p->strip;
-  p->joined = p->dbias && p->strip == lin::kNarrow;
+  const bool narrow = p->strip == lin::kNarrow;
+  int n = clusters ? 8 : 1;  // a cluster's CTAs
+  while (n > 1 && n > most) n /= 2;
+  // Clusters that leave room on the SMs cost more than a second kernel (1 us or so) from some rows on.  Joined and by a second
+  // kernel, us of the pass alone: GELU 64 columns 513 rows 3.7 and 3.6, 16384 rows 20.9 and 6.7; 1216 columns 1500 rows 7.5 and 6.4,
+  // 16384 rows 49 and 26; 2048 columns 1500 rows 8.3 both (and the launch behind it starts 0.4 us later), 4097 rows 16.6 and 12.9;
+  // without an activation 200 columns 2048 rows 3.6 and 3.9, 4097 rows 4.2 both, 65536 rows 39 and 9.8; 2048 columns 16384 rows 16.1 and 15.2.
+  const bool act = p->act != SGEMM_ACT_NONE;
+  const int64_t ctas = strips * n;
+  const bool few = act ? ctas < 4 * sm_count && p->rows > std::max<int64_t>(512, 8 * ctas) : ctas < 2 * sm_count && p->rows > 4096;
+  p->joined = p->dbias && narrow && !few;
   if (p->joined) {
-    int n = clusters ? 8 : 1;  // a cluster's CTAs
-    while (n > 1 && n > most) n /= 2;
     p->row_blocks = n;
   } else {
-    const int64_t want = (8 * (int64_t)sm_count + strips - 1) / strips;  // eight CTAs per SM, of no fewer than 32 rows
+    // CTAs of no fewer than 32 rows, eight per SM; where a second kernel adds the sums of narrow strips, which has little to read
+    // per row block but a wait for each few of them, two, or with an activation's work at least an eighth as many row blocks as SMs
+    int64_t want = ((p->dbias && narrow ? 2 : 8) * (int64_t)sm_count + strips - 1) / strips;
+    if (p->dbias && narrow && act) want = std::max<int64_t>(want, sm_count / 8);
     p->row_blocks = (int)std::max<int64_t>(1, std::min<int64_t>(std::min(want, most), 65535));
   }
 }
