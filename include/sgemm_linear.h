@@ -35,10 +35,14 @@
 extern "C" {
 #endif
 
-/* Activations, in FP32.  Phi is the standard normal distribution's integral. */
+/*
+ * Activations, in FP32.  Phi is the standard normal distribution's integral.  A
+ * NaN gives NaN, and so does -infinity but in RELU (a product of infinity and
+ * 0); derivatives at the infinities are their limits.
+ */
 enum sgemm_activation {
     SGEMM_ACT_NONE = 0,      /* a */
-    SGEMM_ACT_RELU = 1,      /* a where a > 0, else 0; derivative 0 at 0 */
+    SGEMM_ACT_RELU = 1,      /* a where a > 0, 0 where a <= 0; derivative 0 at 0 */
     SGEMM_ACT_SILU = 2,      /* a / (1 + exp(-a)) */
     SGEMM_ACT_GELU = 3,      /* a Phi(a) */
     SGEMM_ACT_GELU_TANH = 4  /* a / (1 + exp(-2 u)), u = sqrt(2 / pi) (a + 0.044715 a^3): a (1 + tanh u) / 2 */
