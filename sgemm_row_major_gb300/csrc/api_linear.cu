@@ -234,7 +234,6 @@ struct Operand {
     m.ld = ld;
     m.scale = scale;
     m.lds = lds;
-    m.vec = scale ? rows_at(p, ld, 1, 8) : rows_at(p, ld, 2, 16);
     copied = scale || !aligned(p, 16) || (ld % 8 != 0 && rows > 1);
   }
   void place(Pieces* w) {

@@ -111,7 +111,7 @@ struct LinearKeptIn {
   const void* data = nullptr;    // nullptr: not read
   const float* scale = nullptr;  // nullptr: BF16
   int64_t ld = 0, lds = 0;
-  int vec = 0;                   // 1: chunks of 8 elements can be read at once
+  int vec = 0;                   // 1: chunks of 8 elements can be read at once (not looked at by the copies)
 };
 struct LinearGradParams {
   int64_t rows = 0;
