@@ -349,13 +349,12 @@ void shape_linear_grad(LinearGradParams* p, bool clusters, int sm_count) {
   const bool narrow = p->strip == lin::kNarrow;
   int n = clusters ? 8 : 1;  // a cluster's CTAs
   while (n > 1 && n > most) n /= 2;
-  // Clusters that leave room on the SMs cost more than a second kernel (1 us or so) from some rows on.  Joined and by a second
-  // kernel, us of the pass alone: GELU 64 columns 513 rows 3.7 and 3.6, 16384 rows 20.9 and 6.7; 1216 columns 1500 rows 7.5 and 6.4,
-  // 16384 rows 49 and 26; 2048 columns 1500 rows 8.3 both (and the launch behind it starts 0.4 us later), 4097 rows 16.6 and 12.9;
-  // without an activation 200 columns 2048 rows 3.6 and 3.9, 4097 rows 4.2 both, 65536 rows 39 and 9.8; 2048 columns 16384 rows 16.1 and 15.2.
+  // Clusters that leave room on the SMs cost more than a second kernel from some rows on: 1 us or so on the GPU, and 4 us of the
+  // host, which a call of fewer rows would wait for.  Joined and by a second kernel, us of the pass alone: GELU 16384 rows 64 columns 20.9
+  // and 6.7, 1216 columns 49 and 26, 2048 columns 52 and 33, 4096 columns 8192 rows 44 and 34; without an activation 65536 rows 64 columns
+  // 33 and 6.9, 512 columns 40 and 15.  (600 rows of 256 columns, whole calls of 256 inputs: 28 joined and 31.)
   const bool act = p->act != SGEMM_ACT_NONE;
-  const int64_t ctas = strips * n;
-  const bool few = act ? ctas < 4 * sm_count && p->rows > std::max<int64_t>(512, 8 * ctas) : ctas < 2 * sm_count && p->rows > 4096;
+  const bool few = strips * n < (act ? 4 : 2) * sm_count && p->rows > (act ? 8192 : 32768);
   p->joined = p->dbias && narrow && !few;
   if (p->joined) {
     p->row_blocks = n;

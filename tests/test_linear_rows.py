@@ -52,16 +52,15 @@ def shape(tmp_path_factory):
 def test_sums_do_not_leave_the_chip_idle(shape):
     """A pass over many rows has at least as many CTAs as the chip has SMs, whether the sums are wanted or not; over few rows a
     cluster adds them, with no second kernel."""
-    for rows in (5000, 16384, 65536, 1 << 20):
+    for rows, activations in ((8193, (2,)), (16384, (1, 4)), (32769, (0, 2)), (65536, (0, 3)), (1 << 20, (0, 2))):
         for cols in (1, 64, 200, 256, 512, 1000, 1024, 1216, 1217, 4096, 5000, 40000):
-            for activation in (0, 2):
+            for activation in activations:
                 for clusters in (True, False):
                     for dbias in (0, 1):
                         strip, blocks, joined = shape(rows, cols, activation, dbias, clusters)
                         assert -(-cols // strip) * blocks >= 152, (rows, cols, activation, dbias, clusters)
                         assert 32 * (blocks - 1) < rows and blocks <= 65535 and (not joined or blocks <= 8)
-    assert shape(1024, 64, 2, 1)[1] == 32
-    for rows, activation in ((1, 0), (31, 2), (256, 2), (512, 3), (4096, 0)):
+    for rows, activation in ((1, 0), (31, 2), (256, 2), (1000, 1), (8192, 3), (32768, 0)):
         for cols in (1, 64, 200, 1024):
             strip, blocks, joined = shape(rows, cols, activation, 1)
             assert (strip, joined) == (64, 1) and blocks <= min(8, -(-rows // 32))
@@ -70,7 +69,7 @@ def test_sums_do_not_leave_the_chip_idle(shape):
 @pytest.mark.gpu
 @pytest.mark.parametrize("how", ["bf16", "fp8"])
 @pytest.mark.parametrize("activation", [None, "relu", "gelu"])
-@pytest.mark.parametrize("T,O", [(513, 8), (600, 64), (16384, 64), (4097, 200), (65536, 200), (1500, 1216), (5000, 1217)])
+@pytest.mark.parametrize("T,O", [(513, 8), (8200, 8), (16384, 64), (33000, 64), (65536, 200), (8193, 1216), (5000, 1217)])
 def test_many_rows_of_few_columns(T, O, activation, how):
     import torch
     if activation is None and how == "fp8":
@@ -87,7 +86,7 @@ def test_many_rows_of_few_columns(T, O, activation, how):
 
 @pytest.mark.gpu
 def test_many_rows_of_few_columns_in_bounds(both):  # noqa: F811
-    for T, O in ((513, 8), (16384, 64), (4097, 200), (1500, 1216)):
+    for T, O in ((8200, 8), (33000, 64), (33000, 200), (8193, 1216)):
         dy, a = rand(1, T, O), rand(2, T, O)
         for d, pre in ((dy, a), (strided(dy, 3, 1), sg.quantize_fp8(a))):
             both(lambda: tuple(sg.linear_bf16_backward(d, None, None, pre, "gelu", dx=False, dweight=False, dbias=True)), (T, O))
