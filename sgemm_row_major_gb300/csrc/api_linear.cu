@@ -58,8 +58,9 @@ struct Shape {
 };
 
 // Times in ns that the choice of kernel goes by, fitted to 640 launches of 54 products (1 to 4096 tokens, gradients and gated ones
-// among them) forced to each kernel, tile and split on a GB300: they give those launches' times to about 12%, and the launch they
-// choose takes 3% longer than the fastest on average.  In the pair kernel, by tile width: a K tile of 64, and the rest of a tile,
+// among them) forced to each kernel, tile and split on a GB300.  Against 1249 launches of these and 15 more products with long sums
+// they are off by 10 to 13% (20% where units of the pair kernel share K), and the launch they choose takes 2.5% longer than the
+// fastest on average, 29% at worst.  In the pair kernel, by tile width: a K tile of 64, and the rest of a tile,
 // and the rate at which few clusters read.  On the short side: a K tile in a CTA that has its SM to itself, the rest of a tile, and
 // what joining a tile's shares adds.
 struct PairCost {

@@ -12,7 +12,8 @@
 // B.  A gated tile has TN / 2 columns of each product: the even CTA's half of B is gate's rows, the odd one's up's, so every
 // thread that reads the accumulator finds both products of an element in its own lane.  The epilogue runs over an accumulator
 // 64 columns at a time while the next tile's products fill the other one.  The tensor cores' own accumulation is not
-// round-to-nearest and drifts by about 1.2e-8 of the sum per instruction of 16 k.  Where FP32 values leave the kernel (an FP32
+// round-to-nearest and drifts by about 1.5e-8 of the sum per instruction of 16 k (where signs are random; up to 1e-7 where the terms
+// have one).  Where FP32 values leave the kernel (an FP32
 // output, the scales of 8-bit values) only `fold` K tiles are summed in one accumulator, and these sums in FP32 registers;
 // BF16 outputs take sums of up to 256 K tiles whole from the tensor memory (off by 1.6e-5 of the sum at that length where the terms'
 // signs are random and by 7.5e-5 where they have one sign; their own rounding is 2e-3), which leaves the next tile's products a whole
